@@ -392,6 +392,134 @@ la_status la_delta_rule_chunked(const void *q, const void *k, const void *v, la_
                                 la_stream_t stream);
 
 /*
+ * Linear attention with a constant decay per head: the recurrence without a feature
+ * map and without a normaliser,
+ *     S_t = g S_{t-1} + k_t v_t^T,    y_t = scale q_t^T S_t        (g = decay[h])
+ * so a write made n tokens ago counts g^n ([LA] "加一个门：让旧记忆逐渐淡出" with a gate that
+ * is a constant of the head).  q and k are used as given; the read follows the
+ * write, as in the other entry points.
+ *   decay  device FP32 [H], 0 <= decay <= 1 (not checked: it stays on the device).
+ *          It is a constant of the model: no gradient is formed for it.
+ *   scale  any finite value, typically 1/sqrt(r).
+ * Inputs are finite; a row with an infinity or NaN may spoil the outputs of the 128
+ * tokens around it as well as all later ones.
+ */
+
+/*
+ * la_decay_prefill -- T tokens of every (b, h) sequence from S0 (a chunk's output is
+ * the read of the carried state plus the masked in-chunk product, [LA] "一个 chunk
+ * 的输出由两部分组成", each term times the decay between its write and its read).
+ *   q, k   device [B,H,T,r] dtype          v, y   device [B,H,T,dv] dtype
+ *   S0     device FP32 [B,H,r,dv] or NULL (zero); may equal S_out (in place)
+ *   S_out  device FP32 [B,H,r,dv] final state
+ *   workspace  device scratch of la_decay_prefill_workspace_bytes(...) bytes, 256-byte
+ *              aligned, owned by the caller; may be NULL when that is 0.  Calls
+ *              sharing one workspace must be ordered.
+ * Kernel: the token recurrence in FP32 on CUDA cores, the value columns split over CTAs.
+ * Requires 1 <= r, dv <= 256, B, H <= 65535; BF16 arrays 2-byte, FP32 arrays 4-byte
+ * aligned.  T may be 0 (S_out = S0; q, k, v, y may then be NULL).
+ * Errors: LA_ERR_NULL, LA_ERR_SHAPE (B, H, r, dv < 1, T < 0, scale not finite),
+ *         LA_ERR_DTYPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (other sizes),
+ *         LA_ERR_WORKSPACE, LA_ERR_CUDA.
+ */
+size_t la_decay_prefill_workspace_bytes(int B, int H, int T, int r, int dv, la_dtype dtype);
+la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                           const float *S0, int B, int H, int T, int r, int dv, float scale, void *y, float *S_out,
+                           void *workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * la_decay_prefill_varlen -- the same for sequences of different lengths packed one after
+ * another: sequence b is tokens cu_seqlens[b] .. cu_seqlens[b+1]-1, from S0[b] into
+ * S_out[b] (an empty sequence copies its state).
+ *   q, k       device [total_T, H, r] dtype (token-major)     v, y  device [total_T, H, dv]
+ *   S0, S_out  device FP32 [B,H,r,dv]; S0 NULL (zero) or equal to S_out (in place) or apart
+ *   cu_seqlens device int32 [B + 1], 0 <= cu_seqlens[0] <= .. <= cu_seqlens[B] <= total_T.  A
+ *              sequence outside [0, total_T] or of negative length is skipped and
+ *              recorded as LA_ERR_SHAPE in the device status word.
+ * Rows of y outside every sequence are not written.  Needs no workspace.
+ * Sizes, alignment and errors as for la_decay_prefill (total_T * H < 2^31).
+ */
+la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                                  const float *S0, const int *cu_seqlens, int B, int H, int total_T, int r, int dv,
+                                  float scale, void *y, float *S_out, la_stream_t stream);
+
+/*
+ * la_decay_decode_step -- one new token per (b, h), the state updated in place.
+ *   q, k  device [B,H,1,r] dtype    v, y  device [B,H,1,dv] dtype    S  device FP32 [B,H,r,dv]
+ * Bound by the state's traffic when dv is a multiple of 4 and S 16-byte aligned;
+ * other sizes take the token recurrence.  Requirements and errors as for
+ * la_decay_prefill.
+ */
+la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                               float *S, int B, int H, int r, int dv, float scale, void *y, la_stream_t stream);
+
+/*
+ * la_decay_backward -- gradients of la_decay_prefill's outputs.  Given dy = dL/dy and
+ * optionally dS_T = dL/dS_T, with G_T = scale q_T dy_T^T + dS_T,
+ *     G_t = scale q_t dy_t^T + g G_{t+1},
+ *     dq_t = scale S_t dy_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   dS0 = g G_1.
+ *   q, k, v, decay, S0, scale: as passed to the forward call (its outputs are not needed).
+ *   dy       device [B,H,T,dv] dtype         dS_T  device FP32 [B,H,r,dv] or NULL (zero)
+ *   dq, dk   device [B,H,T,r] dtype          dv_out  device [B,H,T,dv] dtype
+ *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL); it does not overlap S0,
+ *            and may equal dS_T only when T is 0.
+ *   workspace  la_decay_backward_workspace_bytes(...) bytes, 256-byte aligned (NULL when 0).
+ * Three sweeps like the forward one, in one launch: dq forwards in time, dk and dv backwards.
+ * Sizes, alignment and errors as for la_decay_prefill.  T may be 0 (dS0 = dS_T).
+ */
+size_t la_decay_backward_workspace_bytes(int B, int H, int T, int r, int dv, la_dtype dtype);
+la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                            const float *S0, int B, int H, int T, int r, int dv, float scale, const void *dy,
+                            const float *dS_T, void *dq, void *dk, void *dv_out, float *dS0, void *workspace,
+                            size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * la_beam_select -- a beam search's choice: the best K of a request's K beams x V tokens.
+ * Candidate (k, v) of request b scores
+ *     scores[b,k] + logits[b,k,v] - log sum_u exp logits[b,k,u]
+ * and the K best, best first, become the request's beams; equal scores go to the lower
+ * k * V + v.  (Within one beam candidates rank by their logits.)
+ *   logits      device [B,K,V] dtype, row (b, k) at element (b K + k) row_stride
+ *   scores      device FP32 [B,K] cumulative log-probabilities
+ *   done        device uint8 [B,K], non-zero: beam k has ended; its one candidate is token
+ *               eos with its score unchanged.  NULL: none has.
+ *   eos         the token that ends a beam, 0 .. V-1, or -1 (none; done must be NULL).
+ *   next_scores, parents, tokens   device FP32, int32, int32 [B,K]: slot j's score, the beam it
+ *               continues and the token it appends
+ *   done_out    device uint8 [B,K] or NULL: 1 where the parent has ended or the token is eos
+ * A logit of -infinity (a masked token) is no candidate; nor is any token of a beam whose
+ * score or log-sum-exp is not finite (all its tokens masked, or a NaN or +infinity
+ * among its logits).  A slot left without a candidate gets score -infinity, its own
+ * beam as parent, token 0 and its own done.
+ * next_scores may equal scores, done_out may equal done.
+ * One launch, one cluster of 2 to 8 CTAs per request, the logits read once.
+ * Requires 1 <= K <= 32, 1 <= V <= 2^30, row_stride >= V, B <= 65535; logits aligned to their
+ * element size, FP32 and int32 arrays 4-byte aligned.
+ * Errors: LA_ERR_NULL, LA_ERR_SHAPE (sizes < 1, row_stride < V, eos out of range or missing),
+ *         LA_ERR_DTYPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (K > 32, other sizes), LA_ERR_CUDA.
+ */
+la_status la_beam_select(const void *logits, la_dtype dtype, long long row_stride, const float *scores,
+                         const unsigned char *done, int B, int K, int V, int eos, float *next_scores, int *parents,
+                         int *tokens, unsigned char *done_out, la_stream_t stream);
+
+/*
+ * la_state_reorder -- moves recurrent states after a beam search's choice: slot j of
+ * request b receives the state of its slot parents[b,j].
+ *   S, S_out   device FP32 [B*K, H, r, dv]       z, z_out  device FP32 [B*K, H, r], or both NULL
+ *   parents    device int32 [B,K], values 0 .. K-1.  A slot whose parent is out of range is
+ *              left as it is and recorded as LA_ERR_SHAPE in the device status word.
+ * S_out may equal S and z_out z (in place: slots that keep their state are not touched);
+ * otherwise they must not overlap.  Any parents are allowed, repeated ones too.
+ * The states of la_decode_step (S and z), la_delta_rule and la_decay_decode_step (S) all
+ * have this layout.
+ * Requires 1 <= K <= 32, B <= 65535, 4-byte alignment (16-byte accesses when every slot is
+ * 16-byte aligned).
+ * Errors: LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (K > 32), LA_ERR_CUDA.
+ */
+la_status la_state_reorder(const float *S, const float *z, const int *parents, int B, int K, int H, int r, int dv,
+                           float *S_out, float *z_out, la_stream_t stream);
+
+/*
  * la_last_device_status -- synchronise `stream`, then read and clear the device
  * status word of the current device: LA_OK, or LA_ERR_TIMEOUT when a kernel
  * gave up waiting on an on-chip barrier since the last read.  Returns

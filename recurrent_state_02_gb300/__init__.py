@@ -4,6 +4,10 @@
     S_t = alpha_t S_{t-1} + phi(k_t) v_t^T,   z_t = alpha_t z_{t-1} + phi(k_t)
     y_t = phi(q_t)^T S_t / (phi(q_t)^T z_t + eps)
 
+and its relatives on the same states: the delta rule (delta_rule*), linear attention with a
+constant decay per head (decay_*), and what a beam search does with states between
+decode steps (beam_select, state_reorder).
+
 Every step runs in the CUDA kernels of liblinattn.so, reached through its C ABI
 (include/linattn.h).  The functions below only check tensor metadata, allocate
 outputs with torch, and pass raw device pointers and the current CUDA stream;
@@ -350,6 +354,215 @@ def _delta(entry, q, k, v, beta, S0, y, S_out, workspace):
         st = getattr(_native.lib(), entry)(*args, _stream(dev))
     _native.check(st, entry)
     return y, S_out
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace, or one of `need` bytes (None when there is no need for one), and its size."""
+    if workspace is None:
+        return (torch.empty(need, device=device, dtype=torch.uint8), need) if need else (None, 0)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _call(entry, device, *args):
+    """One library call on `device` and its current stream (appended to args)."""
+    fn = getattr(_native.lib(), entry)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(device))
+    else:
+        with _device_guard(device):
+            st = fn(*args, _stream(device))
+    _native.check(st, entry)
+
+
+def _decay_inputs(q, k, v, decay, shape_qk, shape_v, H):
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    dev = q.device
+    _require(q, "q", shape_qk, q.dtype, dev)
+    _require(k, "k", shape_qk, q.dtype, dev)
+    _require(v, "v", shape_v, q.dtype, dev)
+    if decay is None:
+        raise ValueError("decay must be given (ones for no decay)")
+    _require(decay, "decay", (H,), torch.float32, dev)
+
+
+def _bytes(entry, device, *args):
+    if device is None or device.index == torch.cuda.current_device():
+        return int(getattr(_native.lib(), entry)(*args))
+    with _device_guard(device):
+        return int(getattr(_native.lib(), entry)(*args))
+
+
+def decay_prefill_workspace_bytes(B, H, T, r, dv, dtype=torch.bfloat16, device=None) -> int:
+    """Scratch bytes of decay_prefill for these sizes on `device` (default: the current one)."""
+    return _bytes("la_decay_prefill_workspace_bytes", None if device is None else torch.device(device), B, H, T, r, dv,
+                  _DTYPES[dtype])
+
+
+def decay_prefill(q, k, v, decay, S0=None, scale=1.0, y=None, S_out=None, workspace=None):
+    """Linear attention with a constant decay per head: S <- decay S + k v^T, y = scale S^T q.
+    q, k [B,H,T,r], v [B,H,T,dv] (bf16 or fp32, same dtype); decay [H] fp32 in 0..1; S0
+    [B,H,r,dv] fp32 or None (zero).  Returns (y [B,H,T,dv] in the input dtype, S_T)."""
+    B, H, T, r = q.shape
+    dv = v.shape[3]
+    dev = q.device
+    _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dv), H)
+    _require(S0, "S0", (B, H, r, dv), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(v)
+    else:
+        _require(y, "y", (B, H, T, dv), q.dtype, dev)
+    if S_out is None:
+        S_out = torch.empty((B, H, r, dv), device=dev, dtype=torch.float32)
+    else:
+        _require(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
+    dt = _DTYPES[q.dtype]
+    workspace, ws_bytes = _workspace(workspace, _bytes("la_decay_prefill_workspace_bytes", dev, B, H, T, r, dv, dt), dev)
+    _call("la_decay_prefill", dev, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(decay), _ptr(S0), B, H, T, r, dv, float(scale),
+          _ptr(y), _ptr(S_out), _ptr(workspace), ws_bytes)
+    return y, S_out
+
+
+def decay_prefill_varlen(q, k, v, decay, cu_seqlens, S0=None, scale=1.0, y=None, S_out=None):
+    """decay_prefill for packed sequences: q, k [total_T, H, r], v [total_T, H, dv]
+    (token-major); cu_seqlens int32 [B+1] on the device (sequence b is tokens
+    cu_seqlens[b] .. cu_seqlens[b+1]-1); S0 [B,H,r,dv] fp32 or None.  Returns
+    (y [total_T, H, dv], S_T [B,H,r,dv])."""
+    total_T, H, r = q.shape
+    dv = v.shape[2]
+    dev = q.device
+    _decay_inputs(q, k, v, decay, (total_T, H, r), (total_T, H, dv), H)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.device != dev:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor on the device of q")
+    B = cu_seqlens.numel() - 1
+    _require(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    _require(S0, "S0", (B, H, r, dv), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(v)
+    else:
+        _require(y, "y", (total_T, H, dv), q.dtype, dev)
+    if S_out is None:
+        S_out = torch.empty((B, H, r, dv), device=dev, dtype=torch.float32)
+    else:
+        _require(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
+    _call("la_decay_prefill_varlen", dev, _ptr(q), _ptr(k), _ptr(v), _DTYPES[q.dtype], _ptr(decay), _ptr(S0),
+          _ptr(cu_seqlens), B, H, total_T, r, dv, float(scale), _ptr(y), _ptr(S_out))
+    return y, S_out
+
+
+def decay_decode_step(q, k, v, decay, S, scale=1.0, y=None):
+    """One token per request of decay_prefill, S [B,H,r,dv] fp32 updated in place.
+    q, k [B,H,1,r], v [B,H,1,dv]; decay [H] fp32.  Returns y [B,H,1,dv]."""
+    B, H, one, r = q.shape
+    dv = v.shape[3]
+    dev = q.device
+    if one != 1:
+        raise ValueError("decode takes one token per request")
+    _decay_inputs(q, k, v, decay, (B, H, 1, r), (B, H, 1, dv), H)
+    _require(S, "S", (B, H, r, dv), torch.float32, dev)
+    if y is None:
+        y = torch.empty_like(v)
+    else:
+        _require(y, "y", (B, H, 1, dv), q.dtype, dev)
+    _call("la_decay_decode_step", dev, _ptr(q), _ptr(k), _ptr(v), _DTYPES[q.dtype], _ptr(decay), _ptr(S), B, H, r, dv,
+          float(scale), _ptr(y))
+    return y
+
+
+def decay_backward_workspace_bytes(B, H, T, r, dv, dtype=torch.bfloat16, device=None) -> int:
+    """Scratch bytes of decay_backward for these sizes on `device` (default: the current one)."""
+    return _bytes("la_decay_backward_workspace_bytes", None if device is None else torch.device(device), B, H, T, r, dv,
+                  _DTYPES[dtype])
+
+
+def decay_backward(q, k, v, dy, decay, S0=None, dS_T=None, scale=1.0, workspace=None):
+    """Gradients of decay_prefill: from its inputs, dy [B,H,T,dv] and optionally dS_T
+    [B,H,r,dv] fp32, returns (dq, dk, dv, dS0); dq, dk, dv in the input dtype, dS0 in
+    fp32.  The decay is a constant of the head and gets no gradient."""
+    B, H, T, r = q.shape
+    dvd = v.shape[3]
+    dev = q.device
+    _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dvd), H)
+    _require(dy, "dy", (B, H, T, dvd), q.dtype, dev)
+    _require(S0, "S0", (B, H, r, dvd), torch.float32, dev)
+    _require(dS_T, "dS_T", (B, H, r, dvd), torch.float32, dev)
+    dq, dk, dv_out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dS0 = torch.empty((B, H, r, dvd), device=dev, dtype=torch.float32)
+    dt = _DTYPES[q.dtype]
+    workspace, ws_bytes = _workspace(workspace, _bytes("la_decay_backward_workspace_bytes", dev, B, H, T, r, dvd, dt), dev)
+    _call("la_decay_backward", dev, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(decay), _ptr(S0), B, H, T, r, dvd, float(scale),
+          _ptr(dy), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv_out), _ptr(dS0), _ptr(workspace), ws_bytes)
+    return dq, dk, dv_out, dS0
+
+
+def beam_select(logits, scores, done=None, eos=-1, next_scores=None, parents=None, tokens=None, done_out=None):
+    """A beam search's choice: the best K of K beams x V tokens of every request, by
+    scores + log_softmax(logits), best first, ties to the lower k V + v.
+    logits [B,K,V] (bf16 or fp32; rows may be padded: any stride between them, one for
+    all); scores [B,K] fp32; done [B,K] uint8 or None: beams that have ended (their one
+    candidate is the token eos, the score unchanged); eos the token that ends a beam, -1 none.
+    Returns (next_scores [B,K] fp32, parents [B,K] int32, tokens [B,K] int32, done_out
+    [B,K] uint8).  A slot without a candidate has score -inf, itself as parent and token 0."""
+    if logits.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {logits.dtype}")
+    B, K, V = logits.shape
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
+    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or (B > 1 and K > 1 and logits.stride(0) != K * stride):
+        raise ValueError("logits must have contiguous rows at one stride")
+    _require(scores, "scores", (B, K), torch.float32, dev)
+    _require(done, "done", (B, K), torch.uint8, dev)
+    if next_scores is None:
+        next_scores = torch.empty((B, K), device=dev, dtype=torch.float32)
+    else:
+        _require(next_scores, "next_scores", (B, K), torch.float32, dev)
+    if parents is None:
+        parents = torch.empty((B, K), device=dev, dtype=torch.int32)
+    else:
+        _require(parents, "parents", (B, K), torch.int32, dev)
+    if tokens is None:
+        tokens = torch.empty((B, K), device=dev, dtype=torch.int32)
+    else:
+        _require(tokens, "tokens", (B, K), torch.int32, dev)
+    if done_out is None:
+        done_out = torch.empty((B, K), device=dev, dtype=torch.uint8)
+    else:
+        _require(done_out, "done_out", (B, K), torch.uint8, dev)
+    _call("la_beam_select", dev, _ptr(logits), _DTYPES[logits.dtype], stride, _ptr(scores), _ptr(done), B, K, V, eos,
+          _ptr(next_scores), _ptr(parents), _ptr(tokens), _ptr(done_out))
+    return next_scores, parents, tokens, done_out
+
+
+def state_reorder(S, parents, z=None, S_out=None, z_out=None):
+    """Moves recurrent states after a beam search's choice: slot j of request b receives
+    the state of its slot parents[b, j].  S [B*K,H,r,dv], z [B*K,H,r] fp32 (or None);
+    parents [B,K] int32 on the device.  In place unless S_out (and z_out) are given.
+    Returns (S_out, z_out)."""
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, K]")
+    B, K = parents.shape
+    n, H, r, dv = S.shape
+    dev = S.device
+    _require(parents, "parents", (B, K), torch.int32, dev)
+    _require(S, "S", (B * K, H, r, dv), torch.float32, dev)
+    _require(z, "z", (B * K, H, r), torch.float32, dev)
+    if z is None and z_out is not None:
+        raise ValueError("z_out is taken only together with z")
+    if S_out is None:
+        if z_out is not None:
+            raise ValueError("z_out is taken only together with S_out")
+        S_out, z_out = S, z
+    else:
+        _require(S_out, "S_out", (B * K, H, r, dv), torch.float32, dev)
+        if z is not None and z_out is None:
+            z_out = z if S_out.data_ptr() == S.data_ptr() else torch.empty_like(z)
+        _require(z_out, "z_out", (B * K, H, r), torch.float32, dev)
+    _call("la_state_reorder", dev, _ptr(S), _ptr(z), _ptr(parents), B, K, H, r, dv, _ptr(S_out), _ptr(z_out))
+    return S_out, z_out
 
 
 def last_device_status(device="cuda") -> int:

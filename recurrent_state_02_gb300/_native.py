@@ -16,6 +16,7 @@ LA_DTYPE_BF16, LA_DTYPE_FP32 = 0, 1
 # Every function the header declares, with its ctypes signature.
 _vp, _fp, _i, _f, _sz, _u64 = (ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
                                ctypes.c_ulonglong)
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "la_state_init": (_i, [_fp, _fp, _i, _i, _i, _i, _vp]),
     "la_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
@@ -38,6 +39,15 @@ SIGNATURES = {
                                      _fp, _fp, _vp, _sz, _vp]),
     "la_prefill_backward_saved": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _fp, _i, _i, _i, _i, _i, _vp, _vp, _fp, _fp,
                                        _fp, _fp, _vp, _vp, _vp, _fp, _fp, _fp, _vp, _sz, _vp]),
+    "la_decay_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "la_decay_prefill": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _i, _i, _i, _i, _i, _f, _vp, _fp, _vp, _sz, _vp]),
+    "la_decay_prefill_varlen": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _vp, _i, _i, _i, _i, _i, _f, _vp, _fp, _vp]),
+    "la_decay_decode_step": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _i, _i, _i, _i, _f, _vp, _vp]),
+    "la_decay_backward_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "la_decay_backward": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _i, _i, _i, _i, _i, _f, _vp, _fp, _vp, _vp, _vp, _fp,
+                               _vp, _sz, _vp]),
+    "la_beam_select": (_i, [_vp, _i, _ll, _fp, _vp, _i, _i, _i, _i, _fp, _vp, _vp, _vp, _vp]),
+    "la_state_reorder": (_i, [_fp, _fp, _vp, _i, _i, _i, _i, _i, _fp, _fp, _vp]),
     "la_last_device_status": (_i, [_vp]),
     "la_status_string": (ctypes.c_char_p, [_i]),
     "la_debug_wait_probe": (_i, [_u64, _vp]),

@@ -1,11 +1,13 @@
 // api.cu -- the C ABI declared in include/linattn.h: argument validation,
 // kernel selection, TMA descriptor set-up and the device status word.
 #include "../../include/linattn.h"
+#include "decay.h"
 #include "delta_tc.h"
 #include "kernels.h"
 #include "side_lane.h"
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -784,6 +786,193 @@ la_status la_delta_rule_chunked(const void *q, const void *k, const void *v, la_
     a.status = status;
     a.wait_limit_ns = la::kWaitLimitNs;
     return from_cuda(la::launch_delta_tc(mq, mk, mv, a, B, st));
+}
+
+// ------------------------------------------- decayed linear attention, beams
+
+namespace {
+
+bool elem_aligned(const void *p, la_dtype dtype) { return !p || aligned(p, dtype == LA_DTYPE_BF16 ? 2 : 4); }
+
+// What every decayed entry point checks of its sizes.
+la_status check_decay_sizes(la_dtype dtype, int B, int H, int T, int r, int dv, float scale)
+{
+    if (B < 1 || H < 1 || T < 0 || r < 1 || dv < 1 || !std::isfinite(scale)) return LA_ERR_SHAPE;
+    if (dtype != LA_DTYPE_BF16 && dtype != LA_DTYPE_FP32) return LA_ERR_DTYPE;
+    if (r > 256 || dv > 256 || B > 65535 || H > 65535) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// Prefill as a sweep.
+la::DecaySweep forward_sweep(const void *q, const void *k, const void *v, const float *S0, int r, int dv, float scale,
+                             void *y, float *S_out)
+{
+    la::DecaySweep s;
+    s.a = q, s.b = k, s.c = v, s.out = y;
+    s.S_init = S0, s.S_fin = S_out;
+    s.ra = r, s.n = dv;
+    s.out_scale = scale;
+    return s;
+}
+
+}  // namespace
+
+size_t la_decay_prefill_workspace_bytes(int, int, int, int, int, la_dtype) { return 0; }
+
+la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                           const float *S0, int B, int H, int T, int r, int dv, float scale, void *y, float *S_out,
+                           void *workspace, size_t workspace_bytes, la_stream_t stream)
+{
+    if (!decay || !S_out || (T > 0 && (!q || !k || !v || !y))) return LA_ERR_NULL;
+    if (const la_status e = check_decay_sizes(dtype, B, H, T, r, dv, scale)) return e;
+    for (const void *p : {q, k, v, (const void *)y})
+        if (!elem_aligned(p, dtype)) return LA_ERR_ALIGN;
+    for (const void *p : {(const void *)decay, (const void *)S0, (const void *)S_out})
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    const size_t need = la_decay_prefill_workspace_bytes(B, H, T, r, dv, dtype);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return LA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return LA_ERR_ALIGN;
+    }
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    la::DecayArgs a;
+    a.decay = decay;
+    a.H = H;
+    a.T = T;
+    a.status = status_word();
+    if (!a.status) return LA_ERR_CUDA;
+    const la::DecaySweep sw = forward_sweep(q, k, v, S0, r, dv, scale, y, S_out);
+    return from_cuda(la::launch_decay_rec(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st));
+}
+
+la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                                  const float *S0, const int *cu_seqlens, int B, int H, int total_T, int r, int dv,
+                                  float scale, void *y, float *S_out, la_stream_t stream)
+{
+    if (!decay || !cu_seqlens || !S_out || (total_T > 0 && (!q || !k || !v || !y))) return LA_ERR_NULL;
+    if (const la_status e = check_decay_sizes(dtype, B, H, total_T, r, dv, scale)) return e;
+    if ((long long)total_T * H > 0x7fffffffLL) return LA_ERR_SHAPE;
+    for (const void *p : {q, k, v, (const void *)y})
+        if (!elem_aligned(p, dtype)) return LA_ERR_ALIGN;
+    for (const void *p : {(const void *)decay, (const void *)S0, (const void *)S_out, (const void *)cu_seqlens})
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    la::DecayArgs a;
+    a.decay = decay;
+    a.cu_seqlens = cu_seqlens;
+    a.H = H;
+    a.T = total_T;
+    a.status = status_word();
+    if (!a.status) return LA_ERR_CUDA;
+    const la::DecaySweep sw = forward_sweep(q, k, v, S0, r, dv, scale, y, S_out);
+    return from_cuda(la::launch_decay_rec(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st));
+}
+
+la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                               float *S, int B, int H, int r, int dv, float scale, void *y, la_stream_t stream)
+{
+    if (!q || !k || !v || !decay || !S || !y) return LA_ERR_NULL;
+    if (const la_status e = check_decay_sizes(dtype, B, H, 1, r, dv, scale)) return e;
+    for (const void *p : {q, k, v, (const void *)y})
+        if (!elem_aligned(p, dtype)) return LA_ERR_ALIGN;
+    if (!aligned(decay, 4) || !aligned(S, 4)) return LA_ERR_ALIGN;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dv % 4 == 0 && aligned(S, 16) && (long long)B * H <= 0x7fffffffLL)
+        return from_cuda(la::launch_decay_decode(q, k, v, dtype == LA_DTYPE_BF16, decay, S, B, H, r, dv, scale, y, st));
+    la::DecayArgs a;
+    a.decay = decay;
+    a.H = H;
+    a.T = 1;
+    const la::DecaySweep sw = forward_sweep(q, k, v, S, r, dv, scale, y, S);
+    return from_cuda(la::launch_decay_rec(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st));
+}
+
+size_t la_decay_backward_workspace_bytes(int, int, int, int, int, la_dtype) { return 0; }
+
+la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
+                            const float *S0, int B, int H, int T, int r, int dv, float scale, const void *dy,
+                            const float *dS_T, void *dq, void *dk, void *dv_out, float *dS0, void *workspace,
+                            size_t workspace_bytes, la_stream_t stream)
+{
+    if (!decay || !dS0 || (T > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv_out))) return LA_ERR_NULL;
+    if (const la_status e = check_decay_sizes(dtype, B, H, T, r, dv, scale)) return e;
+    for (const void *p : {q, k, v, dy, (const void *)dq, (const void *)dk, (const void *)dv_out})
+        if (!elem_aligned(p, dtype)) return LA_ERR_ALIGN;
+    for (const void *p : {(const void *)decay, (const void *)S0, (const void *)dS_T, (const void *)dS0})
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    const size_t need = la_decay_backward_workspace_bytes(B, H, T, r, dv, dtype);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return LA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return LA_ERR_ALIGN;
+    }
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    la::DecayArgs a;
+    a.decay = decay;
+    a.H = H;
+    a.T = T;
+    a.status = status_word();
+    if (!a.status) return LA_ERR_CUDA;
+    la::DecaySweep sw[3];
+    sw[0].a = dy, sw[0].b = v, sw[0].c = k, sw[0].out = dq;     // dq
+    sw[0].S_init = S0, sw[0].init_t = true;
+    sw[0].ra = dv, sw[0].n = r;
+    sw[0].out_scale = scale;
+    sw[1].a = v, sw[1].b = dy, sw[1].c = q, sw[1].out = dk;     // dk
+    sw[1].S_init = dS_T, sw[1].init_t = true;
+    sw[1].ra = dv, sw[1].n = r;
+    sw[2].a = k, sw[2].b = q, sw[2].c = dy, sw[2].out = dv_out; // dv
+    sw[2].S_init = dS_T, sw[2].S_fin = dS0;
+    sw[2].ra = r, sw[2].n = dv;
+    for (int i = 1; i < 3; ++i) {
+        sw[i].rev = sw[i].late = true;
+        sw[i].write_scale = scale;
+    }
+    return from_cuda(la::launch_decay_rec(sw, 3, a, dtype == LA_DTYPE_BF16, B, st));
+}
+
+la_status la_beam_select(const void *logits, la_dtype dtype, long long row_stride, const float *scores,
+                         const unsigned char *done, int B, int K, int V, int eos, float *next_scores, int *parents,
+                         int *tokens, unsigned char *done_out, la_stream_t stream)
+{
+    if (!logits || !scores || !next_scores || !parents || !tokens) return LA_ERR_NULL;
+    if (B < 1 || K < 1 || V < 1 || row_stride < V || eos < -1 || eos >= V || (done && eos < 0)) return LA_ERR_SHAPE;
+    if (dtype != LA_DTYPE_BF16 && dtype != LA_DTYPE_FP32) return LA_ERR_DTYPE;
+    if (K > la::kMaxBeams || V > (1 << 30) || B > 65535) return LA_ERR_UNSUPPORTED;
+    // byte offsets of the rows stay in 63 bits
+    if (row_stride > (1LL << 60) / ((long long)B * K)) return LA_ERR_SHAPE;
+    if (!elem_aligned(logits, dtype)) return LA_ERR_ALIGN;
+    for (const void *p : {(const void *)scores, (const void *)next_scores, (const void *)parents, (const void *)tokens})
+        if (!aligned(p, 4)) return LA_ERR_ALIGN;
+    la::BeamSelectArgs a;
+    a.logits = logits;
+    a.row_stride = row_stride;
+    a.scores = scores;
+    a.done = done;
+    a.next_scores = next_scores;
+    a.parents = parents;
+    a.tokens = tokens;
+    a.done_out = done_out;
+    a.K = K;
+    a.V = V;
+    a.eos = eos;
+    return from_cuda(la::launch_beam_select(a, B, dtype == LA_DTYPE_BF16, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+la_status la_state_reorder(const float *S, const float *z, const int *parents, int B, int K, int H, int r, int dv,
+                           float *S_out, float *z_out, la_stream_t stream)
+{
+    if (!S || !S_out || !parents || !z != !z_out) return LA_ERR_NULL;
+    if (B < 1 || K < 1 || H < 1 || r < 1 || dv < 1) return LA_ERR_SHAPE;
+    if (K > la::kMaxBeams || B > 65535) return LA_ERR_UNSUPPORTED;
+    const long long z_len = (long long)H * r;
+    // one thread per word of a slot, 2^31 blocks of 256 at most
+    if (z_len > (1LL << 38) / (dv + 1LL)) return LA_ERR_UNSUPPORTED;
+    for (const void *p : {(const void *)S, (const void *)z, (const void *)parents, (const void *)S_out, (const void *)z_out})
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    int *status = status_word();
+    if (!status) return LA_ERR_CUDA;
+    return from_cuda(la::launch_state_reorder(S, z, parents, B, K, z_len * dv, z_len, S_out, z_out, status,
+                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
 la_status la_last_device_status(la_stream_t stream)

@@ -1,0 +1,403 @@
+// beam.cu -- what a beam search does between two decode steps: choose the best
+// K of a request's K beams x V tokens, and move the beams' states after the choice.
+
+#include "decay.h"
+#include "sm103_ptx.cuh"
+
+#include <cuda_bf16.h>
+
+namespace la {
+namespace {
+
+// ------------------------------------------------------------- beam select
+// Candidate (k, v) of a request scores  score_k + x_kv - lse_k,  lse_k = log sum_v
+// exp x_kv.  Within a beam the candidates rank as its logits do, so one pass over
+// a row yields both its log-sum-exp (running maximum and sum per lane) and its
+// best K logits; K * K finalists then settle the request.
+//
+// One cluster of CS CTAs of 16 warps per request.  Warp gw of the cluster's 16 CS
+// takes part gw / K of row gw % K: 512-byte blocks, every (parts)-th one.  A warp keeps
+// the best 32 (logit, index) pairs it has seen sorted across its lanes, as 64-bit
+// keys that order by logit, then by lower index; a block without a logit as
+// high as the K-th key costs one vote.  On random logits a warp inserts about
+// K ln(n / K) of its n values.
+// After the cluster barrier warp w of CTA c merges the parts of row 16 c + w (over
+// distributed shared memory) and leaves the row's K keys and its lse in CTA 0;
+// after the second one a warp of CTA 0 picks the request's K best by the scores
+// in 64 bits, one head per row.
+constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps;
+
+struct SelSmem {
+    unsigned long long keys[kSelWarps][kMaxBeams];        // each warp's best, best first (0: none)
+    float m[kSelWarps], s[kSelWarps];                     // running maximum and sum of its part
+    // CTA 0 only: the rows' best and their lse
+    unsigned long long row_keys[kMaxBeams][kMaxBeams];
+    double row_lse[kMaxBeams];
+};
+
+// Order-preserving map of a float (not NaN) to unsigned; -0 counts as +0.
+__device__ __forceinline__ uint32_t order_f32(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unorder_f32(uint32_t o)
+{
+    return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ unsigned long long order_f64(double x)
+{
+    const unsigned long long u = __double_as_longlong(x + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ unsigned long long make_key(float x, int i)
+{
+    return (static_cast<unsigned long long>(order_f32(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
+}
+__device__ __forceinline__ int key_index(unsigned long long k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
+__device__ __forceinline__ float key_value(unsigned long long k) { return unorder_f32(static_cast<uint32_t>(k >> 32)); }
+
+// Largest key of the warp (every lane gets it).
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
+{
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+    return (static_cast<unsigned long long>(hi) << 32) | lo;
+}
+
+// Distributed shared memory: the generic address of `p` in CTA `rank` of the cluster.
+template <typename T>
+__device__ __forceinline__ T *in_cta(T *p, uint32_t rank)
+{
+    uint64_t out;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<T *>(out);
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 ld_once(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// The 16 bytes of a row's granule, whatever the row's alignment: `mis` bytes
+// (a multiple of the element size) past the 16-byte boundary p0, from the one or two
+// aligned words that hold them.  The second is read only when the row reaches it.
+__device__ __forceinline__ uint4 load_granule(const unsigned char *p0, int mis, long long g, long long row_bytes)
+{
+    const uint4 *p = reinterpret_cast<const uint4 *>(p0) + g;
+    const uint4 a = mis ? *p : ld_once(p);
+    if (!mis) return a;
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (16 * (g + 1) < mis + row_bytes) b = p[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t v[5], o[4];
+    const int ws = mis >> 2, sh = (mis & 3) * 8;   // (warp-uniform)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = ws == 0 ? w[i] : ws == 1 ? w[i + 1 < 8 ? i + 1 : 7] : ws == 2 ? w[i + 2 < 8 ? i + 2 : 7] : w[i + 3 < 8 ? i + 3 : 7];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(v[i], v[i + 1], sh);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen(uint4 w, float *x)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        } else {
+            x[i] = __uint_as_float(u[i]);
+        }
+    }
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <bool BF16>
+__global__ void __launch_bounds__(kSelThreads, 2)
+beam_select_kernel(const BeamSelectArgs args)
+{
+    constexpr int GE = BF16 ? 8 : 4;       // elements of a 16-byte granule
+    constexpr int U = 4;                   // granules in flight per lane
+    __shared__ SelSmem sm;
+    const int K = args.K, V = args.V;
+    const uint32_t rank = blockIdx.x, cs = gridDim.x;   // the cluster spans the grid's x axis
+    const int b = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nw = kSelWarps * cs;
+    {
+        // phase 1: this warp's part of one row
+        const int gw = rank * kSelWarps + warp;
+        const int k = gw % K, part = gw / K, parts = (nw - k + K - 1) / K;
+        const bool skip = args.done && args.done[(size_t)b * K + k];
+        const unsigned char *row = reinterpret_cast<const unsigned char *>(args.logits) +
+                                   ((long long)b * K + k) * args.row_stride * (BF16 ? 2 : 4);
+        const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+        const unsigned char *p0 = row - mis;
+        const long long row_bytes = (long long)V * (BF16 ? 2 : 4);
+        const int granules = (V + GE - 1) / GE;
+        float m = -3.402823466e38f, s = 0.f;
+        unsigned long long key = 0, thr = 0;   // this lane's entry; the K-th entry
+        float thr_x = -INFINITY;
+        auto consume = [&](uint4 raw, int i0) {
+            float x[GE];
+            widen<BF16>(raw, x);
+            if (i0 + GE > V) {
+#pragma unroll
+                for (int e = 0; e < GE; ++e)
+                    if (i0 + e >= V) x[e] = -INFINITY;
+            }
+            float mx = x[0];
+#pragma unroll
+            for (int e = 1; e < GE; ++e) mx = fmaxf(mx, x[e]);   // (a NaN reaches the sum below)
+            if (mx > m) {
+                s *= exp2f((m - mx) * kLog2e);
+                m = mx;
+            }
+            float t = 0.f;
+#pragma unroll
+            for (int e = 0; e < GE; ++e) t += exp2f((x[e] - m) * kLog2e);
+            s += t;
+            if (__any_sync(0xffffffffu, mx >= thr_x && mx > -INFINITY)) {
+#pragma unroll 1
+                for (int e = 0; e < GE; ++e) {
+                    float xe = x[0];
+#pragma unroll
+                    for (int f = 1; f < GE; ++f) xe = e == f ? x[f] : xe;
+                    const unsigned long long mine = xe > -INFINITY ? make_key(xe, i0 + e) : 0;
+                    uint32_t todo = __ballot_sync(0xffffffffu, mine > thr);
+                    while (todo) {
+                        const int src = __ffs(todo) - 1;
+                        const unsigned long long nk = __shfl_sync(0xffffffffu, mine, src);
+                        const int at = __popc(__ballot_sync(0xffffffffu, key > nk));
+                        const unsigned long long up = __shfl_up_sync(0xffffffffu, key, 1);
+                        key = lane > at ? up : lane == at ? nk : key;
+                        thr = __shfl_sync(0xffffffffu, key, K - 1);
+                        todo &= todo - 1;
+                        todo &= __ballot_sync(0xffffffffu, mine > thr);
+                    }
+                }
+                if (thr) thr_x = key_value(thr);
+            }
+        };
+        const int step = parts * 32;
+        if (!skip) {
+            int g = part * 32 + lane;
+            // (every lane runs the same number of steps: the votes below take the whole warp)
+            for (int base = part * 32; base < granules; base += U * step, g += U * step) {
+                uint4 raw[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (g + u * step < granules) raw[u] = load_granule(p0, mis, g + u * step, row_bytes);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (base + u * step >= granules) break;
+                    const int gu = g + u * step;
+                    consume(gu < granules ? raw[u] : make_uint4(0, 0, 0, 0), gu < granules ? gu * GE : V);
+                }
+            }
+        }
+        // the part's maximum and sum
+        float mw = m;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+        s *= exp2f((m - mw) * kLog2e);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane < K) sm.keys[warp][lane] = key;
+        if (lane == 0) sm.m[warp] = mw, sm.s[warp] = s;
+    }
+    cluster_sync_all();
+    // phase 2: merge a row's parts (rows over CTAs first, then over warps)
+    for (int k = rank + cs * warp; k < K; k += cs * kSelWarps) {
+        const int parts = (nw - k + K - 1) / K;
+        SelSmem *home = in_cta(&sm, 0);
+        // lse from the parts' maxima and sums
+        float mx = -3.402823466e38f;
+        for (int i = lane; i < parts; i += 32) {
+            const int gw = k + i * K;
+            mx = fmaxf(mx, in_cta(&sm, gw / kSelWarps)->m[gw % kSelWarps]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        double sum = 0.0;
+        for (int i = lane; i < parts; i += 32) {
+            const int gw = k + i * K;
+            SelSmem *at = in_cta(&sm, gw / kSelWarps);
+            sum += (double)at->s[gw % kSelWarps] * exp2(((double)at->m[gw % kSelWarps] - (double)mx) * 1.4426950408889634);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) home->row_lse[k] = (double)mx + log(sum);
+        // each lane looks after the sorted lists of parts lane, lane + 32, ..: K rounds of
+        // taking the largest head
+        unsigned long long head[4];
+        int pos[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = lane + 32 * u, gw = k + i * K;
+            pos[u] = 0;
+            head[u] = i < parts ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][0] : 0;
+        }
+        for (int r = 0; r < K; ++r) {
+            unsigned long long best = head[0];
+#pragma unroll
+            for (int u = 1; u < 4; ++u) best = head[u] > best ? head[u] : best;
+            best = warp_max(best);
+            if (lane == 0) home->row_keys[k][r] = best;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (best && head[u] == best) {   // (keys differ: one list holds it)
+                    const int gw = k + (lane + 32 * u) * K;
+                    head[u] = ++pos[u] < K ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][pos[u]] : 0;
+                }
+        }
+    }
+    cluster_sync_all();
+    if (rank != 0 || warp != 0) return;
+    // phase 3: lane k holds the head of row k; K rounds of taking the best score
+    const int k = lane;
+    const size_t bk = (size_t)b * K;
+    const double score = k < K ? (double)args.scores[bk + k] : 0.0;
+    const bool ended = k < K && args.done && args.done[bk + k];
+    const double lse = k < K ? sm.row_lse[k] : 0.0;
+    const bool usable = k < K && isfinite(score) && (ended || isfinite(lse));
+    int pos = 0;
+    double cand = 0.0;
+    int token = 0;
+    unsigned long long ord = 0;   // 0: no candidate left
+    auto load_head = [&]() {
+        ord = 0;
+        if (!usable || pos >= K) return;
+        if (ended) {
+            if (pos == 0) cand = score, token = args.eos, ord = order_f64(cand);
+            return;
+        }
+        const unsigned long long key = sm.row_keys[k][pos];
+        if (!key) return;
+        cand = score + (double)key_value(key) - lse;
+        token = key_index(key);
+        ord = order_f64(cand);
+    };
+    load_head();
+    float my_next = -INFINITY;
+    int my_parent = lane, my_token = 0;
+    bool my_end = ended;
+    for (int r = 0; r < K; ++r) {
+        const unsigned long long best = warp_max(ord);
+        if (!best) break;
+        const int win = __ffs(__ballot_sync(0xffffffffu, ord == best)) - 1;   // equal scores: the lower row
+        const double c = __shfl_sync(0xffffffffu, cand, win);
+        const int tk = __shfl_sync(0xffffffffu, token, win);
+        const bool was = __shfl_sync(0xffffffffu, ended ? 1 : 0, win) != 0;
+        if (lane == r) my_next = (float)c, my_parent = win, my_token = tk, my_end = was || tk == args.eos;
+        if (lane == win) ++pos, load_head();
+    }
+    // every lane has read its scores and flags: the outputs may lie over them
+    __syncwarp();
+    if (lane < K) {
+        args.next_scores[bk + lane] = my_next;
+        args.parents[bk + lane] = my_parent;
+        args.tokens[bk + lane] = my_token;
+        if (args.done_out) args.done_out[bk + lane] = my_end ? 1 : 0;
+    }
+}
+
+// ------------------------------------------------------------ state reorder
+// Slot j of a request becomes its slot parents[j].  A thread takes one word of
+// the slots: it loads that word of every parent of a slot that changes and then stores
+// them, so the move may be in place (no thread touches another's word) and a
+// parent that several slots share is read from HBM once.  A slot that keeps its
+// state is neither read (for itself) nor written when the move is in place.
+template <typename W, int KM>
+__global__ void __launch_bounds__(256)
+state_reorder_kernel(const W *S, const W *z, const int *__restrict__ parents, int K, long long s_len,
+                     long long z_len, unsigned s_blocks, W *S_out, W *z_out, int *status)
+{
+    const int b = blockIdx.y;
+    const bool norm = blockIdx.x >= s_blocks;
+    const W *src = norm ? z : S;
+    W *dst = norm ? z_out : S_out;
+    const long long len = norm ? z_len : s_len;
+    const long long e = (long long)(blockIdx.x - (norm ? s_blocks : 0)) * blockDim.x + threadIdx.x;
+    const int *par = parents + (size_t)b * K;
+    if (blockIdx.x == 0 && threadIdx.x < K && static_cast<unsigned>(par[threadIdx.x]) >= static_cast<unsigned>(K))
+        atomicExch(status, kStatusShape);
+    if (e >= len) return;
+    const size_t base = (size_t)b * K * len + e;
+    const bool in_place = src == dst;
+    W v[KM];
+    uint32_t moved = 0;
+#pragma unroll
+    for (int j = 0; j < KM; ++j) {
+        if (j >= K) continue;
+        const int p = par[j];
+        if (static_cast<unsigned>(p) >= static_cast<unsigned>(K) || (in_place && p == j)) continue;
+        v[j] = src[base + (size_t)p * len];
+        moved |= 1u << j;
+    }
+#pragma unroll
+    for (int j = 0; j < KM; ++j)
+        if (moved >> j & 1) dst[base + (size_t)j * len] = v[j];
+}
+
+template <typename W>
+cudaError_t launch_reorder(const W *S, const W *z, const int *parents, int B, int K, long long s_len, long long z_len,
+                           W *S_out, W *z_out, int *status, cudaStream_t stream)
+{
+    const long long sb = (s_len + 255) / 256, zb = z ? (z_len + 255) / 256 : 0;
+    const dim3 grid((unsigned)(sb + zb), B);
+    auto run = [&](auto kern) {
+        kern<<<grid, 256, 0, stream>>>(S, z, parents, K, s_len, z_len, (unsigned)sb, S_out, z_out, status);
+    };
+    if (K <= 4) run(state_reorder_kernel<W, 4>);
+    else if (K <= 8) run(state_reorder_kernel<W, 8>);
+    else if (K <= 16) run(state_reorder_kernel<W, 16>);
+    else run(state_reorder_kernel<W, 32>);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_beam_select(const BeamSelectArgs &a, int B, bool bf16, int sms, cudaStream_t stream)
+{
+    // CTAs per request: as many as keep the batch within the 2 per SM that are resident
+    int cs = 8;
+    while (cs > 2 && (long long)B * cs > 2LL * sms) cs >>= 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cs, B, 1);
+    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return bf16 ? cudaLaunchKernelEx(&cfg, beam_select_kernel<true>, a)
+                : cudaLaunchKernelEx(&cfg, beam_select_kernel<false>, a);
+}
+
+cudaError_t launch_state_reorder(const float *S, const float *z, const int *parents, int B, int K, long long s_len,
+                                 long long z_len, float *S_out, float *z_out, int *status, cudaStream_t stream)
+{
+    auto ok = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    if (s_len % 4 == 0 && ok(S) && ok(S_out) && (!z || (z_len % 4 == 0 && ok(z) && ok(z_out))))
+        return launch_reorder(reinterpret_cast<const float4 *>(S), reinterpret_cast<const float4 *>(z), parents, B, K,
+                              s_len / 4, z_len / 4, reinterpret_cast<float4 *>(S_out), reinterpret_cast<float4 *>(z_out),
+                              status, stream);
+    return launch_reorder(S, z, parents, B, K, s_len, z_len, S_out, z_out, status, stream);
+}
+
+}  // namespace la
