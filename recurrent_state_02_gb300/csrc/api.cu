@@ -815,6 +815,64 @@ la::DecaySweep forward_sweep(const void *q, const void *k, const void *v, const 
     return s;
 }
 
+// Sequences of at most this many tokens take the token recurrence.
+#ifndef LA_DECAY_WALK
+#define LA_DECAY_WALK 32
+#endif
+constexpr int kDecayWalk = LA_DECAY_WALK;
+
+bool tc_sweep(const la::DecaySweep &s, bool bf16)
+{
+    if (!bf16 || (s.ra != 64 && s.ra != 128) || s.n % 64 != 0) return false;
+    for (const void *p : {s.a, s.b, s.c, (const void *)s.out})
+        if (!aligned(p, 16)) return false;
+    return true;
+}
+
+// Runs the sweeps of one call, each on the kernel that takes it.
+la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a, bool bf16, int B, cudaStream_t st)
+{
+    const bool packed = a.cu_seqlens != nullptr;
+    la::DecaySweep rest[3];
+    int nrest = 0, ntc = 0;
+    bool tc[3] = {};
+    for (int i = 0; i < count; ++i) {
+        tc[i] = a.T > kDecayWalk && tc_sweep(sw[i], bf16);
+        ntc += tc[i];
+        if (!tc[i] || packed) rest[nrest++] = sw[i];
+    }
+    if (nrest) {
+        la::DecayArgs ar = a;
+        if (packed && ntc) ar.len_max = kDecayWalk;   // (a packed call has one sweep)
+        const cudaError_t e = la::launch_decay_rec(rest, nrest, ar, bf16, B, st);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    for (int ra = 64; ra <= 128 && ntc; ra += 64) {
+        la::DecayTcParams p;
+        p.d = a;
+        p.d.len_min = kDecayWalk + 1;
+        p.B = B;
+        int m = 0;
+        for (int i = 0; i < count; ++i) {
+            if (!tc[i] || sw[i].ra != ra) continue;
+            const la::DecaySweep &s = sw[i];
+            auto map = [&](CUtensorMap *t, const void *ptr, int cols) {
+                return packed ? make_map_bf16_tok(t, ptr, a.T, a.H, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)
+                              : make_map_bf16(t, ptr, (long long)B * a.H, a.T, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+            };
+            if (!map(&p.maps[m].a, s.a, s.ra) || !map(&p.maps[m].b, s.b, s.ra) || !map(&p.maps[m].c, s.c, s.n) ||
+                !map(&p.maps[m].out, s.out, s.n))
+                return LA_ERR_CUDA;
+            p.sw[m] = s;
+            p.tiles[m++] = s.n / 64;
+        }
+        if (!m) continue;
+        const cudaError_t e = la::launch_decay_tc(p, ra, st);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    return LA_OK;
+}
+
 }  // namespace
 
 size_t la_decay_prefill_workspace_bytes(int, int, int, int, int, la_dtype) { return 0; }
@@ -842,7 +900,7 @@ la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype
     a.status = status_word();
     if (!a.status) return LA_ERR_CUDA;
     const la::DecaySweep sw = forward_sweep(q, k, v, S0, r, dv, scale, y, S_out);
-    return from_cuda(la::launch_decay_rec(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st));
+    return run_sweeps(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st);
 }
 
 la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
@@ -865,7 +923,7 @@ la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, l
     a.status = status_word();
     if (!a.status) return LA_ERR_CUDA;
     const la::DecaySweep sw = forward_sweep(q, k, v, S0, r, dv, scale, y, S_out);
-    return from_cuda(la::launch_decay_rec(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st));
+    return run_sweeps(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st);
 }
 
 la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
@@ -927,7 +985,7 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
         sw[i].rev = sw[i].late = true;
         sw[i].write_scale = scale;
     }
-    return from_cuda(la::launch_decay_rec(sw, 3, a, dtype == LA_DTYPE_BF16, B, st));
+    return run_sweeps(sw, 3, a, dtype == LA_DTYPE_BF16, B, st);
 }
 
 la_status la_beam_select(const void *logits, la_dtype dtype, long long row_stride, const float *scores,

@@ -41,6 +41,23 @@ struct DecayArgs {
 cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArgs &a, bool bf16, int B,
                              cudaStream_t stream);
 
+// The same sweeps in chunks of 128 tokens on the tensor cores (decay_tc.cu): BF16, every
+// sweep with the same ra (64 or 128), n a multiple of 64, late == rev, arrays 16-byte
+// aligned.  Maps: boxes of 64 columns x 128 tokens with the 128-byte swizzle over
+// [B*H, T, d], or [tokens, H, d] when packed.
+struct TcSweepMaps {
+    CUtensorMap a, b, c, out;
+};
+struct alignas(64) DecayTcParams {
+    TcSweepMaps maps[3];
+    DecaySweep sw[3];
+    int tiles[3] = {};     // 64-column tiles of each sweep
+    DecayArgs d;
+    int B = 0;
+    unsigned long long wait_limit_ns = kWaitLimitNs;
+};
+cudaError_t launch_decay_tc(const DecayTcParams &p, int ra, cudaStream_t stream);
+
 // One token, S in place: S <- g S + k v^T, y = scale q^T S.  dv a multiple of 4, S and
 // v 4-element aligned, r <= 256.
 cudaError_t launch_decay_decode(const void *q, const void *k, const void *v, bool bf16, const float *decay, float *S,
