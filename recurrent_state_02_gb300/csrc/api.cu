@@ -860,8 +860,7 @@ la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a
                 return packed ? make_map_bf16_tok(t, ptr, a.T, a.H, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)
                               : make_map_bf16(t, ptr, (long long)B * a.H, a.T, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
             };
-            if (!map(&p.maps[m].a, s.a, s.ra) || !map(&p.maps[m].b, s.b, s.ra) || !map(&p.maps[m].c, s.c, s.n) ||
-                !map(&p.maps[m].out, s.out, s.n))
+            if (!map(&p.maps[m].a, s.a, s.ra) || !map(&p.maps[m].b, s.b, s.ra) || !map(&p.maps[m].c, s.c, s.n))
                 return LA_ERR_CUDA;
             p.sw[m] = s;
             p.tiles[m++] = s.n / 64;

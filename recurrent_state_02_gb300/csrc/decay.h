@@ -46,9 +46,9 @@ cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArg
 // aligned.  Maps: boxes of 64 columns x 128 tokens with the 128-byte swizzle over
 // [B*H, T, d], or [tokens, H, d] when packed.
 struct TcSweepMaps {
-    CUtensorMap a, b, c, out;
+    CUtensorMap a, b, c;
 };
-struct alignas(64) DecayTcParams {
+struct DecayTcParams {
     TcSweepMaps maps[3];
     DecaySweep sw[3];
     int tiles[3] = {};     // 64-column tiles of each sweep

@@ -12,7 +12,7 @@
 //     Yi  = P C                      M=128 N=64  K=128  (P from TMEM)
 //     Ye  = A S                      M=128 N=64  K=ra   (S as BF16)
 //     dS  = B^T [Ch | Cl]            M=ra  N=128 K=128  (Ch + Cl = diag(w g^..) C in two BF16 parts)
-// and out = s_in Yi + s_out g^.. Ye leaves through a TMA store.
+// and out = s_in Yi + s_out g^.. Ye leaves from registers, whole 32-byte sectors a thread.
 //
 // The state is FP32 in the registers of four warps: after each chunk S <- g^n S + dS
 // (both halves), so that its rounding is that of one FP32 sum per chunk.  Two
@@ -24,9 +24,10 @@
 // exponents >= 0; a diagonal block looks its powers up.  So every g in 0 .. 1 (0 too)
 // takes the same path, and what underflows is negligible next to the diagonal.
 //
-// One CTA owns one (b, h, 64 columns of c) and walks its chunks.  18 warps: TMA
-// producer, MMA issuer, and four groups of four (each warp reaches the TMEM lanes of its
-// quadrant, warp % 4): scores, weighted values, state, outputs.
+// One CTA owns one (b, h, 64 columns of c) and walks its chunks.  Four warpgroups (each of a
+// group's warps reaches the TMEM lanes of its quadrant): TMA producer and three MMA
+// issuers (scores, dS, outputs, so that none waits for another's operands); scores; weighted values and
+// outputs; state.
 #include "decay.h"
 #include "tc_common.cuh"
 
@@ -34,10 +35,11 @@ namespace la {
 namespace {
 
 constexpr int kCT = 128;                       // tokens per chunk
-constexpr int kThreads = 18 * 32;
-constexpr int kWarpTma = 0, kWarpMma = 1, kGroupP = 2, kGroupC = 6, kGroupS = 10, kGroupY = 14;   // first warps
+constexpr int kThreads = 512;
+// registers per thread after the split (launched with 128): 56 + 128 + 128 + 200 = 4 * 128
+constexpr int kRegsIssue = 56, kRegsState = 200;
 constexpr uint32_t kBlk = kCT * 128;           // 16 KB: 128 rows x 64 BF16 columns, 128-byte swizzle
-constexpr int kNST = 2;
+constexpr int kStC = 3;                        // stages of c (a and b have two)
 
 // TMEM columns
 constexpr uint32_t kColP = 0, kColYi = 256, kColYe = 320, kColDS = 384;
@@ -45,27 +47,68 @@ constexpr uint32_t kColP = 0, kColYi = 256, kColYe = 320, kColDS = 384;
 template <int KD>
 struct Lay {
     static constexpr int NB = KD / 64;                       // 64-column blocks of a and b
-    static constexpr uint32_t kA = 0, kB = NB * kBlk, kC = 2 * NB * kBlk;
-    static constexpr uint32_t kStage = (2 * NB + 1) * kBlk;
-    static constexpr uint32_t kOffW = kNST * kStage;         // weighted values: Ch, Cl
-    static constexpr uint32_t kOffS = kOffW + 2 * kBlk;      // the state as BF16 [KD x 64]
-    static constexpr uint32_t kOffY = kOffS + KD * 128;      // output tile
-    static constexpr uint32_t kOffSmall = kOffY + kBlk;
+    static constexpr uint32_t kTile = NB * kBlk;
+    static constexpr uint32_t kOffA = 0, kOffB = 2 * kTile, kOffC = 4 * kTile;
+    static constexpr uint32_t kOffW = kOffC + kStC * kBlk;   // weighted values: Ch, Cl
+    static constexpr uint32_t kOffS = kOffW + 2 * kBlk;      // the state as BF16 [128 x 64] (KD rows are read)
+    static constexpr uint32_t kOffSmall = kOffS + kBlk;
 };
 
 struct alignas(16) SmallD {
-    uint64_t fullA[kNST], fullB[kNST], fullC[kNST], emptyA[kNST], emptyB[kNST], emptyC[kNST];
-    uint64_t p_raw[2], p_ready[2], w_full, w_empty, ds_full, ds_empty, s_full, s_empty, y_full, y_empty, t_free, t_full, done;
+    uint64_t fullA[2], fullB[2], fullC[kStC], emptyA[2], emptyB[2], emptyC[kStC];
+    uint64_t p_raw[2], p_ready[2], p_free[2], w_full, w_empty, ds_full, ds_empty, s_full, s_empty, y_full, y_empty, done[3];
     uint32_t tmem_base;
     int abort_flag;
-    int seq;
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
-    alignas(16) float col[32];         // a block's column powers
 };
 
 template <int KD>
 constexpr uint32_t smem_bytes() { return Lay<KD>::kOffSmall + sizeof(SmallD) + 1024; }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory budget");
+
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Waits for this thread's TMEM loads; the values pass through, so that no use of them moves ahead of the wait.
+template <int N>
+__device__ __forceinline__ void wait_loaded(float (&v)[N])
+{
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// Bounded waits as in tc_common.cuh, short enough to be inlined everywhere: by one thread, or by a whole
+// warp (which stays converged).  False when the limit ran out or another thread has given up.
+template <bool WARP>
+__device__ __forceinline__ bool bounded_wait(const Ctx &cx, uint64_t *bar, uint32_t parity)
+{
+    auto all = [](bool x) { return WARP ? __all_sync(0xffffffffu, x) != 0 : x; };
+    if (all(mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    bool go = true;
+    while (go) {
+        if (all(mbar_try_wait_hint(bar, parity, kWaitHintNs))) return true;
+        go = all(!aborted(cx) && global_timer_ns() - t0 <= cx.limit);
+    }
+    if (!aborted(cx)) {
+        atomicExch(cx.status, kStatusTimeout);
+        *reinterpret_cast<volatile int *>(cx.abort_flag) = 1;
+    }
+    return false;
+}
+__device__ __forceinline__ bool wait1(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<false>(cx, bar, parity); }
+__device__ __forceinline__ bool waitw(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<true>(cx, bar, parity); }
+
+// 32 bytes to global memory (32-byte aligned).
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 
 // D[tmem] (+)= A[tmem] * B[smem]
 template <bool ACC>
@@ -78,17 +121,6 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
-}
-
-// 32 lanes x 32 bits, 8 consecutive columns.
-__device__ __forceinline__ void tc_ld_x8(uint32_t taddr, float (&v)[8])
-{
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void tc_st_x16(uint32_t taddr, const uint32_t (&r)[16])
@@ -137,11 +169,18 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
 
     // ------------------------------------------------------------ set-up
     if (tid == 0) {
-        for (int s = 0; s < kNST; ++s) {
-            for (uint64_t *bar : {&sm->fullA[s], &sm->fullB[s], &sm->fullC[s], &sm->emptyA[s], &sm->emptyB[s], &sm->emptyC[s]})
-                mbar_init(bar, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm->fullA[s], 1);
+            mbar_init(&sm->fullB[s], 1);
+            mbar_init(&sm->emptyA[s], 2);      // read by the scores and by Ye
+            mbar_init(&sm->emptyB[s], 2);      // read by the scores and by dS
             mbar_init(&sm->p_raw[s], 1);
             mbar_init(&sm->p_ready[s], 4);
+            mbar_init(&sm->p_free[s], 1);
+        }
+        for (int s = 0; s < kStC; ++s) {
+            mbar_init(&sm->fullC[s], 1);
+            mbar_init(&sm->emptyC[s], 5);      // read by Yi and by the four warps that weight it
         }
         mbar_init(&sm->w_full, 4);
         mbar_init(&sm->w_empty, 1);
@@ -151,30 +190,26 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         mbar_init(&sm->s_empty, 1);
         mbar_init(&sm->y_full, 1);
         mbar_init(&sm->y_empty, 4);
-        mbar_init(&sm->t_free, 1);
-        mbar_init(&sm->t_full, 4);
-        mbar_init(&sm->done, 1);
+        for (int i = 0; i < 3; ++i) mbar_init(&sm->done[i], 1);
         sm->abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&maps.a);
         tma_prefetch_desc(&maps.b);
         tma_prefetch_desc(&maps.c);
-        tma_prefetch_desc(&maps.out);
     }
-    if (warp == kWarpMma) {
+    if (warp == 1) {
         tmem_alloc(&sm->tmem_base, 512);
         tmem_relinquish();
     }
-    if (tid >= 64 && tid - 64 <= kCT) {
+    if (tid >= 128 && tid - 128 <= kCT) {
         // powers of g from its repeated squares in 64 bits: each entry is rounded once
-        const int e = tid - 64;
+        const int e = tid - 128;
         double p = 1.0, q = (double)args.d.decay[h];
         for (int bit = 0; bit < 8; ++bit) {
             if (e >> bit & 1) p *= q;
             q *= q;
         }
         sm->pw[e] = (float)p;
-        if (e < 32) sm->col[rev ? e : 31 - e] = (float)p;
     }
     tc_fence_before();
     __syncthreads();
@@ -182,56 +217,67 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     const uint32_t tmem = sm->tmem_base;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int row = (warp & 3) * 32 + lane;     // the TMEM lane, and tile row, of this thread
+    const int group = warp >> 2;
+    constexpr uint32_t kHi = desc_hi(1024, 2);
+    const uint32_t sA = smem_u32(base + L::kOffA), sB = smem_u32(base + L::kOffB), sC = smem_u32(base + L::kOffC);
 
-    if (warp == kWarpTma) {
-        // ------------------------------------------------------- producer
-        int issued = 0;
-        if (lane == 0) {
+    if (group == 0) {
+        regs_dec<kRegsIssue>();
+        if (warp == 0 && lane == 0) {
+            // --------------------------------------------------- producer
+            // loads in the order in which their buffers come free: b and a of chunk c after
+            // chunk c - 2's dS and Ye, c of chunk c after chunk c - 3's Yi
+            auto load = [&](const CUtensorMap *map, uint32_t off, int blocks, int x, uint64_t *bar, int c) {
+                const int t0 = chunk_t0(c), cy = packed ? h : t0, cz = packed ? seq0 + t0 : (int)bh;
+                mbar_arrive_expect_tx(bar, blocks * kBlk);
+                for (int k = 0; k < blocks; ++k) tma_load_3d(base + off + k * kBlk, map, bar, x + 64 * k, cy, cz);
+            };
+            // warms L2 for a chunk whose buffers are still in use
+            auto warm = [&](const CUtensorMap *map, int blocks, int x, int c) {
+                const int t0 = chunk_t0(c), cy = packed ? h : t0, cz = packed ? seq0 + t0 : (int)bh;
+                for (int k = 0; k < blocks; ++k) tma_prefetch_l2_3d(map, x + 64 * k, cy, cz);
+            };
+            int nb = 0, na = 0, nc = 0;    // chunks issued
             for (int c = 0; c < nch; ++c) {
-                const int s = c & 1, t0 = chunk_t0(c);
-                const uint32_t ph = ((c >> 1) - 1) & 1;
-                const int cy = packed ? h : t0, cz = packed ? seq0 + t0 : (int)bh;
-                uint8_t *st = base + s * L::kStage;
-                if (c >= kNST && !wait(cx, &sm->emptyB[s], ph)) break;
-                mbar_arrive_expect_tx(&sm->fullB[s], L::NB * kBlk);
-#pragma unroll
-                for (int k = 0; k < L::NB; ++k) tma_load_3d(st + L::kB + k * kBlk, &maps.b, &sm->fullB[s], 64 * k, cy, cz);
-                issued = 3 * c + 1;
-                if (c >= kNST && !wait(cx, &sm->emptyC[s], ph)) break;
-                mbar_arrive_expect_tx(&sm->fullC[s], kBlk);
-                tma_load_3d(st + L::kC, &maps.c, &sm->fullC[s], c0, cy, cz);
-                issued = 3 * c + 2;
-                if (c >= kNST && !wait(cx, &sm->emptyA[s], ph)) break;
-                mbar_arrive_expect_tx(&sm->fullA[s], L::NB * kBlk);
-#pragma unroll
-                for (int k = 0; k < L::NB; ++k) tma_load_3d(st + L::kA + k * kBlk, &maps.a, &sm->fullA[s], 64 * k, cy, cz);
-                issued = 3 * c + 3;
+                const int s = c & 1;
+                if (c >= 2 && !wait1(cx, &sm->emptyB[s], ((c >> 1) - 1) & 1)) break;
+                load(&maps.b, L::kOffB + s * L::kTile, L::NB, 0, &sm->fullB[s], c);
+                nb = c + 1;
+                if (c >= 2 && !wait1(cx, &sm->emptyA[s], ((c >> 1) - 1) & 1)) break;
+                load(&maps.a, L::kOffA + s * L::kTile, L::NB, 0, &sm->fullA[s], c);
+                na = c + 1;
+                bool ok = true;
+                for (; ok && nc < nch && nc <= c + 1; ++nc) {
+                    ok = nc < kStC || wait1(cx, &sm->emptyC[nc % kStC], (nc / kStC - 1) & 1);
+                    if (!ok) break;
+                    load(&maps.c, L::kOffC + (nc % kStC) * kBlk, 1, c0, &sm->fullC[nc % kStC], nc);
+                }
+                if (!ok) break;
+                if (c + 2 < nch) {
+                    if (tile == 0) {       // (the other tiles of the head read the same a, b)
+                        warm(&maps.b, L::NB, 0, c + 2);
+                        warm(&maps.a, L::NB, 0, c + 2);
+                    }
+                    warm(&maps.c, 1, c0, c + 2);
+                }
             }
             if (aborted(cx)) {
                 // every issued load lands before the CTA may exit
-                for (int i = issued > 6 ? issued - 6 : 0; i < issued; ++i) {
-                    const int c = i / 3, k = i % 3;
-                    uint64_t *bar = k == 0 ? &sm->fullB[c & 1] : k == 1 ? &sm->fullC[c & 1] : &sm->fullA[c & 1];
-                    mbar_wait(bar, (c >> 1) & 1, cx.limit);
-                }
+                for (int c = max(0, nb - 2); c < nb; ++c) mbar_wait(&sm->fullB[c & 1], (c >> 1) & 1, cx.limit);
+                for (int c = max(0, na - 2); c < na; ++c) mbar_wait(&sm->fullA[c & 1], (c >> 1) & 1, cx.limit);
+                for (int c = max(0, nc - kStC); c < nc; ++c) mbar_wait(&sm->fullC[c % kStC], (c / kStC) & 1, cx.limit);
             }
-        }
-        __syncwarp();
-    } else if (warp == kWarpMma) {
-        // ------------------------------------------------------------ MMA
-        if (lane == 0) {
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------- MMA: scores
             constexpr uint32_t idP = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t idY = idesc_bf16_f32(128, 64, false, true);
-            constexpr uint32_t idDS = idesc_bf16_f32(128, 128, true, true);
-            constexpr uint32_t kHi = desc_hi(1024, 2);
-            // scores of chunk c; their buffer held P of chunk c - 2, whose product is done
-            auto issue_p = [&](int c) -> bool {
+            for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
-                if (!wait(cx, &sm->fullA[s], (c >> 1) & 1) || !wait(cx, &sm->fullB[s], (c >> 1) & 1)) return false;
-                if (c >= 2 && !wait(cx, &sm->y_full, (c - 2) & 1)) return false;
+                if (!wait1(cx, &sm->fullB[s], (c >> 1) & 1) || !wait1(cx, &sm->fullA[s], (c >> 1) & 1)) break;
+                // the buffer held P of chunk c - 2, whose product is done
+                if (c >= 2 && !wait1(cx, &sm->p_free[s], ((c >> 1) - 1) & 1)) break;
                 tc_fence_after();
-                const uint32_t st = smem_u32(base + s * L::kStage);
-                const uint32_t alo = desc_lo(st + L::kA, 16), blo = desc_lo(st + L::kB, 16), d = tmem + kColP + s * 128;
+                const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(sB + s * L::kTile, 16);
+                const uint32_t d = tmem + kColP + s * 128;
 #pragma unroll
                 for (int k = 0; k < KD / 16; ++k) {
                     const uint32_t o = ((k >> 2) * kBlk + (k & 3) * 32) >> 4;
@@ -239,36 +285,39 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     else tc_mma_bf16_w<true>(d, alo + o, kHi, blo + o, kHi, idP);
                 }
                 tc_commit(&sm->p_raw[s]);
-                return true;
-            };
-            bool ok = nch == 0 || issue_p(0);
-            for (int c = 0; c < nch && ok; ++c) {
+                tc_commit(&sm->emptyA[s]);
+                tc_commit(&sm->emptyB[s]);
+            }
+        } else if (warp == 2 && lane == 0) {
+            // ----------------------------------------------------- MMA: dS
+            constexpr uint32_t idDS = idesc_bf16_f32(128, 128, true, true);
+            for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
-                const uint32_t st = smem_u32(base + s * L::kStage);
-                // dS = B^T [Ch | Cl]
-                if (!wait(cx, &sm->w_full, c & 1)) break;
-                if (c >= 1 && !wait(cx, &sm->ds_empty, (c - 1) & 1)) break;
+                if (!wait1(cx, &sm->fullB[s], (c >> 1) & 1) || !wait1(cx, &sm->w_full, c & 1)) break;
+                if (c >= 1 && !wait1(cx, &sm->ds_empty, (c - 1) & 1)) break;
                 tc_fence_after();
-                {
-                    // (ra = 64: rows 64 .. 127 of the product come from the tile behind b and are not used)
-                    const uint32_t alo = desc_lo(st + L::kB, kBlk), blo = desc_lo(smem_u32(base + L::kOffW), kBlk);
+                // (ra = 64: rows 64 .. 127 of the product come from the tile behind b and are not used)
+                const uint32_t alo = desc_lo(sB + s * L::kTile, kBlk), blo = desc_lo(smem_u32(base + L::kOffW), kBlk);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t o = k * (2048 >> 4);
-                        if (k == 0) tc_mma_bf16_w<false>(tmem + kColDS, alo, kHi, blo, kHi, idDS);
-                        else tc_mma_bf16_w<true>(tmem + kColDS, alo + o, kHi, blo + o, kHi, idDS);
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = k * (2048 >> 4);
+                    if (k == 0) tc_mma_bf16_w<false>(tmem + kColDS, alo, kHi, blo, kHi, idDS);
+                    else tc_mma_bf16_w<true>(tmem + kColDS, alo + o, kHi, blo + o, kHi, idDS);
                 }
                 tc_commit(&sm->ds_full);
                 tc_commit(&sm->w_empty);
-                tc_commit(&sm->emptyB[s]);   // (the scores read b before)
-                if (c + 1 < nch && !issue_p(c + 1)) break;
-                // Ye = A S
-                if (!wait(cx, &sm->s_full, c & 1)) break;
-                if (c >= 1 && !wait(cx, &sm->y_empty, (c - 1) & 1)) break;
+                tc_commit(&sm->emptyB[s]);
+            }
+        } else if (warp == 3 && lane == 0) {
+            // ------------------------------------------------ MMA: outputs
+            constexpr uint32_t idY = idesc_bf16_f32(128, 64, false, true);
+            for (int c = 0; c < nch; ++c) {
+                const int s = c & 1;
+                if (!wait1(cx, &sm->fullA[s], (c >> 1) & 1) || !wait1(cx, &sm->s_full, c & 1)) break;
+                if (c >= 1 && !wait1(cx, &sm->y_empty, (c - 1) & 1)) break;
                 tc_fence_after();
                 {
-                    const uint32_t alo = desc_lo(st + L::kA, 16), blo = desc_lo(smem_u32(base + L::kOffS), kBlk);
+                    const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(smem_u32(base + L::kOffS), kBlk);
 #pragma unroll
                     for (int k = 0; k < KD / 16; ++k) {
                         const uint32_t o = ((k >> 2) * kBlk + (k & 3) * 32) >> 4;
@@ -278,247 +327,232 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 }
                 tc_commit(&sm->s_empty);
                 tc_commit(&sm->emptyA[s]);
-                // Yi = P C
-                if (!wait(cx, &sm->p_ready[s], (c >> 1) & 1)) break;
+                if (!wait1(cx, &sm->fullC[c % kStC], (c / kStC) & 1) || !wait1(cx, &sm->p_ready[s], (c >> 1) & 1)) break;
+                // the rows behind a packed sequence are zeros in c once its weighted values are written
+                // (only the last chunk has any: no later phase of w_full can hide this one)
+                if (packed && c == nch - 1 && !wait1(cx, &sm->w_full, c & 1)) break;
                 tc_fence_after();
-                {
-                    const uint32_t blo = desc_lo(st + L::kC, kBlk), a = tmem + kColP + s * 128;
+                const uint32_t blo = desc_lo(sC + (c % kStC) * kBlk, kBlk), a = tmem + kColP + s * 128;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (k == 0) tc_mma_bf16_ts<false>(tmem + kColYi, a, blo, kHi, idY);
-                        else tc_mma_bf16_ts<true>(tmem + kColYi, a + 8 * k, blo + k * (2048 >> 4), kHi, idY);
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    if (k == 0) tc_mma_bf16_ts<false>(tmem + kColYi, a, blo, kHi, idY);
+                    else tc_mma_bf16_ts<true>(tmem + kColYi, a + 8 * k, blo + k * (2048 >> 4), kHi, idY);
                 }
                 tc_commit(&sm->y_full);
-                tc_commit(&sm->emptyC[s]);
+                tc_commit(&sm->p_free[s]);
+                tc_commit(&sm->emptyC[c % kStC]);
             }
-            // every MMA issued above completes before TMEM is released
-            tc_commit(&sm->done);
-            mbar_wait(&sm->done, 0, cx.limit);
+        }
+        if (warp >= 1 && lane == 0) {
+            // every MMA that this thread issued completes before TMEM is released
+            tc_commit(&sm->done[warp - 1]);
+            mbar_wait(&sm->done[warp - 1], 0, cx.limit);
         }
         __syncwarp();
-    } else if (warp < kGroupC) {
+    } else if (group == 1) {
         // --------------------------------------------------------- scores
+        // the powers of a diagonal block's row, and of a column of the blocks below: the same for every chunk
         const int R = warp & 3;
-        const float *pw = sm->pw;
+        // (a masked score is dropped, not multiplied by 0: behind a packed sequence it may be anything)
+        float2 wd[16], wc[16];
+        const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int e = rev ? j - lane : lane - j;
+            const float d = sm->pw[e >= 0 ? e : 0], f = sm->pw[rev ? j : 31 - j];
+            (j & 1 ? wd[j / 2].y : wd[j / 2].x) = d;
+            (j & 1 ? wc[j / 2].y : wc[j / 2].x) = f;
+        }
         for (int c = 0; c < nch; ++c) {
             const int s = c & 1;
-            if (!warp_wait(cx, &sm->p_raw[s], (c >> 1) & 1)) break;
+            if (!waitw(cx, &sm->p_raw[s], (c >> 1) & 1)) break;
             tc_fence_after();
             const uint32_t tP = tmem + lane_base + kColP + s * 128;
 #pragma unroll 1
             for (int J = 0; J < 4; ++J) {
                 uint32_t o[16];
-                if (rev ? J < R : J > R) {
+                if (rev ? J < R : J > R) {      // above the diagonal
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = 0;
                 } else {
                     float v[32];
                     tc_ld_32x32b_x32(tP + 32 * J, v);
-                    tc_wait_ld();
+                    wait_loaded(v);
                     if (J == R) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int e = rev ? j - lane : lane - j;
-                            v[j] = e >= 0 ? v[j] * pw[e >= 0 ? e : 0] : 0.f;
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), wd[i]);
+                            o[i] = pack_bf16x2(keep >> (2 * i) & 1 ? x.x : 0.f, keep >> (2 * i + 1) & 1 ? x.y : 0.f);
                         }
                     } else {
-                        const float rf = pw[rev ? 32 * J - row : row - 32 * J - 31];
+                        const float rf = sm->pw[rev ? 32 * J - row : row - 32 * J - 31];
+                        const float2 rf2 = make_float2(rf, rf);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 cf = *reinterpret_cast<const float4 *>(sm->col + j);
-                            v[j] *= rf * cf.x, v[j + 1] *= rf * cf.y, v[j + 2] *= rf * cf.z, v[j + 3] *= rf * cf.w;
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), __fmul2_rn(wc[i], rf2));
+                            o[i] = pack_bf16x2(x.x, x.y);
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
                 }
-                // (P's columns 16 J .. overwrite scores of blocks <= J, which this warp has read)
+                // (P's columns 16 J .. lie over scores of blocks <= J / 2, which this warp has read)
                 tc_st_x16(tP + 16 * J, o);
             }
             tc_wait_st();
             tc_fence_before();
             warp_arrive(&sm->p_ready[s]);
         }
-    } else if (warp < kGroupS) {
-        // ------------------------------------------------ weighted values
-        for (int c = 0; c < nch; ++c) {
-            const int s = c & 1, n = chunk_n(c);
-            if (!warp_wait(cx, &sm->fullC[s], (c >> 1) & 1)) break;
-            uint8_t *tC = base + s * L::kStage + L::kC;
-            const bool in = row < n;
-            const float w = in ? sm->pw[rev ? row + 1 : n - 1 - row] * sw.write_scale : 0.f;
-            uint4 raw[8];
+    } else if (group == 2) {
+        // ------------------------------------ weighted values and outputs
+        const float s_in = sw.out_scale * sw.write_scale;
+        uint16_t *out = static_cast<uint16_t *>(sw.out);
+        const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+        uint8_t *tW = base + L::kOffW;
+        for (int c = 0; c <= nch; ++c) {
+            if (c < nch) {
+                // the weighted values of chunk c
+                const int s = c % kStC, n = chunk_n(c);
+                if (!waitw(cx, &sm->fullC[s], (c / kStC) & 1)) break;
+                uint8_t *tC = base + L::kOffC + s * kBlk;
+                const bool in = row < n;
+                const float w = in ? sm->pw[rev ? row + 1 : n - 1 - row] * sw.write_scale : 0.f;
+                if (packed && n < kCT) {
+                    // the rows behind the sequence are another's (or nobody's): they become zeros in b and c
+                    if (!waitw(cx, &sm->fullB[c & 1], (c >> 1) & 1)) break;
+                    if (!in) {
+#pragma unroll 1
+                        for (int x = 0; x < 8; ++x) {
+                            *reinterpret_cast<uint4 *>(tC + sw128_offset(row, x)) = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < L::NB; ++k)
+                                *reinterpret_cast<uint4 *>(base + L::kOffB + (c & 1) * L::kTile + k * kBlk + sw128_offset(row, x)) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
+                if (c >= 1 && !waitw(cx, &sm->w_empty, (c - 1) & 1)) break;
+#pragma unroll 2
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t at = sw128_offset(row, x);
+                    const uint4 raw = *reinterpret_cast<const uint4 *>(tC + at);
+                    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) raw[x] = *reinterpret_cast<const uint4 *>(tC + sw128_offset(row, x));
-            if (packed && n < kCT) {
-                // the rows behind the sequence are another's (or nobody's): they become zeros in b and c
-                if (!warp_wait(cx, &sm->fullB[s], (c >> 1) & 1)) break;
-                if (!in) {
+                    for (int e = 0; e < 4; ++e) {
+                        // (the second part takes what the first leaves of the exact product)
+                        const float v0 = bf16_lo(u[e]), v1 = bf16_hi(u[e]);
+                        hi[e] = pack_bf16x2(v0 * w, v1 * w);
+                        lo[e] = pack_bf16x2(fmaf(v0, w, -bf16_lo(hi[e])), fmaf(v1, w, -bf16_hi(hi[e])));
+                    }
+                    *reinterpret_cast<uint4 *>(tW + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(tW + kBlk + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                warp_arrive(&sm->emptyC[s]);
+                fence_proxy_async_smem();
+                warp_arrive(&sm->w_full);
+            }
+            if (c > 0) {
+                // the outputs of chunk c - 1
+                const int ce = c - 1, n = chunk_n(ce), t0 = chunk_t0(ce);
+                const int e = rev ? n - 1 - row : row + 1;
+                const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
+                const size_t at = packed ? (size_t)(seq0 + t0 + row) * H + h : bh * T + t0 + row;
+                uint16_t *dst = out + at * n_all + c0;
+                if (!waitw(cx, &sm->y_full, ce & 1)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 64; x += 16) {
+                    float yi[16], ye[16];
+                    tc_ld_32x32b_x16(tmem + lane_base + kColYi + x, yi);
+                    tc_ld_32x32b_x16(tmem + lane_base + kColYe + x, ye);
+                    wait_loaded(yi);
+                    wait_loaded(ye);
+                    if (x == 48) {
+                        tc_fence_before();
+                        warp_arrive(&sm->y_empty);
+                    }
+                    uint32_t o[8];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        raw[x] = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(tC + sw128_offset(row, x)) = raw[x];
-#pragma unroll
-                        for (int k = 0; k < L::NB; ++k)
-                            *reinterpret_cast<uint4 *>(base + s * L::kStage + L::kB + k * kBlk + sw128_offset(row, x)) = raw[x];
+                    for (int j = 0; j < 16; j += 2)
+                        o[j / 2] = pack_bf16x2(fmaf(s_in, yi[j], s_ex * ye[j]), fmaf(s_in, yi[j + 1], s_ex * ye[j + 1]));
+                    if (row < n) {
+                        if (wide) {
+                            st_global_32(dst + x, o);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
                     }
                 }
             }
-            if (c >= 1 && !warp_wait(cx, &sm->w_empty, (c - 1) & 1)) break;
-            uint8_t *tW = base + L::kOffW;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float f0 = bf16_lo(u[e]) * w, f1 = bf16_hi(u[e]) * w;
-                    hi[e] = pack_bf16x2(f0, f1);
-                    lo[e] = pack_bf16x2(f0 - bf16_lo(hi[e]), f1 - bf16_hi(hi[e]));
-                }
-                *reinterpret_cast<uint4 *>(tW + sw128_offset(row, x)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(tW + kBlk + sw128_offset(row, x)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-            fence_proxy_async_smem();
-            warp_arrive(&sm->w_full);
         }
-    } else if (warp < kGroupY) {
+    } else {
         // ---------------------------------------------------------- state
-        const bool mine = row < KD;    // (ra = 64: two of the four warps)
-        float S[64];
+        regs_inc<kRegsState>();
+        const bool mine = row < KD;    // (ra = 64: the other rows hold what the unused rows of dS give)
+        float2 S[32];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = 0.f;
-        if (mine && sw.S_init) {
-            if (sw.init_t) {
-                const float *src = sw.S_init + (bh * n_all + c0) * KD + row;
+        for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
+        if (sw.S_init) {
+            // element j of the row: contiguous, or a row of the transposed state apart
+            const int i = row & (KD - 1);
+            const float *src = sw.init_t ? sw.S_init + (bh * n_all + c0) * KD + i : sw.S_init + (bh * KD + i) * n_all + c0;
+            const size_t step = sw.init_t ? KD : 1;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) S[j] = src[(size_t)j * KD];
-            } else {
-                const float *src = sw.S_init + (bh * KD + row) * n_all + c0;
-                if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-#pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        const float4 q = *reinterpret_cast<const float4 *>(src + j);
-                        S[j] = q.x, S[j + 1] = q.y, S[j + 2] = q.z, S[j + 3] = q.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) S[j] = src[j];
-                }
-            }
+            for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * step], src[(2 * j + 1) * step]);
         }
         auto publish = [&]() {
-            if (mine) {
-                uint8_t *tS = base + L::kOffS;
+            uint8_t *tS = base + L::kOffS;
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    *reinterpret_cast<uint4 *>(tS + sw128_offset(row, x)) =
-                        make_uint4(pack_bf16x2(S[8 * x], S[8 * x + 1]), pack_bf16x2(S[8 * x + 2], S[8 * x + 3]),
-                                   pack_bf16x2(S[8 * x + 4], S[8 * x + 5]), pack_bf16x2(S[8 * x + 6], S[8 * x + 7]));
-            }
+            for (int x = 0; x < 8; ++x)
+                *reinterpret_cast<uint4 *>(tS + sw128_offset(row, x)) =
+                    make_uint4(pack_bf16x2(S[4 * x].x, S[4 * x].y), pack_bf16x2(S[4 * x + 1].x, S[4 * x + 1].y),
+                               pack_bf16x2(S[4 * x + 2].x, S[4 * x + 2].y), pack_bf16x2(S[4 * x + 3].x, S[4 * x + 3].y));
             fence_proxy_async_smem();
             warp_arrive(&sm->s_full);
         };
-        if (nch > 0) publish();
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
+            // the state that enters chunk c, once chunk c - 1's Ye has read its own
+            if (c >= 1 && !(ok = waitw(cx, &sm->s_empty, (c - 1) & 1))) break;
+            publish();
             const float gn = sm->pw[chunk_n(c)];
-            ok = warp_wait(cx, &sm->ds_full, c & 1);
+            ok = waitw(cx, &sm->ds_full, c & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < 64; x += 8) {
-                float hi[8], lo[8];
-                tc_ld_x8(tmem + lane_base + kColDS + x, hi);
-                tc_ld_x8(tmem + lane_base + kColDS + 64 + x, lo);
-                tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) S[x + j] = fmaf(gn, S[x + j], hi[j] + lo[j]);
-            }
+            const float2 gn2 = make_float2(gn, gn);
+            float h0[32], h1[32], l0[32], l1[32];
+            tc_ld_32x32b_x32(tmem + lane_base + kColDS, h0);
+            tc_ld_32x32b_x32(tmem + lane_base + kColDS + 32, h1);
+            tc_ld_32x32b_x32(tmem + lane_base + kColDS + 64, l0);
+            tc_ld_32x32b_x32(tmem + lane_base + kColDS + 96, l1);
+            wait_loaded(h0);
+            wait_loaded(h1);
+            wait_loaded(l0);
+            wait_loaded(l1);
             tc_fence_before();
             warp_arrive(&sm->ds_empty);
-            if (c + 1 < nch) {
-                ok = warp_wait(cx, &sm->s_empty, c & 1);
-                if (!ok) break;
-                publish();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                S[j] = __ffma2_rn(gn2, S[j], __fadd2_rn(make_float2(h0[2 * j], h0[2 * j + 1]), make_float2(l0[2 * j], l0[2 * j + 1])));
+                S[16 + j] = __ffma2_rn(gn2, S[16 + j], __fadd2_rn(make_float2(h1[2 * j], h1[2 * j + 1]), make_float2(l1[2 * j], l1[2 * j + 1])));
             }
         }
         if (ok && mine && sw.S_fin) {
             float *dst = sw.S_fin + (bh * KD + row) * n_all + c0;
             if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
 #pragma unroll
-                for (int j = 0; j < 64; j += 4)
-                    *reinterpret_cast<float4 *>(dst + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                for (int j = 0; j < 32; j += 2)
+                    *reinterpret_cast<float4 *>(dst + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
             } else {
 #pragma unroll
-                for (int j = 0; j < 64; ++j) dst[j] = S[j];
+                for (int j = 0; j < 32; ++j) dst[2 * j] = S[j].x, dst[2 * j + 1] = S[j].y;
             }
         }
-    } else {
-        // -------------------------------------------------------- outputs
-        const float s_in = sw.out_scale * sw.write_scale;
-        uint8_t *tY = base + L::kOffY;
-        for (int c = 0; c < nch; ++c) {
-            const int n = chunk_n(c), t0 = chunk_t0(c);
-            const int e = rev ? n - 1 - row : row + 1;
-            const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
-            if (!warp_wait(cx, &sm->y_full, c & 1)) break;
-            tc_fence_after();
-            uint32_t o[32];
-#pragma unroll
-            for (int x = 0; x < 64; x += 16) {
-                float yi[16], ye[16];
-                tc_ld_32x32b_x16(tmem + lane_base + kColYi + x, yi);
-                tc_ld_32x32b_x16(tmem + lane_base + kColYe + x, ye);
-                tc_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; j += 2)
-                    o[(x + j) / 2] = pack_bf16x2(fmaf(s_in, yi[j], s_ex * ye[j]), fmaf(s_in, yi[j + 1], s_ex * ye[j + 1]));
-            }
-            tc_fence_before();
-            warp_arrive(&sm->y_empty);
-            // the tile is free once its last store has been read out of shared memory
-            if (warp == kGroupY) {
-                if (lane == 0) {
-                    tma_store_wait_read<0>();
-                    mbar_arrive(&sm->t_free);
-                }
-                __syncwarp();
-            }
-            if (!warp_wait(cx, &sm->t_free, c & 1)) break;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                *reinterpret_cast<uint4 *>(tY + sw128_offset(row, x)) = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-            if (packed && n < kCT) {
-                // only the sequence's own rows: each warp its 32, 8 lanes per row
-                __syncwarp();
-                uint16_t *y = static_cast<uint16_t *>(sw.out);
-                const int r0 = (warp & 3) * 32;
-                for (int r = r0 + (lane >> 3); r < min(n, r0 + 32); r += 4)
-                    *reinterpret_cast<uint4 *>(y + ((size_t)(seq0 + t0 + r) * H + h) * n_all + c0 + (lane & 7) * 8) =
-                        *reinterpret_cast<const uint4 *>(tY + sw128_offset(r, lane & 7));
-            } else {
-                fence_proxy_async_smem();
-                warp_arrive(&sm->t_full);
-                if (warp == kGroupY) {
-                    if (!warp_wait(cx, &sm->t_full, c & 1)) break;
-                    if (lane == 0) {
-                        tma_store_3d(&maps.out, tY, c0, packed ? h : t0, packed ? seq0 + t0 : (int)bh);
-                        tma_store_commit();
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-        if (warp == kGroupY && lane == 0) tma_store_wait_all<0>();
-        __syncwarp();
     }
     // ------------------------------------------------------------ teardown
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 template <int KD>
