@@ -36,8 +36,8 @@ namespace {
 
 constexpr int kCT = 128;                       // tokens per chunk
 constexpr int kThreads = 512;
-// registers per thread after the split (launched with 128): 56 + 128 + 128 + 200 = 4 * 128
-constexpr int kRegsIssue = 56, kRegsState = 200;
+// registers per thread after the split (launched with 128): 56 + 128 + 88 + 240 = 4 * 128
+constexpr int kRegsIssue = 56, kRegsValues = 88, kRegsState = 240;
 constexpr uint32_t kBlk = kCT * 128;           // 16 KB: 128 rows x 64 BF16 columns, 128-byte swizzle
 constexpr int kStC = 3;                        // stages of c (a and b have two)
 
@@ -60,6 +60,7 @@ struct alignas(16) SmallD {
     uint32_t tmem_base;
     int abort_flag;
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
+    alignas(16) float col[32];         // the powers of a column of the blocks below the diagonal
 };
 
 template <int KD>
@@ -210,6 +211,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             q *= q;
         }
         sm->pw[e] = (float)p;
+        if (e < 32) sm->col[rev ? e : 31 - e] = (float)p;
     }
     tc_fence_before();
     __syncthreads();
@@ -351,18 +353,18 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         __syncwarp();
     } else if (group == 1) {
         // --------------------------------------------------------- scores
-        // the powers of a diagonal block's row, and of a column of the blocks below: the same for every chunk
-        const int R = warp & 3;
+        // the powers of a diagonal block's row: the same for every chunk
         // (a masked score is dropped, not multiplied by 0: behind a packed sequence it may be anything)
+        const int R = warp & 3;
         float2 wd[16], wc[16];
         const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const int e = rev ? j - lane : lane - j;
-            const float d = sm->pw[e >= 0 ? e : 0], f = sm->pw[rev ? j : 31 - j];
-            (j & 1 ? wd[j / 2].y : wd[j / 2].x) = d;
-            (j & 1 ? wc[j / 2].y : wc[j / 2].x) = f;
+            (j & 1 ? wd[j / 2].y : wd[j / 2].x) = sm->pw[e >= 0 ? e : 0];
+            (j & 1 ? wc[j / 2].y : wc[j / 2].x) = sm->pw[rev ? j : 31 - j];
         }
+        const int J0 = rev ? R : 0, J1 = rev ? 3 : R;     // the 32-column blocks that the mask leaves
         for (int c = 0; c < nch; ++c) {
             const int s = c & 1;
             if (!waitw(cx, &sm->p_raw[s], (c >> 1) & 1)) break;
@@ -371,7 +373,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
 #pragma unroll 1
             for (int J = 0; J < 4; ++J) {
                 uint32_t o[16];
-                if (rev ? J < R : J > R) {      // above the diagonal
+                if (J < J0 || J > J1) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = 0;
                 } else {
@@ -381,16 +383,16 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     if (J == R) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), wd[i]);
-                            o[i] = pack_bf16x2(keep >> (2 * i) & 1 ? x.x : 0.f, keep >> (2 * i + 1) & 1 ? x.y : 0.f);
+                            const float2 p = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), wd[i]);
+                            o[i] = pack_bf16x2(keep >> (2 * i) & 1 ? p.x : 0.f, keep >> (2 * i + 1) & 1 ? p.y : 0.f);
                         }
                     } else {
                         const float rf = sm->pw[rev ? 32 * J - row : row - 32 * J - 31];
                         const float2 rf2 = make_float2(rf, rf);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), __fmul2_rn(wc[i], rf2));
-                            o[i] = pack_bf16x2(x.x, x.y);
+                            const float2 p = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), __fmul2_rn(wc[i], rf2));
+                            o[i] = pack_bf16x2(p.x, p.y);
                         }
                     }
                 }
@@ -402,90 +404,57 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             warp_arrive(&sm->p_ready[s]);
         }
     } else if (group == 2) {
-        // ------------------------------------ weighted values and outputs
-        const float s_in = sw.out_scale * sw.write_scale;
-        uint16_t *out = static_cast<uint16_t *>(sw.out);
-        const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+        // ------------------------------------------------ weighted values
+        regs_dec<kRegsValues>();
         uint8_t *tW = base + L::kOffW;
-        for (int c = 0; c <= nch; ++c) {
-            if (c < nch) {
-                // the weighted values of chunk c
-                const int s = c % kStC, n = chunk_n(c);
-                if (!waitw(cx, &sm->fullC[s], (c / kStC) & 1)) break;
-                uint8_t *tC = base + L::kOffC + s * kBlk;
-                const bool in = row < n;
-                const float w = in ? sm->pw[rev ? row + 1 : n - 1 - row] * sw.write_scale : 0.f;
-                if (packed && n < kCT) {
-                    // the rows behind the sequence are another's (or nobody's): they become zeros in b and c
-                    if (!waitw(cx, &sm->fullB[c & 1], (c >> 1) & 1)) break;
-                    if (!in) {
+        for (int c = 0; c < nch; ++c) {
+            const int s = c % kStC, n = chunk_n(c);
+            uint8_t *tC = base + L::kOffC + s * kBlk;
+            const bool in = row < n;
+            const float w = in ? sm->pw[rev ? row + 1 : n - 1 - row] * sw.write_scale : 0.f;
+            const float2 w2 = make_float2(w, w), nw2 = make_float2(-w, -w);
+            if (!waitw(cx, &sm->fullC[s], (c / kStC) & 1)) break;
+            if (packed && n < kCT) {
+                // the rows behind the sequence are another's (or nobody's): they become zeros in b and c
+                if (!waitw(cx, &sm->fullB[c & 1], (c >> 1) & 1)) break;
+                if (!in) {
 #pragma unroll 1
-                        for (int x = 0; x < 8; ++x) {
-                            *reinterpret_cast<uint4 *>(tC + sw128_offset(row, x)) = make_uint4(0, 0, 0, 0);
-                            for (int k = 0; k < L::NB; ++k)
-                                *reinterpret_cast<uint4 *>(base + L::kOffB + (c & 1) * L::kTile + k * kBlk + sw128_offset(row, x)) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
+                    for (int x = 0; x < 8; ++x) {
+                        *reinterpret_cast<uint4 *>(tC + sw128_offset(row, x)) = make_uint4(0, 0, 0, 0);
+                        for (int k = 0; k < L::NB; ++k)
+                            *reinterpret_cast<uint4 *>(base + L::kOffB + (c & 1) * L::kTile + k * kBlk + sw128_offset(row, x)) =
+                                make_uint4(0, 0, 0, 0);
                     }
                 }
-                if (c >= 1 && !waitw(cx, &sm->w_empty, (c - 1) & 1)) break;
-#pragma unroll 2
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t at = sw128_offset(row, x);
-                    const uint4 raw = *reinterpret_cast<const uint4 *>(tC + at);
-                    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // (the second part takes what the first leaves of the exact product)
-                        const float v0 = bf16_lo(u[e]), v1 = bf16_hi(u[e]);
-                        hi[e] = pack_bf16x2(v0 * w, v1 * w);
-                        lo[e] = pack_bf16x2(fmaf(v0, w, -bf16_lo(hi[e])), fmaf(v1, w, -bf16_hi(hi[e])));
-                    }
-                    *reinterpret_cast<uint4 *>(tW + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(tW + kBlk + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                warp_arrive(&sm->emptyC[s]);
-                fence_proxy_async_smem();
-                warp_arrive(&sm->w_full);
             }
-            if (c > 0) {
-                // the outputs of chunk c - 1
-                const int ce = c - 1, n = chunk_n(ce), t0 = chunk_t0(ce);
-                const int e = rev ? n - 1 - row : row + 1;
-                const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
-                const size_t at = packed ? (size_t)(seq0 + t0 + row) * H + h : bh * T + t0 + row;
-                uint16_t *dst = out + at * n_all + c0;
-                if (!waitw(cx, &sm->y_full, ce & 1)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < 64; x += 16) {
-                    float yi[16], ye[16];
-                    tc_ld_32x32b_x16(tmem + lane_base + kColYi + x, yi);
-                    tc_ld_32x32b_x16(tmem + lane_base + kColYe + x, ye);
-                    wait_loaded(yi);
-                    wait_loaded(ye);
-                    if (x == 48) {
-                        tc_fence_before();
-                        warp_arrive(&sm->y_empty);
-                    }
-                    uint32_t o[8];
+            if (c >= 1 && !waitw(cx, &sm->w_empty, (c - 1) & 1)) break;
+#pragma unroll 2
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t at = sw128_offset(row, x);
+                const uint4 raw = *reinterpret_cast<const uint4 *>(tC + at);
+                const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2)
-                        o[j / 2] = pack_bf16x2(fmaf(s_in, yi[j], s_ex * ye[j]), fmaf(s_in, yi[j + 1], s_ex * ye[j + 1]));
-                    if (row < n) {
-                        if (wide) {
-                            st_global_32(dst + x, o);
-                        } else {
-                            *reinterpret_cast<uint4 *>(dst + x) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    // the second part is what the first leaves of the exact product, with its sign turned
+                    const float2 v = make_float2(bf16_lo(u[e]), bf16_hi(u[e]));
+                    const float2 p = __fmul2_rn(v, w2);
+                    hi[e] = pack_bf16x2(p.x, p.y);
+                    const float2 q = __ffma2_rn(v, nw2, make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])));
+                    lo[e] = pack_bf16x2(q.x, q.y);
                 }
+                *reinterpret_cast<uint4 *>(tW + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(tW + kBlk + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm->w_full);
+                mbar_arrive(&sm->emptyC[s]);
             }
         }
     } else {
-        // ---------------------------------------------------------- state
+        // ---------------------------------------------- state and outputs
         regs_inc<kRegsState>();
         const bool mine = row < KD;    // (ra = 64: the other rows hold what the unused rows of dS give)
         float2 S[32];
@@ -509,16 +478,59 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             fence_proxy_async_smem();
             warp_arrive(&sm->s_full);
         };
+        const float s_in = sw.out_scale * sw.write_scale;
+        const float2 si2 = make_float2(s_in, s_in);
+        uint16_t *out = static_cast<uint16_t *>(sw.out);
+        const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
         bool ok = true;
-        for (int c = 0; c < nch; ++c) {
+        for (int c = 0; c <= nch; ++c) {
             // the state that enters chunk c, once chunk c - 1's Ye has read its own
             if (c >= 1 && !(ok = waitw(cx, &sm->s_empty, (c - 1) & 1))) break;
-            publish();
+            if (c < nch) publish();
+            if (c >= 1) {
+                // the outputs of chunk c - 1
+                const int n = chunk_n(c - 1), t0 = chunk_t0(c - 1);
+                const int e = rev ? n - 1 - row : row + 1;
+                const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
+                const float2 se2 = make_float2(s_ex, s_ex);
+                const size_t at = packed ? (size_t)(seq0 + t0 + row) * H + h : bh * T + t0 + row;
+                uint16_t *dst = out + at * n_all + c0;
+                ok = waitw(cx, &sm->y_full, (c - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 64; x += 16) {
+                    float yi[16], ye[16];
+                    tc_ld_32x32b_x16(tmem + lane_base + kColYi + x, yi);
+                    tc_ld_32x32b_x16(tmem + lane_base + kColYe + x, ye);
+                    wait_loaded(yi);
+                    wait_loaded(ye);
+                    if (x == 48) {
+                        tc_fence_before();
+                        warp_arrive(&sm->y_empty);
+                    }
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 y = __ffma2_rn(si2, make_float2(yi[j], yi[j + 1]), __fmul2_rn(se2, make_float2(ye[j], ye[j + 1])));
+                        o[j / 2] = pack_bf16x2(y.x, y.y);
+                    }
+                    if (row < n) {
+                        if (wide) {
+                            st_global_32(dst + x, o);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
+                }
+            }
+            if (c == nch) break;
             const float gn = sm->pw[chunk_n(c)];
             ok = waitw(cx, &sm->ds_full, c & 1);
             if (!ok) break;
             tc_fence_after();
-            const float2 gn2 = make_float2(gn, gn);
+            const float2 gn2 = make_float2(gn, gn), minus = make_float2(-1.f, -1.f);
             float h0[32], h1[32], l0[32], l1[32];
             tc_ld_32x32b_x32(tmem + lane_base + kColDS, h0);
             tc_ld_32x32b_x32(tmem + lane_base + kColDS + 32, h1);
@@ -531,9 +543,9 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             tc_fence_before();
             warp_arrive(&sm->ds_empty);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                S[j] = __ffma2_rn(gn2, S[j], __fadd2_rn(make_float2(h0[2 * j], h0[2 * j + 1]), make_float2(l0[2 * j], l0[2 * j + 1])));
-                S[16 + j] = __ffma2_rn(gn2, S[16 + j], __fadd2_rn(make_float2(h1[2 * j], h1[2 * j + 1]), make_float2(l1[2 * j], l1[2 * j + 1])));
+            for (int j = 0; j < 16; ++j) {    // (the second part's sign is turned)
+                S[j] = __ffma2_rn(gn2, S[j], __ffma2_rn(minus, make_float2(l0[2 * j], l0[2 * j + 1]), make_float2(h0[2 * j], h0[2 * j + 1])));
+                S[16 + j] = __ffma2_rn(gn2, S[16 + j], __ffma2_rn(minus, make_float2(l1[2 * j], l1[2 * j + 1]), make_float2(h1[2 * j], h1[2 * j + 1])));
             }
         }
         if (ok && mine && sw.S_fin) {
