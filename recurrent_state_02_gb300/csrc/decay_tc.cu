@@ -56,11 +56,10 @@ struct Lay {
 
 struct alignas(16) SmallD {
     uint64_t fullA[2], fullB[2], fullC[kStC], emptyA[2], emptyB[2], emptyC[kStC];
-    uint64_t p_raw[2], p_ready[2], p_free[2], w_full, w_empty, ds_full, ds_empty, s_full, s_empty, y_full, y_empty, done[3];
+    uint64_t p_raw[2], p_ready[2], p_free[2], w_full, w_empty, ds_full, ds_empty, s_full, ye_full, yi_full, yi_empty, done[3];
     uint32_t tmem_base;
     int abort_flag;
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
-    alignas(16) float col[32];         // the powers of a column of the blocks below the diagonal
 };
 
 template <int KD>
@@ -81,23 +80,26 @@ __device__ __forceinline__ void wait_loaded(float (&v)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
+__device__ __forceinline__ uint32_t timer_lo()
+{
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
 // Bounded waits as in tc_common.cuh, short enough to be inlined everywhere: by one thread, or by a whole
-// warp (which stays converged).  False when the limit ran out or another thread has given up.
+// warp (which stays converged).  False when the limit (below 2^32 ns) ran out or another thread has given
+// up: the CTA's flag is then up, and the teardown records the timeout.
 template <bool WARP>
 __device__ __forceinline__ bool bounded_wait(const Ctx &cx, uint64_t *bar, uint32_t parity)
 {
     auto all = [](bool x) { return WARP ? __all_sync(0xffffffffu, x) != 0 : x; };
     if (all(mbar_try_wait(bar, parity))) return true;
-    const uint64_t t0 = global_timer_ns();
-    bool go = true;
-    while (go) {
+    const uint32_t t0 = timer_lo();
+    do {
         if (all(mbar_try_wait_hint(bar, parity, kWaitHintNs))) return true;
-        go = all(!aborted(cx) && global_timer_ns() - t0 <= cx.limit);
-    }
-    if (!aborted(cx)) {
-        atomicExch(cx.status, kStatusTimeout);
-        *reinterpret_cast<volatile int *>(cx.abort_flag) = 1;
-    }
+    } while (all(!aborted(cx) && timer_lo() - t0 <= (uint32_t)cx.limit));
+    *reinterpret_cast<volatile int *>(cx.abort_flag) = 1;
     return false;
 }
 __device__ __forceinline__ bool wait1(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<false>(cx, bar, parity); }
@@ -111,16 +113,26 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t *r)
                  : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-template <bool ACC>
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc)
+// D[tmem] (+)= A * B, B in shared memory and A there or in TMEM.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}"
+        ::"r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool acc)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
         "mov.b64 db, {%2, %3};\n\t"
         "setp.ne.b32 p, %5, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+        ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
 
@@ -188,9 +200,9 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         mbar_init(&sm->ds_full, 1);
         mbar_init(&sm->ds_empty, 4);
         mbar_init(&sm->s_full, 4);
-        mbar_init(&sm->s_empty, 1);
-        mbar_init(&sm->y_full, 1);
-        mbar_init(&sm->y_empty, 4);
+        mbar_init(&sm->ye_full, 1);
+        mbar_init(&sm->yi_full, 1);
+        mbar_init(&sm->yi_empty, 4);
         for (int i = 0; i < 3; ++i) mbar_init(&sm->done[i], 1);
         sm->abort_flag = 0;
         fence_mbarrier_init();
@@ -211,7 +223,6 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             q *= q;
         }
         sm->pw[e] = (float)p;
-        if (e < 32) sm->col[rev ? e : 31 - e] = (float)p;
     }
     tc_fence_before();
     __syncthreads();
@@ -280,11 +291,10 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 tc_fence_after();
                 const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(sB + s * L::kTile, 16);
                 const uint32_t d = tmem + kColP + s * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < KD / 16; ++k) {
                     const uint32_t o = ((k >> 2) * kBlk + (k & 3) * 32) >> 4;
-                    if (k == 0) tc_mma_bf16_w<false>(d, alo, kHi, blo, kHi, idP);
-                    else tc_mma_bf16_w<true>(d, alo + o, kHi, blo + o, kHi, idP);
+                    mma_ss(d, alo + o, kHi, blo + o, kHi, idP, k > 0);
                 }
                 tc_commit(&sm->p_raw[s]);
                 tc_commit(&sm->emptyA[s]);
@@ -300,11 +310,10 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 tc_fence_after();
                 // (ra = 64: rows 64 .. 127 of the product come from the tile behind b and are not used)
                 const uint32_t alo = desc_lo(sB + s * L::kTile, kBlk), blo = desc_lo(smem_u32(base + L::kOffW), kBlk);
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t o = k * (2048 >> 4);
-                    if (k == 0) tc_mma_bf16_w<false>(tmem + kColDS, alo, kHi, blo, kHi, idDS);
-                    else tc_mma_bf16_w<true>(tmem + kColDS, alo + o, kHi, blo + o, kHi, idDS);
+                    mma_ss(tmem + kColDS, alo + o, kHi, blo + o, kHi, idDS, k > 0);
                 }
                 tc_commit(&sm->ds_full);
                 tc_commit(&sm->w_empty);
@@ -315,32 +324,29 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             constexpr uint32_t idY = idesc_bf16_f32(128, 64, false, true);
             for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
+                // (the state of chunk c is published once Ye of chunk c - 1 has been read)
                 if (!wait1(cx, &sm->fullA[s], (c >> 1) & 1) || !wait1(cx, &sm->s_full, c & 1)) break;
-                if (c >= 1 && !wait1(cx, &sm->y_empty, (c - 1) & 1)) break;
                 tc_fence_after();
                 {
                     const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(smem_u32(base + L::kOffS), kBlk);
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < KD / 16; ++k) {
                         const uint32_t o = ((k >> 2) * kBlk + (k & 3) * 32) >> 4;
-                        if (k == 0) tc_mma_bf16_w<false>(tmem + kColYe, alo, kHi, blo, kHi, idY);
-                        else tc_mma_bf16_w<true>(tmem + kColYe, alo + o, kHi, blo + k * (2048 >> 4), kHi, idY);
+                        mma_ss(tmem + kColYe, alo + o, kHi, blo + k * (2048 >> 4), kHi, idY, k > 0);
                     }
                 }
-                tc_commit(&sm->s_empty);
+                tc_commit(&sm->ye_full);
                 tc_commit(&sm->emptyA[s]);
                 if (!wait1(cx, &sm->fullC[c % kStC], (c / kStC) & 1) || !wait1(cx, &sm->p_ready[s], (c >> 1) & 1)) break;
+                if (c >= 1 && !wait1(cx, &sm->yi_empty, (c - 1) & 1)) break;
                 // the rows behind a packed sequence are zeros in c once its weighted values are written
                 // (only the last chunk has any: no later phase of w_full can hide this one)
                 if (packed && c == nch - 1 && !wait1(cx, &sm->w_full, c & 1)) break;
                 tc_fence_after();
                 const uint32_t blo = desc_lo(sC + (c % kStC) * kBlk, kBlk), a = tmem + kColP + s * 128;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k == 0) tc_mma_bf16_ts<false>(tmem + kColYi, a, blo, kHi, idY);
-                    else tc_mma_bf16_ts<true>(tmem + kColYi, a + 8 * k, blo + k * (2048 >> 4), kHi, idY);
-                }
-                tc_commit(&sm->y_full);
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) mma_ts(tmem + kColYi, a + 8 * k, blo + k * (2048 >> 4), kHi, idY, k > 0);
+                tc_commit(&sm->yi_full);
                 tc_commit(&sm->p_free[s]);
                 tc_commit(&sm->emptyC[c % kStC]);
             }
@@ -484,9 +490,44 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
         bool ok = true;
         for (int c = 0; c <= nch; ++c) {
-            // the state that enters chunk c, once chunk c - 1's Ye has read its own
-            if (c >= 1 && !(ok = waitw(cx, &sm->s_empty, (c - 1) & 1))) break;
-            if (c < nch) publish();
+            float ye[64];
+            if (c >= 1) {
+                // Ye of chunk c - 1 moves to registers, which frees its accumulator and the state's tile
+                ok = waitw(cx, &sm->ye_full, (c - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                float(&y0)[32] = *reinterpret_cast<float(*)[32]>(ye), (&y1)[32] = *reinterpret_cast<float(*)[32]>(ye + 32);
+                tc_ld_32x32b_x32(tmem + lane_base + kColYe, y0);
+                tc_ld_32x32b_x32(tmem + lane_base + kColYe + 32, y1);
+                wait_loaded(y0);
+                wait_loaded(y1);
+                tc_fence_before();
+            }
+            if (c < nch) {
+                publish();
+                const float gn = sm->pw[chunk_n(c)];
+                ok = waitw(cx, &sm->ds_full, c & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 gn2 = make_float2(gn, gn), minus = make_float2(-1.f, -1.f);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float hi[32], lo[32];
+                    tc_ld_32x32b_x32(tmem + lane_base + kColDS + 32 * x, hi);
+                    tc_ld_32x32b_x32(tmem + lane_base + kColDS + 64 + 32 * x, lo);
+                    wait_loaded(hi);
+                    wait_loaded(lo);
+                    if (x == 1) {
+                        tc_fence_before();
+                        warp_arrive(&sm->ds_empty);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)    // (the second part's sign is turned)
+                        S[16 * x + j] = __ffma2_rn(gn2, S[16 * x + j],
+                                                   __ffma2_rn(minus, make_float2(lo[2 * j], lo[2 * j + 1]),
+                                                              make_float2(hi[2 * j], hi[2 * j + 1])));
+                }
+            }
             if (c >= 1) {
                 // the outputs of chunk c - 1
                 const int n = chunk_n(c - 1), t0 = chunk_t0(c - 1);
@@ -495,57 +536,36 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 const float2 se2 = make_float2(s_ex, s_ex);
                 const size_t at = packed ? (size_t)(seq0 + t0 + row) * H + h : bh * T + t0 + row;
                 uint16_t *dst = out + at * n_all + c0;
-                ok = waitw(cx, &sm->y_full, (c - 1) & 1);
+                ok = waitw(cx, &sm->yi_full, (c - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < 64; x += 16) {
-                    float yi[16], ye[16];
-                    tc_ld_32x32b_x16(tmem + lane_base + kColYi + x, yi);
-                    tc_ld_32x32b_x16(tmem + lane_base + kColYe + x, ye);
-                    wait_loaded(yi);
-                    wait_loaded(ye);
-                    if (x == 48) {
-                        tc_fence_before();
-                        warp_arrive(&sm->y_empty);
-                    }
-                    uint32_t o[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 y = __ffma2_rn(si2, make_float2(yi[j], yi[j + 1]), __fmul2_rn(se2, make_float2(ye[j], ye[j + 1])));
+                for (int x = 0; x < 64; x += 32) {
+                    float yi[32];
+                    tc_ld_32x32b_x32(tmem + lane_base + kColYi + x, yi);
+                    wait_loaded(yi);
+                    if (x == 32) {
+                        tc_fence_before();
+                        warp_arrive(&sm->yi_empty);
+                    }
+                    uint32_t o[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 y = __ffma2_rn(si2, make_float2(yi[j], yi[j + 1]),
+                                                    __fmul2_rn(se2, make_float2(ye[x + j], ye[x + j + 1])));
                         o[j / 2] = pack_bf16x2(y.x, y.y);
                     }
                     if (row < n) {
                         if (wide) {
                             st_global_32(dst + x, o);
+                            st_global_32(dst + x + 16, o + 8);
                         } else {
-                            *reinterpret_cast<uint4 *>(dst + x) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(dst + x + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                *reinterpret_cast<uint4 *>(dst + x + 8 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                         }
                     }
                 }
-            }
-            if (c == nch) break;
-            const float gn = sm->pw[chunk_n(c)];
-            ok = waitw(cx, &sm->ds_full, c & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const float2 gn2 = make_float2(gn, gn), minus = make_float2(-1.f, -1.f);
-            float h0[32], h1[32], l0[32], l1[32];
-            tc_ld_32x32b_x32(tmem + lane_base + kColDS, h0);
-            tc_ld_32x32b_x32(tmem + lane_base + kColDS + 32, h1);
-            tc_ld_32x32b_x32(tmem + lane_base + kColDS + 64, l0);
-            tc_ld_32x32b_x32(tmem + lane_base + kColDS + 96, l1);
-            wait_loaded(h0);
-            wait_loaded(h1);
-            wait_loaded(l0);
-            wait_loaded(l1);
-            tc_fence_before();
-            warp_arrive(&sm->ds_empty);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {    // (the second part's sign is turned)
-                S[j] = __ffma2_rn(gn2, S[j], __ffma2_rn(minus, make_float2(l0[2 * j], l0[2 * j + 1]), make_float2(h0[2 * j], h0[2 * j + 1])));
-                S[16 + j] = __ffma2_rn(gn2, S[16 + j], __ffma2_rn(minus, make_float2(l1[2 * j], l1[2 * j + 1]), make_float2(h1[2 * j], h1[2 * j + 1])));
             }
         }
         if (ok && mine && sw.S_fin) {
@@ -564,6 +584,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && aborted(cx)) atomicExch(cx.status, kStatusTimeout);
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
