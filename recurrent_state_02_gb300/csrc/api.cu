@@ -856,11 +856,12 @@ la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a
         for (int i = 0; i < count; ++i) {
             if (!tc[i] || sw[i].ra != ra) continue;
             const la::DecaySweep &s = sw[i];
-            auto map = [&](CUtensorMap *t, const void *ptr, int cols) {
-                return packed ? make_map_bf16_tok(t, ptr, a.T, a.H, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)
-                              : make_map_bf16(t, ptr, (long long)B * a.H, a.T, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+            auto map = [&](CUtensorMap *t, const void *ptr, int cols, int rows) {
+                return packed ? make_map_bf16_tok(t, ptr, a.T, a.H, cols, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B)
+                              : make_map_bf16(t, ptr, (long long)B * a.H, a.T, cols, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
             };
-            if (!map(&p.maps[m].a, s.a, s.ra) || !map(&p.maps[m].b, s.b, s.ra) || !map(&p.maps[m].c, s.c, s.n))
+            if (!map(&p.maps[m].a, s.a, s.ra, 128) || !map(&p.maps[m].b, s.b, s.ra, 128) ||
+                !map(&p.maps[m].c, s.c, s.n, 128) || !map(&p.maps[m].out, s.out, s.n, 32))
                 return LA_ERR_CUDA;
             p.sw[m] = s;
             p.tiles[m++] = s.n / 64;

@@ -46,7 +46,7 @@ cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArg
 // aligned.  Maps: boxes of 64 columns x 128 tokens with the 128-byte swizzle over
 // [B*H, T, d], or [tokens, H, d] when packed.
 struct TcSweepMaps {
-    CUtensorMap a, b, c;
+    CUtensorMap a, b, c, out;   // (out: boxes of 64 columns x 32 tokens)
 };
 struct DecayTcParams {
     TcSweepMaps maps[3];

@@ -12,7 +12,7 @@
 //     Yi  = P C                      M=128 N=64  K=128  (P from TMEM)
 //     Ye  = A S                      M=128 N=64  K=ra   (S as BF16)
 //     dS  = B^T [Ch | Cl]            M=ra  N=128 K=128  (Ch + Cl = diag(w g^..) C in two BF16 parts)
-// and out = s_in Yi + s_out g^.. Ye leaves from registers, whole 32-byte sectors a thread.
+// and out = s_in Yi + s_out g^.. Ye leaves through a TMA store from the chunk's tile of C, which is done with by then.
 //
 // The state is FP32 in the registers of four warps: after each chunk S <- g^n S + dS
 // (both halves), so that its rounding is that of one FP32 sum per chunk.  Two
@@ -36,8 +36,8 @@ namespace {
 
 constexpr int kCT = 128;                       // tokens per chunk
 constexpr int kThreads = 512;
-// registers per thread after the split (launched with 128): 56 + 128 + 88 + 240 = 4 * 128
-constexpr int kRegsIssue = 56, kRegsValues = 88, kRegsState = 240;
+// registers per thread after the split (launched with 128): 56 + 128 + 120 + 208 = 4 * 128
+constexpr int kRegsIssue = 56, kRegsValues = 120, kRegsState = 208;
 constexpr uint32_t kBlk = kCT * 128;           // 16 KB: 128 rows x 64 BF16 columns, 128-byte swizzle
 constexpr int kStC = 3;                        // stages of c (a and b have two)
 
@@ -104,14 +104,6 @@ __device__ __forceinline__ bool bounded_wait(const Ctx &cx, uint64_t *bar, uint3
 }
 __device__ __forceinline__ bool wait1(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<false>(cx, bar, parity); }
 __device__ __forceinline__ bool waitw(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<true>(cx, bar, parity); }
-
-// 32 bytes to global memory (32-byte aligned).
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t *r)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 
 // D[tmem] (+)= A * B, B in shared memory and A there or in TMEM.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool acc)
@@ -193,7 +185,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         }
         for (int s = 0; s < kStC; ++s) {
             mbar_init(&sm->fullC[s], 1);
-            mbar_init(&sm->emptyC[s], 5);      // read by Yi and by the four warps that weight it
+            mbar_init(&sm->emptyC[s], 4);      // the output rows of four warps have left it
         }
         mbar_init(&sm->w_full, 4);
         mbar_init(&sm->w_empty, 1);
@@ -209,6 +201,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         tma_prefetch_desc(&maps.a);
         tma_prefetch_desc(&maps.b);
         tma_prefetch_desc(&maps.c);
+        tma_prefetch_desc(&maps.out);
     }
     if (warp == 1) {
         tmem_alloc(&sm->tmem_base, 512);
@@ -239,7 +232,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         if (warp == 0 && lane == 0) {
             // --------------------------------------------------- producer
             // loads in the order in which their buffers come free: b and a of chunk c after
-            // chunk c - 2's dS and Ye, c of chunk c after chunk c - 3's Yi
+            // chunk c - 2's dS and Ye, c of chunk c once chunk c - 3's outputs have left
             auto load = [&](const CUtensorMap *map, uint32_t off, int blocks, int x, uint64_t *bar, int c) {
                 const int t0 = chunk_t0(c), cy = packed ? h : t0, cz = packed ? seq0 + t0 : (int)bh;
                 mbar_arrive_expect_tx(bar, blocks * kBlk);
@@ -260,7 +253,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 load(&maps.a, L::kOffA + s * L::kTile, L::NB, 0, &sm->fullA[s], c);
                 na = c + 1;
                 bool ok = true;
-                for (; ok && nc < nch && nc <= c + 1; ++nc) {
+                for (; ok && nc < nch && nc <= (c == 1 ? 2 : c); ++nc) {
                     ok = nc < kStC || wait1(cx, &sm->emptyC[nc % kStC], (nc / kStC - 1) & 1);
                     if (!ok) break;
                     load(&maps.c, L::kOffC + (nc % kStC) * kBlk, 1, c0, &sm->fullC[nc % kStC], nc);
@@ -348,7 +341,6 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 for (int k = 0; k < 8; ++k) mma_ts(tmem + kColYi, a + 8 * k, blo + k * (2048 >> 4), kHi, idY, k > 0);
                 tc_commit(&sm->yi_full);
                 tc_commit(&sm->p_free[s]);
-                tc_commit(&sm->emptyC[c % kStC]);
             }
         }
         if (warp >= 1 && lane == 0) {
@@ -433,31 +425,32 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     }
                 }
             }
-            if (c >= 1 && !waitw(cx, &sm->w_empty, (c - 1) & 1)) break;
-#pragma unroll 2
+            // both parts are formed while dS of chunk c - 1 still reads its own
+            uint32_t hi[32], lo[32];
+#pragma unroll
             for (int x = 0; x < 8; ++x) {
-                const uint32_t at = sw128_offset(row, x);
-                const uint4 raw = *reinterpret_cast<const uint4 *>(tC + at);
+                const uint4 raw = *reinterpret_cast<const uint4 *>(tC + sw128_offset(row, x));
                 const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-                uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     // the second part is what the first leaves of the exact product, with its sign turned
                     const float2 v = make_float2(bf16_lo(u[e]), bf16_hi(u[e]));
                     const float2 p = __fmul2_rn(v, w2);
-                    hi[e] = pack_bf16x2(p.x, p.y);
-                    const float2 q = __ffma2_rn(v, nw2, make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])));
-                    lo[e] = pack_bf16x2(q.x, q.y);
+                    const uint32_t q = pack_bf16x2(p.x, p.y);
+                    const float2 d = __ffma2_rn(v, nw2, make_float2(bf16_lo(q), bf16_hi(q)));
+                    hi[4 * x + e] = q;
+                    lo[4 * x + e] = pack_bf16x2(d.x, d.y);
                 }
-                *reinterpret_cast<uint4 *>(tW + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(tW + kBlk + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (c >= 1 && !waitw(cx, &sm->w_empty, (c - 1) & 1)) break;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t at = sw128_offset(row, x);
+                *reinterpret_cast<uint4 *>(tW + at) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                *reinterpret_cast<uint4 *>(tW + kBlk + at) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
             }
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sm->w_full);
-                mbar_arrive(&sm->emptyC[s]);
-            }
+            warp_arrive(&sm->w_full);
         }
     } else {
         // ---------------------------------------------- state and outputs
@@ -487,7 +480,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         const float s_in = sw.out_scale * sw.write_scale;
         const float2 si2 = make_float2(s_in, s_in);
         uint16_t *out = static_cast<uint16_t *>(sw.out);
-        const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+        const int r0 = (warp & 3) * 32;    // this warp's rows of a tile
         bool ok = true;
         for (int c = 0; c <= nch; ++c) {
             float ye[64];
@@ -503,8 +496,57 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 wait_loaded(y1);
                 tc_fence_before();
             }
+            if (c < nch) publish();
+            if (c >= 1) {
+                // the outputs of chunk c - 1
+                const int n = chunk_n(c - 1), t0 = chunk_t0(c - 1);
+                const int e = rev ? n - 1 - row : row + 1;
+                const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
+                const float2 se2 = make_float2(s_ex, s_ex);
+                // the rows leave through the chunk's own tile of c: Yi has read it, and so has the weighting
+                // of its values (dS of this chunk was waited for)
+                uint8_t *tY = base + L::kOffC + ((c - 1) % kStC) * kBlk;
+                ok = waitw(cx, &sm->yi_full, (c - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < 64; x += 32) {
+                    float yi[32];
+                    tc_ld_32x32b_x32(tmem + lane_base + kColYi + x, yi);
+                    wait_loaded(yi);
+                    if (x == 32) {
+                        tc_fence_before();
+                        warp_arrive(&sm->yi_empty);
+                    }
+                    uint32_t o[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 y = __ffma2_rn(si2, make_float2(yi[j], yi[j + 1]),
+                                                    __fmul2_rn(se2, make_float2(ye[x + j], ye[x + j + 1])));
+                        o[j / 2] = pack_bf16x2(y.x, y.y);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(tY + sw128_offset(row, x / 8 + q)) =
+                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+                if (packed && n < kCT) {
+                    // only the sequence's own rows, 8 lanes each
+                    __syncwarp();
+#pragma unroll 1
+                    for (int r = r0 + (lane >> 3); r < min(n, r0 + 32); r += 4)
+                        *reinterpret_cast<uint4 *>(out + ((size_t)(seq0 + t0 + r) * H + h) * n_all + c0 + (lane & 7) * 8) =
+                            *reinterpret_cast<const uint4 *>(tY + sw128_offset(r, lane & 7));
+                } else {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && r0 < n) {    // (rows behind the end of a sequence of its own are not written)
+                        tma_store_3d(&maps.out, tY + r0 * 128, c0, packed ? h : t0 + r0, packed ? seq0 + t0 + r0 : (int)bh);
+                        tma_store_commit();
+                    }
+                }
+            }
             if (c < nch) {
-                publish();
                 const float gn = sm->pw[chunk_n(c)];
                 ok = waitw(cx, &sm->ds_full, c & 1);
                 if (!ok) break;
@@ -529,45 +571,13 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 }
             }
             if (c >= 1) {
-                // the outputs of chunk c - 1
-                const int n = chunk_n(c - 1), t0 = chunk_t0(c - 1);
-                const int e = rev ? n - 1 - row : row + 1;
-                const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
-                const float2 se2 = make_float2(s_ex, s_ex);
-                const size_t at = packed ? (size_t)(seq0 + t0 + row) * H + h : bh * T + t0 + row;
-                uint16_t *dst = out + at * n_all + c0;
-                ok = waitw(cx, &sm->yi_full, (c - 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < 64; x += 32) {
-                    float yi[32];
-                    tc_ld_32x32b_x32(tmem + lane_base + kColYi + x, yi);
-                    wait_loaded(yi);
-                    if (x == 32) {
-                        tc_fence_before();
-                        warp_arrive(&sm->yi_empty);
-                    }
-                    uint32_t o[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 y = __ffma2_rn(si2, make_float2(yi[j], yi[j + 1]),
-                                                    __fmul2_rn(se2, make_float2(ye[x + j], ye[x + j + 1])));
-                        o[j / 2] = pack_bf16x2(y.x, y.y);
-                    }
-                    if (row < n) {
-                        if (wide) {
-                            st_global_32(dst + x, o);
-                            st_global_32(dst + x + 16, o + 8);
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                *reinterpret_cast<uint4 *>(dst + x + 8 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                        }
-                    }
-                }
+                // the rows that left through chunk c - 1's tile have been read: the tile may be filled again
+                if (lane == 0) tma_store_wait_read<0>();
+                warp_arrive(&sm->emptyC[(c - 1) % kStC]);
             }
         }
+        if (lane == 0) tma_store_wait_all<0>();
+        __syncwarp();
         if (ok && mine && sw.S_fin) {
             float *dst = sw.S_fin + (bh * KD + row) * n_all + c0;
             if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
