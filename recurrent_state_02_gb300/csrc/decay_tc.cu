@@ -29,7 +29,9 @@
 // issuers (scores, dS, outputs, so that none waits for another's operands); scores; weighted values and
 // outputs; state.
 #include "decay.h"
-#include "tc_common.cuh"
+#include "sm103_ptx.cuh"
+
+#include <cstddef>
 
 namespace la {
 namespace {
@@ -62,6 +64,9 @@ struct alignas(16) SmallD {
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
 };
 
+// shared-memory address of a barrier (in the kernel: sS is the SmallD's)
+#define BAR(name, i) (sS + (uint32_t)offsetof(SmallD, name) + 8 * (uint32_t)(i))
+
 template <int KD>
 constexpr uint32_t smem_bytes() { return Lay<KD>::kOffSmall + sizeof(SmallD) + 1024; }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory budget");
@@ -80,30 +85,79 @@ __device__ __forceinline__ void wait_loaded(float (&v)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-__device__ __forceinline__ uint32_t timer_lo()
+// Shared memory by 32-bit address: every access is then a shared one (through the rounded-up base pointer
+// the compiler only sees generic addresses, which cost more instructions).
+__device__ __forceinline__ uint4 lds4(uint32_t a)
 {
-    uint32_t t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-    return t;
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float ldsf(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// One arrival per warp, after every lane's preceding writes and fences.
+__device__ __forceinline__ void bar_arrive_warp(uint32_t bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
-// Bounded waits as in tc_common.cuh, short enough to be inlined everywhere: by one thread, or by a whole
-// warp (which stays converged).  False when the limit (below 2^32 ns) ran out or another thread has given
-// up: the CTA's flag is then up, and the teardown records the timeout.
+// Bounded waits, a handful of instructions each because two dozen of them are inlined: by one thread, or by a
+// whole warp (which stays converged).  A try sleeps for up to kTryNs, so a wait that nothing ends
+// gives up within 4 s (and not before some tens of ms should the tries return at once): it raises the CTA's flag,
+// which the teardown records, and the caller leaves its loop; every other wait runs out likewise.
+constexpr uint32_t kTryNs = 4000, kTries = 1000000;
 template <bool WARP>
-__device__ __forceinline__ bool bounded_wait(const Ctx &cx, uint64_t *bar, uint32_t parity)
+__device__ __forceinline__ bool bounded_wait(uint32_t abort_flag, uint32_t bar, uint32_t parity)
 {
-    auto all = [](bool x) { return WARP ? __all_sync(0xffffffffu, x) != 0 : x; };
-    if (all(mbar_try_wait(bar, parity))) return true;
-    const uint32_t t0 = timer_lo();
-    do {
-        if (all(mbar_try_wait_hint(bar, parity, kWaitHintNs))) return true;
-    } while (all(!aborted(cx) && timer_lo() - t0 <= (uint32_t)cx.limit));
-    *reinterpret_cast<volatile int *>(cx.abort_flag) = 1;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kTries; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kTryNs)
+            : "memory");
+        if (WARP ? __all_sync(0xffffffffu, ok) != 0 : ok != 0) return true;
+    }
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
     return false;
 }
-__device__ __forceinline__ bool wait1(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<false>(cx, bar, parity); }
-__device__ __forceinline__ bool waitw(const Ctx &cx, uint64_t *bar, uint32_t parity) { return bounded_wait<true>(cx, bar, parity); }
 
 // D[tmem] (+)= A * B, B in shared memory and A there or in TMEM.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool acc)
@@ -139,7 +193,8 @@ __device__ __forceinline__ void tc_st_x16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-template <int KD>
+// PACKED: packed sequences (forwards); REV: the launch has backward sweeps (of [B,H,T,d] arrays).
+template <int KD, bool PACKED, bool REV>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_kernel(const __grid_constant__ DecayTcParams args)
 {
@@ -147,14 +202,18 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     SmallD *sm = reinterpret_cast<SmallD *>(base + L::kOffSmall);
-    Ctx cx{&sm->abort_flag, args.wait_limit_ns, args.d.status};
+    const uint32_t s0 = smem_u32(base), sS = s0 + L::kOffSmall;
+    auto wait1 = [&](uint32_t bar, uint32_t parity) { return bounded_wait<false>(sS + offsetof(SmallD, abort_flag), bar, parity); };
+    auto waitw = [&](uint32_t bar, uint32_t parity) { return bounded_wait<true>(sS + offsetof(SmallD, abort_flag), bar, parity); };
+    auto power = [&](int e) { return ldsf(sS + (uint32_t)offsetof(SmallD, pw) + 4 * e); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     int tile = blockIdx.x, which = 0;
     while (tile >= args.tiles[which]) tile -= args.tiles[which++];
     const DecaySweep &sw = args.sw[which];
     const TcSweepMaps &maps = args.maps[which];
     const int h = blockIdx.y, H = args.d.H, n_all = sw.n, c0 = tile * 64;
-    const bool rev = sw.rev, packed = args.d.cu_seqlens != nullptr;
+    constexpr bool packed = PACKED;
+    const bool rev = REV && sw.rev;
 
     // this CTA's sequence
     int b = blockIdx.z, T = args.d.T, seq0 = 0;
@@ -225,62 +284,55 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     const int row = (warp & 3) * 32 + lane;     // the TMEM lane, and tile row, of this thread
     const int group = warp >> 2;
     constexpr uint32_t kHi = desc_hi(1024, 2);
-    const uint32_t sA = smem_u32(base + L::kOffA), sB = smem_u32(base + L::kOffB), sC = smem_u32(base + L::kOffC);
+    const uint32_t sA = s0 + L::kOffA, sB = s0 + L::kOffB, sC = s0 + L::kOffC;
 
     if (group == 0) {
         regs_dec<kRegsIssue>();
         if (warp == 0 && lane == 0) {
+            int loaded = 0;
             // --------------------------------------------------- producer
-            // loads in the order in which their buffers come free: b and a of chunk c after
-            // chunk c - 2's dS and Ye, c of chunk c once chunk c - 3's outputs have left
-            auto load = [&](const CUtensorMap *map, uint32_t off, int blocks, int x, uint64_t *bar, int c) {
-                const int t0 = chunk_t0(c), cy = packed ? h : t0, cz = packed ? seq0 + t0 : (int)bh;
-                mbar_arrive_expect_tx(bar, blocks * kBlk);
-                for (int k = 0; k < blocks; ++k) tma_load_3d(base + off + k * kBlk, map, bar, x + 64 * k, cy, cz);
-            };
-            // warms L2 for a chunk whose buffers are still in use
-            auto warm = [&](const CUtensorMap *map, int blocks, int x, int c) {
-                const int t0 = chunk_t0(c), cy = packed ? h : t0, cz = packed ? seq0 + t0 : (int)bh;
-                for (int k = 0; k < blocks; ++k) tma_prefetch_l2_3d(map, x + 64 * k, cy, cz);
-            };
-            int nb = 0, na = 0, nc = 0;    // chunks issued
-            for (int c = 0; c < nch; ++c) {
-                const int s = c & 1;
-                if (c >= 2 && !wait1(cx, &sm->emptyB[s], ((c >> 1) - 1) & 1)) break;
-                load(&maps.b, L::kOffB + s * L::kTile, L::NB, 0, &sm->fullB[s], c);
-                nb = c + 1;
-                if (c >= 2 && !wait1(cx, &sm->emptyA[s], ((c >> 1) - 1) & 1)) break;
-                load(&maps.a, L::kOffA + s * L::kTile, L::NB, 0, &sm->fullA[s], c);
-                na = c + 1;
-                bool ok = true;
-                for (; ok && nc < nch && nc <= (c == 1 ? 2 : c); ++nc) {
-                    ok = nc < kStC || wait1(cx, &sm->emptyC[nc % kStC], (nc / kStC - 1) & 1);
-                    if (!ok) break;
-                    load(&maps.c, L::kOffC + (nc % kStC) * kBlk, 1, c0, &sm->fullC[nc % kStC], nc);
-                }
-                if (!ok) break;
-                if (c + 2 < nch) {
-                    if (tile == 0) {       // (the other tiles of the head read the same a, b)
-                        warm(&maps.b, L::NB, 0, c + 2);
-                        warm(&maps.a, L::NB, 0, c + 2);
+            // a chunk's boxes in the order in which their buffers come free: b and a of chunk c after chunk
+            // c - 2's dS and Ye, c once chunk c - 3's outputs have left.  Each is followed by an L2
+            // prefetch of the same box two chunks on, whose buffer is still in use (a, b: by the
+            // head's first tile only, the others read the same).
+            bool ok = true;
+            for (int c = 0; c < nch && ok; ++c) {
+                const int s = c & 1, t0 = chunk_t0(c), t2 = chunk_t0(c + 2);
+#pragma unroll 1
+                for (int i = 0; i <= 2 * L::NB; ++i) {
+                    const bool is_c = i == 2 * L::NB, is_a = i >= L::NB;
+                    const int k = is_c ? 0 : is_a ? i - L::NB : i, x = is_c ? c0 : 64 * k;
+                    const uint32_t full = is_c ? BAR(fullC, c % kStC) : is_a ? BAR(fullA, s) : BAR(fullB, s);
+                    const uint32_t dst = is_c ? sC + (c % kStC) * kBlk : (is_a ? sA : sB) + s * L::kTile + k * kBlk;
+                    const CUtensorMap *map = is_c ? &maps.c : is_a ? &maps.a : &maps.b;
+                    if (k == 0) {
+                        const uint32_t empty = is_c ? BAR(emptyC, c % kStC) : is_a ? BAR(emptyA, s) : BAR(emptyB, s);
+                        ok = c < (is_c ? kStC : 2) || wait1(empty, (is_c ? c / kStC - 1 : (c >> 1) - 1) & 1);
+                        if (!ok) break;
+                        bar_expect(full, is_c ? kBlk : L::kTile);
                     }
-                    warm(&maps.c, 1, c0, c + 2);
+                    tma_load(dst, map, full, x, packed ? h : t0, packed ? seq0 + t0 : (int)bh);
+                    if (c + 2 < nch && (is_c || tile == 0)) tma_prefetch_l2_3d(map, x, packed ? h : t2, packed ? seq0 + t2 : (int)bh);
+                    loaded = c * 3 + (is_c ? 3 : is_a ? 2 : 1);
                 }
             }
-            if (aborted(cx)) {
-                // every issued load lands before the CTA may exit
-                for (int c = max(0, nb - 2); c < nb; ++c) mbar_wait(&sm->fullB[c & 1], (c >> 1) & 1, cx.limit);
-                for (int c = max(0, na - 2); c < na; ++c) mbar_wait(&sm->fullA[c & 1], (c >> 1) & 1, cx.limit);
-                for (int c = max(0, nc - kStC); c < nc; ++c) mbar_wait(&sm->fullC[c % kStC], (c / kStC) & 1, cx.limit);
+            // every issued load lands before the CTA may exit (the last six, in order)
+            for (int i = max(0, loaded - 9); i < loaded; ++i) {
+                const int c = i / 3, k = i % 3;
+                if (k == 2) wait1(BAR(fullC, c % kStC), (c / kStC) & 1);
+                else if (3 * (c + 2) + k >= loaded) wait1(k ? BAR(fullA, c & 1) : BAR(fullB, c & 1), (c >> 1) & 1);
             }
         } else if (warp == 1 && lane == 0) {
             // ------------------------------------------------- MMA: scores
             constexpr uint32_t idP = idesc_bf16_f32(128, 128, false, false);
             for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
-                if (!wait1(cx, &sm->fullB[s], (c >> 1) & 1) || !wait1(cx, &sm->fullA[s], (c >> 1) & 1)) break;
+                if (!wait1(BAR(fullB, s), (c >> 1) & 1) || !wait1(BAR(fullA, s), (c >> 1) & 1)) break;
+                // the rows behind a packed sequence (in its last chunk) are zeros in b and c once its weighted
+                // values are written: what lies there may be anything, and a mask of zeros would let it through
+                if (packed && c == nch - 1 && !wait1(BAR(w_full, 0), c & 1)) break;
                 // the buffer held P of chunk c - 2, whose product is done
-                if (c >= 2 && !wait1(cx, &sm->p_free[s], ((c >> 1) - 1) & 1)) break;
+                if (c >= 2 && !wait1(BAR(p_free, s), ((c >> 1) - 1) & 1)) break;
                 tc_fence_after();
                 const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(sB + s * L::kTile, 16);
                 const uint32_t d = tmem + kColP + s * 128;
@@ -289,28 +341,28 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     const uint32_t o = ((k >> 2) * kBlk + (k & 3) * 32) >> 4;
                     mma_ss(d, alo + o, kHi, blo + o, kHi, idP, k > 0);
                 }
-                tc_commit(&sm->p_raw[s]);
-                tc_commit(&sm->emptyA[s]);
-                tc_commit(&sm->emptyB[s]);
+                bar_commit(BAR(p_raw, s));
+                bar_commit(BAR(emptyA, s));
+                bar_commit(BAR(emptyB, s));
             }
         } else if (warp == 2 && lane == 0) {
             // ----------------------------------------------------- MMA: dS
             constexpr uint32_t idDS = idesc_bf16_f32(128, 128, true, true);
             for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
-                if (!wait1(cx, &sm->fullB[s], (c >> 1) & 1) || !wait1(cx, &sm->w_full, c & 1)) break;
-                if (c >= 1 && !wait1(cx, &sm->ds_empty, (c - 1) & 1)) break;
+                if (!wait1(BAR(fullB, s), (c >> 1) & 1) || !wait1(BAR(w_full, 0), c & 1)) break;
+                if (c >= 1 && !wait1(BAR(ds_empty, 0), (c - 1) & 1)) break;
                 tc_fence_after();
                 // (ra = 64: rows 64 .. 127 of the product come from the tile behind b and are not used)
-                const uint32_t alo = desc_lo(sB + s * L::kTile, kBlk), blo = desc_lo(smem_u32(base + L::kOffW), kBlk);
+                const uint32_t alo = desc_lo(sB + s * L::kTile, kBlk), blo = desc_lo(s0 + L::kOffW, kBlk);
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t o = k * (2048 >> 4);
                     mma_ss(tmem + kColDS, alo + o, kHi, blo + o, kHi, idDS, k > 0);
                 }
-                tc_commit(&sm->ds_full);
-                tc_commit(&sm->w_empty);
-                tc_commit(&sm->emptyB[s]);
+                bar_commit(BAR(ds_full, 0));
+                bar_commit(BAR(w_empty, 0));
+                bar_commit(BAR(emptyB, s));
             }
         } else if (warp == 3 && lane == 0) {
             // ------------------------------------------------ MMA: outputs
@@ -318,54 +370,51 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
                 // (the state of chunk c is published once Ye of chunk c - 1 has been read)
-                if (!wait1(cx, &sm->fullA[s], (c >> 1) & 1) || !wait1(cx, &sm->s_full, c & 1)) break;
+                if (!wait1(BAR(fullA, s), (c >> 1) & 1) || !wait1(BAR(s_full, 0), c & 1)) break;
                 tc_fence_after();
                 {
-                    const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(smem_u32(base + L::kOffS), kBlk);
+                    const uint32_t alo = desc_lo(sA + s * L::kTile, 16), blo = desc_lo(s0 + L::kOffS, kBlk);
 #pragma unroll 1
                     for (int k = 0; k < KD / 16; ++k) {
                         const uint32_t o = ((k >> 2) * kBlk + (k & 3) * 32) >> 4;
                         mma_ss(tmem + kColYe, alo + o, kHi, blo + k * (2048 >> 4), kHi, idY, k > 0);
                     }
                 }
-                tc_commit(&sm->ye_full);
-                tc_commit(&sm->emptyA[s]);
-                if (!wait1(cx, &sm->fullC[c % kStC], (c / kStC) & 1) || !wait1(cx, &sm->p_ready[s], (c >> 1) & 1)) break;
-                if (c >= 1 && !wait1(cx, &sm->yi_empty, (c - 1) & 1)) break;
-                // the rows behind a packed sequence are zeros in c once its weighted values are written
-                // (only the last chunk has any: no later phase of w_full can hide this one)
-                if (packed && c == nch - 1 && !wait1(cx, &sm->w_full, c & 1)) break;
+                bar_commit(BAR(ye_full, 0));
+                bar_commit(BAR(emptyA, s));
+                if (!wait1(BAR(fullC, c % kStC), (c / kStC) & 1) || !wait1(BAR(p_ready, s), (c >> 1) & 1)) break;
+                if (c >= 1 && !wait1(BAR(yi_empty, 0), (c - 1) & 1)) break;
                 tc_fence_after();
                 const uint32_t blo = desc_lo(sC + (c % kStC) * kBlk, kBlk), a = tmem + kColP + s * 128;
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) mma_ts(tmem + kColYi, a + 8 * k, blo + k * (2048 >> 4), kHi, idY, k > 0);
-                tc_commit(&sm->yi_full);
-                tc_commit(&sm->p_free[s]);
+                bar_commit(BAR(yi_full, 0));
+                bar_commit(BAR(p_free, s));
             }
         }
         if (warp >= 1 && lane == 0) {
             // every MMA that this thread issued completes before TMEM is released
-            tc_commit(&sm->done[warp - 1]);
-            mbar_wait(&sm->done[warp - 1], 0, cx.limit);
+            bar_commit(BAR(done, warp - 1));
+            wait1(BAR(done, warp - 1), 0);
         }
         __syncwarp();
     } else if (group == 1) {
         // --------------------------------------------------------- scores
-        // the powers of a diagonal block's row: the same for every chunk
-        // (a masked score is dropped, not multiplied by 0: behind a packed sequence it may be anything)
+        // the powers of a diagonal block's row (0 behind the mask), and of a column of the blocks below: the same
+        // for every chunk
         const int R = warp & 3;
         float2 wd[16], wc[16];
-        const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const int e = rev ? j - lane : lane - j;
-            (j & 1 ? wd[j / 2].y : wd[j / 2].x) = sm->pw[e >= 0 ? e : 0];
-            (j & 1 ? wc[j / 2].y : wc[j / 2].x) = sm->pw[rev ? j : 31 - j];
+            const float d = power(e >= 0 ? e : 0);
+            (j & 1 ? wd[j / 2].y : wd[j / 2].x) = e >= 0 ? d : 0.f;
+            (j & 1 ? wc[j / 2].y : wc[j / 2].x) = power(rev ? j : 31 - j);
         }
         const int J0 = rev ? R : 0, J1 = rev ? 3 : R;     // the 32-column blocks that the mask leaves
         for (int c = 0; c < nch; ++c) {
             const int s = c & 1;
-            if (!waitw(cx, &sm->p_raw[s], (c >> 1) & 1)) break;
+            if (!waitw(BAR(p_raw, s), (c >> 1) & 1)) break;
             tc_fence_after();
             const uint32_t tP = tmem + lane_base + kColP + s * 128;
 #pragma unroll 1
@@ -382,10 +431,10 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float2 p = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), wd[i]);
-                            o[i] = pack_bf16x2(keep >> (2 * i) & 1 ? p.x : 0.f, keep >> (2 * i + 1) & 1 ? p.y : 0.f);
+                            o[i] = pack_bf16x2(p.x, p.y);
                         }
                     } else {
-                        const float rf = sm->pw[rev ? 32 * J - row : row - 32 * J - 31];
+                        const float rf = power(rev ? 32 * J - row : row - 32 * J - 31);
                         const float2 rf2 = make_float2(rf, rf);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -399,29 +448,28 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             }
             tc_wait_st();
             tc_fence_before();
-            warp_arrive(&sm->p_ready[s]);
+            bar_arrive_warp(BAR(p_ready, s));
         }
     } else if (group == 2) {
         // ------------------------------------------------ weighted values
         regs_dec<kRegsValues>();
-        uint8_t *tW = base + L::kOffW;
+        const uint32_t tW = s0 + L::kOffW;
         for (int c = 0; c < nch; ++c) {
             const int s = c % kStC, n = chunk_n(c);
-            uint8_t *tC = base + L::kOffC + s * kBlk;
+            const uint32_t tC = sC + s * kBlk;
             const bool in = row < n;
-            const float w = in ? sm->pw[rev ? row + 1 : n - 1 - row] * sw.write_scale : 0.f;
+            const float w = in ? power(rev ? row + 1 : n - 1 - row) * sw.write_scale : 0.f;
             const float2 w2 = make_float2(w, w), nw2 = make_float2(-w, -w);
-            if (!waitw(cx, &sm->fullC[s], (c / kStC) & 1)) break;
+            if (!waitw(BAR(fullC, s), (c / kStC) & 1)) break;
             if (packed && n < kCT) {
                 // the rows behind the sequence are another's (or nobody's): they become zeros in b and c
-                if (!waitw(cx, &sm->fullB[c & 1], (c >> 1) & 1)) break;
+                if (!waitw(BAR(fullB, c & 1), (c >> 1) & 1)) break;
                 if (!in) {
 #pragma unroll 1
                     for (int x = 0; x < 8; ++x) {
-                        *reinterpret_cast<uint4 *>(tC + sw128_offset(row, x)) = make_uint4(0, 0, 0, 0);
+                        sts4(tC + sw128_offset(row, x), 0, 0, 0, 0);
                         for (int k = 0; k < L::NB; ++k)
-                            *reinterpret_cast<uint4 *>(base + L::kOffB + (c & 1) * L::kTile + k * kBlk + sw128_offset(row, x)) =
-                                make_uint4(0, 0, 0, 0);
+                            sts4(sB + (c & 1) * L::kTile + k * kBlk + sw128_offset(row, x), 0, 0, 0, 0);
                     }
                 }
             }
@@ -429,7 +477,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             uint32_t hi[32], lo[32];
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                const uint4 raw = *reinterpret_cast<const uint4 *>(tC + sw128_offset(row, x));
+                const uint4 raw = lds4(tC + sw128_offset(row, x));
                 const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -442,15 +490,15 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     lo[4 * x + e] = pack_bf16x2(d.x, d.y);
                 }
             }
-            if (c >= 1 && !waitw(cx, &sm->w_empty, (c - 1) & 1)) break;
+            if (c >= 1 && !waitw(BAR(w_empty, 0), (c - 1) & 1)) break;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 const uint32_t at = sw128_offset(row, x);
-                *reinterpret_cast<uint4 *>(tW + at) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-                *reinterpret_cast<uint4 *>(tW + kBlk + at) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+                sts4(tW + at, hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
+                sts4(tW + kBlk + at, lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
             }
             fence_proxy_async_smem();
-            warp_arrive(&sm->w_full);
+            bar_arrive_warp(BAR(w_full, 0));
         }
     } else {
         // ---------------------------------------------- state and outputs
@@ -468,14 +516,13 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * step], src[(2 * j + 1) * step]);
         }
         auto publish = [&]() {
-            uint8_t *tS = base + L::kOffS;
+            const uint32_t tS = s0 + L::kOffS;
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                *reinterpret_cast<uint4 *>(tS + sw128_offset(row, x)) =
-                    make_uint4(pack_bf16x2(S[4 * x].x, S[4 * x].y), pack_bf16x2(S[4 * x + 1].x, S[4 * x + 1].y),
-                               pack_bf16x2(S[4 * x + 2].x, S[4 * x + 2].y), pack_bf16x2(S[4 * x + 3].x, S[4 * x + 3].y));
+                sts4(tS + sw128_offset(row, x), pack_bf16x2(S[4 * x].x, S[4 * x].y), pack_bf16x2(S[4 * x + 1].x, S[4 * x + 1].y),
+                     pack_bf16x2(S[4 * x + 2].x, S[4 * x + 2].y), pack_bf16x2(S[4 * x + 3].x, S[4 * x + 3].y));
             fence_proxy_async_smem();
-            warp_arrive(&sm->s_full);
+            bar_arrive_warp(BAR(s_full, 0));
         };
         const float s_in = sw.out_scale * sw.write_scale;
         const float2 si2 = make_float2(s_in, s_in);
@@ -486,7 +533,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             float ye[64];
             if (c >= 1) {
                 // Ye of chunk c - 1 moves to registers, which frees its accumulator and the state's tile
-                ok = waitw(cx, &sm->ye_full, (c - 1) & 1);
+                ok = waitw(BAR(ye_full, 0), (c - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 float(&y0)[32] = *reinterpret_cast<float(*)[32]>(ye), (&y1)[32] = *reinterpret_cast<float(*)[32]>(ye + 32);
@@ -501,12 +548,12 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 // the outputs of chunk c - 1
                 const int n = chunk_n(c - 1), t0 = chunk_t0(c - 1);
                 const int e = rev ? n - 1 - row : row + 1;
-                const float s_ex = sw.out_scale * sm->pw[e >= 0 ? e : 0];
+                const float s_ex = sw.out_scale * power(e >= 0 ? e : 0);
                 const float2 se2 = make_float2(s_ex, s_ex);
                 // the rows leave through the chunk's own tile of c: Yi has read it, and so has the weighting
                 // of its values (dS of this chunk was waited for)
-                uint8_t *tY = base + L::kOffC + ((c - 1) % kStC) * kBlk;
-                ok = waitw(cx, &sm->yi_full, (c - 1) & 1);
+                const uint32_t tY = sC + ((c - 1) % kStC) * kBlk;
+                ok = waitw(BAR(yi_full, 0), (c - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -516,7 +563,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     wait_loaded(yi);
                     if (x == 32) {
                         tc_fence_before();
-                        warp_arrive(&sm->yi_empty);
+                        bar_arrive_warp(BAR(yi_empty, 0));
                     }
                     uint32_t o[16];
 #pragma unroll
@@ -527,8 +574,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4 *>(tY + sw128_offset(row, x / 8 + q)) =
-                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        sts4(tY + sw128_offset(row, x / 8 + q), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
                 if (packed && n < kCT) {
                     // only the sequence's own rows, 8 lanes each
@@ -536,19 +582,19 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
 #pragma unroll 1
                     for (int r = r0 + (lane >> 3); r < min(n, r0 + 32); r += 4)
                         *reinterpret_cast<uint4 *>(out + ((size_t)(seq0 + t0 + r) * H + h) * n_all + c0 + (lane & 7) * 8) =
-                            *reinterpret_cast<const uint4 *>(tY + sw128_offset(r, lane & 7));
+                            lds4(tY + sw128_offset(r, lane & 7));
                 } else {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && r0 < n) {    // (rows behind the end of a sequence of its own are not written)
-                        tma_store_3d(&maps.out, tY + r0 * 128, c0, packed ? h : t0 + r0, packed ? seq0 + t0 + r0 : (int)bh);
+                        tma_store(&maps.out, tY + r0 * 128, c0, packed ? h : t0 + r0, packed ? seq0 + t0 + r0 : (int)bh);
                         tma_store_commit();
                     }
                 }
             }
             if (c < nch) {
-                const float gn = sm->pw[chunk_n(c)];
-                ok = waitw(cx, &sm->ds_full, c & 1);
+                const float gn = power(chunk_n(c));
+                ok = waitw(BAR(ds_full, 0), c & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const float2 gn2 = make_float2(gn, gn), minus = make_float2(-1.f, -1.f);
@@ -561,7 +607,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                     wait_loaded(lo);
                     if (x == 1) {
                         tc_fence_before();
-                        warp_arrive(&sm->ds_empty);
+                        bar_arrive_warp(BAR(ds_empty, 0));
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)    // (the second part's sign is turned)
@@ -573,7 +619,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             if (c >= 1) {
                 // the rows that left through chunk c - 1's tile have been read: the tile may be filled again
                 if (lane == 0) tma_store_wait_read<0>();
-                warp_arrive(&sm->emptyC[(c - 1) % kStC]);
+                bar_arrive_warp(BAR(emptyC, (c - 1) % kStC));
             }
         }
         if (lane == 0) tma_store_wait_all<0>();
@@ -594,19 +640,28 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && aborted(cx)) atomicExch(cx.status, kStatusTimeout);
+    if (tid == 0 && sm->abort_flag) atomicExch(args.d.status, kStatusTimeout);
     if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int KD, bool PACKED, bool REV>
+cudaError_t launch(const DecayTcParams &p, cudaStream_t stream)
+{
+    static OncePerDevice once;
+    const cudaError_t e = set_smem_once(decay_tc_kernel<KD, PACKED, REV>, smem_bytes<KD>(), once);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(p.tiles[0] + p.tiles[1] + p.tiles[2], p.d.H, p.B);
+    decay_tc_kernel<KD, PACKED, REV><<<grid, kThreads, smem_bytes<KD>(), stream>>>(p);
+    return cudaGetLastError();
 }
 
 template <int KD>
 cudaError_t launch(const DecayTcParams &p, cudaStream_t stream)
 {
-    static OncePerDevice once;
-    const cudaError_t e = set_smem_once(decay_tc_kernel<KD>, smem_bytes<KD>(), once);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(p.tiles[0] + p.tiles[1] + p.tiles[2], p.d.H, p.B);
-    decay_tc_kernel<KD><<<grid, kThreads, smem_bytes<KD>(), stream>>>(p);
-    return cudaGetLastError();
+    bool rev = false;
+    for (int i = 0; i < 3; ++i) rev = rev || (p.tiles[i] && p.sw[i].rev);
+    if (p.d.cu_seqlens) return launch<KD, true, false>(p, stream);
+    return rev ? launch<KD, false, true>(p, stream) : launch<KD, false, false>(p, stream);
 }
 
 }  // namespace
