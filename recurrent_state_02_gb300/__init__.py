@@ -368,24 +368,43 @@ def _workspace(workspace, need, device):
 def _call(entry, device, *args):
     """One library call on `device` and its current stream (appended to args)."""
     fn = getattr(_native.lib(), entry)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(device))
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with _device_guard(device):
             st = fn(*args, _stream(device))
-    _native.check(st, entry)
+    if st:
+        _native.check(st, entry)
+
+
+def _want(t, name, shape, dtype, device):
+    """_require for a tensor that must be given: one pass over what it compares, as these calls may be
+    a few microseconds long."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous() or not t.is_cuda:
+        _require(t, name, shape, dtype, device)
+
+
+def _out(t, name, shape, dtype, device):
+    """The caller's output tensor, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(t, name, shape, dtype, device)
+    return t
 
 
 def _decay_inputs(q, k, v, decay, shape_qk, shape_v, H):
-    if q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {q.dtype}")
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
     dev = q.device
-    _require(q, "q", shape_qk, q.dtype, dev)
-    _require(k, "k", shape_qk, q.dtype, dev)
-    _require(v, "v", shape_v, q.dtype, dev)
+    _want(q, "q", shape_qk, dt, dev)
+    _want(k, "k", shape_qk, dt, dev)
+    _want(v, "v", shape_v, dt, dev)
     if decay is None:
         raise ValueError("decay must be given (ones for no decay)")
-    _require(decay, "decay", (H,), torch.float32, dev)
+    _want(decay, "decay", (H,), torch.float32, dev)
+    return dt, dev
 
 
 def _bytes(entry, device, *args):
@@ -407,21 +426,15 @@ def decay_prefill(q, k, v, decay, S0=None, scale=1.0, y=None, S_out=None, worksp
     [B,H,r,dv] fp32 or None (zero).  Returns (y [B,H,T,dv] in the input dtype, S_T)."""
     B, H, T, r = q.shape
     dv = v.shape[3]
-    dev = q.device
-    _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dv), H)
-    _require(S0, "S0", (B, H, r, dv), torch.float32, dev)
-    if y is None:
-        y = torch.empty_like(v)
-    else:
-        _require(y, "y", (B, H, T, dv), q.dtype, dev)
-    if S_out is None:
-        S_out = torch.empty((B, H, r, dv), device=dev, dtype=torch.float32)
-    else:
-        _require(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
-    dt = _DTYPES[q.dtype]
+    dt, dev = _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dv), H)
+    if S0 is not None:
+        _want(S0, "S0", (B, H, r, dv), torch.float32, dev)
+    y = _out(y, "y", (B, H, T, dv), dt, dev)
+    S_out = _out(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
+    dt = _DTYPES[dt]
     workspace, ws_bytes = _workspace(workspace, _bytes("la_decay_prefill_workspace_bytes", dev, B, H, T, r, dv, dt), dev)
-    _call("la_decay_prefill", dev, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(decay), _ptr(S0), B, H, T, r, dv, float(scale),
-          _ptr(y), _ptr(S_out), _ptr(workspace), ws_bytes)
+    _call("la_decay_prefill", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, decay.data_ptr(), _ptr(S0), B, H, T, r,
+          dv, scale, y.data_ptr(), S_out.data_ptr(), _ptr(workspace), ws_bytes)
     return y, S_out
 
 
@@ -432,23 +445,17 @@ def decay_prefill_varlen(q, k, v, decay, cu_seqlens, S0=None, scale=1.0, y=None,
     (y [total_T, H, dv], S_T [B,H,r,dv])."""
     total_T, H, r = q.shape
     dv = v.shape[2]
-    dev = q.device
-    _decay_inputs(q, k, v, decay, (total_T, H, r), (total_T, H, dv), H)
+    dt, dev = _decay_inputs(q, k, v, decay, (total_T, H, r), (total_T, H, dv), H)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.device != dev:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor on the device of q")
     B = cu_seqlens.numel() - 1
-    _require(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
-    _require(S0, "S0", (B, H, r, dv), torch.float32, dev)
-    if y is None:
-        y = torch.empty_like(v)
-    else:
-        _require(y, "y", (total_T, H, dv), q.dtype, dev)
-    if S_out is None:
-        S_out = torch.empty((B, H, r, dv), device=dev, dtype=torch.float32)
-    else:
-        _require(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
-    _call("la_decay_prefill_varlen", dev, _ptr(q), _ptr(k), _ptr(v), _DTYPES[q.dtype], _ptr(decay), _ptr(S0),
-          _ptr(cu_seqlens), B, H, total_T, r, dv, float(scale), _ptr(y), _ptr(S_out))
+    _want(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    if S0 is not None:
+        _want(S0, "S0", (B, H, r, dv), torch.float32, dev)
+    y = _out(y, "y", (total_T, H, dv), dt, dev)
+    S_out = _out(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
+    _call("la_decay_prefill_varlen", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dt], decay.data_ptr(),
+          _ptr(S0), cu_seqlens.data_ptr(), B, H, total_T, r, dv, scale, y.data_ptr(), S_out.data_ptr())
     return y, S_out
 
 
@@ -457,17 +464,13 @@ def decay_decode_step(q, k, v, decay, S, scale=1.0, y=None):
     q, k [B,H,1,r], v [B,H,1,dv]; decay [H] fp32.  Returns y [B,H,1,dv]."""
     B, H, one, r = q.shape
     dv = v.shape[3]
-    dev = q.device
     if one != 1:
         raise ValueError("decode takes one token per request")
-    _decay_inputs(q, k, v, decay, (B, H, 1, r), (B, H, 1, dv), H)
-    _require(S, "S", (B, H, r, dv), torch.float32, dev)
-    if y is None:
-        y = torch.empty_like(v)
-    else:
-        _require(y, "y", (B, H, 1, dv), q.dtype, dev)
-    _call("la_decay_decode_step", dev, _ptr(q), _ptr(k), _ptr(v), _DTYPES[q.dtype], _ptr(decay), _ptr(S), B, H, r, dv,
-          float(scale), _ptr(y))
+    dt, dev = _decay_inputs(q, k, v, decay, (B, H, 1, r), (B, H, 1, dv), H)
+    _want(S, "S", (B, H, r, dv), torch.float32, dev)
+    y = _out(y, "y", (B, H, 1, dv), dt, dev)
+    _call("la_decay_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dt], decay.data_ptr(),
+          S.data_ptr(), B, H, r, dv, scale, y.data_ptr())
     return y
 
 
@@ -483,17 +486,19 @@ def decay_backward(q, k, v, dy, decay, S0=None, dS_T=None, scale=1.0, workspace=
     fp32.  The decay is a constant of the head and gets no gradient."""
     B, H, T, r = q.shape
     dvd = v.shape[3]
-    dev = q.device
-    _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dvd), H)
-    _require(dy, "dy", (B, H, T, dvd), q.dtype, dev)
-    _require(S0, "S0", (B, H, r, dvd), torch.float32, dev)
-    _require(dS_T, "dS_T", (B, H, r, dvd), torch.float32, dev)
+    dt, dev = _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dvd), H)
+    _want(dy, "dy", (B, H, T, dvd), dt, dev)
+    if S0 is not None:
+        _want(S0, "S0", (B, H, r, dvd), torch.float32, dev)
+    if dS_T is not None:
+        _want(dS_T, "dS_T", (B, H, r, dvd), torch.float32, dev)
     dq, dk, dv_out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dS0 = torch.empty((B, H, r, dvd), device=dev, dtype=torch.float32)
-    dt = _DTYPES[q.dtype]
+    dt = _DTYPES[dt]
     workspace, ws_bytes = _workspace(workspace, _bytes("la_decay_backward_workspace_bytes", dev, B, H, T, r, dvd, dt), dev)
-    _call("la_decay_backward", dev, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(decay), _ptr(S0), B, H, T, r, dvd, float(scale),
-          _ptr(dy), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv_out), _ptr(dS0), _ptr(workspace), ws_bytes)
+    _call("la_decay_backward", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, decay.data_ptr(), _ptr(S0), B, H, T, r,
+          dvd, scale, dy.data_ptr(), _ptr(dS_T), dq.data_ptr(), dk.data_ptr(), dv_out.data_ptr(), dS0.data_ptr(),
+          _ptr(workspace), ws_bytes)
     return dq, dk, dv_out, dS0
 
 
@@ -505,35 +510,29 @@ def beam_select(logits, scores, done=None, eos=-1, next_scores=None, parents=Non
     candidate is the token eos, the score unchanged); eos the token that ends a beam, -1 none.
     Returns (next_scores [B,K] fp32, parents [B,K] int32, tokens [B,K] int32, done_out
     [B,K] uint8).  A slot without a candidate has score -inf, itself as parent and token 0."""
-    if logits.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {logits.dtype}")
-    B, K, V = logits.shape
-    dev = logits.device
+    dt = logits.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
     if not logits.is_cuda:
         raise ValueError("logits must be on a CUDA device")
-    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
-    if (V > 1 and logits.stride(2) != 1) or (B > 1 and K > 1 and logits.stride(0) != K * stride):
-        raise ValueError("logits must have contiguous rows at one stride")
-    _require(scores, "scores", (B, K), torch.float32, dev)
-    _require(done, "done", (B, K), torch.uint8, dev)
-    if next_scores is None:
-        next_scores = torch.empty((B, K), device=dev, dtype=torch.float32)
+    B, K, V = logits.shape
+    dev = logits.device
+    if logits.is_contiguous():
+        stride = V
     else:
-        _require(next_scores, "next_scores", (B, K), torch.float32, dev)
-    if parents is None:
-        parents = torch.empty((B, K), device=dev, dtype=torch.int32)
-    else:
-        _require(parents, "parents", (B, K), torch.int32, dev)
-    if tokens is None:
-        tokens = torch.empty((B, K), device=dev, dtype=torch.int32)
-    else:
-        _require(tokens, "tokens", (B, K), torch.int32, dev)
-    if done_out is None:
-        done_out = torch.empty((B, K), device=dev, dtype=torch.uint8)
-    else:
-        _require(done_out, "done_out", (B, K), torch.uint8, dev)
-    _call("la_beam_select", dev, _ptr(logits), _DTYPES[logits.dtype], stride, _ptr(scores), _ptr(done), B, K, V, eos,
-          _ptr(next_scores), _ptr(parents), _ptr(tokens), _ptr(done_out))
+        stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+        if (V > 1 and logits.stride(2) != 1) or (B > 1 and K > 1 and logits.stride(0) != K * stride):
+            raise ValueError("logits must have contiguous rows at one stride")
+    bk = (B, K)
+    _want(scores, "scores", bk, torch.float32, dev)
+    if done is not None:
+        _want(done, "done", bk, torch.uint8, dev)
+    next_scores = _out(next_scores, "next_scores", bk, torch.float32, dev)
+    parents = _out(parents, "parents", bk, torch.int32, dev)
+    tokens = _out(tokens, "tokens", bk, torch.int32, dev)
+    done_out = _out(done_out, "done_out", bk, torch.uint8, dev)
+    _call("la_beam_select", dev, logits.data_ptr(), _DTYPES[dt], stride, scores.data_ptr(), _ptr(done), B, K, V, eos,
+          next_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), done_out.data_ptr())
     return next_scores, parents, tokens, done_out
 
 
@@ -547,21 +546,23 @@ def state_reorder(S, parents, z=None, S_out=None, z_out=None):
     B, K = parents.shape
     n, H, r, dv = S.shape
     dev = S.device
-    _require(parents, "parents", (B, K), torch.int32, dev)
-    _require(S, "S", (B * K, H, r, dv), torch.float32, dev)
-    _require(z, "z", (B * K, H, r), torch.float32, dev)
-    if z is None and z_out is not None:
+    _want(parents, "parents", (B, K), torch.int32, dev)
+    _want(S, "S", (B * K, H, r, dv), torch.float32, dev)
+    if z is not None:
+        _want(z, "z", (B * K, H, r), torch.float32, dev)
+    elif z_out is not None:
         raise ValueError("z_out is taken only together with z")
     if S_out is None:
         if z_out is not None:
             raise ValueError("z_out is taken only together with S_out")
         S_out, z_out = S, z
     else:
-        _require(S_out, "S_out", (B * K, H, r, dv), torch.float32, dev)
-        if z is not None and z_out is None:
-            z_out = z if S_out.data_ptr() == S.data_ptr() else torch.empty_like(z)
-        _require(z_out, "z_out", (B * K, H, r), torch.float32, dev)
-    _call("la_state_reorder", dev, _ptr(S), _ptr(z), _ptr(parents), B, K, H, r, dv, _ptr(S_out), _ptr(z_out))
+        _want(S_out, "S_out", (B * K, H, r, dv), torch.float32, dev)
+        if z is not None:
+            if z_out is None:
+                z_out = z if S_out.data_ptr() == S.data_ptr() else torch.empty_like(z)
+            _want(z_out, "z_out", (B * K, H, r), torch.float32, dev)
+    _call("la_state_reorder", dev, S.data_ptr(), _ptr(z), parents.data_ptr(), B, K, H, r, dv, S_out.data_ptr(), _ptr(z_out))
     return S_out, z_out
 
 

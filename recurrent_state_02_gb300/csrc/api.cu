@@ -278,10 +278,17 @@ bool make_map_bf16_tok(CUtensorMap *map, const void *ptr, long long tokens, long
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Device address of the status word on the current device, looked up once per device (see noalloc_scratch).
 int *status_word()
 {
-    void *p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
+    static std::atomic<void *> addr[la::kMaxDevices];
+    const int dev = la::current_device_index();
+    if (dev < 0) return nullptr;
+    void *p = addr[dev].load(std::memory_order_acquire);
+    if (!p) {
+        if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess || !p) return nullptr;
+        addr[dev].store(p, std::memory_order_release);
+    }
     return static_cast<int *>(p);
 }
 
@@ -815,11 +822,9 @@ la::DecaySweep forward_sweep(const void *q, const void *k, const void *v, const 
     return s;
 }
 
-// Sequences of at most this many tokens take the token recurrence.
-#ifndef LA_DECAY_WALK
-#define LA_DECAY_WALK 32
-#endif
-constexpr int kDecayWalk = LA_DECAY_WALK;
+// Sequences of at most this many tokens take the token recurrence.  r = dv = 128, BF16: 8 heads 6.6 us at 16
+// tokens, 8.4 at 24, against 7.1 in chunks at any length up to 64; 1024 heads 66 and 107 us against 92.
+constexpr int kDecayWalk = 16;
 
 bool tc_sweep(const la::DecaySweep &s, bool bf16)
 {

@@ -16,20 +16,23 @@ namespace {
 // best K logits; K * K finalists then settle the request.
 //
 // One cluster of CS CTAs of 16 warps per request.  Warp gw of the cluster's 16 CS
-// takes part gw / K of row gw % K: 512-byte blocks, every (parts)-th one.  A warp keeps
-// the best 32 (logit, index) pairs it has seen sorted across its lanes, as 64-bit
-// keys that order by logit, then by lower index; a block without a logit as
-// high as the K-th key costs one vote.  On random logits a warp inserts about
-// K ln(n / K) of its n values.
-// After the cluster barrier warp w of CTA c merges the parts of row 16 c + w (over
+// takes part gw / K of row gw % K: 512-byte blocks, every (parts)-th one.  It pushes the logits
+// that may be among the row's K best into a buffer of its own, as 64-bit keys that order by
+// logit, then by lower index, and keeps the K best of a full buffer; the K-th of them, at
+// first the K-th largest of the lanes' maxima, is what a logit has to beat, so a block
+// without one costs a vote.
+// After the cluster barrier warp w of CTA c merges the parts of row c + CS w (over
 // distributed shared memory) and leaves the row's K keys and its lse in CTA 0;
 // after the second one a warp of CTA 0 picks the request's K best by the scores
 // in 64 bits, one head per row.
 constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps;
 
+constexpr int kSelBuf = 128;    // keys of a warp's buffer
+
 struct SelSmem {
-    unsigned long long keys[kSelWarps][kMaxBeams];        // each warp's best, best first (0: none)
+    unsigned long long keys[kSelWarps][kSelBuf];          // each warp's candidates; at the end its K best, best first (0: none)
     float m[kSelWarps], s[kSelWarps];                     // running maximum and sum of its part
+    int count[kSelWarps];                                 // keys in its buffer
     // CTA 0 only: the rows' best and their lse
     unsigned long long row_keys[kMaxBeams][kMaxBeams];
     double row_lse[kMaxBeams];
@@ -123,6 +126,14 @@ __device__ __forceinline__ void widen(uint4 w, float *x)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// 2^x, relative error about 2^-22 (results below 2^-126 are 0: nothing next to the maximum's 1)
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kSelThreads, 2)
 beam_select_kernel(const BeamSelectArgs args)
@@ -147,9 +158,40 @@ beam_select_kernel(const BeamSelectArgs args)
         const long long row_bytes = (long long)V * (BF16 ? 2 : 4);
         const int granules = (V + GE - 1) / GE;
         float m = -3.402823466e38f, s = 0.f;
-        unsigned long long key = 0, thr = 0;   // this lane's entry; the K-th entry
-        float thr_x = -INFINITY;
-        auto consume = [&](uint4 raw, int i0) {
+        unsigned long long thr = 0;      // what a key has to beat
+        float thr_x = -INFINITY;         // its logit
+        bool seeded = false;
+        int count = 0;                   // keys in the buffer
+        unsigned long long *buf = sm.keys[warp];
+        // keeps the K best of the buffer, sorted
+        auto keep_best = [&]() {
+            __syncwarp();
+            unsigned long long k4[kSelBuf / 32], mine = 0;
+#pragma unroll
+            for (int i = 0; i < kSelBuf / 32; ++i) k4[i] = lane + 32 * i < count ? buf[lane + 32 * i] : 0;
+#pragma unroll 1
+            for (int r = 0; r < K; ++r) {
+                unsigned long long best = k4[0];
+#pragma unroll
+                for (int i = 1; i < kSelBuf / 32; ++i) best = k4[i] > best ? k4[i] : best;
+                best = warp_max(best);
+                if (lane == r) mine = best;
+#pragma unroll
+                for (int i = 0; i < kSelBuf / 32; ++i)
+                    if (k4[i] == best) k4[i] = 0;
+            }
+            if (lane < K) buf[lane] = mine;
+            __syncwarp();
+            if (count >= K) {
+                thr = __shfl_sync(0xffffffffu, mine, K - 1);
+                thr_x = key_value(thr);
+                count = K;
+                if (lane == 0) sm.count[warp] = K;
+                __syncwarp();
+            }
+        };
+        // takes a granule into the running maximum and sum; returns its maximum
+        auto sum_up = [&](uint4 raw, int i0) -> float {
             float x[GE];
             widen<BF16>(raw, x);
             if (i0 + GE > V) {
@@ -161,60 +203,108 @@ beam_select_kernel(const BeamSelectArgs args)
 #pragma unroll
             for (int e = 1; e < GE; ++e) mx = fmaxf(mx, x[e]);   // (a NaN reaches the sum below)
             if (mx > m) {
-                s *= exp2f((m - mx) * kLog2e);
+                s *= ex2((m - mx) * kLog2e);
                 m = mx;
             }
-            float t = 0.f;
+            const float2 minus = make_float2(-m, -m), l2 = make_float2(kLog2e, kLog2e);
+            float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < GE; ++e) t += exp2f((x[e] - m) * kLog2e);
-            s += t;
-            if (__any_sync(0xffffffffu, mx >= thr_x && mx > -INFINITY)) {
-#pragma unroll 1
-                for (int e = 0; e < GE; ++e) {
-                    float xe = x[0];
-#pragma unroll
-                    for (int f = 1; f < GE; ++f) xe = e == f ? x[f] : xe;
-                    const unsigned long long mine = xe > -INFINITY ? make_key(xe, i0 + e) : 0;
-                    uint32_t todo = __ballot_sync(0xffffffffu, mine > thr);
-                    while (todo) {
-                        const int src = __ffs(todo) - 1;
-                        const unsigned long long nk = __shfl_sync(0xffffffffu, mine, src);
-                        const int at = __popc(__ballot_sync(0xffffffffu, key > nk));
-                        const unsigned long long up = __shfl_up_sync(0xffffffffu, key, 1);
-                        key = lane > at ? up : lane == at ? nk : key;
-                        thr = __shfl_sync(0xffffffffu, key, K - 1);
-                        todo &= todo - 1;
-                        todo &= __ballot_sync(0xffffffffu, mine > thr);
-                    }
-                }
-                if (thr) thr_x = key_value(thr);
+            for (int e = 0; e < GE; e += 2) {
+                const float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), minus), l2);
+                t = __fadd2_rn(t, make_float2(ex2(a.x), ex2(a.y)));
             }
+            s += t.x + t.y;
+            return mx;
         };
         const int step = parts * 32;
+        if (lane == 0) sm.count[warp] = 0;
+        __syncwarp();
         if (!skip) {
-            int g = part * 32 + lane;
             // (every lane runs the same number of steps: the votes below take the whole warp)
-            for (int base = part * 32; base < granules; base += U * step, g += U * step) {
+            for (int base = part * 32; base < granules; base += U * step) {
+                const int g = base + lane;
                 uint4 raw[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (g + u * step < granules) raw[u] = load_granule(p0, mis, g + u * step, row_bytes);
+                float mx[U], top = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (base + u * step >= granules) break;
-                    const int gu = g + u * step;
-                    consume(gu < granules ? raw[u] : make_uint4(0, 0, 0, 0), gu < granules ? gu * GE : V);
+                    raw[u] = make_uint4(0, 0, 0, 0);
+                    if (g + u * step < granules) raw[u] = load_granule(p0, mis, g + u * step, row_bytes);
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    mx[u] = -INFINITY;
+                    if (g + u * step < granules) mx[u] = sum_up(raw[u], (g + u * step) * GE);
+                    top = fmaxf(top, mx[u]);
+                }
+                if (!__any_sync(0xffffffffu, top >= thr_x && top > -INFINITY)) continue;
+                if (!seeded) {
+                    // K lanes have a maximum of at least this
+                    uint32_t o = top > -INFINITY ? order_f32(top) : 0, best = 0;
+#pragma unroll 1
+                    for (int r = 0; r < K; ++r) {
+                        best = __reduce_max_sync(0xffffffffu, o);
+                        if (lane == __ffs(__ballot_sync(0xffffffffu, o == best)) - 1) o = 0;
+                    }
+                    if (best) {
+                        thr = (static_cast<unsigned long long>(best) << 32) - 1;
+                        thr_x = unorder_f32(best);
+                    }
+                    seeded = true;
+                }
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    float mu = mx[0];
+                    uint4 ru = raw[0];
+#pragma unroll
+                    for (int w = 1; w < U; ++w)
+                        if (u == w) mu = mx[w], ru = raw[w];
+                    const bool hit = mu >= thr_x && mu > -INFINITY;
+                    const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+                    if (!hits) continue;
+                    float x[GE];
+                    widen<BF16>(ru, x);
+                    const int i0 = (g + u * step) * GE;
+                    if (count + GE * __popc(hits) <= kSelBuf) {
+                        // the few lanes with a candidate push on their own
+                        if (hit) {
+#pragma unroll
+                            for (int e = 0; e < GE; ++e)
+                                if (x[e] >= thr_x && x[e] > -INFINITY && i0 + e < V) {
+                                    const unsigned long long key = make_key(x[e], i0 + e);
+                                    if (key > thr) buf[atomicAdd(&sm.count[warp], 1)] = key;
+                                }
+                        }
+                        __syncwarp();
+                        count = *reinterpret_cast<volatile int *>(&sm.count[warp]);
+                    } else {
+                        // one element of every lane at a time, making room when there is none
+#pragma unroll 1
+                        for (int e = 0; e < GE; ++e) {
+                            if (count > kSelBuf - 32) keep_best();
+                            float xe = x[0];
+#pragma unroll
+                            for (int f = 1; f < GE; ++f) xe = e == f ? x[f] : xe;
+                            const unsigned long long key = make_key(xe, i0 + e);
+                            const bool in = hit && xe > -INFINITY && i0 + e < V && key > thr;
+                            const uint32_t who = __ballot_sync(0xffffffffu, in);
+                            if (in) buf[count + __popc(who & ((1u << lane) - 1u))] = key;
+                            count += __popc(who);
+                        }
+                        if (lane == 0) sm.count[warp] = count;
+                        __syncwarp();
+                    }
+                }
+                if (count >= 2 * K) keep_best();    // a tighter bound for what follows
             }
         }
+        keep_best();
         // the part's maximum and sum
         float mw = m;
 #pragma unroll
         for (int o = 16; o; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
-        s *= exp2f((m - mw) * kLog2e);
+        s *= ex2((m - mw) * kLog2e);
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane < K) sm.keys[warp][lane] = key;
         if (lane == 0) sm.m[warp] = mw, sm.s[warp] = s;
     }
     cluster_sync_all();
@@ -234,7 +324,7 @@ beam_select_kernel(const BeamSelectArgs args)
         for (int i = lane; i < parts; i += 32) {
             const int gw = k + i * K;
             SelSmem *at = in_cta(&sm, gw / kSelWarps);
-            sum += (double)at->s[gw % kSelWarps] * exp2(((double)at->m[gw % kSelWarps] - (double)mx) * 1.4426950408889634);
+            sum += (double)(at->s[gw % kSelWarps] * ex2((at->m[gw % kSelWarps] - mx) * kLog2e));
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

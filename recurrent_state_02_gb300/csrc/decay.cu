@@ -28,26 +28,30 @@ __device__ __forceinline__ void store_elem(void *p, size_t i, float x)
 }
 
 // ------------------------------------------------------- token recurrence
-// One CTA of 4 warps per (b, h, 64 columns), the state in registers: lane
-// (g, jj), g = lane / 4, holds rows {4 (8 m + g) + e : m < RP/32, e < 4} of the
-// four columns 4 jj .. 4 jj + 3 of its warp's 16.  A row's two operands come from
-// shared memory as 16-byte words that serve four columns (the 8 groups of a warp
-// read 128 different bytes), so a token costs a warp RP/16 shared loads
-// for 3 RP/32 * 16 / 2 packed FP32 instructions: the FMA pipe is the limit, not
-// shared memory.  The sums over rows are reduced two tokens at a time: 8 partial
-// sums per lane (2 tokens x 4 columns) over the 8 row groups, by a
-// reduce-scatter of 4 + 2 + 1 shuffles, which leaves each lane one total.
-// Tokens are staged in blocks of TB; the next block's values are fetched
-// into registers while this one is computed.
-constexpr int kRecCols = 64, kRecThreads = 128;
+// One CTA per (b, h, 32 columns), the state in registers.  Its W * CB warps (CB = 4 / CPL) split
+// the rows into blocks of 32 and the columns into blocks of 8 CPL; lane (g, jj), g = lane / 8,
+// holds rows 8 g .. 8 g + 7 of its warp's in CPL columns.  A token costs a warp four 16-byte
+// shared loads of its rows' q and k, one of its columns' v, 12 CPL packed FP32 instructions (row
+// pairs: k v, g S + k v, the sum with q) and one store of its partial sums; the 4 W partial outputs of a
+// column are added once per block of TB tokens.
+// CPL = 4 is for grids that fill the GPU: loads that a whole warp shares still take shared memory about
+// two cycles each, and one column per lane, with three FMAs per load, was bound by them.
+// CPL = 1 is for few heads, where a token's latency counts: four times the warps, a quarter of the
+// instructions each.
+// Tokens are staged in blocks; the next block's values are fetched into registers while this
+// one is computed.
+constexpr int kRecCols = 32, kRecRows = 32;
+// One CTA per SM at most takes CPL = 1: 24 CTAs of r = 64 (T = 1001, FP32) 114 us, against 203 with CPL = 4;
+// 128 CTAs of r = 128 158 us either way; 256 CTAs 278 against 235.
+constexpr long long kRecFew = 152;
 
-template <int RP>
+template <int W, int CPL>
 struct RecCfg {
-    static constexpr int M = RP / 32;                 // float4 row blocks per lane
-    static constexpr int TB = RP >= 256 ? 8 : 16;     // tokens per staged block
-    static constexpr int RS = RP + 4;                 // row stride of the staged a, b (floats)
-    static constexpr int NA = TB * RP / kRecThreads;  // staged a (or b) values per thread
-    static constexpr int NC = TB * kRecCols / kRecThreads;
+    static constexpr int R = W * kRecRows, CB = 4 / CPL, NW = W * CB, kThreads = 32 * NW;
+    static constexpr int TB = W <= 2 ? 32 : W == 4 ? 16 : 8;    // tokens per staged block
+    static constexpr int NA = TB / CB;                          // staged a (or b) values per thread
+    static constexpr int NC = (TB + NW - 1) / NW;
+    static constexpr uint32_t kSmem = 4 * (2 * TB * R + TB * kRecCols + 4 * W * TB * kRecCols);
 };
 
 struct RecArgs {
@@ -57,23 +61,24 @@ struct RecArgs {
 };
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 lo2(float4 a) { return make_float2(a.x, a.y); }
+__device__ __forceinline__ float2 hi2(float4 a) { return make_float2(a.z, a.w); }
 
-template <bool BF16, int RP>
-__global__ void __launch_bounds__(kRecThreads)
+template <bool BF16, int W, int CPL>
+__global__ void __launch_bounds__(32 * W * 4 / CPL)
 decay_rec_kernel(const __grid_constant__ RecArgs args)
 {
-    using C = RecCfg<RP>;
-    constexpr int M = C::M, TB = C::TB, RS = C::RS;
-    __shared__ float4 as4[TB * RS / 4], bs4[TB * RS / 4], cs4[TB * kRecCols / 4];
-    __shared__ float ys[TB][kRecCols];
-    float *as = reinterpret_cast<float *>(as4), *bs = reinterpret_cast<float *>(bs4),
-          *cs = reinterpret_cast<float *>(cs4);
+    using C = RecCfg<W, CPL>;
+    constexpr int R = C::R, TB = C::TB, NT = C::kThreads, NW = C::NW;
+    extern __shared__ float4 rec_smem[];
+    float *as = reinterpret_cast<float *>(rec_smem), *bs = as + TB * R, *cs = bs + TB * R;
+    float *ys = cs + TB * kRecCols;              // [4 W][TB][kRecCols]
     int tile = blockIdx.x, which = 0;
     while (tile >= args.tiles[which]) tile -= args.tiles[which++];
     const DecaySweep &sw = args.sw[which];
     const DecayArgs &d = args.d;
     const int h = blockIdx.y, b = blockIdx.z, H = d.H, ra = sw.ra, n = sw.n;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, jj = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool packed = d.cu_seqlens != nullptr;
     int T = d.T, seq0 = 0;
     if (packed) {
@@ -87,155 +92,131 @@ decay_rec_kernel(const __grid_constant__ RecArgs args)
         if (T < d.len_min || T > d.len_max) return;
     }
     const size_t bh = (size_t)b * H + h;
-    // row (of ra or n elements) of the sweep's t-th token
-    auto row = [&](int t) -> size_t {
-        const int at = sw.rev ? T - 1 - t : t;
-        return packed ? (size_t)(seq0 + at) * H + h : bh * T + at;
-    };
+    // the sweep's token t is row first + t * step of a, b (rows of ra elements) and c, out (of n)
+    const long long step = (sw.rev ? -1 : 1) * (packed ? (long long)H : 1);
+    const long long first = (packed ? (long long)seq0 * H + h : (long long)bh * T) + (sw.rev ? -step * (T - 1) : 0);
     const float g = d.decay[h];
-    const int c0 = tile * kRecCols, wc = warp * 16 + jj * 4;   // first column of the CTA; of the lane, inside it
-    const bool active = c0 + warp * 16 < n;                    // (warp-uniform)
+    const int c0 = tile * kRecCols, wr = warp % W, part = lane >> 3;
+    const int j1 = (warp / W * 8 + (lane & 7)) * CPL, j0 = c0 + j1;   // this lane's first column
+    const int i0 = wr * kRecRows + part * 8;                          // its 8 rows, as 4 pairs
 
-    // state rows 4 (8 m + g8) + e, columns c0 + wc + (0 .. 3) as two packed pairs
-    float2 s[M][4][2];
-    const bool vec = !sw.init_t && (n & 3) == 0 && (reinterpret_cast<uintptr_t>(sw.S_init) & 15) == 0;
+    float2 s[4][CPL];     // [row pair][column]
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int p = 0; p < 4; ++p)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 4 * (8 * m + g8) + e, j = c0 + wc;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (sw.S_init && i < ra && j < n) {
-                const float *src = sw.S_init + bh * ra * n;
-                if (vec) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(src + (size_t)i * n + j);
-                    v[0] = q4.x, v[1] = q4.y, v[2] = q4.z, v[3] = q4.w;
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (j + x < n) v[x] = sw.init_t ? src[(size_t)(j + x) * ra + i] : src[(size_t)i * n + j + x];
-                }
-            }
-            s[m][e][0] = make_float2(v[0], v[1]);
-            s[m][e][1] = make_float2(v[2], v[3]);
+        for (int c = 0; c < CPL; ++c) {
+            const int i = i0 + 2 * p, j = j0 + c;
+            // element i of column j: rows apart, or contiguous in a transposed state
+            const float *src = sw.S_init + (sw.init_t ? (bh * n + j) * ra : bh * ra * n + j);
+            const size_t step = sw.init_t ? 1 : n;
+            const bool ok = sw.S_init && j < n;
+            s[p][c] = make_float2(ok && i < ra ? src[i * step] : 0.f, ok && i + 1 < ra ? src[(i + 1) * step] : 0.f);
         }
-
+    // staging: thread e + R x fetches element e of the tokens x, x + CB, .. of a and b; warp w column
+    // `lane` of the tokens w, w + NW, .. of c
     float pa[C::NA], pb[C::NA], pc[C::NC];
+    const int ea = tid % R, xa = tid / R;
+    const bool in_a = ea < ra, in_c = c0 + lane < n;
+    const long long sa = step * ra, sc = step * n;
+    long long oa = (first + xa * step) * ra + ea, oc = (first + warp * step) * n + c0 + lane;   // at token t0
     auto fetch = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < C::NA; ++i) {
-            const int x = i * kRecThreads + tid, t = t0 + x / RP, e = x % RP;
-            const bool ok = t < T && e < ra;
-            const size_t at = ok ? row(t) * ra + e : 0;
-            pa[i] = ok ? load_elem<BF16>(sw.a, at) : 0.f;
-            pb[i] = ok ? load_elem<BF16>(sw.b, at) : 0.f;
+        for (int x = 0; x < C::NA; ++x) {
+            const bool ok = in_a && t0 + x * C::CB + xa < T;
+            pa[x] = ok ? load_elem<BF16>(sw.a, oa + x * C::CB * sa) : 0.f;
+            pb[x] = ok ? load_elem<BF16>(sw.b, oa + x * C::CB * sa) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < C::NC; ++i) {
-            const int x = i * kRecThreads + tid, t = t0 + x / kRecCols, e = c0 + x % kRecCols;
-            const bool ok = t < T && e < n;
-            pc[i] = ok ? load_elem<BF16>(sw.c, row(t) * n + e) * sw.write_scale : 0.f;
+        for (int x = 0; x < C::NC; ++x) {
+            const int t = x * NW + warp;
+            pc[x] = in_c && t < TB && t0 + t < T ? load_elem<BF16>(sw.c, oc + x * NW * sc) * sw.write_scale : 0.f;
         }
+        oa += TB * sa;
     };
     if (T > 0) fetch(0);
     for (int t0 = 0; t0 < T; t0 += TB) {
         const int nt = min(TB, T - t0);
 #pragma unroll
-        for (int i = 0; i < C::NA; ++i) {
-            const int x = i * kRecThreads + tid;
-            as[(x / RP) * RS + x % RP] = pa[i];
-            bs[(x / RP) * RS + x % RP] = pb[i];
-        }
+        for (int x = 0; x < C::NA; ++x) as[x * NT + tid] = pa[x], bs[x * NT + tid] = pb[x];
 #pragma unroll
-        for (int i = 0; i < C::NC; ++i) cs[i * kRecThreads + tid] = pc[i];
+        for (int x = 0; x < C::NC; ++x)
+            if (NW * C::NC == TB || x * NW + warp < TB) cs[x * NT + tid] = pc[x];
         __syncthreads();
+        const long long oy = oc;    // of the outputs too
+        oc += TB * sc;
         if (t0 + TB < T) fetch(t0 + TB);
-        if (active) {
-            for (int t = 0; t < nt; t += 2) {
-                // (the second token of an odd last pair: zeros are staged, and a factor 1 keeps the state)
-                const float2 f0 = splat((t0 + t == 0 && sw.late) ? 1.f : g), f1 = splat(t + 1 < nt ? g : 1.f);
-                float2 y[2][2] = {};
-                const float4 cv0 = *reinterpret_cast<const float4 *>(cs + t * kRecCols + wc);
-                const float4 cv1 = *reinterpret_cast<const float4 *>(cs + (t + 1) * kRecCols + wc);
-                const float2 c00 = make_float2(cv0.x, cv0.y), c01 = make_float2(cv0.z, cv0.w);
-                const float2 c10 = make_float2(cv1.x, cv1.y), c11 = make_float2(cv1.z, cv1.w);
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const int o = 4 * (8 * m + g8);
-                    const float4 a0 = *reinterpret_cast<const float4 *>(as + t * RS + o);
-                    const float4 b0 = *reinterpret_cast<const float4 *>(bs + t * RS + o);
-                    const float4 a1 = *reinterpret_cast<const float4 *>(as + (t + 1) * RS + o);
-                    const float4 b1 = *reinterpret_cast<const float4 *>(bs + (t + 1) * RS + o);
-                    const float aa0[4] = {a0.x, a0.y, a0.z, a0.w}, bb0[4] = {b0.x, b0.y, b0.z, b0.w};
-                    const float aa1[4] = {a1.x, a1.y, a1.z, a1.w}, bb1[4] = {b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 u = __ffma2_rn(f0, s[m][e][0], __fmul2_rn(splat(bb0[e]), c00));
-                        float2 v = __ffma2_rn(f0, s[m][e][1], __fmul2_rn(splat(bb0[e]), c01));
-                        y[0][0] = __ffma2_rn(splat(aa0[e]), u, y[0][0]);
-                        y[0][1] = __ffma2_rn(splat(aa0[e]), v, y[0][1]);
-                        u = __ffma2_rn(f1, u, __fmul2_rn(splat(bb1[e]), c10));
-                        v = __ffma2_rn(f1, v, __fmul2_rn(splat(bb1[e]), c11));
-                        y[1][0] = __ffma2_rn(splat(aa1[e]), u, y[1][0]);
-                        y[1][1] = __ffma2_rn(splat(aa1[e]), v, y[1][1]);
-                        s[m][e][0] = u;
-                        s[m][e][1] = v;
-                    }
-                }
-                // reduce-scatter over the row groups (lane bits 4, 3, 2): token, column pair, column
-                const bool hi4 = lane & 16, hi3 = lane & 8, hi2 = lane & 4;
-                float k0[4] = {hi4 ? y[1][0].x : y[0][0].x, hi4 ? y[1][0].y : y[0][0].y,
-                               hi4 ? y[1][1].x : y[0][1].x, hi4 ? y[1][1].y : y[0][1].y};
-                const float o0[4] = {hi4 ? y[0][0].x : y[1][0].x, hi4 ? y[0][0].y : y[1][0].y,
-                                     hi4 ? y[0][1].x : y[1][1].x, hi4 ? y[0][1].y : y[1][1].y};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) k0[x] += __shfl_xor_sync(0xffffffffu, o0[x], 16);
-                float k1[2] = {hi3 ? k0[2] : k0[0], hi3 ? k0[3] : k0[1]};
-                const float o1[2] = {hi3 ? k0[0] : k0[2], hi3 ? k0[1] : k0[3]};
-#pragma unroll
-                for (int x = 0; x < 2; ++x) k1[x] += __shfl_xor_sync(0xffffffffu, o1[x], 8);
-                const float total = (hi2 ? k1[1] : k1[0]) + __shfl_xor_sync(0xffffffffu, hi2 ? k1[0] : k1[1], 4);
-                ys[t + (hi4 ? 1 : 0)][wc + (hi3 ? 2 : 0) + (hi2 ? 1 : 0)] = total;
+#pragma unroll 2
+        for (int t = 0; t < nt; ++t) {
+            const float2 f = splat(sw.late && t0 + t == 0 ? 1.f : g);
+            const float4 *a4 = reinterpret_cast<const float4 *>(as + t * R + i0), *b4 = reinterpret_cast<const float4 *>(bs + t * R + i0);
+            float2 v[CPL];
+            if constexpr (CPL == 4) {
+                const float4 v4 = *reinterpret_cast<const float4 *>(cs + t * kRecCols + j1);
+                v[0] = splat(v4.x), v[1] = splat(v4.y), v[2] = splat(v4.z), v[3] = splat(v4.w);
+            } else {
+                v[0] = splat(cs[t * kRecCols + j1]);
             }
+            const float4 x0 = a4[0], x1 = a4[1], k0 = b4[0], k1 = b4[1];
+            const float2 x[4] = {lo2(x0), hi2(x0), lo2(x1), hi2(x1)}, k[4] = {lo2(k0), hi2(k0), lo2(k1), hi2(k1)};
+            float2 y[CPL] = {};
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) {
+                    s[p][c] = __ffma2_rn(f, s[p][c], __fmul2_rn(k[p], v[c]));
+                    y[c] = __ffma2_rn(x[p], s[p][c], y[c]);
+                }
+            float *yt = ys + ((4 * wr + part) * TB + t) * kRecCols + j1;
+            if constexpr (CPL == 4)
+                *reinterpret_cast<float4 *>(yt) = make_float4(y[0].x + y[0].y, y[1].x + y[1].y, y[2].x + y[2].y, y[3].x + y[3].y);
+            else
+                *yt = y[0].x + y[0].y;
         }
         __syncthreads();
-        for (int x = tid; x < nt * kRecCols; x += kRecThreads) {
-            const int t = x / kRecCols, e = x % kRecCols;
-            if (c0 + e < n) store_elem<BF16>(sw.out, row(t0 + t) * n + c0 + e, ys[t][e] * sw.out_scale);
+#pragma unroll
+        for (int x = 0; x < C::NC; ++x) {
+            if (x * NW + warp >= nt) break;
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4 * W; ++w) y += ys[w * TB * kRecCols + x * NT + tid];
+            if (in_c) store_elem<BF16>(sw.out, oy + x * NW * sc, y * sw.out_scale);
         }
         // (the next iteration's first barrier orders these reads of ys before its next writes, and
         // this iteration's last one its reads of the staged tokens before they are overwritten)
     }
     if (!sw.S_fin) return;
-    const float2 f = splat(sw.late && T > 0 ? g : 1.f);
-    const bool vec_out = (n & 3) == 0 && (reinterpret_cast<uintptr_t>(sw.S_fin) & 15) == 0;
+    const float f = sw.late && T > 0 ? g : 1.f;
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int p = 0; p < 4; ++p)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 4 * (8 * m + g8) + e, j = c0 + wc;
-            if (i >= ra || j >= n) continue;
-            const float2 u = __fmul2_rn(s[m][e][0], f), v = __fmul2_rn(s[m][e][1], f);
-            float *dst = sw.S_fin + bh * ra * n + (size_t)i * n + j;
-            if (vec_out) {
-                *reinterpret_cast<float4 *>(dst) = make_float4(u.x, u.y, v.x, v.y);
-            } else {
-                const float x[4] = {u.x, u.y, v.x, v.y};
+        for (int e = 0; e < 2; ++e) {
+            const int i = i0 + 2 * p + e;
+            if (i >= ra) continue;
+            float *dst = sw.S_fin + bh * ra * n + (size_t)i * n + j0;
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (j + w < n) dst[w] = x[w];
-            }
+            for (int c = 0; c < CPL; ++c)
+                if (j0 + c < n) dst[c] = (e ? s[p][c].y : s[p][c].x) * f;
         }
 }
 
-template <bool BF16>
-cudaError_t launch_rec(const RecArgs &r, int rp, dim3 grid, cudaStream_t stream)
+template <bool BF16, int W, int CPL>
+cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
 {
-    if (rp <= 32) decay_rec_kernel<BF16, 32><<<grid, kRecThreads, 0, stream>>>(r);
-    else if (rp <= 64) decay_rec_kernel<BF16, 64><<<grid, kRecThreads, 0, stream>>>(r);
-    else if (rp <= 128) decay_rec_kernel<BF16, 128><<<grid, kRecThreads, 0, stream>>>(r);
-    else decay_rec_kernel<BF16, 256><<<grid, kRecThreads, 0, stream>>>(r);
+    using C = RecCfg<W, CPL>;
+    static OncePerDevice once;
+    const cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL>, C::kSmem, once);
+    if (e != cudaSuccess) return e;
+    decay_rec_kernel<BF16, W, CPL><<<grid, C::kThreads, C::kSmem, stream>>>(r);
     return cudaGetLastError();
+}
+
+template <bool BF16, int CPL>
+cudaError_t launch_rec(const RecArgs &r, int rows, dim3 grid, cudaStream_t stream)
+{
+    if (rows <= 32) return launch_rec_w<BF16, 1, CPL>(r, grid, stream);
+    if (rows <= 64) return launch_rec_w<BF16, 2, CPL>(r, grid, stream);
+    if (rows <= 128) return launch_rec_w<BF16, 4, CPL>(r, grid, stream);
+    return launch_rec_w<BF16, 8, CPL>(r, grid, stream);
 }
 
 // ------------------------------------------------------------ decode step
@@ -344,7 +325,9 @@ cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArg
         rows = sweeps[i].ra > rows ? sweeps[i].ra : rows;
     }
     const dim3 grid(tiles, a.H, B);
-    return bf16 ? launch_rec<true>(r, rows, grid, stream) : launch_rec<false>(r, rows, grid, stream);
+    const bool wide = (long long)tiles * a.H * B > kRecFew;
+    if (bf16) return wide ? launch_rec<true, 4>(r, rows, grid, stream) : launch_rec<true, 1>(r, rows, grid, stream);
+    return wide ? launch_rec<false, 4>(r, rows, grid, stream) : launch_rec<false, 1>(r, rows, grid, stream);
 }
 
 cudaError_t launch_decay_decode(const void *q, const void *k, const void *v, bool bf16, const float *decay, float *S,
