@@ -33,6 +33,7 @@ struct SelSmem {
     unsigned long long keys[kSelWarps][kSelBuf];          // each warp's candidates; at the end its K best, best first (0: none)
     float m[kSelWarps], s[kSelWarps];                     // running maximum and sum of its part
     int count[kSelWarps];                                 // keys in its buffer
+    unsigned long long bound[kMaxBeams];                  // a K-th key of some part of a row, which all its warps share
     // CTA 0 only: the rows' best and their lse
     unsigned long long row_keys[kMaxBeams][kMaxBeams];
     double row_lse[kMaxBeams];
@@ -134,7 +135,8 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-template <bool BF16>
+// ALIGNED: every row starts on a 16-byte boundary.
+template <bool BF16, bool ALIGNED>
 __global__ void __launch_bounds__(kSelThreads, 2)
 beam_select_kernel(const BeamSelectArgs args)
 {
@@ -146,14 +148,23 @@ beam_select_kernel(const BeamSelectArgs args)
     const int b = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nw = kSelWarps * cs;
+    if (threadIdx.x < kMaxBeams) sm.bound[threadIdx.x] = 0;
+    // what phase 3 needs, in flight from the start
+    const bool picks = rank == 0 && warp == 0 && lane < K;
+    const size_t bk = (size_t)b * K;
+    const float score_f = picks ? args.scores[bk + lane] : 0.f;
+    const bool ended = picks && args.done && args.done[bk + lane];
+    __syncthreads();
     {
         // phase 1: this warp's part of one row
         const int gw = rank * kSelWarps + warp;
-        const int k = gw % K, part = gw / K, parts = (nw - k + K - 1) / K;
-        const bool skip = args.done && args.done[(size_t)b * K + k];
+        // (every row has the same number of parts, so that equal rows have equal sums to the last bit and tie;
+        // warps left over are idle)
+        const int k = gw % K, part = gw / K, parts = nw / K;
+        const bool skip = part >= parts || (args.done && args.done[(size_t)b * K + k]);
         const unsigned char *row = reinterpret_cast<const unsigned char *>(args.logits) +
                                    ((long long)b * K + k) * args.row_stride * (BF16 ? 2 : 4);
-        const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+        const int mis = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
         const unsigned char *p0 = row - mis;
         const long long row_bytes = (long long)V * (BF16 ? 2 : 4);
         const int granules = (V + GE - 1) / GE;
@@ -166,29 +177,36 @@ beam_select_kernel(const BeamSelectArgs args)
         // keeps the K best of the buffer, sorted
         auto keep_best = [&]() {
             __syncwarp();
-            unsigned long long k4[kSelBuf / 32], mine = 0;
-#pragma unroll
-            for (int i = 0; i < kSelBuf / 32; ++i) k4[i] = lane + 32 * i < count ? buf[lane + 32 * i] : 0;
+            unsigned long long k0 = lane < count ? buf[lane] : 0, mine = 0;
+            if (count <= 32) {
 #pragma unroll 1
-            for (int r = 0; r < K; ++r) {
-                unsigned long long best = k4[0];
-#pragma unroll
-                for (int i = 1; i < kSelBuf / 32; ++i) best = k4[i] > best ? k4[i] : best;
-                best = warp_max(best);
-                if (lane == r) mine = best;
-#pragma unroll
-                for (int i = 0; i < kSelBuf / 32; ++i)
-                    if (k4[i] == best) k4[i] = 0;
+                for (int r = 0; r < K; ++r) {
+                    const unsigned long long best = warp_max(k0);
+                    if (lane == r) mine = best;
+                    if (k0 == best) k0 = 0;
+                }
+            } else {
+                unsigned long long k1 = lane + 32 < count ? buf[lane + 32] : 0, k2 = lane + 64 < count ? buf[lane + 64] : 0,
+                                   k3 = lane + 96 < count ? buf[lane + 96] : 0;
+#pragma unroll 1
+                for (int r = 0; r < K; ++r) {
+                    const unsigned long long a = k0 > k1 ? k0 : k1, c = k2 > k3 ? k2 : k3;
+                    const unsigned long long best = warp_max(a > c ? a : c);
+                    if (lane == r) mine = best;
+                    if (k0 == best) k0 = 0;
+                    if (k1 == best) k1 = 0;
+                    if (k2 == best) k2 = 0;
+                    if (k3 == best) k3 = 0;
+                }
             }
             if (lane < K) buf[lane] = mine;
-            __syncwarp();
             if (count >= K) {
                 thr = __shfl_sync(0xffffffffu, mine, K - 1);
                 thr_x = key_value(thr);
                 count = K;
-                if (lane == 0) sm.count[warp] = K;
-                __syncwarp();
+                if (lane == 0) sm.count[warp] = K, atomicMax(&sm.bound[k], thr);
             }
+            __syncwarp();
         };
         // takes a granule into the running maximum and sum; returns its maximum
         auto sum_up = [&](uint4 raw, int i0) -> float {
@@ -228,7 +246,9 @@ beam_select_kernel(const BeamSelectArgs args)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     raw[u] = make_uint4(0, 0, 0, 0);
-                    if (g + u * step < granules) raw[u] = load_granule(p0, mis, g + u * step, row_bytes);
+                    if (g + u * step < granules)
+                        raw[u] = ALIGNED ? ld_once(reinterpret_cast<const uint4 *>(p0) + (g + u * step))
+                                         : load_granule(p0, mis, g + u * step, row_bytes);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -236,6 +256,8 @@ beam_select_kernel(const BeamSelectArgs args)
                     if (g + u * step < granules) mx[u] = sum_up(raw[u], (g + u * step) * GE);
                     top = fmaxf(top, mx[u]);
                 }
+                const unsigned long long shared_thr = *reinterpret_cast<volatile unsigned long long *>(&sm.bound[k]);
+                if (shared_thr > thr) thr = shared_thr, thr_x = key_value(thr);
                 if (!__any_sync(0xffffffffu, top >= thr_x && top > -INFINITY)) continue;
                 if (!seeded) {
                     // K lanes have a maximum of at least this
@@ -251,8 +273,13 @@ beam_select_kernel(const BeamSelectArgs args)
                     }
                     seeded = true;
                 }
+                uint32_t todo = 0;      // granules with a candidate in some lane
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    todo |= (__any_sync(0xffffffffu, mx[u] >= thr_x && mx[u] > -INFINITY) ? 1u : 0u) << u;
 #pragma unroll 1
-                for (int u = 0; u < U; ++u) {
+                for (; todo; todo &= todo - 1) {
+                    const int u = __ffs(todo) - 1;
                     float mu = mx[0];
                     uint4 ru = raw[0];
 #pragma unroll
@@ -310,7 +337,7 @@ beam_select_kernel(const BeamSelectArgs args)
     cluster_sync_all();
     // phase 2: merge a row's parts (rows over CTAs first, then over warps)
     for (int k = rank + cs * warp; k < K; k += cs * kSelWarps) {
-        const int parts = (nw - k + K - 1) / K;
+        const int parts = nw / K;
         SelSmem *home = in_cta(&sm, 0);
         // lse from the parts' maxima and sums
         float mx = -3.402823466e38f;
@@ -329,37 +356,31 @@ beam_select_kernel(const BeamSelectArgs args)
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) home->row_lse[k] = (double)mx + log(sum);
-        // each lane looks after the sorted lists of parts lane, lane + 32, ..: K rounds of
-        // taking the largest head
-        unsigned long long head[4];
-        int pos[4];
+        // the parts' keys, at most 16 CS + K of them, and K rounds of taking the largest
+        constexpr int N = (kSelWarps * 8 + kMaxBeams) / 32;
+        unsigned long long k5[N];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = lane + 32 * u, gw = k + i * K;
-            pos[u] = 0;
-            head[u] = i < parts ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][0] : 0;
+        for (int u = 0; u < N; ++u) {
+            const int i = lane + 32 * u, gw = k + i / K * K;
+            k5[u] = i < parts * K ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][i % K] : 0;
         }
+#pragma unroll 1
         for (int r = 0; r < K; ++r) {
-            unsigned long long best = head[0];
+            unsigned long long best = k5[0];
 #pragma unroll
-            for (int u = 1; u < 4; ++u) best = head[u] > best ? head[u] : best;
+            for (int u = 1; u < N; ++u) best = k5[u] > best ? k5[u] : best;
             best = warp_max(best);
-            if (lane == 0) home->row_keys[k][r] = best;
+            if (lane == r) home->row_keys[k][r] = best;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (best && head[u] == best) {   // (keys differ: one list holds it)
-                    const int gw = k + (lane + 32 * u) * K;
-                    head[u] = ++pos[u] < K ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][pos[u]] : 0;
-                }
+            for (int u = 0; u < N; ++u)
+                if (k5[u] == best) k5[u] = 0;
         }
     }
     cluster_sync_all();
     if (rank != 0 || warp != 0) return;
     // phase 3: lane k holds the head of row k; K rounds of taking the best score
     const int k = lane;
-    const size_t bk = (size_t)b * K;
-    const double score = k < K ? (double)args.scores[bk + k] : 0.0;
-    const bool ended = k < K && args.done && args.done[bk + k];
+    const double score = score_f;
     const double lse = k < K ? sm.row_lse[k] : 0.0;
     const bool usable = k < K && isfinite(score) && (ended || isfinite(lse));
     int pos = 0;
@@ -475,8 +496,13 @@ cudaError_t launch_beam_select(const BeamSelectArgs &a, int B, bool bf16, int sm
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, beam_select_kernel<true>, a)
-                : cudaLaunchKernelEx(&cfg, beam_select_kernel<false>, a);
+    const int el = bf16 ? 2 : 4;
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.row_stride * el % 16 == 0;
+    if (bf16)
+        return aligned ? cudaLaunchKernelEx(&cfg, beam_select_kernel<true, true>, a)
+                       : cudaLaunchKernelEx(&cfg, beam_select_kernel<true, false>, a);
+    return aligned ? cudaLaunchKernelEx(&cfg, beam_select_kernel<false, true>, a)
+                   : cudaLaunchKernelEx(&cfg, beam_select_kernel<false, false>, a);
 }
 
 cudaError_t launch_state_reorder(const float *S, const float *z, const int *parents, int B, int K, long long s_len,
