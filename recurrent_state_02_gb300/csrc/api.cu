@@ -834,8 +834,50 @@ bool tc_sweep(const la::DecaySweep &s, bool bf16)
     return true;
 }
 
-// Runs the sweeps of one call, each on the kernel that takes it.
-la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a, bool bf16, int B, cudaStream_t st)
+// How a sweep of T tokens over `units` CTAs (heads x 64-column tiles) is split: into nseg segments that run at
+// once, when all of them and all parts of the state pass fit the SMs, one CTA each.  Estimated times in
+// microseconds: a chunk costs 1.6 in the sweep and 0.8 in the state pass, a launch about 5 to 7 around them, and a
+// segment reads the parts before it at 0.5 each.  (B1 H32 T65536 755 us whole, 529 split; B1 H8 r = dv = 128: T = 4096
+// 57 and 31, T = 1024 18 whole, 24 in four segments.)
+struct DecaySplit {
+    int nseg = 1, seg_chunks = 0, part_chunks = 0, nparts = 0;
+};
+DecaySplit decay_split(long long units, int T)
+{
+    DecaySplit best;
+    const int sms = sm_count(), nch = (T + 127) / 128;
+    if (units < 1 || units * 2 > sms) return best;
+    double best_us = 5 + 1.6 * nch;
+    for (int g = 2; g * units <= sms && g <= nch; ++g)
+        for (int sub = 1; units * (g - 1) * sub <= sms; ++sub) {
+            const int pc = ((nch + g - 1) / g + sub - 1) / sub, len = pc * sub, n = (nch + len - 1) / len;
+            if (n < 2) continue;
+            const double us = 12 + 1.6 * len + 0.8 * pc + 0.5 * (n - 1) * sub;
+            if (us < best_us) {
+                best_us = us;
+                best.nseg = n, best.seg_chunks = len, best.part_chunks = pc, best.nparts = (n - 1) * sub;
+            }
+        }
+    return best;
+}
+
+// Bytes of the parts of the sweeps of r keys that a call makes (tiles: their 64-column tiles together).
+size_t split_bytes(long long heads, int tiles, int T, int ra)
+{
+    const DecaySplit d = decay_split(heads * tiles, T);
+    return d.nseg > 1 ? sizeof(float) * (size_t)heads * tiles * (d.nparts + 1) * ra * 64 : 0;
+}
+
+bool tc_sizes(la_dtype dtype, int B, int H, int T, int r, int dv)
+{
+    return dtype == LA_DTYPE_BF16 && B >= 1 && H >= 1 && B <= 65535 && H <= 65535 && T > kDecayWalk && r >= 1 && dv >= 1 &&
+           r <= 256 && dv <= 256;
+}
+
+// Runs the sweeps of one call, each on the kernel that takes it; parts: workspace of the split sweeps (sweeps
+// that it does not hold are not split: fewer may be eligible than the query counted, by their alignment).
+la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a, bool bf16, int B, cudaStream_t st,
+                     void *workspace = nullptr, size_t workspace_bytes = 0)
 {
     const bool packed = a.cu_seqlens != nullptr;
     la::DecaySweep rest[3];
@@ -872,6 +914,16 @@ la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a
             p.tiles[m++] = s.n / 64;
         }
         if (!m) continue;
+        const long long heads = (long long)B * a.H;
+        const int tiles = p.tiles[0] + p.tiles[1] + p.tiles[2];
+        const size_t bytes = packed ? 0 : split_bytes(heads, tiles, a.T, ra);
+        if (bytes && bytes <= workspace_bytes) {
+            const DecaySplit d = decay_split(heads * tiles, a.T);
+            p.nseg = d.nseg, p.seg_chunks = d.seg_chunks, p.part_chunks = d.part_chunks, p.nparts = d.nparts;
+            p.parts = static_cast<float *>(workspace);
+            workspace = static_cast<char *>(workspace) + bytes;
+            workspace_bytes -= bytes;
+        }
         const cudaError_t e = la::launch_decay_tc(p, ra, st);
         if (e != cudaSuccess) return from_cuda(e);
     }
@@ -880,7 +932,11 @@ la_status run_sweeps(const la::DecaySweep *sw, int count, const la::DecayArgs &a
 
 }  // namespace
 
-size_t la_decay_prefill_workspace_bytes(int, int, int, int, int, la_dtype) { return 0; }
+size_t la_decay_prefill_workspace_bytes(int B, int H, int T, int r, int dv, la_dtype dtype)
+{
+    if (!tc_sizes(dtype, B, H, T, r, dv) || (r != 64 && r != 128) || dv % 64 != 0) return 0;
+    return split_bytes((long long)B * H, dv / 64, T, r);
+}
 
 la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
                            const float *S0, int B, int H, int T, int r, int dv, float scale, void *y, float *S_out,
@@ -905,7 +961,7 @@ la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype
     a.status = status_word();
     if (!a.status) return LA_ERR_CUDA;
     const la::DecaySweep sw = forward_sweep(q, k, v, S0, r, dv, scale, y, S_out);
-    return run_sweeps(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st);
+    return run_sweeps(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st, workspace, need);
 }
 
 la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
@@ -950,7 +1006,17 @@ la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_d
     return from_cuda(la::launch_decay_rec(&sw, 1, a, dtype == LA_DTYPE_BF16, B, st));
 }
 
-size_t la_decay_backward_workspace_bytes(int, int, int, int, int, la_dtype) { return 0; }
+size_t la_decay_backward_workspace_bytes(int B, int H, int T, int r, int dv, la_dtype dtype)
+{
+    if (!tc_sizes(dtype, B, H, T, r, dv)) return 0;
+    // the sweeps by their key width: dq and dk have dv keys and r columns, dv the reverse
+    size_t bytes = 0;
+    for (int ra = 64; ra <= 128; ra += 64) {
+        const int tiles = (dv == ra && r % 64 == 0 ? 2 * (r / 64) : 0) + (r == ra && dv % 64 == 0 ? dv / 64 : 0);
+        if (tiles) bytes += split_bytes((long long)B * H, tiles, T, ra);
+    }
+    return bytes;
+}
 
 la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
                             const float *S0, int B, int H, int T, int r, int dv, float scale, const void *dy,
@@ -990,7 +1056,7 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
         sw[i].rev = sw[i].late = true;
         sw[i].write_scale = scale;
     }
-    return run_sweeps(sw, 3, a, dtype == LA_DTYPE_BF16, B, st);
+    return run_sweeps(sw, 3, a, dtype == LA_DTYPE_BF16, B, st, workspace, need);
 }
 
 la_status la_beam_select(const void *logits, la_dtype dtype, long long row_stride, const float *scores,

@@ -54,7 +54,11 @@ struct DecayTcParams {
     int tiles[3] = {};     // 64-column tiles of each sweep
     DecayArgs d;
     int B = 0;
-    unsigned long long wait_limit_ns = kWaitLimitNs;
+    // The split of [B,H,T,d] sweeps (decay_split): nseg segments of seg_chunks chunks; the first nseg - 1
+    // are parts of part_chunks chunks (nparts of them), whose sums the state pass leaves in
+    // parts [B*H][tiles][nparts + 1][ra][64] (the last one: the state that enters the sweep).
+    int nseg = 1, seg_chunks = 0, part_chunks = 0, nparts = 0;
+    float *parts = nullptr;
 };
 cudaError_t launch_decay_tc(const DecayTcParams &p, int ra, cudaStream_t stream);
 

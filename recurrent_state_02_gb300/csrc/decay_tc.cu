@@ -24,7 +24,10 @@
 // exponents >= 0; a diagonal block looks its powers up.  So every g in 0 .. 1 (0 too)
 // takes the same path, and what underflows is negligible next to the diagonal.
 //
-// One CTA owns one (b, h, 64 columns of c) and walks its chunks.  Four warpgroups (each of a
+// One CTA owns one (b, h, 64 columns of c) and walks its chunks, or, where that leaves most SMs idle, one
+// segment of them: a state pass then forms what every part of the sweep adds to the state ("门控递推为什么能做并行 scan？"
+// of "Linear attention：把历史写进状态": updates compose as affine maps, and with a constant decay the map
+// of a part is g^tokens and that sum), and a later segment starts from the parts before it.  Four warpgroups (each of a
 // group's warps reaches the TMEM lanes of its quadrant): TMA producer and three MMA
 // issuers (scores, dS, outputs, so that none waits for another's operands); scores; weighted values and
 // outputs; state.
@@ -62,6 +65,7 @@ struct alignas(16) SmallD {
     uint32_t tmem_base;
     int abort_flag;
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
+    float gpart;                       // g^(tokens of a part)
 };
 
 // shared-memory address of a barrier (in the kernel: sS is the SmallD's)
@@ -194,7 +198,9 @@ __device__ __forceinline__ void tc_st_x16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // PACKED: packed sequences (forwards); REV: the launch has backward sweeps (of [B,H,T,d] arrays).
-template <int KD, bool PACKED, bool REV>
+// STATE: the state pass of a split sweep: what each part of it adds to the state, from zero; only b and
+// c are read, only dS is formed.
+template <int KD, bool PACKED, bool REV, bool STATE>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_kernel(const __grid_constant__ DecayTcParams args)
 {
@@ -216,7 +222,8 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     const bool rev = REV && sw.rev;
 
     // this CTA's sequence
-    int b = blockIdx.z, T = args.d.T, seq0 = 0;
+    const int B = args.B, z = blockIdx.z / B;      // z: the segment, or part, of the sweep
+    int b = blockIdx.z % B, T = args.d.T, seq0 = 0;
     if (packed) {
         seq0 = args.d.cu_seqlens[b];
         const int seq1 = args.d.cu_seqlens[b + 1];
@@ -226,9 +233,11 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         if (T < args.d.len_min || T > args.d.len_max) return;
     }
     const size_t bh = (size_t)b * H + h;
-    const int nch = (T + kCT - 1) / kCT;
-    // chunk of the sweep's step c, its first token and its tokens
-    auto chunk_t0 = [&](int c) { return (rev ? nch - 1 - c : c) * kCT; };
+    // the chunks of the sweep, and the run of them that is this CTA's: all, a segment or a part
+    const int all = (T + kCT - 1) / kCT, run = STATE ? args.part_chunks : args.seg_chunks;
+    const int cb = packed ? 0 : z * run, nch = packed || run == 0 ? all : min(run, all - cb);
+    // chunk of this CTA's step c, its first token and its tokens
+    auto chunk_t0 = [&](int c) { return (rev ? all - 1 - cb - c : cb + c) * kCT; };
     auto chunk_n = [&](int c) { return min(kCT, T - chunk_t0(c)); };
 
     // ------------------------------------------------------------ set-up
@@ -237,7 +246,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             mbar_init(&sm->fullA[s], 1);
             mbar_init(&sm->fullB[s], 1);
             mbar_init(&sm->emptyA[s], 2);      // read by the scores and by Ye
-            mbar_init(&sm->emptyB[s], 2);      // read by the scores and by dS
+            mbar_init(&sm->emptyB[s], STATE ? 1 : 2);      // read by the scores and by dS
             mbar_init(&sm->p_raw[s], 1);
             mbar_init(&sm->p_ready[s], 4);
             mbar_init(&sm->p_free[s], 1);
@@ -275,6 +284,14 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             q *= q;
         }
         sm->pw[e] = (float)p;
+        if (e == 0 && !STATE) {
+            // what a part of a split sweep decays an entering state by (all are full but the first of a
+            // backward sweep, which nothing enters)
+            double r = 1.0, x = (double)args.d.decay[h];
+            for (long long n = z > 1 || args.nparts > 1 ? (long long)args.part_chunks * kCT : 0; n; n >>= 1, x *= x)
+                if (n & 1) r *= x;
+            sm->gpart = (float)r;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -300,6 +317,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 const int s = c & 1, t0 = chunk_t0(c), t2 = chunk_t0(c + 2);
 #pragma unroll 1
                 for (int i = 0; i <= 2 * L::NB; ++i) {
+                    if (STATE && i >= L::NB && i < 2 * L::NB) continue;
                     const bool is_c = i == 2 * L::NB, is_a = i >= L::NB;
                     const int k = is_c ? 0 : is_a ? i - L::NB : i, x = is_c ? c0 : 64 * k;
                     const uint32_t full = is_c ? BAR(fullC, c % kStC) : is_a ? BAR(fullA, s) : BAR(fullB, s);
@@ -319,10 +337,11 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             // every issued load lands before the CTA may exit (the last six, in order)
             for (int i = max(0, loaded - 9); i < loaded; ++i) {
                 const int c = i / 3, k = i % 3;
+                if (STATE && k == 1) continue;
                 if (k == 2) wait1(BAR(fullC, c % kStC), (c / kStC) & 1);
                 else if (3 * (c + 2) + k >= loaded) wait1(k ? BAR(fullA, c & 1) : BAR(fullB, c & 1), (c >> 1) & 1);
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (!STATE && warp == 1 && lane == 0) {
             // ------------------------------------------------- MMA: scores
             constexpr uint32_t idP = idesc_bf16_f32(128, 128, false, false);
             for (int c = 0; c < nch; ++c) {
@@ -364,7 +383,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 bar_commit(BAR(w_empty, 0));
                 bar_commit(BAR(emptyB, s));
             }
-        } else if (warp == 3 && lane == 0) {
+        } else if (!STATE && warp == 3 && lane == 0) {
             // ------------------------------------------------ MMA: outputs
             constexpr uint32_t idY = idesc_bf16_f32(128, 64, false, true);
             for (int c = 0; c < nch; ++c) {
@@ -412,7 +431,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             (j & 1 ? wc[j / 2].y : wc[j / 2].x) = power(rev ? j : 31 - j);
         }
         const int J0 = rev ? R : 0, J1 = rev ? 3 : R;     // the 32-column blocks that the mask leaves
-        for (int c = 0; c < nch; ++c) {
+        for (int c = 0; !STATE && c < nch; ++c) {
             const int s = c & 1;
             if (!waitw(BAR(p_raw, s), (c >> 1) & 1)) break;
             tc_fence_after();
@@ -499,6 +518,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             }
             fence_proxy_async_smem();
             bar_arrive_warp(BAR(w_full, 0));
+            if (STATE) bar_arrive_warp(BAR(emptyC, s));
         }
     } else {
         // ---------------------------------------------- state and outputs
@@ -507,13 +527,37 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         float2 S[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
-        if (sw.S_init) {
+        // the state that enters: S_init for a whole sweep and for the first part of a split one; a segment
+        // takes what the parts before it leave, the first one the copy of S_init that the first part makes (S_fin
+        // may lie over S_init, and the last segment may end before the first one begins)
+        const size_t slots = args.nparts + 1;
+        float *const parts = args.parts + ((bh * gridDim.x + blockIdx.x) * slots * KD + (row & (KD - 1))) * 64;
+        if (sw.S_init && (STATE ? z == 0 : args.nseg == 1)) {
             // element j of the row: contiguous, or a row of the transposed state apart
             const int i = row & (KD - 1);
             const float *src = sw.init_t ? sw.S_init + (bh * n_all + c0) * KD + i : sw.S_init + (bh * KD + i) * n_all + c0;
             const size_t step = sw.init_t ? KD : 1;
 #pragma unroll
             for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * step], src[(2 * j + 1) * step]);
+        }
+        if (STATE && z == 0 && mine) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                reinterpret_cast<float4 *>(parts + (size_t)args.nparts * KD * 64)[j] = make_float4(S[2 * j].x, S[2 * j].y, S[2 * j + 1].x, S[2 * j + 1].y);
+        }
+        if (!STATE && args.nseg > 1) {
+            const int first = z ? 0 : args.nparts, end = z ? z * (args.seg_chunks / args.part_chunks) : first + 1;
+            const float2 g2 = make_float2(sm->gpart, sm->gpart);
+#pragma unroll 1
+            for (int q = first; q < end; ++q) {
+                const float4 *src = reinterpret_cast<const float4 *>(parts + (size_t)q * KD * 64);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float4 d = src[j];
+                    S[2 * j] = __ffma2_rn(g2, S[2 * j], make_float2(d.x, d.y));
+                    S[2 * j + 1] = __ffma2_rn(g2, S[2 * j + 1], make_float2(d.z, d.w));
+                }
+            }
         }
         auto publish = [&]() {
             const uint32_t tS = s0 + L::kOffS;
@@ -531,7 +575,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         bool ok = true;
         for (int c = 0; c <= nch; ++c) {
             float ye[64];
-            if (c >= 1) {
+            if (!STATE && c >= 1) {
                 // Ye of chunk c - 1 moves to registers, which frees its accumulator and the state's tile
                 ok = waitw(BAR(ye_full, 0), (c - 1) & 1);
                 if (!ok) break;
@@ -543,8 +587,8 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                 wait_loaded(y1);
                 tc_fence_before();
             }
-            if (c < nch) publish();
-            if (c >= 1) {
+            if (!STATE && c < nch) publish();
+            if (!STATE && c >= 1) {
                 // the outputs of chunk c - 1
                 const int n = chunk_n(c - 1), t0 = chunk_t0(c - 1);
                 const int e = rev ? n - 1 - row : row + 1;
@@ -616,7 +660,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                                                               make_float2(hi[2 * j], hi[2 * j + 1])));
                 }
             }
-            if (c >= 1) {
+            if (!STATE && c >= 1) {
                 // the rows that left through chunk c - 1's tile have been read: the tile may be filled again
                 if (lane == 0) tma_store_wait_read<0>();
                 bar_arrive_warp(BAR(emptyC, (c - 1) % kStC));
@@ -624,8 +668,9 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         }
         if (lane == 0) tma_store_wait_all<0>();
         __syncwarp();
-        if (ok && mine && sw.S_fin) {
-            float *dst = sw.S_fin + (bh * KD + row) * n_all + c0;
+        const bool last = cb + nch == all;
+        if (ok && mine && (STATE || (sw.S_fin && last))) {
+            float *dst = STATE ? parts + (size_t)z * KD * 64 : sw.S_fin + (bh * KD + row) * n_all + c0;
             if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
@@ -644,15 +689,23 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int KD, bool PACKED, bool REV>
+template <int KD, bool PACKED, bool REV, bool STATE>
 cudaError_t launch(const DecayTcParams &p, cudaStream_t stream)
 {
     static OncePerDevice once;
-    const cudaError_t e = set_smem_once(decay_tc_kernel<KD, PACKED, REV>, smem_bytes<KD>(), once);
+    const cudaError_t e = set_smem_once(decay_tc_kernel<KD, PACKED, REV, STATE>, smem_bytes<KD>(), once);
     if (e != cudaSuccess) return e;
-    const dim3 grid(p.tiles[0] + p.tiles[1] + p.tiles[2], p.d.H, p.B);
-    decay_tc_kernel<KD, PACKED, REV><<<grid, kThreads, smem_bytes<KD>(), stream>>>(p);
+    const dim3 grid(p.tiles[0] + p.tiles[1] + p.tiles[2], p.d.H, p.B * (STATE ? p.nparts : p.nseg));
+    decay_tc_kernel<KD, PACKED, REV, STATE><<<grid, kThreads, smem_bytes<KD>(), stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int KD, bool REV>
+cudaError_t launch_dense(const DecayTcParams &p, cudaStream_t stream)
+{
+    if (p.nseg > 1)
+        if (const cudaError_t e = launch<KD, false, REV, true>(p, stream)) return e;
+    return launch<KD, false, REV, false>(p, stream);
 }
 
 template <int KD>
@@ -660,8 +713,8 @@ cudaError_t launch(const DecayTcParams &p, cudaStream_t stream)
 {
     bool rev = false;
     for (int i = 0; i < 3; ++i) rev = rev || (p.tiles[i] && p.sw[i].rev);
-    if (p.d.cu_seqlens) return launch<KD, true, false>(p, stream);
-    return rev ? launch<KD, false, true>(p, stream) : launch<KD, false, false>(p, stream);
+    if (p.d.cu_seqlens) return launch<KD, true, false, false>(p, stream);
+    return rev ? launch_dense<KD, true>(p, stream) : launch_dense<KD, false>(p, stream);
 }
 
 }  // namespace

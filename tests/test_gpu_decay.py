@@ -109,6 +109,34 @@ def test_prefill_continues(la, split):
     R.check(y2, ref_y[:, :, split:], 2 * R.bounds(300, 128, 128, True, abs_y, ref_y, True)[:, :, split:], "y")
 
 
+@pytest.mark.parametrize("size", [(1, 2, 2000, 128, 128), (1, 3, 1500, 64, 64), (2, 8, 1921, 128, 64), (1, 1, 5000, 64, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_split_sweeps(la, size):
+    """Few heads and a long sequence: the sweep runs in segments (also over its own state, and with a workspace of the
+    caller's), and so do the three sweeps of the gradients."""
+    B, H, T, r, dv = size
+    assert la.decay_prefill_workspace_bytes(*size) > 0
+    q, k, v, dy, decay, S0, dS_T = make(*size, torch.bfloat16, True, seed=sum(size))
+    scale = r ** -0.5
+    ref_y, ref_S = R.prefill(q, k, v, decay, S0, scale)
+    abs_y, abs_S = R.prefill(*R.absolute(q, k, v), decay, *R.absolute(S0), scale)
+    ws = torch.full((la.decay_prefill_workspace_bytes(*size),), 255, dtype=torch.uint8, device="cuda")
+    S = S0.clone()
+    y, _ = la.decay_prefill(q, k, v, decay, S0=S, scale=scale, S_out=S, workspace=ws)
+    assert la.last_device_status() == 0
+    R.check(S, ref_S, R.state_bound(T, abs_S, True), "S")
+    R.check(y, ref_y, R.bounds(T, r, dv, True, abs_y, ref_y, True), "y")
+    with pytest.raises(la.LinAttnError):
+        la.decay_prefill(q, k, v, decay, S0=S0, workspace=ws[:-1])
+    got = la.decay_backward(q, k, v, dy, decay, S0=S0, dS_T=dS_T, scale=scale)
+    assert la.last_device_status() == 0
+    ref = R.backward(q, k, v, dy, decay, S0, dS_T, scale)
+    mag = R.backward(*R.absolute(q, k, v, dy), decay, *R.absolute(S0, dS_T), scale)
+    for x, z, m, name in zip(got[:3], ref[:3], mag[:3], ("dq", "dk", "dv")):
+        R.check(x, z, R.bounds(T, r, dv, True, m, z, True), name)
+    R.check(got[3], ref[3], R.state_bound(T, mag[3], True), "dS0")
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("r,dv", [(128, 128), (64, 128), (40, 24)])
 def test_packed(la, r, dv, dtype):
