@@ -46,6 +46,9 @@ constexpr int kRegsIssue = 56, kRegsValues = 120, kRegsState = 208;
 constexpr uint32_t kBlk = kCT * 128;           // 16 KB: 128 rows x 64 BF16 columns, 128-byte swizzle
 constexpr int kStC = 3;                        // stages of c (a and b have two)
 
+// Packed batches of at most this many sequences run the longest first.
+constexpr int kOrdered = 256;
+
 // TMEM columns
 constexpr uint32_t kColP = 0, kColYi = 256, kColYe = 320, kColDS = 384;
 
@@ -66,6 +69,8 @@ struct alignas(16) SmallD {
     int abort_flag;
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
     float gpart;                       // g^(tokens of a part)
+    int seq[3];                        // packed: this CTA's sequence and its bounds
+    int len[kOrdered];                 // and the lengths of all
 };
 
 // shared-memory address of a barrier (in the kernel: sS is the SmallD's)
@@ -225,8 +230,33 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     const int B = args.B, z = blockIdx.z / B;      // z: the segment, or part, of the sweep
     int b = blockIdx.z % B, T = args.d.T, seq0 = 0;
     if (packed) {
-        seq0 = args.d.cu_seqlens[b];
-        const int seq1 = args.d.cu_seqlens[b + 1];
+        int seq1 = 0;
+        if (B <= kOrdered) {
+            // CTA row z takes the sequence with z longer ones (equal ones in order), so that no long one starts last.
+            // H = 16: a prompt of 16384 tokens behind 47 of 512, 323 us in the batch's own order, 215 so;
+            // 48 prompts of 128 .. 8192 tokens, 343 and 350.
+            int start = 0;
+            if (tid < B) {
+                start = args.d.cu_seqlens[tid];
+                sm->len[tid] = args.d.cu_seqlens[tid + 1] - start;
+            }
+            __syncthreads();
+            if (tid < B) {
+                const int mine = sm->len[tid];
+                int rank = 0;
+#pragma unroll 8
+                for (int i = 0; i < B; ++i) {
+                    const int other = sm->len[i];
+                    rank += other > mine || (other == mine && i < tid);
+                }
+                if (rank == b) sm->seq[0] = tid, sm->seq[1] = start, sm->seq[2] = start + mine;
+            }
+            __syncthreads();
+            b = sm->seq[0], seq0 = sm->seq[1], seq1 = sm->seq[2];
+        } else {
+            seq0 = args.d.cu_seqlens[b];
+            seq1 = args.d.cu_seqlens[b + 1];
+        }
         // (bad bounds are recorded by the token kernel's launch, which looks at every sequence)
         if (seq0 < 0 || seq1 < seq0 || seq1 > args.d.T) return;
         T = seq1 - seq0;
@@ -239,6 +269,35 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     // chunk of this CTA's step c, its first token and its tokens
     auto chunk_t0 = [&](int c) { return (rev ? all - 1 - cb - c : cb + c) * kCT; };
     auto chunk_n = [&](int c) { return min(kCT, T - chunk_t0(c)); };
+
+    // Loads of a chunk, by thread 0: its boxes in the order in which their buffers come free: b and a of
+    // chunk c after chunk c - 2's dS and Ye, c once chunk c - 3's outputs have left.  Each is followed by an
+    // L2 prefetch of the same box two chunks on, whose buffer is still in use (a, b: by the
+    // head's first tile only, the others read the same).
+    constexpr uint32_t kHi = desc_hi(1024, 2);
+    const uint32_t sA = s0 + L::kOffA, sB = s0 + L::kOffB, sC = s0 + L::kOffC;
+    int loaded = 0;
+    auto load_chunk = [&](int c) -> bool {
+        const int s = c & 1, t0 = chunk_t0(c), t2 = chunk_t0(c + 2);
+#pragma unroll 1
+        for (int i = 0; i <= 2 * L::NB; ++i) {
+            if (STATE && i >= L::NB && i < 2 * L::NB) continue;
+            const bool is_c = i == 2 * L::NB, is_a = i >= L::NB;
+            const int k = is_c ? 0 : is_a ? i - L::NB : i, x = is_c ? c0 : 64 * k;
+            const uint32_t full = is_c ? BAR(fullC, c % kStC) : is_a ? BAR(fullA, s) : BAR(fullB, s);
+            const uint32_t dst = is_c ? sC + (c % kStC) * kBlk : (is_a ? sA : sB) + s * L::kTile + k * kBlk;
+            const CUtensorMap *map = is_c ? &maps.c : is_a ? &maps.a : &maps.b;
+            if (k == 0) {
+                const uint32_t empty = is_c ? BAR(emptyC, c % kStC) : is_a ? BAR(emptyA, s) : BAR(emptyB, s);
+                if (c >= (is_c ? kStC : 2) && !wait1(empty, (is_c ? c / kStC - 1 : (c >> 1) - 1) & 1)) return false;
+                bar_expect(full, is_c ? kBlk : L::kTile);
+            }
+            tma_load(dst, map, full, x, packed ? h : t0, packed ? seq0 + t0 : (int)bh);
+            if (c + 2 < nch && (is_c || tile == 0)) tma_prefetch_l2_3d(map, x, packed ? h : t2, packed ? seq0 + t2 : (int)bh);
+            loaded = c * 3 + (is_c ? 3 : is_a ? 2 : 1);
+        }
+        return true;
+    };
 
     // ------------------------------------------------------------ set-up
     if (tid == 0) {
@@ -266,9 +325,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         for (int i = 0; i < 3; ++i) mbar_init(&sm->done[i], 1);
         sm->abort_flag = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&maps.a);
-        tma_prefetch_desc(&maps.b);
-        tma_prefetch_desc(&maps.c);
+        if (nch > 0) load_chunk(0);     // in flight during the rest of the set-up
         tma_prefetch_desc(&maps.out);
     }
     if (warp == 1) {
@@ -300,40 +357,12 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int row = (warp & 3) * 32 + lane;     // the TMEM lane, and tile row, of this thread
     const int group = warp >> 2;
-    constexpr uint32_t kHi = desc_hi(1024, 2);
-    const uint32_t sA = s0 + L::kOffA, sB = s0 + L::kOffB, sC = s0 + L::kOffC;
 
     if (group == 0) {
         regs_dec<kRegsIssue>();
         if (warp == 0 && lane == 0) {
-            int loaded = 0;
             // --------------------------------------------------- producer
-            // a chunk's boxes in the order in which their buffers come free: b and a of chunk c after chunk
-            // c - 2's dS and Ye, c once chunk c - 3's outputs have left.  Each is followed by an L2
-            // prefetch of the same box two chunks on, whose buffer is still in use (a, b: by the
-            // head's first tile only, the others read the same).
-            bool ok = true;
-            for (int c = 0; c < nch && ok; ++c) {
-                const int s = c & 1, t0 = chunk_t0(c), t2 = chunk_t0(c + 2);
-#pragma unroll 1
-                for (int i = 0; i <= 2 * L::NB; ++i) {
-                    if (STATE && i >= L::NB && i < 2 * L::NB) continue;
-                    const bool is_c = i == 2 * L::NB, is_a = i >= L::NB;
-                    const int k = is_c ? 0 : is_a ? i - L::NB : i, x = is_c ? c0 : 64 * k;
-                    const uint32_t full = is_c ? BAR(fullC, c % kStC) : is_a ? BAR(fullA, s) : BAR(fullB, s);
-                    const uint32_t dst = is_c ? sC + (c % kStC) * kBlk : (is_a ? sA : sB) + s * L::kTile + k * kBlk;
-                    const CUtensorMap *map = is_c ? &maps.c : is_a ? &maps.a : &maps.b;
-                    if (k == 0) {
-                        const uint32_t empty = is_c ? BAR(emptyC, c % kStC) : is_a ? BAR(emptyA, s) : BAR(emptyB, s);
-                        ok = c < (is_c ? kStC : 2) || wait1(empty, (is_c ? c / kStC - 1 : (c >> 1) - 1) & 1);
-                        if (!ok) break;
-                        bar_expect(full, is_c ? kBlk : L::kTile);
-                    }
-                    tma_load(dst, map, full, x, packed ? h : t0, packed ? seq0 + t0 : (int)bh);
-                    if (c + 2 < nch && (is_c || tile == 0)) tma_prefetch_l2_3d(map, x, packed ? h : t2, packed ? seq0 + t2 : (int)bh);
-                    loaded = c * 3 + (is_c ? 3 : is_a ? 2 : 1);
-                }
-            }
+            for (int c = 1; c < nch && load_chunk(c); ++c) {}
             // every issued load lands before the CTA may exit (the last six, in order)
             for (int i = max(0, loaded - 9); i < loaded; ++i) {
                 const int c = i / 3, k = i % 3;
@@ -537,8 +566,16 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             const int i = row & (KD - 1);
             const float *src = sw.init_t ? sw.S_init + (bh * n_all + c0) * KD + i : sw.S_init + (bh * KD + i) * n_all + c0;
             const size_t step = sw.init_t ? KD : 1;
+            if (!sw.init_t && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * step], src[(2 * j + 1) * step]);
+                for (int j = 0; j < 16; ++j) {
+                    const float4 d = reinterpret_cast<const float4 *>(src)[j];
+                    S[2 * j] = make_float2(d.x, d.y), S[2 * j + 1] = make_float2(d.z, d.w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[j] = make_float2(src[2 * j * step], src[(2 * j + 1) * step]);
+            }
         }
         if (STATE && z == 0 && mine) {
 #pragma unroll
