@@ -402,7 +402,18 @@ la_status la_delta_rule_chunked(const void *q, const void *k, const void *v, la_
  *          It is a constant of the model: no gradient is formed for it.
  *   scale  any finite value, typically 1/sqrt(r).
  * Inputs are finite; a row with an infinity or NaN may spoil the outputs of the 128
- * tokens around it as well as all later ones.
+ * tokens around it as well as all later ones.  Outputs do not overlap inputs, but for the
+ * states where it says so.
+ * Kernels:
+ *   BF16, r in {64, 128}, dv a multiple of 64, token arrays 16-byte aligned, more than 16
+ *         tokens: chunks of 128 tokens on the tensor cores.  The scores of a chunk and the state that enters
+ *         it are rounded to BF16 once; the state itself is FP32, each write to it kept to 2^-16
+ *         of its size.  Few heads run their sequences in segments, which needs the workspace.
+ *   else  the token recurrence in FP32 on CUDA cores (for one token of la_decay_decode_step a
+ *         kernel of its own, bound by the state's traffic, when dv is a multiple of 4 and
+ *         S 16-byte aligned).
+ * The first call of each kind on a device sets kernel attributes: make it before any stream
+ * capture.
  */
 
 /*
@@ -414,9 +425,9 @@ la_status la_delta_rule_chunked(const void *q, const void *k, const void *v, la_
  *   S_out  device FP32 [B,H,r,dv] final state
  *   workspace  device scratch of la_decay_prefill_workspace_bytes(...) bytes, 256-byte
  *              aligned, owned by the caller; may be NULL when that is 0.  Calls
- *              sharing one workspace must be ordered.
- * Kernel: the token recurrence in FP32 on CUDA cores, the value columns split over CTAs.
- * Requires 1 <= r, dv <= 256, B, H <= 65535; BF16 arrays 2-byte, FP32 arrays 4-byte
+ *              sharing one workspace must be ordered.  The size depends on the
+ *              device's SM count (0 for sizes the call rejects).
+ * Requires 1 <= r, dv <= 256, B, H <= 65535, T <= 2^30; BF16 arrays 2-byte, FP32 arrays 4-byte
  * aligned.  T may be 0 (S_out = S0; q, k, v, y may then be NULL).
  * Errors: LA_ERR_NULL, LA_ERR_SHAPE (B, H, r, dv < 1, T < 0, scale not finite),
  *         LA_ERR_DTYPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (other sizes),
@@ -436,7 +447,9 @@ la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype
  *   cu_seqlens device int32 [B + 1], 0 <= cu_seqlens[0] <= .. <= cu_seqlens[B] <= total_T.  A
  *              sequence outside [0, total_T] or of negative length is skipped and
  *              recorded as LA_ERR_SHAPE in the device status word.
- * Rows of y outside every sequence are not written.  Needs no workspace.
+ * Rows of y outside every sequence are not written, and what q, k, v hold there (or in
+ * another sequence) reaches no output.  Up to 256 sequences run the longest first; a sequence is
+ * not split.  Needs no workspace.
  * Sizes, alignment and errors as for la_decay_prefill (total_T * H < 2^31).
  */
 la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
@@ -446,9 +459,7 @@ la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, l
 /*
  * la_decay_decode_step -- one new token per (b, h), the state updated in place.
  *   q, k  device [B,H,1,r] dtype    v, y  device [B,H,1,dv] dtype    S  device FP32 [B,H,r,dv]
- * Bound by the state's traffic when dv is a multiple of 4 and S 16-byte aligned;
- * other sizes take the token recurrence.  Requirements and errors as for
- * la_decay_prefill.
+ * Requirements and errors as for la_decay_prefill.
  */
 la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_dtype dtype, const float *decay,
                                float *S, int B, int H, int r, int dv, float scale, void *y, la_stream_t stream);
@@ -461,10 +472,11 @@ la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_d
  *   q, k, v, decay, S0, scale: as passed to the forward call (its outputs are not needed).
  *   dy       device [B,H,T,dv] dtype         dS_T  device FP32 [B,H,r,dv] or NULL (zero)
  *   dq, dk   device [B,H,T,r] dtype          dv_out  device [B,H,T,dv] dtype
- *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL); it does not overlap S0,
- *            and may equal dS_T only when T is 0.
- *   workspace  la_decay_backward_workspace_bytes(...) bytes, 256-byte aligned (NULL when 0).
- * Three sweeps like the forward one, in one launch: dq forwards in time, dk and dv backwards.
+ *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL); overlaps neither S0 nor dS_T.
+ *   workspace  la_decay_backward_workspace_bytes(...) bytes, as for la_decay_prefill.
+ * Three sweeps like the forward one, each with two of the arrays as keys and a third as values: dq
+ * forwards in time, dk and dv backwards, in one launch where they take the same kernel.  On the tensor
+ * cores a sweep's keys are 64 or 128 wide and its values a multiple of 64 (dq and dk: dv keys, r values).
  * Sizes, alignment and errors as for la_decay_prefill.  T may be 0 (dS0 = dS_T).
  */
 size_t la_decay_backward_workspace_bytes(int B, int H, int T, int r, int dv, la_dtype dtype);
@@ -478,7 +490,8 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  * Candidate (k, v) of request b scores
  *     scores[b,k] + logits[b,k,v] - log sum_u exp logits[b,k,u]
  * and the K best, best first, become the request's beams; equal scores go to the lower
- * k * V + v.  (Within one beam candidates rank by their logits.)
+ * k * V + v.  (Within one beam candidates rank by their logits.)  Scores are compared in 64
+ * bits, the log-sum-exp carrying the error of its FP32 exponentials.
  *   logits      device [B,K,V] dtype, row (b, k) at element (b K + k) row_stride
  *   scores      device FP32 [B,K] cumulative log-probabilities
  *   done        device uint8 [B,K], non-zero: beam k has ended; its one candidate is token
@@ -492,7 +505,8 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  * among its logits).  A slot left without a candidate gets score -infinity, its own
  * beam as parent, token 0 and its own done.
  * next_scores may equal scores, done_out may equal done.
- * One launch, one cluster of 2 to 8 CTAs per request, the logits read once.
+ * One launch, one cluster of 2 to 8 CTAs per request, the logits read once; rows that start on
+ * 16-byte boundaries are read fastest.
  * Requires 1 <= K <= 32, 1 <= V <= 2^30, row_stride >= V, B <= 65535; logits aligned to their
  * element size, FP32 and int32 arrays 4-byte aligned.
  * Errors: LA_ERR_NULL, LA_ERR_SHAPE (sizes < 1, row_stride < V, eos out of range or missing),

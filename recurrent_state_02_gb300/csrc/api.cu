@@ -806,7 +806,7 @@ la_status check_decay_sizes(la_dtype dtype, int B, int H, int T, int r, int dv, 
 {
     if (B < 1 || H < 1 || T < 0 || r < 1 || dv < 1 || !std::isfinite(scale)) return LA_ERR_SHAPE;
     if (dtype != LA_DTYPE_BF16 && dtype != LA_DTYPE_FP32) return LA_ERR_DTYPE;
-    if (r > 256 || dv > 256 || B > 65535 || H > 65535) return LA_ERR_UNSUPPORTED;
+    if (r > 256 || dv > 256 || B > 65535 || H > 65535 || T > (1 << 30)) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
 
@@ -870,7 +870,7 @@ size_t split_bytes(long long heads, int tiles, int T, int ra)
 
 bool tc_sizes(la_dtype dtype, int B, int H, int T, int r, int dv)
 {
-    return dtype == LA_DTYPE_BF16 && B >= 1 && H >= 1 && B <= 65535 && H <= 65535 && T > kDecayWalk && r >= 1 && dv >= 1 &&
+    return dtype == LA_DTYPE_BF16 && B >= 1 && H >= 1 && B <= 65535 && H <= 65535 && T <= (1 << 30) && T > kDecayWalk && r >= 1 && dv >= 1 &&
            r <= 256 && dv <= 256;
 }
 

@@ -90,24 +90,22 @@ __device__ __forceinline__ uint4 ld_once(const uint4 *p)
     return v;
 }
 
-// The 16 bytes of a row's granule, whatever the row's alignment: `mis` bytes
-// (a multiple of the element size) past the 16-byte boundary p0, from the one or two
-// aligned words that hold them.  The second is read only when the row reaches it.
-__device__ __forceinline__ uint4 load_granule(const unsigned char *p0, int mis, long long g, long long row_bytes)
+// A lane's granule of rows that do not all start on 16-byte boundaries: elements i, i + 32, .. of the row (0 past
+// its end), one load each, packed like the 16 bytes of an aligned one.
+template <bool BF16>
+__device__ __forceinline__ uint4 load_elements(const void *row, int i, int V)
 {
-    const uint4 *p = reinterpret_cast<const uint4 *>(p0) + g;
-    const uint4 a = mis ? *p : ld_once(p);
-    if (!mis) return a;
-    uint4 b = make_uint4(0, 0, 0, 0);
-    if (16 * (g + 1) < mis + row_bytes) b = p[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t v[5], o[4];
-    const int ws = mis >> 2, sh = (mis & 3) * 8;   // (warp-uniform)
+    constexpr int GE = BF16 ? 8 : 4;
+    uint32_t x[GE], w[4];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = ws == 0 ? w[i] : ws == 1 ? w[i + 1 < 8 ? i + 1 : 7] : ws == 2 ? w[i + 2 < 8 ? i + 2 : 7] : w[i + 3 < 8 ? i + 3 : 7];
+    for (int e = 0; e < GE; ++e) {
+        x[e] = 0;
+        if (i + 32 * e < V)
+            x[e] = BF16 ? reinterpret_cast<const uint16_t *>(row)[i + 32 * e] : reinterpret_cast<const uint32_t *>(row)[i + 32 * e];
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(v[i], v[i + 1], sh);
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < 4; ++j) w[j] = BF16 ? x[2 * j] | x[2 * j + 1] << 16 : x[j];
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <bool BF16>
@@ -135,13 +133,15 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// ALIGNED: every row starts on a 16-byte boundary.
+// ALIGNED: every row starts on a 16-byte boundary, and a lane's granule is 16 bytes of it; else it is elements 32 apart.
+// (Which element goes to which lane depends on its index alone, so equal rows have equal sums.)
 template <bool BF16, bool ALIGNED>
 __global__ void __launch_bounds__(kSelThreads, 2)
 beam_select_kernel(const BeamSelectArgs args)
 {
     constexpr int GE = BF16 ? 8 : 4;       // elements of a 16-byte granule
     constexpr int U = 4;                   // granules in flight per lane
+    constexpr int ES = ALIGNED ? 1 : 32;   // from one element of a granule to the next
     __shared__ SelSmem sm;
     const int K = args.K, V = args.V;
     const uint32_t rank = blockIdx.x, cs = gridDim.x;   // the cluster spans the grid's x axis
@@ -164,10 +164,7 @@ beam_select_kernel(const BeamSelectArgs args)
         const bool skip = part >= parts || (args.done && args.done[(size_t)b * K + k]);
         const unsigned char *row = reinterpret_cast<const unsigned char *>(args.logits) +
                                    ((long long)b * K + k) * args.row_stride * (BF16 ? 2 : 4);
-        const int mis = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
-        const unsigned char *p0 = row - mis;
-        const long long row_bytes = (long long)V * (BF16 ? 2 : 4);
-        const int granules = (V + GE - 1) / GE;
+        const int granules = ALIGNED ? (V + GE - 1) / GE : (V + 32 * GE - 1) / (32 * GE) * 32;
         float m = -3.402823466e38f, s = 0.f;
         unsigned long long thr = 0;      // what a key has to beat
         float thr_x = -INFINITY;         // its logit
@@ -212,10 +209,10 @@ beam_select_kernel(const BeamSelectArgs args)
         auto sum_up = [&](uint4 raw, int i0) -> float {
             float x[GE];
             widen<BF16>(raw, x);
-            if (i0 + GE > V) {
+            if (i0 + (GE - 1) * ES >= V) {
 #pragma unroll
                 for (int e = 0; e < GE; ++e)
-                    if (i0 + e >= V) x[e] = -INFINITY;
+                    if (i0 + e * ES >= V) x[e] = -INFINITY;
             }
             float mx = x[0];
 #pragma unroll
@@ -235,6 +232,8 @@ beam_select_kernel(const BeamSelectArgs args)
             return mx;
         };
         const int step = parts * 32;
+        // the first element of granule g (whose number modulo 32 is the lane's)
+        auto first = [&](int g) { return ALIGNED ? g * GE : (g - lane) * GE + lane; };
         if (lane == 0) sm.count[warp] = 0;
         __syncwarp();
         if (!skip) {
@@ -247,13 +246,13 @@ beam_select_kernel(const BeamSelectArgs args)
                 for (int u = 0; u < U; ++u) {
                     raw[u] = make_uint4(0, 0, 0, 0);
                     if (g + u * step < granules)
-                        raw[u] = ALIGNED ? ld_once(reinterpret_cast<const uint4 *>(p0) + (g + u * step))
-                                         : load_granule(p0, mis, g + u * step, row_bytes);
+                        raw[u] = ALIGNED ? ld_once(reinterpret_cast<const uint4 *>(row) + (g + u * step))
+                                         : load_elements<BF16>(row, first(g + u * step), V);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     mx[u] = -INFINITY;
-                    if (g + u * step < granules) mx[u] = sum_up(raw[u], (g + u * step) * GE);
+                    if (g + u * step < granules) mx[u] = sum_up(raw[u], first(g + u * step));
                     top = fmaxf(top, mx[u]);
                 }
                 const unsigned long long shared_thr = *reinterpret_cast<volatile unsigned long long *>(&sm.bound[k]);
@@ -290,14 +289,14 @@ beam_select_kernel(const BeamSelectArgs args)
                     if (!hits) continue;
                     float x[GE];
                     widen<BF16>(ru, x);
-                    const int i0 = (g + u * step) * GE;
+                    const int i0 = first(g + u * step);
                     if (count + GE * __popc(hits) <= kSelBuf) {
                         // the few lanes with a candidate push on their own
                         if (hit) {
 #pragma unroll
                             for (int e = 0; e < GE; ++e)
-                                if (x[e] >= thr_x && x[e] > -INFINITY && i0 + e < V) {
-                                    const unsigned long long key = make_key(x[e], i0 + e);
+                                if (x[e] >= thr_x && x[e] > -INFINITY && i0 + e * ES < V) {
+                                    const unsigned long long key = make_key(x[e], i0 + e * ES);
                                     if (key > thr) buf[atomicAdd(&sm.count[warp], 1)] = key;
                                 }
                         }
@@ -311,8 +310,8 @@ beam_select_kernel(const BeamSelectArgs args)
                             float xe = x[0];
 #pragma unroll
                             for (int f = 1; f < GE; ++f) xe = e == f ? x[f] : xe;
-                            const unsigned long long key = make_key(xe, i0 + e);
-                            const bool in = hit && xe > -INFINITY && i0 + e < V && key > thr;
+                            const unsigned long long key = make_key(xe, i0 + e * ES);
+                            const bool in = hit && xe > -INFINITY && i0 + e * ES < V && key > thr;
                             const uint32_t who = __ballot_sync(0xffffffffu, in);
                             if (in) buf[count + __popc(who & ((1u << lane) - 1u))] = key;
                             count += __popc(who);

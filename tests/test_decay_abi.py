@@ -40,7 +40,7 @@ def test_decay_refusals(native, entry, names, outs):
     for n in "B H r dv".split():
         assert f(**{n: 0}) == N.LA_ERR_SHAPE, n
     if "T" in names.split():
-        assert f(T=-1) == N.LA_ERR_SHAPE
+        assert f(T=-1) == N.LA_ERR_SHAPE and f(T=(1 << 30) + 1, H=1) == N.LA_ERR_UNSUPPORTED
     assert f(scale=float("nan")) == N.LA_ERR_SHAPE and f(scale=float("inf")) == N.LA_ERR_SHAPE
     assert f(dtype=5) == N.LA_ERR_DTYPE
     assert f(r=257) == N.LA_ERR_UNSUPPORTED and f(dv=257) == N.LA_ERR_UNSUPPORTED
