@@ -34,16 +34,16 @@ __device__ __forceinline__ void store_elem(void *p, size_t i, float x)
 // shared loads of its rows' q and k, one of its columns' v, 12 CPL packed FP32 instructions (row
 // pairs: k v, g S + k v, the sum with q) and one store of its partial sums; the 4 W partial outputs of a
 // column are added once per block of TB tokens.
-// CPL = 4 is for grids that fill the GPU: loads that a whole warp shares still take shared memory about
-// two cycles each, and one column per lane, with three FMAs per load, was bound by them.
-// CPL = 1 is for few heads, where a token's latency counts: four times the warps, a quarter of the
-// instructions each.
+// The columns per lane set how a token's time divides.  Loads that a whole warp shares still take shared
+// memory about two cycles each, so few columns per lane load it; many make a token's chain of instructions
+// long.  One CTA per SM at most (us, FP32, T = 1001): r = 64 82 with CPL = 1, 104 with 2, 203 with 4; r = 128 156, 129,
+// 157.  More CTAs: 512 of r = 64 (T = 1000) 239 with 2, 277 with 4; 256 of r = 128 233 and 249; 4096 of r = 128
+// and 8 tokens (BF16), where the state's traffic counts, 52 and 44.
 // Tokens are staged in blocks; the next block's values are fetched into registers while this
 // one is computed.
 constexpr int kRecCols = 32, kRecRows = 32;
-// One CTA per SM at most takes CPL = 1: 24 CTAs of r = 64 (T = 1001, FP32) 114 us, against 203 with CPL = 4;
-// 128 CTAs of r = 128 158 us either way; 256 CTAs 278 against 235.
-constexpr long long kRecFew = 152;
+constexpr long long kRecFew = 152;   // CTAs
+constexpr int kRecShort = 64;        // tokens
 
 template <int W, int CPL>
 struct RecCfg {
@@ -145,32 +145,48 @@ decay_rec_kernel(const __grid_constant__ RecArgs args)
         const long long oy = oc;    // of the outputs too
         oc += TB * sc;
         if (t0 + TB < T) fetch(t0 + TB);
-#pragma unroll 2
-        for (int t = 0; t < nt; ++t) {
-            const float2 f = splat(sw.late && t0 + t == 0 ? 1.f : g);
+        // a token's operands are loaded while the token before is computed
+        struct Token {
+            float4 x0, x1, k0, k1;
+            float v[CPL];
+        };
+        auto load_token = [&](int t) {
             const float4 *a4 = reinterpret_cast<const float4 *>(as + t * R + i0), *b4 = reinterpret_cast<const float4 *>(bs + t * R + i0);
-            float2 v[CPL];
+            Token k{a4[0], a4[1], b4[0], b4[1], {}};
             if constexpr (CPL == 4) {
                 const float4 v4 = *reinterpret_cast<const float4 *>(cs + t * kRecCols + j1);
-                v[0] = splat(v4.x), v[1] = splat(v4.y), v[2] = splat(v4.z), v[3] = splat(v4.w);
+                k.v[0] = v4.x, k.v[1] = v4.y, k.v[2] = v4.z, k.v[3] = v4.w;
+            } else if constexpr (CPL == 1) {
+                k.v[0] = cs[t * kRecCols + j1];
             } else {
-                v[0] = splat(cs[t * kRecCols + j1]);
+                const float2 v2 = *reinterpret_cast<const float2 *>(cs + t * kRecCols + j1);
+                k.v[0] = v2.x, k.v[1] = v2.y;
             }
-            const float4 x0 = a4[0], x1 = a4[1], k0 = b4[0], k1 = b4[1];
-            const float2 x[4] = {lo2(x0), hi2(x0), lo2(x1), hi2(x1)}, k[4] = {lo2(k0), hi2(k0), lo2(k1), hi2(k1)};
+            return k;
+        };
+        Token next = load_token(0);
+#pragma unroll 2
+        for (int t = 0; t < nt; ++t) {
+            const Token now = next;
+            next = load_token(t + 1 < nt ? t + 1 : t);
+            const float2 f = splat(sw.late && t0 + t == 0 ? 1.f : g);
+            const float2 x[4] = {lo2(now.x0), hi2(now.x0), lo2(now.x1), hi2(now.x1)};
+            const float2 k[4] = {lo2(now.k0), hi2(now.k0), lo2(now.k1), hi2(now.k1)};
             float2 y[CPL] = {};
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
-                    s[p][c] = __ffma2_rn(f, s[p][c], __fmul2_rn(k[p], v[c]));
+                    s[p][c] = __ffma2_rn(f, s[p][c], __fmul2_rn(k[p], splat(now.v[c])));
                     y[c] = __ffma2_rn(x[p], s[p][c], y[c]);
                 }
             float *yt = ys + ((4 * wr + part) * TB + t) * kRecCols + j1;
             if constexpr (CPL == 4)
                 *reinterpret_cast<float4 *>(yt) = make_float4(y[0].x + y[0].y, y[1].x + y[1].y, y[2].x + y[2].y, y[3].x + y[3].y);
-            else
+            else if constexpr (CPL == 1)
                 *yt = y[0].x + y[0].y;
+            else
+                *reinterpret_cast<float2 *>(yt) = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
         }
         __syncthreads();
 #pragma unroll
@@ -210,13 +226,14 @@ cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <bool BF16, int CPL>
+template <bool BF16>
 cudaError_t launch_rec(const RecArgs &r, int rows, dim3 grid, cudaStream_t stream)
 {
-    if (rows <= 32) return launch_rec_w<BF16, 1, CPL>(r, grid, stream);
-    if (rows <= 64) return launch_rec_w<BF16, 2, CPL>(r, grid, stream);
-    if (rows <= 128) return launch_rec_w<BF16, 4, CPL>(r, grid, stream);
-    return launch_rec_w<BF16, 8, CPL>(r, grid, stream);
+    const bool few = (long long)grid.x * grid.y * grid.z <= kRecFew, brief = r.d.cu_seqlens || r.d.T <= kRecShort;
+    if (rows <= 32) return few ? launch_rec_w<BF16, 1, 1>(r, grid, stream) : brief ? launch_rec_w<BF16, 1, 4>(r, grid, stream) : launch_rec_w<BF16, 1, 2>(r, grid, stream);
+    if (rows <= 64) return few ? launch_rec_w<BF16, 2, 1>(r, grid, stream) : brief ? launch_rec_w<BF16, 2, 4>(r, grid, stream) : launch_rec_w<BF16, 2, 2>(r, grid, stream);
+    if (rows <= 128) return !few && brief ? launch_rec_w<BF16, 4, 4>(r, grid, stream) : launch_rec_w<BF16, 4, 2>(r, grid, stream);
+    return !few && brief ? launch_rec_w<BF16, 8, 4>(r, grid, stream) : launch_rec_w<BF16, 8, 2>(r, grid, stream);
 }
 
 // ------------------------------------------------------------ decode step
@@ -325,9 +342,7 @@ cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArg
         rows = sweeps[i].ra > rows ? sweeps[i].ra : rows;
     }
     const dim3 grid(tiles, a.H, B);
-    const bool wide = (long long)tiles * a.H * B > kRecFew;
-    if (bf16) return wide ? launch_rec<true, 4>(r, rows, grid, stream) : launch_rec<true, 1>(r, rows, grid, stream);
-    return wide ? launch_rec<false, 4>(r, rows, grid, stream) : launch_rec<false, 1>(r, rows, grid, stream);
+    return bf16 ? launch_rec<true>(r, rows, grid, stream) : launch_rec<false>(r, rows, grid, stream);
 }
 
 cudaError_t launch_decay_decode(const void *q, const void *k, const void *v, bool bf16, const float *decay, float *S,

@@ -42,7 +42,8 @@ SIZES = [
     (1, 1, 1, 128, 128), (2, 3, 2, 64, 64), (1, 8, 31, 128, 128), (1, 8, 33, 128, 128), (1, 2, 64, 64, 128),
     (1, 2, 127, 128, 64), (2, 8, 128, 128, 128), (1, 3, 129, 64, 64), (1, 8, 300, 128, 128), (1, 2, 513, 128, 192),
     (1, 2, 777, 64, 256), (1, 2, 40, 96, 80), (2, 2, 37, 33, 7), (1, 1, 50, 256, 160), (1, 2, 19, 1, 1),
-    (1, 1, 130, 128, 100),
+    (1, 1, 130, 128, 100), (8, 20, 70, 64, 32), (8, 20, 70, 128, 32), (8, 20, 9, 100, 32), (8, 20, 9, 40, 32), (8, 20, 66, 200, 32),
+    (160, 1, 65, 20, 20),
 ]
 
 
