@@ -167,6 +167,29 @@ def test_packed(la, r, dv, dtype):
                 R.bounds(n, r, dv, dtype == torch.bfloat16, abs_y, ref_y, chunked(dtype)), f"y {n}")
 
 
+@pytest.mark.parametrize("B", [256, 300])
+def test_packed_many_sequences(la, B):
+    """Batches on both sides of the size up to which the longest sequences run first: every sequence finds its own rows
+    and state (short ones, which take the recurrence, beside chunked ones)."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 60, (B,), generator=g).tolist()
+    lens[B - 1], lens[7] = 400, 0
+    H, total = 1, sum(lens)
+    q, k, v, _, _, _, _ = make(1, H, total, 64, 64, torch.bfloat16, False, 8, layout="tok")
+    decay = torch.tensor([0.97], device="cuda")
+    S0 = torch.randn((B, H, 64, 64), generator=g).cuda()
+    cu = torch.tensor([sum(lens[:i]) for i in range(B + 1)], dtype=torch.int32, device="cuda")
+    y, S = la.decay_prefill_varlen(q, k, v, decay, cu, S0=S0, scale=0.5)
+    assert la.last_device_status() == 0
+    for b in [*range(0, B, 17), 7, 8, B - 2, B - 1]:
+        a, n = int(cu[b]), lens[b]
+        one = [x[a:a + n].transpose(0, 1)[None] for x in (q, k, v)]
+        ref_y, ref_S = R.prefill(*one, decay, S0[b:b + 1], 0.5)
+        abs_y, abs_S = R.prefill(*R.absolute(*one), decay, S0[b:b + 1].abs(), 0.5)
+        R.check(S[b:b + 1], ref_S, R.state_bound(n, abs_S, True), f"S {b}")
+        R.check(y[a:a + n].transpose(0, 1)[None], ref_y, R.bounds(n, 64, 64, True, abs_y, ref_y, True), f"y {b}")
+
+
 def test_packed_neighbours_do_not_leak(la):
     """A sequence of NaN between two others leaves them finite and unchanged."""
     lens, H = [100, 70, 300, 40], 2
