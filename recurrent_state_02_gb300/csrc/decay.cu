@@ -10,6 +10,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 namespace la {
 namespace {
 
@@ -27,6 +29,25 @@ __device__ __forceinline__ void store_elem(void *p, size_t i, float x)
     else reinterpret_cast<float *>(p)[i] = x;
 }
 
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address in CTA `rank` of the cluster of what is at shared address `addr` here.
+__device__ __forceinline__ uint32_t in_cluster(uint32_t addr, uint32_t rank)
+{
+    uint32_t out;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+    return out;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr));
+    return x;
+}
+
 // ------------------------------------------------------- token recurrence
 // One CTA per (b, h, 32 columns), the state in registers.  Its W * CB warps (CB = 4 / CPL) split
 // the rows into blocks of 32 and the columns into blocks of 8 CPL; lane (g, jj), g = lane / 8,
@@ -41,6 +62,11 @@ __device__ __forceinline__ void store_elem(void *p, size_t i, float x)
 // and 8 tokens (BF16), where the state's traffic counts, 52 and 44.
 // Tokens are staged in blocks; the next block's values are fetched into registers while this
 // one is computed.
+//
+// SPLIT: few CTAs leave SMs idle while each walks its tokens one by one, 80 to 230 ns each.  A cluster then takes
+// one (b, h, 32 columns), a CTA a segment of its tokens: all form what their segment adds to the state
+// from zero (the first one from S_init, with its outputs), exchange the sums over distributed shared
+// memory, S <- g^seg S + sum over the segments before, and pass their tokens again with outputs.
 constexpr int kRecCols = 32, kRecRows = 32;
 constexpr long long kRecFew = 152;   // CTAs
 constexpr int kRecShort = 64;        // tokens
@@ -58,13 +84,14 @@ struct RecArgs {
     DecaySweep sw[3];
     DecayArgs d;
     int tiles[3];   // column tiles of each sweep
+    int nseg, seg;  // segments of a sequence, one CTA of a cluster each, and their tokens
 };
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 lo2(float4 a) { return make_float2(a.x, a.y); }
 __device__ __forceinline__ float2 hi2(float4 a) { return make_float2(a.z, a.w); }
 
-template <bool BF16, int W, int CPL>
+template <bool BF16, int W, int CPL, bool SPLIT>
 __global__ void __launch_bounds__(32 * W * 4 / CPL)
 decay_rec_kernel(const __grid_constant__ RecArgs args)
 {
@@ -73,7 +100,8 @@ decay_rec_kernel(const __grid_constant__ RecArgs args)
     extern __shared__ float4 rec_smem[];
     float *as = reinterpret_cast<float *>(rec_smem), *bs = as + TB * R, *cs = bs + TB * R;
     float *ys = cs + TB * kRecCols;              // [4 W][TB][kRecCols]
-    int tile = blockIdx.x, which = 0;
+    const int rank = SPLIT ? blockIdx.x % args.nseg : 0;   // (the cluster spans nseg CTAs of the x axis)
+    int tile = SPLIT ? blockIdx.x / args.nseg : blockIdx.x, which = 0;
     while (tile >= args.tiles[which]) tile -= args.tiles[which++];
     const DecaySweep &sw = args.sw[which];
     const DecayArgs &d = args.d;
@@ -109,7 +137,7 @@ decay_rec_kernel(const __grid_constant__ RecArgs args)
             // element i of column j: rows apart, or contiguous in a transposed state
             const float *src = sw.S_init + (sw.init_t ? (bh * n + j) * ra : bh * ra * n + j);
             const size_t step = sw.init_t ? 1 : n;
-            const bool ok = sw.S_init && j < n;
+            const bool ok = sw.S_init && j < n && rank == 0;
             s[p][c] = make_float2(ok && i < ra ? src[i * step] : 0.f, ok && i + 1 < ra ? src[(i + 1) * step] : 0.f);
         }
     // staging: thread e + R x fetches element e of the tokens x, x + CB, .. of a and b; warp w column
@@ -118,87 +146,143 @@ decay_rec_kernel(const __grid_constant__ RecArgs args)
     const int ea = tid % R, xa = tid / R;
     const bool in_a = ea < ra, in_c = c0 + lane < n;
     const long long sa = step * ra, sc = step * n;
-    long long oa = (first + xa * step) * ra + ea, oc = (first + warp * step) * n + c0 + lane;   // at token t0
-    auto fetch = [&](int t0) {
+    // the tokens begin .. end-1; `outs`: with their outputs (else the state alone)
+    auto pass = [&](int begin, int end, auto outs) {
+        constexpr bool OUT = decltype(outs)::value;
+        // this thread's first elements at token t0
+        long long oa = (first + (begin + xa) * step) * ra + ea, oc = (first + (begin + warp) * step) * n + c0 + lane;
+        auto fetch = [&](int t0) {
 #pragma unroll
-        for (int x = 0; x < C::NA; ++x) {
-            const bool ok = in_a && t0 + x * C::CB + xa < T;
-            pa[x] = ok ? load_elem<BF16>(sw.a, oa + x * C::CB * sa) : 0.f;
-            pb[x] = ok ? load_elem<BF16>(sw.b, oa + x * C::CB * sa) : 0.f;
-        }
-#pragma unroll
-        for (int x = 0; x < C::NC; ++x) {
-            const int t = x * NW + warp;
-            pc[x] = in_c && t < TB && t0 + t < T ? load_elem<BF16>(sw.c, oc + x * NW * sc) * sw.write_scale : 0.f;
-        }
-        oa += TB * sa;
-    };
-    if (T > 0) fetch(0);
-    for (int t0 = 0; t0 < T; t0 += TB) {
-        const int nt = min(TB, T - t0);
-#pragma unroll
-        for (int x = 0; x < C::NA; ++x) as[x * NT + tid] = pa[x], bs[x * NT + tid] = pb[x];
-#pragma unroll
-        for (int x = 0; x < C::NC; ++x)
-            if (NW * C::NC == TB || x * NW + warp < TB) cs[x * NT + tid] = pc[x];
-        __syncthreads();
-        const long long oy = oc;    // of the outputs too
-        oc += TB * sc;
-        if (t0 + TB < T) fetch(t0 + TB);
-        // a token's operands are loaded while the token before is computed
-        struct Token {
-            float4 x0, x1, k0, k1;
-            float v[CPL];
-        };
-        auto load_token = [&](int t) {
-            const float4 *a4 = reinterpret_cast<const float4 *>(as + t * R + i0), *b4 = reinterpret_cast<const float4 *>(bs + t * R + i0);
-            Token k{a4[0], a4[1], b4[0], b4[1], {}};
-            if constexpr (CPL == 4) {
-                const float4 v4 = *reinterpret_cast<const float4 *>(cs + t * kRecCols + j1);
-                k.v[0] = v4.x, k.v[1] = v4.y, k.v[2] = v4.z, k.v[3] = v4.w;
-            } else if constexpr (CPL == 1) {
-                k.v[0] = cs[t * kRecCols + j1];
-            } else {
-                const float2 v2 = *reinterpret_cast<const float2 *>(cs + t * kRecCols + j1);
-                k.v[0] = v2.x, k.v[1] = v2.y;
+            for (int x = 0; x < C::NA; ++x) {
+                const bool ok = in_a && t0 + x * C::CB + xa < end;
+                if (OUT) pa[x] = ok ? load_elem<BF16>(sw.a, oa + x * C::CB * sa) : 0.f;
+                pb[x] = ok ? load_elem<BF16>(sw.b, oa + x * C::CB * sa) : 0.f;
             }
-            return k;
+#pragma unroll
+            for (int x = 0; x < C::NC; ++x) {
+                const int t = x * NW + warp;
+                pc[x] = in_c && t < TB && t0 + t < end ? load_elem<BF16>(sw.c, oc + x * NW * sc) * sw.write_scale : 0.f;
+            }
+            oa += TB * sa;
         };
-        Token next = load_token(0);
+        if (begin < end) fetch(begin);
+        for (int t0 = begin; t0 < end; t0 += TB) {
+            const int nt = min(TB, end - t0);
+#pragma unroll
+            for (int x = 0; x < C::NA; ++x) {
+                if (OUT) as[x * NT + tid] = pa[x];
+                bs[x * NT + tid] = pb[x];
+            }
+#pragma unroll
+            for (int x = 0; x < C::NC; ++x)
+                if (NW * C::NC == TB || x * NW + warp < TB) cs[x * NT + tid] = pc[x];
+            __syncthreads();
+            const long long oy = oc;    // of the outputs too
+            oc += TB * sc;
+            if (t0 + TB < end) fetch(t0 + TB);
+            // a token's operands are loaded while the token before is computed
+            struct Token {
+                float4 x0, x1, k0, k1;
+                float v[CPL];
+            };
+            auto load_token = [&](int t) {
+                const float4 *a4 = reinterpret_cast<const float4 *>(as + t * R + i0), *b4 = reinterpret_cast<const float4 *>(bs + t * R + i0);
+                Token k;
+                if (OUT) k.x0 = a4[0], k.x1 = a4[1];
+                k.k0 = b4[0], k.k1 = b4[1];
+                if constexpr (CPL == 4) {
+                    const float4 v4 = *reinterpret_cast<const float4 *>(cs + t * kRecCols + j1);
+                    k.v[0] = v4.x, k.v[1] = v4.y, k.v[2] = v4.z, k.v[3] = v4.w;
+                } else if constexpr (CPL == 1) {
+                    k.v[0] = cs[t * kRecCols + j1];
+                } else {
+                    const float2 v2 = *reinterpret_cast<const float2 *>(cs + t * kRecCols + j1);
+                    k.v[0] = v2.x, k.v[1] = v2.y;
+                }
+                return k;
+            };
+            Token next = load_token(0);
 #pragma unroll 2
-        for (int t = 0; t < nt; ++t) {
-            const Token now = next;
-            next = load_token(t + 1 < nt ? t + 1 : t);
-            const float2 f = splat(sw.late && t0 + t == 0 ? 1.f : g);
-            const float2 x[4] = {lo2(now.x0), hi2(now.x0), lo2(now.x1), hi2(now.x1)};
-            const float2 k[4] = {lo2(now.k0), hi2(now.k0), lo2(now.k1), hi2(now.k1)};
-            float2 y[CPL] = {};
+            for (int t = 0; t < nt; ++t) {
+                const Token now = next;
+                next = load_token(t + 1 < nt ? t + 1 : t);
+                const float2 f = splat(sw.late && t0 + t == 0 ? 1.f : g);
+                float2 x[4];
+                if (OUT) x[0] = lo2(now.x0), x[1] = hi2(now.x0), x[2] = lo2(now.x1), x[3] = hi2(now.x1);
+                const float2 k[4] = {lo2(now.k0), hi2(now.k0), lo2(now.k1), hi2(now.k1)};
+                float2 y[CPL] = {};
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c) {
+                        s[p][c] = __ffma2_rn(f, s[p][c], __fmul2_rn(k[p], splat(now.v[c])));
+                        if (OUT) y[c] = __ffma2_rn(x[p], s[p][c], y[c]);
+                    }
+                if (!OUT) continue;
+                float *yt = ys + ((4 * wr + part) * TB + t) * kRecCols + j1;
+                if constexpr (CPL == 4)
+                    *reinterpret_cast<float4 *>(yt) = make_float4(y[0].x + y[0].y, y[1].x + y[1].y, y[2].x + y[2].y, y[3].x + y[3].y);
+                else if constexpr (CPL == 1)
+                    *yt = y[0].x + y[0].y;
+                else
+                    *reinterpret_cast<float2 *>(yt) = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+            }
+            __syncthreads();
+            if (!OUT) continue;
+#pragma unroll
+            for (int x = 0; x < C::NC; ++x) {
+                if (x * NW + warp >= nt) break;
+                float y = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4 * W; ++w) y += ys[w * TB * kRecCols + x * NT + tid];
+                if (in_c) store_elem<BF16>(sw.out, oy + x * NW * sc, y * sw.out_scale);
+            }
+            // (the next iteration's first barrier orders these reads of ys before its next writes, and
+            // this iteration's last one its reads of the staged tokens before they are overwritten)
+        }
+    };
+    if constexpr (!SPLIT) {
+        pass(0, T, std::true_type{});
+    } else {
+        // what each segment adds to the state (the first one: its final state, and its outputs) ..
+        const int begin = rank * args.seg, end = min(T, begin + args.seg);
+        const bool last = rank == args.nseg - 1;
+        if (rank == 0) pass(begin, end, std::true_type{});
+        else if (!last) pass(begin, end, std::false_type{});
+        __syncthreads();
+        if (!last) {
+            // .. to the CTAs behind it, in the words of ys (R x kRecCols of them are there); a thread
+            // holds the same elements in every CTA
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
-                    s[p][c] = __ffma2_rn(f, s[p][c], __fmul2_rn(k[p], splat(now.v[c])));
-                    y[c] = __ffma2_rn(x[p], s[p][c], y[c]);
+                    ys[((2 * p) * CPL + c) * NT + tid] = s[p][c].x;
+                    ys[((2 * p + 1) * CPL + c) * NT + tid] = s[p][c].y;
                 }
-            float *yt = ys + ((4 * wr + part) * TB + t) * kRecCols + j1;
-            if constexpr (CPL == 4)
-                *reinterpret_cast<float4 *>(yt) = make_float4(y[0].x + y[0].y, y[1].x + y[1].y, y[2].x + y[2].y, y[3].x + y[3].y);
-            else if constexpr (CPL == 1)
-                *yt = y[0].x + y[0].y;
-            else
-                *reinterpret_cast<float2 *>(yt) = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
         }
-        __syncthreads();
+        cluster_sync();
+        if (rank > 0) {
+            // g^seg by repeated squares in 64 bits
+            double gp = 1.0, gb = g;
+            for (int e = args.seg; e; e >>= 1, gb *= gb)
+                if (e & 1) gp *= gb;
+            const float gs = static_cast<float>(gp);
+            for (int part_rank = 0; part_rank < rank; ++part_rank) {
+                const uint32_t from = in_cluster(smem_u32(ys + tid), part_rank);
 #pragma unroll
-        for (int x = 0; x < C::NC; ++x) {
-            if (x * NW + warp >= nt) break;
-            float y = 0.f;
+                for (int p = 0; p < 4; ++p)
 #pragma unroll
-            for (int w = 0; w < 4 * W; ++w) y += ys[w * TB * kRecCols + x * NT + tid];
-            if (in_c) store_elem<BF16>(sw.out, oy + x * NW * sc, y * sw.out_scale);
+                    for (int c = 0; c < CPL; ++c) {
+                        const float x0 = ld_cluster(from + 4 * ((2 * p) * CPL + c) * NT);
+                        const float x1 = ld_cluster(from + 4 * ((2 * p + 1) * CPL + c) * NT);
+                        s[p][c] = part_rank ? make_float2(fmaf(gs, s[p][c].x, x0), fmaf(gs, s[p][c].y, x1)) : make_float2(x0, x1);
+                    }
+            }
         }
-        // (the next iteration's first barrier orders these reads of ys before its next writes, and
-        // this iteration's last one its reads of the staged tokens before they are overwritten)
+        cluster_sync();   // (every CTA's ys has been read)
+        if (rank > 0) pass(begin, end, std::true_type{});
+        if (!last) return;
     }
     if (!sw.S_fin) return;
     const float f = sw.late && T > 0 ? g : 1.f;
@@ -215,21 +299,56 @@ decay_rec_kernel(const __grid_constant__ RecArgs args)
         }
 }
 
-template <bool BF16, int W, int CPL>
+template <bool BF16, int W, int CPL, bool SPLIT = false>
 cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
 {
     using C = RecCfg<W, CPL>;
     static OncePerDevice once;
-    const cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL>, C::kSmem, once);
+    const cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL, SPLIT>, C::kSmem, once);
     if (e != cudaSuccess) return e;
-    decay_rec_kernel<BF16, W, CPL><<<grid, C::kThreads, C::kSmem, stream>>>(r);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = SPLIT ? dim3(grid.x * r.nseg, grid.y, grid.z) : grid;
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = SPLIT ? r.nseg : 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, decay_rec_kernel<BF16, W, CPL, SPLIT>, r);
+}
+
+// Segments of a sequence of T tokens whose sweeps have `units` CTAs.  Every segment but the
+// first and the last is passed twice at the same cost per token, so that n of them take
+// 2 / n of the time if each of their CTAs has an SM (with many tokens and up to 128
+// rows: half of one).  A cluster lies in one GPC, of 16 SMs or more, so 8 (16 / n) clusters
+// find an SM per CTA (24 of 5 do, 24 of 6 do not).  FP32, us whole and in n segments:
+//   T = 1001  r = 64   24 CTAs 80 and 40 (8); 48 CTAs 80 and 60 (5); 76 CTAs 80 and 91 (7, the best: stays whole)
+//             r = 128  32 CTAs 126 and 63 (8); 64 CTAs 126 and 105 (4)
+//             r = 256  32 CTAs 230 and 119 (4), 203 (8)
+//   T = 128   r = 64   24 CTAs 12.8 and 10.1 (5), 12.9 (8);  T = 64 7.8 and 8.3 (5)
+int rec_segments(long long units, int rows, int T)
+{
+    if (T < 2 * kRecShort) return 1;
+    const bool share = T >= 512 && rows <= 128;
+    for (int n = 8; n >= (share ? 4 : 3); --n)
+        if (units <= 8 * ((share ? 32 : 16) / n)) return n;
+    return 1;
 }
 
 template <bool BF16>
 cudaError_t launch_rec(const RecArgs &r, int rows, dim3 grid, cudaStream_t stream)
 {
     const bool few = (long long)grid.x * grid.y * grid.z <= kRecFew, brief = r.d.cu_seqlens || r.d.T <= kRecShort;
+    if (r.nseg > 1) {
+        if (rows <= 32) return launch_rec_w<BF16, 1, 1, true>(r, grid, stream);
+        if (rows <= 64) return launch_rec_w<BF16, 2, 1, true>(r, grid, stream);
+        if (rows <= 128) return launch_rec_w<BF16, 4, 2, true>(r, grid, stream);
+        return launch_rec_w<BF16, 8, 2, true>(r, grid, stream);
+    }
     if (rows <= 32) return few ? launch_rec_w<BF16, 1, 1>(r, grid, stream) : brief ? launch_rec_w<BF16, 1, 4>(r, grid, stream) : launch_rec_w<BF16, 1, 2>(r, grid, stream);
     if (rows <= 64) return few ? launch_rec_w<BF16, 2, 1>(r, grid, stream) : brief ? launch_rec_w<BF16, 2, 4>(r, grid, stream) : launch_rec_w<BF16, 2, 2>(r, grid, stream);
     if (rows <= 128) return !few && brief ? launch_rec_w<BF16, 4, 4>(r, grid, stream) : launch_rec_w<BF16, 4, 2>(r, grid, stream);
@@ -343,6 +462,11 @@ cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArg
         rows = sweeps[i].ra > rows ? sweeps[i].ra : rows;
     }
     const dim3 grid(tiles, a.H, B);
+    r.nseg = 1, r.seg = a.T;
+    if (const int want = a.cu_seqlens ? 1 : rec_segments((long long)tiles * a.H * B, rows, a.T); want > 1) {
+        r.seg = (a.T + want - 1) / want;
+        r.nseg = (a.T + r.seg - 1) / r.seg;
+    }
     return bf16 ? launch_rec<true>(r, rows, grid, stream) : launch_rec<false>(r, rows, grid, stream);
 }
 

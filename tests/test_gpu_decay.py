@@ -138,6 +138,49 @@ def test_split_sweeps(la, size):
     R.check(got[3], ref[3], R.state_bound(T, mag[3], True), "dS0")
 
 
+# one CTA per 32 columns: 1 to 65 of them, so that 8 to 3 segments run, or one
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("size", [
+    (1, 1, 128, 20, 20), (1, 2, 129, 96, 40), (2, 3, 255, 40, 100), (1, 3, 600, 64, 50), (1, 5, 200, 100, 150), (2, 10, 131, 30, 64),
+    (1, 10, 150, 50, 100), (3, 12, 513, 100, 30), (1, 12, 520, 64, 100), (4, 16, 512, 40, 9), (5, 13, 515, 40, 9),
+    (1, 2, 700, 200, 256), (1, 5, 160, 256, 200)], ids=lambda s: "x".join(map(str, s)))
+def test_recurrence_in_segments(la, size, dtype):
+    """Few CTAs and some length: the recurrence runs its segments side by side, over its own state too, and so do the
+    sweeps of the gradients.  (A term is rounded at most twice per segment and token: within the bounds.)"""
+    B, H, T, r, dv = size
+    q, k, v, dy, decay, S0, dS_T = make(*size, dtype, True, seed=sum(size))
+    scale = r ** -0.5
+    S = S0.clone()
+    y, _ = la.decay_prefill(q, k, v, decay, S0=S, scale=scale, S_out=S)
+    got = la.decay_backward(q, k, v, dy, decay, S0=S0, dS_T=dS_T, scale=scale)
+    assert la.last_device_status() == 0
+    ref_y, ref_S = R.prefill(q, k, v, decay, S0, scale)
+    abs_y, abs_S = R.prefill(*R.absolute(q, k, v), decay, *R.absolute(S0), scale)
+    bf16 = dtype == torch.bfloat16
+    R.check(S, ref_S, R.state_bound(T, abs_S, False), "S")
+    R.check(y, ref_y, R.bounds(T, r, dv, bf16, abs_y, ref_y, False), "y")
+    ref = R.backward(q, k, v, dy, decay, S0, dS_T, scale)
+    mag = R.backward(*R.absolute(q, k, v, dy), decay, *R.absolute(S0, dS_T), scale)
+    for x, z, m, name in zip(got[:3], ref[:3], mag[:3], ("dq", "dk", "dv")):
+        R.check(x, z, R.bounds(T, r, dv, bf16, m, z, False), name)
+    R.check(got[3], ref[3], R.state_bound(T, mag[3], False), "dS0")
+
+
+def test_recurrence_in_segments_is_captured(la):
+    """A graph of the call gives the same bits as the call, twice."""
+    q, k, v, _, decay, S0, _ = make(1, 3, 300, 40, 70, torch.float32, True, seed=9)
+    y, S = la.decay_prefill(q, k, v, decay, S0=S0)
+    y2, S2 = torch.zeros_like(y), torch.zeros_like(S)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        la.decay_prefill(q, k, v, decay, S0=S0, y=y2, S_out=S2)
+    for _ in range(2):
+        y2.zero_(), S2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(S, S2)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("r,dv", [(128, 128), (64, 128), (40, 24)])
 def test_packed(la, r, dv, dtype):
