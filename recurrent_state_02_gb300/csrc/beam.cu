@@ -486,9 +486,11 @@ cudaError_t launch_reorder(const W *S, const W *z, const int *parents, int B, in
 
 cudaError_t launch_beam_select(const BeamSelectArgs &a, int B, bool bf16, int sms, cudaStream_t stream)
 {
-    // CTAs per request: as many as keep the batch within the 2 per SM that are resident
+    // CTAs per request: as many as keep the batch resident at 2 per SM.  A cluster lies in one GPC and leaves some of
+    // its SMs over, so 7/8 of them are counted on: K4 V131072 BF16 at B = 76 takes 48.9 us with 4 (304 CTAs, a second
+    // wave) and 37.6 with 3, B = 48 32.2 with 4, 29.6 with 5 and 41.0 with 6, B = 88 46.1 with 2 and 38.1 with 3.
     int cs = 8;
-    while (cs > 2 && (long long)B * cs > 2LL * sms) cs >>= 1;
+    while (cs > 2 && 4LL * B * cs > 7LL * sms) --cs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cs, B, 1);
     cfg.blockDim = dim3(kSelThreads, 1, 1);

@@ -51,6 +51,13 @@ def test_select(la, size, dtype):
     check(la, *make(*size, dtype, sum(size)))
 
 
+@pytest.mark.parametrize("K", [1, 5, 32])
+@pytest.mark.parametrize("B", [33, 38, 44, 53, 66, 88, 89, 153])
+def test_select_batches(la, B, K):
+    """Batches on every number of CTAs per request (8 to 2), with as many parts per row as fit or one."""
+    check(la, *make(B, K, 300 if K < 32 else 70, torch.bfloat16, B + K))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("offset", [0, 1, 2, 3, 5, 7])
 def test_select_padded_and_misaligned_rows(la, offset, dtype):
