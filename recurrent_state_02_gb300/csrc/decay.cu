@@ -304,8 +304,17 @@ cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
 {
     using C = RecCfg<W, CPL>;
     static OncePerDevice once;
-    const cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL, SPLIT>, C::kSmem, once);
+    cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL, SPLIT>, C::kSmem, once);
     if (e != cudaSuccess) return e;
+    if (SPLIT && r.nseg > 8) {
+        static OncePerDevice wide;   // clusters of more than 8
+        const int dev = current_device_index();
+        if (!wide.done[dev].load(std::memory_order_acquire)) {
+            e = cudaFuncSetAttribute(decay_rec_kernel<BF16, W, CPL, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            wide.done[dev].store(true, std::memory_order_release);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = SPLIT ? dim3(grid.x * r.nseg, grid.y, grid.z) : grid;
     cfg.blockDim = dim3(C::kThreads, 1, 1);
@@ -330,10 +339,16 @@ cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
 //             r = 128  32 CTAs 126 and 63 (8); 64 CTAs 126 and 105 (4)
 //             r = 256  32 CTAs 230 and 119 (4), 203 (8)
 //   T = 128   r = 64   24 CTAs 12.8 and 10.1 (5), 12.9 (8);  T = 64 7.8 and 8.3 (5)
+// Clusters of more than 8 have to be asked for, and fewer GPCs have room for them: T = 16384
+// r = 64, 4 CTAs 1258 whole, 332 (8), 225 (12), 172 (16); 8 CTAs 1271, 337 (8), 228 (12), 276 (16).
+// 14 clusters of 8 still find an SM per CTA (r = 96, T = 1001: 41, two CTAs per SM in clusters of 12 48), 16 do not (r = 128:
+// 58 and 49).
 int rec_segments(long long units, int rows, int T)
 {
     if (T < 2 * kRecShort) return 1;
     const bool share = T >= 512 && rows <= 128;
+    if (T >= 512 && units <= 4) return 16;
+    if (T >= 512 && (units <= 8 || (share && units > 14 && units <= 16))) return 12;
     for (int n = 8; n >= (share ? 4 : 3); --n)
         if (units <= 8 * ((share ? 32 : 16) / n)) return n;
     return 1;

@@ -138,12 +138,13 @@ def test_split_sweeps(la, size):
     R.check(got[3], ref[3], R.state_bound(T, mag[3], True), "dS0")
 
 
-# one CTA per 32 columns: 1 to 65 of them, so that 8 to 3 segments run, or one
+# one CTA per 32 columns: 1 to 65 of them, so that 16 to 3 segments run, or one
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("size", [
     (1, 1, 128, 20, 20), (1, 2, 129, 96, 40), (2, 3, 255, 40, 100), (1, 3, 600, 64, 50), (1, 5, 200, 100, 150), (2, 10, 131, 30, 64),
     (1, 10, 150, 50, 100), (3, 12, 513, 100, 30), (1, 12, 520, 64, 100), (4, 16, 512, 40, 9), (5, 13, 515, 40, 9),
-    (1, 2, 700, 200, 256), (1, 5, 160, 256, 200)], ids=lambda s: "x".join(map(str, s)))
+    (1, 2, 700, 200, 256), (1, 5, 160, 256, 200), (1, 1, 515, 20, 60), (1, 4, 513, 100, 100), (1, 1, 512, 256, 100),
+    (1, 1, 1030, 200, 200), (1, 1, 2049, 128, 20)], ids=lambda s: "x".join(map(str, s)))
 def test_recurrence_in_segments(la, size, dtype):
     """Few CTAs and some length: the recurrence runs its segments side by side, over its own state too, and so do the
     sweeps of the gradients.  (A term is rounded at most twice per segment and token: within the bounds.)"""
