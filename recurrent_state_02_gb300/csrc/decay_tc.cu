@@ -76,7 +76,7 @@ struct Lay {
 
 struct alignas(16) SmallD {
     uint64_t fullA[2], fullB[2], fullC[kStC], emptyA[2], emptyB[2], emptyC[kStC];
-    uint64_t p_raw[2], p_ready[2], p_free[2], w_full, w_empty, ds_full, ds_empty, s_full, ye_full, yi_full, yi_empty, done[3];
+    uint64_t p_raw[2], p_ready[2], p_free[2], w_full, w_empty, ds_full, ds_empty, s_full, ye_full, yi_full, yi_empty, tail, done[3];
     uint32_t tmem_base;
     int abort_flag;
     alignas(16) float pw[kCT + 4];     // g^0 .. g^128
@@ -334,6 +334,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         mbar_init(&sm->ye_full, 1);
         mbar_init(&sm->yi_full, 1);
         mbar_init(&sm->yi_empty, 4);
+        mbar_init(&sm->tail, 4);
         for (int i = 0; i < 3; ++i) mbar_init(&sm->done[i], 1);
         sm->abort_flag = 0;
         fence_mbarrier_init();
@@ -388,9 +389,11 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
             for (int c = 0; c < nch; ++c) {
                 const int s = c & 1;
                 if (!wait1(BAR(fullB, s), (c >> 1) & 1) || !wait1(BAR(fullA, s), (c >> 1) & 1)) break;
-                // the rows behind a packed sequence (in its last chunk) are zeros in b and c once its weighted
-                // values are written: what lies there may be anything, and a mask of zeros would let it through
-                if (packed && c == nch - 1 && !wait1(BAR(w_full, 0), c & 1)) break;
+                // the rows behind a packed sequence (in its last chunk) become zeros in b and c before its scores, and
+                // so its Yi, are formed: what lies there may be anything, and a mask of zeros would let it through.
+                // A barrier of one phase: one that every chunk completes would have to be waited for in
+                // every chunk, as a wait by parity also returns when the phase before is still open.
+                if (packed && c == nch - 1 && chunk_n(c) < kCT && !wait1(BAR(tail, 0), 0)) break;
                 // the buffer held P of chunk c - 2, whose product is done
                 if (c >= 2 && !wait1(BAR(p_free, s), ((c >> 1) - 1) & 1)) break;
                 tc_fence_after();
@@ -532,6 +535,8 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
                             sts4(sB + (c & 1) * L::kTile + k * kBlk + sw128_offset(row, x), 0, 0, 0, 0);
                     }
                 }
+                fence_proxy_async_smem();
+                bar_arrive_warp(BAR(tail, 0));
             }
             // both parts are formed while dS of chunk c - 1 still reads its own
             uint32_t hi[32], lo[32];

@@ -382,3 +382,45 @@ def test_python_refusals(la):
         la.decay_prefill(q, k, v, decay, scale=float("nan"))
     with pytest.raises(ValueError):
         la.decay_prefill(q.half(), k.half(), v.half(), decay)
+
+
+@pytest.mark.parametrize("r,dv", [(128, 128), (64, 64), (64, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_packed_tail_is_isolated(la, r, dv, bad):
+    """Sequences of one chunk and of several, with a ragged last one, right before rows that are not finite (another
+    sequence's, long and short, and what lies behind the last one): outputs and states have the bits of the run with
+    finite rows there, whatever the timing of the loads (L2 warm and flushed)."""
+    lens, ends, H = [129, 40, 200, 3, 255, 20, 257, 40, 300, 3, 1000, 130, 385, 7, 100], {40, 3, 20, 130, 7}, 16
+    total = sum(lens) + 150
+    q, k, v, _, _, _, _ = make(1, H, total, r, dv, torch.bfloat16, False, 21, layout="tok")
+    decay = torch.tensor([DECAYS[h % len(DECAYS)] for h in range(H)]).cuda()
+    S0 = torch.randn((len(lens), H, r, dv), generator=torch.Generator().manual_seed(22)).cuda()
+    start = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    cu = torch.tensor(start, dtype=torch.int32, device="cuda")
+    keep = [b for b, n in enumerate(lens) if n not in ends]
+    rows = torch.cat([torch.arange(start[b], start[b + 1]) for b in keep]).cuda()
+    y, S = la.decay_prefill_varlen(q, k, v, decay, cu, S0=S0, scale=0.25)
+    assert la.last_device_status() == 0 and torch.isfinite(y[rows]).all() and torch.isfinite(S).all()
+    spoilt = torch.ones(total, dtype=torch.bool, device="cuda")
+    spoilt[rows] = False
+    for t in (q, k, v):
+        t[spoilt] = bad
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(24):
+        if i % 2:
+            flush.fill_(i)
+        y2, S2 = la.decay_prefill_varlen(q, k, v, decay, cu, S0=S0, scale=0.25)
+        assert torch.equal(y[rows], y2[rows]) and torch.equal(S[keep], S2[keep]), i
+    # one sequence alone, nothing but padding behind it
+    for n in (129, 130, 200, 255, 257, 300, 385, 1000):
+        one = [torch.randn((n + 128, H, d), generator=torch.Generator().manual_seed(n + d)).bfloat16().cuda() for d in (r, r, dv)]
+        cu1 = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        y, S = la.decay_prefill_varlen(*one, decay, cu1, scale=0.25)
+        for t in one:
+            t[n:] = bad
+        for i in range(6):
+            if i % 2:
+                flush.fill_(i)
+            y2, S2 = la.decay_prefill_varlen(*one, decay, cu1, scale=0.25)
+            assert torch.equal(y[:n], y2[:n]) and torch.equal(S, S2) and torch.isfinite(y2[:n]).all(), (n, i)
+    assert la.last_device_status() == 0
