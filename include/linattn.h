@@ -492,7 +492,8 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  *     scores[b,k] + logits[b,k,v] - log sum_u exp logits[b,k,u]
  * and the K best, best first, become the request's beams; equal scores go to the lower
  * k * V + v.  (Within one beam candidates rank by their logits.)  Scores are compared in 64
- * bits, the log-sum-exp carrying the error of its FP32 exponentials.
+ * bits, the log-sum-exp carrying the error of its FP32 exponentials; a row's largest logit is taken off
+ * first, so that rows of one huge value (masks of the type's lowest) keep their log-probabilities.
  *   logits      device [B,K,V] dtype, row (b, k) at element (b K + k) row_stride
  *   scores      device FP32 [B,K] cumulative log-probabilities
  *   done        device uint8 [B,K], non-zero: beam k has ended; its one candidate is token

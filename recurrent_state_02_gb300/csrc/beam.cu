@@ -37,9 +37,11 @@ struct SelSmem {
     float m[kSelWarps], s[kSelWarps];                     // running maximum and sum of its part
     int count[kSelWarps];                                 // keys in its buffer
     unsigned long long bound[kMaxBeams];                  // a K-th key of some part of a row, which all its warps share
-    // CTA 0 only: the rows' best and their lse
+    // CTA 0 only: the rows' best, and their lse as a maximum and the logarithm of the sum next to it (a maximum of
+    // 1e17 or more, a mask of the type's lowest value for one, would swallow the logarithm)
     unsigned long long row_keys[kMaxBeams][kMaxBeams];
-    double row_lse[kMaxBeams];
+    float row_max[kMaxBeams];
+    double row_log[kMaxBeams];
 };
 
 // Order-preserving map of a float (not NaN) to unsigned; -0 counts as +0.
@@ -357,7 +359,7 @@ beam_select_kernel(const BeamSelectArgs args)
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) home->row_lse[k] = (double)mx + log(sum);
+        if (lane == 0) home->row_max[k] = mx, home->row_log[k] = log(sum);
         // the parts' keys, at most 16 CS + K of them, and K rounds of taking the largest
         constexpr int N = (kSelWarps * 8 + kMaxBeams) / 32;
         unsigned long long k5[N];
@@ -383,8 +385,8 @@ beam_select_kernel(const BeamSelectArgs args)
     // phase 3: lane k holds the head of row k; K rounds of taking the best score
     const int k = lane;
     const double score = score_f;
-    const double lse = k < K ? sm.row_lse[k] : 0.0;
-    const bool usable = k < K && isfinite(score) && (ended || isfinite(lse));
+    const double mx = k < K ? sm.row_max[k] : 0.0, lg = k < K ? sm.row_log[k] : 0.0;
+    const bool usable = k < K && isfinite(score) && (ended || (isfinite(mx) && isfinite(lg)));
     int pos = 0;
     double cand = 0.0;
     int token = 0;
@@ -398,7 +400,7 @@ beam_select_kernel(const BeamSelectArgs args)
         }
         const unsigned long long key = sm.row_keys[k][pos];
         if (!key) return;
-        cand = score + (double)key_value(key) - lse;
+        cand = score + (((double)key_value(key) - mx) - lg);
         token = key_index(key);
         ord = order_f64(cand);
     };

@@ -282,3 +282,26 @@ def test_beam_search(la, kind):
     # FP32 throughout: logits are sums of H d products of size about 1, each carrying about 1e-5
     assert ((total - scores.double()).abs() <= steps * 1e-3).all()
     assert (scores[:, :-1] >= scores[:, 1:]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("level", ["low", "high", -1e30, 1e25, 1e9])
+def test_select_rows_of_huge_logits(la, level, dtype):
+    """Rows whose logits all lie near one huge value, masks of the type's lowest among them: their log-probabilities are
+    those of the differences, log(1 / V) for a constant row, and do not vanish next to the value.  (Bound: the
+    module's; the differences here are 0 or beyond the exponential's range.)"""
+    B, K, V = 2, 3, 611
+    level = {"low": torch.finfo(dtype).min, "high": torch.finfo(dtype).max}.get(level, level)
+    x, scores = make(B, K, V, dtype, 71)
+    x[0, 1] = level                            # one beam of three
+    x[1] = level                               # every beam
+    scores[0, 1] = scores[0].max() + 6.0       # log 611 = 6.4: near the other beams' best
+    scores[1] = torch.tensor([-3.0, -1.0, -1.0], device="cuda")
+    next_scores, parents, tokens, _ = la.beam_select(x, scores)
+    lp = torch.log_softmax(x.double().cpu(), 2)
+    cand = (scores.double().cpu()[..., None] + lp).reshape(B, -1)
+    best = torch.sort(cand, dim=1, descending=True, stable=True)
+    assert torch.equal(parents.cpu().long() * V + tokens.cpu(), best.indices[:, :K])
+    want = best.values[:, :K]
+    assert ((next_scores.double().cpu() - want).abs() <= 80 * R.U32 + R.U32 * want.abs()).all()
+    assert parents[1].tolist() == [1, 1, 1] and tokens[1].tolist() == [0, 1, 2]
