@@ -2,6 +2,7 @@
 // K of a request's K beams x V tokens, and move the beams' states after the choice.
 
 #include "decay.h"
+#include "launch_rules.h"
 #include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -95,9 +96,9 @@ __device__ __forceinline__ uint4 ld_once(const uint4 *p)
     return v;
 }
 
-// A lane's granule of rows that do not all start on 16-byte boundaries: elements i, i + 32, .. of the row (0 past
-// its end), one load each, packed like the 16 bytes of an aligned one.
-template <bool BF16>
+// A lane's granule by single elements i, i + ES, .. of the row (0 past its end), packed like the 16 bytes of a whole
+// one: of rows that do not all start on 16-byte boundaries (ES = 32), or what is left of an aligned row (ES = 1).
+template <bool BF16, int ES>
 __device__ __forceinline__ uint4 load_elements(const void *row, int i, int V)
 {
     constexpr int GE = BF16 ? 8 : 4;
@@ -105,8 +106,8 @@ __device__ __forceinline__ uint4 load_elements(const void *row, int i, int V)
 #pragma unroll
     for (int e = 0; e < GE; ++e) {
         x[e] = 0;
-        if (i + 32 * e < V)
-            x[e] = BF16 ? reinterpret_cast<const uint16_t *>(row)[i + 32 * e] : reinterpret_cast<const uint32_t *>(row)[i + 32 * e];
+        if (i + ES * e < V)
+            x[e] = BF16 ? reinterpret_cast<const uint16_t *>(row)[i + ES * e] : reinterpret_cast<const uint32_t *>(row)[i + ES * e];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = BF16 ? x[2 * j] | x[2 * j + 1] << 16 : x[j];
@@ -140,7 +141,9 @@ __device__ __forceinline__ float ex2(float x)
 
 // ALIGNED: every row starts on a 16-byte boundary, and a lane's granule is 16 bytes of it; else it is elements 32 apart.
 // (Which element goes to which lane depends on its index alone, so equal rows have equal sums.)
-template <bool BF16, bool ALIGNED>
+// REST: a granule may be left over at the end of an aligned row (an instance of its own, as even an untaken branch costs
+// the loop registers: B64 K4 V131072 30.4 us with it, 29.8 without).
+template <bool BF16, bool ALIGNED, bool REST>
 __global__ void __launch_bounds__(kSelThreads, 2)
 beam_select_kernel(const BeamSelectArgs args)
 {
@@ -170,6 +173,7 @@ beam_select_kernel(const BeamSelectArgs args)
         const unsigned char *row = reinterpret_cast<const unsigned char *>(args.logits) +
                                    ((long long)b * K + k) * args.row_stride * (BF16 ? 2 : 4);
         const int granules = ALIGNED ? (V + GE - 1) / GE : (V + 32 * GE - 1) / (32 * GE) * 32;
+        const int whole = REST ? whole_granules(V, GE) : granules;
         float m = -3.402823466e38f, s = 0.f;
         unsigned long long thr = 0;      // what a key has to beat
         float thr_x = -INFINITY;         // its logit
@@ -250,9 +254,21 @@ beam_select_kernel(const BeamSelectArgs args)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     raw[u] = make_uint4(0, 0, 0, 0);
-                    if (g + u * step < granules)
+                    if (g + u * step < whole)
                         raw[u] = ALIGNED ? ld_once(reinterpret_cast<const uint4 *>(row) + (g + u * step))
-                                         : load_elements<BF16>(row, first(g + u * step), V);
+                                         : load_elements<BF16, ES>(row, first(g + u * step), V);
+                }
+                if (REST && base + 31 + (U - 1) * step >= whole) {
+                    // (the last step of the warps that reach the end; one lane of one of them has the rest of the row)
+                    bool mine = false;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) mine = mine || g + u * step == whole;
+                    if (mine) {
+                        const uint4 rest = load_elements<BF16, 1>(row, whole * GE, V);
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (g + u * step == whole) raw[u] = rest;
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -506,11 +522,16 @@ cudaError_t launch_beam_select(const BeamSelectArgs &a, int B, bool bf16, int sm
     cfg.numAttrs = 1;
     const int el = bf16 ? 2 : 4;
     const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.row_stride * el % 16 == 0;
+    auto run = [&](auto kern) { return cudaLaunchKernelEx(&cfg, kern, a); };
+    const int ge = 16 / el;
+    const bool rest = whole_granules(a.V, ge) * ge < a.V;
     if (bf16)
-        return aligned ? cudaLaunchKernelEx(&cfg, beam_select_kernel<true, true>, a)
-                       : cudaLaunchKernelEx(&cfg, beam_select_kernel<true, false>, a);
-    return aligned ? cudaLaunchKernelEx(&cfg, beam_select_kernel<false, true>, a)
-                   : cudaLaunchKernelEx(&cfg, beam_select_kernel<false, false>, a);
+        return !aligned ? run(beam_select_kernel<true, false, false>)
+               : rest   ? run(beam_select_kernel<true, true, true>)
+                        : run(beam_select_kernel<true, true, false>);
+    return !aligned ? run(beam_select_kernel<false, false, false>)
+           : rest   ? run(beam_select_kernel<false, true, true>)
+                    : run(beam_select_kernel<false, true, false>);
 }
 
 cudaError_t launch_state_reorder(const float *S, const float *z, const int *parents, int B, int K, long long s_len,

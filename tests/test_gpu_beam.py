@@ -305,3 +305,20 @@ def test_select_rows_of_huge_logits(la, level, dtype):
     want = best.values[:, :K]
     assert ((next_scores.double().cpu() - want).abs() <= 80 * R.U32 + R.U32 * want.abs()).all()
     assert parents[1].tolist() == [1, 1, 1] and tokens[1].tolist() == [0, 1, 2]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("V", [1, 3, 7, 8, 9, 250, 2049, 2050, 2051, 2052, 2053, 2054, 2055, 2056, 40961])
+def test_select_rows_that_end_inside_a_granule(la, V, dtype):
+    """Rows that start on 16-byte boundaries and end anywhere, the last one with the buffer: the padding between them would
+    win, and the best tokens are a row's last ones."""
+    B, K = 2, 3
+    ld = (V + 8) // 8 * 8
+    buf = torch.full(((B * K - 1) * ld + V,), 99.0, device="cuda", dtype=dtype)
+    rows = buf.as_strided((B, K, V), (K * ld, ld, 1))
+    x, scores = make(B, K, V, dtype, 80 + V)
+    x[..., -3:] += 9.0
+    rows.copy_(x)
+    got = check(la, rows, scores)
+    want = la.beam_select(x, scores)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])

@@ -1,0 +1,27 @@
+"""Sizes and choices behind the launches (csrc/launch_rules.h), compiled for the host: what a kernel
+reads stays in its arrays, and what is chosen is what the device can run."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "recurrent_state_02_gb300", "csrc")
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    d = tmp_path_factory.mktemp("rules")
+    src, lib = d / "rules.cpp", d / "rules.so"
+    src.write_text('#include "launch_rules.h"\n'
+                   'extern "C" int whole_granules(int V, int ge) { return la::whole_granules(V, ge); }\n')
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)], check=True)
+    return ctypes.CDLL(str(lib))
+
+
+@pytest.mark.parametrize("ge", [4, 8])
+def test_granules_end_inside_the_row(rules, ge):
+    """The 16-byte loads of an aligned row cover no element past its end, and leave less than a granule."""
+    for V in [*range(1, 70), 1501, 32003, 131071, 131072, (1 << 30) - 1, 1 << 30]:
+        n = rules.whole_granules(V, ge)
+        assert n * ge <= V < (n + 1) * ge, V
