@@ -376,24 +376,24 @@ beam_select_kernel(const BeamSelectArgs args)
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) home->row_max[k] = mx, home->row_log[k] = log(sum);
-        // the parts' keys, at most 16 CS + K of them, and K rounds of taking the largest
-        constexpr int N = (kSelWarps * 8 + kMaxBeams) / 32;
-        unsigned long long k5[N];
+        // the parts' keys, at most 16 CS of them, and K rounds of taking the largest
+        constexpr int N = kSelWarps * 8 / 32;
+        unsigned long long kp[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int i = lane + 32 * u, gw = k + i / K * K;
-            k5[u] = i < parts * K ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][i % K] : 0;
+            kp[u] = i < parts * K ? in_cta(&sm, gw / kSelWarps)->keys[gw % kSelWarps][i % K] : 0;
         }
 #pragma unroll 1
         for (int r = 0; r < K; ++r) {
-            unsigned long long best = k5[0];
+            unsigned long long best = kp[0];
 #pragma unroll
-            for (int u = 1; u < N; ++u) best = k5[u] > best ? k5[u] : best;
+            for (int u = 1; u < N; ++u) best = kp[u] > best ? kp[u] : best;
             best = warp_max(best);
             if (lane == r) home->row_keys[k][r] = best;
 #pragma unroll
             for (int u = 0; u < N; ++u)
-                if (k5[u] == best) k5[u] = 0;
+                if (kp[u] == best) kp[u] = 0;
         }
     }
     cluster_sync_all();
