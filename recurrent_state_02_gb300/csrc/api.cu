@@ -956,6 +956,7 @@ la_status la_decay_prefill(const void *q, const void *k, const void *v, la_dtype
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     la::DecayArgs a;
     a.decay = decay;
+    a.sms = sm_count();
     a.H = H;
     a.T = T;
     a.status = status_word();
@@ -978,6 +979,7 @@ la_status la_decay_prefill_varlen(const void *q, const void *k, const void *v, l
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     la::DecayArgs a;
     a.decay = decay;
+    a.sms = sm_count();
     a.cu_seqlens = cu_seqlens;
     a.H = H;
     a.T = total_T;
@@ -1000,6 +1002,7 @@ la_status la_decay_decode_step(const void *q, const void *k, const void *v, la_d
         return from_cuda(la::launch_decay_decode(q, k, v, dtype == LA_DTYPE_BF16, decay, S, B, H, r, dv, scale, y, st));
     la::DecayArgs a;
     a.decay = decay;
+    a.sms = sm_count();
     a.H = H;
     a.T = 1;
     const la::DecaySweep sw = forward_sweep(q, k, v, S, r, dv, scale, y, S);
@@ -1037,6 +1040,7 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     la::DecayArgs a;
     a.decay = decay;
+    a.sms = sm_count();
     a.H = H;
     a.T = T;
     a.status = status_word();

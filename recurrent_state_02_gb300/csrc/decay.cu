@@ -6,6 +6,7 @@
 // There is no feature map and no normaliser; g is a constant of the head.
 
 #include "decay.h"
+#include "launch_rules.h"
 #include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -58,8 +59,12 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
 // The columns per lane set how a token's time divides.  Loads that a whole warp shares still take shared
 // memory about two cycles each, so few columns per lane load it; many make a token's chain of instructions
 // long.  One CTA per SM at most (us, FP32, T = 1001): r = 64 82 with CPL = 1, 104 with 2, 203 with 4; r = 128 156, 129,
-// 157.  More CTAs: 512 of r = 64 (T = 1000) 239 with 2, 277 with 4; 256 of r = 128 233 and 249; 4096 of r = 128
-// and 8 tokens (BF16), where the state's traffic counts, 52 and 44.
+// 157.  More CTAs, up to 64 rows: 2 (4 in brackets), us: 512 of r = 64 (T = 1000) 239 (277), 4096 of r = 64 and 16 tokens
+// 37 (41), 48 packed FP32 prompts of 128 .. 2048 tokens (H = 16, r = dv = 64) 575 (760), 1000 packed BF16 requests of
+// 12 tokens 402 (463); only 1024 CTAs of r = 32 lose, 22 (20) at 64 tokens.  More rows: 256 CTAs of r = 128 (T = 1000) 233
+// (249), but brief ones, where the state's traffic counts, take 4: 4096 of r = 128 and 8 tokens (BF16) 54 (45), the 48
+// prompts at r = dv = 128 1620 (1406), 1000 requests of 12 tokens at r = 256 2380 (1647); one prompt of 2048 tokens among
+// 255 of 8 at r = 128 loses, 348 (383).
 // Tokens are staged in blocks; the next block's values are fetched into registers while this
 // one is computed.
 //
@@ -68,7 +73,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
 // from zero (the first one from S_init, with its outputs), exchange the sums over distributed shared
 // memory, S <- g^seg S + sum over the segments before, and pass their tokens again with outputs.
 constexpr int kRecCols = 32, kRecRows = 32;
-constexpr long long kRecFew = 152;   // CTAs
 constexpr int kRecShort = 64;        // tokens
 
 template <int W, int CPL>
@@ -357,17 +361,18 @@ int rec_segments(long long units, int rows, int T)
 template <bool BF16>
 cudaError_t launch_rec(const RecArgs &r, int rows, dim3 grid, cudaStream_t stream)
 {
-    const bool few = (long long)grid.x * grid.y * grid.z <= kRecFew, brief = r.d.cu_seqlens || r.d.T <= kRecShort;
     if (r.nseg > 1) {
         if (rows <= 32) return launch_rec_w<BF16, 1, 1, true>(r, grid, stream);
         if (rows <= 64) return launch_rec_w<BF16, 2, 1, true>(r, grid, stream);
         if (rows <= 128) return launch_rec_w<BF16, 4, 2, true>(r, grid, stream);
         return launch_rec_w<BF16, 8, 2, true>(r, grid, stream);
     }
-    if (rows <= 32) return few ? launch_rec_w<BF16, 1, 1>(r, grid, stream) : brief ? launch_rec_w<BF16, 1, 4>(r, grid, stream) : launch_rec_w<BF16, 1, 2>(r, grid, stream);
-    if (rows <= 64) return few ? launch_rec_w<BF16, 2, 1>(r, grid, stream) : brief ? launch_rec_w<BF16, 2, 4>(r, grid, stream) : launch_rec_w<BF16, 2, 2>(r, grid, stream);
-    if (rows <= 128) return !few && brief ? launch_rec_w<BF16, 4, 4>(r, grid, stream) : launch_rec_w<BF16, 4, 2>(r, grid, stream);
-    return !few && brief ? launch_rec_w<BF16, 8, 4>(r, grid, stream) : launch_rec_w<BF16, 8, 2>(r, grid, stream);
+    const bool brief = r.d.cu_seqlens || r.d.T <= kRecShort;
+    const int columns = rec_columns(rows, (long long)grid.x * grid.y * grid.z, brief, r.d.sms);
+    if (rows <= 32) return columns == 1 ? launch_rec_w<BF16, 1, 1>(r, grid, stream) : launch_rec_w<BF16, 1, 2>(r, grid, stream);
+    if (rows <= 64) return columns == 1 ? launch_rec_w<BF16, 2, 1>(r, grid, stream) : launch_rec_w<BF16, 2, 2>(r, grid, stream);
+    if (rows <= 128) return columns == 4 ? launch_rec_w<BF16, 4, 4>(r, grid, stream) : launch_rec_w<BF16, 4, 2>(r, grid, stream);
+    return columns == 4 ? launch_rec_w<BF16, 8, 4>(r, grid, stream) : launch_rec_w<BF16, 8, 2>(r, grid, stream);
 }
 
 // ------------------------------------------------------------ decode step

@@ -34,6 +34,7 @@ struct DecayArgs {
     int H = 0, T = 0;                        // T: tokens per sequence, or in all when packed
     int len_min = 0, len_max = 0x7fffffff;   // packed: the lengths this launch takes
     int *status = nullptr;
+    int sms = 0;                             // of the device
 };
 
 // The token recurrence in FP32 on CUDA cores, for any 1 <= ra, n <= 256 and either
