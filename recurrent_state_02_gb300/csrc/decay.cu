@@ -11,6 +11,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <type_traits>
 
 namespace la {
@@ -73,7 +74,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
 // from zero (the first one from S_init, with its outputs), exchange the sums over distributed shared
 // memory, S <- g^seg S + sum over the segments before, and pass their tokens again with outputs.
 constexpr int kRecCols = 32, kRecRows = 32;
-constexpr int kRecShort = 64;        // tokens
+constexpr int kRecShort = 64;         // tokens
 
 template <int W, int CPL>
 struct RecCfg {
@@ -307,17 +308,10 @@ template <bool BF16, int W, int CPL, bool SPLIT = false>
 cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
 {
     using C = RecCfg<W, CPL>;
-    static OncePerDevice once;
-    cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL, SPLIT>, C::kSmem, once);
-    if (e != cudaSuccess) return e;
-    if (SPLIT && r.nseg > 8) {
-        static OncePerDevice wide;   // clusters of more than 8
-        const int dev = current_device_index();
-        if (!wide.done[dev].load(std::memory_order_acquire)) {
-            e = cudaFuncSetAttribute(decay_rec_kernel<BF16, W, CPL, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            wide.done[dev].store(true, std::memory_order_release);
-        }
+    if (!SPLIT) {    // (rec_room has set the attributes of a split instance)
+        static OncePerDevice once;
+        const cudaError_t e = set_smem_once(decay_rec_kernel<BF16, W, CPL, SPLIT>, C::kSmem, once);
+        if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = SPLIT ? dim3(grid.x * r.nseg, grid.y, grid.z) : grid;
@@ -334,45 +328,86 @@ cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, decay_rec_kernel<BF16, W, CPL, SPLIT>, r);
 }
 
-// Segments of a sequence of T tokens whose sweeps have `units` CTAs.  Every segment but the
-// first and the last is passed twice at the same cost per token, so that n of them take
-// 2 / n of the time if each of their CTAs has an SM (with many tokens and up to 128
-// rows: half of one).  A cluster lies in one GPC, of 16 SMs or more, so 8 (16 / n) clusters
-// find an SM per CTA (24 of 5 do, 24 of 6 do not).  FP32, us whole and in n segments:
-//   T = 1001  r = 64   24 CTAs 80 and 40 (8); 48 CTAs 80 and 60 (5); 76 CTAs 80 and 91 (7, the best: stays whole)
-//             r = 128  32 CTAs 126 and 63 (8); 64 CTAs 126 and 105 (4)
-//             r = 256  32 CTAs 230 and 119 (4), 203 (8)
-//   T = 128   r = 64   24 CTAs 12.8 and 10.1 (5), 12.9 (8);  T = 64 7.8 and 8.3 (5)
-// Clusters of more than 8 have to be asked for, and fewer GPCs have room for them: T = 16384
-// r = 64, 4 CTAs 1258 whole, 332 (8), 225 (12), 172 (16); 8 CTAs 1271, 337 (8), 228 (12), 276 (16).
-// 14 clusters of 8 still find an SM per CTA (r = 96, T = 1001: 41, two CTAs per SM in clusters of 12 48), 16 do not (r = 128:
-// 58 and 49).
-int rec_segments(long long units, int rows, int T)
+// Clusters of 2 .. kMaxRecSegments CTAs of a split instance that the device places at once with one CTA per SM, and with two.
+// Asked of the driver once per device, as it depends on the GPCs that the device (or a partition of it) has; what the
+// driver cannot answer counts as no room.  (152 SMs: 15 clusters of 8 with an SM per CTA, 8 of 12, 7 of 16.)
+struct RecRoom {
+    int one[kMaxRecSegments + 1], two[kMaxRecSegments + 1];
+};
+
+template <bool BF16, int W, int CPL>
+RecRoom rec_room()
 {
-    if (T < 2 * kRecShort) return 1;
-    const bool share = T >= 512 && rows <= 128;
-    if (T >= 512 && units <= 4) return 16;
-    if (T >= 512 && (units <= 8 || (share && units > 14 && units <= 16))) return 12;
-    for (int n = 8; n >= (share ? 4 : 3); --n)
-        if (units <= 8 * ((share ? 32 : 16) / n)) return n;
-    return 1;
+    static std::atomic<int> one[kMaxDevices][kMaxRecSegments + 1], two[kMaxDevices][kMaxRecSegments + 1];
+    static OncePerDevice once;
+    RecRoom room = {};
+    const int dev = current_device_index();
+    if (dev < 0) return room;
+    if (!once.done[dev].load(std::memory_order_acquire)) {
+        // shared memory that leaves an SM room for one CTA, or for two
+        constexpr int kOne = 120 * 1024, kTwo = 80 * 1024;
+        static_assert(RecCfg<W, CPL>::kSmem <= kTwo, "an SM holds two CTAs");
+        auto kern = decay_rec_kernel<BF16, W, CPL, true>;
+        auto works = [](cudaError_t e) {
+            if (e != cudaSuccess) cudaGetLastError();    // (an answer of no is not an error of the caller's)
+            return e == cudaSuccess;
+        };
+        if (works(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kOne)) &&
+            works(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))) {
+            for (int n = 2; n <= kMaxRecSegments; ++n) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(n, 1, 1);
+                cfg.blockDim = dim3(RecCfg<W, CPL>::kThreads, 1, 1);
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = n;
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                auto clusters = [&](int smem) {
+                    cfg.dynamicSmemBytes = smem;
+                    int k = 0;
+                    return works(cudaOccupancyMaxActiveClusters(&k, kern, &cfg)) ? k : 0;
+                };
+                one[dev][n].store(clusters(kOne), std::memory_order_relaxed);
+                two[dev][n].store(clusters(kTwo), std::memory_order_relaxed);
+            }
+        }
+        once.done[dev].store(true, std::memory_order_release);
+    }
+    for (int n = 2; n <= kMaxRecSegments; ++n) {
+        room.one[n] = one[dev][n].load(std::memory_order_relaxed);
+        room.two[n] = two[dev][n].load(std::memory_order_relaxed);
+    }
+    return room;
+}
+
+template <bool BF16, int W, int FEW, int MANY>
+cudaError_t launch_rec_rows(RecArgs r, int rows, dim3 grid, cudaStream_t stream)
+{
+    const long long ctas = (long long)grid.x * grid.y * grid.z;
+    if (!r.d.cu_seqlens && r.d.T >= kMinRecSplit) {
+        const RecRoom room = rec_room<BF16, W, FEW>();
+        const int want = rec_segments(ctas, rows, r.d.T, room.one, room.two);
+        if (want > 1) {
+            r.seg = (r.d.T + want - 1) / want;
+            r.nseg = (r.d.T + r.seg - 1) / r.seg;
+            return launch_rec_w<BF16, W, FEW, true>(r, grid, stream);
+        }
+    }
+    const bool brief = r.d.cu_seqlens || r.d.T <= kRecShort;
+    return rec_columns(rows, ctas, brief, r.d.sms) == FEW ? launch_rec_w<BF16, W, FEW>(r, grid, stream)
+                                                          : launch_rec_w<BF16, W, MANY>(r, grid, stream);
 }
 
 template <bool BF16>
 cudaError_t launch_rec(const RecArgs &r, int rows, dim3 grid, cudaStream_t stream)
 {
-    if (r.nseg > 1) {
-        if (rows <= 32) return launch_rec_w<BF16, 1, 1, true>(r, grid, stream);
-        if (rows <= 64) return launch_rec_w<BF16, 2, 1, true>(r, grid, stream);
-        if (rows <= 128) return launch_rec_w<BF16, 4, 2, true>(r, grid, stream);
-        return launch_rec_w<BF16, 8, 2, true>(r, grid, stream);
-    }
-    const bool brief = r.d.cu_seqlens || r.d.T <= kRecShort;
-    const int columns = rec_columns(rows, (long long)grid.x * grid.y * grid.z, brief, r.d.sms);
-    if (rows <= 32) return columns == 1 ? launch_rec_w<BF16, 1, 1>(r, grid, stream) : launch_rec_w<BF16, 1, 2>(r, grid, stream);
-    if (rows <= 64) return columns == 1 ? launch_rec_w<BF16, 2, 1>(r, grid, stream) : launch_rec_w<BF16, 2, 2>(r, grid, stream);
-    if (rows <= 128) return columns == 4 ? launch_rec_w<BF16, 4, 4>(r, grid, stream) : launch_rec_w<BF16, 4, 2>(r, grid, stream);
-    return columns == 4 ? launch_rec_w<BF16, 8, 4>(r, grid, stream) : launch_rec_w<BF16, 8, 2>(r, grid, stream);
+    if (rows <= 32) return launch_rec_rows<BF16, 1, 1, 2>(r, rows, grid, stream);
+    if (rows <= 64) return launch_rec_rows<BF16, 2, 1, 2>(r, rows, grid, stream);
+    if (rows <= 128) return launch_rec_rows<BF16, 4, 2, 4>(r, rows, grid, stream);
+    return launch_rec_rows<BF16, 8, 2, 4>(r, rows, grid, stream);
 }
 
 // ------------------------------------------------------------ decode step
@@ -483,10 +518,6 @@ cudaError_t launch_decay_rec(const DecaySweep *sweeps, int count, const DecayArg
     }
     const dim3 grid(tiles, a.H, B);
     r.nseg = 1, r.seg = a.T;
-    if (const int want = a.cu_seqlens ? 1 : rec_segments((long long)tiles * a.H * B, rows, a.T); want > 1) {
-        r.seg = (a.T + want - 1) / want;
-        r.nseg = (a.T + r.seg - 1) / r.seg;
-    }
     return bf16 ? launch_rec<true>(r, rows, grid, stream) : launch_rec<false>(r, rows, grid, stream);
 }
 
