@@ -322,3 +322,29 @@ def test_select_rows_that_end_inside_a_granule(la, V, dtype):
     got = check(la, rows, scores)
     want = la.beam_select(x, scores)
     assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_select_many_beams_over_a_large_vocabulary(la, dtype):
+    """32 beams whose candidates fill every warp's buffer again and again: ascending rows, where each block beats the
+    last, rows of few distinct values, and random ones."""
+    B, K, V = 2, 32, 32768
+    x, scores = make(B, K, V, dtype, 90)
+    scores[:] = -5.0 - torch.arange(K, device="cuda") * 0.25
+    up = torch.arange(V, device="cuda").float() / 64        # BF16: runs of equal values
+    x[0, ::2] = up.to(dtype)
+    x[1, 1::2] = (torch.arange(V, device="cuda") % 5).to(dtype)
+    got = la.beam_select(x, scores)
+    cand = (scores.double()[..., None] + torch.log_softmax(x.double(), 2)).reshape(B, -1)
+    # 64-bit scores of equal candidates differ in their last bits by the row: the choice is compared by score
+    best = torch.sort(cand, dim=1, descending=True).values[:, :K]
+    mine = cand.gather(1, got[1].long() * V + got[2].long())
+    assert ((mine - best).abs() <= 80 * R.U32).all()
+    assert ((got[0].double() - best).abs() <= 80 * R.U32 + R.U32 * best.abs()).all()
+    for b in range(B):
+        chosen = list(zip(got[1][b].tolist(), got[2][b].tolist()))
+        assert len(set(chosen)) == K
+        for k in range(K):      # within a beam: its best logits, equal ones by the lower token
+            mine_k = [t for p, t in chosen if p == k]
+            order = torch.sort(x[b, k].double(), descending=True, stable=True).indices[:len(mine_k)].tolist()
+            assert sorted(mine_k) == sorted(order)

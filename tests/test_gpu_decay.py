@@ -424,3 +424,24 @@ def test_packed_tail_is_isolated(la, r, dv, bad):
             y2, S2 = la.decay_prefill_varlen(*one, decay, cu1, scale=0.25)
             assert torch.equal(y[:n], y2[:n]) and torch.equal(S, S2) and torch.isfinite(y2[:n]).all(), (n, i)
     assert la.last_device_status() == 0
+
+
+def test_backward_workspace_of_the_callers(la):
+    """Gradients in segments over a workspace of the caller's: larger than asked for gives the same bits; one byte short, off
+    its 256-byte boundary or elsewhere is refused and leaves the outputs to the next call."""
+    size = (1, 2, 1500, 128, 128)
+    q, k, v, dy, decay, S0, dS_T = make(*size, torch.bfloat16, True, seed=23)
+    need = la.decay_backward_workspace_bytes(*size)
+    assert need > 0
+    want = la.decay_backward(q, k, v, dy, decay, S0=S0, dS_T=dS_T, scale=0.1)
+    buf = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")
+    got = la.decay_backward(q, k, v, dy, decay, S0=S0, dS_T=dS_T, scale=0.1, workspace=buf)
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and (buf[need:] == 255).all()
+    for ws in (buf[:need - 1], buf[16:16 + need], buf[128:]):
+        with pytest.raises(la.LinAttnError):
+            la.decay_backward(q, k, v, dy, decay, S0=S0, dS_T=dS_T, scale=0.1, workspace=ws)
+    with pytest.raises(ValueError):
+        la.decay_backward(q, k, v, dy, decay, S0=S0, dS_T=dS_T, scale=0.1, workspace=buf.cpu())
+    with pytest.raises(la.LinAttnError):
+        la.decay_prefill(q, k, v, decay, workspace=buf[16:])
+    assert la.last_device_status() == 0
