@@ -408,7 +408,8 @@ la_status la_delta_rule_chunked(const void *q, const void *k, const void *v, la_
  *   BF16, r in {64, 128}, dv a multiple of 64, token arrays 16-byte aligned, more than 16
  *         tokens: chunks of 128 tokens on the tensor cores.  The scores of a chunk and the state that enters
  *         it are rounded to BF16 once; the state itself is FP32, each write to it kept to 2^-16
- *         of its size.  Few heads run their sequences in segments, which needs the workspace.
+ *         of its size (passed as FP32, the same values take the recurrence below and are kept to 2^-24).
+ *         Few heads run their sequences in segments, which needs the workspace.
  *   else  the token recurrence in FP32 on CUDA cores, in segments side by side where few heads
  *         have 128 tokens or more and are not packed (for one token of la_decay_decode_step a
  *         kernel of its own, bound by the state's traffic, when dv is a multiple of 4 and

@@ -423,7 +423,10 @@ def decay_prefill_workspace_bytes(B, H, T, r, dv, dtype=torch.bfloat16, device=N
 def decay_prefill(q, k, v, decay, S0=None, scale=1.0, y=None, S_out=None, workspace=None):
     """Linear attention with a constant decay per head: S <- decay S + k v^T, y = scale S^T q.
     q, k [B,H,T,r], v [B,H,T,dv] (bf16 or fp32, same dtype); decay [H] fp32 in 0..1; S0
-    [B,H,r,dv] fp32 or None (zero).  Returns (y [B,H,T,dv] in the input dtype, S_T)."""
+    [B,H,r,dv] fp32 or None (zero).  Returns (y [B,H,T,dv] in the input dtype, S_T).
+    Prompts run on the tensor cores when they are bf16, r is 64 or 128, dv a multiple of 64 and
+    q, k, v, y start on 16-byte boundaries (a slice at an odd offset may not); everything else, and
+    fp32 for a state to fp32's own rounding, takes the token recurrence, several times slower."""
     B, H, T, r = q.shape
     dv = v.shape[3]
     dt, dev = _decay_inputs(q, k, v, decay, (B, H, T, r), (B, H, T, dv), H)

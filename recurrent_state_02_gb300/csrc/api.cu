@@ -837,8 +837,9 @@ bool tc_sweep(const la::DecaySweep &s, bool bf16)
 // How a sweep of T tokens over `units` CTAs (heads x 64-column tiles) is split: into nseg segments that run at
 // once, when all of them and all parts of the state pass fit the SMs, one CTA each.  Estimated times in
 // microseconds: a chunk costs 1.6 in the sweep and 0.8 in the state pass, a launch about 5 to 7 around them, and a
-// segment reads the parts before it at 0.5 each.  (B1 H32 T65536 755 us whole, 529 split; B1 H8 r = dv = 128: T = 4096
-// 57 and 31, T = 1024 18 whole, 24 in four segments.)
+// segment reads the parts before it at 0.5 each.  (B1 H32 T65536 755 us whole, 530 split; B1 H8, dv = 128, r = 128 and 64:
+// T = 4096 54 and 31, 53 and 28; T = 1024 stays whole, 18 and 17, where two segments take 23 and 20.  Within a tenth of the
+// best number of segments for both, from 2 to 64 CTAs and 256 to 16384 tokens.)
 struct DecaySplit {
     int nseg = 1, seg_chunks = 0, part_chunks = 0, nparts = 0;
 };

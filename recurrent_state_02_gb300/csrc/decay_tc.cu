@@ -18,7 +18,9 @@
 // The state is FP32 in the registers of four warps: after each chunk S <- g^n S + dS
 // (both halves), so that its rounding is that of one FP32 sum per chunk.  Two
 // BF16 parts of the weighted values keep the state to 2^-16 per term, where one
-// part would leave 2^-8; the outputs, which are BF16, take P and S rounded once.
+// part would leave 2^-8; the outputs, which are BF16, take P and S rounded once.  (A third part leaves
+// FP32's own rounding, but its tile takes the place of a quarter of a's buffers: 62.5 us at B4 H16 T4096
+// against 55.6.  The same prompt as FP32 takes the FP32 recurrence.)
 //
 // No power of g is ever divided by: a block of 32 x 32 scores below the diagonal carries
 // g^{p_i - p_j} as the product of a row's power and a column's power, both with
@@ -38,9 +40,9 @@
 // unrolled and long waits the same arithmetic took 238 us where it now takes 55.
 //
 // Bound by shared memory: counting one read of each operand per MMA, a chunk moves about
-// 400 KB through it (P 64, Ye 48, Yi 16, dS 64, loads 80, stores 16, the weighted values
-// 80, state and outputs 32), 3100 cycles at 128 bytes a cycle, or 1.6 us; at HBM's rate
-// it would be 1.3.  Measured at r = dv = 128: B4 H16 T4096 55 us (272 MB, 74 % of the copy
+// 370 KB through it (P 64, Ye 48, Yi 16, dS 64, loads 80, stores 16, the weighted values
+// 48, state and outputs 32), 2900 cycles at 128 bytes a cycle, or 1.5 us of the 1.6 that it takes; at
+// HBM's rate it would be 1.3.  Measured at r = dv = 128: B4 H16 T4096 55 us (272 MB, 74 % of the copy
 // bandwidth), B1 H32 T65536 in segments 529 us, the gradients' three sweeps of
 // B4 H16 T4096 162 us.
 #include "decay.h"
@@ -376,7 +378,7 @@ decay_tc_kernel(const __grid_constant__ DecayTcParams args)
         if (warp == 0 && lane == 0) {
             // --------------------------------------------------- producer
             for (int c = 1; c < nch && load_chunk(c); ++c) {}
-            // every issued load lands before the CTA may exit (the last six, in order)
+            // every issued load lands before the CTA may exit (those of the last three chunks, in order)
             for (int i = max(0, loaded - 9); i < loaded; ++i) {
                 const int c = i / 3, k = i % 3;
                 if (STATE && k == 1) continue;
