@@ -19,8 +19,8 @@
 // (both halves), so that its rounding is that of one FP32 sum per chunk.  Two
 // BF16 parts of the weighted values keep the state to 2^-16 per term, where one
 // part would leave 2^-8; the outputs, which are BF16, take P and S rounded once.  (A third part leaves
-// FP32's own rounding, but its tile takes the place of a quarter of a's buffers: 62.5 us at B4 H16 T4096
-// against 55.6.  The same prompt as FP32 takes the FP32 recurrence.)
+// FP32's own rounding, 1.7e-7 of the state's norm in place of 2.4e-6, but its tile takes the place of a quarter
+// of a's buffers: 62.5 us at B4 H16 T4096 against 55.6.  The same prompt as FP32 takes the FP32 recurrence.)
 //
 // No power of g is ever divided by: a block of 32 x 32 scores below the diagonal carries
 // g^{p_i - p_j} as the product of a row's power and a column's power, both with
