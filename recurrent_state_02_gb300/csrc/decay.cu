@@ -329,8 +329,8 @@ cudaError_t launch_rec_w(const RecArgs &r, dim3 grid, cudaStream_t stream)
 }
 
 // Clusters of 2 .. kMaxRecSegments CTAs of a split instance that the device places at once with one CTA per SM, and with two.
-// Asked of the driver once per device, as it depends on the GPCs that the device (or a partition of it) has; what the
-// driver cannot answer counts as no room.  (152 SMs: 15 clusters of 8 with an SM per CTA, 8 of 12, 7 of 16.)
+// Asked of the CUDA driver once per device, as it depends on the GPCs that the device (or a partition of it) has; what the
+// CUDA driver cannot answer counts as no room.  (152 SMs: 15 clusters of 8 with an SM per CTA, 8 of 12, 7 of 16.)
 struct RecRoom {
     int one[kMaxRecSegments + 1], two[kMaxRecSegments + 1];
 };
