@@ -488,6 +488,98 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
                             size_t workspace_bytes, la_stream_t stream);
 
 /*
+ * The gated delta rule: the delta-rule memory of la_delta_rule with a gate per token and head, as
+ * la_prefill_chunked's ([LA] "Delta rule：先读旧答案，再写误差" and "加一个门：让旧记忆逐渐淡出"):
+ *     S' = alpha_t S_{t-1},  S_t = S' + beta_t k_t (v_t - S'^T k_t)^T,  y_t = scale S_t^T q_t
+ * The memory fades, reads its answer for the key, writes beta times the error back and is then read by
+ * the query.  q and k are used as given (models bring them to length one; the update contracts for
+ * 0 <= beta |k|^2 <= 2).
+ * Shared heads: q and k have Hk heads, v, the gates and the state H, a multiple of Hk; value head h reads key
+ * head h / (H / Hk), and the gradients of a key head are summed over its value heads.
+ *   alpha  device FP32, 0 <= alpha <= 1, or NULL (1)      beta  device FP32 write strength, or NULL (1)
+ *   scale  any finite value, typically 1/sqrt(r)
+ * Inputs are finite; a row with an infinity or NaN may spoil its whole chunk of 64 tokens as well as all later ones.
+ * Outputs overlap neither inputs nor one another, but for the states where it says so.
+ * Kernels:
+ *   the token recurrence in FP32 on CUDA cores (for one token of la_gated_delta_decode_step a kernel of its
+ *   own, bound by the state's traffic, when dv is a multiple of 4 and S 16-byte aligned).
+ * The first call of each kind on a device sets kernel attributes: make it before any stream capture.
+ * Requires 1 <= r, dv <= 256, B, H <= 65535, T <= 2^30; BF16 arrays 2-byte, FP32 and int32 arrays 4-byte
+ * aligned, workspaces 256-byte.
+ * Errors of every entry point: LA_ERR_NULL, LA_ERR_SHAPE (B, H, Hk, r, dv < 1, T < 0, H not a multiple of Hk,
+ * scale not finite), LA_ERR_DTYPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (other sizes), LA_ERR_WORKSPACE, LA_ERR_CUDA.
+ */
+
+/*
+ * la_gated_delta_prefill -- T tokens of every (b, h) sequence from S0.
+ *   q, k   device [B,Hk,T,r] dtype         v, y   device [B,H,T,dv] dtype
+ *   alpha, beta  device FP32 [B,H,T] or NULL
+ *   S0     device FP32 [B,H,r,dv] or NULL (zero); may equal S_out (in place)
+ *   S_out  device FP32 [B,H,r,dv] final state
+ *   workspace  device scratch of la_gated_delta_prefill_workspace_bytes(...) bytes, owned by the caller; may be
+ *              NULL when that is 0.  Calls sharing one workspace must be ordered.
+ * T may be 0 (S_out = S0; q, k, v, y may then be NULL).
+ */
+size_t la_gated_delta_prefill_workspace_bytes(int B, int H, int Hk, int T, int r, int dv, la_dtype dtype);
+la_status la_gated_delta_prefill(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                 const float *beta, const float *S0, int B, int H, int Hk, int T, int r, int dv,
+                                 float scale, void *y, float *S_out, void *workspace, size_t workspace_bytes,
+                                 la_stream_t stream);
+
+/*
+ * la_gated_delta_prefill_varlen -- the same for sequences of different lengths packed one after
+ * another: sequence b is tokens cu_seqlens[b] .. cu_seqlens[b+1]-1, from S0[b] into
+ * S_out[b] (an empty sequence copies its state).
+ *   q, k         device [total_T, Hk, r] dtype (token-major)     v, y  device [total_T, H, dv]
+ *   alpha, beta  device FP32 [total_T, H] or NULL
+ *   S0, S_out    device FP32 [B,H,r,dv]; S0 NULL (zero) or equal to S_out (in place) or apart
+ *   cu_seqlens   device int32 [B + 1], 0 <= cu_seqlens[0] <= .. <= cu_seqlens[B] <= total_T.  A
+ *                sequence outside [0, total_T] or of negative length is skipped and
+ *                recorded as LA_ERR_SHAPE in the device status word.
+ *   workspace    la_gated_delta_prefill_varlen_workspace_bytes(...) bytes, as above
+ * Rows of y outside every sequence are not written, and what q, k, v hold there (or in
+ * another sequence) reaches no output.  total_T * H < 2^31.
+ */
+size_t la_gated_delta_prefill_varlen_workspace_bytes(int B, int H, int Hk, int total_T, int r, int dv, la_dtype dtype);
+la_status la_gated_delta_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                        const float *beta, const float *S0, const int *cu_seqlens, int B, int H, int Hk,
+                                        int total_T, int r, int dv, float scale, void *y, float *S_out, void *workspace,
+                                        size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * la_gated_delta_decode_step -- one new token per (b, h), the state updated in place.
+ *   q, k  device [B,Hk,1,r] dtype    v, y  device [B,H,1,dv] dtype    alpha, beta  device FP32 [B,H] or NULL
+ *   S     device FP32 [B,H,r,dv]
+ */
+la_status la_gated_delta_decode_step(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                     const float *beta, float *S, int B, int H, int Hk, int r, int dv, float scale,
+                                     void *y, la_stream_t stream);
+
+/*
+ * la_gated_delta_backward -- gradients of la_gated_delta_prefill's outputs, by the chain rule through the
+ * recurrence.  Given dy = dL/dy and optionally dS_T = dL/dS_T, with e_t = v_t - S'^T k_t,
+ *     G_t = scale q_t dy_t^T + alpha_{t+1} (G_{t+1} - k_{t+1} dv_{t+1}^T),   G_T = scale q_T dy_T^T + dS_T,
+ *     dv_t = beta_t G_t^T k_t,   dk_t = beta_t G_t e_t - S'_t dv_t,   dq_t = scale S_t dy_t,
+ *     dbeta_t = (G_t^T k_t) . e_t,   dS0 = alpha_1 (G_1 - k_1 dv_1^T),
+ *     dalpha_t = (<S_T, dS_T> + sum_{s >= t} (q_s . dq_s - v_s . dv_s)) / alpha_t.
+ *   q, k, v, alpha, beta, S0, scale: as passed to the forward call (its outputs are not needed).
+ *   dy       device [B,H,T,dv] dtype         dS_T  device FP32 [B,H,r,dv] or NULL (zero)
+ *   dq, dk   device [B,Hk,T,r] dtype         dv_out  device [B,H,T,dv] dtype
+ *   dalpha   device FP32 [B,H,T] or NULL (not formed; ignored without alpha).  Defined where alpha > 0 (it is the
+ *            log-gate's gradient over alpha); 0 is written where alpha is 0.
+ *   dbeta    device FP32 [B,H,T] or NULL (not formed)
+ *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL)
+ *   workspace  la_gated_delta_backward_workspace_bytes(...) bytes, as above
+ * T may be 0 (dS0 = dS_T).
+ */
+size_t la_gated_delta_backward_workspace_bytes(int B, int H, int Hk, int T, int r, int dv, la_dtype dtype);
+la_status la_gated_delta_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                  const float *beta, const float *S0, int B, int H, int Hk, int T, int r, int dv,
+                                  float scale, const void *dy, const float *dS_T, void *dq, void *dk, void *dv_out,
+                                  float *dalpha, float *dbeta, float *dS0, void *workspace, size_t workspace_bytes,
+                                  la_stream_t stream);
+
+/*
  * la_beam_select -- a beam search's choice: the best K of a request's K beams x V tokens.
  * Candidate (k, v) of request b scores
  *     scores[b,k] + logits[b,k,v] - log sum_u exp logits[b,k,u]
@@ -520,6 +612,47 @@ la_status la_beam_select(const void *logits, la_dtype dtype, long long row_strid
                          int *tokens, unsigned char *done_out, la_stream_t stream);
 
 /*
+ * la_token_logprobs -- scores of given tokens under rows of logits (what a model answered with, or is trained
+ * on):  lse = log sum_v exp x_v,  logprob = x_token - lse,  entropy = lse - sum_v p_v x_v  with p_v = exp(x_v - lse),
+ * and the best alternatives of the row.
+ *   logits    device [N,V] dtype, row n at element n row_stride
+ *   tokens    device int32 [N].  A negative token skips its row (padding), which is not read: its logprob,
+ *             entropy and lse are 0 and it has no alternatives.  A token >= V does the same and is
+ *             recorded as LA_ERR_SHAPE in the device status word.
+ *   top       alternatives per row, 0 .. 32
+ *   logprobs  device FP32 [N];  entropy, lse  device FP32 [N] or NULL
+ *   top_logprobs, top_tokens  device FP32, int32 [N,top] (may be NULL when top is 0): the top most probable
+ *             tokens, best first, equal logits in the order of their indices
+ * A logit of -infinity (a masked token) has probability 0 and is no alternative; slots left over get -infinity and token -1.
+ * A row of nothing else has lse and logprob -infinity and entropy 0.  A row with a NaN or +infinity gives NaN
+ * and no alternatives.
+ * One launch, the logits read once (blocks that hold an alternative once more, out of the L2 cache); rows that start on
+ * 16-byte boundaries are read fastest.  A row's results do not depend on the others.
+ * Requires N >= 0, 1 <= V <= 2^30, row_stride >= V; logits aligned to their element size, other arrays 4-byte.
+ * Errors: LA_ERR_NULL, LA_ERR_SHAPE (N < 0, V < 1, top < 0, row_stride < V), LA_ERR_DTYPE, LA_ERR_ALIGN,
+ *         LA_ERR_UNSUPPORTED (top > 32, other sizes), LA_ERR_CUDA.
+ */
+la_status la_token_logprobs(const void *logits, la_dtype dtype, long long row_stride, const int *tokens, int N, int V,
+                            int top, float *logprobs, float *entropy, float *lse, float *top_logprobs, int *top_tokens,
+                            la_stream_t stream);
+
+/*
+ * la_token_logprobs_backward -- the gradient of la_token_logprobs' logprobs and entropies: from dlogprobs = dL/dlogprobs
+ * and dentropy = dL/dentropy,
+ *     dlogits_v = dlogprob (1[v = token] - p_v) - dentropy p_v (log p_v + entropy).
+ *   logits, tokens, row_stride: as passed to the forward call       lse, entropy  device FP32 [N]: its results
+ *             (entropy may be NULL without dentropy)
+ *   dlogprobs device FP32 [N];  dentropy  device FP32 [N] or NULL (zero)
+ *   dlogits   device [N,V] dtype, row n at element n grad_stride; may equal logits (with the same stride)
+ * A skipped row (and one of -infinity only) gets zeros; masked logits get 0.
+ * Requirements and errors as for la_token_logprobs (grad_stride as row_stride).
+ */
+la_status la_token_logprobs_backward(const void *logits, la_dtype dtype, long long row_stride, const int *tokens,
+                                     const float *lse, const float *entropy, const float *dlogprobs,
+                                     const float *dentropy, int N, int V, void *dlogits, long long grad_stride,
+                                     la_stream_t stream);
+
+/*
  * la_state_reorder -- moves recurrent states after a beam search's choice: slot j of
  * request b receives the state of its slot parents[b,j].
  *   S, S_out   device FP32 [B*K, H, r, dv]       z, z_out  device FP32 [B*K, H, r], or both NULL
@@ -527,8 +660,8 @@ la_status la_beam_select(const void *logits, la_dtype dtype, long long row_strid
  *              left as it is and recorded as LA_ERR_SHAPE in the device status word.
  * S_out may equal S and z_out z (in place: slots that keep their state are not touched);
  * otherwise they must not overlap.  Any parents are allowed, repeated ones too.
- * The states of la_decode_step (S and z), la_delta_rule and la_decay_decode_step (S) all
- * have this layout.
+ * The states of la_decode_step (S and z), la_delta_rule, la_decay_decode_step and
+ * la_gated_delta_decode_step (S) all have this layout.
  * Requires 1 <= K <= 32, B <= 65535, 4-byte alignment (16-byte accesses when every slot is
  * 16-byte aligned).
  * Errors: LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (K > 32), LA_ERR_CUDA.

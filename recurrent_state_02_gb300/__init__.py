@@ -4,9 +4,10 @@
     S_t = alpha_t S_{t-1} + phi(k_t) v_t^T,   z_t = alpha_t z_{t-1} + phi(k_t)
     y_t = phi(q_t)^T S_t / (phi(q_t)^T z_t + eps)
 
-and its relatives on the same states: the delta rule (delta_rule*), linear attention with a
-constant decay per head (decay_*), and what a beam search does with states between
-decode steps (beam_select, state_reorder).
+and its relatives on the same states: the delta rule (delta_rule*), the same with a gate and its
+gradients (gated_delta_*), linear attention with a constant decay per head (decay_*), what a beam
+search does with states between decode steps (beam_select, state_reorder), and the scores of given
+tokens (token_logprobs*).
 
 Every step runs in the CUDA kernels of liblinattn.so, reached through its C ABI
 (include/linattn.h).  The functions below only check tensor metadata, allocate
@@ -505,6 +506,129 @@ def decay_backward(q, k, v, dy, decay, S0=None, dS_T=None, scale=1.0, workspace=
     return dq, dk, dv_out, dS0
 
 
+def _gdelta_inputs(q, k, v, alpha, beta, lead, Hk, H, r, dv):
+    """Checks q, k [*lead with Hk heads, r], v and the gates; lead(heads) gives the leading sizes."""
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    dev = q.device
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} value heads cannot share {Hk} key heads evenly")
+    _want(q, "q", (*lead(Hk), r), dt, dev)
+    _want(k, "k", (*lead(Hk), r), dt, dev)
+    _want(v, "v", (*lead(H), dv), dt, dev)
+    if alpha is not None:
+        _want(alpha, "alpha", lead(H), torch.float32, dev)
+    if beta is not None:
+        _want(beta, "beta", lead(H), torch.float32, dev)
+    return dt, dev
+
+
+def gated_delta_prefill_workspace_bytes(B, H, Hk, T, r, dv, dtype=torch.bfloat16, device=None) -> int:
+    """Scratch bytes of gated_delta_prefill for these sizes on `device` (default: the current one)."""
+    return _bytes("la_gated_delta_prefill_workspace_bytes", None if device is None else torch.device(device), B, H, Hk, T, r,
+                  dv, _DTYPES[dtype])
+
+
+def gated_delta_prefill(q, k, v, alpha=None, beta=None, S0=None, scale=1.0, y=None, S_out=None, workspace=None):
+    """The gated delta rule: S' = alpha S, S <- S' + beta k (v - S'^T k)^T, y = scale S^T q.
+    q, k [B,Hk,T,r], v [B,H,T,dv] (bf16 or fp32, same dtype; Hk divides H, and neighbouring value heads share
+    a key head); alpha, beta [B,H,T] fp32 or None (1); S0 [B,H,r,dv] fp32 or None (zero).
+    Returns (y [B,H,T,dv] in the input dtype, S_T)."""
+    B, Hk, T, r = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    dt, dev = _gdelta_inputs(q, k, v, alpha, beta, lambda h: (B, h, T), Hk, H, r, dv)
+    if S0 is not None:
+        _want(S0, "S0", (B, H, r, dv), torch.float32, dev)
+    y = _out(y, "y", (B, H, T, dv), dt, dev)
+    S_out = _out(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
+    dt = _DTYPES[dt]
+    workspace, ws_bytes = _workspace(workspace, _bytes("la_gated_delta_prefill_workspace_bytes", dev, B, H, Hk, T, r, dv, dt), dev)
+    _call("la_gated_delta_prefill", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, _ptr(alpha), _ptr(beta), _ptr(S0), B, H,
+          Hk, T, r, dv, scale, y.data_ptr(), S_out.data_ptr(), _ptr(workspace), ws_bytes)
+    return y, S_out
+
+
+def gated_delta_prefill_varlen_workspace_bytes(B, H, Hk, total_T, r, dv, dtype=torch.bfloat16, device=None) -> int:
+    """Scratch bytes of gated_delta_prefill_varlen for these sizes on `device` (default: the current one)."""
+    return _bytes("la_gated_delta_prefill_varlen_workspace_bytes", None if device is None else torch.device(device), B, H, Hk,
+                  total_T, r, dv, _DTYPES[dtype])
+
+
+def gated_delta_prefill_varlen(q, k, v, cu_seqlens, alpha=None, beta=None, S0=None, scale=1.0, y=None, S_out=None,
+                               workspace=None):
+    """gated_delta_prefill for packed sequences: q, k [total_T, Hk, r], v [total_T, H, dv], alpha, beta
+    [total_T, H] (token-major); cu_seqlens int32 [B+1] on the device (sequence b is tokens
+    cu_seqlens[b] .. cu_seqlens[b+1]-1); S0 [B,H,r,dv] fp32 or None.  Returns
+    (y [total_T, H, dv], S_T [B,H,r,dv])."""
+    total_T, Hk, r = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    dt, dev = _gdelta_inputs(q, k, v, alpha, beta, lambda h: (total_T, h), Hk, H, r, dv)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.device != dev:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor on the device of q")
+    B = cu_seqlens.numel() - 1
+    _want(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    if S0 is not None:
+        _want(S0, "S0", (B, H, r, dv), torch.float32, dev)
+    y = _out(y, "y", (total_T, H, dv), dt, dev)
+    S_out = _out(S_out, "S_out", (B, H, r, dv), torch.float32, dev)
+    dt = _DTYPES[dt]
+    workspace, ws_bytes = _workspace(
+        workspace, _bytes("la_gated_delta_prefill_varlen_workspace_bytes", dev, B, H, Hk, total_T, r, dv, dt), dev)
+    _call("la_gated_delta_prefill_varlen", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, _ptr(alpha), _ptr(beta), _ptr(S0),
+          cu_seqlens.data_ptr(), B, H, Hk, total_T, r, dv, scale, y.data_ptr(), S_out.data_ptr(), _ptr(workspace), ws_bytes)
+    return y, S_out
+
+
+def gated_delta_decode_step(q, k, v, S, alpha=None, beta=None, scale=1.0, y=None):
+    """One token per request of gated_delta_prefill, S [B,H,r,dv] fp32 updated in place.
+    q, k [B,Hk,1,r], v [B,H,1,dv]; alpha, beta [B,H] fp32 or None (1).  Returns y [B,H,1,dv]."""
+    B, Hk, one, r = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    if one != 1:
+        raise ValueError("decode takes one token per request")
+    dt, dev = _gdelta_inputs(q, k, v, None, None, lambda h: (B, h, 1), Hk, H, r, dv)
+    if alpha is not None:
+        _want(alpha, "alpha", (B, H), torch.float32, dev)
+    if beta is not None:
+        _want(beta, "beta", (B, H), torch.float32, dev)
+    _want(S, "S", (B, H, r, dv), torch.float32, dev)
+    y = _out(y, "y", (B, H, 1, dv), dt, dev)
+    _call("la_gated_delta_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dt], _ptr(alpha), _ptr(beta),
+          S.data_ptr(), B, H, Hk, r, dv, scale, y.data_ptr())
+    return y
+
+
+def gated_delta_backward_workspace_bytes(B, H, Hk, T, r, dv, dtype=torch.bfloat16, device=None) -> int:
+    """Scratch bytes of gated_delta_backward for these sizes on `device` (default: the current one)."""
+    return _bytes("la_gated_delta_backward_workspace_bytes", None if device is None else torch.device(device), B, H, Hk, T, r,
+                  dv, _DTYPES[dtype])
+
+
+def gated_delta_backward(q, k, v, dy, alpha=None, beta=None, S0=None, dS_T=None, scale=1.0, workspace=None):
+    """Gradients of gated_delta_prefill: from its inputs, dy [B,H,T,dv] and optionally dS_T [B,H,r,dv] fp32,
+    returns (dq, dk, dv, dalpha, dbeta, dS0): dq, dk [B,Hk,T,r] and dv in the input dtype, dalpha and
+    dbeta [B,H,T] fp32 (None for a gate that was not given), dS0 fp32.  dalpha is 0 where alpha is 0."""
+    B, Hk, T, r = q.shape
+    H, dvd = v.shape[1], v.shape[3]
+    dt, dev = _gdelta_inputs(q, k, v, alpha, beta, lambda h: (B, h, T), Hk, H, r, dvd)
+    _want(dy, "dy", (B, H, T, dvd), dt, dev)
+    if S0 is not None:
+        _want(S0, "S0", (B, H, r, dvd), torch.float32, dev)
+    if dS_T is not None:
+        _want(dS_T, "dS_T", (B, H, r, dvd), torch.float32, dev)
+    dq, dk, dv_out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dalpha = None if alpha is None else torch.empty_like(alpha)
+    dbeta = None if beta is None else torch.empty_like(beta)
+    dS0 = torch.empty((B, H, r, dvd), device=dev, dtype=torch.float32)
+    dt = _DTYPES[dt]
+    workspace, ws_bytes = _workspace(workspace, _bytes("la_gated_delta_backward_workspace_bytes", dev, B, H, Hk, T, r, dvd, dt), dev)
+    _call("la_gated_delta_backward", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, _ptr(alpha), _ptr(beta), _ptr(S0), B, H,
+          Hk, T, r, dvd, scale, dy.data_ptr(), _ptr(dS_T), dq.data_ptr(), dk.data_ptr(), dv_out.data_ptr(), _ptr(dalpha),
+          _ptr(dbeta), dS0.data_ptr(), _ptr(workspace), ws_bytes)
+    return dq, dk, dv_out, dalpha, dbeta, dS0
+
+
 def beam_select(logits, scores, done=None, eos=-1, next_scores=None, parents=None, tokens=None, done_out=None):
     """A beam search's choice: the best K of K beams x V tokens of every request, by
     scores + log_softmax(logits), best first, ties to the lower k V + v.
@@ -537,6 +661,63 @@ def beam_select(logits, scores, done=None, eos=-1, next_scores=None, parents=Non
     _call("la_beam_select", dev, logits.data_ptr(), _DTYPES[dt], stride, scores.data_ptr(), _ptr(done), B, K, V, eos,
           next_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), done_out.data_ptr())
     return next_scores, parents, tokens, done_out
+
+
+def _logit_rows(t, name):
+    """N, V and the row stride of a matrix of logits (rows contiguous, at any one stride)."""
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix on a CUDA device")
+    N, V = t.shape
+    if t.is_contiguous() or N <= 1:
+        stride = V
+    else:
+        stride = t.stride(0)
+    if V > 1 and t.stride(1) != 1 or stride < V:
+        raise ValueError(f"{name} must have contiguous rows at one stride")
+    return N, V, stride
+
+
+def token_logprobs(logits, tokens, top=0, logprobs=None, entropy=None, lse=None):
+    """Log-probabilities of given tokens under rows of logits, the rows' entropy and best alternatives.
+    logits [N,V] (bf16 or fp32; rows may be padded: any stride between them); tokens [N] int32, negative: the
+    row is skipped (its results are 0, and it is not read); top 0..32 alternatives.
+    Returns (logprobs, entropy, lse [N] fp32, top_logprobs [N,top] fp32, top_tokens [N,top] int32); equal logits
+    rank in the order of their indices, masked ones (-inf) are no alternatives (token -1)."""
+    N, V, stride = _logit_rows(logits, "logits")
+    dev = logits.device
+    _want(tokens, "tokens", (N,), torch.int32, dev)
+    logprobs = _out(logprobs, "logprobs", (N,), torch.float32, dev)
+    entropy = _out(entropy, "entropy", (N,), torch.float32, dev)
+    lse = _out(lse, "lse", (N,), torch.float32, dev)
+    shape = (N, max(0, top))
+    top_logprobs, top_tokens = torch.empty(shape, device=dev, dtype=torch.float32), torch.empty(shape, device=dev, dtype=torch.int32)
+    _call("la_token_logprobs", dev, logits.data_ptr(), _DTYPES[logits.dtype], stride, tokens.data_ptr(), N, V, top,
+          logprobs.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top_logprobs.data_ptr(), top_tokens.data_ptr())
+    return logprobs, entropy, lse, top_logprobs, top_tokens
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, dlogprobs, dentropy=None, dlogits=None):
+    """Gradient of token_logprobs with respect to the logits: from its inputs and results, dlogprobs [N] and
+    optionally dentropy [N] fp32 (entropy may be None without it).  dlogits may be the logits (in place) or a
+    matrix of their shape.  Returns dlogits [N,V] in the logits' dtype."""
+    N, V, stride = _logit_rows(logits, "logits")
+    dev = logits.device
+    _want(tokens, "tokens", (N,), torch.int32, dev)
+    for t, name in ((lse, "lse"), (dlogprobs, "dlogprobs")):
+        _want(t, name, (N,), torch.float32, dev)
+    if dentropy is not None:
+        _want(dentropy, "dentropy", (N,), torch.float32, dev)
+        _want(entropy, "entropy", (N,), torch.float32, dev)
+    if dlogits is None:
+        dlogits = torch.empty((N, V), device=dev, dtype=logits.dtype)
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or dlogits.device != dev:
+        raise ValueError("dlogits must have the logits' shape, dtype and device")
+    _, _, grad_stride = _logit_rows(dlogits, "dlogits")
+    _call("la_token_logprobs_backward", dev, logits.data_ptr(), _DTYPES[logits.dtype], stride, tokens.data_ptr(), lse.data_ptr(),
+          _ptr(entropy), dlogprobs.data_ptr(), _ptr(dentropy), N, V, dlogits.data_ptr(), grad_stride)
+    return dlogits
 
 
 def state_reorder(S, parents, z=None, S_out=None, z_out=None):

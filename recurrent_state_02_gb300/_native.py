@@ -46,7 +46,18 @@ SIGNATURES = {
     "la_decay_backward_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "la_decay_backward": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _i, _i, _i, _i, _i, _f, _vp, _fp, _vp, _vp, _vp, _fp,
                                _vp, _sz, _vp]),
+    "la_gated_delta_prefill_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "la_gated_delta_prefill": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _fp, _i, _i, _i, _i, _i, _i, _f, _vp, _fp, _vp, _sz, _vp]),
+    "la_gated_delta_prefill_varlen_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "la_gated_delta_prefill_varlen": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _fp,
+                                           _vp, _sz, _vp]),
+    "la_gated_delta_decode_step": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _fp, _i, _i, _i, _i, _i, _f, _vp, _vp]),
+    "la_gated_delta_backward_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "la_gated_delta_backward": (_i, [_vp, _vp, _vp, _i, _fp, _fp, _fp, _i, _i, _i, _i, _i, _i, _f, _vp, _fp, _vp, _vp, _vp,
+                                     _fp, _fp, _fp, _vp, _sz, _vp]),
     "la_beam_select": (_i, [_vp, _i, _ll, _fp, _vp, _i, _i, _i, _i, _fp, _vp, _vp, _vp, _vp]),
+    "la_token_logprobs": (_i, [_vp, _i, _ll, _vp, _i, _i, _i, _fp, _fp, _fp, _fp, _vp, _vp]),
+    "la_token_logprobs_backward": (_i, [_vp, _i, _ll, _vp, _fp, _fp, _fp, _fp, _i, _i, _vp, _ll, _vp]),
     "la_state_reorder": (_i, [_fp, _fp, _vp, _i, _i, _i, _i, _i, _fp, _fp, _vp]),
     "la_last_device_status": (_i, [_vp]),
     "la_status_string": (ctypes.c_char_p, [_i]),

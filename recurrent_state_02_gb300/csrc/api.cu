@@ -3,6 +3,7 @@
 #include "../../include/linattn.h"
 #include "decay.h"
 #include "delta_tc.h"
+#include "gdelta_tc.h"
 #include "kernels.h"
 #include "side_lane.h"
 
@@ -11,6 +12,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 namespace {
 
@@ -1064,6 +1066,186 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
     return run_sweeps(sw, 3, a, dtype == LA_DTYPE_BF16, B, st, workspace, need);
 }
 
+// ------------------------------------------------------- gated delta rule
+
+namespace {
+
+// What every gated delta entry point checks of its sizes.
+la_status check_gdelta_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, float scale)
+{
+    if (Hk < 1 || H < 1 || H % Hk != 0) return LA_ERR_SHAPE;
+    if (const la_status e = check_decay_sizes(dtype, B, H, T, r, dv, scale)) return e;
+    // a thread per element of every token's row in the gradients' last passes
+    if ((long long)B * H * (T + 1LL) > (1LL << 38) / 256) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+la::GdeltaShape gdelta_shape(int B, int H, int Hk, int T, int r, int dv, const float *alpha, const float *beta, int *status,
+                             const int *cu_seqlens = nullptr)
+{
+    la::GdeltaShape s;
+    s.B = B, s.H = H, s.Hk = Hk, s.T = T, s.r = r, s.dv = dv;
+    s.alpha = alpha, s.beta = beta;
+    s.cu_seqlens = cu_seqlens;
+    s.status = status;
+    return s;
+}
+
+la_status check_gdelta_pointers(la_dtype dtype, std::initializer_list<const void *> elems, std::initializer_list<const void *> words)
+{
+    for (const void *p : elems)
+        if (!elem_aligned(p, dtype)) return LA_ERR_ALIGN;
+    for (const void *p : words)
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    return LA_OK;
+}
+
+la_status check_workspace(const void *workspace, size_t bytes, size_t need)
+{
+    if (!need) return LA_OK;
+    if (!workspace || bytes < need) return LA_ERR_WORKSPACE;
+    return aligned(workspace, 256) ? LA_OK : LA_ERR_ALIGN;
+}
+
+// Sequences of at most this many tokens take the token recurrence (packed ones do not: their lengths are not known here).
+constexpr int kGdeltaWalk = 16;
+
+// Whether prompts of these sizes run in chunks (with every token array on a 16-byte boundary).
+bool gdelta_tc_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, bool packed)
+{
+    return check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, 1.f) == LA_OK && dtype == LA_DTYPE_BF16 && (r == 64 || r == 128) &&
+           dv % 64 == 0 && T > (packed ? 0 : kGdeltaWalk) && la::gdelta_tc_slots(B, T, packed) * H <= 0x7fffffffLL;
+}
+
+size_t gdelta_workspace(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, bool packed)
+{
+    return gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, packed) ? la::gdelta_tc_workspace_bytes(B, H, T, packed) : 0;
+}
+
+la_status gdelta_forward(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha, const float *beta,
+                         const float *S0, const int *cu_seqlens, int B, int H, int Hk, int T, int r, int dv, float scale, void *y,
+                         float *S_out, void *workspace, size_t workspace_bytes, la_stream_t stream)
+{
+    if (!S_out || (T > 0 && (!q || !k || !v || !y))) return LA_ERR_NULL;
+    if (const la_status e = check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, scale)) return e;
+    if (const la_status e = check_gdelta_pointers(dtype, {q, k, v, y}, {alpha, beta, S0, S_out, cu_seqlens})) return e;
+    const bool packed = cu_seqlens != nullptr;
+    if (const la_status e = check_workspace(workspace, workspace_bytes, gdelta_workspace(dtype, B, H, Hk, T, r, dv, packed))) return e;
+    const la::GdeltaShape s = gdelta_shape(B, H, Hk, T, r, dv, alpha, beta, status_word(), cu_seqlens);
+    if (!s.status) return LA_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, packed) && aligned(q, 16) && aligned(k, 16) && aligned(v, 16)) {
+        la::GdeltaTcMaps m;
+        auto map = [&](CUtensorMap *t, const void *p, int heads, int cols) {
+            return packed ? make_map_bf16_tok(t, p, T, heads, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                          : make_map_bf16(t, p, (long long)B * heads, T, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        if (!map(&m.q, q, Hk, r) || !map(&m.k, k, Hk, r) || !map(&m.v, v, H, dv)) return LA_ERR_CUDA;
+        la::GdeltaTcArgs a;
+        a.s = s;
+        a.S0 = S0, a.S_out = S_out;
+        a.y = static_cast<uint16_t *>(y);
+        a.scale = scale;
+        a.ws = static_cast<uint8_t *>(workspace);
+        if (packed) {
+            a.slot_base = static_cast<int *>(workspace);
+            a.order = a.slot_base + B + 1;
+            a.ws += la::gdelta_tc_plan_bytes(B);
+        }
+        return from_cuda(la::launch_gdelta_tc(m, a, st));
+    }
+    la::GdeltaForward f;
+    f.q = q, f.k = k, f.v = v, f.y = y;
+    f.S0 = S0, f.S_out = S_out;
+    f.scale = scale;
+    return from_cuda(la::launch_gdelta_rec(s, f, dtype == LA_DTYPE_BF16, st));
+}
+
+}  // namespace
+
+size_t la_gated_delta_prefill_workspace_bytes(int B, int H, int Hk, int T, int r, int dv, la_dtype dtype)
+{
+    return gdelta_workspace(dtype, B, H, Hk, T, r, dv, false);
+}
+
+la_status la_gated_delta_prefill(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                 const float *beta, const float *S0, int B, int H, int Hk, int T, int r, int dv,
+                                 float scale, void *y, float *S_out, void *workspace, size_t workspace_bytes,
+                                 la_stream_t stream)
+{
+    return gdelta_forward(q, k, v, dtype, alpha, beta, S0, nullptr, B, H, Hk, T, r, dv, scale, y, S_out, workspace,
+                          workspace_bytes, stream);
+}
+
+size_t la_gated_delta_prefill_varlen_workspace_bytes(int B, int H, int Hk, int total_T, int r, int dv, la_dtype dtype)
+{
+    return gdelta_workspace(dtype, B, H, Hk, total_T, r, dv, true);
+}
+
+la_status la_gated_delta_prefill_varlen(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                        const float *beta, const float *S0, const int *cu_seqlens, int B, int H, int Hk,
+                                        int total_T, int r, int dv, float scale, void *y, float *S_out, void *workspace,
+                                        size_t workspace_bytes, la_stream_t stream)
+{
+    if (!cu_seqlens) return LA_ERR_NULL;
+    if (H > 0 && (long long)total_T * H > 0x7fffffffLL) return LA_ERR_SHAPE;
+    return gdelta_forward(q, k, v, dtype, alpha, beta, S0, cu_seqlens, B, H, Hk, total_T, r, dv, scale, y, S_out, workspace,
+                          workspace_bytes, stream);
+}
+
+la_status la_gated_delta_decode_step(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                     const float *beta, float *S, int B, int H, int Hk, int r, int dv, float scale, void *y,
+                                     la_stream_t stream)
+{
+    if (!q || !k || !v || !S || !y) return LA_ERR_NULL;
+    if (const la_status e = check_gdelta_sizes(dtype, B, H, Hk, 1, r, dv, scale)) return e;
+    if (const la_status e = check_gdelta_pointers(dtype, {q, k, v, y}, {alpha, beta, S})) return e;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == LA_DTYPE_BF16;
+    la::GdeltaShape s = gdelta_shape(B, H, Hk, 1, r, dv, alpha, beta, nullptr);
+    if (dv % 4 == 0 && aligned(S, 16) && (long long)B * H <= 0x7fffffffLL)
+        return from_cuda(la::launch_gdelta_decode(s, q, k, v, bf16, S, scale, y, st));
+    la::GdeltaForward f;
+    f.q = q, f.k = k, f.v = v, f.y = y;
+    f.S0 = f.S_out = S;
+    f.scale = scale;
+    return from_cuda(la::launch_gdelta_rec(s, f, bf16, st));
+}
+
+size_t la_gated_delta_backward_workspace_bytes(int B, int H, int Hk, int T, int r, int dv, la_dtype dtype)
+{
+    if (check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, 1.f) != LA_OK || T == 0) return 0;
+    return sizeof(float) * la::gdelta_rec_backward_floats(B, H, T, r, dv);
+}
+
+la_status la_gated_delta_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
+                                  const float *beta, const float *S0, int B, int H, int Hk, int T, int r, int dv,
+                                  float scale, const void *dy, const float *dS_T, void *dq, void *dk, void *dv_out,
+                                  float *dalpha, float *dbeta, float *dS0, void *workspace, size_t workspace_bytes,
+                                  la_stream_t stream)
+{
+    if (!dS0 || (T > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv_out))) return LA_ERR_NULL;
+    if (const la_status e = check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, scale)) return e;
+    if (const la_status e = check_gdelta_pointers(dtype, {q, k, v, dy, dq, dk, dv_out}, {alpha, beta, S0, dS_T, dalpha, dbeta, dS0}))
+        return e;
+    if (const la_status e = check_workspace(workspace, workspace_bytes, la_gated_delta_backward_workspace_bytes(B, H, Hk, T, r, dv, dtype)))
+        return e;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        const size_t bytes = sizeof(float) * (size_t)B * H * r * dv;
+        return from_cuda(dS_T ? cudaMemcpyAsync(dS0, dS_T, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(dS0, 0, bytes, st));
+    }
+    const la::GdeltaShape s = gdelta_shape(B, H, Hk, T, r, dv, alpha, beta, nullptr);
+    la::GdeltaBackward g;
+    g.q = q, g.k = k, g.v = v, g.dy = dy;
+    g.S0 = S0, g.dS_T = dS_T;
+    g.dq = dq, g.dk = dk, g.dv_out = dv_out;
+    g.dalpha = dalpha, g.dbeta = dbeta, g.dS0 = dS0;
+    g.scale = scale;
+    g.ws = static_cast<float *>(workspace);
+    return from_cuda(la::launch_gdelta_rec_backward(s, g, dtype == LA_DTYPE_BF16, st));
+}
+
 la_status la_beam_select(const void *logits, la_dtype dtype, long long row_stride, const float *scores,
                          const unsigned char *done, int B, int K, int V, int eos, float *next_scores, int *parents,
                          int *tokens, unsigned char *done_out, la_stream_t stream)
@@ -1090,6 +1272,70 @@ la_status la_beam_select(const void *logits, la_dtype dtype, long long row_strid
     a.V = V;
     a.eos = eos;
     return from_cuda(la::launch_beam_select(a, B, dtype == LA_DTYPE_BF16, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+la_status check_logit_rows(const void *p, la_dtype dtype, long long row_stride, int N, int V)
+{
+    if (N < 0 || V < 1 || row_stride < V) return LA_ERR_SHAPE;
+    if (dtype != LA_DTYPE_BF16 && dtype != LA_DTYPE_FP32) return LA_ERR_DTYPE;
+    if (V > (1 << 30)) return LA_ERR_UNSUPPORTED;
+    // byte offsets of the rows stay in 63 bits
+    if (N > 0 && row_stride > (1LL << 60) / N) return LA_ERR_SHAPE;
+    return elem_aligned(p, dtype) ? LA_OK : LA_ERR_ALIGN;
+}
+
+}  // namespace
+
+la_status la_token_logprobs(const void *logits, la_dtype dtype, long long row_stride, const int *tokens, int N, int V,
+                            int top, float *logprobs, float *entropy, float *lse, float *top_logprobs, int *top_tokens,
+                            la_stream_t stream)
+{
+    if (N > 0 && (!logits || !tokens || !logprobs || (top > 0 && (!top_logprobs || !top_tokens)))) return LA_ERR_NULL;
+    if (top < 0) return LA_ERR_SHAPE;
+    if (const la_status e = check_logit_rows(logits, dtype, row_stride, N, V)) return e;
+    if (top > la::kMaxTop) return LA_ERR_UNSUPPORTED;
+    for (const void *p : {(const void *)tokens, (const void *)logprobs, (const void *)entropy, (const void *)lse,
+                          (const void *)top_logprobs, (const void *)top_tokens})
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    if (N == 0) return LA_OK;
+    la::LogprobArgs a;
+    a.logits = logits;
+    a.row_stride = row_stride;
+    a.tokens = tokens;
+    a.N = N, a.V = V, a.top = top;
+    a.logprobs = logprobs, a.entropy = entropy, a.lse = lse;
+    a.top_logprobs = top_logprobs, a.top_tokens = top_tokens;
+    a.status = status_word();
+    if (!a.status) return LA_ERR_CUDA;
+    return from_cuda(la::launch_token_logprobs(a, dtype == LA_DTYPE_BF16, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+la_status la_token_logprobs_backward(const void *logits, la_dtype dtype, long long row_stride, const int *tokens,
+                                     const float *lse, const float *entropy, const float *dlogprobs,
+                                     const float *dentropy, int N, int V, void *dlogits, long long grad_stride,
+                                     la_stream_t stream)
+{
+    if (N > 0 && (!logits || !tokens || !lse || !dlogprobs || !dlogits || (dentropy && !entropy))) return LA_ERR_NULL;
+    if (const la_status e = check_logit_rows(logits, dtype, row_stride, N, V)) return e;
+    if (const la_status e = check_logit_rows(dlogits, dtype, grad_stride, N, V)) return e;
+    if (dlogits == logits && grad_stride != row_stride) return LA_ERR_SHAPE;
+    // one CTA per row and 8192 elements (BF16: 16384)
+    if ((long long)N * ((V + 8191) / 8192) > 0x7fffffffLL) return LA_ERR_UNSUPPORTED;
+    for (const void *p : {(const void *)tokens, (const void *)lse, (const void *)entropy, (const void *)dlogprobs, (const void *)dentropy})
+        if (p && !aligned(p, 4)) return LA_ERR_ALIGN;
+    if (N == 0) return LA_OK;
+    la::LogprobGradArgs a;
+    a.logits = logits;
+    a.row_stride = row_stride, a.grad_stride = grad_stride;
+    a.tokens = tokens;
+    a.lse = lse, a.entropy = entropy, a.dlogprobs = dlogprobs, a.dentropy = dentropy;
+    a.N = N, a.V = V;
+    a.dlogits = dlogits;
+    a.status = status_word();
+    if (!a.status) return LA_ERR_CUDA;
+    return from_cuda(la::launch_token_logprobs_backward(a, dtype == LA_DTYPE_BF16, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 la_status la_state_reorder(const float *S, const float *z, const int *parents, int B, int K, int H, int r, int dv,

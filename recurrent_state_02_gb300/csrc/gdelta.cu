@@ -1,0 +1,575 @@
+// gdelta.cu -- the gated delta rule on CUDA cores: the token recurrence in FP32 with its gradients, and
+// the single-token step.  (Prompts of the common sizes run in chunks on the tensor cores: gdelta_tc.cu.)
+//
+// The rule with a gate per token and head:
+//     S' = alpha_t S_{t-1},  e_t = v_t - S'^T k_t,  S_t = S' + beta_t k_t e_t^T,  y_t = scale S_t^T q_t.
+//
+// Its gradients, with G_t = dL/dS_t (what dS_T and the tokens from t on ask of the state):
+//     G_t = scale q_t dy_t^T + alpha_{t+1} (G_{t+1} - k_{t+1} dv_{t+1}^T),    G_T = scale q_T dy_T^T + dS_T,
+//     lam_t = G_t^T k_t,  dv_t = beta_t lam_t,  dbeta_t = lam_t . e_t,  dS0 = alpha_1 (G_1 - k_1 dv_1^T),
+//     dq_t = scale S_t dy_t,   dk_t = beta_t G_t e_t - S'_t dv_t.
+// Every column of S is a recurrence of its own given k, and so is every column of G: one sweep forwards
+// leaves e, one backwards lam.  With e and dv known every row of S, and of G, is one as well: the products
+// S dy, S' dv and G e are two more sweeps over the transposed states.  The gates: log alpha_t
+// scales what the states from t on hold of the ones before, and taking that scale out of the state moves
+// it to q (e^{+}) and v (e^{-}) of the tokens from t on, so
+//     dL/dlog alpha_t = <S_T, dS_T> + sum_{s >= t} (q_s . dq_s - v_s . dv_s).
+
+#include "gdelta.h"
+#include "sm103_ptx.cuh"
+
+#include <cuda_bf16.h>
+
+namespace la {
+namespace {
+
+template <bool BF16>
+__device__ __forceinline__ float load_elem(const void *p, size_t i)
+{
+    return BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16) : static_cast<const float *>(p)[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_elem(void *p, size_t i, float x)
+{
+    if (BF16) static_cast<uint16_t *>(p)[i] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+    else static_cast<float *>(p)[i] = x;
+}
+
+// ------------------------------------------------------------ the recurrence
+// The four sweeps; X is the state (rows x columns), a row vector has an element per row, a column
+// element belongs to the lane's column:
+//     FWD  X = S    (r x dv), forwards:   X *= alpha;  p = X^T k;  X += k (beta (v - p))^T;  out = scale X^T q;  e = v - p
+//     REV  X = G    (r x dv), backwards:  X += q (scale dy)^T;  p = X^T k = lam;  X -= k (beta p)^T;  X *= alpha
+//     QUE  X = S^T  (dv x r), forwards:   X *= alpha;  w = X^T dv;  X += e (beta k)^T;  dq = scale X^T dy
+//     KEY  X = G^T  (dv x r), backwards:  X += dy (scale q)^T;  m = X^T e;  X -= dv k^T;  X *= alpha;  dk = beta m - w
+enum RecMode { kFwd, kRev, kQue, kKey };
+
+struct RecArgs {
+    GdeltaShape s;
+    const void *q, *k, *v, *dy;
+    const float *e, *lam;        // FP32 [B,H,T,dv] (read by kQue, kKey)
+    float *e_out, *lam_out;      // (written by kFwd, kRev)
+    float *w, *dq;               // FP32 [B,H,T,r]: w of kQue, over which kKey leaves dk; dq
+    void *y;                     // kFwd: y or nullptr
+    void *dv_out;                // kRev
+    const float *S_init;         // [B,H,r,dv] or nullptr
+    float *S_fin;                // [B,H,r,dv] or nullptr
+    float scale;
+};
+
+constexpr int kRecTok = 16;              // tokens per staged block
+constexpr int kRecComp = 128;            // threads that compute: 4 warps of 8 columns
+constexpr int kRecThreads = 2 * kRecComp;   // and as many that stage the next block and write out the last one
+constexpr int kRecCols = 32;
+
+template <int RPL>
+constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2);
+
+// A warp's lane (g, jj), g = lane / 4, holds rows 4 (8 m + g) + i (m < RPL / 4, i < 4) of the columns 2 jj and
+// 2 jj + 1 of its warp's 8; sums over the rows are reduced over the 8 groups by shuffles.  The staging
+// warps convert a block of 16 tokens to FP32 while the computing ones work on the one before, and store its
+// results.  4 r dv FMAs per token and head bound it; few heads are bound by a token's latency.
+template <int MODE, bool BF16, int RPL>
+__global__ void __launch_bounds__(kRecThreads)
+gdelta_rec_kernel(const RecArgs a)
+{
+    constexpr bool kT = MODE == kQue || MODE == kKey;      // transposed state
+    constexpr bool kBack = MODE == kRev || MODE == kKey;
+    constexpr int W = 8 * RPL;                             // padded rows
+    extern __shared__ __align__(16) float smem[];
+    // per stage: row vectors x (q, q, dy, dy), b (k, k, dv, e), d (-, -, e, dv), column elements, results, gates
+    float *const st0 = smem;
+    constexpr int kOffB = kRecTok * W, kOffD = 2 * kRecTok * W, kOffC = 3 * kRecTok * W, kOffC2 = kOffC + kRecTok * kRecCols,
+                  kOffO = kOffC2 + kRecTok * kRecCols, kOffO2 = kOffO + kRecTok * kRecCols, kOffG = kOffO2 + kRecTok * kRecCols;
+    constexpr int kStage = kRecStageFloats<RPL>;
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int b = blockIdx.z, h = blockIdx.y, c0 = blockIdx.x * kRecCols;
+    const GdeltaShape &s = a.s;
+    const int rows = kT ? s.dv : s.r, cols = kT ? s.r : s.dv;
+    const int hk = h / (s.H / s.Hk);
+    int T = s.T;
+    size_t tok0 = 0;                         // packed: the sequence's first token
+    const bool packed = s.cu_seqlens != nullptr;
+    if (packed) {
+        const int lo = s.cu_seqlens[b], hi = s.cu_seqlens[b + 1];
+        if (lo < 0 || hi < lo || hi > s.T) {
+            if (tid == 0 && blockIdx.x == 0) atomicExch(s.status, kStatusShape);
+            return;
+        }
+        T = hi - lo;
+        tok0 = lo;
+    }
+    // element (t, 0) of a token array with `heads` heads, its head hh, d elements a row
+    auto at = [&](int t, int heads, int hh, int d) -> size_t {
+        return packed ? ((tok0 + t) * heads + hh) * (size_t)d : (((size_t)b * heads + hh) * s.T + t) * (size_t)d;
+    };
+    const size_t bh = (size_t)b * s.H + h;
+
+    const bool computes = tid < kRecComp;
+    const int warp = tid >> 5, g = lane >> 2, jl = (warp & 3) * 8 + 2 * (lane & 3);
+    float X[2][RPL];
+    if (computes) {
+#pragma unroll
+        for (int m = 0; m < RPL; ++m) {
+            const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = c0 + jl + c;
+                X[c][m] = 0.f;
+                if (a.S_init && row < rows && col < cols)
+                    X[c][m] = a.S_init[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)];
+            }
+        }
+    }
+
+    const int nblk = (T + kRecTok - 1) / kRecTok;
+    // token of position i of block n in the sweep's order
+    auto token = [&](int n, int i) { const int t = n * kRecTok + i; return kBack ? T - 1 - t : t; };
+    auto stage_in = [&](int n, int i0, int step) {
+        float *st = st0 + (n & 1) * kStage;
+        const int nt = min(kRecTok, T - n * kRecTok);
+        for (int x = i0; x < nt * W; x += step) {
+            const int i = x / W, row = x % W, t = token(n, i);
+            float vx = 0.f, vb = 0.f, vd = 0.f;
+            if (row < rows) {
+                if (!kT) {
+                    vx = load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + row);
+                    vb = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + row);
+                } else {
+                    const size_t o = at(t, s.H, h, s.dv) + row;
+                    const float bt = s.beta ? s.beta[at(t, s.H, h, 1)] : 1.f;
+                    vx = load_elem<BF16>(a.dy, o);
+                    const float dvt = bt * a.lam[o], et = a.e[o];
+                    vb = MODE == kQue ? dvt : et;
+                    vd = MODE == kQue ? et : dvt;
+                }
+            }
+            st[x] = vx;
+            st[kOffB + x] = vb;
+            if (kT) st[kOffD + x] = vd;
+        }
+        for (int x = i0; x < nt * kRecCols; x += step) {
+            const int i = x / kRecCols, col = c0 + x % kRecCols, t = token(n, i);
+            float u = 0.f, u2 = 0.f;
+            if (col < cols) {
+                if (MODE == kFwd) u = load_elem<BF16>(a.v, at(t, s.H, h, s.dv) + col);
+                if (MODE == kRev) u = a.scale * load_elem<BF16>(a.dy, at(t, s.H, h, s.dv) + col);
+                if (kT) u = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + col);
+                if (MODE == kKey) u2 = a.scale * load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + col);
+            }
+            st[kOffC + x] = u;
+            if (MODE == kKey) st[kOffC2 + x] = u2;
+        }
+        for (int i = i0; i < nt; i += step) {
+            const int t = token(n, i);
+            st[kOffG + i] = s.alpha ? s.alpha[at(t, s.H, h, 1)] : 1.f;
+            st[kOffG + kRecTok + i] = s.beta ? s.beta[at(t, s.H, h, 1)] : 1.f;
+        }
+    };
+    auto stage_out = [&](int n, int i0, int step) {
+        const float *st = st0 + (n & 1) * kStage;
+        const int nt = min(kRecTok, T - n * kRecTok);
+        for (int x = i0; x < nt * kRecCols; x += step) {
+            const int i = x / kRecCols, col = c0 + x % kRecCols, t = token(n, i);
+            if (col >= cols) continue;
+            const float o = st[kOffO + x], o2 = st[kOffO2 + x], bt = st[kOffG + kRecTok + i];
+            const size_t at_o = at(t, s.H, h, cols) + col;
+            if (MODE == kFwd) {
+                if (a.y) store_elem<BF16>(a.y, at_o, a.scale * o);
+                if (a.e_out) a.e_out[at_o] = o2;
+            } else if (MODE == kRev) {
+                a.lam_out[at_o] = o;
+                store_elem<BF16>(a.dv_out, at_o, bt * o);
+            } else if (MODE == kQue) {
+                a.dq[at_o] = a.scale * o;
+                a.w[at_o] = o2;
+            } else {
+                a.w[at_o] = fmaf(bt, o, -a.w[at_o]);
+            }
+        }
+    };
+
+    if (nblk > 0) stage_in(0, tid, kRecThreads);
+    __syncthreads();
+    for (int n = 0; n < nblk; ++n) {
+        if (computes) {
+            float *st = st0 + (n & 1) * kStage;
+            const int nt = min(kRecTok, T - n * kRecTok);
+#pragma unroll 1
+            for (int i = 0; i < nt; ++i) {
+                const float4 *xr = reinterpret_cast<const float4 *>(st + i * W) + g;
+                const float4 *br = reinterpret_cast<const float4 *>(st + kOffB + i * W) + g;
+                const float4 *dr = reinterpret_cast<const float4 *>(st + kOffD + i * W) + g;
+                const float al = st[kOffG + i], be = st[kOffG + kRecTok + i];
+                const float2 cu = *reinterpret_cast<const float2 *>(st + kOffC + i * kRecCols + jl);
+                const float u[2] = {cu.x, cu.y};
+                float add[2] = {0.f, 0.f};
+                if (MODE == kRev) add[0] = u[0], add[1] = u[1];
+                if (MODE == kKey) {
+                    const float2 t2 = *reinterpret_cast<const float2 *>(st + kOffC2 + i * kRecCols + jl);
+                    add[0] = t2.x, add[1] = t2.y;
+                }
+                float p[2] = {0.f, 0.f};
+#pragma unroll
+                for (int m4 = 0; m4 < RPL / 4; ++m4) {
+                    const float4 vb = br[8 * m4];
+                    const float bb[4] = {vb.x, vb.y, vb.z, vb.w};
+                    float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (kBack) vx = xr[8 * m4];
+                    const float xx[4] = {vx.x, vx.y, vx.z, vx.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float &X1 = X[c][4 * m4 + z];
+                            X1 = kBack ? fmaf(xx[z], add[c], X1) : al * X1;
+                            p[c] = fmaf(X1, bb[z], p[c]);
+                        }
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) p[c] += __shfl_xor_sync(0xffffffffu, p[c], o);
+                float wr[2], out[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    wr[c] = MODE == kFwd ? be * (u[c] - p[c]) : MODE == kRev ? -be * p[c] : MODE == kQue ? be * u[c] : -u[c];
+#pragma unroll
+                for (int m4 = 0; m4 < RPL / 4; ++m4) {
+                    const float4 vd = kT ? dr[8 * m4] : br[8 * m4];
+                    const float dd[4] = {vd.x, vd.y, vd.z, vd.w};
+                    float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!kBack) vx = xr[8 * m4];
+                    const float xx[4] = {vx.x, vx.y, vx.z, vx.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float &X1 = X[c][4 * m4 + z];
+                            X1 = fmaf(dd[z], wr[c], X1);
+                            if (kBack) X1 *= al;
+                            else out[c] = fmaf(X1, xx[z], out[c]);
+                        }
+                }
+                if (!kBack) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) out[c] += __shfl_xor_sync(0xffffffffu, out[c], o);
+                }
+                if (g == 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        st[kOffO + i * kRecCols + jl + c] = kBack ? p[c] : out[c];
+                        if (!kBack) st[kOffO2 + i * kRecCols + jl + c] = MODE == kFwd ? u[c] - p[c] : p[c];
+                    }
+                }
+            }
+        } else {
+            if (n > 0) stage_out(n - 1, tid - kRecComp, kRecComp);
+            asm volatile("bar.sync 1, %0;" ::"n"(kRecComp) : "memory");   // the results are read before their stage is refilled
+            if (n + 1 < nblk) stage_in(n + 1, tid - kRecComp, kRecComp);
+        }
+        __syncthreads();
+    }
+    if (nblk > 0) stage_out(nblk - 1, tid, kRecThreads);
+    if (a.S_fin && computes) {
+#pragma unroll
+        for (int m = 0; m < RPL; ++m) {
+            const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = c0 + jl + c;
+                if (row < rows && col < cols)
+                    a.S_fin[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)] = X[c][m];
+            }
+        }
+    }
+}
+
+template <int MODE, bool BF16, int RPL>
+cudaError_t launch_rec_as(const RecArgs &a, cudaStream_t stream)
+{
+    static OncePerDevice once;
+    constexpr uint32_t bytes = 2 * kRecStageFloats<RPL> * 4;
+    const cudaError_t e = set_smem_once(gdelta_rec_kernel<MODE, BF16, RPL>, bytes, once);
+    if (e != cudaSuccess) return e;
+    const int cols = MODE == kQue || MODE == kKey ? a.s.r : a.s.dv;
+    const dim3 grid((cols + kRecCols - 1) / kRecCols, a.s.H, a.s.B);
+    gdelta_rec_kernel<MODE, BF16, RPL><<<grid, kRecThreads, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t launch_rec(const RecArgs &a, bool bf16, cudaStream_t stream)
+{
+    const int rows = MODE == kQue || MODE == kKey ? a.s.dv : a.s.r;
+    if (rows <= 64) return bf16 ? launch_rec_as<MODE, true, 8>(a, stream) : launch_rec_as<MODE, false, 8>(a, stream);
+    if (rows <= 128) return bf16 ? launch_rec_as<MODE, true, 16>(a, stream) : launch_rec_as<MODE, false, 16>(a, stream);
+    return bf16 ? launch_rec_as<MODE, true, 32>(a, stream) : launch_rec_as<MODE, false, 32>(a, stream);
+}
+
+// ------------------------------------------------- the gradients' last passes
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// dbeta_t = lam . e and the token's part of the gates' gradient, q . dq - v . dv: one warp per (b, h, t).
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+gdelta_token_terms_kernel(GdeltaShape s, const void *q, const void *v, const float *dq, const float *lam, const float *e,
+                          float *dbeta, float *dG)
+{
+    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (i >= (long long)s.B * s.H * s.T) return;
+    const long long bh = i / s.T, t = i % s.T;
+    const int b = (int)(bh / s.H), hk = (int)(bh % s.H) / (s.H / s.Hk);
+    const size_t qo = (((size_t)b * s.Hk + hk) * s.T + t) * s.r;
+    float db = 0.f, gq = 0.f, gv = 0.f;
+    for (int x = lane; x < s.dv; x += 32) {
+        const float l = lam[i * s.dv + x];
+        db = fmaf(l, e[i * s.dv + x], db);
+        gv = fmaf(l, load_elem<BF16>(v, i * s.dv + x), gv);
+    }
+    for (int x = lane; x < s.r; x += 32) gq = fmaf(load_elem<BF16>(q, qo + x), dq[i * s.r + x], gq);
+    db = warp_sum(db), gq = warp_sum(gq), gv = warp_sum(gv);
+    if (lane == 0) {
+        if (dbeta) dbeta[i] = db;
+        if (dG) dG[i] = gq - (s.beta ? s.beta[i] : 1.f) * gv;
+    }
+}
+
+// dq and dk of a key head: the sum over the value heads that share it, in their order.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+gdelta_group_sum_kernel(GdeltaShape s, const float *dq, const float *dk, void *dq_out, void *dk_out)
+{
+    const long long n = (long long)s.T * s.r, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n * s.B * s.Hk) return;
+    const int group = s.H / s.Hk;
+    const size_t from = (i / n) * group * n + i % n;
+    float a = 0.f, c = 0.f;
+    for (int u = 0; u < group; ++u) {
+        a += dq[from + u * n];
+        c += dk[from + u * n];
+    }
+    store_elem<BF16>(dq_out, i, a);
+    store_elem<BF16>(dk_out, i, c);
+}
+
+// dalpha_t = (<S_T, dS_T> + sum_{s >= t} dG_s) / alpha_t: one CTA per (b, h).  The sum runs in 64 bits: over a long
+// sequence it is much smaller than the terms that cancel in it.
+__global__ void __launch_bounds__(256)
+gdelta_gate_sum_kernel(GdeltaShape s, const float *S_T, const float *dS_T, const float *dG, float *dalpha)
+{
+    __shared__ double part[8];
+    const size_t bh = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n = s.r * s.dv;
+    double acc = 0.0;
+    if (dS_T)
+        for (int x = tid; x < n; x += 256) acc += (double)S_T[bh * n + x] * dS_T[bh * n + x];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0) part[warp] = acc;
+    __syncthreads();
+    double carry = 0.0;
+    for (int w = 0; w < 8; ++w) carry += part[w];
+    for (int t1 = s.T; t1 > 0; t1 -= 256) {       // tokens from the last on, thread i the i-th
+        const int t = t1 - 1 - tid;
+        double x = t >= 0 ? dG[bh * s.T + t] : 0.0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        double before = carry;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) before += part[w];
+            carry += part[w];
+        }
+        if (t >= 0) {
+            const float al = s.alpha[bh * s.T + t];
+            dalpha[bh * s.T + t] = al > 0.f ? (float)((before + x) / (double)al) : 0.f;
+        }
+    }
+}
+
+// ------------------------------------------------------------ decode step
+// With p = S^T k and u = S^T q of the state as it is, both in one pass over it, the step needs no second
+// pass before the write: e = v - alpha p, y = scale (alpha u + beta (k . q) e), S <- alpha S + k (beta e)^T.
+// Reads and rewrites r dv FP32 words per head, three FMAs each: bound by HBM.  CTA (b, h, 128 columns) of 8 warps; a
+// warp takes RW rows, its lanes 4 columns each, and issues every state load before any arithmetic.
+__device__ __forceinline__ float4 ld_stream(const float4 *p)
+{
+    float4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void st_stream(float4 *p, float4 v)
+{
+    asm volatile("st.global.cs.v4.f32 [%0], {%1,%2,%3,%4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ float4 fma4(float a, float4 x, float4 y)
+{
+    return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
+}
+
+template <bool BF16, int RW>
+__global__ void __launch_bounds__(256)
+gdelta_decode_kernel(const void *__restrict__ q, const void *__restrict__ k, const void *__restrict__ v, GdeltaShape s,
+                     float *__restrict__ S, float scale, void *__restrict__ y)
+{
+    __shared__ float qs[8 * RW], ks[8 * RW];
+    __shared__ float4 part[8][2][32];
+    const int r = s.r, dv = s.dv;
+    const size_t bh = blockIdx.x, kh = bh / s.H * s.Hk + (bh % s.H) / (s.H / s.Hk);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int j = blockIdx.y * 128 + 4 * lane;
+    const bool col = j < dv;
+    float4 *Sr = reinterpret_cast<float4 *>(S + (bh * r + (size_t)warp * RW) * dv + (col ? j : 0));
+    const int dv4 = dv >> 2;
+    float4 x[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col && warp * RW + i < r) x[i] = ld_stream(Sr + (size_t)i * dv4);
+    }
+    for (int i = tid; i < 8 * RW; i += 256) {
+        qs[i] = i < r ? load_elem<BF16>(q, kh * r + i) : 0.f;
+        ks[i] = i < r ? load_elem<BF16>(k, kh * r + i) : 0.f;
+    }
+    const float al = s.alpha ? s.alpha[bh] : 1.f, be = s.beta ? s.beta[bh] : 1.f;
+    float4 vv = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col) {
+        vv.x = load_elem<BF16>(v, bh * dv + j);
+        vv.y = load_elem<BF16>(v, bh * dv + j + 1);
+        vv.z = load_elem<BF16>(v, bh * dv + j + 2);
+        vv.w = load_elem<BF16>(v, bh * dv + j + 3);
+    }
+    __syncthreads();
+    float4 p = make_float4(0.f, 0.f, 0.f, 0.f), u = p;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        p = fma4(ks[warp * RW + i], x[i], p);
+        u = fma4(qs[warp * RW + i], x[i], u);
+    }
+    part[warp][0][lane] = p;
+    part[warp][1][lane] = u;
+    float kq = 0.f;                          // (every warp for itself, in the same order)
+    for (int i = lane; i < 8 * RW; i += 32) kq = fmaf(ks[i], qs[i], kq);
+    kq = warp_sum(kq);
+    __syncthreads();
+    p = part[0][0][lane];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) p = fma4(1.f, part[w][0][lane], p);
+    const float4 c = make_float4(be * fmaf(-al, p.x, vv.x), be * fmaf(-al, p.y, vv.y), be * fmaf(-al, p.z, vv.z),
+                                 be * fmaf(-al, p.w, vv.w));
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const float kr = ks[warp * RW + i];
+        if (col && warp * RW + i < r)
+            st_stream(Sr + (size_t)i * dv4, make_float4(fmaf(al, x[i].x, kr * c.x), fmaf(al, x[i].y, kr * c.y),
+                                                        fmaf(al, x[i].z, kr * c.z), fmaf(al, x[i].w, kr * c.w)));
+    }
+    if (warp == 0 && col) {
+        u = part[0][1][lane];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) u = fma4(1.f, part[w][1][lane], u);
+        store_elem<BF16>(y, bh * dv + j, scale * fmaf(al, u.x, kq * c.x));
+        store_elem<BF16>(y, bh * dv + j + 1, scale * fmaf(al, u.y, kq * c.y));
+        store_elem<BF16>(y, bh * dv + j + 2, scale * fmaf(al, u.z, kq * c.z));
+        store_elem<BF16>(y, bh * dv + j + 3, scale * fmaf(al, u.w, kq * c.w));
+    }
+}
+
+template <bool BF16>
+cudaError_t launch_dec(const GdeltaShape &s, const void *q, const void *k, const void *v, float *S, float scale, void *y,
+                       cudaStream_t stream)
+{
+    const dim3 grid((unsigned)(s.B * s.H), (s.dv + 127) / 128);
+    if (s.r <= 64) gdelta_decode_kernel<BF16, 8><<<grid, 256, 0, stream>>>(q, k, v, s, S, scale, y);
+    else if (s.r <= 128) gdelta_decode_kernel<BF16, 16><<<grid, 256, 0, stream>>>(q, k, v, s, S, scale, y);
+    else gdelta_decode_kernel<BF16, 32><<<grid, 256, 0, stream>>>(q, k, v, s, S, scale, y);
+    return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_last_passes(const GdeltaShape &s, const GdeltaBackward &g, const float *e, const float *lam, const float *dq,
+                               const float *dk, const float *S_T, float *dG, cudaStream_t stream)
+{
+    const long long tokens = (long long)s.B * s.H * s.T, elems = (long long)s.B * s.Hk * s.T * s.r;
+    float *dal = s.alpha ? g.dalpha : nullptr;
+    if (tokens > 0) {
+        gdelta_token_terms_kernel<BF16><<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(s, g.q, g.v, dq, lam, e, g.dbeta,
+                                                                                        dal ? dG : nullptr);
+        gdelta_group_sum_kernel<BF16><<<(unsigned)((elems + 255) / 256), 256, 0, stream>>>(s, dq, dk, g.dq, g.dk);
+    }
+    if (dal && tokens > 0) gdelta_gate_sum_kernel<<<(unsigned)(s.B * s.H), 256, 0, stream>>>(s, S_T, g.dS_T, dG, dal);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gdelta_rec(const GdeltaShape &s, const GdeltaForward &f, bool bf16, cudaStream_t stream)
+{
+    RecArgs a{};
+    a.s = s;
+    a.q = f.q, a.k = f.k, a.v = f.v, a.y = f.y;
+    a.S_init = f.S0, a.S_fin = f.S_out;
+    a.scale = f.scale;
+    return launch_rec<kFwd>(a, bf16, stream);
+}
+
+cudaError_t launch_gdelta_decode(const GdeltaShape &s, const void *q, const void *k, const void *v, bool bf16, float *S,
+                                 float scale, void *y, cudaStream_t stream)
+{
+    return bf16 ? launch_dec<true>(s, q, k, v, S, scale, y, stream) : launch_dec<false>(s, q, k, v, S, scale, y, stream);
+}
+
+// e, lam [B,H,T,dv]; w (then dk), dq [B,H,T,r]; S_T; dG [B,H,T]
+size_t gdelta_rec_backward_floats(int B, int H, int T, int r, int dv)
+{
+    const size_t tokens = (size_t)B * H * T;
+    return tokens * (2 * (size_t)dv + 2 * (size_t)r + 1) + (size_t)B * H * r * dv;
+}
+
+cudaError_t launch_gdelta_rec_backward(const GdeltaShape &s, const GdeltaBackward &g, bool bf16, cudaStream_t stream)
+{
+    const size_t tokens = (size_t)s.B * s.H * s.T;
+    float *e = g.ws, *lam = e + tokens * s.dv, *w = lam + tokens * s.dv, *dq = w + tokens * s.r, *S_T = dq + tokens * s.r,
+          *dG = S_T + (size_t)s.B * s.H * s.r * s.dv;
+    RecArgs a{};
+    a.s = s;
+    a.q = g.q, a.k = g.k, a.v = g.v, a.dy = g.dy;
+    a.scale = g.scale;
+    a.e = a.e_out = e, a.lam = a.lam_out = lam;
+    a.w = w, a.dq = dq, a.dv_out = g.dv_out;
+    cudaError_t st = cudaSuccess;
+    a.S_init = g.S0, a.S_fin = S_T;
+    if ((st = launch_rec<kFwd>(a, bf16, stream)) != cudaSuccess) return st;
+    a.S_init = g.dS_T, a.S_fin = g.dS0;
+    if ((st = launch_rec<kRev>(a, bf16, stream)) != cudaSuccess) return st;
+    a.S_fin = nullptr;
+    a.S_init = g.S0;
+    if ((st = launch_rec<kQue>(a, bf16, stream)) != cudaSuccess) return st;
+    a.S_init = g.dS_T;
+    if ((st = launch_rec<kKey>(a, bf16, stream)) != cudaSuccess) return st;
+    return bf16 ? launch_last_passes<true>(s, g, e, lam, dq, w, S_T, dG, stream)
+                : launch_last_passes<false>(s, g, e, lam, dq, w, S_T, dG, stream);
+}
+
+}  // namespace la

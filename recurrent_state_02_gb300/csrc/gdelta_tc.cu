@@ -1,0 +1,887 @@
+// gdelta_tc.cu -- the gated delta rule chunk by chunk on the tensor cores (BF16 inputs, FP32 state).
+//
+// With G_i the running sum of log alpha inside a chunk of C = 64 tokens and S the state before it, the errors
+// e_i = v_i - S'^T k_i that the rule writes solve, row by row,
+//     (I + L) E = R,   R = V - e^G K S,   L_ij = e^{G_i - G_j} (k_i . k_j) beta_j  (j < i),
+// so with X = (I + L)^{-1} (unit lower triangular, known from k and the gates alone) and V' = beta E
+//     E = X R,   Y = scale (e^G Q S + A V'),   S_next = e^{G_C} S + K^T (e^{G_C - G} V'),   A_ij = e^{G_i - G_j} q_i . k_j  (j <= i).
+// Every exponent is a difference that is <= 0.
+//
+// A first kernel (gdelta_prep_kernel, one CTA per chunk and head) forms A, X and the gates; the second one
+// (gdelta_chain_kernel, one CTA per head and 128 value columns) carries the state.  It works on transposes: S^T has a value
+// column per TMEM lane, so that the products' left operands (S^T, R^T, V'^T) are what a thread has just computed
+// for its lane and go back to TMEM as they are, never through shared memory; K, Q, X and A are right operands in the
+// layout in which they arrive.  Per chunk
+//     1  P^T = S^T K^T                     R^T = V^T - e^G P^T
+//     2  E^T = R^T X^T                     V'^T = beta E^T
+//     3  dS^T = (e^{G_C - G} V'^T) K       S^T = e^{G_C} S^T + dS^T
+// and off the chain  Q S  after 2 and  A V'  after 3, which the threads turn into y during the next chunk's step 1.
+//
+// Precision: the state lives in FP32 registers.  q, k, v are exact as BF16 operands; what the kernels derive is split into
+// two BF16 parts (16 bits of mantissa and a sign) wherever it reaches the state -- S, R, X and V' in steps 1 to 3, the product of
+// two such parts' low halves left out -- and is rounded to one where it reaches y only (which is BF16).
+
+#include "gdelta_tc.h"
+#include "tc_common.cuh"
+
+namespace la {
+namespace {
+
+constexpr uint32_t kHi128 = desc_hi(1024, 2);   // SBO and swizzle of 128-byte rows
+constexpr uint32_t kTile = kC * 128;            // 8 KB: 64 rows of 64 BF16
+// workspace per chunk and head: A, then X's high and low parts (BF16 shared-memory images), then the gates
+constexpr uint32_t kWsA = 0, kWsX = kTile, kWsGates = 3 * kTile, kGateBytes = 3 * kC * 4, kWsChunk = kWsGates + 1024;
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p)
+{
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ uint4 pack8(const float *f)
+{
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// 2^x, relative error about 2^-22; 0 below 2^-126
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x0, x1 as a high and a low BF16 part each
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x0, x1);
+    lo = pack_bf16x2(x0 - bf16_lo(hi), x1 - bf16_hi(hi));
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], BF16 operands, FP32 accumulator.
+template <bool ACC>
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+
+// The sequence and the chunks of a CTA.
+struct Span {
+    int T;            // tokens of the sequence
+    size_t tok0;      // packed: its first token
+    size_t slot;      // its first chunk in the workspace (times H heads)
+    bool valid;
+};
+
+// Packed sequences: slot_base[b] numbers the chunks of all sequences in order; -1 for one whose bounds are invalid.
+__device__ __forceinline__ Span span_of(const GdeltaTcArgs &a, int b)
+{
+    Span s;
+    if (!a.s.cu_seqlens) {
+        s.T = a.s.T, s.tok0 = 0, s.valid = true;
+        s.slot = (size_t)b * ((a.s.T + kC - 1) / kC);
+        return s;
+    }
+    const int base = a.slot_base[b];
+    s.valid = base >= 0;
+    s.tok0 = s.valid ? a.s.cu_seqlens[b] : 0;
+    s.T = s.valid ? a.s.cu_seqlens[b + 1] - (int)s.tok0 : 0;
+    s.slot = s.valid ? base : 0;
+    return s;
+}
+
+// ------------------------------------------------------------------- the plan
+// Packed sequences, one CTA: checks the bounds, numbers the chunks (slot_base[b], slot_base[B] = their count)
+// and ranks the sequences, longest first (order), so that a long one does not start last.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads)
+gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, int *status)
+{
+    __shared__ int part[32], len[kPlanThreads];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int carry = 0;
+    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int n = 0;
+        bool ok = false;
+        if (b < B) {
+            const int lo = cu[b], hi = cu[b + 1];
+            ok = lo >= 0 && hi >= lo && hi <= total;
+            if (ok) n = (hi - lo + kC - 1) / kC;
+            else atomicExch(status, kStatusShape);
+        }
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) part[warp] = x;
+        len[tid] = ok ? n : -1;
+        __syncthreads();
+        int before = carry, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) before += part[w];
+            all += part[w];
+        }
+        // (sequences that overlap may add up to more chunks than the workspace holds: the rest is left out)
+        if (b < B) slot_base[b] = ok && before + x <= total / kC + B ? before + x - n : -1;
+        if (ok && before + x > total / kC + B) atomicExch(status, kStatusShape);
+        if (B <= kPlanThreads && b < B) {
+            int rank = 0;
+            for (int i = 0; i < B; ++i) rank += len[i] > len[tid] || (len[i] == len[tid] && i < tid);
+            order[rank] = b;
+        } else if (b < B) {
+            order[b] = b;
+        }
+        carry += all;
+        __syncthreads();
+    }
+    if (tid == 0) slot_base[B] = min(carry, total / kC + B);
+}
+
+// ------------------------------------------------------- A, X and the gates
+constexpr int kPThreads = 128;
+constexpr int LD = 68;                           // FP32 row stride of Lt
+constexpr int LDT = 36;                          // FP32 row stride of the 32 x 32 blocks
+// K and Q interleaved by 64-feature block ([K; Q] is one 128-row operand per block); once [G; P] is complete the region
+// holds L and the solve's FP32 blocks, and X's high part in rows of L that the last products do not read
+constexpr uint32_t kPL = 0;                      // Lt (FP32, 64 x LD): Lt[u][i] holds row i, column u
+constexpr uint32_t kPT00 = kPL + kC * LD * 4;    // X00 (FP32, [u][j])
+constexpr uint32_t kPT11t = kPT00 + 32 * LDT * 4;   // X11 transposed (FP32, [u][i])
+constexpr uint32_t kPM = kPT11t + 32 * LDT * 4;  // M = L10 X00 (FP32, [u][j])
+constexpr uint32_t kPXh = 9 * 1024;
+constexpr uint32_t kPXl = 32 * 1024;
+constexpr uint32_t kPGate = kPXl + kTile;        // per token: log2 gate sum (high, low part), beta
+constexpr uint32_t kPSmall = kPGate + kC * 16;
+static_assert(kPM + 32 * LDT * 4 <= kPXl, "L and the solve's blocks fit in the K, Q region");
+static_assert(kPXh >= (uint32_t)(kPL + 32 * LD * 4) && kPXh + kTile <= kPT00, "X's high part lies past what the products read of Lt");
+
+struct alignas(16) PSmall {
+    uint64_t full, mma;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+constexpr uint32_t kPSmemBytes = kPSmall + sizeof(PSmall) + 1024;
+
+__device__ __forceinline__ uint32_t tile_off(int row, int col)
+{
+    return sw128_offset(row, col >> 3) + (uint32_t)(col & 7) * 2;
+}
+
+// One element of X as its two parts in the images.
+__device__ __forceinline__ void put_x(uint8_t *base, int row, int col, float x)
+{
+    const uint32_t h = pack_bf16x2(x, 0.f), o = tile_off(row, col);
+    *reinterpret_cast<uint16_t *>(base + kPXh + o) = (uint16_t)h;
+    *reinterpret_cast<uint16_t *>(base + kPXl + o) = (uint16_t)pack_bf16x2(x - bf16_lo(h), 0.f);
+}
+
+template <int KD>
+__global__ void __launch_bounds__(kPThreads, 5)
+gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const GdeltaTcArgs args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = align1024(smem_raw);
+    PSmall *sm = reinterpret_cast<PSmall *>(base + kPSmall);
+    float *Lt = reinterpret_cast<float *>(base + kPL);
+    float *T00f = reinterpret_cast<float *>(base + kPT00);
+    float *T11t = reinterpret_cast<float *>(base + kPT11t);
+    float *Mf = reinterpret_cast<float *>(base + kPM);
+    float4 *gate = reinterpret_cast<float4 *>(base + kPGate);
+
+    const GdeltaShape &s = args.s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool packed = s.cu_seqlens != nullptr;
+    // this CTA's head, sequence and chunk
+    const int h = blockIdx.x % s.H, hk = h / (s.H / s.Hk);
+    const int slot = blockIdx.x / s.H;
+    int b, c;
+    Span sp;
+    if (packed) {
+        if (slot >= args.slot_base[s.B]) return;
+        // the last sequence that starts at or before the slot, 32 probes at a time (-1: skipped ones are passed over below)
+        int lo = 0, n = s.B;
+        while (n > 0) {
+            const int step = (n + 31) / 32, at = lo + lane * step;
+            bool before = false;
+            if (lane * step < n) {
+                int base_at = -1, i = at;
+                const int end = min(at + step, lo + n);
+                while (i < end && (base_at = args.slot_base[i]) < 0) ++i;
+                before = base_at >= 0 && base_at <= slot;
+            }
+            const uint32_t v = __ballot_sync(0xffffffffu, before);
+            const int last = v ? 31 - __clz(v) : 0;
+            lo += last * step;
+            n = min(step, n - last * step);
+            if (step == 1) break;
+        }
+        b = lo;
+        sp = span_of(args, b);
+        c = slot - (int)sp.slot;
+        if (!sp.valid || c < 0 || c * kC >= sp.T) return;
+    } else {
+        const int nch = (s.T + kC - 1) / kC;
+        b = slot / nch, c = slot % nch;
+        sp = span_of(args, b);
+    }
+    const int t0 = c * kC, nt = min(kC, sp.T - t0);
+    Ctx cx{&sm->abort_flag, kWaitLimitNs, s.status};
+
+    if (tid == 0) {
+        mbar_init(&sm->full, 1);
+        mbar_init(&sm->mma, 1);
+        sm->abort_flag = 0;
+        fence_mbarrier_init();
+        mbar_arrive_expect_tx(&sm->full, KD / 64 * 2 * kTile);
+#pragma unroll
+        for (int x = 0; x < KD / 64; ++x) {
+            uint8_t *dst = base + x * 2 * kTile;
+            if (packed) {
+                tma_load_3d(dst, &map_k, &sm->full, 64 * x, hk, (int)sp.tok0 + t0);
+                tma_load_3d(dst + kTile, &map_q, &sm->full, 64 * x, hk, (int)sp.tok0 + t0);
+            } else {
+                tma_load_3d(dst, &map_k, &sm->full, 64 * x, t0, b * s.Hk + hk);
+                tma_load_3d(dst + kTile, &map_q, &sm->full, 64 * x, t0, b * s.Hk + hk);
+            }
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm->tmem_base, 64);
+        tmem_relinquish();
+    }
+    uint8_t *wsc = args.ws + ((size_t)slot * s.H + h) * kWsChunk;
+    if (warp == 0) {
+        // G in 64 bits, kept as two FP32 parts: differences over a few tokens stay exact to FP32 behind gates near 0.
+        // A gate of 0 counts as 2^-400, which every exponential takes to 0.
+        const int i0 = 2 * lane;
+        float al[2], be[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = t0 + i0 + e;
+            const size_t at = packed ? (sp.tok0 + t) * s.H + h : ((size_t)b * s.H + h) * s.T + t;
+            const bool in = i0 + e < nt;
+            al[e] = in && s.alpha ? s.alpha[at] : 1.f;
+            be[e] = in ? (s.beta ? s.beta[at] : 1.f) : 0.f;
+        }
+        const double l0 = al[0] > 0.f ? (double)log2f(al[0]) : -400.0, l1 = al[1] > 0.f ? (double)log2f(al[1]) : -400.0;
+        double inc = l0 + l1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const double total = __shfl_sync(0xffffffffu, inc, 31);
+        float *g = reinterpret_cast<float *>(wsc + kWsGates);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const double G = e ? inc : inc - l1;
+            const float hi = (float)G;
+            gate[i0 + e] = make_float4(hi, (float)(G - hi), be[e], 0.f);
+            g[i0 + e] = ex2((float)G);
+            g[kC + i0 + e] = ex2((float)(total - G));
+            g[2 * kC + i0 + e] = be[e];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+
+    // [G; P] = [K; Q] K^T (M = 128: G in TMEM lanes 0..63, P in lanes 64..127)
+    bool ok = true, issued = false;
+    if (warp == 1) {
+        ok = warp_wait(cx, &sm->full, 0);
+        if (ok && lane == 0) {
+            tc_fence_after();
+            constexpr uint32_t id = idesc_bf16_f32(128, 64, false, false);
+            const uint32_t klo = desc_lo(smem_u32(base), 16);
+#pragma unroll
+            for (int kk = 0; kk < KD / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * 2 * kTile + (kk & 3) * 32) >> 4;
+                if (kk == 0) tc_mma_bf16_w<false>(tmem, klo, kHi128, klo, kHi128, id);
+                else tc_mma_bf16_w<true>(tmem, klo + o, kHi128, klo + o, kHi128, id);
+            }
+            tc_commit(&sm->mma);
+            issued = true;
+        }
+        __syncwarp();
+    }
+    ok = warp_wait(cx, &sm->mma, 0) && ok;
+    tc_fence_after();
+    if (!__syncthreads_or(!ok)) {
+        // Warps 0, 1 (TMEM lanes 0..63): row ri of L, transposed into Lt.  Warps 2, 3: row ri of A, as its image.  Rows
+        // and columns past the sequence's end (which hold another one's tokens) count as 0.
+        {
+            const int ri = 32 * (warp & 1) + lane;
+            float v0[32], v1[32];
+            const uint32_t tq = tmem + ((uint32_t)(32 * warp) << 16);
+            tc_ld_32x32b_x32(tq, v0);
+            if (warp & 1) tc_ld_32x32b_x32(tq + 32, v1);
+            tc_wait_ld();
+            const float4 gi = gate[ri];
+            const int end = ri < nt ? ri : -1;         // the last column of A's row, one past L's
+            if (warp < 2) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    if (j >= 32 && !(warp & 1)) break;
+                    const float4 gj = gate[j];
+                    const float x = ex2((gi.x - gj.x) + (gi.y - gj.y)) * (j < 32 ? v0[j & 31] : v1[j & 31]) * gj.z;
+                    Lt[j * LD + ri] = j < end ? x : 0.f;
+                }
+            } else {
+                uint8_t *arow = wsc + kWsA + (size_t)ri * 128;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    float a[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = 8 * x + e;
+                        a[e] = 0.f;
+                        if (j < 32 || (warp & 1)) {
+                            const float4 gj = gate[j];
+                            const float p = ex2((gi.x - gj.x) + (gi.y - gj.y)) * (j < 32 ? v0[j & 31] : v1[j & 31]);
+                            a[e] = j <= end ? p : 0.f;
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(arow + ((x ^ (ri & 7)) << 4)) = pack8(a);
+                }
+            }
+        }
+        __syncthreads();
+        // X00, X11 by forward substitution: lane j of warp 0 (1) owns column j of the block; after step u, acc[u] is final and
+        // is subtracted from the rows below.
+        float acc[32];
+        if (warp < 2) {
+            const int bb = 32 * warp;
+            const float *Lb = Lt + bb * LD + bb;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+            for (int u = 0; u < 31; ++u) {
+                const float t = acc[u];
+#pragma unroll
+                for (int g4 = (u + 1) >> 2; g4 < 8; ++g4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(Lb + u * LD + 4 * g4);
+                    const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * g4 + e > u) acc[4 * g4 + e] = fmaf(-lv[e], t, acc[4 * g4 + e]);
+                }
+            }
+            if (warp == 0) {
+#pragma unroll
+                for (int u = 0; u < 32; ++u) T00f[u * LDT + lane] = acc[u];
+            } else {
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+                    *reinterpret_cast<float4 *>(T11t + lane * LDT + 4 * m) =
+                        make_float4(acc[4 * m], acc[4 * m + 1], acc[4 * m + 2], acc[4 * m + 3]);
+            }
+        }
+        __syncthreads();
+        // both substitutions are done: X00 and X11 into the images (over Lt's last rows), and zeros above the diagonal
+        if (warp < 2) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) put_x(base, 32 * warp + u, 32 * warp + lane, acc[u]);
+        } else {
+            const int i = tid - 64;   // rows 0..31 of the images, two of their upper 16-byte chunks each
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t o = sw128_offset(i >> 1, 4 + 2 * (i & 1) + x);
+                *reinterpret_cast<uint4 *>(base + kPXh + o) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(base + kPXl + o) = make_uint4(0, 0, 0, 0);
+            }
+        }
+        // M = L10 X00 and then X10 = -X11 M: thread (warp, lane) computes rows 4 rg .. 4 rg + 3 and columns 2 cp, 2 cp + 1,
+        // rg = 2 warp + lane / 16
+        const int rg = 2 * warp + (lane >> 4), cp = lane & 15;
+        {
+            float2 m4[4] = {};
+#pragma unroll 8
+            for (int u = 0; u < 32; ++u) {
+                const float2 tj = *reinterpret_cast<const float2 *>(T00f + u * LDT + 2 * cp);
+                const float4 g = *reinterpret_cast<const float4 *>(Lt + u * LD + 32 + 4 * rg);
+                const float gv[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m4[e] = __ffma2_rn(make_float2(gv[e], gv[e]), tj, m4[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(Mf + (4 * rg + e) * LDT + 2 * cp) = m4[e];
+        }
+        __syncthreads();
+        {
+            float2 o4[4] = {};
+#pragma unroll 8
+            for (int u = 0; u < 32; ++u) {
+                const float2 mj = *reinterpret_cast<const float2 *>(Mf + u * LDT + 2 * cp);
+                const float4 a = *reinterpret_cast<const float4 *>(T11t + u * LDT + 4 * rg);
+                const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o4[e] = __ffma2_rn(make_float2(av[e], av[e]), mj, o4[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t hi, lo;
+                split2(-o4[e].x, -o4[e].y, hi, lo);
+                const uint32_t o = tile_off(32 + 4 * rg + e, 2 * cp);
+                *reinterpret_cast<uint32_t *>(base + kPXh + o) = hi;
+                *reinterpret_cast<uint32_t *>(base + kPXl + o) = lo;
+            }
+        }
+        __syncthreads();
+        uint4 *dst = reinterpret_cast<uint4 *>(wsc + kWsX);
+        for (int x = tid; x < (int)(kTile / 16); x += kPThreads) {
+            dst[x] = reinterpret_cast<const uint4 *>(base + kPXh)[x];
+            dst[x + kTile / 16] = reinterpret_cast<const uint4 *>(base + kPXl)[x];
+        }
+    } else {
+        // gave up waiting: the copy and the MMAs already started complete before the CTA exits
+        if (tid == 0) mbar_wait(&sm->full, 0, cx.limit);
+        if (warp == 1 && lane == 0 && issued) mbar_wait(&sm->mma, 0, cx.limit);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 64);
+    }
+}
+
+// ------------------------------------------------------------------ the chain
+constexpr int kTmWarps = 8, kIssuer = 8, kLoader = 9;   // warps 0..7 own the lanes, 8 issues MMAs, 9 loads
+constexpr int kMThreads = 32 * (kLoader + 1);
+constexpr int kGateRing = 4;
+template <int KD>
+struct ChainCfg {
+    static constexpr uint32_t kTK = KD / 64 * kTile;    // a K or Q tile (64-feature blocks)
+    // a stage (two): K, Q, V (two blocks of 64 columns), X's two parts, A
+    static constexpr uint32_t kSK = 0, kSQ = kTK, kSV = 2 * kTK, kSX = kSV + 2 * kTile, kSA = kSX + 2 * kTile, kStage = kSA + kTile;
+    static constexpr uint32_t kGates = 2 * kStage;      // ring of kGateRing
+    static constexpr uint32_t kSmall = kGates + kGateRing * 1024;
+};
+// TMEM columns: the left operands S^T (two parts), R^T (two parts, then those of the decayed V'^T) and V'^T; the accumulators
+// P^T (then E^T, then dS^T), (Q S)^T and (A V')^T
+constexpr uint32_t kcS = 0, kcP = 128, kcQS = 256, kcAV = 320, kcR = 384, kcV = 448;
+
+struct alignas(16) MSmall {
+    uint64_t full_k[2], full_vx[2], full_qa[2];
+    uint64_t got_s, got_r, got_v;       // the lanes' operands are in TMEM (8 warps)
+    uint64_t done1, done2;              // P, E
+    // dS, and Q S and A V', of even and odd chunks (the loader may look at them late, but not two chunks late)
+    uint64_t done3[2], done4[2];
+    uint64_t fin;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <int KD>
+constexpr uint32_t kMSmemBytes = ChainCfg<KD>::kSmall + sizeof(MSmall) + 1024;
+static_assert(kMSmemBytes<128> <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t (&w)[16])
+{
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]);
+    tc_st_32x32b_x16(addr, f);
+}
+
+template <int KD>
+__global__ void __launch_bounds__(kMThreads, 1)
+gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, const GdeltaTcArgs args)
+{
+    using Cfg = ChainCfg<KD>;
+    constexpr int KH = KD / 2;                  // state rows per thread (a thread has a column, half its rows)
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = align1024(smem_raw);
+    MSmall *sm = reinterpret_cast<MSmall *>(base + Cfg::kSmall);
+
+    const GdeltaShape &s = args.s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool packed = s.cu_seqlens != nullptr;
+    const int tiles = (s.dv + 127) / 128;
+    const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % s.H, hk = h / (s.H / s.Hk);
+    int b = blockIdx.x / (tiles * s.H);
+    if (packed) b = args.order[b];
+    const Span sp = span_of(args, b);
+    if (!sp.valid) return;
+    const int T = sp.T, nch = (T + kC - 1) / kC;
+    const int ncols = min(128, s.dv - 128 * tile);      // of this CTA: 128 or 64
+    const uint8_t *ws = args.ws + (sp.slot * s.H + h) * kWsChunk;
+    const size_t ws_step = (size_t)s.H * kWsChunk;      // from one chunk to the next
+    Ctx cx{&sm->abort_flag, kWaitLimitNs, s.status};
+    const bool issuer = warp == kIssuer, loader = warp == kLoader;
+
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->full_k[i], 1);
+            mbar_init(&sm->full_vx[i], 1);
+            mbar_init(&sm->full_qa[i], 1);
+            mbar_init(&sm->done3[i], 1);
+            mbar_init(&sm->done4[i], 1);
+        }
+        mbar_init(&sm->got_s, kTmWarps);
+        mbar_init(&sm->got_r, kTmWarps);
+        mbar_init(&sm->got_v, kTmWarps);
+        mbar_init(&sm->done1, 1);
+        mbar_init(&sm->done2, 1);
+        mbar_init(&sm->fin, 1);
+        sm->abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (issuer) {
+        tmem_alloc(&sm->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+
+    if (loader) {
+        auto tok = [&](void *dst, const CUtensorMap *map, uint64_t *bar, int x, int n, int heads, int head) {
+            if (packed) tma_load_3d(dst, map, bar, x, head, (int)sp.tok0 + n * kC);
+            else tma_load_3d(dst, map, bar, x, n * kC, b * heads + head);
+        };
+        auto load_k = [&](int n) {
+            uint8_t *st = base + (n & 1) * Cfg::kStage;
+            uint64_t *bar = &sm->full_k[n & 1];
+            mbar_arrive_expect_tx(bar, Cfg::kTK);
+#pragma unroll
+            for (int x = 0; x < KD / 64; ++x) tok(st + Cfg::kSK + x * kTile, &map_k, bar, 64 * x, n, s.Hk, hk);
+        };
+        auto load_vx = [&](int n) {
+            uint8_t *st = base + (n & 1) * Cfg::kStage;
+            uint64_t *bar = &sm->full_vx[n & 1];
+            const uint8_t *w = ws + n * ws_step;
+            mbar_arrive_expect_tx(bar, ncols / 64 * kTile + 2 * kTile + kGateBytes);
+            for (int x = 0; x < ncols / 64; ++x) tok(st + Cfg::kSV + x * kTile, &map_v, bar, 128 * tile + 64 * x, n, s.H, h);
+            bulk_load(base + Cfg::kGates + (n % kGateRing) * 1024, w + kWsGates, kGateBytes, bar);
+            bulk_load(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
+        };
+        auto load_qa = [&](int n) {
+            uint8_t *st = base + (n & 1) * Cfg::kStage;
+            uint64_t *bar = &sm->full_qa[n & 1];
+            mbar_arrive_expect_tx(bar, Cfg::kTK + kTile);
+#pragma unroll
+            for (int x = 0; x < KD / 64; ++x) tok(st + Cfg::kSQ + x * kTile, &map_q, bar, 64 * x, n, s.Hk, hk);
+            bulk_load(st + Cfg::kSA, ws + n * ws_step + kWsA, kTile, bar);
+        };
+        int n1 = 0, n2 = 0;                    // chunks whose K, V, X / Q, A loads were started
+        for (; n1 < 2 && n1 < nch; n1 = ++n2)
+            if (lane == 0) load_k(n1), load_vx(n1), load_qa(n1);
+        bool ok = true;
+        for (int n = 0; n + 2 < nch && ok; ++n) {
+            // step 3 of chunk n has read K (and before it V, X and Q were read), A V' after it A
+            ok = warp_wait(cx, &sm->done3[n & 1], (n >> 1) & 1);
+            if (!ok) break;
+            if (lane == 0) load_k(n + 2), load_vx(n + 2);
+            n1 = n + 3;
+            ok = warp_wait(cx, &sm->done4[n & 1], (n >> 1) & 1);
+            if (!ok) break;
+            if (lane == 0) load_qa(n + 2);
+            n2 = n + 3;
+        }
+        // loads still in flight complete before the CTA exits (also after a wait that was given up)
+        if (lane == 0) {
+            for (int i = n1 > 2 ? n1 - 2 : 0; i < n1; ++i) {
+                mbar_wait(&sm->full_k[i & 1], (i >> 1) & 1, cx.limit);
+                mbar_wait(&sm->full_vx[i & 1], (i >> 1) & 1, cx.limit);
+            }
+            for (int i = n2 > 2 ? n2 - 2 : 0; i < n2; ++i) mbar_wait(&sm->full_qa[i & 1], (i >> 1) & 1, cx.limit);
+        }
+        __syncwarp();
+    } else if (issuer) {
+        if (lane == 0) {
+            constexpr uint32_t id64 = idesc_bf16_f32(128, 64, false, false), idS = idesc_bf16_f32(128, KD, false, true);
+            bool ok = true;
+            for (int n = 0; n < nch && ok; ++n) {
+                const uint32_t st = smem_u32(base + (n & 1) * Cfg::kStage), ph = n & 1, fph = (n >> 1) & 1;
+                // 1  P^T = S^T K^T, both parts of S
+                ok = wait<0>(cx, &sm->full_k[n & 1], fph) && wait<0>(cx, &sm->got_s, ph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t klo = desc_lo(st + Cfg::kSK, 16), xlo = desc_lo(st + Cfg::kSX, 16);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int kk = 0; kk < KD / 16; ++kk) {
+                        const uint32_t a = tmem + kcS + p * KH + kk * 8, bo = klo + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4);
+                        if (p == 0 && kk == 0) tc_mma_ts<false>(tmem + kcP, a, bo, kHi128, id64);
+                        else tc_mma_ts<true>(tmem + kcP, a, bo, kHi128, id64);
+                    }
+                tc_commit(&sm->done1);
+                // 2  E^T = R^T X^T: high X with both parts of R, low X with the high one
+                ok = wait<0>(cx, &sm->full_vx[n & 1], fph) && wait<0>(cx, &sm->got_r, ph);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t a = tmem + kcR + (p == 1 ? 32 : 0) + kk * 8, bo = xlo + (((p == 2 ? kTile : 0) + kk * 32) >> 4);
+                        if (p == 0 && kk == 0) tc_mma_ts<false>(tmem + kcP, a, bo, kHi128, id64);
+                        else tc_mma_ts<true>(tmem + kcP, a, bo, kHi128, id64);
+                    }
+                tc_commit(&sm->done2);
+                // (Q S)^T
+                ok = wait<0>(cx, &sm->full_qa[n & 1], fph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t qlo = desc_lo(st + Cfg::kSQ, 16), alo = desc_lo(st + Cfg::kSA, 16);
+#pragma unroll
+                for (int kk = 0; kk < KD / 16; ++kk) {
+                    const uint32_t a = tmem + kcS + kk * 8, bo = qlo + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4);
+                    if (kk == 0) tc_mma_ts<false>(tmem + kcQS, a, bo, kHi128, id64);
+                    else tc_mma_ts<true>(tmem + kcQS, a, bo, kHi128, id64);
+                }
+                // 3  dS^T = V'^T K, both parts of the decayed V'
+                ok = wait<0>(cx, &sm->got_v, ph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t kmn = desc_lo(st + Cfg::kSK, kTile);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t a = tmem + kcR + p * 32 + kk * 8, bo = kmn + kk * (2048 >> 4);
+                        if (p == 0 && kk == 0) tc_mma_ts<false>(tmem + kcP, a, bo, kHi128, idS);
+                        else tc_mma_ts<true>(tmem + kcP, a, bo, kHi128, idS);
+                    }
+                tc_commit(&sm->done3[n & 1]);
+                // (A V')^T
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t a = tmem + kcV + kk * 8, bo = alo + ((kk * 32) >> 4);
+                    if (kk == 0) tc_mma_ts<false>(tmem + kcAV, a, bo, kHi128, id64);
+                    else tc_mma_ts<true>(tmem + kcAV, a, bo, kHi128, id64);
+                }
+                tc_commit(&sm->done4[n & 1]);
+            }
+            // every MMA completes before the CTA exits
+            tc_commit(&sm->fin);
+            mbar_wait(&sm->fin, 0, cx.limit);
+        }
+        __syncwarp();
+    } else {
+        // lane quadrant q4, half ch of the columns (tokens, or state rows)
+        const int q4 = warp & 3, ch = warp >> 2;
+        const uint32_t tq = tmem + ((uint32_t)(32 * q4) << 16);
+        const int d = 32 * q4 + lane;                   // value column of the CTA
+        const bool live = d < ncols;
+        const size_t bh = (size_t)b * s.H + h;
+        float S[KH];                                    // S[i]: state row KH ch + i of the lane's column
+        const size_t s_at = (bh * KD + KH * ch) * s.dv + 128 * tile + d;
+#pragma unroll
+        for (int i = 0; i < KH; ++i) S[i] = args.S0 && live ? args.S0[s_at + (size_t)i * s.dv] : 0.f;
+        auto put_s = [&]() {
+#pragma unroll
+            for (int x = 0; x < KH / 32; ++x) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split2(S[32 * x + 2 * i], S[32 * x + 2 * i + 1], hi[i], lo[i]);
+                tm_store(tq + kcS + KH / 2 * ch + 16 * x, hi);
+                tm_store(tq + kcS + KH + KH / 2 * ch + 16 * x, lo);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            warp_arrive(&sm->got_s);
+        };
+        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * s.H + h) * s.dv : bh * s.T * s.dv) + 128 * tile + d;
+        const size_t y_step = packed ? (size_t)s.H * s.dv : s.dv;
+        // y of chunk n, tokens 32 ch ..
+        auto store_y = [&](int n) {
+            const float4 *eg = reinterpret_cast<const float4 *>(base + Cfg::kGates + (n % kGateRing) * 1024 + 128 * ch);
+            const int left = T - n * kC - 32 * ch;
+            uint16_t *yp = y0 + (size_t)(n * kC + 32 * ch) * y_step;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float qs[16], av[16];
+                tc_ld_32x32b_x16(tq + kcQS + 32 * ch + 16 * x, qs);
+                tc_ld_32x32b_x16(tq + kcAV + 32 * ch + 16 * x, av);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 g = eg[4 * x + (i >> 2)];
+                    const float gi = (i & 3) == 0 ? g.x : (i & 3) == 1 ? g.y : (i & 3) == 2 ? g.z : g.w;
+                    const float o = args.scale * fmaf(gi, qs[i], av[i]);
+                    if (live && 16 * x + i < left) yp[(16 * x + i) * y_step] = (uint16_t)(pack_bf16x2(o, 0.f) & 0xffffu);
+                }
+            }
+        };
+        bool ok = true;
+        if (nch > 0) put_s();
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t ph = n & 1;
+            uint8_t *st = base + (n & 1) * Cfg::kStage;
+            const float *gates = reinterpret_cast<const float *>(base + Cfg::kGates + (n % kGateRing) * 1024);
+            const int left = T - n * kC;                // tokens from this chunk on
+            if (n > 0) {
+                ok = warp_wait(cx, &sm->done4[(n - 1) & 1], ((n - 1) >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                store_y(n - 1);
+            }
+            // this thread's column of V, tokens 32 ch ..
+            ok = warp_wait(cx, &sm->full_vx[n & 1], (n >> 1) & 1);
+            if (!ok) break;
+            uint32_t v[16];
+            {
+                const uint8_t *vt = st + Cfg::kSV + (d >> 6) * kTile;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = 32 * ch + 2 * i;
+                    const uint32_t lo = live && t < left ? *reinterpret_cast<const uint16_t *>(vt + tile_off(t, d & 63)) : 0;
+                    const uint32_t hi = live && t + 1 < left ? *reinterpret_cast<const uint16_t *>(vt + tile_off(t + 1, d & 63)) : 0;
+                    v[i] = lo | hi << 16;
+                }
+            }
+            // R^T = V^T - e^G P^T (0 past the sequence's end)
+            ok = warp_wait(cx, &sm->done1, ph);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                float p[32];
+                tc_ld_32x32b_x32(tq + kcP + 32 * ch, p);
+                tc_wait_ld();
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 g = *reinterpret_cast<const float2 *>(gates + 32 * ch + 2 * i);
+                    float r0 = fmaf(-g.x, p[2 * i], bf16_lo(v[i]));
+                    float r1 = fmaf(-g.y, p[2 * i + 1], bf16_hi(v[i]));
+                    if (left < kC) {
+                        if (32 * ch + 2 * i >= left) r0 = 0.f;
+                        if (32 * ch + 2 * i + 1 >= left) r1 = 0.f;
+                    }
+                    split2(r0, r1, hi[i], lo[i]);
+                }
+                tm_store(tq + kcR + 16 * ch, hi);
+                tm_store(tq + kcR + 32 + 16 * ch, lo);
+                if (packed && left < kC) {
+                    // rows of K past the end hold another sequence's keys, which step 3 multiplies by 0: they become 0 (step 1
+                    // has read the tile)
+                    for (int x = tid; x < (kC - left) * (KD / 8); x += 32 * kTmWarps) {
+                        const int row = left + x / (KD / 8), c16 = x % (KD / 8);
+                        *reinterpret_cast<uint4 *>(st + Cfg::kSK + (c16 >> 3) * kTile + sw128_offset(row, c16 & 7)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                warp_arrive(&sm->got_r);
+            }
+            // V'^T = beta E^T, and decayed to the chunk's end
+            ok = warp_wait(cx, &sm->done2, ph);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                float e[32];
+                tc_ld_32x32b_x32(tq + kcP + 32 * ch, e);
+                tc_wait_ld();
+                uint32_t vp[16], hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 be = *reinterpret_cast<const float2 *>(gates + 2 * kC + 32 * ch + 2 * i);
+                    const float2 er = *reinterpret_cast<const float2 *>(gates + kC + 32 * ch + 2 * i);
+                    const float w0 = be.x * e[2 * i], w1 = be.y * e[2 * i + 1];
+                    vp[i] = pack_bf16x2(w0, w1);
+                    split2(er.x * w0, er.y * w1, hi[i], lo[i]);
+                }
+                tm_store(tq + kcR + 16 * ch, hi);
+                tm_store(tq + kcR + 32 + 16 * ch, lo);
+                tm_store(tq + kcV + 16 * ch, vp);
+                tc_wait_st();
+                tc_fence_before();
+                warp_arrive(&sm->got_v);
+            }
+            const float gC = gates[kC - 1];
+            ok = warp_wait(cx, &sm->done3[n & 1], (n >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < KH / 32; ++x) {
+                float ds[32];
+                tc_ld_32x32b_x32(tq + kcP + KH * ch + 32 * x, ds);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[32 * x + i] = fmaf(gC, S[32 * x + i], ds[i]);
+            }
+            if (n + 1 < nch) put_s();
+        }
+        if (ok) {
+            if (nch > 0) {
+                ok = warp_wait(cx, &sm->done4[(nch - 1) & 1], ((nch - 1) >> 1) & 1);
+                if (ok) {
+                    tc_fence_after();
+                    store_y(nch - 1);
+                }
+            }
+            if (ok && live) {
+#pragma unroll
+                for (int i = 0; i < KH; ++i) args.S_out[s_at + (size_t)i * s.dv] = S[i];
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (issuer) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+}  // namespace
+
+long long gdelta_tc_slots(int B, int T, bool packed)
+{
+    return packed ? (long long)T / kC + B : (long long)B * ((T + kC - 1) / kC);
+}
+
+size_t gdelta_tc_plan_bytes(int B) { return round_up((2 * (size_t)B + 1) * sizeof(int), 256); }
+
+size_t gdelta_tc_workspace_bytes(int B, int H, int T, bool packed)
+{
+    return (packed ? gdelta_tc_plan_bytes(B) : 0) + (size_t)gdelta_tc_slots(B, T, packed) * H * kWsChunk;
+}
+
+template <int KD>
+static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream)
+{
+    static OncePerDevice once_p, once_m;
+    cudaError_t e = set_smem_once(gdelta_prep_kernel<KD>, kPSmemBytes, once_p);
+    if (e != cudaSuccess) return e;
+    e = set_smem_once(gdelta_chain_kernel<KD>, kMSmemBytes<KD>, once_m);
+    if (e != cudaSuccess) return e;
+    const GdeltaShape &s = a.s;
+    const long long nprep = gdelta_tc_slots(s.B, s.T, s.cu_seqlens != nullptr) * s.H,
+                    nmain = (long long)s.B * s.H * ((s.dv + 127) / 128);
+    if (nprep > 0x7fffffffLL || nmain > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (s.cu_seqlens) {
+        gdelta_plan_kernel<<<1, kPlanThreads, 0, stream>>>(s.cu_seqlens, s.B, s.T, a.slot_base, a.order, s.status);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (nprep > 0) gdelta_prep_kernel<KD><<<(unsigned)nprep, kPThreads, kPSmemBytes, stream>>>(m.q, m.k, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    gdelta_chain_kernel<KD><<<(unsigned)nmain, kMThreads, kMSmemBytes<KD>, stream>>>(m.q, m.k, m.v, a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream)
+{
+    return a.s.r == 64 ? launch_as<64>(m, a, stream) : launch_as<128>(m, a, stream);
+}
+
+}  // namespace la

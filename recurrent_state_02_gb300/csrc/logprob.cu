@@ -1,0 +1,503 @@
+// logprob.cu -- scoring given tokens: log-probabilities, entropy and best alternatives of rows of logits, and
+// the gradient of the first two.
+//
+//     lse = log sum_v exp x_v,   logprob = x_token - lse,   H = lse - sum_v p_v x_v,   p_v = exp(x_v - lse)
+//     dL/dx_v = dlogprob (1[v = token] - p_v) - dH p_v (log p_v + H)
+
+#include "gdelta.h"
+#include "sm103_ptx.cuh"
+
+#include <cuda_bf16.h>
+
+namespace la {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e38f;
+
+// 2^x, relative error about 2^-22 (results below 2^-126 are 0: nothing next to the maximum's 1)
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Order-preserving map of a float (not NaN) to unsigned; -0 counts as +0.
+__device__ __forceinline__ uint32_t order_f32(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float unorder_f32(uint32_t o)
+{
+    return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
+}
+// Keys that order by value, then by lower index; 0 is none.
+__device__ __forceinline__ unsigned long long make_key(float x, int i)
+{
+    return (static_cast<unsigned long long>(order_f32(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(i));
+}
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long k)
+{
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+    return (static_cast<unsigned long long>(hi) << 32) | lo;
+}
+
+template <typename T>
+__device__ __forceinline__ T *in_cta(T *p, uint32_t rank)
+{
+    uint64_t out;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<T *>(out);
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 ld_once(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen(uint4 w, float *x)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (BF16) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        } else {
+            x[i] = __uint_as_float(u[i]);
+        }
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_elem(const void *p, long long i)
+{
+    return BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16) : static_cast<const float *>(p)[i];
+}
+
+// Granule `lane` of block `blk` of a row of V elements: 16 bytes of an aligned row, else elements 32 apart
+// (element e of the granule is element granule_first + e * ES of the row).  -infinity past the row's end.
+template <bool BF16, bool ALIGNED>
+__device__ __forceinline__ uint4 load_granule(const void *row, int blk, int lane, int V)
+{
+    constexpr int GE = BF16 ? 8 : 4, ES = ALIGNED ? 1 : 32;
+    const int i0 = ALIGNED ? (blk * 32 + lane) * GE : blk * 32 * GE + lane;
+    if (ALIGNED && i0 + GE <= V) return ld_once(reinterpret_cast<const uint4 *>(row) + (blk * 32 + lane));
+    uint32_t x[GE], w[4];
+#pragma unroll
+    for (int e = 0; e < GE; ++e) {
+        x[e] = BF16 ? 0xff80u : 0xff800000u;
+        if (i0 + ES * e < V)
+            x[e] = BF16 ? static_cast<const uint16_t *>(row)[i0 + ES * e] : static_cast<const uint32_t *>(row)[i0 + ES * e];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = BF16 ? x[2 * j] | x[2 * j + 1] << 16 : x[j];
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------- scoring
+// One cluster of CS CTAs of 8 warps per row, one pass over the row: every lane carries a running maximum m, the sum
+// s of 2^a and the sum w of a 2^a, a = (x - m) log2 e, from which lse and the entropy follow.  The alternatives come
+// almost free: the pass leaves the largest logit of each of a CTA's 64 groups of blocks, and the top-th largest of
+// those bounds the top-th best from below, so only blocks that reach it are read again (about as many as there are
+// alternatives, out of L2), and what reaches it is sorted.
+// Bound by HBM and, within a fifth of it, by exponentials and issue slots.
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kEntries = 64;       // block maxima per warp: an entry covers 2^shift of its blocks
+constexpr int kGroups = 64;        // of a CTA's entries: 8 per warp
+constexpr int kCand = 512;
+
+struct ScoreSmem {
+    uint32_t entry[kWarps][kEntries];              // order_f32 of the maximum (0: no logit above -infinity)
+    uint32_t group[kGroups];
+    unsigned long long cand[kCand];
+    unsigned long long best[kMaxTop];              // this CTA's
+    float m[kWarps], s[kWarps], w[kWarps];
+    float cm, cs, cw;                              // the CTA's
+    int count;
+};
+
+// Merges (m, s, w) of two parts.
+__device__ __forceinline__ void merge(float &m, float &s, float &w, float m2, float s2, float w2)
+{
+    const float mm = fmaxf(m, m2);
+    // (an empty part has s = 0 and m = kLowest: its difference must not become 0 * infinity)
+    const float d1 = fmaxf((m - mm) * kLog2e, -400.f), d2 = fmaxf((m2 - mm) * kLog2e, -400.f);
+    const float c1 = ex2(d1), c2 = ex2(d2);
+    w = (w + s * d1) * c1 + (w2 + s2 * d2) * c2;
+    s = s * c1 + s2 * c2;
+    m = mm;
+}
+
+template <bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads)
+token_logprobs_kernel(const LogprobArgs args)
+{
+    constexpr int GE = BF16 ? 8 : 4, ES = ALIGNED ? 1 : 32, U = 4;
+    __shared__ ScoreSmem sm;
+    const int V = args.V, top = args.top;
+    const uint32_t rank = blockIdx.x, cs = gridDim.x;   // the cluster spans the grid's x axis
+    const long long n = blockIdx.y + (long long)gridDim.y * blockIdx.z;
+    if (n >= args.N) return;                            // (the whole cluster)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int token = args.tokens[n];
+    if (token < 0 || token >= V) {
+        if (rank == 0) {
+            if (tid == 0) {
+                args.logprobs[n] = 0.f;
+                if (args.entropy) args.entropy[n] = 0.f;
+                if (args.lse) args.lse[n] = 0.f;
+                if (token >= V) atomicExch(args.status, kStatusShape);
+            }
+            if (tid < top) args.top_logprobs[n * top + tid] = -INFINITY, args.top_tokens[n * top + tid] = -1;
+        }
+        return;
+    }
+    const unsigned char *row = static_cast<const unsigned char *>(args.logits) + n * args.row_stride * (BF16 ? 2 : 4);
+    const float x_token = rank == 0 && tid == 0 ? load_elem<BF16>(row, token) : 0.f;
+    const int blocks = (V + 32 * GE - 1) / (32 * GE);
+    const int nw = kWarps * cs, gw = rank * kWarps + warp;
+    int shift = 0;
+    while (((blocks + nw - 1) / nw - 1) >> shift >= kEntries) ++shift;
+    if (top) {
+        for (int i = tid; i < kWarps * kEntries; i += kThreads) (&sm.entry[0][0])[i] = 0;
+        if (tid == 0) sm.count = 0;
+        __syncthreads();
+    }
+    float m = kLowest, s = 0.f, w = 0.f;
+    for (int j = 0, blk = gw; blk < blocks; j += U, blk += U * nw) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (blk + u * nw < blocks) raw[u] = load_granule<BF16, ALIGNED>(row, blk + u * nw, lane, V);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (blk + u * nw >= blocks) break;
+            float x[GE];
+            widen<BF16>(raw[u], x);
+            float mx = x[0];
+#pragma unroll
+            for (int e = 1; e < GE; ++e) mx = fmaxf(mx, x[e]);   // (a NaN reaches the sums below)
+            if (mx > m) {
+                const float d = fmaxf((m - mx) * kLog2e, -400.f);
+                w = (w + s * d) * ex2(d);
+                s *= ex2(d);
+                m = mx;
+            }
+            const float2 minus = make_float2(-m, -m), l2 = make_float2(kLog2e, kLog2e);
+            float2 t = make_float2(0.f, 0.f), tw = t;
+#pragma unroll
+            for (int e = 0; e < GE; e += 2) {
+                float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), minus), l2);
+                // (a masked logit's a would be -infinity, and a 2^a not a number; a NaN stays one)
+                a.x = a.x < -200.f ? -200.f : a.x;
+                a.y = a.y < -200.f ? -200.f : a.y;
+                const float2 p = make_float2(ex2(a.x), ex2(a.y));
+                t = __fadd2_rn(t, p);
+                tw = __ffma2_rn(a, p, tw);
+            }
+            s += t.x + t.y;
+            w += tw.x + tw.y;
+            if (top) {
+                const uint32_t o = __reduce_max_sync(0xffffffffu, mx > -INFINITY ? order_f32(mx) : 0u);
+                uint32_t &en = sm.entry[warp][(j + u) >> shift];
+                if (lane == 0 && o > en) en = o;
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o),
+                    w2 = __shfl_xor_sync(0xffffffffu, w, o);
+        merge(m, s, w, m2, s2, w2);
+    }
+    if (lane == 0) sm.m[warp] = m, sm.s[warp] = s, sm.w[warp] = w;
+    if (top) {
+        __syncwarp();
+        if (lane < 8) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int e = 0; e < kEntries; e += 8) best = max(best, sm.entry[warp][e + lane]);
+            sm.group[warp * 8 + lane] = best;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        m = sm.m[0], s = sm.s[0], w = sm.w[0];
+        for (int i = 1; i < kWarps; ++i) merge(m, s, w, sm.m[i], sm.s[i], sm.w[i]);
+        sm.cm = m, sm.cs = s, sm.cw = w;
+    }
+    if (top) {
+        // the top-th largest group maximum, found by every warp for itself: lane l ranks groups l and l + 32
+        const uint32_t a = sm.group[lane], c = sm.group[lane + 32];
+        int ra = 0, rc = 0;
+#pragma unroll 8
+        for (int i = 0; i < kGroups; ++i) {
+            const uint32_t g = sm.group[i];
+            ra += g > a || (g == a && i < lane);
+            rc += g > c || (g == c && i < lane + 32);
+        }
+        const uint32_t thr = max(1u, __reduce_max_sync(0xffffffffu, ra == top - 1 ? a : rc == top - 1 ? c : 0u));
+        for (int e = 0; e < kEntries; ++e) {
+            if (sm.entry[warp][e] < thr) continue;
+            for (int j = e << shift, blk = gw + j * nw; j < (e + 1) << shift && blk < blocks; ++j, blk += nw) {
+                float x[GE];
+                widen<BF16>(load_granule<BF16, ALIGNED>(row, blk, lane, V), x);
+#pragma unroll
+                for (int i = 0; i < GE; ++i)
+                    if (x[i] > -INFINITY && order_f32(x[i]) >= thr) {
+                        const int at = atomicAdd(&sm.count, 1);
+                        if (at < kCand) sm.cand[at] = make_key(x[i], (ALIGNED ? (blk * 32 + lane) * GE : blk * 32 * GE + lane) + i * ES);
+                    }
+            }
+        }
+        __syncthreads();
+        const int count = sm.count;
+        if (count > kCand) {
+            // many equal logits: every warp keeps the best of its blocks, lane r the r-th, and no order of the
+            // pushes matters (sorted by value and index)
+            __syncthreads();
+            unsigned long long mine = 0;
+            for (int blk = gw; blk < blocks; blk += nw) {
+                float x[GE];
+                widen<BF16>(load_granule<BF16, ALIGNED>(row, blk, lane, V), x);
+#pragma unroll 1
+                for (int i = 0; i < GE; ++i) {
+                    float xi = x[0];
+#pragma unroll
+                    for (int f = 1; f < GE; ++f) xi = i == f ? x[f] : xi;
+                    unsigned long long key = xi > -INFINITY && order_f32(xi) >= thr
+                                                 ? make_key(xi, (ALIGNED ? (blk * 32 + lane) * GE : blk * 32 * GE + lane) + i * ES)
+                                                 : 0;
+                    const unsigned long long least = __shfl_sync(0xffffffffu, mine, top - 1);
+                    if (key <= least) key = 0;
+                    while (__any_sync(0xffffffffu, key != 0)) {
+                        const unsigned long long k = warp_max(key);
+                        if (key == k) key = 0;
+                        const unsigned long long up = __shfl_up_sync(0xffffffffu, mine, 1);
+                        if (k > mine) mine = lane == 0 || up > k ? k : up;
+                        if (key <= __shfl_sync(0xffffffffu, mine, top - 1)) key = 0;
+                    }
+                }
+            }
+            if (lane < top) sm.cand[warp * top + lane] = mine;
+            __syncthreads();
+        }
+        if (warp == 0) {
+            const int have = count > kCand ? kWarps * top : count;
+            unsigned long long last = ~0ull;
+#pragma unroll 1
+            for (int r = 0; r < top; ++r) {
+                unsigned long long best = 0;
+                for (int i = lane; i < have; i += 32) {
+                    const unsigned long long k = sm.cand[i];
+                    if (k < last && k > best) best = k;
+                }
+                last = warp_max(best);
+                if (lane == 0) sm.best[r] = last;
+            }
+        }
+    }
+    if (cs > 1) cluster_sync_all();
+    else __syncthreads();
+    if (rank == 0 && warp == 0) {
+        // (every lane forms the same row sums)
+        m = sm.cm, s = sm.cs, w = sm.cw;
+        for (uint32_t c = 1; c < cs; ++c) {
+            ScoreSmem *at = in_cta(&sm, c);
+            merge(m, s, w, at->cm, at->cs, at->cw);
+        }
+        const float lg = logf(s);
+        const bool fine = s > 0.f && m < INFINITY, empty = s == 0.f;   // (a NaN is neither)
+        const float nan = __int_as_float(0x7fffffff);
+        if (lane == 0) {
+            args.logprobs[n] = fine ? (x_token - m) - lg : empty ? -INFINITY : nan;
+            if (args.entropy) args.entropy[n] = fine ? fmaxf(lg - kLn2 * (w / s), 0.f) : empty ? 0.f : nan;
+            if (args.lse) args.lse[n] = fine ? m + lg : empty ? -INFINITY : nan;
+        }
+        unsigned long long last = ~0ull;
+#pragma unroll 1
+        for (int r = 0; r < top; ++r) {
+            if (cs > 1) {
+                unsigned long long best = 0;
+                for (int i = lane; i < (int)cs * top; i += 32) {
+                    const unsigned long long k = in_cta(&sm, i / top)->best[i % top];
+                    if (k < last && k > best) best = k;
+                }
+                last = warp_max(best);
+            } else {
+                last = sm.best[r];
+            }
+            if (lane == 0) {
+                const bool have = fine && last != 0;
+                args.top_logprobs[n * top + r] = have ? (unorder_f32((uint32_t)(last >> 32)) - m) - lg : -INFINITY;
+                args.top_tokens[n * top + r] = have ? (int)(0xffffffffu - (uint32_t)last) : -1;
+            }
+            if (last == 0) last = 1;      // (nothing is below it)
+        }
+    }
+    if (cs > 1) cluster_sync_all();       // a CTA's shared memory stays until it has been read
+}
+
+template <bool BF16, bool ALIGNED>
+cudaError_t launch_score(const LogprobArgs &a, int cs, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    const long long rows = a.N;
+    const unsigned ny = (unsigned)(rows < 65535 ? rows : 65535);
+    cfg.gridDim = dim3(cs, ny, (unsigned)((rows + ny - 1) / ny));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<BF16, ALIGNED>, a);
+}
+
+// ------------------------------------------------------------------ gradient
+// One CTA per row and 2048 granules of 16 bytes; each is read, turned into its gradient and written, eight in flight per
+// thread.  Rows without a token get zeros and are not read.  Bound by HBM.
+// lse is FP32, so p carries half a step of it, 2^-18 at 64 to 128.  Rows further off than that (one huge value, as a mask
+// of the type's lowest) have their maximum and sum formed again, by a single CTA, which then does the whole row.
+constexpr int kGradThreads = 256, kGradU = 8;
+constexpr float kFarLse = 128.f;
+
+template <bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(kGradThreads)
+token_logprobs_backward_kernel(const LogprobGradArgs args, int slices)
+{
+    constexpr int GE = BF16 ? 8 : 4, ES = ALIGNED ? 1 : 32, kWarpsG = kGradThreads / 32;
+    __shared__ float part[2][kWarpsG];
+    const int V = args.V;
+    const long long n = blockIdx.x / slices;
+    const int slice = blockIdx.x % slices, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int token = args.tokens[n];
+    const unsigned char *row = static_cast<const unsigned char *>(args.logits) + n * args.row_stride * (BF16 ? 2 : 4);
+    unsigned char *out = static_cast<unsigned char *>(args.dlogits) + n * args.grad_stride * (BF16 ? 2 : 4);
+    const bool skip = token < 0 || token >= V;
+    if (token >= V && tid == 0) atomicExch(args.status, kStatusShape);
+    const int blocks = (V + 32 * GE - 1) / (32 * GE);
+    uint4 raw[kGradU];
+    // this warp's u-th block of 32 granules of a slice
+    auto block_of = [&](int sl, int u) { return (sl * kGradU + u) * kWarpsG + warp; };
+    auto load = [&](int sl) {
+#pragma unroll
+        for (int u = 0; u < kGradU; ++u)
+            if (block_of(sl, u) < blocks) raw[u] = load_granule<BF16, ALIGNED>(row, block_of(sl, u), lane, V);
+    };
+    if (!skip) load(slice);
+    const float lse = skip ? 0.f : args.lse[n], dlp = skip ? 0.f : args.dlogprobs[n];
+    const float dH = skip || !args.dentropy ? 0.f : args.dentropy[n], H = dH != 0.f ? args.entropy[n] : 0.f;
+    const bool zero = skip || lse == -INFINITY;
+    // log p_v = (x_v - m) - lg
+    float m = lse, lg = 0.f;
+    const bool far = !zero && fabsf(lse) >= kFarLse;
+    if (far) {
+        if (slice) return;
+        float s = 0.f, w = 0.f;
+        m = kLowest;
+        for (int blk = warp; blk < blocks; blk += kWarpsG) {
+            float x[GE];
+            widen<BF16>(load_granule<BF16, ALIGNED>(row, blk, lane, V), x);
+#pragma unroll
+            for (int e = 0; e < GE; ++e)
+                if (x[e] > -INFINITY) merge(m, s, w, x[e], 1.f, 0.f);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+            merge(m, s, w, m2, s2, 0.f);
+        }
+        if (lane == 0) part[0][warp] = m, part[1][warp] = s;
+        __syncthreads();
+        m = kLowest, s = 0.f;
+        for (int i = 0; i < kWarpsG; ++i) merge(m, s, w, part[0][i], part[1][i], 0.f);
+        lg = logf(s);
+    }
+    // g = -p (c0 + dH log p), c0 = dlp + dH H
+    const float c0 = fmaf(dH, H, dlp);
+    const int end = far ? slices : slice + 1;
+    for (int sl = slice; sl < end; ++sl) {
+        if (far) load(sl);
+#pragma unroll
+        for (int u = 0; u < kGradU; ++u) {
+            const int blk = block_of(sl, u);
+            if (blk >= blocks) break;
+            const int i0 = ALIGNED ? (blk * 32 + lane) * GE : blk * 32 * GE + lane;
+            float x[GE], gr[GE];
+            if (!zero) widen<BF16>(raw[u], x);
+#pragma unroll
+            for (int e = 0; e < GE; ++e) {
+                gr[e] = 0.f;
+                if (!zero) {
+                    float lp = (x[e] - m) - lg;
+                    lp = lp < -200.f ? -200.f : lp;        // (a masked logit: p = 0, and not 0 times infinity)
+                    gr[e] = -ex2(lp * kLog2e) * fmaf(dH, lp, c0);
+                    if (i0 + e * ES == token) gr[e] += dlp;
+                }
+            }
+            if (ALIGNED && i0 + GE <= V) {
+                uint4 o;
+                if (BF16) o = make_uint4(pack_bf16x2(gr[0], gr[1]), pack_bf16x2(gr[2], gr[3]), pack_bf16x2(gr[4 % GE], gr[5 % GE]),
+                                         pack_bf16x2(gr[6 % GE], gr[7 % GE]));
+                else o = make_uint4(__float_as_uint(gr[0]), __float_as_uint(gr[1]), __float_as_uint(gr[2]), __float_as_uint(gr[3]));
+                reinterpret_cast<uint4 *>(out)[blk * 32 + lane] = o;
+            } else {
+#pragma unroll
+                for (int e = 0; e < GE; ++e)
+                    if (i0 + e * ES < V) {
+                        if (BF16) reinterpret_cast<uint16_t *>(out)[i0 + e * ES] = (uint16_t)(pack_bf16x2(gr[e], 0.f) & 0xffffu);
+                        else reinterpret_cast<float *>(out)[i0 + e * ES] = gr[e];
+                    }
+            }
+        }
+    }
+}
+
+bool rows_aligned(const void *p, long long stride, bool bf16)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (stride * (bf16 ? 2 : 4)) % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobArgs &a, bool bf16, int sms, cudaStream_t stream)
+{
+    // a row is spread over up to 8 CTAs until the device has about two per SM
+    int cs = 1;
+    while (cs < 8 && (long long)a.N * cs < 2LL * sms) cs *= 2;
+    const bool al = a.N == 1 ? rows_aligned(a.logits, 0, bf16) : rows_aligned(a.logits, a.row_stride, bf16);
+    if (bf16) return al ? launch_score<true, true>(a, cs, stream) : launch_score<true, false>(a, cs, stream);
+    return al ? launch_score<false, true>(a, cs, stream) : launch_score<false, false>(a, cs, stream);
+}
+
+cudaError_t launch_token_logprobs_backward(const LogprobGradArgs &a, bool bf16, int, cudaStream_t stream)
+{
+    const int ge = bf16 ? 8 : 4, per = kGradThreads * kGradU * ge, slices = (a.V + per - 1) / per;
+    const unsigned grid = (unsigned)((long long)a.N * slices);
+    const bool al = (a.N == 1 ? rows_aligned(a.logits, 0, bf16) : rows_aligned(a.logits, a.row_stride, bf16)) &&
+                    (a.N == 1 ? rows_aligned(a.dlogits, 0, bf16) : rows_aligned(a.dlogits, a.grad_stride, bf16));
+    if (bf16) {
+        if (al) token_logprobs_backward_kernel<true, true><<<grid, kGradThreads, 0, stream>>>(a, slices);
+        else token_logprobs_backward_kernel<true, false><<<grid, kGradThreads, 0, stream>>>(a, slices);
+    } else {
+        if (al) token_logprobs_backward_kernel<false, true><<<grid, kGradThreads, 0, stream>>>(a, slices);
+        else token_logprobs_backward_kernel<false, false><<<grid, kGradThreads, 0, stream>>>(a, slices);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace la
