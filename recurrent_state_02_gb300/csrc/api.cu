@@ -1134,7 +1134,8 @@ la_status gdelta_forward(const void *q, const void *k, const void *v, la_dtype d
     const la::GdeltaShape s = gdelta_shape(B, H, Hk, T, r, dv, alpha, beta, status_word(), cu_seqlens);
     if (!s.status) return LA_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, packed) && aligned(q, 16) && aligned(k, 16) && aligned(v, 16)) {
+    if (gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, packed) && aligned(q, 16) && aligned(k, 16) && aligned(v, 16) &&
+        aligned(y, 16)) {
         la::GdeltaTcMaps m;
         auto map = [&](CUtensorMap *t, const void *p, int heads, int cols) {
             return packed ? make_map_bf16_tok(t, p, T, heads, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)

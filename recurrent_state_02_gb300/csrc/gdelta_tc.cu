@@ -23,6 +23,9 @@
 
 #include "gdelta_tc.h"
 #include "tc_common.cuh"
+#include "tc_short.cuh"
+
+#include <cstddef>
 
 namespace la {
 namespace {
@@ -56,19 +59,6 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_
 {
     hi = pack_bf16x2(x0, x1);
     lo = pack_bf16x2(x0 - bf16_lo(hi), x1 - bf16_hi(hi));
-}
-
-// D[tmem] (+)= A[tmem] * B[smem], BF16 operands, FP32 accumulator.
-template <bool ACC>
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
-        "mov.b64 db, {%2, %3};\n\t"
-        "setp.ne.u32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
-        : "memory");
 }
 
 // The sequence and the chunks of a CTA.
@@ -456,388 +446,468 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 }
 
 // ------------------------------------------------------------------ the chain
-constexpr int kTmWarps = 8, kIssuer = 8, kLoader = 9;   // warps 0..7 own the lanes, 8 issues MMAs, 9 loads
-constexpr int kMThreads = 32 * (kLoader + 1);
+// Four warpgroups: 0 and 1 own the state (warp w: TMEM lanes 32 (w % 4) .., half w / 4 of the tokens in steps 1 and 2 and of
+// the state's rows in step 3), 2 (a lane quadrant per warp) brings V's columns to their lanes and y from them to memory, and in 3
+// one warp issues the MMAs and one loads.  The halves run staggered: the second one's products overlap the first one's
+// conversions.
+constexpr int kOwners = 8, kHelpers = 4, kIssuer = 12, kLoader = 13;
+constexpr int kMThreads = 512;
 constexpr int kGateRing = 4;
+// registers per thread after the split (launched with 128): 2 x 160 + 104 + 88 = 4 x 128
+constexpr int kRegsOwn = 160, kRegsHelp = 104, kRegsRest = 88;
 template <int KD>
 struct ChainCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;    // a K or Q tile (64-feature blocks)
     // a stage (two): K, Q, V (two blocks of 64 columns), X's two parts, A
     static constexpr uint32_t kSK = 0, kSQ = kTK, kSV = 2 * kTK, kSX = kSV + 2 * kTile, kSA = kSX + 2 * kTile, kStage = kSA + kTile;
-    static constexpr uint32_t kGates = 2 * kStage;      // ring of kGateRing
+    static constexpr uint32_t kY = 2 * kStage;          // y of a chunk (two blocks of 64 columns)
+    static constexpr uint32_t kGates = kY + 2 * kTile;  // ring of kGateRing
     static constexpr uint32_t kSmall = kGates + kGateRing * 1024;
 };
-// TMEM columns: the left operands S^T (two parts), R^T (two parts, then those of the decayed V'^T) and V'^T; the accumulators
-// P^T (then E^T, then dS^T), (Q S)^T and (A V')^T
-constexpr uint32_t kcS = 0, kcP = 128, kcQS = 256, kcAV = 320, kcR = 384, kcV = 448;
+// TMEM columns (all 512 are allocated, so they start at 0): S^T (two parts); the accumulators P^T and E^T (then both dS^T),
+// (Q S)^T, (A V')^T; R^T (two parts, then those of the decayed V'^T), V'^T, V^T
+constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcQS = 256, kcAV = 320, kcR = 384, kcW = 448, kcV = 480;
 
 struct alignas(16) MSmall {
     uint64_t full_k[2], full_vx[2], full_qa[2];
-    uint64_t got_s, got_r, got_v;       // the lanes' operands are in TMEM (8 warps)
-    uint64_t done1, done2;              // P, E
-    // dS, and Q S and A V', of even and odd chunks (the loader may look at them late, but not two chunks late)
-    uint64_t done3[2], done4[2];
+    uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (4 warps)
+    uint64_t got_v;                          // V^T is (the helpers)
+    uint64_t y_read;                         // Q S and A V' have been read (the helpers)
+    uint64_t tail;                           // packed: the last chunk's rows of K past the end are 0 (the helpers)
+    uint64_t done1[2], done2[2];             // halves of P, E
+    // halves of dS of even and odd chunks, Q S and A V' (the loader may look at them late, but not two chunks late)
+    uint64_t done3[4], done4[2];
     uint64_t fin;
     uint32_t tmem_base;
     int abort_flag;
 };
+#define MBAR(name, i) (sS + (uint32_t)offsetof(MSmall, name) + 8 * (uint32_t)(i))
+
 template <int KD>
 constexpr uint32_t kMSmemBytes = ChainCfg<KD>::kSmall + sizeof(MSmall) + 1024;
 static_assert(kMSmemBytes<128> <= 232448, "shared memory budget");
 
-__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t (&w)[16])
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    float f[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]);
-    tc_st_32x32b_x16(addr, f);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_u16(uint32_t a, uint32_t x)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)x) : "memory");
+}
+// 8 columns of 32 lanes
+__device__ __forceinline__ void tm_ld8(uint32_t a, float (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tm_st8(uint32_t a, const uint32_t (&w)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+// x as a high and a low BF16 part
+__device__ __forceinline__ void split(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 r = __ffma2_rn(make_float2(bf16_lo(hi), bf16_hi(hi)), make_float2(-1.f, -1.f), x);
+    lo = pack_bf16x2(r.x, r.y);
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a)
+{
+    const uint4 v = lds4(a);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+// One lane of a converged warp, in a form that keeps what it guards warp-uniform (an MMA's operands then stay in uniform
+// registers: 20 cycles to issue one, 45 behind a test of the lane).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <int KD>
 __global__ void __launch_bounds__(kMThreads, 1)
 gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                    const __grid_constant__ CUtensorMap map_v, const GdeltaTcArgs args)
+                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ GdeltaTcArgs args)
 {
     using Cfg = ChainCfg<KD>;
-    constexpr int KH = KD / 2;                  // state rows per thread (a thread has a column, half its rows)
+    constexpr int KH = KD / 2;                  // state rows per owner thread (a thread has a column, half its rows)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = align1024(smem_raw);
     MSmall *sm = reinterpret_cast<MSmall *>(base + Cfg::kSmall);
+    const uint32_t s0 = smem_u32(base), sS = s0 + Cfg::kSmall;
+    auto wait1 = [&](uint32_t bar, uint32_t parity) { return bounded_wait<false>(sS + offsetof(MSmall, abort_flag), bar, parity); };
+    auto waitw = [&](uint32_t bar, uint32_t parity) { return bounded_wait<true>(sS + offsetof(MSmall, abort_flag), bar, parity); };
 
-    const GdeltaShape &s = args.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool packed = s.cu_seqlens != nullptr;
-    const int tiles = (s.dv + 127) / 128;
-    const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % s.H, hk = h / (s.H / s.Hk);
-    int b = blockIdx.x / (tiles * s.H);
+    const int H = args.s.H, dv = args.s.dv;
+    const bool packed = args.s.cu_seqlens != nullptr;
+    const int tiles = (dv + 127) / 128;
+    const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % H;
+    int b = blockIdx.x / (tiles * H);
     if (packed) b = args.order[b];
     const Span sp = span_of(args, b);
     if (!sp.valid) return;
     const int T = sp.T, nch = (T + kC - 1) / kC;
-    const int ncols = min(128, s.dv - 128 * tile);      // of this CTA: 128 or 64
-    const uint8_t *ws = args.ws + (sp.slot * s.H + h) * kWsChunk;
-    const size_t ws_step = (size_t)s.H * kWsChunk;      // from one chunk to the next
-    Ctx cx{&sm->abort_flag, kWaitLimitNs, s.status};
-    const bool issuer = warp == kIssuer, loader = warp == kLoader;
+    const int ncols = min(128, dv - 128 * tile);        // of this CTA: 128 or 64
+    const size_t bh = (size_t)b * H + h;
+    const bool tail = packed && nch > 0 && T < nch * kC;
 
     if (tid == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm->full_k[i], 1);
-            mbar_init(&sm->full_vx[i], 1);
-            mbar_init(&sm->full_qa[i], 1);
-            mbar_init(&sm->done3[i], 1);
-            mbar_init(&sm->done4[i], 1);
-        }
-        mbar_init(&sm->got_s, kTmWarps);
-        mbar_init(&sm->got_r, kTmWarps);
-        mbar_init(&sm->got_v, kTmWarps);
-        mbar_init(&sm->done1, 1);
-        mbar_init(&sm->done2, 1);
-        mbar_init(&sm->fin, 1);
+        for (uint64_t *bar = sm->full_k; bar <= &sm->fin; ++bar)
+            mbar_init(bar, bar >= sm->got_s && bar < &sm->got_v ? kOwners / 2 : bar >= &sm->got_v && bar <= &sm->tail ? kHelpers : 1);
         sm->abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (issuer) {
+    if (warp == kIssuer) {
         tmem_alloc(&sm->tmem_base, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm->tmem_base;
 
-    if (loader) {
-        auto tok = [&](void *dst, const CUtensorMap *map, uint64_t *bar, int x, int n, int heads, int head) {
-            if (packed) tma_load_3d(dst, map, bar, x, head, (int)sp.tok0 + n * kC);
-            else tma_load_3d(dst, map, bar, x, n * kC, b * heads + head);
-        };
-        auto load_k = [&](int n) {
-            uint8_t *st = base + (n & 1) * Cfg::kStage;
-            uint64_t *bar = &sm->full_k[n & 1];
-            mbar_arrive_expect_tx(bar, Cfg::kTK);
-#pragma unroll
-            for (int x = 0; x < KD / 64; ++x) tok(st + Cfg::kSK + x * kTile, &map_k, bar, 64 * x, n, s.Hk, hk);
-        };
-        auto load_vx = [&](int n) {
-            uint8_t *st = base + (n & 1) * Cfg::kStage;
-            uint64_t *bar = &sm->full_vx[n & 1];
-            const uint8_t *w = ws + n * ws_step;
-            mbar_arrive_expect_tx(bar, ncols / 64 * kTile + 2 * kTile + kGateBytes);
-            for (int x = 0; x < ncols / 64; ++x) tok(st + Cfg::kSV + x * kTile, &map_v, bar, 128 * tile + 64 * x, n, s.H, h);
-            bulk_load(base + Cfg::kGates + (n % kGateRing) * 1024, w + kWsGates, kGateBytes, bar);
-            bulk_load(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
-        };
-        auto load_qa = [&](int n) {
-            uint8_t *st = base + (n & 1) * Cfg::kStage;
-            uint64_t *bar = &sm->full_qa[n & 1];
-            mbar_arrive_expect_tx(bar, Cfg::kTK + kTile);
-#pragma unroll
-            for (int x = 0; x < KD / 64; ++x) tok(st + Cfg::kSQ + x * kTile, &map_q, bar, 64 * x, n, s.Hk, hk);
-            bulk_load(st + Cfg::kSA, ws + n * ws_step + kWsA, kTile, bar);
-        };
-        int n1 = 0, n2 = 0;                    // chunks whose K, V, X / Q, A loads were started
-        for (; n1 < 2 && n1 < nch; n1 = ++n2)
-            if (lane == 0) load_k(n1), load_vx(n1), load_qa(n1);
-        bool ok = true;
-        for (int n = 0; n + 2 < nch && ok; ++n) {
-            // step 3 of chunk n has read K (and before it V, X and Q were read), A V' after it A
-            ok = warp_wait(cx, &sm->done3[n & 1], (n >> 1) & 1);
-            if (!ok) break;
-            if (lane == 0) load_k(n + 2), load_vx(n + 2);
-            n1 = n + 3;
-            ok = warp_wait(cx, &sm->done4[n & 1], (n >> 1) & 1);
-            if (!ok) break;
-            if (lane == 0) load_qa(n + 2);
-            n2 = n + 3;
-        }
-        // loads still in flight complete before the CTA exits (also after a wait that was given up)
-        if (lane == 0) {
-            for (int i = n1 > 2 ? n1 - 2 : 0; i < n1; ++i) {
-                mbar_wait(&sm->full_k[i & 1], (i >> 1) & 1, cx.limit);
-                mbar_wait(&sm->full_vx[i & 1], (i >> 1) & 1, cx.limit);
-            }
-            for (int i = n2 > 2 ? n2 - 2 : 0; i < n2; ++i) mbar_wait(&sm->full_qa[i & 1], (i >> 1) & 1, cx.limit);
-        }
-        __syncwarp();
-    } else if (issuer) {
-        if (lane == 0) {
-            constexpr uint32_t id64 = idesc_bf16_f32(128, 64, false, false), idS = idesc_bf16_f32(128, KD, false, true);
+    if (warp >= kOwners + kHelpers) {
+        regs_dec<kRegsRest>();
+        if (warp == kLoader && elect_one()) {
+            const int hk = h / (H / args.s.Hk);
+            const uint8_t *ws = args.ws + (sp.slot * H + h) * kWsChunk;
+            const size_t ws_step = (size_t)H * kWsChunk;      // from one chunk to the next
+            auto tok = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int n, int heads, int head) {
+                if (packed) tma_load(dst, map, bar, x, head, (int)sp.tok0 + n * kC);
+                else tma_load(dst, map, bar, x, n * kC, b * heads + head);
+            };
+            int n1 = 0, n2 = 0;                    // chunks whose K, V, X / Q, A loads were started
             bool ok = true;
+            // stage n & 1 takes chunk n once step 3 of chunk n - 2 has read K (and before it V, X and Q were read), and A V' after
+            // it A
+#pragma unroll 1
             for (int n = 0; n < nch && ok; ++n) {
-                const uint32_t st = smem_u32(base + (n & 1) * Cfg::kStage), ph = n & 1, fph = (n >> 1) & 1;
-                // 1  P^T = S^T K^T, both parts of S
-                ok = wait<0>(cx, &sm->full_k[n & 1], fph) && wait<0>(cx, &sm->got_s, ph);
+                const uint32_t st = s0 + (n & 1) * Cfg::kStage, wph = ((n >> 1) - 1) & 1;
+                const uint8_t *w = ws + n * ws_step;
+                if (n >= 2) ok = wait1(MBAR(done3, 2 + (n & 1)), wph);
                 if (!ok) break;
-                tc_fence_after();
+                uint32_t bar = MBAR(full_k, n & 1);
+                bar_expect(bar, Cfg::kTK);
+#pragma unroll 1
+                for (int x = 0; x < KD / 64; ++x) tok(st + Cfg::kSK + x * kTile, &map_k, bar, 64 * x, n, args.s.Hk, hk);
+                bar = MBAR(full_vx, n & 1);
+                bar_expect(bar, ncols / 64 * kTile + 2 * kTile + kGateBytes);
+                bulk_copy(s0 + Cfg::kGates + (n % kGateRing) * 1024, w + kWsGates, kGateBytes, bar);
+#pragma unroll 1
+                for (int x = 0; x < ncols / 64; ++x) tok(st + Cfg::kSV + x * kTile, &map_v, bar, 128 * tile + 64 * x, n, H, h);
+                bulk_copy(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
+                n1 = n + 1;
+                if (n >= 2) ok = wait1(MBAR(done4, n & 1), wph);
+                if (!ok) break;
+                bar = MBAR(full_qa, n & 1);
+                bar_expect(bar, Cfg::kTK + kTile);
+#pragma unroll 1
+                for (int x = 0; x < KD / 64; ++x) tok(st + Cfg::kSQ + x * kTile, &map_q, bar, 64 * x, n, args.s.Hk, hk);
+                bulk_copy(st + Cfg::kSA, w + kWsA, kTile, bar);
+                n2 = n + 1;
+            }
+            // loads still in flight complete before the CTA exits (also after a wait that was given up)
+#pragma unroll 1
+            for (int i = max(0, n1 - 2); i < n1; ++i) {
+                wait1(MBAR(full_k, i & 1), (i >> 1) & 1);
+                wait1(MBAR(full_vx, i & 1), (i >> 1) & 1);
+                if (i < n2) wait1(MBAR(full_qa, i & 1), (i >> 1) & 1);
+            }
+        } else if (warp == kIssuer && elect_one()) {
+            constexpr uint32_t id64 = idesc_bf16_f32(128, 64, false, false), id32 = idesc_bf16_f32(128, 32, false, false),
+                               idS = idesc_bf16_f32(128, KH, false, true);
+            constexpr uint32_t kHalfRows = (32 * 128) >> 4;       // from a tile's first 32 rows to its last
+#pragma unroll 1
+            for (int n = 0; n < nch; ++n) {
+                const uint32_t st = s0 + (n & 1) * Cfg::kStage, ph = n & 1, fph = (n >> 1) & 1;
                 const uint32_t klo = desc_lo(st + Cfg::kSK, 16), xlo = desc_lo(st + Cfg::kSX, 16);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int kk = 0; kk < KD / 16; ++kk) {
-                        const uint32_t a = tmem + kcS + p * KH + kk * 8, bo = klo + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4);
-                        if (p == 0 && kk == 0) tc_mma_ts<false>(tmem + kcP, a, bo, kHi128, id64);
-                        else tc_mma_ts<true>(tmem + kcP, a, bo, kHi128, id64);
-                    }
-                tc_commit(&sm->done1);
-                // 2  E^T = R^T X^T: high X with both parts of R, low X with the high one
-                ok = wait<0>(cx, &sm->full_vx[n & 1], fph) && wait<0>(cx, &sm->got_r, ph);
-                if (!ok) break;
+                // 1  P^T = S^T K^T, both parts of S: the first half of S's rows for all tokens, the second one for one half
+                // of the tokens after the other
+                if (!wait1(MBAR(full_k, n & 1), fph)) break;
+                if (tail && n == nch - 1 && !wait1(MBAR(tail, 0), 0)) break;
+                if (!wait1(MBAR(got_s, 0), ph)) break;
                 tc_fence_after();
-#pragma unroll
-                for (int p = 0; p < 3; ++p)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t a = tmem + kcR + (p == 1 ? 32 : 0) + kk * 8, bo = xlo + (((p == 2 ? kTile : 0) + kk * 32) >> 4);
-                        if (p == 0 && kk == 0) tc_mma_ts<false>(tmem + kcP, a, bo, kHi128, id64);
-                        else tc_mma_ts<true>(tmem + kcP, a, bo, kHi128, id64);
+#pragma unroll 1
+                for (int i = 0; i < KD / 16; ++i) {        // part i % 2, k-step i / 2
+                    const int kk = i >> 1;
+                    mma_ts(kcP, kcS + (i & 1) * KH + kk * 8, klo + kk * 2, kHi128, id64, i > 0);
+                }
+                if (!wait1(MBAR(got_s, 1), ph)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    // (the second half of the rows: K's second block, or the second half of its one block's rows)
+                    const uint32_t k2 = klo + t * kHalfRows + ((KD == 128 ? kTile : 64u) >> 4);
+#pragma unroll 1
+                    for (int i = 0; i < KD / 16; ++i) {
+                        const int kk = i >> 1;
+                        mma_ts(kcP + 32 * t, kcS + (i & 1) * KH + KD / 4 + kk * 8, k2 + kk * 2, kHi128, id32, true);
                     }
-                tc_commit(&sm->done2);
-                // (Q S)^T
-                ok = wait<0>(cx, &sm->full_qa[n & 1], fph);
+                    bar_commit(MBAR(done1, t));
+                }
+                // 2  E^T = R^T X^T: high X with both parts of R, low X with the high one.  X is lower triangular: the first
+                // half of E needs the first half of R, the second one both.
+                if (!wait1(MBAR(full_vx, n & 1), fph)) break;
+                bool ok = true;
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    ok = wait1(MBAR(got_r, t), ph);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int o = t; o < 2; ++o) {          // half o of E from half t of R
+                        const uint32_t d = kcE + 32 * o, xo = xlo + o * kHalfRows + 4 * t, r = kcR + 16 * t;
+#pragma unroll 1
+                        for (int kk = 0; kk < 2; ++kk) {
+                            mma_ts(d, r + kk * 8, xo + kk * 2, kHi128, id32, t + kk > 0);
+                            mma_ts(d, r + 32 + kk * 8, xo + kk * 2, kHi128, id32, true);
+                            mma_ts(d, r + kk * 8, xo + kk * 2 + (kTile >> 4), kHi128, id32, true);
+                        }
+                    }
+                    bar_commit(MBAR(done2, t));
+                }
                 if (!ok) break;
+                // (Q S)^T
+                if (!wait1(MBAR(full_qa, n & 1), fph) || (n > 0 && !wait1(MBAR(y_read, 0), ph ^ 1))) break;
                 tc_fence_after();
                 const uint32_t qlo = desc_lo(st + Cfg::kSQ, 16), alo = desc_lo(st + Cfg::kSA, 16);
-#pragma unroll
-                for (int kk = 0; kk < KD / 16; ++kk) {
-                    const uint32_t a = tmem + kcS + kk * 8, bo = qlo + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4);
-                    if (kk == 0) tc_mma_ts<false>(tmem + kcQS, a, bo, kHi128, id64);
-                    else tc_mma_ts<true>(tmem + kcQS, a, bo, kHi128, id64);
-                }
-                // 3  dS^T = V'^T K, both parts of the decayed V'
-                ok = wait<0>(cx, &sm->got_v, ph);
-                if (!ok) break;
+#pragma unroll 1
+                for (int kk = 0; kk < KD / 16; ++kk)
+                    mma_ts(kcQS, kcS + kk * 8, qlo + (kk >> 2) * (kTile >> 4) + (kk & 3) * 2, kHi128, id64, kk > 0);
+                // 3  dS^T = V'^T K, both parts of the decayed V', one half of the state's rows after the other
+                if (!wait1(MBAR(got_w, 0), ph) || !wait1(MBAR(got_w, 1), ph)) break;
                 tc_fence_after();
                 const uint32_t kmn = desc_lo(st + Cfg::kSK, kTile);
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t a = tmem + kcR + p * 32 + kk * 8, bo = kmn + kk * (2048 >> 4);
-                        if (p == 0 && kk == 0) tc_mma_ts<false>(tmem + kcP, a, bo, kHi128, idS);
-                        else tc_mma_ts<true>(tmem + kcP, a, bo, kHi128, idS);
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t ko = kmn + t * ((KD == 128 ? kTile : 64u) >> 4);
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {          // part i / 4, k-step i % 4
+                        const int kk = i & 3;
+                        mma_ts(kcP + KH * t, kcR + (i >> 2) * 32 + kk * 8, ko + kk * (2048 >> 4), kHi128, idS, i > 0);
                     }
-                tc_commit(&sm->done3[n & 1]);
-                // (A V')^T
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint32_t a = tmem + kcV + kk * 8, bo = alo + ((kk * 32) >> 4);
-                    if (kk == 0) tc_mma_ts<false>(tmem + kcAV, a, bo, kHi128, id64);
-                    else tc_mma_ts<true>(tmem + kcAV, a, bo, kHi128, id64);
+                    bar_commit(MBAR(done3, 2 * t + (n & 1)));
                 }
-                tc_commit(&sm->done4[n & 1]);
+                // (A V')^T
+#pragma unroll 1
+                for (int kk = 0; kk < 4; ++kk) mma_ts(kcAV, kcW + kk * 8, alo + kk * 2, kHi128, id64, kk > 0);
+                bar_commit(MBAR(done4, n & 1));
             }
             // every MMA completes before the CTA exits
-            tc_commit(&sm->fin);
-            mbar_wait(&sm->fin, 0, cx.limit);
+            bar_commit(MBAR(fin, 0));
+            wait1(MBAR(fin, 0), 0);
         }
         __syncwarp();
-    } else {
-        // lane quadrant q4, half ch of the columns (tokens, or state rows)
-        const int q4 = warp & 3, ch = warp >> 2;
-        const uint32_t tq = tmem + ((uint32_t)(32 * q4) << 16);
-        const int d = 32 * q4 + lane;                   // value column of the CTA
-        const bool live = d < ncols;
-        const size_t bh = (size_t)b * s.H + h;
-        float S[KH];                                    // S[i]: state row KH ch + i of the lane's column
-        const size_t s_at = (bh * KD + KH * ch) * s.dv + 128 * tile + d;
-#pragma unroll
-        for (int i = 0; i < KH; ++i) S[i] = args.S0 && live ? args.S0[s_at + (size_t)i * s.dv] : 0.f;
-        auto put_s = [&]() {
-#pragma unroll
-            for (int x = 0; x < KH / 32; ++x) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) split2(S[32 * x + 2 * i], S[32 * x + 2 * i + 1], hi[i], lo[i]);
-                tm_store(tq + kcS + KH / 2 * ch + 16 * x, hi);
-                tm_store(tq + kcS + KH + KH / 2 * ch + 16 * x, lo);
-            }
-            tc_wait_st();
-            tc_fence_before();
-            warp_arrive(&sm->got_s);
-        };
-        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * s.H + h) * s.dv : bh * s.T * s.dv) + 128 * tile + d;
-        const size_t y_step = packed ? (size_t)s.H * s.dv : s.dv;
-        // y of chunk n, tokens 32 ch ..
-        auto store_y = [&](int n) {
-            const float4 *eg = reinterpret_cast<const float4 *>(base + Cfg::kGates + (n % kGateRing) * 1024 + 128 * ch);
-            const int left = T - n * kC - 32 * ch;
-            uint16_t *yp = y0 + (size_t)(n * kC + 32 * ch) * y_step;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float qs[16], av[16];
-                tc_ld_32x32b_x16(tq + kcQS + 32 * ch + 16 * x, qs);
-                tc_ld_32x32b_x16(tq + kcAV + 32 * ch + 16 * x, av);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float4 g = eg[4 * x + (i >> 2)];
-                    const float gi = (i & 3) == 0 ? g.x : (i & 3) == 1 ? g.y : (i & 3) == 2 ? g.z : g.w;
-                    const float o = args.scale * fmaf(gi, qs[i], av[i]);
-                    if (live && 16 * x + i < left) yp[(16 * x + i) * y_step] = (uint16_t)(pack_bf16x2(o, 0.f) & 0xffffu);
-                }
-            }
-        };
+    } else if (warp >= kOwners) {
+        regs_dec<kRegsHelp>();
+        const int q4 = warp & 3, d = 32 * q4 + lane;    // lane quadrant, value column of the CTA
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;   // this column in a tile of V or y
+        const size_t y_step = (packed ? (size_t)H : 1) * dv;
+        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * H + h) * dv : bh * args.s.T * dv) + 128 * tile;
+        const float scale = args.scale;
+        // (a helper that gave up waiting still meets the others at their barriers)
         bool ok = true;
-        if (nch > 0) put_s();
-        for (int n = 0; n < nch; ++n) {
-            const uint32_t ph = n & 1;
-            uint8_t *st = base + (n & 1) * Cfg::kStage;
-            const float *gates = reinterpret_cast<const float *>(base + Cfg::kGates + (n % kGateRing) * 1024);
-            const int left = T - n * kC;                // tokens from this chunk on
-            if (n > 0) {
-                ok = warp_wait(cx, &sm->done4[(n - 1) & 1], ((n - 1) >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                store_y(n - 1);
-            }
-            // this thread's column of V, tokens 32 ch ..
-            ok = warp_wait(cx, &sm->full_vx[n & 1], (n >> 1) & 1);
-            if (!ok) break;
-            uint32_t v[16];
-            {
-                const uint8_t *vt = st + Cfg::kSV + (d >> 6) * kTile;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 32 * ch + 2 * i;
-                    const uint32_t lo = live && t < left ? *reinterpret_cast<const uint16_t *>(vt + tile_off(t, d & 63)) : 0;
-                    const uint32_t hi = live && t + 1 < left ? *reinterpret_cast<const uint16_t *>(vt + tile_off(t + 1, d & 63)) : 0;
-                    v[i] = lo | hi << 16;
-                }
-            }
-            // R^T = V^T - e^G P^T (0 past the sequence's end)
-            ok = warp_wait(cx, &sm->done1, ph);
-            if (!ok) break;
-            tc_fence_after();
-            {
-                float p[32];
-                tc_ld_32x32b_x32(tq + kcP + 32 * ch, p);
-                tc_wait_ld();
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 g = *reinterpret_cast<const float2 *>(gates + 32 * ch + 2 * i);
-                    float r0 = fmaf(-g.x, p[2 * i], bf16_lo(v[i]));
-                    float r1 = fmaf(-g.y, p[2 * i + 1], bf16_hi(v[i]));
-                    if (left < kC) {
-                        if (32 * ch + 2 * i >= left) r0 = 0.f;
-                        if (32 * ch + 2 * i + 1 >= left) r1 = 0.f;
-                    }
-                    split2(r0, r1, hi[i], lo[i]);
-                }
-                tm_store(tq + kcR + 16 * ch, hi);
-                tm_store(tq + kcR + 32 + 16 * ch, lo);
-                if (packed && left < kC) {
-                    // rows of K past the end hold another sequence's keys, which step 3 multiplies by 0: they become 0 (step 1
-                    // has read the tile)
-                    for (int x = tid; x < (kC - left) * (KD / 8); x += 32 * kTmWarps) {
-                        const int row = left + x / (KD / 8), c16 = x % (KD / 8);
-                        *reinterpret_cast<uint4 *>(st + Cfg::kSK + (c16 >> 3) * kTile + sw128_offset(row, c16 & 7)) =
-                            make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int n = 0; n <= nch; ++n) {
+            // this thread's column of V (0 past the sequence's end), once the owners have read the last chunk's
+            if (ok && n < nch) ok = waitw(MBAR(full_vx, n & 1), (n >> 1) & 1);
+            if (ok && n > 0 && n < nch) ok = waitw(MBAR(got_r, 0), (n - 1) & 1) && waitw(MBAR(got_r, 1), (n - 1) & 1);
+            if (ok && n < nch) {
+                const uint32_t st = s0 + (n & 1) * Cfg::kStage;
+                const int left = T - n * kC;
+                if (tail && n == nch - 1) {
+                    // rows of K past the end hold another sequence's keys, which step 3 would multiply by 0: they become 0
+                    ok = waitw(MBAR(full_k, n & 1), (n >> 1) & 1);
+                    for (int x = tid - 32 * kOwners; x < (kC - left) * (KD / 8); x += 32 * kHelpers) {
+                        const int c = x % (KD / 8);
+                        sts4(st + Cfg::kSK + (c >> 3) * kTile + sw128_offset(left + x / (KD / 8), c & 7), 0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
+                    bar_arrive_warp(MBAR(tail, 0));
+                }
+                tc_fence_after();
+                const int last = d < ncols ? left : 0;
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t v[8];
+                    const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = 2 * i;
+                        const uint32_t lo = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
+                                       hi = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
+                        v[i] = (16 * x + t < last ? lo : 0) | (16 * x + t + 1 < last ? hi << 16 : 0);
+                    }
+                    tm_st8(tq + kcV + 8 * x, v);
                 }
                 tc_wait_st();
                 tc_fence_before();
-                warp_arrive(&sm->got_r);
+                bar_arrive_warp(MBAR(got_v, 0));
             }
-            // V'^T = beta E^T, and decayed to the chunk's end
-            ok = warp_wait(cx, &sm->done2, ph);
-            if (!ok) break;
-            tc_fence_after();
-            {
-                float e[32];
-                tc_ld_32x32b_x32(tq + kcP + 32 * ch, e);
-                tc_wait_ld();
-                uint32_t vp[16], hi[16], lo[16];
+            if (n == 0) continue;
+            // y of chunk n - 1, through shared memory to whole rows
+            const int m = n - 1, rows = min(kC, T - m * kC);
+            if (ok) ok = waitw(MBAR(done4, m & 1), (m >> 1) & 1);
+            if (ok) {
+                tc_fence_after();
+                const uint32_t eg = s0 + Cfg::kGates + (m % kGateRing) * 1024;
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    float qs[8], av[8];
+                    tm_ld8(tq + kcQS + 8 * x, qs);
+                    tm_ld8(tq + kcAV + 8 * x, av);
+                    const float4 g0 = lds_f4(eg + 32 * x), g1 = lds_f4(eg + 32 * x + 16);
+                    const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+                    wait_loaded(qs);
+                    wait_loaded(av);
+                    const uint32_t a = s0 + Cfg::kY + col + x * (8 * 128);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 be = *reinterpret_cast<const float2 *>(gates + 2 * kC + 32 * ch + 2 * i);
-                    const float2 er = *reinterpret_cast<const float2 *>(gates + kC + 32 * ch + 2 * i);
-                    const float w0 = be.x * e[2 * i], w1 = be.y * e[2 * i + 1];
-                    vp[i] = pack_bf16x2(w0, w1);
-                    split2(er.x * w0, er.y * w1, hi[i], lo[i]);
+                    for (int i = 0; i < 8; ++i) sts_u16(a + i * 128 + ((c16 ^ i) << 4), pack_bf16x2(scale * fmaf(g[i], qs[i], av[i]), 0.f));
                 }
-                tm_store(tq + kcR + 16 * ch, hi);
-                tm_store(tq + kcR + 32 + 16 * ch, lo);
-                tm_store(tq + kcV + 16 * ch, vp);
-                tc_wait_st();
                 tc_fence_before();
-                warp_arrive(&sm->got_v);
+                bar_arrive_warp(MBAR(y_read, 0));
             }
-            const float gC = gates[kC - 1];
-            ok = warp_wait(cx, &sm->done3[n & 1], (n >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int x = 0; x < KH / 32; ++x) {
-                float ds[32];
-                tc_ld_32x32b_x32(tq + kcP + KH * ch + 32 * x, ds);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) S[32 * x + i] = fmaf(gC, S[32 * x + i], ds[i]);
+            named_barrier_sync(1, 32 * kHelpers);
+            if (ok) {
+                const int per = ncols / 8;                  // 16-byte words of a row
+#pragma unroll 1
+                for (int x = tid - 32 * kOwners; x < rows * per; x += 32 * kHelpers) {
+                    const int t = x / per, w = x % per;
+                    *reinterpret_cast<uint4 *>(y0 + (size_t)(m * kC + t) * y_step + 8 * w) =
+                        lds4(s0 + Cfg::kY + (w >> 3) * kTile + sw128_offset(t, w & 7));
+                }
             }
-            if (n + 1 < nch) put_s();
+            named_barrier_sync(1, 32 * kHelpers);
         }
-        if (ok) {
-            if (nch > 0) {
-                ok = warp_wait(cx, &sm->done4[(nch - 1) & 1], ((nch - 1) >> 1) & 1);
-                if (ok) {
-                    tc_fence_after();
-                    store_y(nch - 1);
-                }
-            }
-            if (ok && live) {
+        tc_fence_before();
+    } else {
+        regs_inc<kRegsOwn>();
+        const int q4 = warp & 3, ch = warp >> 2, d = 32 * q4 + lane;
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const bool live = d < ncols;
+        float2 S[KH / 2];                               // S[i]: state rows KH ch + 2 i, + 1 of the lane's column
+        const size_t s_at = (bh * KD + KH * ch) * dv + 128 * tile + d;
 #pragma unroll
-                for (int i = 0; i < KH; ++i) args.S_out[s_at + (size_t)i * s.dv] = S[i];
+        for (int i = 0; i < KH / 2; ++i) {
+            S[i] = make_float2(0.f, 0.f);
+            if (args.S0 && live) S[i] = make_float2(args.S0[s_at + (size_t)(2 * i) * dv], args.S0[s_at + (size_t)(2 * i + 1) * dv]);
+        }
+        // rows 16 x .. of this half as left operands
+        auto put_s = [&](int x, const float2 *v) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split(v[i], hi[i], lo[i]);
+            tm_st8(tq + kcS + KH / 2 * ch + 8 * x, hi);
+            tm_st8(tq + kcS + KH + KH / 2 * ch + 8 * x, lo);
+        };
+        auto stored = [&](uint32_t bar) {
+            tc_wait_st();
+            tc_fence_before();
+            bar_arrive_warp(bar);
+        };
+        if (nch > 0) {
+#pragma unroll
+            for (int x = 0; x < KH / 16; ++x) put_s(x, S + 8 * x);
+            stored(MBAR(got_s, ch));
+        }
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t ph = n & 1, gates = s0 + Cfg::kGates + (n % kGateRing) * 1024;
+            // R^T = V^T - e^G P^T, tokens 32 ch ..  (past the sequence's end V and P are 0)
+            ok = waitw(MBAR(full_vx, n & 1), (n >> 1) & 1) && waitw(MBAR(got_v, 0), ph) && waitw(MBAR(done1, ch), ph);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
+                float p[16], v[8];
+                tc_ld_32x32b_x16(tq + kcP + 16 * x, p);
+                tm_ld8(tq + kcV + 8 * x, v);
+                wait_loaded(p);
+                wait_loaded(v);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = lds_f4(gates + 64 * x + 16 * i);
+                    const uint32_t v0 = __float_as_uint(v[2 * i]), v1 = __float_as_uint(v[2 * i + 1]);
+                    split(__ffma2_rn(make_float2(-g.x, -g.y), make_float2(p[4 * i], p[4 * i + 1]), make_float2(bf16_lo(v0), bf16_hi(v0))),
+                          hi[2 * i], lo[2 * i]);
+                    split(__ffma2_rn(make_float2(-g.z, -g.w), make_float2(p[4 * i + 2], p[4 * i + 3]), make_float2(bf16_lo(v1), bf16_hi(v1))),
+                          hi[2 * i + 1], lo[2 * i + 1]);
+                }
+                tm_st8(tq + kcR + 8 * x, hi);
+                tm_st8(tq + kcR + 32 + 8 * x, lo);
+            }
+            stored(MBAR(got_r, ch));
+            // V'^T = beta E^T, and decayed to the chunk's end
+            ok = waitw(MBAR(done2, ch), ph);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
+                float e[16];
+                tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
+                wait_loaded(e);
+                uint32_t w[8], hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 er = lds_f4(gates + 4 * kC + 64 * x + 16 * i), be = lds_f4(gates + 8 * kC + 64 * x + 16 * i);
+                    const float2 w0 = __fmul2_rn(make_float2(be.x, be.y), make_float2(e[4 * i], e[4 * i + 1]));
+                    const float2 w1 = __fmul2_rn(make_float2(be.z, be.w), make_float2(e[4 * i + 2], e[4 * i + 3]));
+                    w[2 * i] = pack_bf16x2(w0.x, w0.y);
+                    w[2 * i + 1] = pack_bf16x2(w1.x, w1.y);
+                    split(__fmul2_rn(make_float2(er.x, er.y), w0), hi[2 * i], lo[2 * i]);
+                    split(__fmul2_rn(make_float2(er.z, er.w), w1), hi[2 * i + 1], lo[2 * i + 1]);
+                }
+                tm_st8(tq + kcR + 8 * x, hi);
+                tm_st8(tq + kcR + 32 + 8 * x, lo);
+                tm_st8(tq + kcW + 8 * x, w);
+            }
+            stored(MBAR(got_w, ch));
+            const float gC = ldsf(gates + 4 * (kC - 1));
+            ok = waitw(MBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < KH / 16; ++x) {
+                float ds[16];
+                tc_ld_32x32b_x16(tq + kcP + KH * ch + 16 * x, ds);
+                wait_loaded(ds);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
+                if (n + 1 < nch) put_s(x, S + 8 * x);
+            }
+            if (n + 1 < nch) stored(MBAR(got_s, ch));
+        }
+        if (ok && live) {
+#pragma unroll
+            for (int i = 0; i < KH / 2; ++i) {
+                args.S_out[s_at + (size_t)(2 * i) * dv] = S[i].x;
+                args.S_out[s_at + (size_t)(2 * i + 1) * dv] = S[i].y;
             }
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (issuer) {
+    if (tid == 0 && sm->abort_flag) atomicExch(args.s.status, kStatusTimeout);
+    if (warp == kIssuer) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(sm->tmem_base, 512);
     }
 }
 
