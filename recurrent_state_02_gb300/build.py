@@ -18,7 +18,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "liblinattn.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "backward.cu", "beam.cu", "bwd_tc.cu", "decay.cu", "decay_tc.cu", "decode.cu", "delta.cu", "delta_tc.cu",
-           "gdelta.cu", "gdelta_tc.cu", "logprob.cu", "prefill_f32.cu", "prefill_tc.cu", "state_tc.cu"]
+           "gdelta.cu", "gdelta_bwd.cu", "gdelta_tc.cu", "logprob.cu", "prefill_f32.cu", "prefill_tc.cu", "state_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -1213,10 +1213,24 @@ la_status la_gated_delta_decode_step(const void *q, const void *k, const void *v
     return from_cuda(la::launch_gdelta_rec(s, f, bf16, st));
 }
 
+namespace {
+
+// Whether the gradients of these sizes run in chunks (with every token array on a 16-byte boundary).
+bool gdelta_tc_backward_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv)
+{
+    return gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, false) && dv <= 128;
+}
+
+}  // namespace
+
 size_t la_gated_delta_backward_workspace_bytes(int B, int H, int Hk, int T, int r, int dv, la_dtype dtype)
 {
     if (check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, 1.f) != LA_OK || T == 0) return 0;
-    return sizeof(float) * la::gdelta_rec_backward_floats(B, H, T, r, dv);
+    // (enough for the recurrences too: misaligned arrays take them)
+    const size_t rec = sizeof(float) * la::gdelta_rec_backward_floats(B, H, T, r, dv);
+    if (!gdelta_tc_backward_sizes(dtype, B, H, Hk, T, r, dv)) return rec;
+    const size_t tc = la::gdelta_tc_backward_bytes(gdelta_shape(B, H, Hk, T, r, dv, nullptr, nullptr, nullptr));
+    return rec > tc ? rec : tc;
 }
 
 la_status la_gated_delta_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,
@@ -1236,7 +1250,8 @@ la_status la_gated_delta_backward(const void *q, const void *k, const void *v, l
         const size_t bytes = sizeof(float) * (size_t)B * H * r * dv;
         return from_cuda(dS_T ? cudaMemcpyAsync(dS0, dS_T, bytes, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(dS0, 0, bytes, st));
     }
-    const la::GdeltaShape s = gdelta_shape(B, H, Hk, T, r, dv, alpha, beta, nullptr);
+    const la::GdeltaShape s = gdelta_shape(B, H, Hk, T, r, dv, alpha, beta, status_word());
+    if (!s.status) return LA_ERR_CUDA;
     la::GdeltaBackward g;
     g.q = q, g.k = k, g.v = v, g.dy = dy;
     g.S0 = S0, g.dS_T = dS_T;
@@ -1244,6 +1259,16 @@ la_status la_gated_delta_backward(const void *q, const void *k, const void *v, l
     g.dalpha = dalpha, g.dbeta = dbeta, g.dS0 = dS0;
     g.scale = scale;
     g.ws = static_cast<float *>(workspace);
+    bool tc = gdelta_tc_backward_sizes(dtype, B, H, Hk, T, r, dv);
+    for (const void *p : {q, k, v, dy, (const void *)dq, (const void *)dk, (const void *)dv_out}) tc = tc && aligned(p, 16);
+    if (tc) {
+        la::GdeltaTcBackMaps m;
+        auto map = [&](CUtensorMap *t, const void *p, int heads, int cols) {
+            return make_map_bf16(t, p, (long long)B * heads, T, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        if (!map(&m.q, q, Hk, r) || !map(&m.k, k, Hk, r) || !map(&m.v, v, H, dv) || !map(&m.dy, dy, H, dv)) return LA_ERR_CUDA;
+        return from_cuda(la::launch_gdelta_tc_backward(m, s, g, st));
+    }
     return from_cuda(la::launch_gdelta_rec_backward(s, g, dtype == LA_DTYPE_BF16, st));
 }
 

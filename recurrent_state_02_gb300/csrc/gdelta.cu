@@ -511,12 +511,13 @@ template <bool BF16>
 cudaError_t launch_last_passes(const GdeltaShape &s, const GdeltaBackward &g, const float *e, const float *lam, const float *dq,
                                const float *dk, const float *S_T, float *dG, cudaStream_t stream)
 {
-    const long long tokens = (long long)s.B * s.H * s.T, elems = (long long)s.B * s.Hk * s.T * s.r;
+    const long long tokens = (long long)s.B * s.H * s.T;
     float *dal = s.alpha ? g.dalpha : nullptr;
     if (tokens > 0) {
         gdelta_token_terms_kernel<BF16><<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(s, g.q, g.v, dq, lam, e, g.dbeta,
                                                                                         dal ? dG : nullptr);
-        gdelta_group_sum_kernel<BF16><<<(unsigned)((elems + 255) / 256), 256, 0, stream>>>(s, dq, dk, g.dq, g.dk);
+        const cudaError_t st = launch_gdelta_group_sum(s, dq, dk, BF16, g.dq, g.dk, stream);
+        if (st != cudaSuccess) return st;
     }
     if (dal && tokens > 0) gdelta_gate_sum_kernel<<<(unsigned)(s.B * s.H), 256, 0, stream>>>(s, S_T, g.dS_T, dG, dal);
     return cudaGetLastError();
@@ -538,6 +539,15 @@ cudaError_t launch_gdelta_decode(const GdeltaShape &s, const void *q, const void
                                  float scale, void *y, cudaStream_t stream)
 {
     return bf16 ? launch_dec<true>(s, q, k, v, S, scale, y, stream) : launch_dec<false>(s, q, k, v, S, scale, y, stream);
+}
+
+cudaError_t launch_gdelta_group_sum(const GdeltaShape &s, const float *dq, const float *dk, bool bf16, void *dq_out, void *dk_out,
+                                    cudaStream_t stream)
+{
+    const unsigned grid = (unsigned)(((long long)s.B * s.Hk * s.T * s.r + 255) / 256);
+    if (bf16) gdelta_group_sum_kernel<true><<<grid, 256, 0, stream>>>(s, dq, dk, dq_out, dk_out);
+    else gdelta_group_sum_kernel<false><<<grid, 256, 0, stream>>>(s, dq, dk, dq_out, dk_out);
+    return cudaGetLastError();
 }
 
 // e, lam [B,H,T,dv]; w (then dk), dq [B,H,T,r]; S_T; dG [B,H,T]

@@ -43,6 +43,10 @@ struct GdeltaBackward {
 size_t gdelta_rec_backward_floats(int B, int H, int T, int r, int dv);
 cudaError_t launch_gdelta_rec_backward(const GdeltaShape &s, const GdeltaBackward &g, bool bf16, cudaStream_t stream);
 
+// dq and dk [B,Hk,T,r] as the sums of FP32 [B,H,T,r] over the value heads that share a key head.
+cudaError_t launch_gdelta_group_sum(const GdeltaShape &s, const float *dq, const float *dk, bool bf16, void *dq_out, void *dk_out,
+                                    cudaStream_t stream);
+
 // Token log-probabilities (logprob.cu): rows of logits, row_stride elements apart.
 struct LogprobArgs {
     const void *logits = nullptr;

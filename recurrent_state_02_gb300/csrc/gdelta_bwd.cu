@@ -1,0 +1,904 @@
+// gdelta_bwd.cu -- the gradients of the gated delta rule in chunks of 64 tokens on the tensor cores (BF16 inputs, r 64 or
+// 128, dv 64 or 128).
+//
+// With the chunk form of gdelta_tc.cu (E = X R, R = V - e^G K S, V' = beta E, Y = scale (e^G Q S + A V'),
+// S_next = e^{G_C} S + K^T (e^{G_C - G} V')) and dS the gradient of the state behind the chunk, the chain rule gives
+//     D = dL/dV' = scale A^T dY + e^{G_C - G} K dS,      N = dL/dR = X^T (beta D) = dL/dV,
+//     dS_before = e^{G_C} dS + Q^T (scale e^G dY) - K^T (e^G N),
+// a recurrence over the chunks like the forward one, run backwards.  Then, for every chunk by itself, with dA = scale dY V'^T and
+// Z = N E^T, where dec_ij = e^{G_i - G_j}:
+//     dP = dA . dec (j <= i),  dL = -Z diag(beta) . dec (j < i)                     gradients of Q K^T and K K^T
+//     dQ = dP K + scale e^G dY S^T
+//     dK = dP^T Q + dL K + dL^T K - e^G N S^T + beta e^{G_C - G} E dS^T
+//     dbeta_j = Z_jj / beta_j                                                       (N_j is beta_j times its error's gradient)
+//     dlog alpha_t = <S_next, dS> + sum_{s >= t, in the chunk} (q_s . (scale e^G dY S^T)_s + sum_j A_sj dA_sj - v_s . N_s)
+// (the gates' gradient is anchored at every chunk's end, so that nothing is summed over the sequence).
+// Kernels: gdelta_prep (A, X, gates), the forward chain again, keeping S before and E of every chunk, the backward chain,
+// keeping dS behind and N, and a kernel over all chunks.
+// Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand; what reaches dq and
+// dk only, the high one.
+
+#include "gdelta_tc.cuh"
+
+namespace la {
+namespace {
+
+constexpr uint32_t kImg = 128 * 128;             // 16 KB: 128 value columns (rows) x 64 BF16
+constexpr uint32_t kTokImg = 2 * kImg;           // E or N: [value column][token], two parts
+template <int KD>
+constexpr uint32_t kStateImg = KD / 64 * kImg;   // a part of S or dS: [value column][state row] by blocks of 64 rows
+
+// ----------------------------------------------------------------- the chains
+// Roles as in gdelta_chain_kernel; the helpers bring V (backwards: scale e^G dY, in two parts) to its lanes, and take S
+// and E (dS and N) of every chunk to memory.
+constexpr int kOwners = 8, kHelpers = 4, kIssuer = 12, kLoader = 13;
+constexpr int kThreads = 512;
+constexpr int kGateRing = 4;
+constexpr uint32_t kGateStep = 2048;
+constexpr int kRegsOwn = 160, kRegsHelp = 104, kRegsRest = 88;   // 2 x 160 + 104 + 88 = 4 x 128
+
+template <int KD, bool REV>
+struct BackCfg {
+    static constexpr uint32_t kTK = KD / 64 * kTile;
+    // a stage (two): K, V or dY (two blocks of 64 columns), X's parts; backwards also Q and A's parts
+    static constexpr uint32_t kSK = 0, kSV = kTK, kSX = kSV + 2 * kTile, kSQ = kSX + 2 * kTile, kSA = kSQ + kTK,
+                              kStage = REV ? kSA + 2 * kTile : kSQ;
+    // what goes to memory: S (two parts), then E; backwards dS and N share the space, and dv has its own
+    static constexpr uint32_t kOutS = 2 * kStage, kOutE = REV ? kOutS : kOutS + 2 * kStateImg<KD>, kOutV = kOutE + kTokImg,
+                              kGates = REV ? kOutV + 2 * kTile : kOutV, kSmall = kGates + kGateRing * kGateStep;
+};
+static_assert(kStateImg<128> <= kTokImg, "dS's high part fits where N is staged");
+// TMEM columns: S^T (two parts), P^T and E^T (then dS^T), (A^T dY)^T, the scaled dY^T (two parts), R^T (two parts, then the decayed
+// V'^T's, or the scaled N^T's), V^T
+constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcA = 256, kcY = 320, kcR = 384, kcV = 448;
+
+struct alignas(16) BSmall {
+    uint64_t full[2];
+    uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (4 warps)
+    uint64_t got_v, s_read, e_read;          // V^T (dY^T) is there, S and E have been read (the helpers)
+    uint64_t done0, done1[2], done2[2];      // A^T dY, halves of P, E
+    uint64_t done3[4];                       // halves of dS of even and odd chunks
+    uint64_t fin;
+    uint32_t tmem_base;
+    int abort_flag;
+    float part[kHelpers];
+};
+#define BBAR(name, i) (sS + (uint32_t)offsetof(BSmall, name) + 8 * (uint32_t)(i))
+
+template <int KD, bool REV>
+constexpr uint32_t kBSmemBytes = BackCfg<KD, REV>::kSmall + sizeof(BSmall) + 1024;
+static_assert(kBSmemBytes<128, true> <= 232448 && kBSmemBytes<128, false> <= 232448, "shared memory budget");
+
+__device__ __forceinline__ float2 unpack(uint32_t x) { return make_float2(bf16_lo(x), bf16_hi(x)); }
+
+template <int KD, bool REV>
+__global__ void __launch_bounds__(kThreads, 1)
+gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ GdeltaTcBackArgs args)
+{
+    using Cfg = BackCfg<KD, REV>;
+    constexpr int KH = KD / 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = align1024(smem_raw);
+    BSmall *sm = reinterpret_cast<BSmall *>(base + Cfg::kSmall);
+    const uint32_t s0 = smem_u32(base), sS = s0 + Cfg::kSmall;
+    auto wait1 = [&](uint32_t bar, uint32_t parity) { return bounded_wait<false>(sS + offsetof(BSmall, abort_flag), bar, parity); };
+    auto waitw = [&](uint32_t bar, uint32_t parity) { return bounded_wait<true>(sS + offsetof(BSmall, abort_flag), bar, parity); };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = args.s.H, dv = args.s.dv, T = args.s.T, nch = (T + kC - 1) / kC;
+    const int h = blockIdx.x % H, b = blockIdx.x / H;
+    const size_t bh = blockIdx.x;
+    auto chunk = [&](int n) { return REV ? nch - 1 - n : n; };
+
+    if (tid == 0) {
+        for (uint64_t *bar = sm->full; bar <= &sm->fin; ++bar)
+            mbar_init(bar, bar >= sm->got_s && bar < &sm->got_v ? kOwners / 2 : bar >= &sm->got_v && bar <= &sm->e_read ? kHelpers : 1);
+        sm->abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == kIssuer) {
+        tmem_alloc(&sm->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp >= kOwners + kHelpers) {
+        regs_dec<kRegsRest>();
+        if (warp == kLoader && elect_one()) {
+            const int hk = h / (H / args.s.Hk), kh = b * args.s.Hk + hk;
+            int n1 = 0;
+#pragma unroll 1
+            for (int n = 0; n < nch; ++n) {
+                const uint32_t st = s0 + (n & 1) * Cfg::kStage, bar = BBAR(full, n & 1);
+                const int c = chunk(n);
+                const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
+                if (n >= 2 && !wait1(BBAR(done3, 2 + (n & 1)), ((n >> 1) - 1) & 1)) break;
+                bar_expect(bar, (REV ? 2 : 1) * Cfg::kTK + dv / 64 * kTile + (REV ? 4 : 2) * kTile + kGateBytesB);
+#pragma unroll 1
+                for (int x = 0; x < KD / 64; ++x) tma_load(st + Cfg::kSK + x * kTile, &map_k, bar, 64 * x, c * kC, kh);
+#pragma unroll 1
+                for (int x = 0; x < dv / 64; ++x) tma_load(st + Cfg::kSV + x * kTile, &map_v, bar, 64 * x, c * kC, (int)bh);
+                bulk_copy(s0 + Cfg::kGates + (n % kGateRing) * kGateStep, w + kWsGates, kGateBytesB, bar);
+                bulk_copy(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
+                if (REV) {
+#pragma unroll 1
+                    for (int x = 0; x < KD / 64; ++x) tma_load(st + Cfg::kSQ + x * kTile, &map_q, bar, 64 * x, c * kC, kh);
+                    bulk_copy(st + Cfg::kSA, w + kWsA, kTile, bar);
+                    bulk_copy(st + Cfg::kSA + kTile, w + kWsAl, kTile, bar);
+                }
+                n1 = n + 1;
+            }
+            // loads still in flight complete before the CTA exits (also after a wait that was given up)
+#pragma unroll 1
+            for (int i = max(0, n1 - 2); i < n1; ++i) wait1(BBAR(full, i & 1), (i >> 1) & 1);
+        } else if (warp == kIssuer && elect_one()) {
+            constexpr uint32_t id64 = idesc_bf16_f32(128, 64, false, false), id32 = idesc_bf16_f32(128, 32, false, REV),
+                               idP = idesc_bf16_f32(128, 32, false, false), idS = idesc_bf16_f32(128, KH, false, true),
+                               idA = idesc_bf16_f32(128, 64, true, true);
+            constexpr uint32_t kHalfRows = (32 * 128) >> 4;
+            // (A^T dY)^T = dY^T A, both parts of A
+            auto mma_a = [&](int n) {
+                const uint32_t st = s0 + (n & 1) * Cfg::kStage;
+                const uint32_t ylo = desc_lo(st + Cfg::kSV, kTile), alo = desc_lo(st + Cfg::kSA, kTile);
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t o = (i & 3) * (2048 >> 4);
+                    mma_ss(kcA, ylo + o, kHi128, alo + (i >> 2) * (kTile >> 4) + o, kHi128, idA, i > 0);
+                }
+                bar_commit(BBAR(done0, 0));
+            };
+            if (REV && nch > 0 && wait1(BBAR(full, 0), 0)) {
+                tc_fence_after();
+                mma_a(0);
+            }
+#pragma unroll 1
+            for (int n = 0; n < nch; ++n) {
+                const uint32_t st = s0 + (n & 1) * Cfg::kStage, ph = n & 1;
+                const uint32_t klo = desc_lo(st + Cfg::kSK, 16), xlo = desc_lo(st + Cfg::kSX, REV ? kTile : 16);
+                // 1  P^T = S^T K^T
+                if (!wait1(BBAR(full, n & 1), (n >> 1) & 1) || !wait1(BBAR(got_s, 0), ph)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int i = 0; i < KD / 16; ++i) {
+                    const int kk = i >> 1;
+                    mma_ts(kcP, kcS + (i & 1) * KH + kk * 8, klo + kk * 2, kHi128, id64, i > 0);
+                }
+                if (!wait1(BBAR(got_s, 1), ph)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int t = REV ? 1 - u : u;
+                    const uint32_t k2 = klo + t * kHalfRows + ((KD == 128 ? kTile : 64u) >> 4);
+#pragma unroll 1
+                    for (int i = 0; i < KD / 16; ++i) {
+                        const int kk = i >> 1;
+                        mma_ts(kcP + 32 * t, kcS + (i & 1) * KH + KD / 4 + kk * 8, k2 + kk * 2, kHi128, idP, true);
+                    }
+                    bar_commit(BBAR(done1, t));
+                }
+                // 2  E^T = R^T X^T, the first half of R first; backwards N^T = (beta D)^T X, the second half first
+                bool ok = true;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int t = REV ? 1 - u : u;
+                    ok = wait1(BBAR(got_r, t), ph);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int w = u; w < 2; ++w) {           // half o of the result from half t of R
+                        const int o = REV ? 1 - w : w;
+                        const uint32_t d = kcE + 32 * o, r = kcR + 16 * t;
+                        // X's rows are the result's tokens forwards, its columns backwards
+                        const uint32_t xo = xlo + (REV ? t * kHalfRows + 4 * o : o * kHalfRows + 4 * t);
+                        constexpr uint32_t kStep = REV ? 2048 >> 4 : 2;
+#pragma unroll 1
+                        for (int kk = 0; kk < 2; ++kk) {
+                            mma_ts(d, r + kk * 8, xo + kk * kStep, kHi128, id32, u + kk > 0);
+                            mma_ts(d, r + 32 + kk * 8, xo + kk * kStep, kHi128, id32, true);
+                            mma_ts(d, r + kk * 8, xo + kk * kStep + (kTile >> 4), kHi128, id32, true);
+                        }
+                    }
+                    bar_commit(BBAR(done2, t));
+                }
+                if (!ok) break;
+                // 3  dS^T = V'^T K; backwards (scale e^G dY)^T Q - (e^G N)^T K.  One half of the state's rows after the other
+                // (the second one where E has been read)
+                const uint32_t kmn = desc_lo(st + Cfg::kSK, kTile), qmn = desc_lo(st + Cfg::kSQ, kTile);
+                if (REV) {
+                    if (!wait1(BBAR(got_v, 0), ph)) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i)
+                        mma_ts(kcP, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
+                }
+                if (!wait1(BBAR(got_w, 0), ph) || !wait1(BBAR(got_w, 1), ph)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t half = t * ((KD == 128 ? kTile : 64u) >> 4);
+                    if (t == 1) {
+                        ok = wait1(BBAR(e_read, 0), ph);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (REV) {
+#pragma unroll 1
+                            for (int i = 0; i < 8; ++i)
+                                mma_ts(kcP + KH, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + half + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
+                        }
+                    }
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i)
+                        mma_ts(kcP + KH * t, kcR + (i >> 2) * 32 + (i & 3) * 8, kmn + half + (i & 3) * (2048 >> 4), kHi128, idS, REV || i > 0);
+                    bar_commit(BBAR(done3, 2 * t + (n & 1)));
+                }
+                if (!ok) break;
+                if (REV && n + 1 < nch) {
+                    if (!wait1(BBAR(full, (n + 1) & 1), ((n + 1) >> 1) & 1)) break;
+                    tc_fence_after();
+                    mma_a(n + 1);
+                }
+            }
+            // every MMA completes before the CTA exits
+            bar_commit(BBAR(fin, 0));
+            wait1(BBAR(fin, 0), 0);
+        }
+        __syncwarp();
+    } else if (warp >= kOwners) {
+        regs_dec<kRegsHelp>();
+        const int q4 = warp & 3, d = 32 * q4 + lane, ht = tid - 32 * kOwners;
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
+        const bool live = d < dv;
+        const float scale = args.scale;
+        bool ok = true;
+        // (a helper that gave up waiting still meets the others at their barriers)
+#pragma unroll 1
+        for (int n = 0; n < nch + (REV ? 0 : 1); ++n) {
+            const int c = chunk(n);
+            const uint32_t st = s0 + (n & 1) * Cfg::kStage, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
+            // V's column, or the scaled dY's (0 past the sequence's end, where TMA fills up)
+            if (ok && n < nch) ok = waitw(BBAR(full, n & 1), (n >> 1) & 1);
+            if (ok && n > 0 && n < nch)
+                ok = REV ? waitw(BBAR(done3, 2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1)
+                         : waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1);
+            if (ok && n < nch) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t v[8], lo[8];
+                    const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = 2 * i;
+                        const uint32_t x0 = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
+                                       x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
+                        v[i] = live ? x0 | x1 << 16 : 0;
+                        if (REV) {
+                            const float2 w = unpack(v[i]);
+                            split(make_float2(scale * ldsf(gates + 64 * x + 4 * t) * w.x, scale * ldsf(gates + 64 * x + 4 * t + 4) * w.y),
+                                  v[i], lo[i]);
+                        }
+                    }
+                    tm_st8(tq + (REV ? kcY : kcV) + 8 * x, v);
+                    if (REV) tm_st8(tq + kcY + 32 + 8 * x, lo);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                bar_arrive_warp(BBAR(got_v, 0));
+            }
+            // the state before the chunk (backwards: behind it)
+            if (ht == 0) tma_store_wait_read<0>();
+            named_barrier_sync(1, 32 * kHelpers);
+            if (ok) ok = waitw(BBAR(got_s, 0), n & 1) && waitw(BBAR(got_s, 1), n & 1);
+            if (ok) {
+                tc_fence_after();
+                float2 dot = make_float2(0.f, 0.f);
+                const uint8_t *next = args.S + (bh * (nch + 1) + c + 1) * (2 * kStateImg<KD>);   // (backwards: the state there)
+#pragma unroll 1
+                for (int x = 0; x < KD / 16; ++x) {
+                    float hi[8], lo[8];
+                    tm_ld8(tq + kcS + 8 * x, hi);
+                    tm_ld8(tq + kcS + KH + 8 * x, lo);
+                    const uint32_t o = (x >> 2) * kImg + sw128_offset(d, 2 * (x & 3)), o2 = (x >> 2) * kImg + sw128_offset(d, 2 * (x & 3) + 1);
+                    uint4 s4[4];
+                    if (REV && live) {
+                        s4[0] = *reinterpret_cast<const uint4 *>(next + o);
+                        s4[1] = *reinterpret_cast<const uint4 *>(next + o2);
+                        s4[2] = *reinterpret_cast<const uint4 *>(next + kStateImg<KD> + o);
+                        s4[3] = *reinterpret_cast<const uint4 *>(next + kStateImg<KD> + o2);
+                    }
+                    wait_loaded(hi);
+                    wait_loaded(lo);
+                    uint32_t hw[8], lw[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) hw[i] = __float_as_uint(hi[i]), lw[i] = __float_as_uint(lo[i]);
+                    sts4(s0 + Cfg::kOutS + o, hw[0], hw[1], hw[2], hw[3]);
+                    sts4(s0 + Cfg::kOutS + o2, hw[4], hw[5], hw[6], hw[7]);
+                    if (!REV) {
+                        sts4(s0 + Cfg::kOutS + kStateImg<KD> + o, lw[0], lw[1], lw[2], lw[3]);
+                        sts4(s0 + Cfg::kOutS + kStateImg<KD> + o2, lw[4], lw[5], lw[6], lw[7]);
+                    } else if (live) {
+                        const uint32_t sh[8] = {s4[0].x, s4[0].y, s4[0].z, s4[0].w, s4[1].x, s4[1].y, s4[1].z, s4[1].w},
+                                       sl[8] = {s4[2].x, s4[2].y, s4[2].z, s4[2].w, s4[3].x, s4[3].y, s4[3].z, s4[3].w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dot = __ffma2_rn(__fadd2_rn(unpack(hw[i]), unpack(lw[i])), __fadd2_rn(unpack(sh[i]), unpack(sl[i])), dot);
+                    }
+                }
+                tc_fence_before();
+                bar_arrive_warp(BBAR(s_read, 0));
+                if (REV) {
+                    float p = dot.x + dot.y;
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+                    if (lane == 0) sm->part[q4] = p;
+                }
+            }
+            if (REV) {
+                fence_proxy_async_smem();
+                named_barrier_sync(1, 32 * kHelpers);
+                if (ht == 0) {
+                    if (ok) {
+                        bulk_store(args.dS + (bh * nch + c) * kStateImg<KD>, s0 + Cfg::kOutS, kStateImg<KD>);
+                        args.anchor[bh * nch + c] = (sm->part[0] + sm->part[1]) + (sm->part[2] + sm->part[3]);
+                    }
+                    tma_store_commit();
+                    tma_store_wait_read<0>();
+                }
+                named_barrier_sync(1, 32 * kHelpers);
+            }
+            // E, or N
+            if (ok && n < nch) ok = waitw(BBAR(done2, 0), n & 1) && waitw(BBAR(done2, 1), n & 1);
+            if (ok && n < nch) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    float e[8];
+                    tm_ld8(tq + kcE + 8 * x, e);
+                    wait_loaded(e);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
+                    const uint32_t o = s0 + Cfg::kOutE + sw128_offset(d, x);
+                    sts4(o, hi[0], hi[1], hi[2], hi[3]);
+                    sts4(o + kImg, lo[0], lo[1], lo[2], lo[3]);
+                    if (REV) {
+                        const uint32_t a = s0 + Cfg::kOutV + col + x * (8 * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sts_u16(a + i * 128 + ((c16 ^ i) << 4), pack_bf16x2(e[i] * ldsf(gates + kGateRatio + 32 * x + 4 * i), 0.f));
+                    }
+                }
+                tc_fence_before();
+                bar_arrive_warp(BBAR(e_read, 0));
+            }
+            fence_proxy_async_smem();
+            named_barrier_sync(1, 32 * kHelpers);
+            if (ht == 0) {
+                if (ok && !REV) bulk_store(args.S + (bh * (nch + 1) + c) * (2 * kStateImg<KD>), s0 + Cfg::kOutS, 2 * kStateImg<KD>);
+                if (ok && n < nch) bulk_store((REV ? args.N : args.E) + (bh * nch + c) * kTokImg, s0 + Cfg::kOutE, kTokImg);
+                tma_store_commit();
+            }
+            if (REV && ok) {
+                const int per = dv / 8, rows = min(kC, T - c * kC);
+                uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC) * dv;
+#pragma unroll 1
+                for (int x = ht; x < rows * per; x += 32 * kHelpers) {
+                    const int t = x / per, w = x % per;
+                    *reinterpret_cast<uint4 *>(y0 + (size_t)t * dv + 8 * w) = lds4(s0 + Cfg::kOutV + (w >> 3) * kTile + sw128_offset(t, w & 7));
+                }
+            }
+        }
+        if (ht == 0) tma_store_wait_all<0>();
+        tc_fence_before();
+    } else {
+        regs_inc<kRegsOwn>();
+        const int q4 = warp & 3, ch = warp >> 2, d = 32 * q4 + lane;
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const bool live = d < dv;
+        const float scale = args.scale;
+        const float *S_init = REV ? args.dS_T : args.S0;
+        float2 S[KH / 2];                               // S[i]: state rows KH ch + 2 i, + 1 of the lane's column
+        const size_t s_at = (bh * KD + KH * ch) * dv + d;
+#pragma unroll
+        for (int i = 0; i < KH / 2; ++i) {
+            S[i] = make_float2(0.f, 0.f);
+            if (S_init && live) S[i] = make_float2(S_init[s_at + (size_t)(2 * i) * dv], S_init[s_at + (size_t)(2 * i + 1) * dv]);
+        }
+        auto put_s = [&](int x, const float2 *v) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split(v[i], hi[i], lo[i]);
+            tm_st8(tq + kcS + KH / 2 * ch + 8 * x, hi);
+            tm_st8(tq + kcS + KH + KH / 2 * ch + 8 * x, lo);
+        };
+        auto stored = [&](uint32_t bar) {
+            tc_wait_st();
+            tc_fence_before();
+            bar_arrive_warp(bar);
+        };
+#pragma unroll
+        for (int x = 0; x < KH / 16; ++x) put_s(x, S + 8 * x);
+        stored(BBAR(got_s, ch));
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n) {
+            const uint32_t ph = n & 1, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
+            // R^T = V^T - e^G P^T; backwards beta D^T = beta (scale (A^T dY)^T + e^{G_C - G} P^T)
+            ok = waitw(BBAR(full, n & 1), (n >> 1) & 1) && waitw(REV ? BBAR(done0, 0) : BBAR(got_v, 0), ph) && waitw(BBAR(done1, ch), ph);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
+                float p[16], v[REV ? 16 : 8];
+                tc_ld_32x32b_x16(tq + kcP + 16 * x, p);
+                if constexpr (REV) tc_ld_32x32b_x16(tq + kcA + 16 * x, v);
+                else tm_ld8(tq + kcV + 8 * x, v);
+                wait_loaded(p);
+                wait_loaded(v);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 pp = make_float2(p[2 * i], p[2 * i + 1]);
+                    float2 r;
+                    if constexpr (REV) {
+                        const float2 er = make_float2(ldsf(gates + 4 * kC + 64 * x + 8 * i), ldsf(gates + 4 * kC + 64 * x + 8 * i + 4)),
+                                     be = make_float2(ldsf(gates + 8 * kC + 64 * x + 8 * i), ldsf(gates + 8 * kC + 64 * x + 8 * i + 4));
+                        r = __fmul2_rn(be, __ffma2_rn(make_float2(scale, scale), make_float2(v[2 * i], v[2 * i + 1]), __fmul2_rn(er, pp)));
+                    } else {
+                        const float2 g = make_float2(-ldsf(gates + 64 * x + 8 * i), -ldsf(gates + 64 * x + 8 * i + 4));
+                        r = __ffma2_rn(g, pp, unpack(__float_as_uint(v[i])));
+                    }
+                    split(r, hi[i], lo[i]);
+                }
+                tm_st8(tq + kcR + 8 * x, hi);
+                tm_st8(tq + kcR + 32 + 8 * x, lo);
+            }
+            stored(BBAR(got_r, ch));
+            // beta e^{G_C - G} E^T; backwards -e^G N^T
+            ok = waitw(BBAR(done2, ch), ph);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
+                float e[16];
+                tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
+                wait_loaded(e);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = lds_f4(gates + (REV ? 0 : 4 * kC) + 64 * x + 16 * i);
+                    float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
+                    if (!REV) f = lds_f4(gates + 8 * kC + 64 * x + 16 * i);
+                    split(__fmul2_rn(make_float2(g.x, g.y), __fmul2_rn(make_float2(f.x, f.y), make_float2(e[4 * i], e[4 * i + 1]))),
+                          hi[2 * i], lo[2 * i]);
+                    split(__fmul2_rn(make_float2(g.z, g.w), __fmul2_rn(make_float2(f.z, f.w), make_float2(e[4 * i + 2], e[4 * i + 3]))),
+                          hi[2 * i + 1], lo[2 * i + 1]);
+                }
+                tm_st8(tq + kcR + 8 * x, hi);
+                tm_st8(tq + kcR + 32 + 8 * x, lo);
+            }
+            stored(BBAR(got_w, ch));
+            const float gC = ldsf(gates + 4 * (kC - 1));
+            // (the helpers have read S of this chunk before it makes room for the next one's)
+            ok = waitw(BBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1) && waitw(BBAR(s_read, 0), ph);
+            if (!ok) break;
+            tc_fence_after();
+            const bool more = !REV || n + 1 < nch;
+#pragma unroll
+            for (int x = 0; x < KH / 16; ++x) {
+                float ds[16];
+                tc_ld_32x32b_x16(tq + kcP + KH * ch + 16 * x, ds);
+                wait_loaded(ds);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
+                if (more) put_s(x, S + 8 * x);
+            }
+            if (more) stored(BBAR(got_s, ch));
+        }
+        if (REV && ok && live) {
+#pragma unroll
+            for (int i = 0; i < KH / 2; ++i) {
+                args.dS0[s_at + (size_t)(2 * i) * dv] = S[i].x;
+                args.dS0[s_at + (size_t)(2 * i + 1) * dv] = S[i].y;
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid == 0 && sm->abort_flag) atomicExch(args.s.status, kStatusTimeout);
+    if (warp == kIssuer) {
+        tc_fence_after();
+        tmem_dealloc(sm->tmem_base, 512);
+    }
+}
+
+// -------------------------------------------------- the gradients of a chunk
+// One CTA per chunk and head: 8 warps compute (warp w: rows 16 (w % 4) .. of the M = 64 accumulators, half w / 4 of their columns),
+// one issues the MMAs, one loads.
+constexpr int kGComp = 8, kGIssuer = 8, kGLoader = 9, kGThreads = 320;
+template <int KD>
+struct GradCfg {
+    static constexpr uint32_t kTK = KD / 64 * kTile;
+    // Q, K, dY, V, E and N (two parts each; dS's blocks take the place of their low parts), S (two parts), dP, dL, the gates
+    static constexpr uint32_t kQ = 0, kK = kTK, kY = 2 * kTK, kV = kY + 2 * kTile, kE = kV + 2 * kTile, kN = kE + kTokImg,
+                              kS = kN + kTokImg, kP = kS + 2 * kStateImg<KD>, kL = kP + kTile, kGates = kL + kTile,
+                              kSmall = kGates + kGateStep;
+};
+// TMEM columns: Q K^T, dY E^T, N E^T, V N^T (then dP K and dP^T Q + dL K + dL^T K), dY S^T (then E dS^T), N S^T
+constexpr uint32_t kgP = 0, kgYE = 64, kgNE = 128, kgVN = 192, kgQ = 0, kgK = 128, kgYS = 256, kgNS = 384;
+struct alignas(16) GSmall {
+    uint64_t full[3];            // Q, K, dY, V, E, N; S; dS
+    uint64_t got_p, got_x;       // dP and dL are in shared memory; dY S^T has been read
+    uint64_t doneG, doneS, doneQ, doneF;
+    uint64_t fin;
+    uint32_t tmem_base;
+    int abort_flag;
+    float dG[2][kC], diag[kC];
+};
+#define GBAR(name, i) (sS + (uint32_t)offsetof(GSmall, name) + 8 * (uint32_t)(i))
+template <int KD>
+constexpr uint32_t kGSmemBytes = GradCfg<KD>::kSmall + sizeof(GSmall) + 1024;
+static_assert(kGSmemBytes<128> <= 232448, "shared memory budget");
+
+template <int KD, bool OUT32>
+__global__ void __launch_bounds__(kGThreads, 1)
+gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dy,
+                   const __grid_constant__ GdeltaTcBackArgs args)
+{
+    using Cfg = GradCfg<KD>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = align1024(smem_raw);
+    GSmall *sm = reinterpret_cast<GSmall *>(base + Cfg::kSmall);
+    const uint32_t s0 = smem_u32(base), sS = s0 + Cfg::kSmall;
+    auto wait1 = [&](uint32_t bar, uint32_t parity) { return bounded_wait<false>(sS + offsetof(GSmall, abort_flag), bar, parity); };
+    auto waitw = [&](uint32_t bar, uint32_t parity) { return bounded_wait<true>(sS + offsetof(GSmall, abort_flag), bar, parity); };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = args.s.H, dv = args.s.dv, T = args.s.T, nch = (T + kC - 1) / kC;
+    const int c = blockIdx.x % nch;
+    const size_t bh = blockIdx.x / nch;
+    const int h = (int)(bh % H), b = (int)(bh / H);
+
+    if (tid == 0) {
+        for (uint64_t *bar = sm->full; bar <= &sm->fin; ++bar) mbar_init(bar, bar == &sm->got_p || bar == &sm->got_x ? kGComp : 1);
+        sm->abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == kGIssuer) {
+        tmem_alloc(&sm->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp == kGLoader) {
+        if (elect_one()) {
+            const int kh = b * args.s.Hk + h / (H / args.s.Hk);
+            const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
+            bar_expect(GBAR(full, 0), 2 * Cfg::kTK + 2 * (dv / 64) * kTile + 2 * kTokImg + kGateBytesB);
+            bulk_copy(s0 + Cfg::kGates, w + kWsGates, kGateBytesB, GBAR(full, 0));
+#pragma unroll 1
+            for (int x = 0; x < KD / 64; ++x) {
+                tma_load(s0 + Cfg::kQ + x * kTile, &map_q, GBAR(full, 0), 64 * x, c * kC, kh);
+                tma_load(s0 + Cfg::kK + x * kTile, &map_k, GBAR(full, 0), 64 * x, c * kC, kh);
+            }
+#pragma unroll 1
+            for (int x = 0; x < dv / 64; ++x) {
+                tma_load(s0 + Cfg::kY + x * kTile, &map_dy, GBAR(full, 0), 64 * x, c * kC, (int)bh);
+                tma_load(s0 + Cfg::kV + x * kTile, &map_v, GBAR(full, 0), 64 * x, c * kC, (int)bh);
+            }
+            bulk_copy(s0 + Cfg::kE, args.E + (bh * nch + c) * kTokImg, kTokImg, GBAR(full, 0));
+            bulk_copy(s0 + Cfg::kN, args.N + (bh * nch + c) * kTokImg, kTokImg, GBAR(full, 0));
+            bar_expect(GBAR(full, 1), 2 * kStateImg<KD>);
+            bulk_copy(s0 + Cfg::kS, args.S + (bh * (nch + 1) + c) * (2 * kStateImg<KD>), 2 * kStateImg<KD>, GBAR(full, 1));
+            // dS's blocks over the low parts of E and N, which the first products have read
+            const bool ok = wait1(GBAR(doneG, 0), 0);
+            if (ok) {
+                bar_expect(GBAR(full, 2), kStateImg<KD>);
+#pragma unroll 1
+                for (int x = 0; x < KD / 64; ++x)
+                    bulk_copy(s0 + (x ? Cfg::kN : Cfg::kE) + kImg, args.dS + (bh * nch + c) * kStateImg<KD> + x * kImg, kImg, GBAR(full, 2));
+            }
+            // what was started lands before the CTA exits
+            wait1(GBAR(full, 0), 0);
+            wait1(GBAR(full, 1), 0);
+            if (ok) wait1(GBAR(full, 2), 0);
+        }
+        __syncwarp();
+    } else if (warp == kGIssuer) {
+        if (elect_one()) {
+            constexpr uint32_t M = 64;
+            const int nk = dv / 16;
+            const uint32_t qk = desc_lo(s0 + Cfg::kQ, 16), kk_ = desc_lo(s0 + Cfg::kK, 16), y = desc_lo(s0 + Cfg::kY, 16),
+                           v = desc_lo(s0 + Cfg::kV, 16), e = desc_lo(s0 + Cfg::kE, kImg), nn = desc_lo(s0 + Cfg::kN, kImg),
+                           S = desc_lo(s0 + Cfg::kS, kImg);
+            constexpr uint32_t kLo = kImg >> 4, kMn = 2048 >> 4;
+            auto kmaj = [&](int k) { return (uint32_t)((k >> 2) * (kTile >> 4) + (k & 3) * 2); };
+            do {
+                if (!wait1(GBAR(full, 0), 0)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < KD / 16; ++k)
+                    mma_ss(kgP, qk + kmaj(k), kHi128, kk_ + kmaj(k), kHi128, idesc_bf16_f32(M, 64, false, false), k > 0);
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k) {
+                    constexpr uint32_t idK = idesc_bf16_f32(M, 64, false, true), idM = idesc_bf16_f32(M, 64, true, true);
+                    const uint32_t o = k * kMn, ok = kmaj(k);
+                    mma_ss(kgYE, y + ok, kHi128, e + o, kHi128, idK, k > 0);
+                    mma_ss(kgNE, nn + o, kHi128, e + o, kHi128, idM, k > 0);
+                    mma_ss(kgVN, v + ok, kHi128, nn + o, kHi128, idK, k > 0);
+                    mma_ss(kgYE, y + ok, kHi128, e + kLo + o, kHi128, idK, true);
+                    mma_ss(kgNE, nn + o, kHi128, e + kLo + o, kHi128, idM, true);
+                    mma_ss(kgVN, v + ok, kHi128, nn + kLo + o, kHi128, idK, true);
+                    mma_ss(kgNE, nn + kLo + o, kHi128, e + o, kHi128, idM, true);
+                }
+                bar_commit(GBAR(doneG, 0));
+                if (!wait1(GBAR(full, 1), 0)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < nk; ++k) {
+                    constexpr uint32_t idK = idesc_bf16_f32(M, KD, false, true), idM = idesc_bf16_f32(M, KD, true, true);
+                    const uint32_t o = k * kMn, ok = kmaj(k);
+                    mma_ss(kgYS, y + ok, kHi128, S + o, kHi128, idK, k > 0);
+                    mma_ss(kgNS, nn + o, kHi128, S + o, kHi128, idM, k > 0);
+                    mma_ss(kgYS, y + ok, kHi128, S + (kStateImg<KD> >> 4) + o, kHi128, idK, true);
+                }
+                bar_commit(GBAR(doneS, 0));
+                if (!wait1(GBAR(got_p, 0), 0)) break;
+                tc_fence_after();
+                {
+                    constexpr uint32_t idK = idesc_bf16_f32(M, KD, false, true), idM = idesc_bf16_f32(M, KD, true, true);
+                    const uint32_t qm = desc_lo(s0 + Cfg::kQ, kTile), km = desc_lo(s0 + Cfg::kK, kTile), p = desc_lo(s0 + Cfg::kP, 16),
+                                   l = desc_lo(s0 + Cfg::kL, 16);
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        mma_ss(kgQ, p + 2 * k, kHi128, km + k * kMn, kHi128, idK, k > 0);          // dP K
+                        mma_ss(kgK, p + k * kMn, kHi128, qm + k * kMn, kHi128, idM, k > 0);        // dP^T Q
+                        mma_ss(kgK, l + 2 * k, kHi128, km + k * kMn, kHi128, idK, true);           // dL K
+                        mma_ss(kgK, l + k * kMn, kHi128, km + k * kMn, kHi128, idM, true);         // dL^T K
+                    }
+                }
+                bar_commit(GBAR(doneQ, 0));
+                if (!wait1(GBAR(full, 2), 0) || !wait1(GBAR(got_x, 0), 0)) break;
+                tc_fence_after();
+                {
+                    constexpr uint32_t idM = idesc_bf16_f32(M, KD, true, true);
+                    const uint32_t dS = desc_lo(s0 + Cfg::kE + kImg, Cfg::kN - Cfg::kE);
+#pragma unroll 1
+                    for (int k = 0; k < nk; ++k) mma_ss(kgYS, e + k * kMn, kHi128, dS + k * kMn, kHi128, idM, k > 0);
+                }
+                bar_commit(GBAR(doneF, 0));
+            } while (false);
+            // every MMA completes before the CTA exits
+            bar_commit(GBAR(fin, 0));
+            wait1(GBAR(fin, 0), 0);
+        }
+        __syncwarp();
+    } else {
+        const int q4 = warp & 3, g = warp >> 2, i = 16 * q4 + (lane & 15), hl = lane >> 4;
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const uint32_t gates = s0 + Cfg::kGates;
+        const float scale = args.scale;
+        float x[KD / 4];                 // scale e^G dY S^T: columns KD / 2 g + 32 p + 16 hl + e
+        bool ok = waitw(GBAR(full, 0), 0) && waitw(GBAR(doneG, 0), 0);
+        float eG = 0.f, eR = 0.f, be = 0.f, acc = 0.f;
+        if (ok) {
+            tc_fence_after();
+            eG = ldsf(gates + 4 * i), eR = ldsf(gates + 4 * kC + 4 * i), be = ldsf(gates + 8 * kC + 4 * i);
+            const float Gh = ldsf(gates + kGateLog + 8 * i), Gl = ldsf(gates + kGateLog + 8 * i + 4);
+            float P[16], YE[16], NE[16], VN[16];
+            tc_ld_16x32bx2_x16<16>(tq + kgP + 32 * g, P);
+            tc_ld_16x32bx2_x16<16>(tq + kgYE + 32 * g, YE);
+            tc_ld_16x32bx2_x16<16>(tq + kgNE + 32 * g, NE);
+            tc_ld_16x32bx2_x16<16>(tq + kgVN + 32 * g, VN);
+            wait_loaded(P);
+            wait_loaded(YE);
+            wait_loaded(NE);
+            wait_loaded(VN);
+            const int j0 = 32 * g + 16 * hl;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int j = j0 + u;
+                const float bj = ldsf(gates + 8 * kC + 4 * j);
+                const float dec = ex2((Gh - ldsf(gates + kGateLog + 8 * j)) + (Gl - ldsf(gates + kGateLog + 8 * j + 4)));
+                const float dA = scale * bj * YE[u];
+                if (j == i) {
+                    acc -= VN[u];
+                    sm->diag[i] = NE[u];
+                }
+                if (j <= i) acc = fmaf(dec * P[u], dA, acc);
+                P[u] = j <= i ? dec * dA : 0.f;
+                NE[u] = j < i ? -bj * dec * NE[u] : 0.f;
+            }
+            const uint32_t o = s0 + sw128_offset(i, j0 >> 3), o2 = s0 + sw128_offset(i, (j0 >> 3) + 1);
+            const uint4 p0 = pack8(P), p1 = pack8(P + 8), l0 = pack8(NE), l1 = pack8(NE + 8);
+            sts4(o + Cfg::kP, p0.x, p0.y, p0.z, p0.w);
+            sts4(o2 + Cfg::kP, p1.x, p1.y, p1.z, p1.w);
+            sts4(o + Cfg::kL, l0.x, l0.y, l0.z, l0.w);
+            sts4(o2 + Cfg::kL, l1.x, l1.y, l1.z, l1.w);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            bar_arrive_warp(GBAR(got_p, 0));
+        }
+        ok = ok && waitw(GBAR(doneS, 0), 0);
+        if (ok) {
+            tc_fence_after();
+            const float f = scale * eG;
+#pragma unroll
+            for (int p = 0; p < KD / 64; ++p) {
+                const int c0 = KD / 2 * g + 32 * p;
+                float t[16];
+                tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, t);
+                wait_loaded(t);
+                const int cc = c0 + 16 * hl;
+                const uint32_t qa = s0 + Cfg::kQ + (cc >> 6) * kTile;
+                const uint4 q0 = lds4(qa + sw128_offset(i, (cc & 63) >> 3)), q1 = lds4(qa + sw128_offset(i, ((cc & 63) >> 3) + 1));
+                const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    x[16 * p + 2 * u] = f * t[2 * u];
+                    x[16 * p + 2 * u + 1] = f * t[2 * u + 1];
+                    acc = fmaf(bf16_lo(qw[u]), x[16 * p + 2 * u], acc);
+                    acc = fmaf(bf16_hi(qw[u]), x[16 * p + 2 * u + 1], acc);
+                }
+            }
+            tc_fence_before();
+            bar_arrive_warp(GBAR(got_x, 0));
+            acc += __shfl_xor_sync(0xffffffffu, acc, 16);
+            if (hl == 0) sm->dG[g][i] = acc;
+        }
+        // (all compute warps meet here, whatever they have waited for)
+        named_barrier_sync(1, 32 * kGComp);
+        const int t0 = c * kC;
+        if (ok && warp == 0) {
+            // dlog alpha: the chunk's terms from each token on, and the anchor at its end
+            const int a0 = 2 * lane;
+            const float d0 = sm->dG[0][a0] + sm->dG[1][a0], d1 = sm->dG[0][a0 + 1] + sm->dG[1][a0 + 1];
+            float inc = d0 + d1;         // from this lane on
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float y = __shfl_down_sync(0xffffffffu, inc, o);
+                if (lane + o < 32) inc += y;
+            }
+            const float anchor = args.anchor[bh * nch + c];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = t0 + a0 + u;
+                if (t >= T) continue;
+                const size_t at = bh * T + t;
+                if (args.dalpha && args.s.alpha) {
+                    const float al = args.s.alpha[at];
+                    args.dalpha[at] = al > 0.f ? (anchor + (u ? inc - d0 : inc)) / al : 0.f;
+                }
+                if (args.dbeta) args.dbeta[at] = sm->diag[a0 + u] / ldsf(gates + 8 * kC + 4 * (a0 + u));
+            }
+        }
+        ok = ok && waitw(GBAR(doneQ, 0), 0) && waitw(GBAR(doneF, 0), 0);
+        if (ok) {
+            tc_fence_after();
+            const size_t row = (bh * T + t0 + i) * KD;
+            const bool in = t0 + i < T;
+            const float fe = be * eR;
+#pragma unroll
+            for (int p = 0; p < KD / 64; ++p) {
+                const int c0 = KD / 2 * g + 32 * p;
+                float a[16], k3[16], ns[16], ed[16];
+                tc_ld_16x32bx2_x16<16>(tq + kgQ + c0, a);
+                tc_ld_16x32bx2_x16<16>(tq + kgK + c0, k3);
+                tc_ld_16x32bx2_x16<16>(tq + kgNS + c0, ns);
+                tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, ed);
+                wait_loaded(a);
+                wait_loaded(k3);
+                wait_loaded(ns);
+                wait_loaded(ed);
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    a[u] += x[16 * p + u];
+                    k3[u] = fmaf(fe, ed[u], fmaf(-eG, ns[u], k3[u]));
+                }
+                if (in) {
+                    const size_t at = row + c0 + 16 * hl;
+                    if (OUT32) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            reinterpret_cast<float4 *>(static_cast<float *>(args.dq) + at)[u] = make_float4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
+                            reinterpret_cast<float4 *>(static_cast<float *>(args.dk) + at)[u] = make_float4(k3[4 * u], k3[4 * u + 1], k3[4 * u + 2], k3[4 * u + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(args.dq) + at)[u] = pack8(a + 8 * u);
+                            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(args.dk) + at)[u] = pack8(k3 + 8 * u);
+                        }
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid == 0 && sm->abort_flag) atomicExch(args.s.status, kStatusTimeout);
+    if (warp == kGIssuer) {
+        tc_fence_after();
+        tmem_dealloc(sm->tmem_base, 512);
+    }
+}
+
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace's parts, in order.
+struct BackSpace {
+    size_t ws, E, N, S, dS, anchor, dq, dk, bytes;
+};
+BackSpace back_space(const GdeltaShape &s)
+{
+    const size_t heads = (size_t)s.B * s.H, nch = (s.T + kC - 1) / kC, state = (size_t)s.r * 256;
+    BackSpace p;
+    p.ws = 0;
+    p.E = p.ws + heads * nch * kWsChunkB;
+    p.N = p.E + heads * nch * kTokImg;
+    p.S = p.N + heads * nch * kTokImg;
+    p.dS = p.S + heads * (nch + 1) * 2 * state;
+    p.anchor = p.dS + heads * nch * state;
+    p.dq = p.anchor + round_up(heads * nch * sizeof(float));
+    const size_t part = s.Hk < s.H ? round_up(heads * s.T * s.r * sizeof(float)) : 0;
+    p.dk = p.dq + part;
+    p.bytes = p.dk + part;
+    return p;
+}
+
+template <int KD>
+cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const GdeltaTcArgs &prep, cudaStream_t stream)
+{
+    static OncePerDevice once_f, once_r, once_g, once_g32;
+    cudaError_t e;
+    if ((e = set_smem_once(gdelta_back_chain_kernel<KD, false>, kBSmemBytes<KD, false>, once_f)) != cudaSuccess) return e;
+    if ((e = set_smem_once(gdelta_back_chain_kernel<KD, true>, kBSmemBytes<KD, true>, once_r)) != cudaSuccess) return e;
+    if ((e = set_smem_once(gdelta_grad_kernel<KD, false>, kGSmemBytes<KD>, once_g)) != cudaSuccess) return e;
+    if ((e = set_smem_once(gdelta_grad_kernel<KD, true>, kGSmemBytes<KD>, once_g32)) != cudaSuccess) return e;
+    const unsigned heads = (unsigned)(a.s.B * a.s.H), chunks = heads * (unsigned)((a.s.T + kC - 1) / kC);
+    if ((e = launch_gdelta_prep_backward(m.q, m.k, prep, stream)) != cudaSuccess) return e;
+    gdelta_back_chain_kernel<KD, false><<<heads, kThreads, kBSmemBytes<KD, false>, stream>>>(m.q, m.k, m.v, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    gdelta_back_chain_kernel<KD, true><<<heads, kThreads, kBSmemBytes<KD, true>, stream>>>(m.q, m.k, m.dy, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (a.s.Hk < a.s.H) gdelta_grad_kernel<KD, true><<<chunks, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a);
+    else gdelta_grad_kernel<KD, false><<<chunks, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gdelta_tc_backward_bytes(const GdeltaShape &s) { return back_space(s).bytes; }
+
+cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, cudaStream_t stream)
+{
+    const BackSpace p = back_space(s);
+    uint8_t *ws = reinterpret_cast<uint8_t *>(g.ws);
+    GdeltaTcArgs prep;
+    prep.s = s;
+    prep.ws = ws + p.ws;
+    GdeltaTcBackArgs a;
+    a.s = s;
+    a.S0 = g.S0, a.dS_T = g.dS_T, a.dS0 = g.dS0;
+    a.dv_out = static_cast<uint16_t *>(g.dv_out);
+    a.dalpha = g.dalpha, a.dbeta = g.dbeta;
+    a.scale = g.scale;
+    a.ws = ws + p.ws, a.E = ws + p.E, a.N = ws + p.N, a.S = ws + p.S, a.dS = ws + p.dS;
+    a.anchor = reinterpret_cast<float *>(ws + p.anchor);
+    const bool shared = s.Hk < s.H;
+    a.dq = shared ? ws + p.dq : g.dq;
+    a.dk = shared ? ws + p.dk : g.dk;
+    const cudaError_t e = s.r == 64 ? launch_as<64>(m, a, prep, stream) : launch_as<128>(m, a, prep, stream);
+    if (e != cudaSuccess || !shared) return e;
+    return launch_gdelta_group_sum(s, static_cast<const float *>(a.dq), static_cast<const float *>(a.dk), true, g.dq, g.dk, stream);
+}
+
+}  // namespace la

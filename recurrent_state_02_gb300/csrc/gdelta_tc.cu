@@ -21,70 +21,10 @@
 // two BF16 parts (16 bits of mantissa and a sign) wherever it reaches the state -- S, R, X and V' in steps 1 to 3, the product of
 // two such parts' low halves left out -- and is rounded to one where it reaches y only (which is BF16).
 
-#include "gdelta_tc.h"
-#include "tc_common.cuh"
-#include "tc_short.cuh"
-
-#include <cstddef>
+#include "gdelta_tc.cuh"
 
 namespace la {
 namespace {
-
-constexpr uint32_t kHi128 = desc_hi(1024, 2);   // SBO and swizzle of 128-byte rows
-constexpr uint32_t kTile = kC * 128;            // 8 KB: 64 rows of 64 BF16
-// workspace per chunk and head: A, then X's high and low parts (BF16 shared-memory images), then the gates
-constexpr uint32_t kWsA = 0, kWsX = kTile, kWsGates = 3 * kTile, kGateBytes = 3 * kC * 4, kWsChunk = kWsGates + 1024;
-
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p)
-{
-    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-}
-
-__device__ __forceinline__ uint4 pack8(const float *f)
-{
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
-
-// 2^x, relative error about 2^-22; 0 below 2^-126
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// x0, x1 as a high and a low BF16 part each
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
-{
-    hi = pack_bf16x2(x0, x1);
-    lo = pack_bf16x2(x0 - bf16_lo(hi), x1 - bf16_hi(hi));
-}
-
-// The sequence and the chunks of a CTA.
-struct Span {
-    int T;            // tokens of the sequence
-    size_t tok0;      // packed: its first token
-    size_t slot;      // its first chunk in the workspace (times H heads)
-    bool valid;
-};
-
-// Packed sequences: slot_base[b] numbers the chunks of all sequences in order; -1 for one whose bounds are invalid.
-__device__ __forceinline__ Span span_of(const GdeltaTcArgs &a, int b)
-{
-    Span s;
-    if (!a.s.cu_seqlens) {
-        s.T = a.s.T, s.tok0 = 0, s.valid = true;
-        s.slot = (size_t)b * ((a.s.T + kC - 1) / kC);
-        return s;
-    }
-    const int base = a.slot_base[b];
-    s.valid = base >= 0;
-    s.tok0 = s.valid ? a.s.cu_seqlens[b] : 0;
-    s.T = s.valid ? a.s.cu_seqlens[b + 1] - (int)s.tok0 : 0;
-    s.slot = s.valid ? base : 0;
-    return s;
-}
 
 // ------------------------------------------------------------------- the plan
 // Packed sequences, one CTA: checks the bounds, numbers the chunks (slot_base[b], slot_base[B] = their count)
@@ -173,7 +113,10 @@ __device__ __forceinline__ void put_x(uint8_t *base, int row, int col, float x)
     *reinterpret_cast<uint16_t *>(base + kPXl + o) = (uint16_t)pack_bf16x2(x - bf16_lo(h), 0.f);
 }
 
-template <int KD>
+// BACK: for the gradients, which take A in two parts and betas of at least 2^-40 (dbeta is formed by dividing by them; the
+// change is far below FP32's rounding).
+constexpr float kLeastBeta = 9.094947017729282e-13f;
+template <int KD, bool BACK>
 __global__ void __launch_bounds__(kPThreads, 5)
 gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const GdeltaTcArgs args)
 {
@@ -247,7 +190,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tmem_alloc(&sm->tmem_base, 64);
         tmem_relinquish();
     }
-    uint8_t *wsc = args.ws + ((size_t)slot * s.H + h) * kWsChunk;
+    uint8_t *wsc = args.ws + ((size_t)slot * s.H + h) * (BACK ? kWsChunkB : kWsChunk);
     if (warp == 0) {
         // G in 64 bits, kept as two FP32 parts: differences over a few tokens stay exact to FP32 behind gates near 0.
         // A gate of 0 counts as 2^-400, which every exponential takes to 0.
@@ -260,6 +203,14 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const bool in = i0 + e < nt;
             al[e] = in && s.alpha ? s.alpha[at] : 1.f;
             be[e] = in ? (s.beta ? s.beta[at] : 1.f) : 0.f;
+            if (BACK) {
+                float ratio = 1.f;
+                if (in && fabsf(be[e]) < kLeastBeta) {
+                    const float least = copysignf(kLeastBeta, be[e]);
+                    ratio = be[e] / least, be[e] = least;
+                }
+                reinterpret_cast<float *>(wsc + kWsGates + kGateRatio)[i0 + e] = ratio;
+            }
         }
         const double l0 = al[0] > 0.f ? (double)log2f(al[0]) : -400.0, l1 = al[1] > 0.f ? (double)log2f(al[1]) : -400.0;
         double inc = l0 + l1;
@@ -278,6 +229,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             g[i0 + e] = ex2((float)G);
             g[kC + i0 + e] = ex2((float)(total - G));
             g[2 * kC + i0 + e] = be[e];
+            if (BACK) reinterpret_cast<float2 *>(g + 3 * kC)[i0 + e] = make_float2(hi, (float)(G - hi));
         }
     }
     tc_fence_before();
@@ -327,7 +279,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     Lt[j * LD + ri] = j < end ? x : 0.f;
                 }
             } else {
-                uint8_t *arow = wsc + kWsA + (size_t)ri * 128;
+                uint8_t *arow = wsc + kWsA + (size_t)ri * 128, *lrow = wsc + kWsAl + (size_t)ri * 128;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     float a[8];
@@ -342,6 +294,11 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         }
                     }
                     *reinterpret_cast<uint4 *>(arow + ((x ^ (ri & 7)) << 4)) = pack8(a);
+                    if (BACK) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) a[e] -= bf16_lo(pack_bf16x2(a[e], 0.f));
+                        *reinterpret_cast<uint4 *>(lrow + ((x ^ (ri & 7)) << 4)) = pack8(a);
+                    }
                 }
             }
         }
@@ -486,56 +443,6 @@ struct alignas(16) MSmall {
 template <int KD>
 constexpr uint32_t kMSmemBytes = ChainCfg<KD>::kSmall + sizeof(MSmall) + 1024;
 static_assert(kMSmemBytes<128> <= 232448, "shared memory budget");
-
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts_u16(uint32_t a, uint32_t x)
-{
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)x) : "memory");
-}
-// 8 columns of 32 lanes
-__device__ __forceinline__ void tm_ld8(uint32_t a, float (&v)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                 : "r"(a));
-}
-__device__ __forceinline__ void tm_st8(uint32_t a, const uint32_t (&w)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-// x as a high and a low BF16 part
-__device__ __forceinline__ void split(float2 x, uint32_t &hi, uint32_t &lo)
-{
-    hi = pack_bf16x2(x.x, x.y);
-    const float2 r = __ffma2_rn(make_float2(bf16_lo(hi), bf16_hi(hi)), make_float2(-1.f, -1.f), x);
-    lo = pack_bf16x2(r.x, r.y);
-}
-__device__ __forceinline__ float4 lds_f4(uint32_t a)
-{
-    const uint4 v = lds4(a);
-    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-}
-// One lane of a converged warp, in a form that keeps what it guards warp-uniform (an MMA's operands then stay in uniform
-// registers: 20 cycles to issue one, 45 behind a test of the lane).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
 
 template <int KD>
 __global__ void __launch_bounds__(kMThreads, 1)
@@ -927,24 +834,37 @@ size_t gdelta_tc_workspace_bytes(int B, int H, int T, bool packed)
     return (packed ? gdelta_tc_plan_bytes(B) : 0) + (size_t)gdelta_tc_slots(B, T, packed) * H * kWsChunk;
 }
 
+template <int KD, bool BACK>
+static cudaError_t launch_prep(const CUtensorMap &q, const CUtensorMap &k, const GdeltaTcArgs &a, cudaStream_t stream)
+{
+    static OncePerDevice once;
+    const cudaError_t e = set_smem_once(gdelta_prep_kernel<KD, BACK>, kPSmemBytes, once);
+    if (e != cudaSuccess) return e;
+    const long long n = gdelta_tc_slots(a.s.B, a.s.T, a.s.cu_seqlens != nullptr) * a.s.H;
+    if (n > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (n > 0) gdelta_prep_kernel<KD, BACK><<<(unsigned)n, kPThreads, kPSmemBytes, stream>>>(q, k, a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gdelta_prep_backward(const CUtensorMap &q, const CUtensorMap &k, const GdeltaTcArgs &a, cudaStream_t stream)
+{
+    return a.s.r == 64 ? launch_prep<64, true>(q, k, a, stream) : launch_prep<128, true>(q, k, a, stream);
+}
+
 template <int KD>
 static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream)
 {
-    static OncePerDevice once_p, once_m;
-    cudaError_t e = set_smem_once(gdelta_prep_kernel<KD>, kPSmemBytes, once_p);
-    if (e != cudaSuccess) return e;
-    e = set_smem_once(gdelta_chain_kernel<KD>, kMSmemBytes<KD>, once_m);
+    static OncePerDevice once_m;
+    cudaError_t e = set_smem_once(gdelta_chain_kernel<KD>, kMSmemBytes<KD>, once_m);
     if (e != cudaSuccess) return e;
     const GdeltaShape &s = a.s;
-    const long long nprep = gdelta_tc_slots(s.B, s.T, s.cu_seqlens != nullptr) * s.H,
-                    nmain = (long long)s.B * s.H * ((s.dv + 127) / 128);
-    if (nprep > 0x7fffffffLL || nmain > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const long long nmain = (long long)s.B * s.H * ((s.dv + 127) / 128);
+    if (nmain > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (s.cu_seqlens) {
         gdelta_plan_kernel<<<1, kPlanThreads, 0, stream>>>(s.cu_seqlens, s.B, s.T, a.slot_base, a.order, s.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if (nprep > 0) gdelta_prep_kernel<KD><<<(unsigned)nprep, kPThreads, kPSmemBytes, stream>>>(m.q, m.k, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_prep<KD, false>(m.q, m.k, a, stream)) != cudaSuccess) return e;
     gdelta_chain_kernel<KD><<<(unsigned)nmain, kMThreads, kMSmemBytes<KD>, stream>>>(m.q, m.k, m.v, a);
     return cudaGetLastError();
 }

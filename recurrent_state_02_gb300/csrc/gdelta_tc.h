@@ -29,4 +29,23 @@ size_t gdelta_tc_workspace_bytes(int B, int H, int T, bool packed);
 
 cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream);
 
+// The gradients (gdelta_bwd.cu): [B,H,T,d], r 64 or 128, dv 64 or 128, token arrays 16-byte aligned, the workspace 256-byte.
+struct GdeltaTcBackMaps {
+    CUtensorMap q, k, v, dy;
+};
+struct GdeltaTcBackArgs {
+    GdeltaShape s;
+    const float *S0 = nullptr, *dS_T = nullptr;
+    float *dS0 = nullptr, *dalpha = nullptr, *dbeta = nullptr;
+    uint16_t *dv_out = nullptr;
+    void *dq = nullptr, *dk = nullptr;      // BF16 [B,H,T,r], or FP32 where key heads are shared
+    float scale = 1.f;
+    // per chunk and head: prep's images and gates; E, N (two parts) and dS's high part by [value column]; per head one S more
+    uint8_t *ws = nullptr, *E = nullptr, *N = nullptr, *S = nullptr, *dS = nullptr;
+    float *anchor = nullptr;                // <S, dS> at every chunk's end
+};
+size_t gdelta_tc_backward_bytes(const GdeltaShape &s);
+cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, cudaStream_t stream);
+cudaError_t launch_gdelta_prep_backward(const CUtensorMap &q, const CUtensorMap &k, const GdeltaTcArgs &a, cudaStream_t stream);
+
 }  // namespace la
