@@ -11,10 +11,10 @@
 //     dQ = dP K + scale e^G dY S^T
 //     dK = dP^T Q + dL K + dL^T K - e^G N S^T + beta e^{G_C - G} E dS^T
 //     dbeta_j = Z_jj / beta_j                                                       (N_j is beta_j times its error's gradient)
-//     dlog alpha_t = <S_next, dS> + sum_{s >= t, in the chunk} (q_s . (scale e^G dY S^T)_s + sum_j A_sj dA_sj - v_s . N_s)
-// (the gates' gradient is anchored at every chunk's end, so that nothing is summed over the sequence).
-// Kernels: gdelta_prep (A, X, gates), the forward chain again, keeping S before and E of every chunk, the backward chain,
-// keeping dS behind and N, and a kernel over all chunks.
+//     dlog alpha_t = <S, dS_before> - sum_{s < t, in the chunk} (q_s . (scale e^G dY S^T)_s + sum_j A_sj dA_sj - v_s . N_s)
+// (the gates' gradient is anchored before every chunk, so that nothing is summed over the sequence).
+// Kernels: gdelta_prep (A, X, gates), the forward chain again, keeping the states between the chunks and E, the backward chain,
+// keeping their gradients and N, and a kernel over all chunks.
 // Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand; what reaches dq and
 // dk only, the high one.
 
@@ -43,11 +43,9 @@ struct BackCfg {
     // a stage (two): K, V or dY (two blocks of 64 columns), X's parts; backwards also Q and A's parts
     static constexpr uint32_t kSK = 0, kSV = kTK, kSX = kSV + 2 * kTile, kSQ = kSX + 2 * kTile, kSA = kSQ + kTK,
                               kStage = REV ? kSA + 2 * kTile : kSQ;
-    // what goes to memory: S (two parts), then E; backwards dS and N share the space, and dv has its own
-    static constexpr uint32_t kOutS = 2 * kStage, kOutE = REV ? kOutS : kOutS + 2 * kStateImg<KD>, kOutV = kOutE + kTokImg,
-                              kGates = REV ? kOutV + 2 * kTile : kOutV, kSmall = kGates + kGateRing * kGateStep;
+    // dv of a chunk (two blocks of 64 columns)
+    static constexpr uint32_t kOutV = 2 * kStage, kGates = kOutV + (REV ? 2 * kTile : 0), kSmall = kGates + kGateRing * kGateStep;
 };
-static_assert(kStateImg<128> <= kTokImg, "dS's high part fits where N is staged");
 // TMEM columns: S^T (two parts), P^T and E^T (then dS^T), (A^T dY)^T, the scaled dY^T (two parts), R^T (two parts, then the decayed
 // V'^T's, or the scaled N^T's), V^T
 constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcA = 256, kcY = 320, kcR = 384, kcV = 448;
@@ -61,7 +59,6 @@ struct alignas(16) BSmall {
     uint64_t fin;
     uint32_t tmem_base;
     int abort_flag;
-    float part[kHelpers];
 };
 #define BBAR(name, i) (sS + (uint32_t)offsetof(BSmall, name) + 8 * (uint32_t)(i))
 
@@ -254,9 +251,9 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         const bool live = d < dv;
         const float scale = args.scale;
         bool ok = true;
-        // (a helper that gave up waiting still meets the others at their barriers)
+        // (a helper that gave up waiting still meets the others at their barriers; one iteration more for the last state)
 #pragma unroll 1
-        for (int n = 0; n < nch + (REV ? 0 : 1); ++n) {
+        for (int n = 0; n <= nch; ++n) {
             const int c = chunk(n);
             const uint32_t st = s0 + (n & 1) * Cfg::kStage, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
             // V's column, or the scaled dY's (0 past the sequence's end, where TMA fills up)
@@ -276,113 +273,79 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                         const uint32_t x0 = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
                                        x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
                         v[i] = live ? x0 | x1 << 16 : 0;
-                        if (REV) {
-                            const float2 w = unpack(v[i]);
-                            split(make_float2(scale * ldsf(gates + 64 * x + 4 * t) * w.x, scale * ldsf(gates + 64 * x + 4 * t + 4) * w.y),
-                                  v[i], lo[i]);
+                    }
+                    if (REV) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 g = lds_f4(gates + 64 * x + 16 * i);
+                            split(__fmul2_rn(make_float2(scale * g.x, scale * g.y), unpack(v[2 * i])), v[2 * i], lo[2 * i]);
+                            split(__fmul2_rn(make_float2(scale * g.z, scale * g.w), unpack(v[2 * i + 1])), v[2 * i + 1], lo[2 * i + 1]);
                         }
+                        tm_st8(tq + kcY + 32 + 8 * x, lo);
                     }
                     tm_st8(tq + (REV ? kcY : kcV) + 8 * x, v);
-                    if (REV) tm_st8(tq + kcY + 32 + 8 * x, lo);
                 }
                 tc_wait_st();
                 tc_fence_before();
                 bar_arrive_warp(BBAR(got_v, 0));
             }
-            // the state before the chunk (backwards: behind it)
-            if (ht == 0) tma_store_wait_read<0>();
-            named_barrier_sync(1, 32 * kHelpers);
+            // the state before the chunk; backwards its gradient behind it
             if (ok) ok = waitw(BBAR(got_s, 0), n & 1) && waitw(BBAR(got_s, 1), n & 1);
             if (ok) {
                 tc_fence_after();
-                float2 dot = make_float2(0.f, 0.f);
-                const uint8_t *next = args.S + (bh * (nch + 1) + c + 1) * (2 * kStateImg<KD>);   // (backwards: the state there)
+                uint8_t *img = (REV ? args.dS : args.S) + (bh * (nch + 1) + (REV ? c + 1 : c)) * (2 * kStateImg<KD>);
 #pragma unroll 1
                 for (int x = 0; x < KD / 16; ++x) {
                     float hi[8], lo[8];
                     tm_ld8(tq + kcS + 8 * x, hi);
                     tm_ld8(tq + kcS + KH + 8 * x, lo);
-                    const uint32_t o = (x >> 2) * kImg + sw128_offset(d, 2 * (x & 3)), o2 = (x >> 2) * kImg + sw128_offset(d, 2 * (x & 3) + 1);
-                    uint4 s4[4];
-                    if (REV && live) {
-                        s4[0] = *reinterpret_cast<const uint4 *>(next + o);
-                        s4[1] = *reinterpret_cast<const uint4 *>(next + o2);
-                        s4[2] = *reinterpret_cast<const uint4 *>(next + kStateImg<KD> + o);
-                        s4[3] = *reinterpret_cast<const uint4 *>(next + kStateImg<KD> + o2);
-                    }
                     wait_loaded(hi);
                     wait_loaded(lo);
                     uint32_t hw[8], lw[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) hw[i] = __float_as_uint(hi[i]), lw[i] = __float_as_uint(lo[i]);
-                    sts4(s0 + Cfg::kOutS + o, hw[0], hw[1], hw[2], hw[3]);
-                    sts4(s0 + Cfg::kOutS + o2, hw[4], hw[5], hw[6], hw[7]);
-                    if (!REV) {
-                        sts4(s0 + Cfg::kOutS + kStateImg<KD> + o, lw[0], lw[1], lw[2], lw[3]);
-                        sts4(s0 + Cfg::kOutS + kStateImg<KD> + o2, lw[4], lw[5], lw[6], lw[7]);
-                    } else if (live) {
-                        const uint32_t sh[8] = {s4[0].x, s4[0].y, s4[0].z, s4[0].w, s4[1].x, s4[1].y, s4[1].z, s4[1].w},
-                                       sl[8] = {s4[2].x, s4[2].y, s4[2].z, s4[2].w, s4[3].x, s4[3].y, s4[3].z, s4[3].w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dot = __ffma2_rn(__fadd2_rn(unpack(hw[i]), unpack(lw[i])), __fadd2_rn(unpack(sh[i]), unpack(sl[i])), dot);
-                    }
+                    st_row16(img + (x >> 2) * kImg, d, x & 3, hw);
+                    st_row16(img + kStateImg<KD> + (x >> 2) * kImg, d, x & 3, lw);
                 }
                 tc_fence_before();
                 bar_arrive_warp(BBAR(s_read, 0));
-                if (REV) {
-                    float p = dot.x + dot.y;
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-                    if (lane == 0) sm->part[q4] = p;
-                }
             }
-            if (REV) {
-                fence_proxy_async_smem();
-                named_barrier_sync(1, 32 * kHelpers);
-                if (ht == 0) {
-                    if (ok) {
-                        bulk_store(args.dS + (bh * nch + c) * kStateImg<KD>, s0 + Cfg::kOutS, kStateImg<KD>);
-                        args.anchor[bh * nch + c] = (sm->part[0] + sm->part[1]) + (sm->part[2] + sm->part[3]);
-                    }
-                    tma_store_commit();
-                    tma_store_wait_read<0>();
-                }
-                named_barrier_sync(1, 32 * kHelpers);
-            }
+            if (n == nch) break;
             // E, or N
-            if (ok && n < nch) ok = waitw(BBAR(done2, 0), n & 1) && waitw(BBAR(done2, 1), n & 1);
-            if (ok && n < nch) {
+            if (ok) ok = waitw(BBAR(done2, 0), n & 1) && waitw(BBAR(done2, 1), n & 1);
+            if (ok) {
                 tc_fence_after();
+                uint8_t *img = (REV ? args.N : args.E) + (bh * nch + c) * kTokImg;
 #pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    float e[8];
-                    tm_ld8(tq + kcE + 8 * x, e);
+                for (int x = 0; x < 4; ++x) {
+                    float e[16];
+                    tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
                     wait_loaded(e);
-                    uint32_t hi[4], lo[4];
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
-                    const uint32_t o = s0 + Cfg::kOutE + sw128_offset(d, x);
-                    sts4(o, hi[0], hi[1], hi[2], hi[3]);
-                    sts4(o + kImg, lo[0], lo[1], lo[2], lo[3]);
+                    for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
+                    st_row16(img, d, x, hi);
+                    st_row16(img + kImg, d, x, lo);
                     if (REV) {
-                        const uint32_t a = s0 + Cfg::kOutV + col + x * (8 * 128);
+                        const uint32_t a = s0 + Cfg::kOutV + col + x * (16 * 128);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            sts_u16(a + i * 128 + ((c16 ^ i) << 4), pack_bf16x2(e[i] * ldsf(gates + kGateRatio + 32 * x + 4 * i), 0.f));
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 g = lds_f4(gates + kGateRatio + 64 * x + 16 * i);
+                            const float f[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int t = 4 * i + u;
+                                sts_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4), pack_bf16x2(e[t] * f[u], 0.f));
+                            }
+                        }
                     }
                 }
                 tc_fence_before();
                 bar_arrive_warp(BBAR(e_read, 0));
             }
-            fence_proxy_async_smem();
+            if (!REV) continue;
             named_barrier_sync(1, 32 * kHelpers);
-            if (ht == 0) {
-                if (ok && !REV) bulk_store(args.S + (bh * (nch + 1) + c) * (2 * kStateImg<KD>), s0 + Cfg::kOutS, 2 * kStateImg<KD>);
-                if (ok && n < nch) bulk_store((REV ? args.N : args.E) + (bh * nch + c) * kTokImg, s0 + Cfg::kOutE, kTokImg);
-                tma_store_commit();
-            }
-            if (REV && ok) {
+            if (ok) {
                 const int per = dv / 8, rows = min(kC, T - c * kC);
                 uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC) * dv;
 #pragma unroll 1
@@ -391,8 +354,8 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                     *reinterpret_cast<uint4 *>(y0 + (size_t)t * dv + 8 * w) = lds4(s0 + Cfg::kOutV + (w >> 3) * kTile + sw128_offset(t, w & 7));
                 }
             }
+            named_barrier_sync(1, 32 * kHelpers);
         }
-        if (ht == 0) tma_store_wait_all<0>();
         tc_fence_before();
     } else {
         regs_inc<kRegsOwn>();
@@ -487,7 +450,6 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             ok = waitw(BBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1) && waitw(BBAR(s_read, 0), ph);
             if (!ok) break;
             tc_fence_after();
-            const bool more = !REV || n + 1 < nch;
 #pragma unroll
             for (int x = 0; x < KH / 16; ++x) {
                 float ds[16];
@@ -496,9 +458,9 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
-                if (more) put_s(x, S + 8 * x);
+                put_s(x, S + 8 * x);
             }
-            if (more) stored(BBAR(got_s, ch));
+            stored(BBAR(got_s, ch));
         }
         if (REV && ok && live) {
 #pragma unroll
@@ -538,7 +500,7 @@ struct alignas(16) GSmall {
     uint64_t fin;
     uint32_t tmem_base;
     int abort_flag;
-    float dG[2][kC], diag[kC];
+    float dG[2][kC], diag[kC], anchor[kGComp];
 };
 #define GBAR(name, i) (sS + (uint32_t)offsetof(GSmall, name) + 8 * (uint32_t)(i))
 template <int KD>
@@ -604,7 +566,7 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 bar_expect(GBAR(full, 2), kStateImg<KD>);
 #pragma unroll 1
                 for (int x = 0; x < KD / 64; ++x)
-                    bulk_copy(s0 + (x ? Cfg::kN : Cfg::kE) + kImg, args.dS + (bh * nch + c) * kStateImg<KD> + x * kImg, kImg, GBAR(full, 2));
+                    bulk_copy(s0 + (x ? Cfg::kN : Cfg::kE) + kImg, args.dS + (bh * (nch + 1) + c + 1) * (2 * kStateImg<KD>) + x * kImg, kImg, GBAR(full, 2));
             }
             // what was started lands before the CTA exits
             wait1(GBAR(full, 0), 0);
@@ -727,6 +689,26 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             tc_fence_before();
             bar_arrive_warp(GBAR(got_p, 0));
         }
+        ok = ok && waitw(GBAR(full, 1), 0);
+        if (ok) {
+            // <S, dS> before the chunk: both are images of the same layout, so any order does
+            const uint4 *ds = reinterpret_cast<const uint4 *>(args.dS + (bh * (nch + 1) + c) * (2 * kStateImg<KD>));
+            constexpr int kWords = kStateImg<KD> / 16, kRow = KD / 64 * 8;    // (rows behind dv hold nothing)
+            float2 dot = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int y = tid; y < dv * kRow; y += 32 * kGComp) {
+                const int w = y / (dv * 8) * (kImg / 16) + y % (dv * 8);
+                const uint4 dh = ds[w], dl = ds[w + kWords], sh = lds4(s0 + Cfg::kS + 16 * w), sl = lds4(s0 + Cfg::kS + kStateImg<KD> + 16 * w);
+                dot = __ffma2_rn(__fadd2_rn(unpack(dh.x), unpack(dl.x)), __fadd2_rn(unpack(sh.x), unpack(sl.x)), dot);
+                dot = __ffma2_rn(__fadd2_rn(unpack(dh.y), unpack(dl.y)), __fadd2_rn(unpack(sh.y), unpack(sl.y)), dot);
+                dot = __ffma2_rn(__fadd2_rn(unpack(dh.z), unpack(dl.z)), __fadd2_rn(unpack(sh.z), unpack(sl.z)), dot);
+                dot = __ffma2_rn(__fadd2_rn(unpack(dh.w), unpack(dl.w)), __fadd2_rn(unpack(sh.w), unpack(sl.w)), dot);
+            }
+            float p = dot.x + dot.y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+            if (lane == 0) sm->anchor[warp] = p;
+        }
         ok = ok && waitw(GBAR(doneS, 0), 0);
         if (ok) {
             tc_fence_after();
@@ -758,16 +740,17 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         named_barrier_sync(1, 32 * kGComp);
         const int t0 = c * kC;
         if (ok && warp == 0) {
-            // dlog alpha: the chunk's terms from each token on, and the anchor at its end
+            // dlog alpha: <S, dS> before the chunk, less the terms of the tokens before each one
             const int a0 = 2 * lane;
             const float d0 = sm->dG[0][a0] + sm->dG[1][a0], d1 = sm->dG[0][a0 + 1] + sm->dG[1][a0 + 1];
-            float inc = d0 + d1;         // from this lane on
+            float inc = d0 + d1;         // up to this lane
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_down_sync(0xffffffffu, inc, o);
-                if (lane + o < 32) inc += y;
+                const float y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
             }
-            const float anchor = args.anchor[bh * nch + c];
+            float anchor = 0.f;
+            for (int w = 0; w < kGComp; ++w) anchor += sm->anchor[w];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = t0 + a0 + u;
@@ -775,7 +758,7 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const size_t at = bh * T + t;
                 if (args.dalpha && args.s.alpha) {
                     const float al = args.s.alpha[at];
-                    args.dalpha[at] = al > 0.f ? (anchor + (u ? inc - d0 : inc)) / al : 0.f;
+                    args.dalpha[at] = al > 0.f ? (anchor - (u ? inc - d1 : inc - d0 - d1)) / al : 0.f;
                 }
                 if (args.dbeta) args.dbeta[at] = sm->diag[a0 + u] / ldsf(gates + 8 * kC + 4 * (a0 + u));
             }
@@ -835,7 +818,7 @@ size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // The workspace's parts, in order.
 struct BackSpace {
-    size_t ws, E, N, S, dS, anchor, dq, dk, bytes;
+    size_t ws, E, N, S, dS, dq, dk, bytes;
 };
 BackSpace back_space(const GdeltaShape &s)
 {
@@ -846,8 +829,7 @@ BackSpace back_space(const GdeltaShape &s)
     p.N = p.E + heads * nch * kTokImg;
     p.S = p.N + heads * nch * kTokImg;
     p.dS = p.S + heads * (nch + 1) * 2 * state;
-    p.anchor = p.dS + heads * nch * state;
-    p.dq = p.anchor + round_up(heads * nch * sizeof(float));
+    p.dq = p.dS + heads * (nch + 1) * 2 * state;
     const size_t part = s.Hk < s.H ? round_up(heads * s.T * s.r * sizeof(float)) : 0;
     p.dk = p.dq + part;
     p.bytes = p.dk + part;
@@ -892,7 +874,6 @@ cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaSha
     a.dalpha = g.dalpha, a.dbeta = g.dbeta;
     a.scale = g.scale;
     a.ws = ws + p.ws, a.E = ws + p.E, a.N = ws + p.N, a.S = ws + p.S, a.dS = ws + p.dS;
-    a.anchor = reinterpret_cast<float *>(ws + p.anchor);
     const bool shared = s.Hk < s.H;
     a.dq = shared ? ws + p.dq : g.dq;
     a.dk = shared ? ws + p.dk : g.dk;

@@ -122,9 +122,16 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes)
+// 16 BF16 values (8 words) of one row of a tile in memory with 128-byte rows and the 128-byte swizzle: 16-byte words 2 x and
+// 2 x + 1 of the row, which the swizzle leaves side by side (exchanged in odd rows): one 32-byte store.
+__device__ __forceinline__ void st_row16(uint8_t *tile, int row, int x, const uint32_t (&w)[8])
 {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+    const bool odd = row & 1;
+    uint8_t *p = tile + row * 128 + ((x ^ ((row & 7) >> 1)) << 5);
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(p), "r"(odd ? w[4] : w[0]), "r"(odd ? w[5] : w[1]), "r"(odd ? w[6] : w[2]), "r"(odd ? w[7] : w[3]),
+                   "r"(odd ? w[0] : w[4]), "r"(odd ? w[1] : w[5]), "r"(odd ? w[2] : w[6]), "r"(odd ? w[3] : w[7])
+                 : "memory");
 }
 
 }  // namespace

@@ -40,9 +40,9 @@ struct GdeltaTcBackArgs {
     uint16_t *dv_out = nullptr;
     void *dq = nullptr, *dk = nullptr;      // BF16 [B,H,T,r], or FP32 where key heads are shared
     float scale = 1.f;
-    // per chunk and head: prep's images and gates; E, N (two parts) and dS's high part by [value column]; per head one S more
+    // per chunk and head: prep's images and gates; E and N (two parts) by [value column]; the states between the chunks
+    // and their gradients (two parts), one more per head
     uint8_t *ws = nullptr, *E = nullptr, *N = nullptr, *S = nullptr, *dS = nullptr;
-    float *anchor = nullptr;                // <S, dS> at every chunk's end
 };
 size_t gdelta_tc_backward_bytes(const GdeltaShape &s);
 cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, cudaStream_t stream);
