@@ -140,7 +140,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             auto mma_a = [&](int n) {
                 const uint32_t st = s0 + (n & 1) * Cfg::kStage;
                 const uint32_t ylo = desc_lo(st + Cfg::kSV, kTile), alo = desc_lo(st + Cfg::kSA, kTile);
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t o = (i & 3) * (2048 >> 4);
                     mma_ss(kcA, ylo + o, kHi128, alo + (i >> 2) * (kTile >> 4) + o, kHi128, idA, i > 0);
@@ -158,7 +158,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 // 1  P^T = S^T K^T
                 if (!wait1(BBAR(full, n & 1), (n >> 1) & 1) || !wait1(BBAR(got_s, 0), ph)) break;
                 tc_fence_after();
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = 0; i < KD / 16; ++i) {
                     const int kk = i >> 1;
                     mma_ts(kcP, kcS + (i & 1) * KH + kk * 8, klo + kk * 2, kHi128, id64, i > 0);
@@ -169,7 +169,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 for (int u = 0; u < 2; ++u) {
                     const int t = REV ? 1 - u : u;
                     const uint32_t k2 = klo + t * kHalfRows + ((KD == 128 ? kTile : 64u) >> 4);
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; i < KD / 16; ++i) {
                         const int kk = i >> 1;
                         mma_ts(kcP + 32 * t, kcS + (i & 1) * KH + KD / 4 + kk * 8, k2 + kk * 2, kHi128, idP, true);
@@ -191,7 +191,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                         // X's rows are the result's tokens forwards, its columns backwards
                         const uint32_t xo = xlo + (REV ? t * kHalfRows + 4 * o : o * kHalfRows + 4 * t);
                         constexpr uint32_t kStep = REV ? 2048 >> 4 : 2;
-#pragma unroll 1
+#pragma unroll
                         for (int kk = 0; kk < 2; ++kk) {
                             mma_ts(d, r + kk * 8, xo + kk * kStep, kHi128, id32, u + kk > 0);
                             mma_ts(d, r + 32 + kk * 8, xo + kk * kStep, kHi128, id32, true);
@@ -207,7 +207,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 if (REV) {
                     if (!wait1(BBAR(got_v, 0), ph)) break;
                     tc_fence_after();
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; i < 8; ++i)
                         mma_ts(kcP, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
                 }
@@ -221,14 +221,14 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                         if (!ok) break;
                         tc_fence_after();
                         if (REV) {
-#pragma unroll 1
+#pragma unroll 4
                             for (int i = 0; i < 8; ++i)
-                                mma_ts(kcP + KH, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + half + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
+                                mma_ts(kcP + 64, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + half + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
                         }
                     }
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; i < 8; ++i)
-                        mma_ts(kcP + KH * t, kcR + (i >> 2) * 32 + (i & 3) * 8, kmn + half + (i & 3) * (2048 >> 4), kHi128, idS, REV || i > 0);
+                        mma_ts(kcP + 64 * t, kcR + (i >> 2) * 32 + (i & 3) * 8, kmn + half + (i & 3) * (2048 >> 4), kHi128, idS, REV || i > 0);
                     bar_commit(BBAR(done3, 2 * t + (n & 1)));
                 }
                 if (!ok) break;
@@ -316,11 +316,17 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             if (ok) {
                 tc_fence_after();
                 uint8_t *img = (REV ? args.N : args.E) + (bh * nch + c) * kTokImg;
-#pragma unroll 1
+                // (all of it at once: the issuer waits for its columns)
+                float e4[4][16];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tc_ld_32x32b_x16(tq + kcE + 16 * x, e4[x]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) wait_loaded(e4[x]);
+                tc_fence_before();
+                bar_arrive_warp(BBAR(e_read, 0));
+#pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    float e[16];
-                    tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
-                    wait_loaded(e);
+                    const float (&e)[16] = e4[x];
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
@@ -340,8 +346,6 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                         }
                     }
                 }
-                tc_fence_before();
-                bar_arrive_warp(BBAR(e_read, 0));
             }
             if (!REV) continue;
             named_barrier_sync(1, 32 * kHelpers);
@@ -404,18 +408,21 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 wait_loaded(v);
                 uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 pp = make_float2(p[2 * i], p[2 * i + 1]);
-                    float2 r;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p0 = make_float2(p[4 * i], p[4 * i + 1]), p1 = make_float2(p[4 * i + 2], p[4 * i + 3]);
+                    float2 r0, r1;
                     if constexpr (REV) {
-                        const float2 er = make_float2(ldsf(gates + 4 * kC + 64 * x + 8 * i), ldsf(gates + 4 * kC + 64 * x + 8 * i + 4)),
-                                     be = make_float2(ldsf(gates + 8 * kC + 64 * x + 8 * i), ldsf(gates + 8 * kC + 64 * x + 8 * i + 4));
-                        r = __fmul2_rn(be, __ffma2_rn(make_float2(scale, scale), make_float2(v[2 * i], v[2 * i + 1]), __fmul2_rn(er, pp)));
+                        const float4 er = lds_f4(gates + 4 * kC + 64 * x + 16 * i), be = lds_f4(gates + 8 * kC + 64 * x + 16 * i);
+                        const float2 sc = make_float2(scale, scale);
+                        r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(sc, make_float2(v[4 * i], v[4 * i + 1]), __fmul2_rn(make_float2(er.x, er.y), p0)));
+                        r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(sc, make_float2(v[4 * i + 2], v[4 * i + 3]), __fmul2_rn(make_float2(er.z, er.w), p1)));
                     } else {
-                        const float2 g = make_float2(-ldsf(gates + 64 * x + 8 * i), -ldsf(gates + 64 * x + 8 * i + 4));
-                        r = __ffma2_rn(g, pp, unpack(__float_as_uint(v[i])));
+                        const float4 g = lds_f4(gates + 64 * x + 16 * i);
+                        r0 = __ffma2_rn(make_float2(-g.x, -g.y), p0, unpack(__float_as_uint(v[2 * i])));
+                        r1 = __ffma2_rn(make_float2(-g.z, -g.w), p1, unpack(__float_as_uint(v[2 * i + 1])));
                     }
-                    split(r, hi[i], lo[i]);
+                    split(r0, hi[2 * i], lo[2 * i]);
+                    split(r1, hi[2 * i + 1], lo[2 * i + 1]);
                 }
                 tm_st8(tq + kcR + 8 * x, hi);
                 tm_st8(tq + kcR + 32 + 8 * x, lo);
@@ -453,7 +460,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
 #pragma unroll
             for (int x = 0; x < KH / 16; ++x) {
                 float ds[16];
-                tc_ld_32x32b_x16(tq + kcP + KH * ch + 16 * x, ds);
+                tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * x, ds);
                 wait_loaded(ds);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)

@@ -547,7 +547,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 if (tail && n == nch - 1 && !wait1(MBAR(tail, 0), 0)) break;
                 if (!wait1(MBAR(got_s, 0), ph)) break;
                 tc_fence_after();
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = 0; i < KD / 16; ++i) {        // part i % 2, k-step i / 2
                     const int kk = i >> 1;
                     mma_ts(kcP, kcS + (i & 1) * KH + kk * 8, klo + kk * 2, kHi128, id64, i > 0);
@@ -558,7 +558,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 for (int t = 0; t < 2; ++t) {
                     // (the second half of the rows: K's second block, or the second half of its one block's rows)
                     const uint32_t k2 = klo + t * kHalfRows + ((KD == 128 ? kTile : 64u) >> 4);
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; i < KD / 16; ++i) {
                         const int kk = i >> 1;
                         mma_ts(kcP + 32 * t, kcS + (i & 1) * KH + KD / 4 + kk * 8, k2 + kk * 2, kHi128, id32, true);
@@ -577,7 +577,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 #pragma unroll 1
                     for (int o = t; o < 2; ++o) {          // half o of E from half t of R
                         const uint32_t d = kcE + 32 * o, xo = xlo + o * kHalfRows + 4 * t, r = kcR + 16 * t;
-#pragma unroll 1
+#pragma unroll
                         for (int kk = 0; kk < 2; ++kk) {
                             mma_ts(d, r + kk * 8, xo + kk * 2, kHi128, id32, t + kk > 0);
                             mma_ts(d, r + 32 + kk * 8, xo + kk * 2, kHi128, id32, true);
@@ -591,7 +591,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 if (!wait1(MBAR(full_qa, n & 1), fph) || (n > 0 && !wait1(MBAR(y_read, 0), ph ^ 1))) break;
                 tc_fence_after();
                 const uint32_t qlo = desc_lo(st + Cfg::kSQ, 16), alo = desc_lo(st + Cfg::kSA, 16);
-#pragma unroll 1
+#pragma unroll 4
                 for (int kk = 0; kk < KD / 16; ++kk)
                     mma_ts(kcQS, kcS + kk * 8, qlo + (kk >> 2) * (kTile >> 4) + (kk & 3) * 2, kHi128, id64, kk > 0);
                 // 3  dS^T = V'^T K, both parts of the decayed V', one half of the state's rows after the other
@@ -601,15 +601,15 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
                     const uint32_t ko = kmn + t * ((KD == 128 ? kTile : 64u) >> 4);
-#pragma unroll 1
+#pragma unroll 4
                     for (int i = 0; i < 8; ++i) {          // part i / 4, k-step i % 4
                         const int kk = i & 3;
-                        mma_ts(kcP + KH * t, kcR + (i >> 2) * 32 + kk * 8, ko + kk * (2048 >> 4), kHi128, idS, i > 0);
+                        mma_ts(kcP + 64 * t, kcR + (i >> 2) * 32 + kk * 8, ko + kk * (2048 >> 4), kHi128, idS, i > 0);
                     }
                     bar_commit(MBAR(done3, 2 * t + (n & 1)));
                 }
                 // (A V')^T
-#pragma unroll 1
+#pragma unroll 4
                 for (int kk = 0; kk < 4; ++kk) mma_ts(kcAV, kcW + kk * 8, alo + kk * 2, kHi128, id64, kk > 0);
                 bar_commit(MBAR(done4, n & 1));
             }
@@ -792,7 +792,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 #pragma unroll
             for (int x = 0; x < KH / 16; ++x) {
                 float ds[16];
-                tc_ld_32x32b_x16(tq + kcP + KH * ch + 16 * x, ds);
+                tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * x, ds);
                 wait_loaded(ds);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
