@@ -29,13 +29,14 @@ template <int KD>
 constexpr uint32_t kStateImg = KD / 64 * kImg;   // a part of S or dS: [value column][state row] by blocks of 64 rows
 
 // ----------------------------------------------------------------- the chains
-// Roles as in gdelta_chain_kernel; the helpers bring V (backwards: scale e^G dY, in two parts) to its lanes, and take S
-// and E (dS and N) of every chunk to memory.
-constexpr int kOwners = 8, kHelpers = 4, kIssuer = 12, kLoader = 13;
-constexpr int kThreads = 512;
+// Roles as in gdelta_chain_kernel: the third warpgroup brings V (backwards: scale e^G dY, in two parts) to its lanes and takes
+// S (dS) of every chunk to memory, the fourth takes E (N, and dv).
+constexpr int kOwners = 8, kHelpers = 4, kBringer = 8, kTaker = 12, kIssuer = 16, kLoader = 17;
+constexpr int kThreads = 640;
 constexpr int kGateRing = 4;
 constexpr uint32_t kGateStep = 2048;
-constexpr int kRegsOwn = 160, kRegsHelp = 104, kRegsRest = 88;   // 2 x 160 + 104 + 88 = 4 x 128
+// registers per thread after the split (launched with 96): 2 x 136 + 56 + 96 + 56 = 5 x 96
+constexpr int kRegsOwn = 136, kRegsBring = 56, kRegsRest = 56;
 
 template <int KD, bool REV>
 struct BackCfg {
@@ -53,7 +54,7 @@ constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcA = 256, kcY = 320, kcR = 38
 struct alignas(16) BSmall {
     uint64_t full[2];
     uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (4 warps)
-    uint64_t got_v, s_read, e_read;          // V^T (dY^T) is there, S and E have been read (the helpers)
+    uint64_t got_v, s_read, e_read;          // V^T (dY^T) is there, S has been read (the bringers); E has (the takers)
     uint64_t done0, done1[2], done2[2];      // A^T dY, halves of P, E
     uint64_t done3[4];                       // halves of dS of even and odd chunks
     uint64_t fin;
@@ -102,7 +103,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
     __syncthreads();
     tc_fence_after();
 
-    if (warp >= kOwners + kHelpers) {
+    if (warp >= kIssuer) {
         regs_dec<kRegsRest>();
         if (warp == kLoader && elect_one()) {
             const int hk = h / (H / args.s.Hk), kh = b * args.s.Hk + hk;
@@ -243,75 +244,17 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             wait1(BBAR(fin, 0), 0);
         }
         __syncwarp();
-    } else if (warp >= kOwners) {
-        regs_dec<kRegsHelp>();
-        const int q4 = warp & 3, d = 32 * q4 + lane, ht = tid - 32 * kOwners;
+    } else if (warp >= kTaker) {
+        const int q4 = warp & 3, d = 32 * q4 + lane, ht = tid - 32 * kTaker;
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
         const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
-        const bool live = d < dv;
-        const float scale = args.scale;
+        // (a warp that gave up waiting still meets the others at their barriers)
         bool ok = true;
-        // (a helper that gave up waiting still meets the others at their barriers; one iteration more for the last state)
 #pragma unroll 1
-        for (int n = 0; n <= nch; ++n) {
+        for (int n = 0; n < nch; ++n) {
             const int c = chunk(n);
-            const uint32_t st = s0 + (n & 1) * Cfg::kStage, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
-            // V's column, or the scaled dY's (0 past the sequence's end, where TMA fills up)
-            if (ok && n < nch) ok = waitw(BBAR(full, n & 1), (n >> 1) & 1);
-            if (ok && n > 0 && n < nch)
-                ok = REV ? waitw(BBAR(done3, 2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1)
-                         : waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1);
-            if (ok && n < nch) {
-                tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t v[8], lo[8];
-                    const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int t = 2 * i;
-                        const uint32_t x0 = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
-                                       x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
-                        v[i] = live ? x0 | x1 << 16 : 0;
-                    }
-                    if (REV) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 g = lds_f4(gates + 64 * x + 16 * i);
-                            split(__fmul2_rn(make_float2(scale * g.x, scale * g.y), unpack(v[2 * i])), v[2 * i], lo[2 * i]);
-                            split(__fmul2_rn(make_float2(scale * g.z, scale * g.w), unpack(v[2 * i + 1])), v[2 * i + 1], lo[2 * i + 1]);
-                        }
-                        tm_st8(tq + kcY + 32 + 8 * x, lo);
-                    }
-                    tm_st8(tq + (REV ? kcY : kcV) + 8 * x, v);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                bar_arrive_warp(BBAR(got_v, 0));
-            }
-            // the state before the chunk; backwards its gradient behind it
-            if (ok) ok = waitw(BBAR(got_s, 0), n & 1) && waitw(BBAR(got_s, 1), n & 1);
-            if (ok) {
-                tc_fence_after();
-                uint8_t *img = (REV ? args.dS : args.S) + (bh * (nch + 1) + (REV ? c + 1 : c)) * (2 * kStateImg<KD>);
-#pragma unroll 1
-                for (int x = 0; x < KD / 16; ++x) {
-                    float hi[8], lo[8];
-                    tm_ld8(tq + kcS + 8 * x, hi);
-                    tm_ld8(tq + kcS + KH + 8 * x, lo);
-                    wait_loaded(hi);
-                    wait_loaded(lo);
-                    uint32_t hw[8], lw[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) hw[i] = __float_as_uint(hi[i]), lw[i] = __float_as_uint(lo[i]);
-                    st_row16(img + (x >> 2) * kImg, d, x & 3, hw);
-                    st_row16(img + kStateImg<KD> + (x >> 2) * kImg, d, x & 3, lw);
-                }
-                tc_fence_before();
-                bar_arrive_warp(BBAR(s_read, 0));
-            }
-            if (n == nch) break;
-            // E, or N
+            const uint32_t gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
+            // E, or N (the gates have been waited for by those whose products this waits for)
             if (ok) ok = waitw(BBAR(done2, 0), n & 1) && waitw(BBAR(done2, 1), n & 1);
             if (ok) {
                 tc_fence_after();
@@ -352,13 +295,81 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             if (ok) {
                 const int per = dv / 8, rows = min(kC, T - c * kC);
                 uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC) * dv;
-#pragma unroll 1
+#pragma unroll 2
                 for (int x = ht; x < rows * per; x += 32 * kHelpers) {
                     const int t = x / per, w = x % per;
                     *reinterpret_cast<uint4 *>(y0 + (size_t)t * dv + 8 * w) = lds4(s0 + Cfg::kOutV + (w >> 3) * kTile + sw128_offset(t, w & 7));
                 }
             }
             named_barrier_sync(1, 32 * kHelpers);
+        }
+        tc_fence_before();
+    } else if (warp >= kBringer) {
+        regs_dec<kRegsBring>();
+        const int q4 = warp & 3, d = 32 * q4 + lane;    // lane quadrant, value column
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
+        const bool live = d < dv;
+        const float scale = args.scale;
+        // (one iteration more for the last state)
+#pragma unroll 1
+        for (int n = 0; n <= nch; ++n) {
+            const int c = chunk(n);
+            const uint32_t st = s0 + (n & 1) * Cfg::kStage, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
+            if (n < nch) {
+                // V's column, or the scaled dY's (0 past the sequence's end, where TMA fills up), once the last chunk's is used
+                if (!waitw(BBAR(full, n & 1), (n >> 1) & 1)) break;
+                if (n > 0 && !(REV ? waitw(BBAR(done3, 2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1)
+                                   : waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1)))
+                    break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t v[8], lo[8];
+                    const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int t = 2 * i;
+                        const uint32_t x0 = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
+                                       x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
+                        v[i] = live ? x0 | x1 << 16 : 0;
+                    }
+                    if (REV) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 g = lds_f4(gates + 64 * x + 16 * i);
+                            split(__fmul2_rn(make_float2(scale * g.x, scale * g.y), unpack(v[2 * i])), v[2 * i], lo[2 * i]);
+                            split(__fmul2_rn(make_float2(scale * g.z, scale * g.w), unpack(v[2 * i + 1])), v[2 * i + 1], lo[2 * i + 1]);
+                        }
+                        tm_st8(tq + kcY + 32 + 8 * x, lo);
+                    }
+                    tm_st8(tq + (REV ? kcY : kcV) + 8 * x, v);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                bar_arrive_warp(BBAR(got_v, 0));
+            }
+            // the state before the chunk; backwards its gradient behind it
+            if (!waitw(BBAR(got_s, 0), n & 1) || !waitw(BBAR(got_s, 1), n & 1)) break;
+            tc_fence_after();
+            uint8_t *img = (REV ? args.dS : args.S) + (bh * (nch + 1) + (REV ? c + 1 : c)) * (2 * kStateImg<KD>);
+#pragma unroll 1
+            for (int x = 0; x < KD / 16; ++x) {
+                float hi[8], lo[8];
+                tm_ld8(tq + kcS + 8 * x, hi);
+                tm_ld8(tq + kcS + KH + 8 * x, lo);
+                wait_loaded(hi);
+                wait_loaded(lo);
+                if (x == KD / 16 - 1) {
+                    tc_fence_before();
+                    bar_arrive_warp(BBAR(s_read, 0));
+                }
+                uint32_t hw[8], lw[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hw[i] = __float_as_uint(hi[i]), lw[i] = __float_as_uint(lo[i]);
+                st_row16(img + (x >> 2) * kImg, d, x & 3, hw);
+                st_row16(img + kStateImg<KD> + (x >> 2) * kImg, d, x & 3, lw);
+            }
         }
         tc_fence_before();
     } else {
@@ -398,58 +409,68 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             ok = waitw(BBAR(full, n & 1), (n >> 1) & 1) && waitw(REV ? BBAR(done0, 0) : BBAR(got_v, 0), ph) && waitw(BBAR(done1, ch), ph);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
-                float p[16], v[REV ? 16 : 8];
-                tc_ld_32x32b_x16(tq + kcP + 16 * x, p);
-                if constexpr (REV) tc_ld_32x32b_x16(tq + kcA + 16 * x, v);
-                else tm_ld8(tq + kcV + 8 * x, v);
-                wait_loaded(p);
-                wait_loaded(v);
-                uint32_t hi[8], lo[8];
+            {
+                float p[2][16], v[2][REV ? 16 : 8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 p0 = make_float2(p[4 * i], p[4 * i + 1]), p1 = make_float2(p[4 * i + 2], p[4 * i + 3]);
-                    float2 r0, r1;
-                    if constexpr (REV) {
-                        const float4 er = lds_f4(gates + 4 * kC + 64 * x + 16 * i), be = lds_f4(gates + 8 * kC + 64 * x + 16 * i);
-                        const float2 sc = make_float2(scale, scale);
-                        r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(sc, make_float2(v[4 * i], v[4 * i + 1]), __fmul2_rn(make_float2(er.x, er.y), p0)));
-                        r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(sc, make_float2(v[4 * i + 2], v[4 * i + 3]), __fmul2_rn(make_float2(er.z, er.w), p1)));
-                    } else {
-                        const float4 g = lds_f4(gates + 64 * x + 16 * i);
-                        r0 = __ffma2_rn(make_float2(-g.x, -g.y), p0, unpack(__float_as_uint(v[2 * i])));
-                        r1 = __ffma2_rn(make_float2(-g.z, -g.w), p1, unpack(__float_as_uint(v[2 * i + 1])));
-                    }
-                    split(r0, hi[2 * i], lo[2 * i]);
-                    split(r1, hi[2 * i + 1], lo[2 * i + 1]);
+                for (int y = 0; y < 2; ++y) {
+                    tc_ld_32x32b_x16(tq + kcP + 32 * ch + 16 * y, p[y]);
+                    if constexpr (REV) tc_ld_32x32b_x16(tq + kcA + 32 * ch + 16 * y, v[y]);
+                    else tm_ld8(tq + kcV + 16 * ch + 8 * y, v[y]);
                 }
-                tm_st8(tq + kcR + 8 * x, hi);
-                tm_st8(tq + kcR + 32 + 8 * x, lo);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    wait_loaded(p[y]);
+                    wait_loaded(v[y]);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p0 = make_float2(p[y][4 * i], p[y][4 * i + 1]), p1 = make_float2(p[y][4 * i + 2], p[y][4 * i + 3]);
+                        const uint32_t ga = gates + 128 * ch + 64 * y + 16 * i;
+                        float2 r0, r1;
+                        if constexpr (REV) {
+                            const float4 er = lds_f4(ga + 4 * kC), be = lds_f4(ga + 8 * kC);
+                            const float2 sc = make_float2(scale, scale);
+                            r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(sc, make_float2(v[y][4 * i], v[y][4 * i + 1]), __fmul2_rn(make_float2(er.x, er.y), p0)));
+                            r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(sc, make_float2(v[y][4 * i + 2], v[y][4 * i + 3]), __fmul2_rn(make_float2(er.z, er.w), p1)));
+                        } else {
+                            const float4 g = lds_f4(ga);
+                            r0 = __ffma2_rn(make_float2(-g.x, -g.y), p0, unpack(__float_as_uint(v[y][2 * i])));
+                            r1 = __ffma2_rn(make_float2(-g.z, -g.w), p1, unpack(__float_as_uint(v[y][2 * i + 1])));
+                        }
+                        split(r0, hi[2 * i], lo[2 * i]);
+                        split(r1, hi[2 * i + 1], lo[2 * i + 1]);
+                    }
+                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
+                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
+                }
             }
             stored(BBAR(got_r, ch));
             // beta e^{G_C - G} E^T; backwards -e^G N^T
             ok = waitw(BBAR(done2, ch), ph);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
-                float e[16];
-                tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
-                wait_loaded(e);
-                uint32_t hi[8], lo[8];
+            {
+                float e[2][16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 g = lds_f4(gates + (REV ? 0 : 4 * kC) + 64 * x + 16 * i);
-                    float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
-                    if (!REV) f = lds_f4(gates + 8 * kC + 64 * x + 16 * i);
-                    split(__fmul2_rn(make_float2(g.x, g.y), __fmul2_rn(make_float2(f.x, f.y), make_float2(e[4 * i], e[4 * i + 1]))),
-                          hi[2 * i], lo[2 * i]);
-                    split(__fmul2_rn(make_float2(g.z, g.w), __fmul2_rn(make_float2(f.z, f.w), make_float2(e[4 * i + 2], e[4 * i + 3]))),
-                          hi[2 * i + 1], lo[2 * i + 1]);
+                for (int y = 0; y < 2; ++y) tc_ld_32x32b_x16(tq + kcE + 32 * ch + 16 * y, e[y]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    wait_loaded(e[y]);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t ga = gates + 128 * ch + 64 * y + 16 * i;
+                        const float4 g = lds_f4(ga + (REV ? 0 : 4 * kC));
+                        float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
+                        if (!REV) f = lds_f4(ga + 8 * kC);
+                        split(__fmul2_rn(make_float2(g.x, g.y), __fmul2_rn(make_float2(f.x, f.y), make_float2(e[y][4 * i], e[y][4 * i + 1]))),
+                              hi[2 * i], lo[2 * i]);
+                        split(__fmul2_rn(make_float2(g.z, g.w), __fmul2_rn(make_float2(f.z, f.w), make_float2(e[y][4 * i + 2], e[y][4 * i + 3]))),
+                              hi[2 * i + 1], lo[2 * i + 1]);
+                    }
+                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
+                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
                 }
-                tm_st8(tq + kcR + 8 * x, hi);
-                tm_st8(tq + kcR + 32 + 8 * x, lo);
             }
             stored(BBAR(got_w, ch));
             const float gC = ldsf(gates + 4 * (kC - 1));
@@ -457,14 +478,15 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             ok = waitw(BBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1) && waitw(BBAR(s_read, 0), ph);
             if (!ok) break;
             tc_fence_after();
+            float ds[2][16];
+            tc_ld_32x32b_x16(tq + kcP + 64 * ch, ds[0]);
 #pragma unroll
             for (int x = 0; x < KH / 16; ++x) {
-                float ds[16];
-                tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * x, ds);
-                wait_loaded(ds);
+                wait_loaded(ds[x & 1]);
+                if (x + 1 < KH / 16) tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * (x + 1), ds[(x + 1) & 1]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
+                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[x & 1][2 * i], ds[x & 1][2 * i + 1]));
                 put_s(x, S + 8 * x);
             }
             stored(BBAR(got_s, ch));

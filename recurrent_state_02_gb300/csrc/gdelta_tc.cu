@@ -403,15 +403,15 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 }
 
 // ------------------------------------------------------------------ the chain
-// Four warpgroups: 0 and 1 own the state (warp w: TMEM lanes 32 (w % 4) .., half w / 4 of the tokens in steps 1 and 2 and of
-// the state's rows in step 3), 2 (a lane quadrant per warp) brings V's columns to their lanes and y from them to memory, and in 3
-// one warp issues the MMAs and one loads.  The halves run staggered: the second one's products overlap the first one's
+// Five warpgroups: 0 and 1 own the state (warp w: TMEM lanes 32 (w % 4) .., half w / 4 of the tokens in steps 1 and 2 and of
+// the state's rows in step 3), 2 (a lane quadrant per warp) brings V's columns to their lanes, 3 takes y from them to memory, and in
+// 4 one warp issues the MMAs and one loads.  The halves run staggered: the second one's products overlap the first one's
 // conversions.
-constexpr int kOwners = 8, kHelpers = 4, kIssuer = 12, kLoader = 13;
-constexpr int kMThreads = 512;
+constexpr int kOwners = 8, kHelpers = 4, kBringer = 8, kTaker = 12, kIssuer = 16, kLoader = 17;
+constexpr int kMThreads = 640;
 constexpr int kGateRing = 4;
-// registers per thread after the split (launched with 128): 2 x 160 + 104 + 88 = 4 x 128
-constexpr int kRegsOwn = 160, kRegsHelp = 104, kRegsRest = 88;
+// registers per thread after the split (launched with 96): 2 x 144 + 56 + 80 + 56 = 5 x 96
+constexpr int kRegsOwn = 144, kRegsBring = 56, kRegsTake = 80, kRegsRest = 56;
 template <int KD>
 struct ChainCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;    // a K or Q tile (64-feature blocks)
@@ -428,9 +428,9 @@ constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcQS = 256, kcAV = 320, kcR = 
 struct alignas(16) MSmall {
     uint64_t full_k[2], full_vx[2], full_qa[2];
     uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (4 warps)
-    uint64_t got_v;                          // V^T is (the helpers)
-    uint64_t y_read;                         // Q S and A V' have been read (the helpers)
-    uint64_t tail;                           // packed: the last chunk's rows of K past the end are 0 (the helpers)
+    uint64_t got_v;                          // V^T is (the bringers)
+    uint64_t y_read;                         // Q S and A V' have been read (the takers)
+    uint64_t tail;                           // packed: the last chunk's rows of K past the end are 0 (the bringers)
     uint64_t done1[2], done2[2];             // halves of P, E
     // halves of dS of even and odd chunks, Q S and A V' (the loader may look at them late, but not two chunks late)
     uint64_t done3[4], done4[2];
@@ -486,7 +486,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     __syncthreads();
     tc_fence_after();
 
-    if (warp >= kOwners + kHelpers) {
+    if (warp >= kIssuer) {
         regs_dec<kRegsRest>();
         if (warp == kLoader && elect_one()) {
             const int hk = h / (H / args.s.Hk);
@@ -618,87 +618,98 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             wait1(MBAR(fin, 0), 0);
         }
         __syncwarp();
-    } else if (warp >= kOwners) {
-        regs_dec<kRegsHelp>();
-        const int q4 = warp & 3, d = 32 * q4 + lane;    // lane quadrant, value column of the CTA
+    } else if (warp >= kTaker) {
+        regs_dec<kRegsTake>();
+        const int q4 = warp & 3, d = 32 * q4 + lane;
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
-        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;   // this column in a tile of V or y
+        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
         const size_t y_step = (packed ? (size_t)H : 1) * dv;
         uint16_t *const y0 = args.y + (packed ? (sp.tok0 * H + h) * dv : bh * args.s.T * dv) + 128 * tile;
         const float scale = args.scale;
-        // (a helper that gave up waiting still meets the others at their barriers)
+        // (a warp that gave up waiting still meets the others at their barriers)
         bool ok = true;
 #pragma unroll 1
-        for (int n = 0; n <= nch; ++n) {
-            // this thread's column of V (0 past the sequence's end), once the owners have read the last chunk's
-            if (ok && n < nch) ok = waitw(MBAR(full_vx, n & 1), (n >> 1) & 1);
-            if (ok && n > 0 && n < nch) ok = waitw(MBAR(got_r, 0), (n - 1) & 1) && waitw(MBAR(got_r, 1), (n - 1) & 1);
-            if (ok && n < nch) {
-                const uint32_t st = s0 + (n & 1) * Cfg::kStage;
-                const int left = T - n * kC;
-                if (tail && n == nch - 1) {
-                    // rows of K past the end hold another sequence's keys, which step 3 would multiply by 0: they become 0
-                    ok = waitw(MBAR(full_k, n & 1), (n >> 1) & 1);
-                    for (int x = tid - 32 * kOwners; x < (kC - left) * (KD / 8); x += 32 * kHelpers) {
-                        const int c = x % (KD / 8);
-                        sts4(st + Cfg::kSK + (c >> 3) * kTile + sw128_offset(left + x / (KD / 8), c & 7), 0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    bar_arrive_warp(MBAR(tail, 0));
-                }
-                tc_fence_after();
-                const int last = d < ncols ? left : 0;
-#pragma unroll 1
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t v[8];
-                    const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int t = 2 * i;
-                        const uint32_t lo = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
-                                       hi = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
-                        v[i] = (16 * x + t < last ? lo : 0) | (16 * x + t + 1 < last ? hi << 16 : 0);
-                    }
-                    tm_st8(tq + kcV + 8 * x, v);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                bar_arrive_warp(MBAR(got_v, 0));
-            }
-            if (n == 0) continue;
-            // y of chunk n - 1, through shared memory to whole rows
-            const int m = n - 1, rows = min(kC, T - m * kC);
-            if (ok) ok = waitw(MBAR(done4, m & 1), (m >> 1) & 1);
+        for (int n = 0; n < nch; ++n) {
+            // y, through shared memory to whole rows (the gates have been waited for by those whose products this waits for)
+            if (ok) ok = waitw(MBAR(done4, n & 1), (n >> 1) & 1);
             if (ok) {
                 tc_fence_after();
-                const uint32_t eg = s0 + Cfg::kGates + (m % kGateRing) * 1024;
+                const uint32_t eg = s0 + Cfg::kGates + (n % kGateRing) * 1024;
 #pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    float qs[8], av[8];
-                    tm_ld8(tq + kcQS + 8 * x, qs);
-                    tm_ld8(tq + kcAV + 8 * x, av);
-                    const float4 g0 = lds_f4(eg + 32 * x), g1 = lds_f4(eg + 32 * x + 16);
-                    const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+                for (int x = 0; x < 4; ++x) {
+                    float qs[16], av[16];
+                    tc_ld_32x32b_x16(tq + kcQS + 16 * x, qs);
+                    tc_ld_32x32b_x16(tq + kcAV + 16 * x, av);
                     wait_loaded(qs);
                     wait_loaded(av);
-                    const uint32_t a = s0 + Cfg::kY + col + x * (8 * 128);
+                    const uint32_t a = s0 + Cfg::kY + col + x * (16 * 128);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sts_u16(a + i * 128 + ((c16 ^ i) << 4), pack_bf16x2(scale * fmaf(g[i], qs[i], av[i]), 0.f));
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 g = lds_f4(eg + 64 * x + 16 * i);
+                        const float f[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = 4 * i + u;
+                            sts_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4), pack_bf16x2(scale * fmaf(f[u], qs[t], av[t]), 0.f));
+                        }
+                    }
                 }
                 tc_fence_before();
                 bar_arrive_warp(MBAR(y_read, 0));
             }
             named_barrier_sync(1, 32 * kHelpers);
             if (ok) {
-                const int per = ncols / 8;                  // 16-byte words of a row
-#pragma unroll 1
-                for (int x = tid - 32 * kOwners; x < rows * per; x += 32 * kHelpers) {
+                const int per = ncols / 8, rows = min(kC, T - n * kC);   // 16-byte words of a row
+#pragma unroll 2
+                for (int x = tid - 32 * kTaker; x < rows * per; x += 32 * kHelpers) {
                     const int t = x / per, w = x % per;
-                    *reinterpret_cast<uint4 *>(y0 + (size_t)(m * kC + t) * y_step + 8 * w) =
+                    *reinterpret_cast<uint4 *>(y0 + (size_t)(n * kC + t) * y_step + 8 * w) =
                         lds4(s0 + Cfg::kY + (w >> 3) * kTile + sw128_offset(t, w & 7));
                 }
             }
             named_barrier_sync(1, 32 * kHelpers);
+        }
+        tc_fence_before();
+    } else if (warp >= kBringer) {
+        regs_dec<kRegsBring>();
+        const int q4 = warp & 3, d = 32 * q4 + lane;    // lane quadrant, value column of the CTA
+        const uint32_t tq = (uint32_t)(32 * q4) << 16;
+        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;   // this column in a tile of V
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n) {
+            // this thread's column of V (0 past the sequence's end), once the owners have read the last chunk's
+            const uint32_t st = s0 + (n & 1) * Cfg::kStage;
+            if (!waitw(MBAR(full_vx, n & 1), (n >> 1) & 1)) break;
+            if (n > 0 && !(waitw(MBAR(got_r, 0), (n - 1) & 1) && waitw(MBAR(got_r, 1), (n - 1) & 1))) break;
+            const int left = T - n * kC;
+            if (tail && n == nch - 1) {
+                // rows of K past the end hold another sequence's keys, which step 3 would multiply by 0: they become 0
+                if (!waitw(MBAR(full_k, n & 1), (n >> 1) & 1)) break;
+                for (int x = tid - 32 * kBringer; x < (kC - left) * (KD / 8); x += 32 * kHelpers) {
+                    const int c = x % (KD / 8);
+                    sts4(st + Cfg::kSK + (c >> 3) * kTile + sw128_offset(left + x / (KD / 8), c & 7), 0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                bar_arrive_warp(MBAR(tail, 0));
+            }
+            tc_fence_after();
+            const int last = d < ncols ? left : 0;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+                uint32_t v[8];
+                const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int t = 2 * i;
+                    const uint32_t lo = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
+                                   hi = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
+                    v[i] = (16 * x + t < last ? lo : 0) | (16 * x + t + 1 < last ? hi << 16 : 0);
+                }
+                tm_st8(tq + kcV + 8 * x, v);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            bar_arrive_warp(MBAR(got_v, 0));
         }
         tc_fence_before();
     } else {
@@ -739,64 +750,74 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             ok = waitw(MBAR(full_vx, n & 1), (n >> 1) & 1) && waitw(MBAR(got_v, 0), ph) && waitw(MBAR(done1, ch), ph);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
-                float p[16], v[8];
-                tc_ld_32x32b_x16(tq + kcP + 16 * x, p);
-                tm_ld8(tq + kcV + 8 * x, v);
-                wait_loaded(p);
-                wait_loaded(v);
-                uint32_t hi[8], lo[8];
+            {
+                float p[2][16], v[2][8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 g = lds_f4(gates + 64 * x + 16 * i);
-                    const uint32_t v0 = __float_as_uint(v[2 * i]), v1 = __float_as_uint(v[2 * i + 1]);
-                    split(__ffma2_rn(make_float2(-g.x, -g.y), make_float2(p[4 * i], p[4 * i + 1]), make_float2(bf16_lo(v0), bf16_hi(v0))),
-                          hi[2 * i], lo[2 * i]);
-                    split(__ffma2_rn(make_float2(-g.z, -g.w), make_float2(p[4 * i + 2], p[4 * i + 3]), make_float2(bf16_lo(v1), bf16_hi(v1))),
-                          hi[2 * i + 1], lo[2 * i + 1]);
+                for (int y = 0; y < 2; ++y) {
+                    tc_ld_32x32b_x16(tq + kcP + 32 * ch + 16 * y, p[y]);
+                    tm_ld8(tq + kcV + 16 * ch + 8 * y, v[y]);
                 }
-                tm_st8(tq + kcR + 8 * x, hi);
-                tm_st8(tq + kcR + 32 + 8 * x, lo);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    wait_loaded(p[y]);
+                    wait_loaded(v[y]);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 g = lds_f4(gates + 128 * ch + 64 * y + 16 * i);
+                        const uint32_t v0 = __float_as_uint(v[y][2 * i]), v1 = __float_as_uint(v[y][2 * i + 1]);
+                        split(__ffma2_rn(make_float2(-g.x, -g.y), make_float2(p[y][4 * i], p[y][4 * i + 1]), make_float2(bf16_lo(v0), bf16_hi(v0))),
+                              hi[2 * i], lo[2 * i]);
+                        split(__ffma2_rn(make_float2(-g.z, -g.w), make_float2(p[y][4 * i + 2], p[y][4 * i + 3]), make_float2(bf16_lo(v1), bf16_hi(v1))),
+                              hi[2 * i + 1], lo[2 * i + 1]);
+                    }
+                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
+                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
+                }
             }
             stored(MBAR(got_r, ch));
             // V'^T = beta E^T, and decayed to the chunk's end
             ok = waitw(MBAR(done2, ch), ph);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 2 * ch; x < 2 * ch + 2; ++x) {
-                float e[16];
-                tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
-                wait_loaded(e);
-                uint32_t w[8], hi[8], lo[8];
+            {
+                float e[2][16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 er = lds_f4(gates + 4 * kC + 64 * x + 16 * i), be = lds_f4(gates + 8 * kC + 64 * x + 16 * i);
-                    const float2 w0 = __fmul2_rn(make_float2(be.x, be.y), make_float2(e[4 * i], e[4 * i + 1]));
-                    const float2 w1 = __fmul2_rn(make_float2(be.z, be.w), make_float2(e[4 * i + 2], e[4 * i + 3]));
-                    w[2 * i] = pack_bf16x2(w0.x, w0.y);
-                    w[2 * i + 1] = pack_bf16x2(w1.x, w1.y);
-                    split(__fmul2_rn(make_float2(er.x, er.y), w0), hi[2 * i], lo[2 * i]);
-                    split(__fmul2_rn(make_float2(er.z, er.w), w1), hi[2 * i + 1], lo[2 * i + 1]);
+                for (int y = 0; y < 2; ++y) tc_ld_32x32b_x16(tq + kcE + 32 * ch + 16 * y, e[y]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    wait_loaded(e[y]);
+                    uint32_t w[8], hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t g = gates + 128 * ch + 64 * y + 16 * i;
+                        const float4 er = lds_f4(g + 4 * kC), be = lds_f4(g + 8 * kC);
+                        const float2 w0 = __fmul2_rn(make_float2(be.x, be.y), make_float2(e[y][4 * i], e[y][4 * i + 1]));
+                        const float2 w1 = __fmul2_rn(make_float2(be.z, be.w), make_float2(e[y][4 * i + 2], e[y][4 * i + 3]));
+                        w[2 * i] = pack_bf16x2(w0.x, w0.y);
+                        w[2 * i + 1] = pack_bf16x2(w1.x, w1.y);
+                        split(__fmul2_rn(make_float2(er.x, er.y), w0), hi[2 * i], lo[2 * i]);
+                        split(__fmul2_rn(make_float2(er.z, er.w), w1), hi[2 * i + 1], lo[2 * i + 1]);
+                    }
+                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
+                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
+                    tm_st8(tq + kcW + 16 * ch + 8 * y, w);
                 }
-                tm_st8(tq + kcR + 8 * x, hi);
-                tm_st8(tq + kcR + 32 + 8 * x, lo);
-                tm_st8(tq + kcW + 8 * x, w);
             }
             stored(MBAR(got_w, ch));
             const float gC = ldsf(gates + 4 * (kC - 1));
             ok = waitw(MBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
+            float ds[2][16];
+            tc_ld_32x32b_x16(tq + kcP + 64 * ch, ds[0]);
 #pragma unroll
             for (int x = 0; x < KH / 16; ++x) {
-                float ds[16];
-                tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * x, ds);
-                wait_loaded(ds);
+                wait_loaded(ds[x & 1]);
+                if (x + 1 < KH / 16) tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * (x + 1), ds[(x + 1) & 1]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
+                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[x & 1][2 * i], ds[x & 1][2 * i + 1]));
                 if (n + 1 < nch) put_s(x, S + 8 * x);
             }
             if (n + 1 < nch) stored(MBAR(got_s, ch));
