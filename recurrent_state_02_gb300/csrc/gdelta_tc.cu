@@ -77,21 +77,25 @@ gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, 
 }
 
 // ------------------------------------------------------- A, X and the gates
+// Four warps per chunk and head.  [G; P] = [K; Q] K^T on the tensor cores; a row of L or A per thread, its decays as running products
+// of the gates from the diagonal to the left (no logarithms, and gates of 0 need no care); then X = (I + L)^{-1} in FP32: the four
+// diagonal blocks of 16 by forward substitution, a warp each, and the blocks below them, 16 and then 32 wide, as
+// X_10 = -X_11 (L_10 X_00).
+// Bound by instructions, about 1500 issue slots per SM quarter and chunk.
 constexpr int kPThreads = 128;
 constexpr int LD = 68;                           // FP32 row stride of Lt
 constexpr int LDT = 36;                          // FP32 row stride of the 32 x 32 blocks
+constexpr int LDS16 = 20;                        // and of the 16 x 16 ones
 // K and Q interleaved by 64-feature block ([K; Q] is one 128-row operand per block); once [G; P] is complete the region
-// holds L and the solve's FP32 blocks, and X's high part in rows of L that the last products do not read
-constexpr uint32_t kPL = 0;                      // Lt (FP32, 64 x LD): Lt[u][i] holds row i, column u
-constexpr uint32_t kPT00 = kPL + kC * LD * 4;    // X00 (FP32, [u][j])
-constexpr uint32_t kPT11t = kPT00 + 32 * LDT * 4;   // X11 transposed (FP32, [u][i])
-constexpr uint32_t kPM = kPT11t + 32 * LDT * 4;  // M = L10 X00 (FP32, [u][j])
-constexpr uint32_t kPXh = 9 * 1024;
-constexpr uint32_t kPXl = 32 * 1024;
-constexpr uint32_t kPGate = kPXl + kTile;        // per token: log2 gate sum (high, low part), beta
-constexpr uint32_t kPSmall = kPGate + kC * 16;
-static_assert(kPM + 32 * LDT * 4 <= kPXl, "L and the solve's blocks fit in the K, Q region");
-static_assert(kPXh >= (uint32_t)(kPL + 32 * LD * 4) && kPXh + kTile <= kPT00, "X's high part lies past what the products read of Lt");
+// holds L and the solve's blocks
+constexpr uint32_t kPL = 0;                      // Lt (64 x LD): Lt[u][i] holds row i, column u; then X10 [i][j]
+constexpr uint32_t kPX00 = kPL + kC * LD * 4;    // X00 [u][j]
+constexpr uint32_t kPX11t = kPX00 + 32 * LDT * 4;   // X11 transposed [u][i]
+constexpr uint32_t kPM = kPX11t + 32 * LDT * 4;  // M = L10 X00 [u][j]
+constexpr uint32_t kPM16 = kPM + 32 * LDT * 4;   // the same for the two 32-blocks' halves
+constexpr uint32_t kPGate = kPM16 + 2 * 16 * LDS16 * 4;   // alpha, beta of the chunk's tokens
+constexpr uint32_t kPSmall = kPGate + 2 * kC * 4;
+static_assert(kPGate >= 4 * kTile && kPGate % 16 == 0, "the gates lie behind the K, Q tiles");
 
 struct alignas(16) PSmall {
     uint64_t full, mma;
@@ -100,34 +104,23 @@ struct alignas(16) PSmall {
 };
 constexpr uint32_t kPSmemBytes = kPSmall + sizeof(PSmall) + 1024;
 
-__device__ __forceinline__ uint32_t tile_off(int row, int col)
-{
-    return sw128_offset(row, col >> 3) + (uint32_t)(col & 7) * 2;
-}
-
-// One element of X as its two parts in the images.
-__device__ __forceinline__ void put_x(uint8_t *base, int row, int col, float x)
-{
-    const uint32_t h = pack_bf16x2(x, 0.f), o = tile_off(row, col);
-    *reinterpret_cast<uint16_t *>(base + kPXh + o) = (uint16_t)h;
-    *reinterpret_cast<uint16_t *>(base + kPXl + o) = (uint16_t)pack_bf16x2(x - bf16_lo(h), 0.f);
-}
-
 // BACK: for the gradients, which take A in two parts and betas of at least 2^-40 (dbeta is formed by dividing by them; the
 // change is far below FP32's rounding).
 constexpr float kLeastBeta = 9.094947017729282e-13f;
 template <int KD, bool BACK>
-__global__ void __launch_bounds__(kPThreads, 5)
+__global__ void __launch_bounds__(kPThreads, 6)
 gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k, const GdeltaTcArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = align1024(smem_raw);
     PSmall *sm = reinterpret_cast<PSmall *>(base + kPSmall);
     float *Lt = reinterpret_cast<float *>(base + kPL);
-    float *T00f = reinterpret_cast<float *>(base + kPT00);
-    float *T11t = reinterpret_cast<float *>(base + kPT11t);
+    float *X10 = Lt;
+    float *X00 = reinterpret_cast<float *>(base + kPX00);
+    float *X11t = reinterpret_cast<float *>(base + kPX11t);
     float *Mf = reinterpret_cast<float *>(base + kPM);
-    float4 *gate = reinterpret_cast<float4 *>(base + kPGate);
+    float *M16 = reinterpret_cast<float *>(base + kPM16);
+    float *alpha = reinterpret_cast<float *>(base + kPGate), *beta = alpha + kC;
 
     const GdeltaShape &s = args.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -139,7 +132,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     Span sp;
     if (packed) {
         if (slot >= args.slot_base[s.B]) return;
-        // the last sequence that starts at or before the slot, 32 probes at a time (-1: skipped ones are passed over below)
+        // the last sequence that starts at or before the slot, 32 probes at a time (-1: skipped ones are passed over)
         int lo = 0, n = s.B;
         while (n > 0) {
             const int step = (n + 31) / 32, at = lo + lane * step;
@@ -192,8 +185,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     }
     uint8_t *wsc = args.ws + ((size_t)slot * s.H + h) * (BACK ? kWsChunkB : kWsChunk);
     if (warp == 0) {
-        // G in 64 bits, kept as two FP32 parts: differences over a few tokens stay exact to FP32 behind gates near 0.
-        // A gate of 0 counts as 2^-400, which every exponential takes to 0.
+        // lane l: tokens 2 l, 2 l + 1.  e^G and e^{G_C - G} as products from the left and from the right.
         const int i0 = 2 * lane;
         float al[2], be[2];
 #pragma unroll
@@ -212,24 +204,35 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 reinterpret_cast<float *>(wsc + kWsGates + kGateRatio)[i0 + e] = ratio;
             }
         }
-        const double l0 = al[0] > 0.f ? (double)log2f(al[0]) : -400.0, l1 = al[1] > 0.f ? (double)log2f(al[1]) : -400.0;
-        double inc = l0 + l1;
+        float left = al[0] * al[1], right = left;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+            const float x = __shfl_up_sync(0xffffffffu, left, o), y = __shfl_down_sync(0xffffffffu, right, o);
+            if (lane >= o) left *= x;
+            if (lane + o < 32) right *= y;
         }
-        const double total = __shfl_sync(0xffffffffu, inc, 31);
-        float *g = reinterpret_cast<float *>(wsc + kWsGates);
+        float before = __shfl_up_sync(0xffffffffu, left, 1), behind = __shfl_down_sync(0xffffffffu, right, 1);
+        if (lane == 0) before = 1.f;
+        if (lane == 31) behind = 1.f;
+        float2 *g = reinterpret_cast<float2 *>(wsc + kWsGates);
+        g[lane] = make_float2(before * al[0], before * al[0] * al[1]);
+        g[kC / 2 + lane] = make_float2(al[1] * behind, behind);
+        g[kC + lane] = make_float2(be[0], be[1]);
+        reinterpret_cast<float2 *>(alpha)[lane] = make_float2(al[0], al[1]);
+        reinterpret_cast<float2 *>(beta)[lane] = make_float2(be[0], be[1]);
+        if (BACK) {
+            // G itself in 64 bits, kept as two FP32 parts: differences over a few tokens stay exact to FP32 behind gates near 0.
+            // A gate of 0 counts as 2^-400, which every exponential takes to 0.
+            const double l0 = al[0] > 0.f ? (double)log2f(al[0]) : -400.0, l1 = al[1] > 0.f ? (double)log2f(al[1]) : -400.0;
+            double inc = l0 + l1;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const double G = e ? inc : inc - l1;
-            const float hi = (float)G;
-            gate[i0 + e] = make_float4(hi, (float)(G - hi), be[e], 0.f);
-            g[i0 + e] = ex2((float)G);
-            g[kC + i0 + e] = ex2((float)(total - G));
-            g[2 * kC + i0 + e] = be[e];
-            if (BACK) reinterpret_cast<float2 *>(g + 3 * kC)[i0 + e] = make_float2(hi, (float)(G - hi));
+            for (int o = 1; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const double G0 = inc - l1;
+            const float h0 = (float)G0, h1 = (float)inc;
+            reinterpret_cast<float4 *>(wsc + kWsGates + kGateLog)[lane] = make_float4(h0, (float)(G0 - h0), h1, (float)(inc - h1));
         }
     }
     tc_fence_before();
@@ -241,112 +244,160 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     bool ok = true, issued = false;
     if (warp == 1) {
         ok = warp_wait(cx, &sm->full, 0);
-        if (ok && lane == 0) {
+        if (ok && elect_one()) {
             tc_fence_after();
             constexpr uint32_t id = idesc_bf16_f32(128, 64, false, false);
             const uint32_t klo = desc_lo(smem_u32(base), 16);
 #pragma unroll
             for (int kk = 0; kk < KD / 16; ++kk) {
                 const uint32_t o = ((kk >> 2) * 2 * kTile + (kk & 3) * 32) >> 4;
-                if (kk == 0) tc_mma_bf16_w<false>(tmem, klo, kHi128, klo, kHi128, id);
-                else tc_mma_bf16_w<true>(tmem, klo + o, kHi128, klo + o, kHi128, id);
+                mma_ss(tmem, klo + o, kHi128, klo + o, kHi128, id, kk > 0);
             }
             tc_commit(&sm->mma);
-            issued = true;
         }
+        issued = ok;
         __syncwarp();
     }
     ok = warp_wait(cx, &sm->mma, 0) && ok;
     tc_fence_after();
     if (!__syncthreads_or(!ok)) {
-        // Warps 0, 1 (TMEM lanes 0..63): row ri of L, transposed into Lt.  Warps 2, 3: row ri of A, as its image.  Rows
-        // and columns past the sequence's end (which hold another one's tokens) count as 0.
+        // Warps 0, 1 (TMEM lanes 0..63): row ri of L, transposed into Lt.  Warps 2, 3: row ri of A, as its image.  Rows past the
+        // sequence's end (which hold another one's tokens) count as 0.
         {
             const int ri = 32 * (warp & 1) + lane;
-            float v0[32], v1[32];
             const uint32_t tq = tmem + ((uint32_t)(32 * warp) << 16);
-            tc_ld_32x32b_x32(tq, v0);
-            if (warp & 1) tc_ld_32x32b_x32(tq + 32, v1);
-            tc_wait_ld();
-            const float4 gi = gate[ri];
-            const int end = ri < nt ? ri : -1;         // the last column of A's row, one past L's
-            if (warp < 2) {
+            const bool real = ri < nt;
+            uint8_t *arow = wsc + kWsA + (size_t)ri * 128, *lrow = wsc + kWsAl + (size_t)ri * 128;
+            float dec = 1.f, next = 1.f;         // e^{G_i - G_j}; the gate of token j + 1
+#pragma unroll 1
+            for (int half = warp & 1; half >= 0; --half) {
+                float v[32];
+                tc_ld_32x32b_x32(tq + 32 * half, v);
+                wait_loaded(v);
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    if (j >= 32 && !(warp & 1)) break;
-                    const float4 gj = gate[j];
-                    const float x = ex2((gi.x - gj.x) + (gi.y - gj.y)) * (j < 32 ? v0[j & 31] : v1[j & 31]) * gj.z;
-                    Lt[j * LD + ri] = j < end ? x : 0.f;
-                }
-            } else {
-                uint8_t *arow = wsc + kWsA + (size_t)ri * 128, *lrow = wsc + kWsAl + (size_t)ri * 128;
+                for (int x = 3; x >= 0; --x) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    float a[8];
+                    for (int y = 1; y >= 0; --y) {
+                        const int j0 = 32 * half + 8 * x + 4 * y;
+                        const float4 a4 = *reinterpret_cast<const float4 *>(alpha + j0), b4 = *reinterpret_cast<const float4 *>(beta + j0);
+                        const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = 8 * x + e;
-                        a[e] = 0.f;
-                        if (j < 32 || (warp & 1)) {
-                            const float4 gj = gate[j];
-                            const float p = ex2((gi.x - gj.x) + (gi.y - gj.y)) * (j < 32 ? v0[j & 31] : v1[j & 31]);
-                            a[e] = j <= end ? p : 0.f;
+                        for (int e = 3; e >= 0; --e) {
+                            const int j = j0 + e;
+                            float &w = v[8 * x + 4 * y + e];
+                            dec = j < ri ? dec * next : 1.f;
+                            next = av[e];
+                            if (warp < 2) Lt[j * LD + ri] = real && j < ri ? dec * bv[e] * w : 0.f;
+                            else w = real && j <= ri ? dec * w : 0.f;
                         }
                     }
-                    *reinterpret_cast<uint4 *>(arow + ((x ^ (ri & 7)) << 4)) = pack8(a);
-                    if (BACK) {
+                    if (warp >= 2) {
+                        const uint4 hi = pack8(v + 8 * x);
+                        const int word = ((4 * half + x) ^ (ri & 7)) << 4;
+                        *reinterpret_cast<uint4 *>(arow + word) = hi;
+                        if (BACK) {
+                            const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) a[e] -= bf16_lo(pack_bf16x2(a[e], 0.f));
-                        *reinterpret_cast<uint4 *>(lrow + ((x ^ (ri & 7)) << 4)) = pack8(a);
+                            for (int e = 0; e < 4; ++e) v[8 * x + 2 * e] -= bf16_lo(hw[e]), v[8 * x + 2 * e + 1] -= bf16_hi(hw[e]);
+                            *reinterpret_cast<uint4 *>(lrow + word) = pack8(v + 8 * x);
+                        }
                     }
+                }
+            }
+            if (warp == 2) {                     // the zeros of A's upper right quarter
+#pragma unroll
+                for (int x = 4; x < 8; ++x) {
+                    *reinterpret_cast<uint4 *>(arow + ((x ^ (ri & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    if (BACK) *reinterpret_cast<uint4 *>(lrow + ((x ^ (ri & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                 }
             }
         }
         __syncthreads();
-        // X00, X11 by forward substitution: lane j of warp 0 (1) owns column j of the block; after step u, acc[u] is final and
-        // is subtracted from the rows below.
-        float acc[32];
-        if (warp < 2) {
-            const int bb = 32 * warp;
-            const float *Lb = Lt + bb * LD + bb;
+        // The diagonal blocks of 16: lane l of warp w owns column l % 16 of block w; after step u, acc[u] is final and is subtracted
+        // from the rows below.
+        {
+            const int l = lane & 15;
+            const float *Lb = Lt + 16 * warp * LD + 16 * warp;
+            float acc[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = i == lane ? 1.f : 0.f;
+            for (int i = 0; i < 16; ++i) acc[i] = i == l ? 1.f : 0.f;
 #pragma unroll
-            for (int u = 0; u < 31; ++u) {
+            for (int u = 0; u < 15; ++u) {
                 const float t = acc[u];
 #pragma unroll
-                for (int g4 = (u + 1) >> 2; g4 < 8; ++g4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(Lb + u * LD + 4 * g4);
-                    const float lv[4] = {l.x, l.y, l.z, l.w};
+                for (int g4 = (u + 1) >> 2; g4 < 4; ++g4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(Lb + u * LD + 4 * g4);
+                    const float lv[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (4 * g4 + e > u) acc[4 * g4 + e] = fmaf(-lv[e], t, acc[4 * g4 + e]);
                 }
             }
-            if (warp == 0) {
+            // X00 by rows, X11 by columns; the upper lanes write the zeros above the diagonal
+            const int o = 16 * (warp & 1);
+            if (warp < 2) {
+                if (lane < 16) {
 #pragma unroll
-                for (int u = 0; u < 32; ++u) T00f[u * LDT + lane] = acc[u];
+                    for (int u = 0; u < 16; ++u) X00[(o + u) * LDT + o + l] = acc[u];
+                } else if (warp == 0) {
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) X00[u * LDT + 16 + l] = 0.f;
+                }
             } else {
+                if (lane < 16) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    *reinterpret_cast<float4 *>(T11t + lane * LDT + 4 * m) =
-                        make_float4(acc[4 * m], acc[4 * m + 1], acc[4 * m + 2], acc[4 * m + 3]);
+                    for (int m = 0; m < 4; ++m)
+                        *reinterpret_cast<float4 *>(X11t + (o + l) * LDT + o + 4 * m) = make_float4(acc[4 * m], acc[4 * m + 1], acc[4 * m + 2], acc[4 * m + 3]);
+                } else if (warp == 2) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) *reinterpret_cast<float4 *>(X11t + (16 + l) * LDT + 4 * m) = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
             }
         }
         __syncthreads();
-        // both substitutions are done: X00 and X11 into the images (over Lt's last rows), and zeros above the diagonal
-        if (warp < 2) {
+        // The blocks of 16 below them: 64 threads per 32-block, 2 x 2 elements each.
+        {
+            const int k2 = tid >> 6, r2 = 2 * ((tid >> 3) & 7), c2 = 2 * (tid & 7);
+            float *M = M16 + k2 * 16 * LDS16;
+            const float *Lo = Lt + 32 * k2 * LD + 32 * k2 + 16 + r2;
+            float m00 = 0.f, m01 = 0.f, m10 = 0.f, m11 = 0.f;
 #pragma unroll
-            for (int u = 0; u < 32; ++u) put_x(base, 32 * warp + u, 32 * warp + lane, acc[u]);
-        } else {
-            const int i = tid - 64;   // rows 0..31 of the images, two of their upper 16-byte chunks each
+            for (int u = 0; u < 16; ++u) {
+                const float2 lv = *reinterpret_cast<const float2 *>(Lo + u * LD);
+                float x0, x1;
+                if (k2 == 0) {
+                    const float2 xv = *reinterpret_cast<const float2 *>(X00 + u * LDT + c2);
+                    x0 = xv.x, x1 = xv.y;
+                } else {
+                    x0 = X11t[c2 * LDT + u], x1 = X11t[(c2 + 1) * LDT + u];
+                }
+                m00 = fmaf(lv.x, x0, m00), m01 = fmaf(lv.x, x1, m01), m10 = fmaf(lv.y, x0, m10), m11 = fmaf(lv.y, x1, m11);
+            }
+            *reinterpret_cast<float2 *>(M + r2 * LDS16 + c2) = make_float2(m00, m01);
+            *reinterpret_cast<float2 *>(M + (r2 + 1) * LDS16 + c2) = make_float2(m10, m11);
+            __syncthreads();
+            m00 = m01 = m10 = m11 = 0.f;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t o = sw128_offset(i >> 1, 4 + 2 * (i & 1) + x);
-                *reinterpret_cast<uint4 *>(base + kPXh + o) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(base + kPXl + o) = make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < 16; ++u) {
+                const float2 mv = *reinterpret_cast<const float2 *>(M + u * LDS16 + c2);
+                float x0, x1;
+                if (k2 == 0) {
+                    x0 = X00[(16 + r2) * LDT + 16 + u], x1 = X00[(17 + r2) * LDT + 16 + u];
+                } else {
+                    const float2 xv = *reinterpret_cast<const float2 *>(X11t + (16 + u) * LDT + 16 + r2);
+                    x0 = xv.x, x1 = xv.y;
+                }
+                m00 = fmaf(-x0, mv.x, m00), m01 = fmaf(-x0, mv.y, m01), m10 = fmaf(-x1, mv.x, m10), m11 = fmaf(-x1, mv.y, m11);
+            }
+            if (k2 == 0) {
+                *reinterpret_cast<float2 *>(X00 + (16 + r2) * LDT + c2) = make_float2(m00, m01);
+                *reinterpret_cast<float2 *>(X00 + (17 + r2) * LDT + c2) = make_float2(m10, m11);
+            } else {
+                *reinterpret_cast<float2 *>(X11t + c2 * LDT + 16 + r2) = make_float2(m00, m10);
+                *reinterpret_cast<float2 *>(X11t + (c2 + 1) * LDT + 16 + r2) = make_float2(m01, m11);
             }
         }
+        __syncthreads();
         // M = L10 X00 and then X10 = -X11 M: thread (warp, lane) computes rows 4 rg .. 4 rg + 3 and columns 2 cp, 2 cp + 1,
         // rg = 2 warp + lane / 16
         const int rg = 2 * warp + (lane >> 4), cp = lane & 15;
@@ -354,7 +405,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             float2 m4[4] = {};
 #pragma unroll 8
             for (int u = 0; u < 32; ++u) {
-                const float2 tj = *reinterpret_cast<const float2 *>(T00f + u * LDT + 2 * cp);
+                const float2 tj = *reinterpret_cast<const float2 *>(X00 + u * LDT + 2 * cp);
                 const float4 g = *reinterpret_cast<const float4 *>(Lt + u * LD + 32 + 4 * rg);
                 const float gv[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
@@ -369,25 +420,35 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll 8
             for (int u = 0; u < 32; ++u) {
                 const float2 mj = *reinterpret_cast<const float2 *>(Mf + u * LDT + 2 * cp);
-                const float4 a = *reinterpret_cast<const float4 *>(T11t + u * LDT + 4 * rg);
+                const float4 a = *reinterpret_cast<const float4 *>(X11t + u * LDT + 4 * rg);
                 const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o4[e] = __ffma2_rn(make_float2(av[e], av[e]), mj, o4[e]);
+                for (int e = 0; e < 4; ++e) o4[e] = __ffma2_rn(make_float2(-av[e], -av[e]), mj, o4[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t hi, lo;
-                split2(-o4[e].x, -o4[e].y, hi, lo);
-                const uint32_t o = tile_off(32 + 4 * rg + e, 2 * cp);
-                *reinterpret_cast<uint32_t *>(base + kPXh + o) = hi;
-                *reinterpret_cast<uint32_t *>(base + kPXl + o) = lo;
-            }
+            for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(X10 + (4 * rg + e) * LDT + 2 * cp) = o4[e];
         }
         __syncthreads();
-        uint4 *dst = reinterpret_cast<uint4 *>(wsc + kWsX);
-        for (int x = tid; x < (int)(kTile / 16); x += kPThreads) {
-            dst[x] = reinterpret_cast<const uint4 *>(base + kPXh)[x];
-            dst[x + kTile / 16] = reinterpret_cast<const uint4 *>(base + kPXl)[x];
+        // X's two parts, 16-byte words of the images' rows
+        uint8_t *xi = wsc + kWsX;
+#pragma unroll 1
+        for (int x = tid; x < 8 * kC; x += kPThreads) {
+            const int row = x >> 3, w = x & 7, r = row & 31, c8 = 8 * (w & 3);
+            float v[8] = {};
+            if (w < 4) {
+                const float *from = (row < 32 ? X00 : X10) + r * LDT + c8;
+                const float4 u0 = *reinterpret_cast<const float4 *>(from), u1 = *reinterpret_cast<const float4 *>(from + 4);
+                v[0] = u0.x, v[1] = u0.y, v[2] = u0.z, v[3] = u0.w, v[4] = u1.x, v[5] = u1.y, v[6] = u1.z, v[7] = u1.w;
+            } else if (row >= 32) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = X11t[(c8 + e) * LDT + r];
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(make_float2(v[2 * e], v[2 * e + 1]), hi[e], lo[e]);
+            const uint32_t o = sw128_offset(row, w);
+            *reinterpret_cast<uint4 *>(xi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(xi + kTile + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     } else {
         // gave up waiting: the copy and the MMAs already started complete before the CTA exits

@@ -40,13 +40,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// x0, x1 as a high and a low BF16 part each
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
-{
-    hi = pack_bf16x2(x0, x1);
-    lo = pack_bf16x2(x0 - bf16_lo(hi), x1 - bf16_hi(hi));
-}
-
 // The sequence and the chunks of a CTA.
 struct Span {
     int T;            // tokens of the sequence
