@@ -29,14 +29,14 @@ template <int KD>
 constexpr uint32_t kStateImg = KD / 64 * kImg;   // a part of S or dS: [value column][state row] by blocks of 64 rows
 
 // ----------------------------------------------------------------- the chains
-// Roles as in gdelta_chain_kernel: the third warpgroup brings V (backwards: scale e^G dY, in two parts) to its lanes and takes
-// S (dS) of every chunk to memory, the fourth takes E (N, and dv).
-constexpr int kOwners = 8, kHelpers = 4, kBringer = 8, kTaker = 12, kIssuer = 16, kLoader = 17;
-constexpr int kThreads = 640;
+// Roles as in gdelta_chain_kernel: the fifth warpgroup brings V (backwards: scale e^G dY, in two parts) to its lanes and takes
+// S (dS) of every chunk to memory, the sixth takes E (N, and dv).
+constexpr int kOwners = 16, kHelpers = 4, kBringer = 16, kTaker = 20, kIssuer = 24, kLoader = 25;
+constexpr int kThreads = 896;
 constexpr int kGateRing = 4;
 constexpr uint32_t kGateStep = 2048;
-// registers per thread after the split (launched with 96): 2 x 136 + 56 + 96 + 56 = 5 x 96
-constexpr int kRegsOwn = 136, kRegsBring = 56, kRegsRest = 56;
+// registers per thread after the split (launched with 72): 4 x 80 + 56 + 72 + 56 = 7 x 72
+constexpr int kRegsOwn = 80, kRegsBring = 56, kRegsRest = 56;
 
 template <int KD, bool REV>
 struct BackCfg {
@@ -75,7 +75,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ GdeltaTcBackArgs args)
 {
     using Cfg = BackCfg<KD, REV>;
-    constexpr int KH = KD / 2;
+    constexpr int KH = KD / 2, KQ = KD / 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = align1024(smem_raw);
     BSmall *sm = reinterpret_cast<BSmall *>(base + Cfg::kSmall);
@@ -259,17 +259,15 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             if (ok) {
                 tc_fence_after();
                 uint8_t *img = (REV ? args.N : args.E) + (bh * nch + c) * kTokImg;
-                // (all of it at once: the issuer waits for its columns)
-                float e4[4][16];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) tc_ld_32x32b_x16(tq + kcE + 16 * x, e4[x]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) wait_loaded(e4[x]);
-                tc_fence_before();
-                bar_arrive_warp(BBAR(e_read, 0));
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 4; ++x) {
-                    const float (&e)[16] = e4[x];
+                    float e[16];
+                    tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
+                    wait_loaded(e);
+                    if (x == 3) {
+                        tc_fence_before();
+                        bar_arrive_warp(BBAR(e_read, 0));
+                    }
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
@@ -374,15 +372,15 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         tc_fence_before();
     } else {
         regs_inc<kRegsOwn>();
-        const int q4 = warp & 3, ch = warp >> 2, d = 32 * q4 + lane;
+        const int q4 = warp & 3, cq = warp >> 2, ch = cq >> 1, d = 32 * q4 + lane;
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
         const bool live = d < dv;
         const float scale = args.scale;
         const float *S_init = REV ? args.dS_T : args.S0;
-        float2 S[KH / 2];                               // S[i]: state rows KH ch + 2 i, + 1 of the lane's column
-        const size_t s_at = (bh * KD + KH * ch) * dv + d;
+        float2 S[KQ / 2];                               // S[i]: state rows KQ cq + 2 i, + 1 of the lane's column
+        const size_t s_at = (bh * KD + KQ * cq) * dv + d;
 #pragma unroll
-        for (int i = 0; i < KH / 2; ++i) {
+        for (int i = 0; i < KQ / 2; ++i) {
             S[i] = make_float2(0.f, 0.f);
             if (S_init && live) S[i] = make_float2(S_init[s_at + (size_t)(2 * i) * dv], S_init[s_at + (size_t)(2 * i + 1) * dv]);
         }
@@ -390,8 +388,8 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) split(v[i], hi[i], lo[i]);
-            tm_st8(tq + kcS + KH / 2 * ch + 8 * x, hi);
-            tm_st8(tq + kcS + KH + KH / 2 * ch + 8 * x, lo);
+            tm_st8(tq + kcS + KQ / 2 * cq + 8 * x, hi);
+            tm_st8(tq + kcS + KH + KQ / 2 * cq + 8 * x, lo);
         };
         auto stored = [&](uint32_t bar) {
             tc_wait_st();
@@ -399,50 +397,43 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             bar_arrive_warp(bar);
         };
 #pragma unroll
-        for (int x = 0; x < KH / 16; ++x) put_s(x, S + 8 * x);
+        for (int x = 0; x < KQ / 16; ++x) put_s(x, S + 8 * x);
         stored(BBAR(got_s, ch));
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
-            const uint32_t ph = n & 1, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
+            const uint32_t ph = n & 1, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep + 64 * cq;
             // R^T = V^T - e^G P^T; backwards beta D^T = beta (scale (A^T dY)^T + e^{G_C - G} P^T)
             ok = waitw(BBAR(full, n & 1), (n >> 1) & 1) && waitw(REV ? BBAR(done0, 0) : BBAR(got_v, 0), ph) && waitw(BBAR(done1, ch), ph);
             if (!ok) break;
             tc_fence_after();
             {
-                float p[2][16], v[2][REV ? 16 : 8];
+                float p[16], v[REV ? 16 : 8];
+                tc_ld_32x32b_x16(tq + kcP + 16 * cq, p);
+                if constexpr (REV) tc_ld_32x32b_x16(tq + kcA + 16 * cq, v);
+                else tm_ld8(tq + kcV + 8 * cq, v);
+                wait_loaded(p);
+                wait_loaded(v);
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    tc_ld_32x32b_x16(tq + kcP + 32 * ch + 16 * y, p[y]);
-                    if constexpr (REV) tc_ld_32x32b_x16(tq + kcA + 32 * ch + 16 * y, v[y]);
-                    else tm_ld8(tq + kcV + 16 * ch + 8 * y, v[y]);
-                }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    wait_loaded(p[y]);
-                    wait_loaded(v[y]);
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 p0 = make_float2(p[y][4 * i], p[y][4 * i + 1]), p1 = make_float2(p[y][4 * i + 2], p[y][4 * i + 3]);
-                        const uint32_t ga = gates + 128 * ch + 64 * y + 16 * i;
-                        float2 r0, r1;
-                        if constexpr (REV) {
-                            const float4 er = lds_f4(ga + 4 * kC), be = lds_f4(ga + 8 * kC);
-                            const float2 sc = make_float2(scale, scale);
-                            r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(sc, make_float2(v[y][4 * i], v[y][4 * i + 1]), __fmul2_rn(make_float2(er.x, er.y), p0)));
-                            r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(sc, make_float2(v[y][4 * i + 2], v[y][4 * i + 3]), __fmul2_rn(make_float2(er.z, er.w), p1)));
-                        } else {
-                            const float4 g = lds_f4(ga);
-                            r0 = __ffma2_rn(make_float2(-g.x, -g.y), p0, unpack(__float_as_uint(v[y][2 * i])));
-                            r1 = __ffma2_rn(make_float2(-g.z, -g.w), p1, unpack(__float_as_uint(v[y][2 * i + 1])));
-                        }
-                        split(r0, hi[2 * i], lo[2 * i]);
-                        split(r1, hi[2 * i + 1], lo[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p0 = make_float2(p[4 * i], p[4 * i + 1]), p1 = make_float2(p[4 * i + 2], p[4 * i + 3]);
+                    float2 r0, r1;
+                    if constexpr (REV) {
+                        const float4 er = lds_f4(gates + 4 * kC + 16 * i), be = lds_f4(gates + 8 * kC + 16 * i);
+                        const float2 sc = make_float2(scale, scale);
+                        r0 = __fmul2_rn(make_float2(be.x, be.y), __ffma2_rn(sc, make_float2(v[4 * i], v[4 * i + 1]), __fmul2_rn(make_float2(er.x, er.y), p0)));
+                        r1 = __fmul2_rn(make_float2(be.z, be.w), __ffma2_rn(sc, make_float2(v[4 * i + 2], v[4 * i + 3]), __fmul2_rn(make_float2(er.z, er.w), p1)));
+                    } else {
+                        const float4 g = lds_f4(gates + 16 * i);
+                        r0 = __ffma2_rn(make_float2(-g.x, -g.y), p0, unpack(__float_as_uint(v[2 * i])));
+                        r1 = __ffma2_rn(make_float2(-g.z, -g.w), p1, unpack(__float_as_uint(v[2 * i + 1])));
                     }
-                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
-                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
+                    split(r0, hi[2 * i], lo[2 * i]);
+                    split(r1, hi[2 * i + 1], lo[2 * i + 1]);
                 }
+                tm_st8(tq + kcR + 8 * cq, hi);
+                tm_st8(tq + kcR + 32 + 8 * cq, lo);
             }
             stored(BBAR(got_r, ch));
             // beta e^{G_C - G} E^T; backwards -e^G N^T
@@ -450,50 +441,46 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             if (!ok) break;
             tc_fence_after();
             {
-                float e[2][16];
+                float e[16];
+                tc_ld_32x32b_x16(tq + kcE + 16 * cq, e);
+                wait_loaded(e);
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) tc_ld_32x32b_x16(tq + kcE + 32 * ch + 16 * y, e[y]);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    wait_loaded(e[y]);
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t ga = gates + 128 * ch + 64 * y + 16 * i;
-                        const float4 g = lds_f4(ga + (REV ? 0 : 4 * kC));
-                        float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
-                        if (!REV) f = lds_f4(ga + 8 * kC);
-                        split(__fmul2_rn(make_float2(g.x, g.y), __fmul2_rn(make_float2(f.x, f.y), make_float2(e[y][4 * i], e[y][4 * i + 1]))),
-                              hi[2 * i], lo[2 * i]);
-                        split(__fmul2_rn(make_float2(g.z, g.w), __fmul2_rn(make_float2(f.z, f.w), make_float2(e[y][4 * i + 2], e[y][4 * i + 3]))),
-                              hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
-                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = lds_f4(gates + (REV ? 0 : 4 * kC) + 16 * i);
+                    float4 f = make_float4(-1.f, -1.f, -1.f, -1.f);
+                    if (!REV) f = lds_f4(gates + 8 * kC + 16 * i);
+                    split(__fmul2_rn(make_float2(g.x, g.y), __fmul2_rn(make_float2(f.x, f.y), make_float2(e[4 * i], e[4 * i + 1]))),
+                          hi[2 * i], lo[2 * i]);
+                    split(__fmul2_rn(make_float2(g.z, g.w), __fmul2_rn(make_float2(f.z, f.w), make_float2(e[4 * i + 2], e[4 * i + 3]))),
+                          hi[2 * i + 1], lo[2 * i + 1]);
                 }
+                tm_st8(tq + kcR + 8 * cq, hi);
+                tm_st8(tq + kcR + 32 + 8 * cq, lo);
             }
             stored(BBAR(got_w, ch));
-            const float gC = ldsf(gates + 4 * (kC - 1));
-            // (the helpers have read S of this chunk before it makes room for the next one's)
+            const float gC = ldsf(gates - 64 * cq + 4 * (kC - 1));
+            // (the bringers have read S of this chunk before it makes room for the next one's)
             ok = waitw(BBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1) && waitw(BBAR(s_read, 0), ph);
             if (!ok) break;
             tc_fence_after();
-            float ds[2][16];
-            tc_ld_32x32b_x16(tq + kcP + 64 * ch, ds[0]);
+            // (the accumulators of the halves are 64 columns apart)
+            const uint32_t from = tq + kcP + 64 * ch + KQ * (cq & 1);
 #pragma unroll
-            for (int x = 0; x < KH / 16; ++x) {
-                wait_loaded(ds[x & 1]);
-                if (x + 1 < KH / 16) tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * (x + 1), ds[(x + 1) & 1]);
+            for (int x = 0; x < KQ / 16; ++x) {
+                float ds[16];
+                tc_ld_32x32b_x16(from + 16 * x, ds);
+                wait_loaded(ds);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[x & 1][2 * i], ds[x & 1][2 * i + 1]));
+                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
                 put_s(x, S + 8 * x);
             }
             stored(BBAR(got_s, ch));
         }
         if (REV && ok && live) {
 #pragma unroll
-            for (int i = 0; i < KH / 2; ++i) {
+            for (int i = 0; i < KQ / 2; ++i) {
                 args.dS0[s_at + (size_t)(2 * i) * dv] = S[i].x;
                 args.dS0[s_at + (size_t)(2 * i + 1) * dv] = S[i].y;
             }

@@ -464,15 +464,15 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 }
 
 // ------------------------------------------------------------------ the chain
-// Five warpgroups: 0 and 1 own the state (warp w: TMEM lanes 32 (w % 4) .., half w / 4 of the tokens in steps 1 and 2 and of
-// the state's rows in step 3), 2 (a lane quadrant per warp) brings V's columns to their lanes, 3 takes y from them to memory, and in
-// 4 one warp issues the MMAs and one loads.  The halves run staggered: the second one's products overlap the first one's
+// Seven warpgroups: 0 to 3 own the state (warp w: TMEM lanes 32 (w % 4) .., quarter w / 4 of the tokens in steps 1 and 2 and of
+// the state's rows in step 3), 4 (a lane quadrant per warp) brings V's columns to their lanes, 5 takes y from them to memory, and in
+// 6 one warp issues the MMAs and one loads.  The two halves run staggered: the second one's products overlap the first one's
 // conversions.
-constexpr int kOwners = 8, kHelpers = 4, kBringer = 8, kTaker = 12, kIssuer = 16, kLoader = 17;
-constexpr int kMThreads = 640;
+constexpr int kOwners = 16, kHelpers = 4, kBringer = 16, kTaker = 20, kIssuer = 24, kLoader = 25;
+constexpr int kMThreads = 896;
 constexpr int kGateRing = 4;
-// registers per thread after the split (launched with 96): 2 x 144 + 56 + 80 + 56 = 5 x 96
-constexpr int kRegsOwn = 144, kRegsBring = 56, kRegsTake = 80, kRegsRest = 56;
+// registers per thread after the split (launched with 72): 4 x 88 + 48 + 56 + 48 = 7 x 72
+constexpr int kRegsOwn = 88, kRegsBring = 48, kRegsTake = 56, kRegsRest = 48;
 template <int KD>
 struct ChainCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;    // a K or Q tile (64-feature blocks)
@@ -511,7 +511,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ GdeltaTcArgs args)
 {
     using Cfg = ChainCfg<KD>;
-    constexpr int KH = KD / 2;                  // state rows per owner thread (a thread has a column, half its rows)
+    constexpr int KH = KD / 2, KQ = KD / 4;     // half of the state's rows; an owner thread has a column, a quarter of its rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = align1024(smem_raw);
     MSmall *sm = reinterpret_cast<MSmall *>(base + Cfg::kSmall);
@@ -697,23 +697,17 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 tc_fence_after();
                 const uint32_t eg = s0 + Cfg::kGates + (n % kGateRing) * 1024;
 #pragma unroll 1
-                for (int x = 0; x < 4; ++x) {
-                    float qs[16], av[16];
-                    tc_ld_32x32b_x16(tq + kcQS + 16 * x, qs);
-                    tc_ld_32x32b_x16(tq + kcAV + 16 * x, av);
+                for (int x = 0; x < 8; ++x) {
+                    float qs[8], av[8];
+                    tm_ld8(tq + kcQS + 8 * x, qs);
+                    tm_ld8(tq + kcAV + 8 * x, av);
+                    const float4 g0 = lds_f4(eg + 32 * x), g1 = lds_f4(eg + 32 * x + 16);
+                    const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
                     wait_loaded(qs);
                     wait_loaded(av);
-                    const uint32_t a = s0 + Cfg::kY + col + x * (16 * 128);
+                    const uint32_t a = s0 + Cfg::kY + col + x * (8 * 128);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 g = lds_f4(eg + 64 * x + 16 * i);
-                        const float f[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int t = 4 * i + u;
-                            sts_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4), pack_bf16x2(scale * fmaf(f[u], qs[t], av[t]), 0.f));
-                        }
-                    }
+                    for (int i = 0; i < 8; ++i) sts_u16(a + i * 128 + ((c16 ^ i) << 4), pack_bf16x2(scale * fmaf(g[i], qs[i], av[i]), 0.f));
                 }
                 tc_fence_before();
                 bar_arrive_warp(MBAR(y_read, 0));
@@ -775,23 +769,23 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         tc_fence_before();
     } else {
         regs_inc<kRegsOwn>();
-        const int q4 = warp & 3, ch = warp >> 2, d = 32 * q4 + lane;
+        const int q4 = warp & 3, cq = warp >> 2, ch = cq >> 1, d = 32 * q4 + lane;
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
         const bool live = d < ncols;
-        float2 S[KH / 2];                               // S[i]: state rows KH ch + 2 i, + 1 of the lane's column
-        const size_t s_at = (bh * KD + KH * ch) * dv + 128 * tile + d;
+        float2 S[KQ / 2];                               // S[i]: state rows KQ cq + 2 i, + 1 of the lane's column
+        const size_t s_at = (bh * KD + KQ * cq) * dv + 128 * tile + d;
 #pragma unroll
-        for (int i = 0; i < KH / 2; ++i) {
+        for (int i = 0; i < KQ / 2; ++i) {
             S[i] = make_float2(0.f, 0.f);
             if (args.S0 && live) S[i] = make_float2(args.S0[s_at + (size_t)(2 * i) * dv], args.S0[s_at + (size_t)(2 * i + 1) * dv]);
         }
-        // rows 16 x .. of this half as left operands
+        // rows 16 x .. of this quarter as left operands
         auto put_s = [&](int x, const float2 *v) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) split(v[i], hi[i], lo[i]);
-            tm_st8(tq + kcS + KH / 2 * ch + 8 * x, hi);
-            tm_st8(tq + kcS + KH + KH / 2 * ch + 8 * x, lo);
+            tm_st8(tq + kcS + KQ / 2 * cq + 8 * x, hi);
+            tm_st8(tq + kcS + KH + KQ / 2 * cq + 8 * x, lo);
         };
         auto stored = [&](uint32_t bar) {
             tc_wait_st();
@@ -800,41 +794,35 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         };
         if (nch > 0) {
 #pragma unroll
-            for (int x = 0; x < KH / 16; ++x) put_s(x, S + 8 * x);
+            for (int x = 0; x < KQ / 16; ++x) put_s(x, S + 8 * x);
             stored(MBAR(got_s, ch));
         }
         bool ok = true;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
-            const uint32_t ph = n & 1, gates = s0 + Cfg::kGates + (n % kGateRing) * 1024;
-            // R^T = V^T - e^G P^T, tokens 32 ch ..  (past the sequence's end V and P are 0)
+            const uint32_t ph = n & 1, gates = s0 + Cfg::kGates + (n % kGateRing) * 1024 + 64 * cq;
+            // R^T = V^T - e^G P^T, tokens 16 cq ..  (past the sequence's end V and P are 0)
             ok = waitw(MBAR(full_vx, n & 1), (n >> 1) & 1) && waitw(MBAR(got_v, 0), ph) && waitw(MBAR(done1, ch), ph);
             if (!ok) break;
             tc_fence_after();
             {
-                float p[2][16], v[2][8];
+                float p[16], v[8];
+                tc_ld_32x32b_x16(tq + kcP + 16 * cq, p);
+                tm_ld8(tq + kcV + 8 * cq, v);
+                wait_loaded(p);
+                wait_loaded(v);
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    tc_ld_32x32b_x16(tq + kcP + 32 * ch + 16 * y, p[y]);
-                    tm_ld8(tq + kcV + 16 * ch + 8 * y, v[y]);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = lds_f4(gates + 16 * i);
+                    const uint32_t v0 = __float_as_uint(v[2 * i]), v1 = __float_as_uint(v[2 * i + 1]);
+                    split(__ffma2_rn(make_float2(-g.x, -g.y), make_float2(p[4 * i], p[4 * i + 1]), make_float2(bf16_lo(v0), bf16_hi(v0))),
+                          hi[2 * i], lo[2 * i]);
+                    split(__ffma2_rn(make_float2(-g.z, -g.w), make_float2(p[4 * i + 2], p[4 * i + 3]), make_float2(bf16_lo(v1), bf16_hi(v1))),
+                          hi[2 * i + 1], lo[2 * i + 1]);
                 }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    wait_loaded(p[y]);
-                    wait_loaded(v[y]);
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 g = lds_f4(gates + 128 * ch + 64 * y + 16 * i);
-                        const uint32_t v0 = __float_as_uint(v[y][2 * i]), v1 = __float_as_uint(v[y][2 * i + 1]);
-                        split(__ffma2_rn(make_float2(-g.x, -g.y), make_float2(p[y][4 * i], p[y][4 * i + 1]), make_float2(bf16_lo(v0), bf16_hi(v0))),
-                              hi[2 * i], lo[2 * i]);
-                        split(__ffma2_rn(make_float2(-g.z, -g.w), make_float2(p[y][4 * i + 2], p[y][4 * i + 3]), make_float2(bf16_lo(v1), bf16_hi(v1))),
-                              hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
-                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
-                }
+                tm_st8(tq + kcR + 8 * cq, hi);
+                tm_st8(tq + kcR + 32 + 8 * cq, lo);
             }
             stored(MBAR(got_r, ch));
             // V'^T = beta E^T, and decayed to the chunk's end
@@ -842,50 +830,46 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             if (!ok) break;
             tc_fence_after();
             {
-                float e[2][16];
+                float e[16];
+                tc_ld_32x32b_x16(tq + kcE + 16 * cq, e);
+                wait_loaded(e);
+                uint32_t w[8], hi[8], lo[8];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) tc_ld_32x32b_x16(tq + kcE + 32 * ch + 16 * y, e[y]);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    wait_loaded(e[y]);
-                    uint32_t w[8], hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t g = gates + 128 * ch + 64 * y + 16 * i;
-                        const float4 er = lds_f4(g + 4 * kC), be = lds_f4(g + 8 * kC);
-                        const float2 w0 = __fmul2_rn(make_float2(be.x, be.y), make_float2(e[y][4 * i], e[y][4 * i + 1]));
-                        const float2 w1 = __fmul2_rn(make_float2(be.z, be.w), make_float2(e[y][4 * i + 2], e[y][4 * i + 3]));
-                        w[2 * i] = pack_bf16x2(w0.x, w0.y);
-                        w[2 * i + 1] = pack_bf16x2(w1.x, w1.y);
-                        split(__fmul2_rn(make_float2(er.x, er.y), w0), hi[2 * i], lo[2 * i]);
-                        split(__fmul2_rn(make_float2(er.z, er.w), w1), hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    tm_st8(tq + kcR + 16 * ch + 8 * y, hi);
-                    tm_st8(tq + kcR + 32 + 16 * ch + 8 * y, lo);
-                    tm_st8(tq + kcW + 16 * ch + 8 * y, w);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 er = lds_f4(gates + 4 * kC + 16 * i), be = lds_f4(gates + 8 * kC + 16 * i);
+                    const float2 w0 = __fmul2_rn(make_float2(be.x, be.y), make_float2(e[4 * i], e[4 * i + 1]));
+                    const float2 w1 = __fmul2_rn(make_float2(be.z, be.w), make_float2(e[4 * i + 2], e[4 * i + 3]));
+                    w[2 * i] = pack_bf16x2(w0.x, w0.y);
+                    w[2 * i + 1] = pack_bf16x2(w1.x, w1.y);
+                    split(__fmul2_rn(make_float2(er.x, er.y), w0), hi[2 * i], lo[2 * i]);
+                    split(__fmul2_rn(make_float2(er.z, er.w), w1), hi[2 * i + 1], lo[2 * i + 1]);
                 }
+                tm_st8(tq + kcR + 8 * cq, hi);
+                tm_st8(tq + kcR + 32 + 8 * cq, lo);
+                tm_st8(tq + kcW + 8 * cq, w);
             }
             stored(MBAR(got_w, ch));
-            const float gC = ldsf(gates + 4 * (kC - 1));
+            const float gC = ldsf(gates - 64 * cq + 4 * (kC - 1));
             ok = waitw(MBAR(done3, 2 * ch + (n & 1)), (n >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            float ds[2][16];
-            tc_ld_32x32b_x16(tq + kcP + 64 * ch, ds[0]);
+            // (the accumulators of the halves are 64 columns apart)
+            const uint32_t from = tq + kcP + 64 * ch + KQ * (cq & 1);
 #pragma unroll
-            for (int x = 0; x < KH / 16; ++x) {
-                wait_loaded(ds[x & 1]);
-                if (x + 1 < KH / 16) tc_ld_32x32b_x16(tq + kcP + 64 * ch + 16 * (x + 1), ds[(x + 1) & 1]);
+            for (int x = 0; x < KQ / 16; ++x) {
+                float ds[16];
+                tc_ld_32x32b_x16(from + 16 * x, ds);
+                wait_loaded(ds);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[x & 1][2 * i], ds[x & 1][2 * i + 1]));
+                    S[8 * x + i] = __ffma2_rn(make_float2(gC, gC), S[8 * x + i], make_float2(ds[2 * i], ds[2 * i + 1]));
                 if (n + 1 < nch) put_s(x, S + 8 * x);
             }
             if (n + 1 < nch) stored(MBAR(got_s, ch));
         }
         if (ok && live) {
 #pragma unroll
-            for (int i = 0; i < KH / 2; ++i) {
+            for (int i = 0; i < KQ / 2; ++i) {
                 args.S_out[s_at + (size_t)(2 * i) * dv] = S[i].x;
                 args.S_out[s_at + (size_t)(2 * i + 1) * dv] = S[i].y;
             }
