@@ -29,33 +29,34 @@ template <int KD>
 constexpr uint32_t kStateImg = KD / 64 * kImg;   // a part of S or dS: [value column][state row] by blocks of 64 rows
 
 // ----------------------------------------------------------------- the chains
-// Roles as in gdelta_chain_kernel: the fifth warpgroup brings V (backwards: scale e^G dY, in two parts) to its lanes and takes
-// S (dS) of every chunk to memory, the sixth takes E (N, and dv).
+// Roles as in gdelta_chain_kernel: the fifth warpgroup brings V to its lanes (forwards) and takes S (dS) of every
+// chunk to memory, the sixth takes E (N, and dv).
 constexpr int kOwners = 16, kHelpers = 4, kBringer = 16, kTaker = 20, kIssuer = 24, kLoader = 25;
 constexpr int kThreads = 896;
 constexpr int kGateRing = 4;
 constexpr uint32_t kGateStep = 2048;
-// registers per thread after the split (launched with 72): 4 x 80 + 56 + 72 + 56 = 7 x 72
-constexpr int kRegsOwn = 80, kRegsBring = 56, kRegsRest = 56;
+// registers per thread after the split (launched with 72): 4 x 80 + 48 + 88 + 48 = 7 x 72
+constexpr int kRegsOwn = 80, kRegsBring = 48, kRegsTake = 88, kRegsRest = 48;
 
 template <int KD, bool REV>
 struct BackCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;
-    // a stage (two): K, V or dY (two blocks of 64 columns), X's parts; backwards also Q and A's parts
-    static constexpr uint32_t kSK = 0, kSV = kTK, kSX = kSV + 2 * kTile, kSQ = kSX + 2 * kTile, kSA = kSQ + kTK,
-                              kStage = REV ? kSA + 2 * kTile : kSQ;
-    // dv of a chunk (two blocks of 64 columns)
+    // a stage (two): K, V or dY (two blocks of 64 columns), X's parts; backwards also A's parts and scale e^G Q's
+    static constexpr uint32_t kSK = 0, kSV = kTK, kSX = kSV + 2 * kTile, kSA = kSX + 2 * kTile, kSQ = kSA + 2 * kTile,
+                              kStage = REV ? kSQ + 2 * kTK : kSA;
+    // dv of a chunk (4 KB per warp that takes it)
     static constexpr uint32_t kOutV = 2 * kStage, kGates = kOutV + (REV ? 2 * kTile : 0), kSmall = kGates + kGateRing * kGateStep;
 };
-// TMEM columns: S^T (two parts), P^T and E^T (then dS^T), (A^T dY)^T, the scaled dY^T (two parts), R^T (two parts, then the decayed
-// V'^T's, or the scaled N^T's), V^T
-constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcA = 256, kcY = 320, kcR = 384, kcV = 448;
+// TMEM columns: S^T (two parts), P^T and E^T (then dS^T), (A^T dY)^T, R^T (two parts, then the decayed V'^T's, or the scaled
+// N^T's), V^T
+constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcA = 256, kcR = 320, kcV = 384;
 
 struct alignas(16) BSmall {
     uint64_t full[2];
     uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (4 warps)
-    uint64_t got_v, s_read, e_read;          // V^T (dY^T) is there, S has been read (the bringers); E has (the takers)
+    uint64_t got_v, s_read, e_read;          // V^T is there, S has been read (the bringers); E has (the takers)
     uint64_t done0, done1[2], done2[2];      // A^T dY, halves of P, E
+    uint64_t done2b;                         // the half of R that comes first has been read
     uint64_t done3[4];                       // halves of dS of even and odd chunks
     uint64_t fin;
     uint32_t tmem_base;
@@ -114,7 +115,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 const int c = chunk(n);
                 const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
                 if (n >= 2 && !wait1(BBAR(done3, 2 + (n & 1)), ((n >> 1) - 1) & 1)) break;
-                bar_expect(bar, (REV ? 2 : 1) * Cfg::kTK + dv / 64 * kTile + (REV ? 4 : 2) * kTile + kGateBytesB);
+                bar_expect(bar, (REV ? 3 : 1) * Cfg::kTK + dv / 64 * kTile + (REV ? 4 : 2) * kTile + kGateBytesB);
 #pragma unroll 1
                 for (int x = 0; x < KD / 64; ++x) tma_load(st + Cfg::kSK + x * kTile, &map_k, bar, 64 * x, c * kC, kh);
 #pragma unroll 1
@@ -122,8 +123,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 bulk_copy(s0 + Cfg::kGates + (n % kGateRing) * kGateStep, w + kWsGates, kGateBytesB, bar);
                 bulk_copy(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
                 if (REV) {
-#pragma unroll 1
-                    for (int x = 0; x < KD / 64; ++x) tma_load(st + Cfg::kSQ + x * kTile, &map_q, bar, 64 * x, c * kC, kh);
+                    bulk_copy(st + Cfg::kSQ, w + kWsQ, 2 * Cfg::kTK, bar);
                     bulk_copy(st + Cfg::kSA, w + kWsA, kTile, bar);
                     bulk_copy(st + Cfg::kSA + kTile, w + kWsAl, kTile, bar);
                 }
@@ -135,7 +135,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         } else if (warp == kIssuer && elect_one()) {
             constexpr uint32_t id64 = idesc_bf16_f32(128, 64, false, false), id32 = idesc_bf16_f32(128, 32, false, REV),
                                idP = idesc_bf16_f32(128, 32, false, false), idS = idesc_bf16_f32(128, KH, false, true),
-                               idA = idesc_bf16_f32(128, 64, true, true);
+                               idA = idesc_bf16_f32(128, 64, true, true), idQ = idesc_bf16_f32(128, KH, true, true);
             constexpr uint32_t kHalfRows = (32 * 128) >> 4;
             // (A^T dY)^T = dY^T A, both parts of A
             auto mma_a = [&](int n) {
@@ -198,20 +198,24 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                             mma_ts(d, r + 32 + kk * 8, xo + kk * kStep, kHi128, id32, true);
                             mma_ts(d, r + kk * 8, xo + kk * kStep + (kTile >> 4), kHi128, id32, true);
                         }
+                        if (u + w == 0) bar_commit(BBAR(done2, t));
                     }
-                    bar_commit(BBAR(done2, t));
+                    bar_commit(u == 0 ? BBAR(done2b, 0) : BBAR(done2, t));
                 }
                 if (!ok) break;
-                // 3  dS^T = V'^T K; backwards (scale e^G dY)^T Q - (e^G N)^T K.  One half of the state's rows after the other
+                // 3  dS^T = V'^T K; backwards dY^T (scale e^G Q) - (e^G N)^T K.  One half of the state's rows after the other
                 // (the second one where E has been read)
-                const uint32_t kmn = desc_lo(st + Cfg::kSK, kTile), qmn = desc_lo(st + Cfg::kSQ, kTile);
-                if (REV) {
-                    if (!wait1(BBAR(got_v, 0), ph)) break;
-                    tc_fence_after();
+                const uint32_t kmn = desc_lo(st + Cfg::kSK, kTile);
+                auto mma_q = [&](int t) {                  // both parts of the scaled Q
+                    const uint32_t ylo = desc_lo(st + Cfg::kSV, kTile),
+                                   qmn = desc_lo(st + Cfg::kSQ, kTile) + t * ((KD == 128 ? kTile : 64u) >> 4);
 #pragma unroll 4
-                    for (int i = 0; i < 8; ++i)
-                        mma_ts(kcP, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
-                }
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t o = (i & 3) * (2048 >> 4);
+                        mma_ss(kcP + 64 * t, ylo + o, kHi128, qmn + (i >> 2) * (Cfg::kTK >> 4) + o, kHi128, idQ, i > 0);
+                    }
+                };
+                if (REV) mma_q(0);
                 if (!wait1(BBAR(got_w, 0), ph) || !wait1(BBAR(got_w, 1), ph)) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -221,11 +225,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                         ok = wait1(BBAR(e_read, 0), ph);
                         if (!ok) break;
                         tc_fence_after();
-                        if (REV) {
-#pragma unroll 4
-                            for (int i = 0; i < 8; ++i)
-                                mma_ts(kcP + 64, kcY + (i >> 2) * 32 + (i & 3) * 8, qmn + half + (i & 3) * (2048 >> 4), kHi128, idS, i > 0);
-                        }
+                        if (REV) mma_q(1);
                     }
 #pragma unroll 4
                     for (int i = 0; i < 8; ++i)
@@ -245,61 +245,56 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         }
         __syncwarp();
     } else if (warp >= kTaker) {
-        const int q4 = warp & 3, d = 32 * q4 + lane, ht = tid - 32 * kTaker;
-        const uint32_t tq = (uint32_t)(32 * q4) << 16;
-        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
-        // (a warp that gave up waiting still meets the others at their barriers)
-        bool ok = true;
+        regs_inc<kRegsTake>();
+        const int q4 = warp & 3, d = 32 * q4 + lane;
+        const uint32_t tq = (uint32_t)(32 * q4) << 16, buf = s0 + Cfg::kOutV + 4096 * q4;
+        const int out_col = 32 * q4 + 8 * (lane & 3), out_tok = lane >> 2;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
             const int c = chunk(n);
             const uint32_t gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
             // E, or N (the gates have been waited for by those whose products this waits for)
-            if (ok) ok = waitw(BBAR(done2, 0), n & 1) && waitw(BBAR(done2, 1), n & 1);
-            if (ok) {
-                tc_fence_after();
-                uint8_t *img = (REV ? args.N : args.E) + (bh * nch + c) * kTokImg;
-#pragma unroll 1
-                for (int x = 0; x < 4; ++x) {
-                    float e[16];
-                    tc_ld_32x32b_x16(tq + kcE + 16 * x, e);
-                    wait_loaded(e);
-                    if (x == 3) {
-                        tc_fence_before();
-                        bar_arrive_warp(BBAR(e_read, 0));
+            if (!waitw(BBAR(done2, 0), n & 1) || !waitw(BBAR(done2, 1), n & 1)) break;
+            tc_fence_after();
+            uint8_t *img = (REV ? args.N : args.E) + (bh * nch + c) * kTokImg;
+            // (all of it at once: the issuer waits for its columns)
+            float e4[4][16];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tc_ld_32x32b_x16(tq + kcE + 16 * x, e4[x]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) wait_loaded(e4[x]);
+            tc_fence_before();
+            bar_arrive_warp(BBAR(e_read, 0));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float (&e)[16] = e4[x];
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
+                st_row16(img, d, x, hi);
+                st_row16(img + kImg, d, x, lo);
+                if (REV) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 g = lds_f4(gates + kGateRatio + 64 * x + 16 * i);
+                        w[2 * i] = pack_bf16x2(g.x * e[4 * i], g.y * e[4 * i + 1]);
+                        w[2 * i + 1] = pack_bf16x2(g.z * e[4 * i + 2], g.w * e[4 * i + 3]);
                     }
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
-                    st_row16(img, d, x, hi);
-                    st_row16(img + kImg, d, x, lo);
-                    if (REV) {
-                        const uint32_t a = s0 + Cfg::kOutV + col + x * (16 * 128);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 g = lds_f4(gates + kGateRatio + 64 * x + 16 * i);
-                            const float f[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int t = 4 * i + u;
-                                sts_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4), pack_bf16x2(e[t] * f[u], 0.f));
-                            }
-                        }
-                    }
+                    cols_put(buf, lane, 2 * x, w[0], w[1], w[2], w[3]);
+                    cols_put(buf, lane, 2 * x + 1, w[4], w[5], w[6], w[7]);
                 }
             }
             if (!REV) continue;
-            named_barrier_sync(1, 32 * kHelpers);
-            if (ok) {
-                const int per = dv / 8, rows = min(kC, T - c * kC);
-                uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC) * dv;
+            __syncwarp();
+            const int rows = T - c * kC - out_tok;
+            uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC + out_tok) * dv + out_col;
 #pragma unroll 2
-                for (int x = ht; x < rows * per; x += 32 * kHelpers) {
-                    const int t = x / per, w = x % per;
-                    *reinterpret_cast<uint4 *>(y0 + (size_t)t * dv + 8 * w) = lds4(s0 + Cfg::kOutV + (w >> 3) * kTile + sw128_offset(t, w & 7));
-                }
+            for (int w = 0; w < 8; ++w) {
+                const uint4 v = cols_get(buf, lane, w);
+                if (8 * w < rows && out_col < dv) *reinterpret_cast<uint4 *>(y0 + (size_t)(8 * w) * dv) = v;
             }
-            named_barrier_sync(1, 32 * kHelpers);
+            __syncwarp();
         }
         tc_fence_before();
     } else if (warp >= kBringer) {
@@ -308,22 +303,19 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
         const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
         const bool live = d < dv;
-        const float scale = args.scale;
         // (one iteration more for the last state)
 #pragma unroll 1
         for (int n = 0; n <= nch; ++n) {
             const int c = chunk(n);
-            const uint32_t st = s0 + (n & 1) * Cfg::kStage, gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
-            if (n < nch) {
-                // V's column, or the scaled dY's (0 past the sequence's end, where TMA fills up), once the last chunk's is used
+            const uint32_t st = s0 + (n & 1) * Cfg::kStage;
+            if (!REV && n < nch) {
+                // V's column (0 past the sequence's end, where TMA fills up), once the last chunk's is used
                 if (!waitw(BBAR(full, n & 1), (n >> 1) & 1)) break;
-                if (n > 0 && !(REV ? waitw(BBAR(done3, 2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1)
-                                   : waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1)))
-                    break;
+                if (n > 0 && !(waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int x = 0; x < 4; ++x) {
-                    uint32_t v[8], lo[8];
+                    uint32_t v[8];
                     const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -332,16 +324,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                                        x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
                         v[i] = live ? x0 | x1 << 16 : 0;
                     }
-                    if (REV) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 g = lds_f4(gates + 64 * x + 16 * i);
-                            split(__fmul2_rn(make_float2(scale * g.x, scale * g.y), unpack(v[2 * i])), v[2 * i], lo[2 * i]);
-                            split(__fmul2_rn(make_float2(scale * g.z, scale * g.w), unpack(v[2 * i + 1])), v[2 * i + 1], lo[2 * i + 1]);
-                        }
-                        tm_st8(tq + kcY + 32 + 8 * x, lo);
-                    }
-                    tm_st8(tq + (REV ? kcY : kcV) + 8 * x, v);
+                    tm_st8(tq + kcV + 8 * x, v);
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -455,6 +438,10 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                     split(__fmul2_rn(make_float2(g.z, g.w), __fmul2_rn(make_float2(f.z, f.w), make_float2(e[4 * i + 2], e[4 * i + 3]))),
                           hi[2 * i + 1], lo[2 * i + 1]);
                 }
+                // (the other half of E has read R's half that comes first)
+                ok = ch != (REV ? 1 : 0) || waitw(BBAR(done2b, 0), ph);
+                if (!ok) break;
+                tc_fence_after();
                 tm_st8(tq + kcR + 8 * cq, hi);
                 tm_st8(tq + kcR + 32 + 8 * cq, lo);
             }
@@ -883,6 +870,7 @@ cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaSha
     GdeltaTcArgs prep;
     prep.s = s;
     prep.ws = ws + p.ws;
+    prep.scale = g.scale;
     GdeltaTcBackArgs a;
     a.s = s;
     a.S0 = g.S0, a.dS_T = g.dS_T, a.dS0 = g.dS0;

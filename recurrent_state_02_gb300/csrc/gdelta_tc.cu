@@ -93,8 +93,8 @@ constexpr uint32_t kPX00 = kPL + kC * LD * 4;    // X00 [u][j]
 constexpr uint32_t kPX11t = kPX00 + 32 * LDT * 4;   // X11 transposed [u][i]
 constexpr uint32_t kPM = kPX11t + 32 * LDT * 4;  // M = L10 X00 [u][j]
 constexpr uint32_t kPM16 = kPM + 32 * LDT * 4;   // the same for the two 32-blocks' halves
-constexpr uint32_t kPGate = kPM16 + 2 * 16 * LDS16 * 4;   // alpha, beta of the chunk's tokens
-constexpr uint32_t kPSmall = kPGate + 2 * kC * 4;
+constexpr uint32_t kPGate = kPM16 + 2 * 16 * LDS16 * 4;   // alpha, beta and e^G of the chunk's tokens
+constexpr uint32_t kPSmall = kPGate + 3 * kC * 4;
 static_assert(kPGate >= 4 * kTile && kPGate % 16 == 0, "the gates lie behind the K, Q tiles");
 
 struct alignas(16) PSmall {
@@ -120,7 +120,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     float *X11t = reinterpret_cast<float *>(base + kPX11t);
     float *Mf = reinterpret_cast<float *>(base + kPM);
     float *M16 = reinterpret_cast<float *>(base + kPM16);
-    float *alpha = reinterpret_cast<float *>(base + kPGate), *beta = alpha + kC;
+    float *alpha = reinterpret_cast<float *>(base + kPGate), *beta = alpha + kC, *expG = beta + kC;
 
     const GdeltaShape &s = args.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,6 +221,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         reinterpret_cast<float2 *>(alpha)[lane] = make_float2(al[0], al[1]);
         reinterpret_cast<float2 *>(beta)[lane] = make_float2(be[0], be[1]);
         if (BACK) {
+            reinterpret_cast<float2 *>(expG)[lane] = make_float2(before * al[0], before * al[0] * al[1]);
             // G itself in 64 bits, kept as two FP32 parts: differences over a few tokens stay exact to FP32 behind gates near 0.
             // A gate of 0 counts as 2^-400, which every exponential takes to 0.
             const double l0 = al[0] > 0.f ? (double)log2f(al[0]) : -400.0, l1 = al[1] > 0.f ? (double)log2f(al[1]) : -400.0;
@@ -257,6 +258,26 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
         issued = ok;
         __syncwarp();
+    }
+    if (BACK) {
+        // scale e^G Q, 16-byte words of its tiles
+        ok = warp_wait(cx, &sm->full, 0) && ok;
+        if (ok) {
+#pragma unroll 2
+            for (int x = tid; x < KD / 64 * 8 * kC; x += kPThreads) {
+                const int row = (x >> 3) & 63;
+                const uint32_t o = sw128_offset(row, x & 7);
+                const uint4 q4 = *reinterpret_cast<const uint4 *>(base + (x >> 9) * 2 * kTile + kTile + o);
+                const float f = args.scale * expG[row];
+                const uint32_t qw[4] = {q4.x, q4.y, q4.z, q4.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split(__fmul2_rn(make_float2(f, f), make_float2(bf16_lo(qw[e]), bf16_hi(qw[e]))), hi[e], lo[e]);
+                uint8_t *to = wsc + kWsQ + (x >> 9) * kTile + o;
+                *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(to + KD / 64 * kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
     }
     ok = warp_wait(cx, &sm->mma, 0) && ok;
     tc_fence_after();
@@ -471,14 +492,14 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 constexpr int kOwners = 16, kHelpers = 4, kBringer = 16, kTaker = 20, kIssuer = 24, kLoader = 25;
 constexpr int kMThreads = 896;
 constexpr int kGateRing = 4;
-// registers per thread after the split (launched with 72): 4 x 88 + 48 + 56 + 48 = 7 x 72
-constexpr int kRegsOwn = 88, kRegsBring = 48, kRegsTake = 56, kRegsRest = 48;
+// registers per thread after the split (launched with 72): 4 x 80 + 48 + 88 + 48 = 7 x 72
+constexpr int kRegsOwn = 80, kRegsBring = 48, kRegsTake = 88, kRegsRest = 48;
 template <int KD>
 struct ChainCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;    // a K or Q tile (64-feature blocks)
     // a stage (two): K, Q, V (two blocks of 64 columns), X's two parts, A
     static constexpr uint32_t kSK = 0, kSQ = kTK, kSV = 2 * kTK, kSX = kSV + 2 * kTile, kSA = kSX + 2 * kTile, kStage = kSA + kTile;
-    static constexpr uint32_t kY = 2 * kStage;          // y of a chunk (two blocks of 64 columns)
+    static constexpr uint32_t kY = 2 * kStage;          // y of a chunk (4 KB per warp that takes it)
     static constexpr uint32_t kGates = kY + 2 * kTile;  // ring of kGateRing
     static constexpr uint32_t kSmall = kGates + kGateRing * 1024;
 };
@@ -493,6 +514,7 @@ struct alignas(16) MSmall {
     uint64_t y_read;                         // Q S and A V' have been read (the takers)
     uint64_t tail;                           // packed: the last chunk's rows of K past the end are 0 (the bringers)
     uint64_t done1[2], done2[2];             // halves of P, E
+    uint64_t done2b;                         // the first half of R has been read
     // halves of dS of even and odd chunks, Q S and A V' (the loader may look at them late, but not two chunks late)
     uint64_t done3[4], done4[2];
     uint64_t fin;
@@ -644,8 +666,9 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                             mma_ts(d, r + 32 + kk * 8, xo + kk * 2, kHi128, id32, true);
                             mma_ts(d, r + kk * 8, xo + kk * 2 + (kTile >> 4), kHi128, id32, true);
                         }
+                        if (t + o == 0) bar_commit(MBAR(done2, 0));
                     }
-                    bar_commit(MBAR(done2, t));
+                    bar_commit(t == 0 ? MBAR(done2b, 0) : MBAR(done2, 1));
                 }
                 if (!ok) break;
                 // (Q S)^T
@@ -680,49 +703,55 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         }
         __syncwarp();
     } else if (warp >= kTaker) {
-        regs_dec<kRegsTake>();
-        const int q4 = warp & 3, d = 32 * q4 + lane;
+        regs_inc<kRegsTake>();
+        const int q4 = warp & 3;
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
-        const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
+        const uint32_t buf = s0 + Cfg::kY + 4096 * q4;
         const size_t y_step = (packed ? (size_t)H : 1) * dv;
-        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * H + h) * dv : bh * args.s.T * dv) + 128 * tile;
-        const float scale = args.scale;
-        // (a warp that gave up waiting still meets the others at their barriers)
-        bool ok = true;
+        // this lane's column and token of a block of 8 when rows go out
+        const int out_col = 32 * q4 + 8 * (lane & 3), out_tok = lane >> 2;
+        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * H + h) * dv : bh * args.s.T * dv) + 128 * tile + out_col + (size_t)out_tok * y_step;
+        const float2 scale = make_float2(args.scale, args.scale);
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
-            // y, through shared memory to whole rows (the gates have been waited for by those whose products this waits for)
-            if (ok) ok = waitw(MBAR(done4, n & 1), (n >> 1) & 1);
-            if (ok) {
-                tc_fence_after();
-                const uint32_t eg = s0 + Cfg::kGates + (n % kGateRing) * 1024;
+            // y, by way of shared memory to whole rows (the gates have been waited for by those whose products this waits for)
+            if (!waitw(MBAR(done4, n & 1), (n >> 1) & 1)) break;
+            tc_fence_after();
+            const uint32_t eg = s0 + Cfg::kGates + (n % kGateRing) * 1024;
 #pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    float qs[8], av[8];
-                    tm_ld8(tq + kcQS + 8 * x, qs);
-                    tm_ld8(tq + kcAV + 8 * x, av);
-                    const float4 g0 = lds_f4(eg + 32 * x), g1 = lds_f4(eg + 32 * x + 16);
-                    const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-                    wait_loaded(qs);
-                    wait_loaded(av);
-                    const uint32_t a = s0 + Cfg::kY + col + x * (8 * 128);
+            for (int x = 0; x < 4; ++x) {
+                float qs[16], av[16];
+                tc_ld_32x32b_x16(tq + kcQS + 16 * x, qs);
+                tc_ld_32x32b_x16(tq + kcAV + 16 * x, av);
+                wait_loaded(qs);
+                wait_loaded(av);
+                if (x == 3) {
+                    tc_fence_before();
+                    bar_arrive_warp(MBAR(y_read, 0));
+                }
+                uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sts_u16(a + i * 128 + ((c16 ^ i) << 4), pack_bf16x2(scale * fmaf(g[i], qs[i], av[i]), 0.f));
+                for (int i = 0; i < 4; ++i) {
+                    const float4 g = lds_f4(eg + 64 * x + 16 * i);
+                    const float2 y01 = __fmul2_rn(scale, __ffma2_rn(make_float2(g.x, g.y), make_float2(qs[4 * i], qs[4 * i + 1]),
+                                                                   make_float2(av[4 * i], av[4 * i + 1])));
+                    const float2 y23 = __fmul2_rn(scale, __ffma2_rn(make_float2(g.z, g.w), make_float2(qs[4 * i + 2], qs[4 * i + 3]),
+                                                                   make_float2(av[4 * i + 2], av[4 * i + 3])));
+                    w[2 * i] = pack_bf16x2(y01.x, y01.y);
+                    w[2 * i + 1] = pack_bf16x2(y23.x, y23.y);
                 }
-                tc_fence_before();
-                bar_arrive_warp(MBAR(y_read, 0));
+                cols_put(buf, lane, 2 * x, w[0], w[1], w[2], w[3]);
+                cols_put(buf, lane, 2 * x + 1, w[4], w[5], w[6], w[7]);
             }
-            named_barrier_sync(1, 32 * kHelpers);
-            if (ok) {
-                const int per = ncols / 8, rows = min(kC, T - n * kC);   // 16-byte words of a row
+            __syncwarp();
+            const int rows = T - n * kC - out_tok;
+            uint16_t *yp = y0 + (size_t)(n * kC) * y_step;
 #pragma unroll 2
-                for (int x = tid - 32 * kTaker; x < rows * per; x += 32 * kHelpers) {
-                    const int t = x / per, w = x % per;
-                    *reinterpret_cast<uint4 *>(y0 + (size_t)(n * kC + t) * y_step + 8 * w) =
-                        lds4(s0 + Cfg::kY + (w >> 3) * kTile + sw128_offset(t, w & 7));
-                }
+            for (int w = 0; w < 8; ++w) {
+                const uint4 v = cols_get(buf, lane, w);
+                if (8 * w < rows && out_col < ncols) *reinterpret_cast<uint4 *>(yp + (size_t)(8 * w) * y_step) = v;
             }
-            named_barrier_sync(1, 32 * kHelpers);
+            __syncwarp();
         }
         tc_fence_before();
     } else if (warp >= kBringer) {
@@ -844,9 +873,13 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     split(__fmul2_rn(make_float2(er.x, er.y), w0), hi[2 * i], lo[2 * i]);
                     split(__fmul2_rn(make_float2(er.z, er.w), w1), hi[2 * i + 1], lo[2 * i + 1]);
                 }
+                tm_st8(tq + kcW + 8 * cq, w);
+                // (the second half of E has read the first one's R)
+                ok = ch || waitw(MBAR(done2b, 0), ph);
+                if (!ok) break;
+                tc_fence_after();
                 tm_st8(tq + kcR + 8 * cq, hi);
                 tm_st8(tq + kcR + 32 + 8 * cq, lo);
-                tm_st8(tq + kcW + 8 * cq, w);
             }
             stored(MBAR(got_w, ch));
             const float gC = ldsf(gates - 64 * cq + 4 * (kC - 1));

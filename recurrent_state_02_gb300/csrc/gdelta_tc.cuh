@@ -14,10 +14,10 @@ namespace {
 constexpr uint32_t kHi128 = desc_hi(1024, 2);   // SBO and swizzle of 128-byte rows
 constexpr uint32_t kTile = kC * 128;            // 8 KB: 64 rows of 64 BF16
 // workspace per chunk and head: A, X's high and low parts (BF16 shared-memory images), then 64 floats each of e^G, e^{G_C - G}
-// and beta.  For the gradients also A's low part, and behind the gates log2 e^G as pairs of a high and a low FP32 part and the
-// true beta over the one used.
+// and beta.  For the gradients also A's low part and scale e^G Q (two parts of up to two blocks of 64 features), and behind the gates
+// log2 e^G as pairs of a high and a low FP32 part and the true beta over the one used.
 constexpr uint32_t kWsA = 0, kWsX = kTile, kWsGates = 3 * kTile, kWsChunk = kWsGates + 1024;
-constexpr uint32_t kWsAl = kWsGates + 2048, kWsChunkB = kWsAl + kTile;
+constexpr uint32_t kWsAl = kWsGates + 2048, kWsQ = kWsAl + kTile, kWsChunkB = kWsQ + 4 * kTile;
 constexpr uint32_t kGateBytes = 3 * kC * 4, kGateBytesB = 6 * kC * 4;
 constexpr uint32_t kGateLog = 3 * kC * 4, kGateRatio = 5 * kC * 4;
 
@@ -121,6 +121,28 @@ __device__ __forceinline__ bool elect_one()
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// A warp's way from a column per lane to rows in memory: lane d has 64 tokens of column d, as 32 words of two BF16, and the rows of
+// the output have 32 columns (64 bytes) of the warp.  The words go to 128-byte rows of shared memory (4 KB per warp), 16-byte
+// word w of row d at w ^ cols_swizzle(d); ldmatrix reads them back transposed, with the rows of its four 8 x 8 matrices chosen so
+// that a lane receives eight neighbouring columns of one token.  Neither side has a bank conflict.
+__device__ __forceinline__ uint32_t cols_swizzle(int d) { return (d & 1) | ((((d >> 3) ^ (d >> 1)) & 3) << 1); }
+// Words 4 w .. 4 w + 3 of this lane's column.
+__device__ __forceinline__ void cols_put(uint32_t buf, int lane, int w, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3)
+{
+    sts4(buf + lane * 128 + ((w ^ cols_swizzle(lane)) << 4), x0, x1, x2, x3);
+}
+// Tokens 8 w .. 8 w + 7: this lane gets columns 8 (lane % 4) .. of token 8 w + lane / 4.
+__device__ __forceinline__ uint4 cols_get(uint32_t buf, int lane, int w)
+{
+    const int i = lane & 7, d = 8 * (i >> 1) + 2 * (lane >> 3) + (i & 1);
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(buf + d * 128 + ((w ^ cols_swizzle(d)) << 4))
+                 : "memory");
+    return v;
 }
 
 // 16 BF16 values (8 words) of one row of a tile in memory with 128-byte rows and the 128-byte swizzle: 16-byte words 2 x and
