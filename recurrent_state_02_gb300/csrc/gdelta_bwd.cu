@@ -41,19 +41,21 @@ constexpr int kRegsOwn = 80, kRegsBring = 48, kRegsTake = 88, kRegsRest = 48;
 template <int KD, bool REV>
 struct BackCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;
-    // a stage (two): K, V or dY (two blocks of 64 columns), X's parts; backwards also A's parts and scale e^G Q's
-    static constexpr uint32_t kSK = 0, kSV = kTK, kSX = kSV + 2 * kTile, kSA = kSX + 2 * kTile, kSQ = kSA + 2 * kTile,
-                              kStage = REV ? kSQ + 2 * kTK : kSA;
-    // dv of a chunk (4 KB per warp that takes it)
-    static constexpr uint32_t kOutV = 2 * kStage, kGates = kOutV + (REV ? 2 * kTile : 0), kSmall = kGates + kGateRing * kGateStep;
+    // a stage (two): K, V or dY (two blocks of 64 columns), forwards X's parts; backwards one buffer each for X's parts, A's, and
+    // scale e^G Q's
+    static constexpr uint32_t kSK = 0, kSV = kTK, kSX = kSV + 2 * kTile, kStage = REV ? kSX : kSX + 2 * kTile;
+    static constexpr uint32_t kX = 2 * kStage, kA = kX + 2 * kTile, kQ = kA + 2 * kTile, kBufs = REV ? kQ + 2 * kTK : kX;
+    // what goes to memory: the state (two parts), and E, or dv (4 KB per warp that takes it)
+    static constexpr uint32_t kOutS = kBufs, kOutE = kOutS + 2 * kStateImg<KD>, kGates = kOutE + (REV ? 2 * kTile : kTokImg),
+                              kSmall = kGates + kGateRing * kGateStep;
 };
 // TMEM columns: S^T (two parts), P^T and E^T (then dS^T), (A^T dY)^T, R^T (two parts, then the decayed V'^T's, or the scaled
 // N^T's), V^T
 constexpr uint32_t kcS = 0, kcP = 128, kcE = 192, kcA = 256, kcR = 320, kcV = 384;
 
 struct alignas(16) BSmall {
-    uint64_t full[2];
-    uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (4 warps)
+    uint64_t full[2], full_x, full_a, full_q;
+    uint64_t got_s[2], got_r[2], got_w[2];   // an owner half's operand is in TMEM (8 warps)
     uint64_t got_v, s_read, e_read;          // V^T is there, S has been read (the bringers); E has (the takers)
     uint64_t done0, done1[2], done2[2];      // A^T dY, halves of P, E
     uint64_t done2b;                         // the half of R that comes first has been read
@@ -108,30 +110,44 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         regs_dec<kRegsRest>();
         if (warp == kLoader && elect_one()) {
             const int hk = h / (H / args.s.Hk), kh = b * args.s.Hk + hk;
-            int n1 = 0;
+            int n1 = 0, nx = 0, na = 0, nq = 0;        // chunks whose loads were started
 #pragma unroll 1
             for (int n = 0; n < nch; ++n) {
                 const uint32_t st = s0 + (n & 1) * Cfg::kStage, bar = BBAR(full, n & 1);
                 const int c = chunk(n);
                 const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
                 if (n >= 2 && !wait1(BBAR(done3, 2 + (n & 1)), ((n >> 1) - 1) & 1)) break;
-                bar_expect(bar, (REV ? 3 : 1) * Cfg::kTK + dv / 64 * kTile + (REV ? 4 : 2) * kTile + kGateBytesB);
+                bar_expect(bar, Cfg::kTK + dv / 64 * kTile + (REV ? 0 : 2 * kTile) + kGateBytesB);
 #pragma unroll 1
                 for (int x = 0; x < KD / 64; ++x) tma_load(st + Cfg::kSK + x * kTile, &map_k, bar, 64 * x, c * kC, kh);
 #pragma unroll 1
                 for (int x = 0; x < dv / 64; ++x) tma_load(st + Cfg::kSV + x * kTile, &map_v, bar, 64 * x, c * kC, (int)bh);
                 bulk_copy(s0 + Cfg::kGates + (n % kGateRing) * kGateStep, w + kWsGates, kGateBytesB, bar);
-                bulk_copy(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
-                if (REV) {
-                    bulk_copy(st + Cfg::kSQ, w + kWsQ, 2 * Cfg::kTK, bar);
-                    bulk_copy(st + Cfg::kSA, w + kWsA, kTile, bar);
-                    bulk_copy(st + Cfg::kSA + kTile, w + kWsAl, kTile, bar);
-                }
+                if (!REV) bulk_copy(st + Cfg::kSX, w + kWsX, 2 * kTile, bar);
                 n1 = n + 1;
+                if (REV) {
+                    // one buffer each, as their last reads end
+                    if (n > 0 && !wait1(BBAR(done0, 0), (n - 1) & 1)) break;
+                    bar_expect(BBAR(full_a, 0), 2 * kTile);
+                    bulk_copy(s0 + Cfg::kA, w + kWsA, kTile, BBAR(full_a, 0));
+                    bulk_copy(s0 + Cfg::kA + kTile, w + kWsAl, kTile, BBAR(full_a, 0));
+                    na = n + 1;
+                    if (n > 0 && !wait1(BBAR(done2, 0), (n - 1) & 1)) break;
+                    bar_expect(BBAR(full_x, 0), 2 * kTile);
+                    bulk_copy(s0 + Cfg::kX, w + kWsX, 2 * kTile, BBAR(full_x, 0));
+                    nx = n + 1;
+                    if (n > 0 && !wait1(BBAR(done3, 2 + ((n - 1) & 1)), ((n - 1) >> 1) & 1)) break;
+                    bar_expect(BBAR(full_q, 0), 2 * Cfg::kTK);
+                    bulk_copy(s0 + Cfg::kQ, w + kWsQ, 2 * Cfg::kTK, BBAR(full_q, 0));
+                    nq = n + 1;
+                }
             }
             // loads still in flight complete before the CTA exits (also after a wait that was given up)
 #pragma unroll 1
             for (int i = max(0, n1 - 2); i < n1; ++i) wait1(BBAR(full, i & 1), (i >> 1) & 1);
+            if (na) wait1(BBAR(full_a, 0), (na - 1) & 1);
+            if (nx) wait1(BBAR(full_x, 0), (nx - 1) & 1);
+            if (nq) wait1(BBAR(full_q, 0), (nq - 1) & 1);
         } else if (warp == kIssuer && elect_one()) {
             constexpr uint32_t id64 = idesc_bf16_f32(128, 64, false, false), id32 = idesc_bf16_f32(128, 32, false, REV),
                                idP = idesc_bf16_f32(128, 32, false, false), idS = idesc_bf16_f32(128, KH, false, true),
@@ -140,7 +156,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
             // (A^T dY)^T = dY^T A, both parts of A
             auto mma_a = [&](int n) {
                 const uint32_t st = s0 + (n & 1) * Cfg::kStage;
-                const uint32_t ylo = desc_lo(st + Cfg::kSV, kTile), alo = desc_lo(st + Cfg::kSA, kTile);
+                const uint32_t ylo = desc_lo(st + Cfg::kSV, kTile), alo = desc_lo(s0 + Cfg::kA, kTile);
 #pragma unroll 4
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t o = (i & 3) * (2048 >> 4);
@@ -148,14 +164,14 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 }
                 bar_commit(BBAR(done0, 0));
             };
-            if (REV && nch > 0 && wait1(BBAR(full, 0), 0)) {
+            if (REV && wait1(BBAR(full, 0), 0) && wait1(BBAR(full_a, 0), 0)) {
                 tc_fence_after();
                 mma_a(0);
             }
 #pragma unroll 1
             for (int n = 0; n < nch; ++n) {
                 const uint32_t st = s0 + (n & 1) * Cfg::kStage, ph = n & 1;
-                const uint32_t klo = desc_lo(st + Cfg::kSK, 16), xlo = desc_lo(st + Cfg::kSX, REV ? kTile : 16);
+                const uint32_t klo = desc_lo(st + Cfg::kSK, 16), xlo = desc_lo(REV ? s0 + Cfg::kX : st + Cfg::kSX, REV ? kTile : 16);
                 // 1  P^T = S^T K^T
                 if (!wait1(BBAR(full, n & 1), (n >> 1) & 1) || !wait1(BBAR(got_s, 0), ph)) break;
                 tc_fence_after();
@@ -179,6 +195,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 }
                 // 2  E^T = R^T X^T, the first half of R first; backwards N^T = (beta D)^T X, the second half first
                 bool ok = true;
+                if (REV && !wait1(BBAR(full_x, 0), ph)) break;
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int t = REV ? 1 - u : u;
@@ -208,14 +225,18 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 const uint32_t kmn = desc_lo(st + Cfg::kSK, kTile);
                 auto mma_q = [&](int t) {                  // both parts of the scaled Q
                     const uint32_t ylo = desc_lo(st + Cfg::kSV, kTile),
-                                   qmn = desc_lo(st + Cfg::kSQ, kTile) + t * ((KD == 128 ? kTile : 64u) >> 4);
+                                   qmn = desc_lo(s0 + Cfg::kQ, kTile) + t * ((KD == 128 ? kTile : 64u) >> 4);
 #pragma unroll 4
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t o = (i & 3) * (2048 >> 4);
                         mma_ss(kcP + 64 * t, ylo + o, kHi128, qmn + (i >> 2) * (Cfg::kTK >> 4) + o, kHi128, idQ, i > 0);
                     }
                 };
-                if (REV) mma_q(0);
+                if (REV) {
+                    if (!wait1(BBAR(full_q, 0), ph)) break;
+                    tc_fence_after();
+                    mma_q(0);
+                }
                 if (!wait1(BBAR(got_w, 0), ph) || !wait1(BBAR(got_w, 1), ph)) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -234,7 +255,7 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
                 }
                 if (!ok) break;
                 if (REV && n + 1 < nch) {
-                    if (!wait1(BBAR(full, (n + 1) & 1), ((n + 1) >> 1) & 1)) break;
+                    if (!wait1(BBAR(full, (n + 1) & 1), ((n + 1) >> 1) & 1) || !wait1(BBAR(full_a, 0), ph ^ 1)) break;
                     tc_fence_after();
                     mma_a(n + 1);
                 }
@@ -247,55 +268,81 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
     } else if (warp >= kTaker) {
         regs_inc<kRegsTake>();
         const int q4 = warp & 3, d = 32 * q4 + lane;
-        const uint32_t tq = (uint32_t)(32 * q4) << 16, buf = s0 + Cfg::kOutV + 4096 * q4;
+        const uint32_t tq = (uint32_t)(32 * q4) << 16, buf = s0 + Cfg::kOutE + 4096 * q4;
         const int out_col = 32 * q4 + 8 * (lane & 3), out_tok = lane >> 2;
+        const bool first = tid == 32 * kTaker;
+        // (a warp that gave up waiting still meets the others at their barriers)
+        bool ok = true;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
             const int c = chunk(n);
             const uint32_t gates = s0 + Cfg::kGates + (n % kGateRing) * kGateStep;
-            // E, or N (the gates have been waited for by those whose products this waits for)
-            if (!waitw(BBAR(done2, 0), n & 1) || !waitw(BBAR(done2, 1), n & 1)) break;
-            tc_fence_after();
             uint8_t *img = (REV ? args.N : args.E) + (bh * nch + c) * kTokImg;
-            // (all of it at once: the issuer waits for its columns)
-            float e4[4][16];
+            if (!REV) {
+                // (the last chunk's E has left its place)
+                if (first) tma_store_wait_read<0>();
+                named_barrier_sync(1, 32 * kHelpers);
+            }
+            // E, or N (the gates have been waited for by those whose products this waits for)
+            if (ok) ok = waitw(BBAR(done2, 0), n & 1) && waitw(BBAR(done2, 1), n & 1);
+            if (ok) {
+                tc_fence_after();
+                // (all of it at once: the issuer waits for its columns)
+                float e4[4][16];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) tc_ld_32x32b_x16(tq + kcE + 16 * x, e4[x]);
+                for (int x = 0; x < 4; ++x) tc_ld_32x32b_x16(tq + kcE + 16 * x, e4[x]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) wait_loaded(e4[x]);
-            tc_fence_before();
-            bar_arrive_warp(BBAR(e_read, 0));
+                for (int x = 0; x < 4; ++x) wait_loaded(e4[x]);
+                tc_fence_before();
+                bar_arrive_warp(BBAR(e_read, 0));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float (&e)[16] = e4[x];
-                uint32_t hi[8], lo[8];
+                for (int x = 0; x < 4; ++x) {
+                    const float (&e)[16] = e4[x];
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
-                st_row16(img, d, x, hi);
-                st_row16(img + kImg, d, x, lo);
-                if (REV) {
-                    uint32_t w[8];
+                    for (int i = 0; i < 8; ++i) split(make_float2(e[2 * i], e[2 * i + 1]), hi[i], lo[i]);
+                    if (!REV) {
+                        const uint32_t o = s0 + Cfg::kOutE + sw128_offset(d, 2 * x), o2 = s0 + Cfg::kOutE + sw128_offset(d, 2 * x + 1);
+                        sts4(o, hi[0], hi[1], hi[2], hi[3]);
+                        sts4(o2, hi[4], hi[5], hi[6], hi[7]);
+                        sts4(o + kImg, lo[0], lo[1], lo[2], lo[3]);
+                        sts4(o2 + kImg, lo[4], lo[5], lo[6], lo[7]);
+                    } else {
+                        // (there is no room left for N in shared memory: it goes straight to its image)
+                        st_row16(img, d, x, hi);
+                        st_row16(img + kImg, d, x, lo);
+                        uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 g = lds_f4(gates + kGateRatio + 64 * x + 16 * i);
-                        w[2 * i] = pack_bf16x2(g.x * e[4 * i], g.y * e[4 * i + 1]);
-                        w[2 * i + 1] = pack_bf16x2(g.z * e[4 * i + 2], g.w * e[4 * i + 3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 g = lds_f4(gates + kGateRatio + 64 * x + 16 * i);
+                            w[2 * i] = pack_bf16x2(g.x * e[4 * i], g.y * e[4 * i + 1]);
+                            w[2 * i + 1] = pack_bf16x2(g.z * e[4 * i + 2], g.w * e[4 * i + 3]);
+                        }
+                        cols_put(buf, lane, 2 * x, w[0], w[1], w[2], w[3]);
+                        cols_put(buf, lane, 2 * x + 1, w[4], w[5], w[6], w[7]);
                     }
-                    cols_put(buf, lane, 2 * x, w[0], w[1], w[2], w[3]);
-                    cols_put(buf, lane, 2 * x + 1, w[4], w[5], w[6], w[7]);
                 }
             }
-            if (!REV) continue;
-            __syncwarp();
-            const int rows = T - c * kC - out_tok;
-            uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC + out_tok) * dv + out_col;
+            if (!REV) {
+                fence_proxy_async_smem();
+                named_barrier_sync(1, 32 * kHelpers);
+                if (first && ok) {
+                    bulk_store(img, s0 + Cfg::kOutE, kTokImg);
+                    tma_store_commit();
+                }
+            } else if (ok) {
+                __syncwarp();
+                const int rows = T - c * kC - out_tok;
+                uint16_t *y0 = args.dv_out + (bh * T + (size_t)c * kC + out_tok) * dv + out_col;
 #pragma unroll 2
-            for (int w = 0; w < 8; ++w) {
-                const uint4 v = cols_get(buf, lane, w);
-                if (8 * w < rows && out_col < dv) *reinterpret_cast<uint4 *>(y0 + (size_t)(8 * w) * dv) = v;
+                for (int w = 0; w < 8; ++w) {
+                    const uint4 v = cols_get(buf, lane, w);
+                    if (8 * w < rows && out_col < dv) *reinterpret_cast<uint4 *>(y0 + (size_t)(8 * w) * dv) = v;
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
+        if (!REV && first) tma_store_wait_all<0>();
         tc_fence_before();
     } else if (warp >= kBringer) {
         regs_dec<kRegsBring>();
@@ -303,55 +350,74 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
         const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
         const bool live = d < dv;
-        // (one iteration more for the last state)
+        const bool first = tid == 32 * kBringer;
+        // (one iteration more for the last state; a warp that gave up waiting still meets the others at their barriers)
+        bool ok = true;
 #pragma unroll 1
         for (int n = 0; n <= nch; ++n) {
             const int c = chunk(n);
             const uint32_t st = s0 + (n & 1) * Cfg::kStage;
             if (!REV && n < nch) {
                 // V's column (0 past the sequence's end, where TMA fills up), once the last chunk's is used
-                if (!waitw(BBAR(full, n & 1), (n >> 1) & 1)) break;
-                if (n > 0 && !(waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1))) break;
+                if (ok) ok = waitw(BBAR(full, n & 1), (n >> 1) & 1);
+                if (ok && n > 0) ok = waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t v[8];
+                        const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int t = 2 * i;
+                            const uint32_t x0 = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
+                                           x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
+                            v[i] = live ? x0 | x1 << 16 : 0;
+                        }
+                        tm_st8(tq + kcV + 8 * x, v);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    bar_arrive_warp(BBAR(got_v, 0));
+                }
+            }
+            // the state before the chunk; backwards its gradient behind it, once the last one has left its place
+            if (first) tma_store_wait_read<0>();
+            named_barrier_sync(2, 32 * kHelpers);
+            if (ok) ok = waitw(BBAR(got_s, 0), n & 1) && waitw(BBAR(got_s, 1), n & 1);
+            if (ok) {
                 tc_fence_after();
 #pragma unroll 1
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t v[8];
-                    const uint32_t a = st + Cfg::kSV + col + x * (16 * 128);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int t = 2 * i;
-                        const uint32_t x0 = lds_u16(a + t * 128 + ((c16 ^ (t & 7)) << 4)),
-                                       x1 = lds_u16(a + (t + 1) * 128 + ((c16 ^ ((t + 1) & 7)) << 4));
-                        v[i] = live ? x0 | x1 << 16 : 0;
+                for (int x = 0; x < KD / 16; ++x) {
+                    float hi[8], lo[8];
+                    tm_ld8(tq + kcS + 8 * x, hi);
+                    tm_ld8(tq + kcS + KH + 8 * x, lo);
+                    wait_loaded(hi);
+                    wait_loaded(lo);
+                    if (x == KD / 16 - 1) {
+                        tc_fence_before();
+                        bar_arrive_warp(BBAR(s_read, 0));
                     }
-                    tm_st8(tq + kcV + 8 * x, v);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                bar_arrive_warp(BBAR(got_v, 0));
-            }
-            // the state before the chunk; backwards its gradient behind it
-            if (!waitw(BBAR(got_s, 0), n & 1) || !waitw(BBAR(got_s, 1), n & 1)) break;
-            tc_fence_after();
-            uint8_t *img = (REV ? args.dS : args.S) + (bh * (nch + 1) + (REV ? c + 1 : c)) * (2 * kStateImg<KD>);
-#pragma unroll 1
-            for (int x = 0; x < KD / 16; ++x) {
-                float hi[8], lo[8];
-                tm_ld8(tq + kcS + 8 * x, hi);
-                tm_ld8(tq + kcS + KH + 8 * x, lo);
-                wait_loaded(hi);
-                wait_loaded(lo);
-                if (x == KD / 16 - 1) {
-                    tc_fence_before();
-                    bar_arrive_warp(BBAR(s_read, 0));
-                }
-                uint32_t hw[8], lw[8];
+                    uint32_t hw[8], lw[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) hw[i] = __float_as_uint(hi[i]), lw[i] = __float_as_uint(lo[i]);
-                st_row16(img + (x >> 2) * kImg, d, x & 3, hw);
-                st_row16(img + kStateImg<KD> + (x >> 2) * kImg, d, x & 3, lw);
+                    for (int i = 0; i < 8; ++i) hw[i] = __float_as_uint(hi[i]), lw[i] = __float_as_uint(lo[i]);
+                    const uint32_t o = s0 + Cfg::kOutS + (x >> 2) * kImg + sw128_offset(d, 2 * (x & 3)),
+                                   o2 = s0 + Cfg::kOutS + (x >> 2) * kImg + sw128_offset(d, 2 * (x & 3) + 1);
+                    sts4(o, hw[0], hw[1], hw[2], hw[3]);
+                    sts4(o2, hw[4], hw[5], hw[6], hw[7]);
+                    sts4(o + kStateImg<KD>, lw[0], lw[1], lw[2], lw[3]);
+                    sts4(o2 + kStateImg<KD>, lw[4], lw[5], lw[6], lw[7]);
+                }
+                fence_proxy_async_smem();
+            }
+            named_barrier_sync(2, 32 * kHelpers);
+            if (first && ok) {
+                bulk_store((REV ? args.dS : args.S) + (bh * (nch + 1) + (REV ? c + 1 : c)) * (2 * kStateImg<KD>), s0 + Cfg::kOutS,
+                           2 * kStateImg<KD>);
+                tma_store_commit();
             }
         }
+        if (first) tma_store_wait_all<0>();
         tc_fence_before();
     } else {
         regs_inc<kRegsOwn>();

@@ -157,5 +157,10 @@ __device__ __forceinline__ void st_row16(uint8_t *tile, int row, int x, const ui
                  : "memory");
 }
 
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 }  // namespace
 }  // namespace la
