@@ -1267,7 +1267,7 @@ la_status la_gated_delta_backward(const void *q, const void *k, const void *v, l
             return make_map_bf16(t, p, (long long)B * heads, T, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
         };
         if (!map(&m.q, q, Hk, r) || !map(&m.k, k, Hk, r) || !map(&m.v, v, H, dv) || !map(&m.dy, dy, H, dv)) return LA_ERR_CUDA;
-        return from_cuda(la::launch_gdelta_tc_backward(m, s, g, st));
+        return from_cuda(la::launch_gdelta_tc_backward(m, s, g, sm_count(), st));
     }
     return from_cuda(la::launch_gdelta_rec_backward(s, g, dtype == LA_DTYPE_BF16, st));
 }

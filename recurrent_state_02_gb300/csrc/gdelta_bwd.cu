@@ -549,22 +549,23 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
 }
 
 // -------------------------------------------------- the gradients of a chunk
-// One CTA per chunk and head: 8 warps compute (warp w: rows 16 (w % 4) .. of the M = 64 accumulators, half w / 4 of their columns),
-// one issues the MMAs, one loads.
+// One CTA per SM walks the chunks of all heads: 8 warps compute (warp w: rows 16 (w % 4) .. of the M = 64 accumulators, half w / 4
+// of their columns), one issues the MMAs, one loads.  What a chunk needs fills shared memory, so the next one's operands come into
+// each buffer as soon as its last product has read it, under the products, sums and stores that remain.
 constexpr int kGComp = 8, kGIssuer = 8, kGLoader = 9, kGThreads = 320;
 template <int KD>
 struct GradCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;
-    // Q, K, dY, V, E and N (two parts each; dS's blocks take the place of their low parts), S (two parts), dP, dL, the gates
+    // Q, K, dY, V, E and N (two parts each), S (two parts; then dS's high one in place of the low one), dP, dL, the gates (two)
     static constexpr uint32_t kQ = 0, kK = kTK, kY = 2 * kTK, kV = kY + 2 * kTile, kE = kV + 2 * kTile, kN = kE + kTokImg,
                               kS = kN + kTokImg, kP = kS + 2 * kStateImg<KD>, kL = kP + kTile, kGates = kL + kTile,
-                              kSmall = kGates + kGateStep;
+                              kSmall = kGates + 2 * kGateStep;
 };
 // TMEM columns: Q K^T, dY E^T, N E^T, V N^T (then dP K and dP^T Q + dL K + dL^T K), dY S^T (then E dS^T), N S^T
 constexpr uint32_t kgP = 0, kgYE = 64, kgNE = 128, kgVN = 192, kgQ = 0, kgK = 128, kgYS = 256, kgNS = 384;
 struct alignas(16) GSmall {
-    uint64_t full[3];            // Q, K, dY, V, E, N; S; dS
-    uint64_t got_p, got_x;       // dP and dL are in shared memory; dY S^T has been read
+    uint64_t full[3];              // Q, K, dY, V, E, N; S; dS
+    uint64_t got_p, got_x, got_e;  // dP and dL are in shared memory; dY S^T and S have been read; all accumulators have
     uint64_t doneG, doneS, doneQ, doneF;
     uint64_t fin;
     uint32_t tmem_base;
@@ -580,7 +581,7 @@ template <int KD, bool OUT32>
 __global__ void __launch_bounds__(kGThreads, 1)
 gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dy,
-                   const __grid_constant__ GdeltaTcBackArgs args)
+                   const __grid_constant__ GdeltaTcBackArgs args, int total)
 {
     using Cfg = GradCfg<KD>;
     extern __shared__ uint8_t smem_raw[];
@@ -592,12 +593,12 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = args.s.H, dv = args.s.dv, T = args.s.T, nch = (T + kC - 1) / kC;
-    const int c = blockIdx.x % nch;
-    const size_t bh = blockIdx.x / nch;
-    const int h = (int)(bh % H), b = (int)(bh / H);
+    const int nit = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // chunks of this CTA
+    // the i-th: neighbours in time run at the same time, and share the states between them
+    auto item = [&](int i) { return (int)blockIdx.x + i * (int)gridDim.x; };
 
     if (tid == 0) {
-        for (uint64_t *bar = sm->full; bar <= &sm->fin; ++bar) mbar_init(bar, bar == &sm->got_p || bar == &sm->got_x ? kGComp : 1);
+        for (uint64_t *bar = sm->full; bar <= &sm->fin; ++bar) mbar_init(bar, bar >= &sm->got_p && bar <= &sm->got_e ? kGComp : 1);
         sm->abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -611,36 +612,64 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     if (warp == kGLoader) {
         if (elect_one()) {
-            const int kh = b * args.s.Hk + h / (H / args.s.Hk);
-            const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
-            bar_expect(GBAR(full, 0), 2 * Cfg::kTK + 2 * (dv / 64) * kTile + 2 * kTokImg + kGateBytesB);
-            bulk_copy(s0 + Cfg::kGates, w + kWsGates, kGateBytesB, GBAR(full, 0));
+            bool started = false;        // loads that no wait below has seen land
 #pragma unroll 1
-            for (int x = 0; x < KD / 64; ++x) {
-                tma_load(s0 + Cfg::kQ + x * kTile, &map_q, GBAR(full, 0), 64 * x, c * kC, kh);
-                tma_load(s0 + Cfg::kK + x * kTile, &map_k, GBAR(full, 0), 64 * x, c * kC, kh);
-            }
+            for (int i = 0; i <= nit; ++i) {
+                // the i-th chunk's operands, and in between dS of the one before it
+                const bool load = i < nit;
+                const uint32_t ph = (i - 1) & 1;
+                const int g = load ? item(i) : 0, c = g % nch;
+                const size_t bh = g / nch;
+                const int h = (int)(bh % H), b = (int)(bh / H), kh = b * args.s.Hk + h / (H / args.s.Hk);
+                const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
+                const uint8_t *E = args.E + (bh * nch + c) * kTokImg, *N = args.N + (bh * nch + c) * kTokImg,
+                              *S = args.S + (bh * (nch + 1) + c) * (2 * kStateImg<KD>);
+                const uint32_t f0 = GBAR(full, 0), f1 = GBAR(full, 1);
+                if (i > 0 && !wait1(GBAR(got_x, 0), ph)) break;
+                if (load) {
+                    bar_expect(f0, 2 * Cfg::kTK + 2 * (dv / 64) * kTile + 2 * kTokImg + kGateBytesB);
+                    bar_expect(f1, 2 * kStateImg<KD>);
+                    started = true;
+                }
+                if (i > 0) {
+                    const int p = item(i - 1);
+                    bar_expect(GBAR(full, 2), kStateImg<KD>);
+                    bulk_copy(s0 + Cfg::kS + kStateImg<KD>, args.dS + ((size_t)(p / nch) * (nch + 1) + p % nch + 1) * (2 * kStateImg<KD>),
+                              kStateImg<KD>, GBAR(full, 2));
+                }
+                if (load) {
+                    bulk_copy(s0 + Cfg::kGates + (i & 1) * kGateStep, w + kWsGates, kGateBytesB, f0);
 #pragma unroll 1
-            for (int x = 0; x < dv / 64; ++x) {
-                tma_load(s0 + Cfg::kY + x * kTile, &map_dy, GBAR(full, 0), 64 * x, c * kC, (int)bh);
-                tma_load(s0 + Cfg::kV + x * kTile, &map_v, GBAR(full, 0), 64 * x, c * kC, (int)bh);
-            }
-            bulk_copy(s0 + Cfg::kE, args.E + (bh * nch + c) * kTokImg, kTokImg, GBAR(full, 0));
-            bulk_copy(s0 + Cfg::kN, args.N + (bh * nch + c) * kTokImg, kTokImg, GBAR(full, 0));
-            bar_expect(GBAR(full, 1), 2 * kStateImg<KD>);
-            bulk_copy(s0 + Cfg::kS, args.S + (bh * (nch + 1) + c) * (2 * kStateImg<KD>), 2 * kStateImg<KD>, GBAR(full, 1));
-            // dS's blocks over the low parts of E and N, which the first products have read
-            const bool ok = wait1(GBAR(doneG, 0), 0);
-            if (ok) {
-                bar_expect(GBAR(full, 2), kStateImg<KD>);
+                    for (int x = 0; x < dv / 64; ++x) {
+                        tma_load(s0 + Cfg::kY + x * kTile, &map_dy, f0, 64 * x, c * kC, (int)bh);
+                        tma_load(s0 + Cfg::kV + x * kTile, &map_v, f0, 64 * x, c * kC, (int)bh);
+                    }
+                    bulk_copy(s0 + Cfg::kE + kImg, E + kImg, kImg, f0);
+                    bulk_copy(s0 + Cfg::kN, N, kTokImg, f0);
+                    bulk_copy(s0 + Cfg::kS, S, kStateImg<KD>, f1);
+                    // what has to wait for its buffer comes into L2 meanwhile
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(E), "r"(kImg) : "memory");
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S + kStateImg<KD>), "r"(kStateImg<KD>) : "memory");
+                }
+                if (i > 0 && !wait1(GBAR(doneQ, 0), ph)) break;
+                if (load) {
 #pragma unroll 1
-                for (int x = 0; x < KD / 64; ++x)
-                    bulk_copy(s0 + (x ? Cfg::kN : Cfg::kE) + kImg, args.dS + (bh * (nch + 1) + c + 1) * (2 * kStateImg<KD>) + x * kImg, kImg, GBAR(full, 2));
+                    for (int x = 0; x < KD / 64; ++x) {
+                        tma_load(s0 + Cfg::kQ + x * kTile, &map_q, f0, 64 * x, c * kC, kh);
+                        tma_load(s0 + Cfg::kK + x * kTile, &map_k, f0, 64 * x, c * kC, kh);
+                    }
+                }
+                if (i > 0 && !wait1(GBAR(doneF, 0), ph)) break;
+                if (load) {
+                    bulk_copy(s0 + Cfg::kE, E, kImg, f0);
+                    bulk_copy(s0 + Cfg::kS + kStateImg<KD>, S + kStateImg<KD>, kStateImg<KD>, f1);
+                    // (a last chunk's loads have landed when its products are done)
+                    started = false;
+                }
+                if (i == nit) started = false;
             }
-            // what was started lands before the CTA exits
-            wait1(GBAR(full, 0), 0);
-            wait1(GBAR(full, 1), 0);
-            if (ok) wait1(GBAR(full, 2), 0);
+            // after a wait that was given up: what was started lands before the CTA exits, or has had the time to
+            if (started) wait1(GBAR(full, 0), 0), wait1(GBAR(full, 0), 1), wait1(GBAR(full, 2), 1);
         }
         __syncwarp();
     } else if (warp == kGIssuer) {
@@ -652,10 +681,12 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                            S = desc_lo(s0 + Cfg::kS, kImg);
             constexpr uint32_t kLo = kImg >> 4, kMn = 2048 >> 4;
             auto kmaj = [&](int k) { return (uint32_t)((k >> 2) * (kTile >> 4) + (k & 3) * 2); };
-            do {
-                if (!wait1(GBAR(full, 0), 0)) break;
-                tc_fence_after();
 #pragma unroll 1
+            for (int i = 0; i < nit; ++i) {
+                const uint32_t ph = i & 1;
+                if (!wait1(GBAR(full, 0), ph) || (i > 0 && !wait1(GBAR(got_e, 0), ph ^ 1))) break;
+                tc_fence_after();
+#pragma unroll 2
                 for (int k = 0; k < KD / 16; ++k)
                     mma_ss(kgP, qk + kmaj(k), kHi128, kk_ + kmaj(k), kHi128, idesc_bf16_f32(M, 64, false, false), k > 0);
 #pragma unroll 1
@@ -671,9 +702,9 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     mma_ss(kgNE, nn + kLo + o, kHi128, e + o, kHi128, idM, true);
                 }
                 bar_commit(GBAR(doneG, 0));
-                if (!wait1(GBAR(full, 1), 0)) break;
+                if (!wait1(GBAR(full, 1), ph)) break;
                 tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
                 for (int k = 0; k < nk; ++k) {
                     constexpr uint32_t idK = idesc_bf16_f32(M, KD, false, true), idM = idesc_bf16_f32(M, KD, true, true);
                     const uint32_t o = k * kMn, ok = kmaj(k);
@@ -682,7 +713,7 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     mma_ss(kgYS, y + ok, kHi128, S + (kStateImg<KD> >> 4) + o, kHi128, idK, true);
                 }
                 bar_commit(GBAR(doneS, 0));
-                if (!wait1(GBAR(got_p, 0), 0)) break;
+                if (!wait1(GBAR(got_p, 0), ph)) break;
                 tc_fence_after();
                 {
                     constexpr uint32_t idK = idesc_bf16_f32(M, KD, false, true), idM = idesc_bf16_f32(M, KD, true, true);
@@ -697,177 +728,187 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                 }
                 bar_commit(GBAR(doneQ, 0));
-                if (!wait1(GBAR(full, 2), 0) || !wait1(GBAR(got_x, 0), 0)) break;
+                if (!wait1(GBAR(full, 2), ph)) break;          // (dS was loaded once dY S^T had been read)
                 tc_fence_after();
                 {
                     constexpr uint32_t idM = idesc_bf16_f32(M, KD, true, true);
-                    const uint32_t dS = desc_lo(s0 + Cfg::kE + kImg, Cfg::kN - Cfg::kE);
-#pragma unroll 1
+                    const uint32_t dS = desc_lo(s0 + Cfg::kS + kStateImg<KD>, kImg);
+#pragma unroll 2
                     for (int k = 0; k < nk; ++k) mma_ss(kgYS, e + k * kMn, kHi128, dS + k * kMn, kHi128, idM, k > 0);
                 }
                 bar_commit(GBAR(doneF, 0));
-            } while (false);
+            }
             // every MMA completes before the CTA exits
             bar_commit(GBAR(fin, 0));
             wait1(GBAR(fin, 0), 0);
         }
         __syncwarp();
     } else {
-        const int q4 = warp & 3, g = warp >> 2, i = 16 * q4 + (lane & 15), hl = lane >> 4;
+        const int q4 = warp & 3, gq = warp >> 2, i = 16 * q4 + (lane & 15), hl = lane >> 4;
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
-        const uint32_t gates = s0 + Cfg::kGates;
         const float scale = args.scale;
-        float x[KD / 4];                 // scale e^G dY S^T: columns KD / 2 g + 32 p + 16 hl + e
-        bool ok = waitw(GBAR(full, 0), 0) && waitw(GBAR(doneG, 0), 0);
-        float eG = 0.f, eR = 0.f, be = 0.f, acc = 0.f;
-        if (ok) {
-            tc_fence_after();
-            eG = ldsf(gates + 4 * i), eR = ldsf(gates + 4 * kC + 4 * i), be = ldsf(gates + 8 * kC + 4 * i);
-            const float Gh = ldsf(gates + kGateLog + 8 * i), Gl = ldsf(gates + kGateLog + 8 * i + 4);
-            float P[16], YE[16], NE[16], VN[16];
-            tc_ld_16x32bx2_x16<16>(tq + kgP + 32 * g, P);
-            tc_ld_16x32bx2_x16<16>(tq + kgYE + 32 * g, YE);
-            tc_ld_16x32bx2_x16<16>(tq + kgNE + 32 * g, NE);
-            tc_ld_16x32bx2_x16<16>(tq + kgVN + 32 * g, VN);
-            wait_loaded(P);
-            wait_loaded(YE);
-            wait_loaded(NE);
-            wait_loaded(VN);
-            const int j0 = 32 * g + 16 * hl;
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const int j = j0 + u;
-                const float bj = ldsf(gates + 8 * kC + 4 * j);
-                const float dec = ex2((Gh - ldsf(gates + kGateLog + 8 * j)) + (Gl - ldsf(gates + kGateLog + 8 * j + 4)));
-                const float dA = scale * bj * YE[u];
-                if (j == i) {
-                    acc -= VN[u];
-                    sm->diag[i] = NE[u];
-                }
-                if (j <= i) acc = fmaf(dec * P[u], dA, acc);
-                P[u] = j <= i ? dec * dA : 0.f;
-                NE[u] = j < i ? -bj * dec * NE[u] : 0.f;
-            }
-            const uint32_t o = s0 + sw128_offset(i, j0 >> 3), o2 = s0 + sw128_offset(i, (j0 >> 3) + 1);
-            const uint4 p0 = pack8(P), p1 = pack8(P + 8), l0 = pack8(NE), l1 = pack8(NE + 8);
-            sts4(o + Cfg::kP, p0.x, p0.y, p0.z, p0.w);
-            sts4(o2 + Cfg::kP, p1.x, p1.y, p1.z, p1.w);
-            sts4(o + Cfg::kL, l0.x, l0.y, l0.z, l0.w);
-            sts4(o2 + Cfg::kL, l1.x, l1.y, l1.z, l1.w);
-            fence_proxy_async_smem();
-            tc_fence_before();
-            bar_arrive_warp(GBAR(got_p, 0));
-        }
-        ok = ok && waitw(GBAR(full, 1), 0);
-        if (ok) {
-            // <S, dS> before the chunk: both are images of the same layout, so any order does
-            const uint4 *ds = reinterpret_cast<const uint4 *>(args.dS + (bh * (nch + 1) + c) * (2 * kStateImg<KD>));
-            constexpr int kWords = kStateImg<KD> / 16, kRow = KD / 64 * 8;    // (rows behind dv hold nothing)
-            float2 dot = make_float2(0.f, 0.f);
-#pragma unroll 4
-            for (int y = tid; y < dv * kRow; y += 32 * kGComp) {
-                const int w = y / (dv * 8) * (kImg / 16) + y % (dv * 8);
-                const uint4 dh = ds[w], dl = ds[w + kWords], sh = lds4(s0 + Cfg::kS + 16 * w), sl = lds4(s0 + Cfg::kS + kStateImg<KD> + 16 * w);
-                dot = __ffma2_rn(__fadd2_rn(unpack(dh.x), unpack(dl.x)), __fadd2_rn(unpack(sh.x), unpack(sl.x)), dot);
-                dot = __ffma2_rn(__fadd2_rn(unpack(dh.y), unpack(dl.y)), __fadd2_rn(unpack(sh.y), unpack(sl.y)), dot);
-                dot = __ffma2_rn(__fadd2_rn(unpack(dh.z), unpack(dl.z)), __fadd2_rn(unpack(sh.z), unpack(sl.z)), dot);
-                dot = __ffma2_rn(__fadd2_rn(unpack(dh.w), unpack(dl.w)), __fadd2_rn(unpack(sh.w), unpack(sl.w)), dot);
-            }
-            float p = dot.x + dot.y;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-            if (lane == 0) sm->anchor[warp] = p;
-        }
-        ok = ok && waitw(GBAR(doneS, 0), 0);
-        if (ok) {
-            tc_fence_after();
-            const float f = scale * eG;
-#pragma unroll
-            for (int p = 0; p < KD / 64; ++p) {
-                const int c0 = KD / 2 * g + 32 * p;
-                float t[16];
-                tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, t);
-                wait_loaded(t);
-                const int cc = c0 + 16 * hl;
-                const uint32_t qa = s0 + Cfg::kQ + (cc >> 6) * kTile;
-                const uint4 q0 = lds4(qa + sw128_offset(i, (cc & 63) >> 3)), q1 = lds4(qa + sw128_offset(i, ((cc & 63) >> 3) + 1));
-                const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    x[16 * p + 2 * u] = f * t[2 * u];
-                    x[16 * p + 2 * u + 1] = f * t[2 * u + 1];
-                    acc = fmaf(bf16_lo(qw[u]), x[16 * p + 2 * u], acc);
-                    acc = fmaf(bf16_hi(qw[u]), x[16 * p + 2 * u + 1], acc);
-                }
-            }
-            tc_fence_before();
-            bar_arrive_warp(GBAR(got_x, 0));
-            acc += __shfl_xor_sync(0xffffffffu, acc, 16);
-            if (hl == 0) sm->dG[g][i] = acc;
-        }
-        // (all compute warps meet here, whatever they have waited for)
-        named_barrier_sync(1, 32 * kGComp);
-        const int t0 = c * kC;
-        if (ok && warp == 0) {
-            // dlog alpha: <S, dS> before the chunk, less the terms of the tokens before each one
-            const int a0 = 2 * lane;
-            const float d0 = sm->dG[0][a0] + sm->dG[1][a0], d1 = sm->dG[0][a0 + 1] + sm->dG[1][a0 + 1];
-            float inc = d0 + d1;         // up to this lane
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            float anchor = 0.f;
-            for (int w = 0; w < kGComp; ++w) anchor += sm->anchor[w];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = t0 + a0 + u;
-                if (t >= T) continue;
-                const size_t at = bh * T + t;
-                if (args.dalpha && args.s.alpha) {
-                    const float al = args.s.alpha[at];
-                    args.dalpha[at] = al > 0.f ? (anchor - (u ? inc - d1 : inc - d0 - d1)) / al : 0.f;
-                }
-                if (args.dbeta) args.dbeta[at] = sm->diag[a0 + u] / ldsf(gates + 8 * kC + 4 * (a0 + u));
-            }
-        }
-        ok = ok && waitw(GBAR(doneQ, 0), 0) && waitw(GBAR(doneF, 0), 0);
-        if (ok) {
-            tc_fence_after();
-            const size_t row = (bh * T + t0 + i) * KD;
-            const bool in = t0 + i < T;
-            const float fe = be * eR;
-#pragma unroll
-            for (int p = 0; p < KD / 64; ++p) {
-                const int c0 = KD / 2 * g + 32 * p;
-                float a[16], k3[16], ns[16], ed[16];
-                tc_ld_16x32bx2_x16<16>(tq + kgQ + c0, a);
-                tc_ld_16x32bx2_x16<16>(tq + kgK + c0, k3);
-                tc_ld_16x32bx2_x16<16>(tq + kgNS + c0, ns);
-                tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, ed);
-                wait_loaded(a);
-                wait_loaded(k3);
-                wait_loaded(ns);
-                wait_loaded(ed);
+        bool ok = true;
+        // (a warp that gave up waiting still meets the others at their barrier)
+#pragma unroll 1
+        for (int it = 0; it < nit; ++it) {
+            const uint32_t ph = it & 1, gates = s0 + Cfg::kGates + (it & 1) * kGateStep;
+            const int c = item(it) % nch;
+            const size_t bh = item(it) / nch;
+            float x[KD / 4];                 // scale e^G dY S^T: columns KD / 2 gq + 32 p + 16 hl + u
+            ok = ok && waitw(GBAR(full, 0), ph) && waitw(GBAR(doneG, 0), ph);
+            float eG = 0.f, eR = 0.f, be = 0.f, acc = 0.f;
+            if (ok) {
+                tc_fence_after();
+                eG = ldsf(gates + 4 * i), eR = ldsf(gates + 4 * kC + 4 * i), be = ldsf(gates + 8 * kC + 4 * i);
+                const float Gh = ldsf(gates + kGateLog + 8 * i), Gl = ldsf(gates + kGateLog + 8 * i + 4);
+                float P[16], YE[16], NE[16], VN[16];
+                tc_ld_16x32bx2_x16<16>(tq + kgP + 32 * gq, P);
+                tc_ld_16x32bx2_x16<16>(tq + kgYE + 32 * gq, YE);
+                tc_ld_16x32bx2_x16<16>(tq + kgNE + 32 * gq, NE);
+                tc_ld_16x32bx2_x16<16>(tq + kgVN + 32 * gq, VN);
+                wait_loaded(P);
+                wait_loaded(YE);
+                wait_loaded(NE);
+                wait_loaded(VN);
+                const int j0 = 32 * gq + 16 * hl;
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
-                    a[u] += x[16 * p + u];
-                    k3[u] = fmaf(fe, ed[u], fmaf(-eG, ns[u], k3[u]));
+                    const int j = j0 + u;
+                    const float bj = ldsf(gates + 8 * kC + 4 * j);
+                    const float dec = ex2((Gh - ldsf(gates + kGateLog + 8 * j)) + (Gl - ldsf(gates + kGateLog + 8 * j + 4)));
+                    const float dA = scale * bj * YE[u];
+                    if (j == i) {
+                        acc -= VN[u];
+                        sm->diag[i] = NE[u];
+                    }
+                    if (j <= i) acc = fmaf(dec * P[u], dA, acc);
+                    P[u] = j <= i ? dec * dA : 0.f;
+                    NE[u] = j < i ? -bj * dec * NE[u] : 0.f;
                 }
-                if (in) {
-                    const size_t at = row + c0 + 16 * hl;
-                    if (OUT32) {
+                const uint32_t o = s0 + sw128_offset(i, j0 >> 3), o2 = s0 + sw128_offset(i, (j0 >> 3) + 1);
+                const uint4 p0 = pack8(P), p1 = pack8(P + 8), l0 = pack8(NE), l1 = pack8(NE + 8);
+                sts4(o + Cfg::kP, p0.x, p0.y, p0.z, p0.w);
+                sts4(o2 + Cfg::kP, p1.x, p1.y, p1.z, p1.w);
+                sts4(o + Cfg::kL, l0.x, l0.y, l0.z, l0.w);
+                sts4(o2 + Cfg::kL, l1.x, l1.y, l1.z, l1.w);
+                fence_proxy_async_smem();
+                tc_fence_before();
+                bar_arrive_warp(GBAR(got_p, 0));
+            }
+            ok = ok && waitw(GBAR(full, 1), ph);
+            if (ok) {
+                // <S, dS> before the chunk: both are images of the same layout, so any order does
+                const uint4 *ds = reinterpret_cast<const uint4 *>(args.dS + (bh * (nch + 1) + c) * (2 * kStateImg<KD>));
+                constexpr int kWords = kStateImg<KD> / 16, kRow = KD / 64 * 8;    // (rows behind dv hold nothing)
+                float2 dot = make_float2(0.f, 0.f);
+#pragma unroll 4
+                for (int y = tid; y < dv * kRow; y += 32 * kGComp) {
+                    const int w = y / (dv * 8) * (kImg / 16) + y % (dv * 8);
+                    const uint4 dh = ds[w], dl = ds[w + kWords], sh = lds4(s0 + Cfg::kS + 16 * w), sl = lds4(s0 + Cfg::kS + kStateImg<KD> + 16 * w);
+                    dot = __ffma2_rn(__fadd2_rn(unpack(dh.x), unpack(dl.x)), __fadd2_rn(unpack(sh.x), unpack(sl.x)), dot);
+                    dot = __ffma2_rn(__fadd2_rn(unpack(dh.y), unpack(dl.y)), __fadd2_rn(unpack(sh.y), unpack(sl.y)), dot);
+                    dot = __ffma2_rn(__fadd2_rn(unpack(dh.z), unpack(dl.z)), __fadd2_rn(unpack(sh.z), unpack(sl.z)), dot);
+                    dot = __ffma2_rn(__fadd2_rn(unpack(dh.w), unpack(dl.w)), __fadd2_rn(unpack(sh.w), unpack(sl.w)), dot);
+                }
+                float p = dot.x + dot.y;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            reinterpret_cast<float4 *>(static_cast<float *>(args.dq) + at)[u] = make_float4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
-                            reinterpret_cast<float4 *>(static_cast<float *>(args.dk) + at)[u] = make_float4(k3[4 * u], k3[4 * u + 1], k3[4 * u + 2], k3[4 * u + 3]);
-                        }
-                    } else {
+                for (int o = 16; o; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+                if (lane == 0) sm->anchor[warp] = p;
+            }
+            ok = ok && waitw(GBAR(doneS, 0), ph);
+            if (ok) {
+                tc_fence_after();
+                const float f = scale * eG;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(args.dq) + at)[u] = pack8(a + 8 * u);
-                            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(args.dk) + at)[u] = pack8(k3 + 8 * u);
+                for (int p = 0; p < KD / 64; ++p) {
+                    const int c0 = KD / 2 * gq + 32 * p;
+                    float t[16];
+                    tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, t);
+                    wait_loaded(t);
+                    const int cc = c0 + 16 * hl;
+                    const uint32_t qa = s0 + Cfg::kQ + (cc >> 6) * kTile;
+                    const uint4 q0 = lds4(qa + sw128_offset(i, (cc & 63) >> 3)), q1 = lds4(qa + sw128_offset(i, ((cc & 63) >> 3) + 1));
+                    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        x[16 * p + 2 * u] = f * t[2 * u];
+                        x[16 * p + 2 * u + 1] = f * t[2 * u + 1];
+                        acc = fmaf(bf16_lo(qw[u]), x[16 * p + 2 * u], acc);
+                        acc = fmaf(bf16_hi(qw[u]), x[16 * p + 2 * u + 1], acc);
+                    }
+                }
+                tc_fence_before();
+                bar_arrive_warp(GBAR(got_x, 0));
+                acc += __shfl_xor_sync(0xffffffffu, acc, 16);
+                if (hl == 0) sm->dG[gq][i] = acc;
+            }
+            named_barrier_sync(1, 32 * kGComp);
+            const int t0 = c * kC;
+            if (ok && warp == 0) {
+                // dlog alpha: <S, dS> before the chunk, less the terms of the tokens before each one
+                const int a0 = 2 * lane;
+                const float d0 = sm->dG[0][a0] + sm->dG[1][a0], d1 = sm->dG[0][a0 + 1] + sm->dG[1][a0 + 1];
+                float inc = d0 + d1;         // up to this lane
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                float anchor = 0.f;
+                for (int w = 0; w < kGComp; ++w) anchor += sm->anchor[w];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = t0 + a0 + u;
+                    if (t >= T) continue;
+                    const size_t at = bh * T + t;
+                    if (args.dalpha && args.s.alpha) {
+                        const float al = args.s.alpha[at];
+                        args.dalpha[at] = al > 0.f ? (anchor - (u ? inc - d1 : inc - d0 - d1)) / al : 0.f;
+                    }
+                    if (args.dbeta) args.dbeta[at] = sm->diag[a0 + u] / ldsf(gates + 8 * kC + 4 * (a0 + u));
+                }
+            }
+            ok = ok && waitw(GBAR(doneQ, 0), ph) && waitw(GBAR(doneF, 0), ph);
+            if (ok) {
+                tc_fence_after();
+                const size_t row = (bh * T + t0 + i) * KD;
+                const bool in = t0 + i < T;
+                const float fe = be * eR;
+#pragma unroll
+                for (int p = 0; p < KD / 64; ++p) {
+                    const int c0 = KD / 2 * gq + 32 * p;
+                    float a[16], k3[16], ns[16], ed[16];
+                    tc_ld_16x32bx2_x16<16>(tq + kgQ + c0, a);
+                    tc_ld_16x32bx2_x16<16>(tq + kgK + c0, k3);
+                    tc_ld_16x32bx2_x16<16>(tq + kgNS + c0, ns);
+                    tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, ed);
+                    wait_loaded(a);
+                    wait_loaded(k3);
+                    wait_loaded(ns);
+                    wait_loaded(ed);
+                    if (p == KD / 64 - 1) {
+                        tc_fence_before();
+                        bar_arrive_warp(GBAR(got_e, 0));
+                    }
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        a[u] += x[16 * p + u];
+                        k3[u] = fmaf(fe, ed[u], fmaf(-eG, ns[u], k3[u]));
+                    }
+                    if (in) {
+                        const size_t at = row + c0 + 16 * hl;
+                        if (OUT32) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                reinterpret_cast<float4 *>(static_cast<float *>(args.dq) + at)[u] = make_float4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
+                                reinterpret_cast<float4 *>(static_cast<float *>(args.dk) + at)[u] = make_float4(k3[4 * u], k3[4 * u + 1], k3[4 * u + 2], k3[4 * u + 3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                reinterpret_cast<uint4 *>(static_cast<uint16_t *>(args.dq) + at)[u] = pack8(a + 8 * u);
+                                reinterpret_cast<uint4 *>(static_cast<uint16_t *>(args.dk) + at)[u] = pack8(k3 + 8 * u);
+                            }
                         }
                     }
                 }
@@ -906,7 +947,7 @@ BackSpace back_space(const GdeltaShape &s)
 }
 
 template <int KD>
-cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const GdeltaTcArgs &prep, cudaStream_t stream)
+cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const GdeltaTcArgs &prep, int sms, cudaStream_t stream)
 {
     static OncePerDevice once_f, once_r, once_g, once_g32;
     cudaError_t e;
@@ -920,8 +961,9 @@ cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const Gdelt
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     gdelta_back_chain_kernel<KD, true><<<heads, kThreads, kBSmemBytes<KD, true>, stream>>>(m.q, m.k, m.dy, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (a.s.Hk < a.s.H) gdelta_grad_kernel<KD, true><<<chunks, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a);
-    else gdelta_grad_kernel<KD, false><<<chunks, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a);
+    const unsigned grid = sms > 0 && (unsigned)sms < chunks ? sms : chunks;
+    if (a.s.Hk < a.s.H) gdelta_grad_kernel<KD, true><<<grid, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a, (int)chunks);
+    else gdelta_grad_kernel<KD, false><<<grid, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a, (int)chunks);
     return cudaGetLastError();
 }
 
@@ -929,7 +971,8 @@ cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const Gdelt
 
 size_t gdelta_tc_backward_bytes(const GdeltaShape &s) { return back_space(s).bytes; }
 
-cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, cudaStream_t stream)
+cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, int sms,
+                                      cudaStream_t stream)
 {
     const BackSpace p = back_space(s);
     uint8_t *ws = reinterpret_cast<uint8_t *>(g.ws);
@@ -947,7 +990,7 @@ cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaSha
     const bool shared = s.Hk < s.H;
     a.dq = shared ? ws + p.dq : g.dq;
     a.dk = shared ? ws + p.dk : g.dk;
-    const cudaError_t e = s.r == 64 ? launch_as<64>(m, a, prep, stream) : launch_as<128>(m, a, prep, stream);
+    const cudaError_t e = s.r == 64 ? launch_as<64>(m, a, prep, sms, stream) : launch_as<128>(m, a, prep, sms, stream);
     if (e != cudaSuccess || !shared) return e;
     return launch_gdelta_group_sum(s, static_cast<const float *>(a.dq), static_cast<const float *>(a.dk), true, g.dq, g.dk, stream);
 }

@@ -45,7 +45,8 @@ struct GdeltaTcBackArgs {
     uint8_t *ws = nullptr, *E = nullptr, *N = nullptr, *S = nullptr, *dS = nullptr;
 };
 size_t gdelta_tc_backward_bytes(const GdeltaShape &s);
-cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, cudaStream_t stream);
+cudaError_t launch_gdelta_tc_backward(const GdeltaTcBackMaps &m, const GdeltaShape &s, const GdeltaBackward &g, int sms,
+                                      cudaStream_t stream);
 cudaError_t launch_gdelta_prep_backward(const CUtensorMap &q, const CUtensorMap &k, const GdeltaTcArgs &a, cudaStream_t stream);
 
 }  // namespace la
