@@ -13,8 +13,8 @@
 //     dbeta_j = Z_jj / beta_j                                                       (N_j is beta_j times its error's gradient)
 //     dlog alpha_t = <S, dS_before> - sum_{s < t, in the chunk} (q_s . (scale e^G dY S^T)_s + sum_j A_sj dA_sj - v_s . N_s)
 // (the gates' gradient is anchored before every chunk, so that nothing is summed over the sequence).
-// Kernels: gdelta_prep (A, X, gates), the forward chain again, keeping the states between the chunks and E, the backward chain,
-// keeping their gradients and N, and a kernel over all chunks.
+// Kernels: gdelta_prep (A, X, gates, scale e^G Q); the forward chain again, keeping the states between the chunks and E, and beside
+// it the backward chain, keeping their gradients and N; and a kernel over all chunks.
 // Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand; what reaches dq and
 // dk only, the high one.
 
@@ -66,16 +66,15 @@ struct alignas(16) BSmall {
 };
 #define BBAR(name, i) (sS + (uint32_t)offsetof(BSmall, name) + 8 * (uint32_t)(i))
 
-template <int KD, bool REV>
-constexpr uint32_t kBSmemBytes = BackCfg<KD, REV>::kSmall + sizeof(BSmall) + 1024;
-static_assert(kBSmemBytes<128, true> <= 232448 && kBSmemBytes<128, false> <= 232448, "shared memory budget");
+template <int KD>
+constexpr uint32_t kBSmemBytes = (BackCfg<KD, true>::kSmall > BackCfg<KD, false>::kSmall ? BackCfg<KD, true>::kSmall : BackCfg<KD, false>::kSmall) +
+                                 sizeof(BSmall) + 1024;
+static_assert(kBSmemBytes<128> <= 232448, "shared memory budget");
 
 __device__ __forceinline__ float2 unpack(uint32_t x) { return make_float2(bf16_lo(x), bf16_hi(x)); }
 
 template <int KD, bool REV>
-__global__ void __launch_bounds__(kThreads, 1)
-gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ GdeltaTcBackArgs args)
+__device__ __forceinline__ void back_chain(const CUtensorMap &map_k, const CUtensorMap &map_v, const GdeltaTcBackArgs &args, int head)
 {
     using Cfg = BackCfg<KD, REV>;
     constexpr int KH = KD / 2, KQ = KD / 4;
@@ -88,8 +87,8 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = args.s.H, dv = args.s.dv, T = args.s.T, nch = (T + kC - 1) / kC;
-    const int h = blockIdx.x % H, b = blockIdx.x / H;
-    const size_t bh = blockIdx.x;
+    const int h = head % H, b = head / H;
+    const size_t bh = head;
     auto chunk = [&](int n) { return REV ? nch - 1 - n : n; };
 
     if (tid == 0) {
@@ -548,6 +547,16 @@ gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid
     }
 }
 
+// Both chains of every head, side by side: neither needs the other's results.
+template <int KD>
+__global__ void __launch_bounds__(kThreads, 1)
+gdelta_back_chain_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ GdeltaTcBackArgs args)
+{
+    if (blockIdx.x & 1) back_chain<KD, false>(map_k, map_v, args, blockIdx.x >> 1);
+    else back_chain<KD, true>(map_k, map_dy, args, blockIdx.x >> 1);
+}
+
 // -------------------------------------------------- the gradients of a chunk
 // One CTA per SM walks the chunks of all heads: 8 warps compute (warp w: rows 16 (w % 4) .. of the M = 64 accumulators, half w / 4
 // of their columns), one issues the MMAs, one loads.  What a chunk needs fills shared memory, so the next one's operands come into
@@ -949,17 +958,14 @@ BackSpace back_space(const GdeltaShape &s)
 template <int KD>
 cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const GdeltaTcArgs &prep, int sms, cudaStream_t stream)
 {
-    static OncePerDevice once_f, once_r, once_g, once_g32;
+    static OncePerDevice once_c, once_g, once_g32;
     cudaError_t e;
-    if ((e = set_smem_once(gdelta_back_chain_kernel<KD, false>, kBSmemBytes<KD, false>, once_f)) != cudaSuccess) return e;
-    if ((e = set_smem_once(gdelta_back_chain_kernel<KD, true>, kBSmemBytes<KD, true>, once_r)) != cudaSuccess) return e;
+    if ((e = set_smem_once(gdelta_back_chain_kernel<KD>, kBSmemBytes<KD>, once_c)) != cudaSuccess) return e;
     if ((e = set_smem_once(gdelta_grad_kernel<KD, false>, kGSmemBytes<KD>, once_g)) != cudaSuccess) return e;
     if ((e = set_smem_once(gdelta_grad_kernel<KD, true>, kGSmemBytes<KD>, once_g32)) != cudaSuccess) return e;
     const unsigned heads = (unsigned)(a.s.B * a.s.H), chunks = heads * (unsigned)((a.s.T + kC - 1) / kC);
     if ((e = launch_gdelta_prep_backward(m.q, m.k, prep, stream)) != cudaSuccess) return e;
-    gdelta_back_chain_kernel<KD, false><<<heads, kThreads, kBSmemBytes<KD, false>, stream>>>(m.q, m.k, m.v, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    gdelta_back_chain_kernel<KD, true><<<heads, kThreads, kBSmemBytes<KD, true>, stream>>>(m.q, m.k, m.dy, a);
+    gdelta_back_chain_kernel<KD><<<2 * heads, kThreads, kBSmemBytes<KD>, stream>>>(m.k, m.v, m.dy, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const unsigned grid = sms > 0 && (unsigned)sms < chunks ? sms : chunks;
     if (a.s.Hk < a.s.H) gdelta_grad_kernel<KD, true><<<grid, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a, (int)chunks);
