@@ -80,6 +80,65 @@ __device__ __forceinline__ void widen(uint4 w, float *x)
     }
 }
 
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// x - m of the two BF16 values in w, without widening them first
+__device__ __forceinline__ float2 minus_bf16x2(uint32_t w, float m)
+{
+    float2 d;
+    asm("{\n\t.reg .b16 a, b, one;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "mov.b16 one, 0x3F80;\n\t"
+        "fma.rn.f32.bf16 %0, a, one, %3;\n\t"
+        "fma.rn.f32.bf16 %1, b, one, %3;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(w), "f"(-m));
+    return d;
+}
+// Logits below this (a BF16 number) count as this in the sums, so that x - m stays finite and a masked one's term is 0; what a
+// lane with nothing above it, or with a maximum as far up, has seen is summed again with care.
+constexpr float kFloor = -1.171875f * 0x1p126f;  // -9.97e37
+
+// Largest of a granule's values (a NaN among them does not show), and its values, at least `floor`, less m.
+template <bool BF16>
+__device__ __forceinline__ float granule_max(uint4 w)
+{
+    if (BF16) {
+        uint32_t a, b, c;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w.x), "r"(w.y));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w.z), "r"(w.w));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+        return fmaxf(bf16_lo(c), bf16_hi(c));
+    }
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+template <bool BF16>
+__device__ __forceinline__ void granule_minus(uint4 w, float m, float floor, float2 *d)
+{
+    if (BF16) {
+        const uint32_t f = pack_bf16x2(floor, floor);
+        d[0] = minus_bf16x2(max_nan_bf16x2(w.x, f), m);
+        d[1] = minus_bf16x2(max_nan_bf16x2(w.y, f), m);
+        d[2] = minus_bf16x2(max_nan_bf16x2(w.z, f), m);
+        d[3] = minus_bf16x2(max_nan_bf16x2(w.w, f), m);
+    } else {
+        const float2 minus = make_float2(-m, -m);
+        d[0] = __fadd2_rn(make_float2(max_nan(__uint_as_float(w.x), floor), max_nan(__uint_as_float(w.y), floor)), minus);
+        d[1] = __fadd2_rn(make_float2(max_nan(__uint_as_float(w.z), floor), max_nan(__uint_as_float(w.w), floor)), minus);
+    }
+}
+
 template <bool BF16>
 __device__ __forceinline__ float load_elem(const void *p, long long i)
 {
@@ -175,7 +234,7 @@ token_logprobs_kernel(const LogprobArgs args)
         if (tid == 0) sm.count = 0;
         __syncthreads();
     }
-    float m = kLowest, s = 0.f, w = 0.f;
+    float m = kFloor, s = 0.f, w = 0.f;
     for (int j = 0, blk = gw; blk < blocks; j += U, blk += U * nw) {
         uint4 raw[U];
 #pragma unroll
@@ -184,28 +243,22 @@ token_logprobs_kernel(const LogprobArgs args)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (blk + u * nw >= blocks) break;
-            float x[GE];
-            widen<BF16>(raw[u], x);
-            float mx = x[0];
-#pragma unroll
-            for (int e = 1; e < GE; ++e) mx = fmaxf(mx, x[e]);   // (a NaN reaches the sums below)
+            const float mx = granule_max<BF16>(raw[u]);
             if (mx > m) {
                 const float d = fmaxf((m - mx) * kLog2e, -400.f);
                 w = (w + s * d) * ex2(d);
                 s *= ex2(d);
                 m = mx;
             }
-            const float2 minus = make_float2(-m, -m), l2 = make_float2(kLog2e, kLog2e);
-            float2 t = make_float2(0.f, 0.f), tw = t;
+            const float2 l2 = make_float2(kLog2e, kLog2e);
+            float2 t = make_float2(0.f, 0.f), tw = t, a[GE / 2];
+            granule_minus<BF16>(raw[u], m, kFloor, a);
 #pragma unroll
-            for (int e = 0; e < GE; e += 2) {
-                float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[e], x[e + 1]), minus), l2);
-                // (a masked logit's a would be -infinity, and a 2^a not a number; a NaN stays one)
-                a.x = a.x < -200.f ? -200.f : a.x;
-                a.y = a.y < -200.f ? -200.f : a.y;
-                const float2 p = make_float2(ex2(a.x), ex2(a.y));
+            for (int e = 0; e < GE / 2; ++e) {
+                a[e] = __fmul2_rn(a[e], l2);
+                const float2 p = make_float2(ex2(a[e].x), ex2(a[e].y));
                 t = __fadd2_rn(t, p);
-                tw = __ffma2_rn(a, p, tw);
+                tw = __ffma2_rn(a[e], p, tw);
             }
             s += t.x + t.y;
             w += tw.x + tw.y;
@@ -215,6 +268,24 @@ token_logprobs_kernel(const LogprobArgs args)
                 if (lane == 0 && o > en) en = o;
             }
         }
+    }
+    // (masks and lowest values only, or none at all, up to a whole row of them; a maximum of +infinity stays: its sums are not
+    // numbers)
+    const bool odd = m <= kFloor || (m >= -kFloor && m < INFINITY);
+    if (__any_sync(0xffffffffu, odd)) {
+        if (odd) {
+            m = kLowest, s = w = 0.f;
+            for (int blk = gw; blk < blocks; blk += nw) {
+                float x[GE];
+                widen<BF16>(load_granule<BF16, ALIGNED>(row, blk, lane, V), x);
+#pragma unroll
+                for (int e = 0; e < GE; ++e) {
+                    if (x[e] > -INFINITY) merge(m, s, w, x[e], 1.f, 0.f);
+                    if (x[e] != x[e]) s = x[e];
+                }
+            }
+        }
+        __syncwarp();
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -249,8 +320,10 @@ token_logprobs_kernel(const LogprobArgs args)
             rc += g > c || (g == c && i < lane + 32);
         }
         const uint32_t thr = max(1u, __reduce_max_sync(0xffffffffu, ra == top - 1 ? a : rc == top - 1 ? c : 0u));
-        for (int e = 0; e < kEntries; ++e) {
-            if (sm.entry[warp][e] < thr) continue;
+        unsigned long long reach = __ballot_sync(0xffffffffu, sm.entry[warp][lane] >= thr) |
+                                   (unsigned long long)__ballot_sync(0xffffffffu, sm.entry[warp][lane + 32] >= thr) << 32;
+        for (; reach; reach &= reach - 1) {
+            const int e = __ffsll(reach) - 1;
             for (int j = e << shift, blk = gw + j * nw; j < (e + 1) << shift && blk < blocks; ++j, blk += nw) {
                 float x[GE];
                 widen<BF16>(load_granule<BF16, ALIGNED>(row, blk, lane, V), x);
@@ -296,16 +369,28 @@ token_logprobs_kernel(const LogprobArgs args)
         }
         if (warp == 0) {
             const int have = count > kCand ? kWarps * top : count;
-            unsigned long long last = ~0ull;
+            if (have <= 64) {
+                // (the usual case: a key or two per lane)
+                unsigned long long k0 = lane < have ? sm.cand[lane] : 0, k1 = lane + 32 < have ? sm.cand[lane + 32] : 0;
 #pragma unroll 1
-            for (int r = 0; r < top; ++r) {
-                unsigned long long best = 0;
-                for (int i = lane; i < have; i += 32) {
-                    const unsigned long long k = sm.cand[i];
-                    if (k < last && k > best) best = k;
+                for (int r = 0; r < top; ++r) {
+                    const unsigned long long best = warp_max(k0 > k1 ? k0 : k1);
+                    if (lane == r) sm.best[r] = best;
+                    if (k0 == best) k0 = 0;
+                    if (k1 == best) k1 = 0;
                 }
-                last = warp_max(best);
-                if (lane == 0) sm.best[r] = last;
+            } else {
+                unsigned long long last = ~0ull;
+#pragma unroll 1
+                for (int r = 0; r < top; ++r) {
+                    unsigned long long best = 0;
+                    for (int i = lane; i < have; i += 32) {
+                        const unsigned long long k = sm.cand[i];
+                        if (k < last && k > best) best = k;
+                    }
+                    last = warp_max(best);
+                    if (lane == 0) sm.best[r] = last;
+                }
             }
         }
     }
@@ -326,25 +411,30 @@ token_logprobs_kernel(const LogprobArgs args)
             if (args.entropy) args.entropy[n] = fine ? fmaxf(lg - kLn2 * (w / s), 0.f) : empty ? 0.f : nan;
             if (args.lse) args.lse[n] = fine ? m + lg : empty ? -INFINITY : nan;
         }
-        unsigned long long last = ~0ull;
+        // the best of the CTAs' best: lane r ends with the r-th
+        unsigned long long mine = 0;
+        if (top && cs == 1) {
+            mine = lane < top ? sm.best[lane] : 0;
+        } else if (top) {
+            unsigned long long k[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = i < (int)cs && lane < top ? in_cta(&sm, i)->best[lane] : 0;
 #pragma unroll 1
-        for (int r = 0; r < top; ++r) {
-            if (cs > 1) {
-                unsigned long long best = 0;
-                for (int i = lane; i < (int)cs * top; i += 32) {
-                    const unsigned long long k = in_cta(&sm, i / top)->best[i % top];
-                    if (k < last && k > best) best = k;
-                }
-                last = warp_max(best);
-            } else {
-                last = sm.best[r];
+            for (int r = 0; r < top; ++r) {
+                unsigned long long best = k[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) best = k[i] > best ? k[i] : best;
+                best = warp_max(best);
+                if (lane == r) mine = best;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (k[i] == best) k[i] = 0;
             }
-            if (lane == 0) {
-                const bool have = fine && last != 0;
-                args.top_logprobs[n * top + r] = have ? (unorder_f32((uint32_t)(last >> 32)) - m) - lg : -INFINITY;
-                args.top_tokens[n * top + r] = have ? (int)(0xffffffffu - (uint32_t)last) : -1;
-            }
-            if (last == 0) last = 1;      // (nothing is below it)
+        }
+        if (lane < top) {
+            const bool have = fine && mine != 0;
+            args.top_logprobs[n * top + lane] = have ? (unorder_f32((uint32_t)(mine >> 32)) - m) - lg : -INFINITY;
+            args.top_tokens[n * top + lane] = have ? (int)(0xffffffffu - (uint32_t)mine) : -1;
         }
     }
     if (cs > 1) cluster_sync_all();       // a CTA's shared memory stays until it has been read
@@ -437,16 +527,33 @@ token_logprobs_backward_kernel(const LogprobGradArgs args, int slices)
             const int blk = block_of(sl, u);
             if (blk >= blocks) break;
             const int i0 = ALIGNED ? (blk * 32 + lane) * GE : blk * 32 * GE + lane;
-            float x[GE], gr[GE];
-            if (!zero) widen<BF16>(raw[u], x);
+            float gr[GE];
+            if (zero) {
 #pragma unroll
-            for (int e = 0; e < GE; ++e) {
-                gr[e] = 0.f;
-                if (!zero) {
-                    float lp = (x[e] - m) - lg;
-                    lp = lp < -200.f ? -200.f : lp;        // (a masked logit: p = 0, and not 0 times infinity)
-                    gr[e] = -ex2(lp * kLog2e) * fmaf(dH, lp, c0);
-                    if (i0 + e * ES == token) gr[e] += dlp;
+                for (int e = 0; e < GE; ++e) gr[e] = 0.f;
+            } else {
+                // (log p of at least -200, where p is 0: a masked logit's is not infinite)
+                float2 lp[GE / 2];
+                if (!far) {
+                    granule_minus<BF16>(raw[u], m, m - 200.f, lp);
+                } else {
+                    float x[GE];
+                    widen<BF16>(raw[u], x);
+#pragma unroll
+                    for (int e = 0; e < GE / 2; ++e)
+                        lp[e] = make_float2(max_nan((x[2 * e] - m) - lg, -200.f), max_nan((x[2 * e + 1] - m) - lg, -200.f));
+                }
+#pragma unroll
+                for (int e = 0; e < GE / 2; ++e) {
+                    const float2 a = __fmul2_rn(lp[e], make_float2(kLog2e, kLog2e));
+                    const float2 g = __fmul2_rn(make_float2(-ex2(a.x), -ex2(a.y)), __ffma2_rn(make_float2(dH, dH), lp[e], make_float2(c0, c0)));
+                    gr[2 * e] = g.x, gr[2 * e + 1] = g.y;
+                }
+                const int at = token - i0;
+                if (at >= 0 && at < GE * ES && at % ES == 0) {
+#pragma unroll
+                    for (int e = 0; e < GE; ++e)
+                        if (at == e * ES) gr[e] += dlp;
                 }
             }
             if (ALIGNED && i0 + GE <= V) {

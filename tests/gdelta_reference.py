@@ -140,9 +140,10 @@ def score(logits, tokens, top):
                 lg = float(d.exp().sum().log())
                 p = (d - lg).exp()
                 H = lg - float((p * torch.where(p > 0, d, 0.0)).sum())
-                order = sorted((-float(d[i]), i) for i in range(len(d)) if d[i] != -math.inf)[:top]
-                best = [-s - lg for s, _ in order] + [-math.inf] * (top - len(order))
-                vals = (float(d[t]) - lg, H, m + lg, best, [i for _, i in order] + [-1] * (top - len(order)))
+                val, at = torch.sort(d, descending=True, stable=True)
+                order = [(float(a), int(b)) for a, b in zip(val[:top], at[:top]) if a != -math.inf]
+                best = [a - lg for a, _ in order] + [-math.inf] * (top - len(order))
+                vals = (float(d[t]) - lg, H, m + lg, best, [b for _, b in order] + [-1] * (top - len(order)))
         for o, v in zip(outs, vals):
             o.append(v)
     res = [torch.tensor(o, dtype=torch.float64) for o in outs[:4]]
