@@ -173,7 +173,7 @@ __device__ __forceinline__ uint4 load_granule(const void *row, int blk, int lane
 // alternatives, out of L2), and what reaches it is sorted.
 // Bound by HBM and, within a fifth of it, by exponentials and issue slots.
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kEntries = 64;       // block maxima per warp: an entry covers 2^shift of its blocks
+constexpr int kEntries = 64;       // maxima per warp: an entry covers 2^shift of its groups of 4 blocks
 constexpr int kGroups = 64;        // of a CTA's entries: 8 per warp
 constexpr int kCand = 512;
 
@@ -184,6 +184,7 @@ struct ScoreSmem {
     unsigned long long best[kMaxTop];              // this CTA's
     float m[kWarps], s[kWarps], w[kWarps];
     float cm, cs, cw;                              // the CTA's
+    uint32_t thr;                                  // what an alternative reaches at least
     int count;
 };
 
@@ -200,7 +201,7 @@ __device__ __forceinline__ void merge(float &m, float &s, float &w, float m2, fl
 }
 
 template <bool BF16, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 token_logprobs_kernel(const LogprobArgs args)
 {
     constexpr int GE = BF16 ? 8 : 4, ES = ALIGNED ? 1 : 32, U = 4;
@@ -228,30 +229,29 @@ token_logprobs_kernel(const LogprobArgs args)
     const int blocks = (V + 32 * GE - 1) / (32 * GE);
     const int nw = kWarps * cs, gw = rank * kWarps + warp;
     int shift = 0;
-    while (((blocks + nw - 1) / nw - 1) >> shift >= kEntries) ++shift;
+    while (((blocks + U * nw - 1) / (U * nw) - 1) >> shift >= kEntries) ++shift;
     if (top) {
-        for (int i = tid; i < kWarps * kEntries; i += kThreads) (&sm.entry[0][0])[i] = 0;
+        sm.entry[warp][lane] = sm.entry[warp][lane + 32] = 0;
         if (tid == 0) sm.count = 0;
-        __syncthreads();
+        __syncwarp();
     }
     float m = kFloor, s = 0.f, w = 0.f;
-    for (int j = 0, blk = gw; blk < blocks; j += U, blk += U * nw) {
-        uint4 raw[U];
+    // takes U granules of this lane into m, s and w, and their maximum into the group's entry
+    auto take = [&](const uint4 (&raw)[U], int group) {
+        float mx = granule_max<BF16>(raw[0]);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (blk + u * nw < blocks) raw[u] = load_granule<BF16, ALIGNED>(row, blk + u * nw, lane, V);
+        for (int u = 1; u < U; ++u) mx = fmaxf(mx, granule_max<BF16>(raw[u]));   // (a NaN reaches the sums below)
+        if (mx > m) {
+            const float d = fmaxf((m - mx) * kLog2e, -400.f);
+            w = (w + s * d) * ex2(d);
+            s *= ex2(d);
+            m = mx;
+        }
+        const float2 l2 = make_float2(kLog2e, kLog2e);
+        float2 t = make_float2(0.f, 0.f), tw = t;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (blk + u * nw >= blocks) break;
-            const float mx = granule_max<BF16>(raw[u]);
-            if (mx > m) {
-                const float d = fmaxf((m - mx) * kLog2e, -400.f);
-                w = (w + s * d) * ex2(d);
-                s *= ex2(d);
-                m = mx;
-            }
-            const float2 l2 = make_float2(kLog2e, kLog2e);
-            float2 t = make_float2(0.f, 0.f), tw = t, a[GE / 2];
+            float2 a[GE / 2];
             granule_minus<BF16>(raw[u], m, kFloor, a);
 #pragma unroll
             for (int e = 0; e < GE / 2; ++e) {
@@ -260,14 +260,28 @@ token_logprobs_kernel(const LogprobArgs args)
                 t = __fadd2_rn(t, p);
                 tw = __ffma2_rn(a[e], p, tw);
             }
-            s += t.x + t.y;
-            w += tw.x + tw.y;
-            if (top) {
-                const uint32_t o = __reduce_max_sync(0xffffffffu, mx > -INFINITY ? order_f32(mx) : 0u);
-                uint32_t &en = sm.entry[warp][(j + u) >> shift];
-                if (lane == 0 && o > en) en = o;
-            }
         }
+        s += t.x + t.y;
+        w += tw.x + tw.y;
+        if (top) {
+            const uint32_t o = __reduce_max_sync(0xffffffffu, mx > -INFINITY ? order_f32(mx) : 0u);
+            uint32_t &en = sm.entry[warp][group >> shift];
+            if (lane == 0 && o > en) en = o;
+        }
+    };
+    int blk = gw, group = 0;
+    // (whole groups of aligned rows need no look at the row's end)
+    for (; ALIGNED && (long long)(blk + (U - 1) * nw + 1) * 32 * GE <= V; blk += U * nw, ++group) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = ld_once(reinterpret_cast<const uint4 *>(row) + ((blk + u * nw) * 32 + lane));
+        take(raw, group);
+    }
+    for (; blk < blocks; blk += U * nw, ++group) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = load_granule<BF16, ALIGNED>(row, blk + u * nw, lane, V);   // (-infinity behind the row)
+        take(raw, group);
     }
     // (masks and lowest values only, or none at all, up to a whole row of them; a maximum of +infinity stays: its sums are not
     // numbers)
@@ -304,35 +318,54 @@ token_logprobs_kernel(const LogprobArgs args)
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        m = sm.m[0], s = sm.s[0], w = sm.w[0];
-        for (int i = 1; i < kWarps; ++i) merge(m, s, w, sm.m[i], sm.s[i], sm.w[i]);
-        sm.cm = m, sm.cs = s, sm.cw = w;
+    if (warp == 0) {
+        m = lane < kWarps ? sm.m[lane] : kLowest, s = lane < kWarps ? sm.s[lane] : 0.f, w = lane < kWarps ? sm.w[lane] : 0.f;
+#pragma unroll
+        for (int o = kWarps / 2; o; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o),
+                        w2 = __shfl_xor_sync(0xffffffffu, w, o);
+            merge(m, s, w, m2, s2, w2);
+        }
+        if (lane == 0) sm.cm = m, sm.cs = s, sm.cw = w;
     }
     if (top) {
-        // the top-th largest group maximum, found by every warp for itself: lane l ranks groups l and l + 32
-        const uint32_t a = sm.group[lane], c = sm.group[lane + 32];
-        int ra = 0, rc = 0;
-#pragma unroll 8
-        for (int i = 0; i < kGroups; ++i) {
-            const uint32_t g = sm.group[i];
-            ra += g > a || (g == a && i < lane);
-            rc += g > c || (g == c && i < lane + 32);
+        // the top-th largest group maximum: four lanes rank a group, a warp its own eight
+        const int g = warp * 8 + (lane >> 2);
+        const uint32_t mine = sm.group[g];
+        int rank = 0;
+#pragma unroll
+        for (int i = 0; i < kGroups / 4; ++i) {
+            const int o = i * 4 + (lane & 3);
+            const uint32_t v = sm.group[o];
+            rank += v > mine || (v == mine && o < g);
         }
-        const uint32_t thr = max(1u, __reduce_max_sync(0xffffffffu, ra == top - 1 ? a : rc == top - 1 ? c : 0u));
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if (rank == top - 1) sm.thr = max(1u, mine);
+        __syncthreads();
+        const uint32_t thr = sm.thr;
         unsigned long long reach = __ballot_sync(0xffffffffu, sm.entry[warp][lane] >= thr) |
                                    (unsigned long long)__ballot_sync(0xffffffffu, sm.entry[warp][lane + 32] >= thr) << 32;
         for (; reach; reach &= reach - 1) {
             const int e = __ffsll(reach) - 1;
-            for (int j = e << shift, blk = gw + j * nw; j < (e + 1) << shift && blk < blocks; ++j, blk += nw) {
-                float x[GE];
-                widen<BF16>(load_granule<BF16, ALIGNED>(row, blk, lane, V), x);
+            for (int j = (e << shift) * U, blk = gw + j * nw; j < ((e + 1) << shift) * U && blk < blocks; j += U, blk += U * nw) {
+                uint4 raw[U];
 #pragma unroll
-                for (int i = 0; i < GE; ++i)
-                    if (x[i] > -INFINITY && order_f32(x[i]) >= thr) {
-                        const int at = atomicAdd(&sm.count, 1);
-                        if (at < kCand) sm.cand[at] = make_key(x[i], (ALIGNED ? (blk * 32 + lane) * GE : blk * 32 * GE + lane) + i * ES);
-                    }
+                for (int u = 0; u < U; ++u) raw[u] = load_granule<BF16, ALIGNED>(row, blk + u * nw, lane, V);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float mx = granule_max<BF16>(raw[u]);
+                    if (!(mx > -INFINITY && order_f32(mx) >= thr)) continue;
+                    float x[GE];
+                    widen<BF16>(raw[u], x);
+#pragma unroll
+                    for (int i = 0; i < GE; ++i)
+                        if (x[i] > -INFINITY && order_f32(x[i]) >= thr) {
+                            const int at = atomicAdd(&sm.count, 1);
+                            if (at < kCand)
+                                sm.cand[at] = make_key(x[i], (ALIGNED ? ((blk + u * nw) * 32 + lane) * GE : (blk + u * nw) * 32 * GE + lane) + i * ES);
+                        }
+                }
             }
         }
         __syncthreads();
