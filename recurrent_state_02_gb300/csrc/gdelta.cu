@@ -19,6 +19,7 @@
 #include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
+#include <type_traits>
 
 namespace la {
 namespace {
@@ -127,46 +128,65 @@ gdelta_rec_kernel(const RecArgs a)
     const int nblk = (T + kRecTok - 1) / kRecTok;
     // token of position i of block n in the sweep's order
     auto token = [&](int n, int i) { const int t = n * kRecTok + i; return kBack ? T - 1 - t : t; };
-    auto stage_in = [&](int n, int i0, int step) {
+    // `step` threads; what a thread reads of 8 passes over the rows is in flight at once (one element after the
+    // other, the loads' latency and not the products was what a token took)
+    auto stage_in = [&](int n, int i0, auto step) {
+        constexpr int kStep = decltype(step)::value;
+        constexpr int kRowIters = kRecTok * W / kStep, kColIters = kRecTok * kRecCols / kStep, kFly = kRowIters < 8 ? kRowIters : 8;
         float *st = st0 + (n & 1) * kStage;
         const int nt = min(kRecTok, T - n * kRecTok);
-        for (int x = i0; x < nt * W; x += step) {
-            const int i = x / W, row = x % W, t = token(n, i);
-            float vx = 0.f, vb = 0.f, vd = 0.f;
-            if (row < rows) {
-                if (!kT) {
-                    vx = load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + row);
-                    vb = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + row);
-                } else {
-                    const size_t o = at(t, s.H, h, s.dv) + row;
-                    const float bt = s.beta ? s.beta[at(t, s.H, h, 1)] : 1.f;
-                    vx = load_elem<BF16>(a.dy, o);
-                    const float dvt = bt * a.lam[o], et = a.e[o];
-                    vb = MODE == kQue ? dvt : et;
-                    vd = MODE == kQue ? et : dvt;
+        float u[kColIters], u2[kColIters], al = 1.f, be = 1.f;
+#pragma unroll
+        for (int j = 0; j < kColIters; ++j) {
+            const int x = i0 + j * kStep, i = x / kRecCols, col = c0 + x % kRecCols, t = token(n, i);
+            u[j] = u2[j] = 0.f;
+            if (i < nt && col < cols) {
+                if (MODE == kFwd) u[j] = load_elem<BF16>(a.v, at(t, s.H, h, s.dv) + col);
+                if (MODE == kRev) u[j] = a.scale * load_elem<BF16>(a.dy, at(t, s.H, h, s.dv) + col);
+                if (kT) u[j] = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + col);
+                if (MODE == kKey) u2[j] = a.scale * load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + col);
+            }
+        }
+        if (i0 < nt) {
+            const size_t o = at(token(n, i0), s.H, h, 1);
+            if (s.alpha) al = s.alpha[o];
+            if (s.beta) be = s.beta[o];
+        }
+#pragma unroll 1
+        for (int j0 = 0; j0 < kRowIters; j0 += kFly) {
+            float vx[kFly], vb[kFly], vd[kFly];
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                const int x = i0 + (j0 + j) * kStep, i = x / W, row = x % W, t = token(n, i);
+                vx[j] = vb[j] = vd[j] = 0.f;
+                if (i < nt && row < rows) {
+                    if (!kT) {
+                        vx[j] = load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + row);
+                        vb[j] = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + row);
+                    } else {
+                        const size_t o = at(t, s.H, h, s.dv) + row;
+                        const float bt = s.beta ? s.beta[at(t, s.H, h, 1)] : 1.f;
+                        vx[j] = load_elem<BF16>(a.dy, o);
+                        const float dvt = bt * a.lam[o], et = a.e[o];
+                        vb[j] = MODE == kQue ? dvt : et;
+                        vd[j] = MODE == kQue ? et : dvt;
+                    }
                 }
             }
-            st[x] = vx;
-            st[kOffB + x] = vb;
-            if (kT) st[kOffD + x] = vd;
-        }
-        for (int x = i0; x < nt * kRecCols; x += step) {
-            const int i = x / kRecCols, col = c0 + x % kRecCols, t = token(n, i);
-            float u = 0.f, u2 = 0.f;
-            if (col < cols) {
-                if (MODE == kFwd) u = load_elem<BF16>(a.v, at(t, s.H, h, s.dv) + col);
-                if (MODE == kRev) u = a.scale * load_elem<BF16>(a.dy, at(t, s.H, h, s.dv) + col);
-                if (kT) u = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + col);
-                if (MODE == kKey) u2 = a.scale * load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + col);
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                const int x = i0 + (j0 + j) * kStep;
+                st[x] = vx[j];
+                st[kOffB + x] = vb[j];
+                if (kT) st[kOffD + x] = vd[j];
             }
-            st[kOffC + x] = u;
-            if (MODE == kKey) st[kOffC2 + x] = u2;
         }
-        for (int i = i0; i < nt; i += step) {
-            const int t = token(n, i);
-            st[kOffG + i] = s.alpha ? s.alpha[at(t, s.H, h, 1)] : 1.f;
-            st[kOffG + kRecTok + i] = s.beta ? s.beta[at(t, s.H, h, 1)] : 1.f;
+#pragma unroll
+        for (int j = 0; j < kColIters; ++j) {
+            st[kOffC + i0 + j * kStep] = u[j];
+            if (MODE == kKey) st[kOffC2 + i0 + j * kStep] = u2[j];
         }
+        if (i0 < kRecTok) st[kOffG + i0] = al, st[kOffG + kRecTok + i0] = be;
     };
     auto stage_out = [&](int n, int i0, int step) {
         const float *st = st0 + (n & 1) * kStage;
@@ -191,7 +211,7 @@ gdelta_rec_kernel(const RecArgs a)
         }
     };
 
-    if (nblk > 0) stage_in(0, tid, kRecThreads);
+    if (nblk > 0) stage_in(0, tid, std::integral_constant<int, kRecThreads>());
     __syncthreads();
     for (int n = 0; n < nblk; ++n) {
         if (computes) {
@@ -270,7 +290,7 @@ gdelta_rec_kernel(const RecArgs a)
         } else {
             if (n > 0) stage_out(n - 1, tid - kRecComp, kRecComp);
             asm volatile("bar.sync 1, %0;" ::"n"(kRecComp) : "memory");   // the results are read before their stage is refilled
-            if (n + 1 < nblk) stage_in(n + 1, tid - kRecComp, kRecComp);
+            if (n + 1 < nblk) stage_in(n + 1, tid - kRecComp, std::integral_constant<int, kRecComp>());
         }
         __syncthreads();
     }
