@@ -63,14 +63,24 @@ constexpr int kRecTok = 16;              // tokens per staged block
 constexpr int kRecComp = 128;            // threads that compute: 4 warps of 8 columns
 constexpr int kRecThreads = 2 * kRecComp;   // and as many that stage the next block and write out the last one
 constexpr int kRecCols = 32;
+constexpr int kRecGroup = 4;             // tokens taken together
 
 template <int RPL>
-constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2);
+constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2 + 6);
 
+// Four tokens are taken together, i and j in the sweep's order, X the state before them.  d_j w_j^T is what token j
+// writes (d = k, k, e, dv), in the backward sweeps with x_j add_j^T before it; the decays are
+//     forwards:   c_i = prod_{l <= i} alpha_l,  m_ji = prod_{j < l <= i} alpha_l;     backwards:  l < i and j <= l < i
+//     p_i = c_i X^T b_i + sum_{j < i} m_ji (d_j . b_i) w_j  [+ sum_{j <= i} m_ji (x_j . b_i) add_j, backwards]
+//     out_i = c_i X^T x_i + sum_{j <= i} m_ji (d_j . x_i) w_j      (forwards)
+// and X takes the four outer products at once.  So only p's chain over four numbers is serial, and the sums over
+// the rows are formed side by side.  The ten and six products of the tokens' vectors come from the staging warps.
+//
 // A warp's lane (g, jj), g = lane / 4, holds rows 4 (8 m + g) + i (m < RPL / 4, i < 4) of the columns 2 jj and
-// 2 jj + 1 of its warp's 8; sums over the rows are reduced over the 8 groups by shuffles.  The staging
+// 2 jj + 1 of its warp's 8; the sums over the rows are exchanged so that group g ends with one of the eight
+// (p of token g, or out of token g - 4): 14 shuffles, and 8 to hand p out, where whole sums for all took 48.  The staging
 // warps convert a block of 16 tokens to FP32 while the computing ones work on the one before, and store its
-// results.  4 r dv FMAs per token and head bound it; few heads are bound by a token's latency.
+// results.  4 r dv FMAs per token and head bound it; few heads are bound by a group's latency.
 template <int MODE, bool BF16, int RPL>
 __global__ void __launch_bounds__(kRecThreads)
 gdelta_rec_kernel(const RecArgs a)
@@ -82,7 +92,8 @@ gdelta_rec_kernel(const RecArgs a)
     // per stage: row vectors x (q, q, dy, dy), b (k, k, dv, e), d (-, -, e, dv), column elements, results, gates
     float *const st0 = smem;
     constexpr int kOffB = kRecTok * W, kOffD = 2 * kRecTok * W, kOffC = 3 * kRecTok * W, kOffC2 = kOffC + kRecTok * kRecCols,
-                  kOffO = kOffC2 + kRecTok * kRecCols, kOffO2 = kOffO + kRecTok * kRecCols, kOffG = kOffO2 + kRecTok * kRecCols;
+                  kOffO = kOffC2 + kRecTok * kRecCols, kOffO2 = kOffO + kRecTok * kRecCols, kOffG = kOffO2 + kRecTok * kRecCols,
+                  kOffM = kOffG + 2 * kRecTok;      // per group: the products 4 x 4, c, m to the group's end
     constexpr int kStage = kRecStageFloats<RPL>;
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -102,16 +113,182 @@ gdelta_rec_kernel(const RecArgs a)
         T = hi - lo;
         tok0 = lo;
     }
-    // element (t, 0) of a token array with `heads` heads, its head hh, d elements a row
-    auto at = [&](int t, int heads, int hh, int d) -> size_t {
-        return packed ? ((tok0 + t) * heads + hh) * (size_t)d : (((size_t)b * heads + hh) * s.T + t) * (size_t)d;
-    };
     const size_t bh = (size_t)b * s.H + h;
-
+    // element (t, 0) of a token array with `heads` heads, its head hh, d elements a row: first + t * stride
+    struct Rows {
+        size_t first;
+        ptrdiff_t stride;
+    };
+    auto rows_of = [&](int heads, int hh, int d) -> Rows {
+        return packed ? Rows{(tok0 * heads + hh) * (size_t)d, (ptrdiff_t)heads * d} : Rows{((size_t)b * heads + hh) * s.T * d, d};
+    };
     const bool computes = tid < kRecComp;
     const int warp = tid >> 5, g = lane >> 2, jl = (warp & 3) * 8 + 2 * (lane & 3);
-    float X[2][RPL];
-    if (computes) {
+    const int nblk = (T + kRecTok - 1) / kRecTok;
+    // token of position i of block n in the sweep's order
+    auto token = [&](int n, int i) { const int t = n * kRecTok + i; return kBack ? T - 1 - t : t; };
+    auto staging_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kRecComp) : "memory"); };
+    auto block_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kRecThreads) : "memory"); };
+    if (!computes) {
+        // A staging thread's share of a block: read into registers a block ahead, so that the loads' latency passes
+        // while the block before is stored, and not within a block's time.
+        constexpr int kRowIters = kRecTok * W / kRecComp, kColIters = kRecTok * kRecCols / kRecComp;
+        constexpr int kRowStep = W < kRecComp ? kRecComp / W : 1, kRowParts = W > kRecComp ? W / kRecComp : 1;
+        float fx[kRowIters], fb[kRowIters], fd[kT ? kRowIters : 1], fu[kColIters], fu2[MODE == kKey ? kColIters : 1], fal = 1.f, fbe = 1.f;
+        const int sid = tid - kRecComp, row0 = sid % W, i_row = sid / W, col = c0 + sid % kRecCols, i_col = sid / kRecCols;
+        const Rows key = rows_of(s.Hk, hk, s.r), val = rows_of(s.H, h, s.dv), gate = rows_of(s.H, h, 1), res = rows_of(s.H, h, cols);
+        const Rows vec = kT ? val : key, elem = kT ? key : val;
+        auto fetch = [&](int n) {
+            const int nt = min(kRecTok, T - n * kRecTok);
+            fal = fbe = 1.f;
+            if (sid < nt) {
+                const size_t o = gate.first + token(n, sid) * gate.stride;
+                if (s.alpha) fal = s.alpha[o];
+                if (s.beta) fbe = s.beta[o];
+            }
+            size_t o = vec.first + row0 + (ptrdiff_t)token(n, i_row) * vec.stride;
+            const ptrdiff_t step = (kBack ? -kRowStep : kRowStep) * vec.stride;
+#pragma unroll
+            for (int j = 0; j < kRowIters; ++j) {
+                const int i = i_row + j / kRowParts * kRowStep, part = j % kRowParts;
+                const size_t oj = o + part * kRecComp;
+                fx[j] = fb[j] = 0.f;
+                if (kT) fd[j] = 0.f;
+                if (i < nt && row0 + part * kRecComp < rows) {
+                    fx[j] = load_elem<BF16>(kT ? a.dy : a.q, oj);
+                    fb[j] = !kT ? load_elem<BF16>(a.k, oj) : MODE == kQue ? a.lam[oj] : a.e[oj];
+                    if (kT) fd[j] = MODE == kQue ? a.e[oj] : a.lam[oj];
+                }
+                if (part == kRowParts - 1) o += step;
+            }
+            size_t oc = elem.first + col + (ptrdiff_t)token(n, i_col) * elem.stride;
+            const ptrdiff_t cstep = (kBack ? -1 : 1) * (kRecComp / kRecCols) * elem.stride;
+#pragma unroll
+            for (int j = 0; j < kColIters; ++j) {
+                fu[j] = 0.f;
+                if (MODE == kKey) fu2[j] = 0.f;
+                if (i_col + j * (kRecComp / kRecCols) < nt && col < cols) {
+                    fu[j] = load_elem<BF16>(kT ? a.k : MODE == kFwd ? a.v : a.dy, oc);
+                    if (MODE == kKey) fu2[j] = load_elem<BF16>(a.q, oc);
+                }
+                oc += cstep;
+            }
+        };
+        auto stage_in = [&](int n) {
+            float *st = st0 + (n & 1) * kStage;
+            if (sid < kRecTok) st[kOffG + sid] = fal, st[kOffG + kRecTok + sid] = fbe;
+            if (kT) staging_sync();
+#pragma unroll
+            for (int j = 0; j < kRowIters; ++j) {
+                const int x = sid + j * kRecComp;
+                const float bt = kT ? st[kOffG + kRecTok + x / W] : 1.f;
+                st[x] = fx[j];
+                st[kOffB + x] = MODE == kQue ? bt * fb[j] : fb[j];
+                if (kT) st[kOffD + x] = MODE == kKey ? bt * fd[j] : fd[j];
+            }
+#pragma unroll
+            for (int j = 0; j < kColIters; ++j) {
+                st[kOffC + sid + j * kRecComp] = MODE == kRev ? a.scale * fu[j] : fu[j];
+                if (MODE == kKey) st[kOffC2 + sid + j * kRecComp] = a.scale * fu2[j];
+            }
+            staging_sync();
+        };
+        // One warp: the products of group `gr`, with their decays.  At [i][j], j <= i: d_j . x_i (backwards x_j . b_i); at [j][i], j < i: d_j . b_i
+        auto stage_products = [&](int n, int gr) {
+            float *st = st0 + (n & 1) * kStage;
+            const float *x = st + gr * kRecGroup * W, *b = x + kOffB, *d = kT ? x + kOffD : b;
+            float m[16];
+#pragma unroll
+            for (int z = 0; z < 16; ++z) m[z] = 0.f;
+#pragma unroll 2
+            for (int row = lane; row < W; row += 32) {
+                float xv[4], bv[4], dv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[i] = x[i * W + row], bv[i] = b[i * W + row], dv[i] = kT ? d[i * W + row] : bv[i];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j <= i; ++j) {
+                        m[4 * i + j] = kBack ? fmaf(xv[j], bv[i], m[4 * i + j]) : fmaf(dv[j], xv[i], m[4 * i + j]);
+                        if (j < i) m[4 * j + i] = fmaf(dv[j], bv[i], m[4 * j + i]);
+                    }
+            }
+#pragma unroll
+            for (int w = 8; w; w >>= 1) {        // the lane ends with the sum of m[lane / 2]
+                const bool up = lane & (2 * w);
+#pragma unroll
+                for (int z = 0; z < w; ++z) {
+                    const float keep = up ? m[z + w] : m[z], give = up ? m[z] : m[z + w];
+                    m[z] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * w);
+                }
+            }
+            m[0] += __shfl_xor_sync(0xffffffffu, m[0], 1);
+            float *out = st + kOffM + gr * 24;
+            const float *al = st + kOffG + gr * kRecGroup;
+            const int z = lane >> 1, i = z >> 2, j = z & 3, lo = min(i, j), hi = max(i, j);
+            float dec = 1.f, c = 1.f, end = 1.f;
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                const float av = al[l];
+                if (kBack ? l >= lo && l < hi : l > lo && l <= hi) dec *= av;
+                if (kBack ? l < lane : l <= lane) c *= av;
+                if (kBack ? l >= lane : l > lane) end *= av;
+            }
+            if (!(lane & 1)) out[z] = dec * m[0];
+            if (lane < 4) out[16 + lane] = c, out[20 + lane] = end;
+        };
+        auto stage_out = [&](int n) {
+            const float *st = st0 + (n & 1) * kStage;
+            const int nt = min(kRecTok, T - n * kRecTok);
+            if (col >= cols) return;
+            size_t o = res.first + col + (ptrdiff_t)token(n, i_col) * res.stride;
+            const ptrdiff_t step = (kBack ? -1 : 1) * (kRecComp / kRecCols) * res.stride;
+            float was[kColIters];
+#pragma unroll
+            for (int j = 0; j < kColIters; ++j)
+                if (MODE == kKey && i_col + j * (kRecComp / kRecCols) < nt) was[j] = a.w[o + j * step];
+#pragma unroll
+            for (int j = 0; j < kColIters; ++j) {
+                const int i = i_col + j * (kRecComp / kRecCols), x = sid + j * kRecComp;
+                if (i >= nt) break;
+                const float out = st[kOffO + x], out2 = st[kOffO2 + x], bt = st[kOffG + kRecTok + i];
+                const size_t oj = o + j * step;
+                if (MODE == kFwd) {
+                    if (a.y) store_elem<BF16>(a.y, oj, a.scale * out);
+                    if (a.e_out) a.e_out[oj] = out2;
+                } else if (MODE == kRev) {
+                    a.lam_out[oj] = out;
+                    store_elem<BF16>(a.dv_out, oj, bt * out);
+                } else if (MODE == kQue) {
+                    a.dq[oj] = a.scale * out;
+                    a.w[oj] = out2;
+                } else {
+                    a.w[oj] = fmaf(bt, out, -was[j]);
+                }
+            }
+        };
+
+        static_assert(kRecTok == kRecGroup * (kRecThreads - kRecComp) / 32, "a group for each staging warp");
+        if (nblk > 0) {
+            fetch(0);
+            stage_in(0);
+            stage_products(0, warp - kRecComp / 32);
+            if (nblk > 1) fetch(1);
+        }
+        block_sync();
+        for (int n = 0; n < nblk; ++n) {
+            if (n > 0) stage_out(n - 1);
+            staging_sync();                  // the results are read before their stage is refilled
+            if (n + 1 < nblk) {
+                stage_in(n + 1);
+                stage_products(n + 1, warp - kRecComp / 32);
+                if (n + 2 < nblk) fetch(n + 2);
+            }
+            block_sync();
+        }
+        if (nblk > 0) stage_out(nblk - 1);
+    } else {
+        float X[2][RPL];
 #pragma unroll
         for (int m = 0; m < RPL; ++m) {
             const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
@@ -123,190 +300,141 @@ gdelta_rec_kernel(const RecArgs a)
                     X[c][m] = a.S_init[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)];
             }
         }
-    }
-
-    const int nblk = (T + kRecTok - 1) / kRecTok;
-    // token of position i of block n in the sweep's order
-    auto token = [&](int n, int i) { const int t = n * kRecTok + i; return kBack ? T - 1 - t : t; };
-    // `step` threads; what a thread reads of 8 passes over the rows is in flight at once (one element after the
-    // other, the loads' latency and not the products was what a token took)
-    auto stage_in = [&](int n, int i0, auto step) {
-        constexpr int kStep = decltype(step)::value;
-        constexpr int kRowIters = kRecTok * W / kStep, kColIters = kRecTok * kRecCols / kStep, kFly = kRowIters < 8 ? kRowIters : 8;
-        float *st = st0 + (n & 1) * kStage;
-        const int nt = min(kRecTok, T - n * kRecTok);
-        float u[kColIters], u2[kColIters], al = 1.f, be = 1.f;
-#pragma unroll
-        for (int j = 0; j < kColIters; ++j) {
-            const int x = i0 + j * kStep, i = x / kRecCols, col = c0 + x % kRecCols, t = token(n, i);
-            u[j] = u2[j] = 0.f;
-            if (i < nt && col < cols) {
-                if (MODE == kFwd) u[j] = load_elem<BF16>(a.v, at(t, s.H, h, s.dv) + col);
-                if (MODE == kRev) u[j] = a.scale * load_elem<BF16>(a.dy, at(t, s.H, h, s.dv) + col);
-                if (kT) u[j] = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + col);
-                if (MODE == kKey) u2[j] = a.scale * load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + col);
-            }
-        }
-        if (i0 < nt) {
-            const size_t o = at(token(n, i0), s.H, h, 1);
-            if (s.alpha) al = s.alpha[o];
-            if (s.beta) be = s.beta[o];
-        }
-#pragma unroll 1
-        for (int j0 = 0; j0 < kRowIters; j0 += kFly) {
-            float vx[kFly], vb[kFly], vd[kFly];
-#pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                const int x = i0 + (j0 + j) * kStep, i = x / W, row = x % W, t = token(n, i);
-                vx[j] = vb[j] = vd[j] = 0.f;
-                if (i < nt && row < rows) {
-                    if (!kT) {
-                        vx[j] = load_elem<BF16>(a.q, at(t, s.Hk, hk, s.r) + row);
-                        vb[j] = load_elem<BF16>(a.k, at(t, s.Hk, hk, s.r) + row);
-                    } else {
-                        const size_t o = at(t, s.H, h, s.dv) + row;
-                        const float bt = s.beta ? s.beta[at(t, s.H, h, 1)] : 1.f;
-                        vx[j] = load_elem<BF16>(a.dy, o);
-                        const float dvt = bt * a.lam[o], et = a.e[o];
-                        vb[j] = MODE == kQue ? dvt : et;
-                        vd[j] = MODE == kQue ? et : dvt;
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                const int x = i0 + (j0 + j) * kStep;
-                st[x] = vx[j];
-                st[kOffB + x] = vb[j];
-                if (kT) st[kOffD + x] = vd[j];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kColIters; ++j) {
-            st[kOffC + i0 + j * kStep] = u[j];
-            if (MODE == kKey) st[kOffC2 + i0 + j * kStep] = u2[j];
-        }
-        if (i0 < kRecTok) st[kOffG + i0] = al, st[kOffG + kRecTok + i0] = be;
-    };
-    auto stage_out = [&](int n, int i0, int step) {
-        const float *st = st0 + (n & 1) * kStage;
-        const int nt = min(kRecTok, T - n * kRecTok);
-        for (int x = i0; x < nt * kRecCols; x += step) {
-            const int i = x / kRecCols, col = c0 + x % kRecCols, t = token(n, i);
-            if (col >= cols) continue;
-            const float o = st[kOffO + x], o2 = st[kOffO2 + x], bt = st[kOffG + kRecTok + i];
-            const size_t at_o = at(t, s.H, h, cols) + col;
-            if (MODE == kFwd) {
-                if (a.y) store_elem<BF16>(a.y, at_o, a.scale * o);
-                if (a.e_out) a.e_out[at_o] = o2;
-            } else if (MODE == kRev) {
-                a.lam_out[at_o] = o;
-                store_elem<BF16>(a.dv_out, at_o, bt * o);
-            } else if (MODE == kQue) {
-                a.dq[at_o] = a.scale * o;
-                a.w[at_o] = o2;
-            } else {
-                a.w[at_o] = fmaf(bt, o, -a.w[at_o]);
-            }
-        }
-    };
-
-    if (nblk > 0) stage_in(0, tid, std::integral_constant<int, kRecThreads>());
-    __syncthreads();
-    for (int n = 0; n < nblk; ++n) {
-        if (computes) {
+        block_sync();
+        for (int n = 0; n < nblk; ++n) {
             float *st = st0 + (n & 1) * kStage;
-            const int nt = min(kRecTok, T - n * kRecTok);
+            const int groups = (min(kRecTok, T - n * kRecTok) + kRecGroup - 1) / kRecGroup;     // tokens after the last are zeros, alpha 1
 #pragma unroll 1
-            for (int i = 0; i < nt; ++i) {
-                const float4 *xr = reinterpret_cast<const float4 *>(st + i * W) + g;
-                const float4 *br = reinterpret_cast<const float4 *>(st + kOffB + i * W) + g;
-                const float4 *dr = reinterpret_cast<const float4 *>(st + kOffD + i * W) + g;
-                const float al = st[kOffG + i], be = st[kOffG + kRecTok + i];
-                const float2 cu = *reinterpret_cast<const float2 *>(st + kOffC + i * kRecCols + jl);
-                const float u[2] = {cu.x, cu.y};
-                float add[2] = {0.f, 0.f};
-                if (MODE == kRev) add[0] = u[0], add[1] = u[1];
-                if (MODE == kKey) {
-                    const float2 t2 = *reinterpret_cast<const float2 *>(st + kOffC2 + i * kRecCols + jl);
-                    add[0] = t2.x, add[1] = t2.y;
+            for (int gr = 0; gr < groups; ++gr) {
+                const int i0 = gr * kRecGroup;
+                const float4 *xr = reinterpret_cast<const float4 *>(st + i0 * W) + g;
+                const float4 *br = reinterpret_cast<const float4 *>(st + kOffB + i0 * W) + g;
+                const float4 *dr = kT ? reinterpret_cast<const float4 *>(st + kOffD + i0 * W) + g : br;
+                const float4 *mr = reinterpret_cast<const float4 *>(st + kOffM + gr * 24);
+                // what the serial part needs, read ahead of it
+                const float4 m0 = mr[0], m1 = mr[1], m2 = mr[2], m3 = mr[3], c4 = mr[4], end4 = mr[5];
+                const float M[4][4] = {{m0.x, m0.y, m0.z, m0.w}, {m1.x, m1.y, m1.z, m1.w}, {m2.x, m2.y, m2.z, m2.w}, {m3.x, m3.y, m3.z, m3.w}};
+                const float cv[4] = {c4.x, c4.y, c4.z, c4.w}, end[4] = {end4.x, end4.y, end4.z, end4.w};
+                const float4 be4 = *reinterpret_cast<const float4 *>(st + kOffG + kRecTok + i0);
+                const float be[4] = {be4.x, be4.y, be4.z, be4.w};
+                float u[4][2], add[4][2], row[4], cg = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 cu = *reinterpret_cast<const float2 *>(st + kOffC + (i0 + i) * kRecCols + jl);
+                    float2 ad = cu;
+                    if (MODE == kKey) ad = *reinterpret_cast<const float2 *>(st + kOffC2 + (i0 + i) * kRecCols + jl);
+                    u[i][0] = cu.x, u[i][1] = cu.y, add[i][0] = ad.x, add[i][1] = ad.y;
+                    row[i] = 0.f;
                 }
-                float p[2] = {0.f, 0.f};
+                if (!kBack) {           // the row of out's token
+                    const float4 r4 = mr[g & 3];
+                    row[0] = r4.x, row[1] = (g & 3) >= 1 ? r4.y : 0.f, row[2] = (g & 3) >= 2 ? r4.z : 0.f, row[3] = (g & 3) == 3 ? r4.w : 0.f;
+                    cg = st[kOffM + gr * 24 + 16 + (g & 3)];
+                }
+                // sums[0..3] X^T b, sums[4..7] X^T x (forwards)
+                constexpr int kSums = kBack ? 4 : 8;
+                float sums[kSums][2];
 #pragma unroll
-                for (int m4 = 0; m4 < RPL / 4; ++m4) {
-                    const float4 vb = br[8 * m4];
-                    const float bb[4] = {vb.x, vb.y, vb.z, vb.w};
-                    float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (kBack) vx = xr[8 * m4];
-                    const float xx[4] = {vx.x, vx.y, vx.z, vx.w};
+                for (int i = 0; i < kSums; ++i) sums[i][0] = sums[i][1] = 0.f;
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
+                for (int m4 = 0; m4 < RPL / 4; ++m4)
+#pragma unroll
+                    for (int i = 0; i < kSums; ++i) {
+                        const float4 vb = i < 4 ? br[i * (W / 4) + 8 * m4] : xr[(i - 4) * (W / 4) + 8 * m4];
+                        const float bb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) sums[i][c] = fmaf(X[c][4 * m4 + z], bb[z], sums[i][c]);
+                    }
+                if (kBack) {            // group g and g + 4 end with the same
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) sums[i][c] += __shfl_xor_sync(0xffffffffu, sums[i][c], 16);
+                }
+#pragma unroll
+                for (int w = kSums / 2; w; w >>= 1) {
+                    const bool up = g & w;
+#pragma unroll
+                    for (int i = 0; i < w; ++i)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float &X1 = X[c][4 * m4 + z];
-                            X1 = kBack ? fmaf(xx[z], add[c], X1) : al * X1;
-                            p[c] = fmaf(X1, bb[z], p[c]);
+                            const float keep = up ? sums[i + w][c] : sums[i][c], give = up ? sums[i][c] : sums[i + w][c];
+                            sums[i][c] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * w);
                         }
                 }
+                float p[4][2], w[4][2];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) p[c] += __shfl_xor_sync(0xffffffffu, p[c], o);
-                float wr[2], out[2] = {0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    wr[c] = MODE == kFwd ? be * (u[c] - p[c]) : MODE == kRev ? -be * p[c] : MODE == kQue ? be * u[c] : -u[c];
-#pragma unroll
-                for (int m4 = 0; m4 < RPL / 4; ++m4) {
-                    const float4 vd = kT ? dr[8 * m4] : br[8 * m4];
-                    const float dd[4] = {vd.x, vd.y, vd.z, vd.w};
-                    float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (!kBack) vx = xr[8 * m4];
-                    const float xx[4] = {vx.x, vx.y, vx.z, vx.w};
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float &X1 = X[c][4 * m4 + z];
-                            X1 = fmaf(dd[z], wr[c], X1);
-                            if (kBack) X1 *= al;
-                            else out[c] = fmaf(X1, xx[z], out[c]);
-                        }
-                }
-                if (!kBack) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) out[c] += __shfl_xor_sync(0xffffffffu, out[c], o);
-                }
-                if (g == 0) {
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        st[kOffO + i * kRecCols + jl + c] = kBack ? p[c] : out[c];
-                        if (!kBack) st[kOffO2 + i * kRecCols + jl + c] = MODE == kFwd ? u[c] - p[c] : p[c];
+                        float t = cv[i] * __shfl_sync(0xffffffffu, sums[0][c], 4 * i + (lane & 3));
+#pragma unroll
+                        for (int j = 0; j <= i; ++j) {
+                            if (kBack) t = fmaf(M[i][j], add[j][c], t);
+                            if (j < i) t = fmaf(M[j][i], w[j][c], t);
+                        }
+                        p[i][c] = MODE == kFwd ? u[i][c] - t : t;
+                        w[i][c] = MODE == kFwd ? be[i] * p[i][c] : MODE == kRev ? -be[i] * t : MODE == kQue ? be[i] * u[i][c] : -u[i][c];
+                    }
+                float o[2];             // groups 0 to 3: p of token g; 4 to 7: out of token g - 4
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float p01 = g & 1 ? p[1][c] : p[0][c], p23 = g & 1 ? p[3][c] : p[2][c];
+                    o[c] = g & 2 ? p23 : p01;
+                    if (!kBack) {
+                        float out = cg * sums[0][c];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) out = fmaf(row[j], w[j][c], out);
+                        o[c] = g & 4 ? out : o[c];
+                    }
+                }
+                if (!kBack || g < 4)
+                    *reinterpret_cast<float2 *>(st + (kBack || g >= 4 ? kOffO : kOffO2) + (i0 + (g & 3)) * kRecCols + jl) = make_float2(o[0], o[1]);
+                const float all = kBack ? end[0] : cv[3];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) w[i][c] *= end[i], add[i][c] *= end[i];
+#pragma unroll
+                for (int m4 = 0; m4 < RPL / 4; ++m4) {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) X[c][4 * m4 + z] *= all;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 vd = dr[i * (W / 4) + 8 * m4];
+                        const float dd[4] = {vd.x, vd.y, vd.z, vd.w};
+                        const float4 vx = kBack ? xr[i * (W / 4) + 8 * m4] : vd;
+                        const float xx[4] = {vx.x, vx.y, vx.z, vx.w};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float &X1 = X[c][4 * m4 + z];
+                                X1 = fmaf(dd[z], w[i][c], X1);
+                                if (kBack) X1 = fmaf(xx[z], add[i][c], X1);
+                            }
                     }
                 }
             }
-        } else {
-            if (n > 0) stage_out(n - 1, tid - kRecComp, kRecComp);
-            asm volatile("bar.sync 1, %0;" ::"n"(kRecComp) : "memory");   // the results are read before their stage is refilled
-            if (n + 1 < nblk) stage_in(n + 1, tid - kRecComp, std::integral_constant<int, kRecComp>());
+            block_sync();
         }
-        __syncthreads();
-    }
-    if (nblk > 0) stage_out(nblk - 1, tid, kRecThreads);
-    if (a.S_fin && computes) {
+        if (a.S_fin) {
 #pragma unroll
-        for (int m = 0; m < RPL; ++m) {
-            const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
+            for (int m = 0; m < RPL; ++m) {
+                const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int col = c0 + jl + c;
-                if (row < rows && col < cols)
-                    a.S_fin[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)] = X[c][m];
+                for (int c = 0; c < 2; ++c) {
+                    const int col = c0 + jl + c;
+                    if (row < rows && col < cols)
+                        a.S_fin[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)] = X[c][m];
+                }
             }
         }
-    }
+        }
 }
 
 template <int MODE, bool BF16, int RPL>
