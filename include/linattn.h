@@ -501,11 +501,15 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  * Inputs are finite; a row with an infinity or NaN may spoil its whole chunk of 64 tokens as well as all later ones.
  * Outputs overlap neither inputs nor one another, but for the states where it says so.
  * Kernels:
- *   the token recurrence in FP32 on CUDA cores (for one token of la_gated_delta_decode_step a kernel of its
- *   own, bound by the state's traffic, when dv is a multiple of 4 and S 16-byte aligned).
+ *   prompts in chunks of 64 tokens on the tensor cores, the state in FP32, for BF16 with r 64 or 128, dv a multiple of 64
+ *   (la_gated_delta_backward: 64 or 128), every token array on a 16-byte boundary and T > 16 (packed sequences: any length);
+ *   the token recurrence in FP32 on CUDA cores for everything else (for one token of la_gated_delta_decode_step a kernel
+ *   of its own, bound by the state's traffic, when dv is a multiple of 4 and S 16-byte aligned).
+ * In the chunked kernels what is derived from the inputs enters the tensor cores as two BF16 parts (16 bits of it) where
+ * it reaches an FP32 result, and as one where it reaches a BF16 one only: relative 2-norms of the errors about 3e-6 and 3e-3.
  * The first call of each kind on a device sets kernel attributes: make it before any stream capture.
- * Requires 1 <= r, dv <= 256, B, H <= 65535, T <= 2^30; BF16 arrays 2-byte, FP32 and int32 arrays 4-byte
- * aligned, workspaces 256-byte.
+ * Requires 1 <= r, dv <= 256, B, H <= 65535, T <= 2^30 and, but for packed sequences, B H (T + 1) <= 2^30; BF16 arrays
+ * 2-byte, FP32 and int32 arrays 4-byte aligned, workspaces 256-byte.
  * Errors of every entry point: LA_ERR_NULL, LA_ERR_SHAPE (B, H, Hk, r, dv < 1, T < 0, H not a multiple of Hk,
  * scale not finite), LA_ERR_DTYPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (other sizes), LA_ERR_WORKSPACE, LA_ERR_CUDA.
  */
@@ -570,7 +574,7 @@ la_status la_gated_delta_decode_step(const void *q, const void *k, const void *v
  *   dbeta    device FP32 [B,H,T] or NULL (not formed)
  *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL)
  *   workspace  la_gated_delta_backward_workspace_bytes(...) bytes, as above
- * T may be 0 (dS0 = dS_T).
+ * T may be 0 (dS0 = dS_T).  Repeated calls give the same bits.
  */
 size_t la_gated_delta_backward_workspace_bytes(int B, int H, int Hk, int T, int r, int dv, la_dtype dtype);
 la_status la_gated_delta_backward(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha,

@@ -1071,12 +1071,12 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
 namespace {
 
 // What every gated delta entry point checks of its sizes.
-la_status check_gdelta_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, float scale)
+la_status check_gdelta_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, float scale, bool packed = false)
 {
     if (Hk < 1 || H < 1 || H % Hk != 0) return LA_ERR_SHAPE;
     if (const la_status e = check_decay_sizes(dtype, B, H, T, r, dv, scale)) return e;
-    // a thread per element of every token's row in the gradients' last passes
-    if ((long long)B * H * (T + 1LL) > (1LL << 38) / 256) return LA_ERR_UNSUPPORTED;
+    // a thread per element of every token's row in the gradients' last passes (packed: T counts all sequences' tokens)
+    if (!packed && (long long)B * H * (T + 1LL) > (1LL << 38) / 256) return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
 
@@ -1113,7 +1113,7 @@ constexpr int kGdeltaWalk = 16;
 // Whether prompts of these sizes run in chunks (with every token array on a 16-byte boundary).
 bool gdelta_tc_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, bool packed)
 {
-    return check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, 1.f) == LA_OK && dtype == LA_DTYPE_BF16 && (r == 64 || r == 128) &&
+    return check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, 1.f, packed) == LA_OK && dtype == LA_DTYPE_BF16 && (r == 64 || r == 128) &&
            dv % 64 == 0 && T > (packed ? 0 : kGdeltaWalk) && la::gdelta_tc_slots(B, T, packed) * H <= 0x7fffffffLL;
 }
 
@@ -1127,9 +1127,9 @@ la_status gdelta_forward(const void *q, const void *k, const void *v, la_dtype d
                          float *S_out, void *workspace, size_t workspace_bytes, la_stream_t stream)
 {
     if (!S_out || (T > 0 && (!q || !k || !v || !y))) return LA_ERR_NULL;
-    if (const la_status e = check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, scale)) return e;
-    if (const la_status e = check_gdelta_pointers(dtype, {q, k, v, y}, {alpha, beta, S0, S_out, cu_seqlens})) return e;
     const bool packed = cu_seqlens != nullptr;
+    if (const la_status e = check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, scale, packed)) return e;
+    if (const la_status e = check_gdelta_pointers(dtype, {q, k, v, y}, {alpha, beta, S0, S_out, cu_seqlens})) return e;
     if (const la_status e = check_workspace(workspace, workspace_bytes, gdelta_workspace(dtype, B, H, Hk, T, r, dv, packed))) return e;
     const la::GdeltaShape s = gdelta_shape(B, H, Hk, T, r, dv, alpha, beta, status_word(), cu_seqlens);
     if (!s.status) return LA_ERR_CUDA;

@@ -60,6 +60,14 @@ def test_gated_delta_workspaces(native):  # noqa: F811
             assert fn(*args) == 0, args
 
 
+def test_many_packed_sequences(native):  # noqa: F811
+    """total_T counts the tokens of all sequences: their number times that is no size of anything."""
+    L = native.lib()
+    sizes = (4096, 16, 8, 1 << 20, 128, 128, BASE["dtype"])
+    assert L.la_gated_delta_prefill_workspace_bytes(*sizes) == 0            # B sequences of that length each
+    assert L.la_gated_delta_prefill_varlen_workspace_bytes(*sizes) > 0
+
+
 SCORE = "logits dtype ld tokens N V top lp ent lse tlp ttok stream"
 GRAD = "logits dtype ld tokens lse ent dlp dent N V out gd stream"
 ROWS = dict(logits=FAKE, dtype=0, ld=1000, tokens=FAKE, N=4, V=1000, top=5, lp=FAKE, ent=FAKE, lse=FAKE, tlp=FAKE, ttok=FAKE, dlp=FAKE,

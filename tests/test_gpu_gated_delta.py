@@ -215,6 +215,27 @@ def test_packed_neighbours_are_not_read(la):
     assert torch.equal(y[:70], want_y[:70]) and torch.equal(y[100:], want_y[100:])
 
 
+def test_packed_many_sequences(la):
+    """More sequences than the plan takes at a time, and more of them times all tokens than 2^30."""
+    g = torch.Generator().manual_seed(21)
+    B, H, Hk, r, dv = 3000, 8, 4, 64, 64
+    lens = torch.randint(0, 31, (B,), generator=g)
+    lens[[5, 1500, 2999]] = torch.tensor([700, 130, 65])
+    cu = torch.cat((torch.zeros(1, dtype=torch.int64), lens.cumsum(0)))
+    total = int(cu[-1])
+    assert B * H * total > 1 << 30
+    q, k, v, _, alpha, beta, _, _ = make(1, H, Hk, total, r, dv, torch.bfloat16, False, 22, layout="tok")
+    S0 = torch.randn((B, H, r, dv), generator=g).mul(0.3).cuda()
+    y, S = la.gated_delta_prefill_varlen(q, k, v, cu.int().cuda(), alpha, beta, S0=S0, scale=0.2)
+    assert la.last_device_status() == 0
+    bh = lambda x, s: x[s].transpose(0, 1)[None]  # noqa: E731
+    for b in [0, 1, 5, 1023, 1024, 1500, 2047, 2048, 2998, 2999]:
+        s = slice(int(cu[b]), int(cu[b + 1]))
+        ref_y, ref_S, _, _ = R.prefill(*(bh(x, s) for x in (q, k, v, alpha, beta)), S0[b:b + 1], 0.2)
+        R.check(S[b:b + 1], ref_S, torch.bfloat16, f"S {b}", int(lens[b]))
+        R.check(bh(y, s), ref_y, torch.bfloat16, f"y {b}", int(lens[b]))
+
+
 def test_packed_bad_bounds(la):
     """A sequence outside the batch, or of negative length, is skipped and recorded; the others run."""
     q, k, v, _, alpha, beta, _, _ = make(3, 2, 2, 100, 128, 128, torch.bfloat16, False, 13, layout="tok")
