@@ -83,17 +83,17 @@ gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, 
 // X_10 = -X_11 (L_10 X_00).
 // Bound by instructions, about 1500 issue slots per SM quarter and chunk.
 constexpr int kPThreads = 128;
-constexpr int LD = 68;                           // FP32 row stride of Lt
-constexpr int LDT = 36;                          // FP32 row stride of the 32 x 32 blocks
-constexpr int LDS16 = 20;                        // and of the 16 x 16 ones
+// FP32 row strides of Lt, of the 32 x 32 blocks and of the 16 x 16 ones: the operands of the small products are read without
+// bank conflicts
+constexpr int LD = 72, LDT = 40, LDS16 = 24;
 // K and Q interleaved by 64-feature block ([K; Q] is one 128-row operand per block); once [G; P] is complete the region
 // holds L and the solve's blocks
 constexpr uint32_t kPL = 0;                      // Lt (64 x LD): Lt[u][i] holds row i, column u; then X10 [i][j]
 constexpr uint32_t kPX00 = kPL + kC * LD * 4;    // X00 [u][j]
 constexpr uint32_t kPX11t = kPX00 + 32 * LDT * 4;   // X11 transposed [u][i]
-constexpr uint32_t kPM = kPX11t + 32 * LDT * 4;  // M = L10 X00 [u][j]
-constexpr uint32_t kPM16 = kPM + 32 * LDT * 4;   // the same for the two 32-blocks' halves
-constexpr uint32_t kPGate = kPM16 + 2 * 16 * LDS16 * 4;   // alpha, beta and e^G of the chunk's tokens
+constexpr uint32_t kPM = kPX11t + 32 * LDT * 4;  // M = L10 X00 [u][j]; before it the same for the two 32-blocks' halves
+constexpr uint32_t kPGate = kPM + 32 * LDT * 4;  // alpha, beta and e^G of the chunk's tokens
+static_assert(2 * 16 * LDS16 <= 32 * LDT, "the halves' products fit");
 constexpr uint32_t kPSmall = kPGate + 3 * kC * 4;
 static_assert(kPGate >= 4 * kTile && kPGate % 16 == 0, "the gates lie behind the K, Q tiles");
 
@@ -103,6 +103,43 @@ struct alignas(16) PSmall {
     int abort_flag;
 };
 constexpr uint32_t kPSmemBytes = kPSmall + sizeof(PSmall) + 1024;
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x as two TF32 numbers, 11 bits of it and the next 11
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo)
+{
+    hi = __float_as_uint(x) & 0xffffe000u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+
+// A warp: c += A B, A 16 x 8 K8 (element (row, k) = a(row, k)), B 8 K8 x 8 N, in FP32 but for the product of the low parts (2^-22
+// of the terms).  c[n][0..3]: rows lane / 4 (+ 8), columns 8 n + 2 (lane % 4) (+ 1) as (row, col), (row, col + 1), (row + 8, ..)
+template <int K8, int N, class A, class B>
+__device__ __forceinline__ void small_product(float (&c)[N][4], int lane, A a, B b)
+{
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int k = 0; k < 8 * K8; k += 8) {
+        uint32_t ah[4], al[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_tf32(a(g + 8 * (i & 1), k + t + 4 * (i >> 1)), ah[i], al[i]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) split_tf32(b(k + t + 4 * i, 8 * n + g), bh[i], bl[i]);
+            mma_tf32(c[n], al, bh[0], bh[1]);
+            mma_tf32(c[n], ah, bl[0], bl[1]);
+            mma_tf32(c[n], ah, bh[0], bh[1]);
+        }
+    }
+}
 
 // BACK: for the gradients, which take A in two parts and betas of at least 2^-40 (dbeta is formed by dividing by them; the
 // change is far below FP32's rounding).
@@ -119,7 +156,6 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     float *X00 = reinterpret_cast<float *>(base + kPX00);
     float *X11t = reinterpret_cast<float *>(base + kPX11t);
     float *Mf = reinterpret_cast<float *>(base + kPM);
-    float *M16 = reinterpret_cast<float *>(base + kPM16);
     float *alpha = reinterpret_cast<float *>(base + kPGate), *beta = alpha + kC, *expG = beta + kC;
 
     const GdeltaShape &s = args.s;
@@ -300,7 +336,8 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                     for (int y = 1; y >= 0; --y) {
                         const int j0 = 32 * half + 8 * x + 4 * y;
-                        const float4 a4 = *reinterpret_cast<const float4 *>(alpha + j0), b4 = *reinterpret_cast<const float4 *>(beta + j0);
+                        const float4 a4 = *reinterpret_cast<const float4 *>(alpha + j0),
+                                     b4 = warp < 2 ? *reinterpret_cast<const float4 *>(beta + j0) : a4;
                         const float av[4] = {a4.x, a4.y, a4.z, a4.w}, bv[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
                         for (int e = 3; e >= 0; --e) {
@@ -376,78 +413,53 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             }
         }
         __syncthreads();
-        // The blocks of 16 below them: 64 threads per 32-block, 2 x 2 elements each.
+        // The blocks of 16 below them, X_b0 = -X_b (L_b0 X_a): two warps per 32-block, 8 columns each.  C's rows and columns of a lane:
+        const int r = lane >> 2, c = 2 * (lane & 3);
         {
-            const int k2 = tid >> 6, r2 = 2 * ((tid >> 3) & 7), c2 = 2 * (tid & 7);
-            float *M = M16 + k2 * 16 * LDS16;
-            const float *Lo = Lt + 32 * k2 * LD + 32 * k2 + 16 + r2;
-            float m00 = 0.f, m01 = 0.f, m10 = 0.f, m11 = 0.f;
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const float2 lv = *reinterpret_cast<const float2 *>(Lo + u * LD);
-                float x0, x1;
-                if (k2 == 0) {
-                    const float2 xv = *reinterpret_cast<const float2 *>(X00 + u * LDT + c2);
-                    x0 = xv.x, x1 = xv.y;
-                } else {
-                    x0 = X11t[c2 * LDT + u], x1 = X11t[(c2 + 1) * LDT + u];
-                }
-                m00 = fmaf(lv.x, x0, m00), m01 = fmaf(lv.x, x1, m01), m10 = fmaf(lv.y, x0, m10), m11 = fmaf(lv.y, x1, m11);
-            }
-            *reinterpret_cast<float2 *>(M + r2 * LDS16 + c2) = make_float2(m00, m01);
-            *reinterpret_cast<float2 *>(M + (r2 + 1) * LDS16 + c2) = make_float2(m10, m11);
+            const int k2 = warp >> 1, n0 = 8 * (warp & 1);
+            float *M = Mf + k2 * 16 * LDS16;
+            const float *Lo = Lt + 32 * k2 * LD + 32 * k2 + 16;
+            float m[1][4] = {};
+            auto lo = [&](int row, int u) { return Lo[u * LD + row]; };
+            if (k2 == 0) small_product<2>(m, lane, lo, [&](int u, int col) { return X00[u * LDT + n0 + col]; });
+            else small_product<2>(m, lane, lo, [&](int u, int col) { return X11t[(n0 + col) * LDT + u]; });
+            *reinterpret_cast<float2 *>(M + r * LDS16 + n0 + c) = make_float2(m[0][0], m[0][1]);
+            *reinterpret_cast<float2 *>(M + (r + 8) * LDS16 + n0 + c) = make_float2(m[0][2], m[0][3]);
             __syncthreads();
-            m00 = m01 = m10 = m11 = 0.f;
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const float2 mv = *reinterpret_cast<const float2 *>(M + u * LDS16 + c2);
-                float x0, x1;
-                if (k2 == 0) {
-                    x0 = X00[(16 + r2) * LDT + 16 + u], x1 = X00[(17 + r2) * LDT + 16 + u];
-                } else {
-                    const float2 xv = *reinterpret_cast<const float2 *>(X11t + (16 + u) * LDT + 16 + r2);
-                    x0 = xv.x, x1 = xv.y;
-                }
-                m00 = fmaf(-x0, mv.x, m00), m01 = fmaf(-x0, mv.y, m01), m10 = fmaf(-x1, mv.x, m10), m11 = fmaf(-x1, mv.y, m11);
-            }
+            float x[1][4] = {};
+            auto mb = [&](int u, int col) { return M[u * LDS16 + n0 + col]; };
             if (k2 == 0) {
-                *reinterpret_cast<float2 *>(X00 + (16 + r2) * LDT + c2) = make_float2(m00, m01);
-                *reinterpret_cast<float2 *>(X00 + (17 + r2) * LDT + c2) = make_float2(m10, m11);
+                small_product<2>(x, lane, [&](int row, int u) { return -X00[(16 + row) * LDT + 16 + u]; }, mb);
+                *reinterpret_cast<float2 *>(X00 + (16 + r) * LDT + n0 + c) = make_float2(x[0][0], x[0][1]);
+                *reinterpret_cast<float2 *>(X00 + (24 + r) * LDT + n0 + c) = make_float2(x[0][2], x[0][3]);
             } else {
-                *reinterpret_cast<float2 *>(X11t + c2 * LDT + 16 + r2) = make_float2(m00, m10);
-                *reinterpret_cast<float2 *>(X11t + (c2 + 1) * LDT + 16 + r2) = make_float2(m01, m11);
+                small_product<2>(x, lane, [&](int row, int u) { return -X11t[(16 + u) * LDT + 16 + row]; }, mb);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X11t[(n0 + c + (e & 1)) * LDT + 16 + r + 8 * (e >> 1)] = x[0][e];
             }
         }
         __syncthreads();
-        // M = L10 X00 and then X10 = -X11 M: thread (warp, lane) computes rows 4 rg .. 4 rg + 3 and columns 2 cp, 2 cp + 1,
-        // rg = 2 warp + lane / 16
-        const int rg = 2 * warp + (lane >> 4), cp = lane & 15;
-        {
-            float2 m4[4] = {};
-#pragma unroll 8
-            for (int u = 0; u < 32; ++u) {
-                const float2 tj = *reinterpret_cast<const float2 *>(X00 + u * LDT + 2 * cp);
-                const float4 g = *reinterpret_cast<const float4 *>(Lt + u * LD + 32 + 4 * rg);
-                const float gv[4] = {g.x, g.y, g.z, g.w};
+        // M = L10 X00 and then X10 = -X11 M: a 16 x 16 quarter per warp
+        const int r0 = 16 * (warp >> 1), n0 = 16 * (warp & 1);
+        auto put = [&](float *to, const float (&o)[2][4]) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m4[e] = __ffma2_rn(make_float2(gv[e], gv[e]), tj, m4[e]);
+            for (int n = 0; n < 2; ++n) {
+                *reinterpret_cast<float2 *>(to + (r0 + r) * LDT + n0 + 8 * n + c) = make_float2(o[n][0], o[n][1]);
+                *reinterpret_cast<float2 *>(to + (r0 + r + 8) * LDT + n0 + 8 * n + c) = make_float2(o[n][2], o[n][3]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(Mf + (4 * rg + e) * LDT + 2 * cp) = m4[e];
+        };
+        {
+            float m[2][4] = {};
+            small_product<4>(m, lane, [&](int row, int u) { return Lt[u * LD + 32 + r0 + row]; },
+                             [&](int u, int col) { return X00[u * LDT + n0 + col]; });
+            put(Mf, m);
         }
         __syncthreads();
         {
-            float2 o4[4] = {};
-#pragma unroll 8
-            for (int u = 0; u < 32; ++u) {
-                const float2 mj = *reinterpret_cast<const float2 *>(Mf + u * LDT + 2 * cp);
-                const float4 a = *reinterpret_cast<const float4 *>(X11t + u * LDT + 4 * rg);
-                const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o4[e] = __ffma2_rn(make_float2(-av[e], -av[e]), mj, o4[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(X10 + (4 * rg + e) * LDT + 2 * cp) = o4[e];
+            float x[2][4] = {};
+            small_product<4>(x, lane, [&](int row, int u) { return -X11t[u * LDT + r0 + row]; },
+                             [&](int u, int col) { return Mf[u * LDT + n0 + col]; });
+            put(X10, x);
         }
         __syncthreads();
         // X's two parts, 16-byte words of the images' rows
