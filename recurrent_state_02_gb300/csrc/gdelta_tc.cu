@@ -92,10 +92,11 @@ constexpr uint32_t kPL = 0;                      // Lt (64 x LD): Lt[u][i] holds
 constexpr uint32_t kPX00 = kPL + kC * LD * 4;    // X00 [u][j]
 constexpr uint32_t kPX11t = kPX00 + 32 * LDT * 4;   // X11 transposed [u][i]
 constexpr uint32_t kPM = kPX11t + 32 * LDT * 4;  // M = L10 X00 [u][j]; before it the same for the two 32-blocks' halves
-constexpr uint32_t kPGate = kPM + 32 * LDT * 4;  // alpha, beta and e^G of the chunk's tokens
+constexpr uint32_t kPA = kPX00;                  // before them A's image (BACK: two), on its way out
+constexpr uint32_t kPGate = kPA + 2 * kTile;     // alpha, beta and e^G of the chunk's tokens
 static_assert(2 * 16 * LDS16 <= 32 * LDT, "the halves' products fit");
 constexpr uint32_t kPSmall = kPGate + 3 * kC * 4;
-static_assert(kPGate >= 4 * kTile && kPGate % 16 == 0, "the gates lie behind the K, Q tiles");
+static_assert(kPGate >= 4 * kTile && kPGate >= kPM + 32 * LDT * 4 && kPGate % 16 == 0, "the gates lie behind the K, Q tiles and the blocks");
 
 struct alignas(16) PSmall {
     uint64_t full, mma;
@@ -324,7 +325,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int ri = 32 * (warp & 1) + lane;
             const uint32_t tq = tmem + ((uint32_t)(32 * warp) << 16);
             const bool real = ri < nt;
-            uint8_t *arow = wsc + kWsA + (size_t)ri * 128, *lrow = wsc + kWsAl + (size_t)ri * 128;
+            uint8_t *arow = base + kPA + ri * 128, *lrow = arow + kTile;
             float dec = 1.f, next = 1.f;         // e^{G_i - G_j}; the gate of token j + 1
 #pragma unroll 1
             for (int half = warp & 1; half >= 0; --half) {
@@ -370,13 +371,19 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
             }
         }
+        fence_proxy_async_smem();
         __syncthreads();
-        // The diagonal blocks of 16: lane l of warp w owns column l % 16 of block w; after step u, acc[u] is final and is subtracted
-        // from the rows below.
-        {
-            const int l = lane & 15;
-            const float *Lb = Lt + 16 * warp * LD + 16 * warp;
-            float acc[16];
+        if (tid == 3 * 32) {            // A goes out as it lies (row by row it would take a line per lane)
+            bulk_store(wsc + kWsA, smem_u32(base + kPA), kTile);
+            if (BACK) bulk_store(wsc + kWsAl, smem_u32(base + kPA) + kTile, kTile);
+            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        // The diagonal blocks of 16, two in each of the first two warps: lane l + 16 m owns column l of block 2 warp + m; after step
+        // u, acc[u] is final and is subtracted from the rows below.
+        const int l = lane & 15, o = lane & 16;
+        float acc[16];
+        if (warp < 2) {
+            const float *Lb = Lt + (32 * warp + o) * LD + 32 * warp + o;
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[i] = i == l ? 1.f : 0.f;
 #pragma unroll
@@ -391,26 +398,22 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (4 * g4 + e > u) acc[4 * g4 + e] = fmaf(-lv[e], t, acc[4 * g4 + e]);
                 }
             }
-            // X00 by rows, X11 by columns; the upper lanes write the zeros above the diagonal
-            const int o = 16 * (warp & 1);
-            if (warp < 2) {
-                if (lane < 16) {
+        }
+        __syncthreads();                // (A has been read)
+        // X00 by rows, X11 by columns, and the zeros above the diagonal
+        if (warp == 0) {
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) X00[(o + u) * LDT + o + l] = acc[u];
-                } else if (warp == 0) {
+            for (int u = 0; u < 16; ++u) X00[(o + u) * LDT + o + l] = acc[u];
+        } else if (warp == 1) {
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) X00[u * LDT + 16 + l] = 0.f;
-                }
-            } else {
-                if (lane < 16) {
+            for (int m = 0; m < 4; ++m)
+                *reinterpret_cast<float4 *>(X11t + (o + l) * LDT + o + 4 * m) = make_float4(acc[4 * m], acc[4 * m + 1], acc[4 * m + 2], acc[4 * m + 3]);
+        } else if (warp == 2) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        *reinterpret_cast<float4 *>(X11t + (o + l) * LDT + o + 4 * m) = make_float4(acc[4 * m], acc[4 * m + 1], acc[4 * m + 2], acc[4 * m + 3]);
-                } else if (warp == 2) {
+            for (int u = 0; u < 8; ++u) X00[(2 * u + (o >> 4)) * LDT + 16 + l] = 0.f;
+        } else {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) *reinterpret_cast<float4 *>(X11t + (16 + l) * LDT + 4 * m) = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-            }
+            for (int u = 0; u < 8; ++u) X11t[(16 + 2 * u + (o >> 4)) * LDT + l] = 0.f;
         }
         __syncthreads();
         // The blocks of 16 below them, X_b0 = -X_b (L_b0 X_a): two warps per 32-block, 8 columns each.  C's rows and columns of a lane:
