@@ -16,6 +16,7 @@
 //     dL/dlog alpha_t = <S_T, dS_T> + sum_{s >= t} (q_s . dq_s - v_s . dv_s).
 
 #include "gdelta.h"
+#include "launch_after.cuh"
 #include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -498,6 +499,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(256)
 gdelta_group_sum_kernel(GdeltaShape s, const float *dq, const float *dk, void *dq_out, void *dk_out)
 {
+    wait_for_last();
     const long long n = (long long)s.T * s.r, i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= n * s.B * s.Hk) return;
     const int group = s.H / s.Hk;
@@ -693,9 +695,8 @@ cudaError_t launch_gdelta_group_sum(const GdeltaShape &s, const float *dq, const
                                     cudaStream_t stream)
 {
     const unsigned grid = (unsigned)(((long long)s.B * s.Hk * s.T * s.r + 255) / 256);
-    if (bf16) gdelta_group_sum_kernel<true><<<grid, 256, 0, stream>>>(s, dq, dk, dq_out, dk_out);
-    else gdelta_group_sum_kernel<false><<<grid, 256, 0, stream>>>(s, dq, dk, dq_out, dk_out);
-    return cudaGetLastError();
+    return launch_after(bf16 ? gdelta_group_sum_kernel<true> : gdelta_group_sum_kernel<false>, grid, 256, 0, stream, s, dq, dk, dq_out,
+                        dk_out);
 }
 
 // e, lam [B,H,T,dv]; w (then dk), dq [B,H,T,r]; S_T; dG [B,H,T]

@@ -104,6 +104,8 @@ __device__ __forceinline__ void back_chain(const CUtensorMap &map_k, const CUten
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_last();
+    let_next_start();
 
     if (warp >= kIssuer) {
         regs_dec<kRegsRest>();
@@ -618,6 +620,8 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_last();
+    let_next_start();
 
     if (warp == kGLoader) {
         if (elect_one()) {
@@ -965,12 +969,11 @@ cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const Gdelt
     if ((e = set_smem_once(gdelta_grad_kernel<KD, true>, kGSmemBytes<KD>, once_g32)) != cudaSuccess) return e;
     const unsigned heads = (unsigned)(a.s.B * a.s.H), chunks = heads * (unsigned)((a.s.T + kC - 1) / kC);
     if ((e = launch_gdelta_prep_backward(m.q, m.k, prep, stream)) != cudaSuccess) return e;
-    gdelta_back_chain_kernel<KD><<<2 * heads, kThreads, kBSmemBytes<KD>, stream>>>(m.k, m.v, m.dy, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(gdelta_back_chain_kernel<KD>, 2 * heads, kThreads, kBSmemBytes<KD>, stream, m.k, m.v, m.dy, a)) != cudaSuccess)
+        return e;
     const unsigned grid = sms > 0 && (unsigned)sms < chunks ? sms : chunks;
-    if (a.s.Hk < a.s.H) gdelta_grad_kernel<KD, true><<<grid, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a, (int)chunks);
-    else gdelta_grad_kernel<KD, false><<<grid, kGThreads, kGSmemBytes<KD>, stream>>>(m.q, m.k, m.v, m.dy, a, (int)chunks);
-    return cudaGetLastError();
+    return launch_after(a.s.Hk < a.s.H ? gdelta_grad_kernel<KD, true> : gdelta_grad_kernel<KD, false>, grid, kGThreads, kGSmemBytes<KD>, stream,
+                        m.q, m.k, m.v, m.dy, a, (int)chunks);
 }
 
 }  // namespace

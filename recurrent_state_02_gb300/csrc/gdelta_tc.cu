@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, int *status)
 {
     __shared__ int part[32], len[kPlanThreads];
+    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int carry = 0;
     for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
@@ -162,6 +163,8 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const GdeltaShape &s = args.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool packed = s.cu_seqlens != nullptr;
+    let_next_start();
+    if (packed) wait_for_last();        // the plan
     // this CTA's head, sequence and chunk
     const int h = blockIdx.x % s.H, hk = h / (s.H / s.Hk);
     const int slot = blockIdx.x / s.H;
@@ -562,7 +565,10 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     const int tiles = (dv + 127) / 128;
     const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % H;
     int b = blockIdx.x / (tiles * H);
-    if (packed) b = args.order[b];
+    if (packed) {
+        wait_for_last();
+        b = args.order[b];
+    }
     const Span sp = span_of(args, b);
     if (!sp.valid) return;
     const int T = sp.T, nch = (T + kC - 1) / kC;
@@ -583,6 +589,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_last();
 
     if (warp >= kIssuer) {
         regs_dec<kRegsRest>();
@@ -956,7 +963,10 @@ static cudaError_t launch_prep(const CUtensorMap &q, const CUtensorMap &k, const
     if (e != cudaSuccess) return e;
     const long long n = gdelta_tc_slots(a.s.B, a.s.T, a.s.cu_seqlens != nullptr) * a.s.H;
     if (n > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (n > 0) gdelta_prep_kernel<KD, BACK><<<(unsigned)n, kPThreads, kPSmemBytes, stream>>>(q, k, a);
+    if (n == 0) return cudaSuccess;
+    // (packed: after the plan; else nothing to start ahead of)
+    if (a.s.cu_seqlens) return launch_after(gdelta_prep_kernel<KD, BACK>, (unsigned)n, kPThreads, kPSmemBytes, stream, q, k, a);
+    gdelta_prep_kernel<KD, BACK><<<(unsigned)n, kPThreads, kPSmemBytes, stream>>>(q, k, a);
     return cudaGetLastError();
 }
 
@@ -979,8 +989,7 @@ static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaS
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if ((e = launch_prep<KD, false>(m.q, m.k, a, stream)) != cudaSuccess) return e;
-    gdelta_chain_kernel<KD><<<(unsigned)nmain, kMThreads, kMSmemBytes<KD>, stream>>>(m.q, m.k, m.v, a);
-    return cudaGetLastError();
+    return launch_after(gdelta_chain_kernel<KD>, (unsigned)nmain, kMThreads, kMSmemBytes<KD>, stream, m.q, m.k, m.v, a);
 }
 
 cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream)

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "gdelta_tc.h"
+#include "launch_after.cuh"
 #include "tc_common.cuh"
 #include "tc_short.cuh"
 
