@@ -555,10 +555,13 @@ gdelta_gate_sum_kernel(GdeltaShape s, const float *S_T, const float *dS_T, const
 }
 
 // ------------------------------------------------------------ decode step
-// With p = S^T k and u = S^T q of the state as it is, both in one pass over it, the step needs no second
-// pass before the write: e = v - alpha p, y = scale (alpha u + beta (k . q) e), S <- alpha S + k (beta e)^T.
-// Reads and rewrites r dv FP32 words per head, three FMAs each: bound by HBM.  CTA (b, h, 128 columns) of 8 warps; a
-// warp takes RW rows, its lanes 4 columns each, and issues every state load before any arithmetic.
+// With p = S^T k of the state as it is: e = v - alpha p, S <- alpha S + k (beta e)^T, y = scale S^T q of the rows as they are
+// written.  Reads and rewrites r dv FP32 words per head, four FMAs each: bound by HBM.  CTA (b, h, 128 columns) of 8
+// warps; a warp takes RW rows, its lanes 4 columns each, issues every state load before any arithmetic and keeps the rows in
+// registers.  No store can leave before all of a head's rows are there, so it is other CTAs that keep HBM busy
+// meanwhile: at 80 registers three fit an SM (537 MB of state, B = 256 H = 16 128 x 128: 87 us, 6.1 TB/s; two at 128
+// registers 96; a ring of three whole states in shared memory, filled and emptied by bulk copies, 98).  So k, q, v and the gates are read
+// from shared memory where they are used, and the read of S^T q waits for the write instead of taking registers beside p.
 __device__ __forceinline__ float4 ld_stream(const float4 *p)
 {
     float4 v;
@@ -578,13 +581,22 @@ __device__ __forceinline__ float4 fma4(float a, float4 x, float4 y)
     return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
 }
 
+__device__ __forceinline__ float2 lds_pair(uint32_t a)      // (volatile: not kept in registers from one use to the next)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+
 template <bool BF16, int RW>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, RW == 8 ? 5 : RW == 16 ? 3 : 1)
 gdelta_decode_kernel(const void *__restrict__ q, const void *__restrict__ k, const void *__restrict__ v, GdeltaShape s,
                      float *__restrict__ S, float scale, void *__restrict__ y)
 {
-    __shared__ float qs[8 * RW], ks[8 * RW];
-    __shared__ float4 part[8][2][32];
+    __shared__ float2 kqs[8 * RW];           // k, q
+    __shared__ float4 vs[32];
+    __shared__ float2 gates;
+    __shared__ float4 part[8][32], part_y[8][32];
     const int r = s.r, dv = s.dv;
     const size_t bh = blockIdx.x, kh = bh / s.H * s.Hk + (bh % s.H) / (s.H / s.Hk);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -598,51 +610,47 @@ gdelta_decode_kernel(const void *__restrict__ q, const void *__restrict__ k, con
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col && warp * RW + i < r) x[i] = ld_stream(Sr + (size_t)i * dv4);
     }
-    for (int i = tid; i < 8 * RW; i += 256) {
-        qs[i] = i < r ? load_elem<BF16>(q, kh * r + i) : 0.f;
-        ks[i] = i < r ? load_elem<BF16>(k, kh * r + i) : 0.f;
+    for (int i = tid; i < 8 * RW; i += 256)
+        kqs[i] = i < r ? make_float2(load_elem<BF16>(k, kh * r + i), load_elem<BF16>(q, kh * r + i)) : make_float2(0.f, 0.f);
+    if (tid < 128) {
+        const int c = blockIdx.y * 128 + tid;
+        reinterpret_cast<float *>(vs)[tid] = c < dv ? load_elem<BF16>(v, bh * dv + c) : 0.f;
     }
-    const float al = s.alpha ? s.alpha[bh] : 1.f, be = s.beta ? s.beta[bh] : 1.f;
-    float4 vv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (col) {
-        vv.x = load_elem<BF16>(v, bh * dv + j);
-        vv.y = load_elem<BF16>(v, bh * dv + j + 1);
-        vv.z = load_elem<BF16>(v, bh * dv + j + 2);
-        vv.w = load_elem<BF16>(v, bh * dv + j + 3);
-    }
+    if (tid == 0) gates = make_float2(s.alpha ? s.alpha[bh] : 1.f, s.beta ? s.beta[bh] : 1.f);
     __syncthreads();
-    float4 p = make_float4(0.f, 0.f, 0.f, 0.f), u = p;
+    const uint32_t kq0 = smem_u32(kqs + warp * RW);
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < RW; ++i) c = fma4(lds_pair(kq0 + 8 * i).x, x[i], c);
+    part[warp][lane] = c;
+    __syncthreads();
+    c = part[0][lane];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) c = fma4(1.f, part[w][lane], c);
+    const float al = gates.x;
+    {
+        const float be = gates.y;
+        const float4 vv = vs[lane];
+        c = make_float4(be * fmaf(-al, c.x, vv.x), be * fmaf(-al, c.y, vv.y), be * fmaf(-al, c.z, vv.z), be * fmaf(-al, c.w, vv.w));
+    }
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        p = fma4(ks[warp * RW + i], x[i], p);
-        u = fma4(qs[warp * RW + i], x[i], u);
+        const float2 kq = lds_pair(kq0 + 8 * i);
+        const float4 n = make_float4(fmaf(al, x[i].x, kq.x * c.x), fmaf(al, x[i].y, kq.x * c.y), fmaf(al, x[i].z, kq.x * c.z),
+                                     fmaf(al, x[i].w, kq.x * c.w));
+        if (col && warp * RW + i < r) st_stream(Sr + (size_t)i * dv4, n);
+        u = fma4(kq.y, n, u);
     }
-    part[warp][0][lane] = p;
-    part[warp][1][lane] = u;
-    float kq = 0.f;                          // (every warp for itself, in the same order)
-    for (int i = lane; i < 8 * RW; i += 32) kq = fmaf(ks[i], qs[i], kq);
-    kq = warp_sum(kq);
+    part_y[warp][lane] = u;
     __syncthreads();
-    p = part[0][0][lane];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) p = fma4(1.f, part[w][0][lane], p);
-    const float4 c = make_float4(be * fmaf(-al, p.x, vv.x), be * fmaf(-al, p.y, vv.y), be * fmaf(-al, p.z, vv.z),
-                                 be * fmaf(-al, p.w, vv.w));
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-        const float kr = ks[warp * RW + i];
-        if (col && warp * RW + i < r)
-            st_stream(Sr + (size_t)i * dv4, make_float4(fmaf(al, x[i].x, kr * c.x), fmaf(al, x[i].y, kr * c.y),
-                                                        fmaf(al, x[i].z, kr * c.z), fmaf(al, x[i].w, kr * c.w)));
-    }
     if (warp == 0 && col) {
-        u = part[0][1][lane];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) u = fma4(1.f, part[w][1][lane], u);
-        store_elem<BF16>(y, bh * dv + j, scale * fmaf(al, u.x, kq * c.x));
-        store_elem<BF16>(y, bh * dv + j + 1, scale * fmaf(al, u.y, kq * c.y));
-        store_elem<BF16>(y, bh * dv + j + 2, scale * fmaf(al, u.z, kq * c.z));
-        store_elem<BF16>(y, bh * dv + j + 3, scale * fmaf(al, u.w, kq * c.w));
+        for (int w = 1; w < 8; ++w) u = fma4(1.f, part_y[w][lane], u);
+        store_elem<BF16>(y, bh * dv + j, scale * u.x);
+        store_elem<BF16>(y, bh * dv + j + 1, scale * u.y);
+        store_elem<BF16>(y, bh * dv + j + 2, scale * u.z);
+        store_elem<BF16>(y, bh * dv + j + 3, scale * u.w);
     }
 }
 

@@ -253,7 +253,8 @@ def test_packed_bad_bounds(la):
 
 @DTYPES
 @pytest.mark.parametrize("size", [(1, 1, 1, 128, 128), (3, 4, 2, 64, 64), (2, 6, 1, 33, 7), (2, 2, 2, 256, 160), (70, 4, 4, 128, 100),
-                                  (1, 2, 1, 1, 1)], ids=ids)
+                                  (1, 2, 1, 1, 1), (99, 8, 4, 128, 128), (100, 8, 2, 64, 64), (41, 16, 8, 60, 256),
+                                  (305, 4, 4, 1, 64)], ids=ids)
 def test_decode_steps(la, size, dtype):
     """Steps of one token each, the state in place, against one prefill of them."""
     B, H, Hk, r, dv = size
