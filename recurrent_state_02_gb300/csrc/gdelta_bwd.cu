@@ -15,6 +15,9 @@
 // (the gates' gradient is anchored before every chunk, so that nothing is summed over the sequence).
 // Kernels: gdelta_prep (A, X, gates, scale e^G Q); the forward chain again, keeping the states between the chunks and E, and beside
 // it the backward chain, keeping their gradients and N; and a kernel over all chunks.
+// At B4 H16 T4096, 128 wide: 78 us, 240 us (both chains, 128 CTAs; 1.44 GB moved, 6 TB/s) and 236 us (1.21 GB, 5.1 TB/s), so that what the
+// kernels hand one another, the states between the chunks and E and N above all, is what bounds them.  Forming each chunk's
+// gradients inside the chains would spare half of it, but needs both chains at the same chunk.
 // Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand; what reaches dq and
 // dk only, the high one.
 

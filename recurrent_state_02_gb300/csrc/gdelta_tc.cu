@@ -19,7 +19,8 @@
 //
 // Precision: the state lives in FP32 registers.  q, k, v are exact as BF16 operands; what the kernels derive is split into
 // two BF16 parts (16 bits of mantissa and a sign) wherever it reaches the state -- S, R, X and V' in steps 1 to 3, the product of
-// two such parts' low halves left out -- and is rounded to one where it reaches y only (which is BF16).
+// two such parts' low halves left out -- and is rounded to one where it reaches y only (which is BF16).  Against 64 bits the
+// state is off by 3e-6 and y by 2.7e-3 (relative 2-norms; the rounding of y alone is 1.7e-3).
 
 #include "gdelta_tc.cuh"
 
@@ -80,9 +81,11 @@ gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, 
 // ------------------------------------------------------- A, X and the gates
 // Four warps per chunk and head.  [G; P] = [K; Q] K^T on the tensor cores; a row of L or A per thread, its decays as running products
 // of the gates from the diagonal to the left (no logarithms, and gates of 0 need no care); then X = (I + L)^{-1} in FP32: the four
-// diagonal blocks of 16 by forward substitution, a warp each, and the blocks below them, 16 and then 32 wide, as
-// X_10 = -X_11 (L_10 X_00).
-// Bound by instructions, about 1500 issue slots per SM quarter and chunk.
+// diagonal blocks of 16 by forward substitution, two in a warp, and the blocks below them, 16 and then 32 wide, as
+// X_10 = -X_11 (L_10 X_00) in warp-wide TF32 products of numbers in two parts.  (As FP32 sums with 2 x 2 and 4 x 2 numbers per thread
+// these products took 60 % of the kernel's 4000 shared-memory wavefronts per chunk, which bound it.)
+// Now 2200 instructions per warp and chunk: 60 us for 4096 chunks (B4 H16 T4096, 128 wide; 76 before), issue slots 55 % and shared
+// memory 56 % busy, the rest being the solve's barriers at 24 warps per SM.  For the gradients 78 us, half of HBM's rate.
 constexpr int kPThreads = 128;
 // FP32 row strides of Lt, of the 32 x 32 blocks and of the 16 x 16 ones: the operands of the small products are read without
 // bank conflicts
@@ -507,6 +510,9 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 // the state's rows in step 3), 4 (a lane quadrant per warp) brings V's columns to their lanes, 5 takes y from them to memory, and in
 // 6 one warp issues the MMAs and one loads.  The two halves run staggered: the second one's products overlap the first one's
 // conversions.
+// Bound by the steps' latency: 2.2 us per chunk, of which the products 1 to 3 are 0.9 and the conversions between them the rest (143 us for
+// the 64 chunks of B4 H16 T4096, whatever the heads' number up to one per SM; with 48 prompts of 128 to 8192 tokens and 16 heads, where
+// all SMs have work, 0.19 of HBM's rate).  Code has to stay small here: fully unrolled it waited for instructions (5 us per chunk).
 constexpr int kOwners = 16, kHelpers = 4, kBringer = 16, kTaker = 20, kIssuer = 24, kLoader = 25;
 constexpr int kMThreads = 896;
 constexpr int kGateRing = 4;
