@@ -84,8 +84,8 @@ gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, 
 // diagonal blocks of 16 by forward substitution, two in a warp, and the blocks below them, 16 and then 32 wide, as
 // X_10 = -X_11 (L_10 X_00) in warp-wide TF32 products of numbers in two parts.  (As FP32 sums with 2 x 2 and 4 x 2 numbers per thread
 // these products took 60 % of the kernel's 4000 shared-memory wavefronts per chunk, which bound it.)
-// Now 2200 instructions per warp and chunk: 60 us for 4096 chunks (B4 H16 T4096, 128 wide; 76 before), issue slots 55 % and shared
-// memory 56 % busy, the rest being the solve's barriers at 24 warps per SM.  For the gradients 78 us, half of HBM's rate.
+// Now 2100 instructions per warp and chunk: 55 us for 4096 chunks (B4 H16 T4096, 128 wide; 76 before), issue slots and shared
+// memory 55 % busy, the rest being the solve's barriers at 24 warps per SM.  For the gradients 75 us, half of HBM's rate.
 constexpr int kPThreads = 128;
 // FP32 row strides of Lt, of the 32 x 32 blocks and of the 16 x 16 ones: the operands of the small products are read without
 // bank conflicts
@@ -116,20 +116,20 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// x as two TF32 numbers, 11 bits of it and the next 11
+// x as two TF32 numbers, 11 bits of it and the next 11, cut off: less than 2^-20 of it is lost (X goes on as two BF16 parts, 2^-17)
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo)
 {
     hi = __float_as_uint(x) & 0xffffe000u;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
 }
 
-// A warp: c += A B, A 16 x 8 K8 (element (row, k) = a(row, k)), B 8 K8 x 8 N, in FP32 but for the product of the low parts (2^-22
+// A warp: c += A B, A 16 x 8 K8 (element (row, k) = a(row, k)), B 8 K8 x 8 N, in FP32 but for the product of the low parts (2^-20
 // of the terms).  c[n][0..3]: rows lane / 4 (+ 8), columns 8 n + 2 (lane % 4) (+ 1) as (row, col), (row, col + 1), (row + 8, ..)
 template <int K8, int N, class A, class B>
 __device__ __forceinline__ void small_product(float (&c)[N][4], int lane, A a, B b)
 {
     const int g = lane >> 2, t = lane & 3;
-#pragma unroll
+#pragma unroll 1               // (unrolled, the kernel waits for instructions)
     for (int k = 0; k < 8 * K8; k += 8) {
         uint32_t ah[4], al[4];
 #pragma unroll
