@@ -332,6 +332,40 @@ def test_workspace_and_poison(la, dtype):
         la.gated_delta_backward(q, k, v, dy, alpha, beta, S0=S0, dS_T=dS_T, workspace=ws[:-1])
 
 
+@DTYPES
+def test_offsets_past_32_bits(la, dtype):
+    """A sequence of more than 2^31 elements: its end is that of its last tokens run from the state before them, and the
+    same packed."""
+    T, r, dv = (1 << 24) + 4096 + 37, 64 if dtype == torch.bfloat16 else 1, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k = (torch.randn((1, 1, T, r), generator=g, device="cuda", dtype=dtype).mul_(r ** -0.5) for _ in range(2))
+    v = torch.randn((1, 1, T, dv), generator=g, device="cuda", dtype=dtype)
+    alpha, beta = (torch.rand((1, 1, T), generator=g, device="cuda").mul_(0.4).add_(c) for c in (0.6, 0.1))
+    y, S = la.gated_delta_prefill(q, k, v, alpha, beta)
+    cut = (T - 1000) // 64 * 64
+    part = lambda s: [x[:, :, s].contiguous() for x in (q, k, v, alpha, beta)]  # noqa: E731
+    _, before = la.gated_delta_prefill(*part(slice(0, cut)))
+    y2, S2 = la.gated_delta_prefill(*part(slice(cut, T)), S0=before)
+    assert torch.equal(S, S2) and torch.equal(y[:, :, cut:], y2) and torch.isfinite(S).all()
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    y3, S3 = la.gated_delta_prefill_varlen(*(x.reshape(T, 1, -1) for x in (q, k, v)), cu, alpha.reshape(T, 1), beta.reshape(T, 1))
+    assert torch.equal(S, S3) and torch.equal(y.reshape(-1), y3.reshape(-1))
+    assert la.last_device_status() == 0
+
+
+def test_decode_offsets_past_32_bits(la):
+    B, H, r, dv = 8200, 16, 128, 128
+    g = torch.Generator(device="cuda").manual_seed(4)
+    S = torch.randn((B, H, r, dv), generator=g, device="cuda")
+    q, k, v = (torch.randn((B, H, 1, 128), generator=g, device="cuda", dtype=torch.bfloat16).mul_(0.1) for _ in range(3))
+    alpha, beta = (torch.rand((B, H), generator=g, device="cuda") for _ in range(2))
+    ends = [0, 1, B // 2, B - 2, B - 1]
+    few = [x[ends].contiguous() for x in (q, k, v, S, alpha, beta)]
+    y = la.gated_delta_decode_step(q, k, v, S, alpha, beta)
+    y_few = la.gated_delta_decode_step(*few)
+    assert torch.equal(S[ends], few[3]) and torch.equal(y[ends], y_few)
+
+
 def test_streams_and_graphs(la):
     """Calls on a side stream, captured into a graph and replayed on new inputs, give the eager calls' bits."""
     size = (1, 4, 2, 150, 128, 128)

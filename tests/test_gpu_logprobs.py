@@ -180,6 +180,24 @@ def test_gradient(la, N, V, entropy, dtype):
     check_grad(wide[:, :V], x, tokens, dlp, dent)
 
 
+@DTYPES
+def test_rows_past_32_bits(la, dtype):
+    """Rows whose elements lie more than 2^31 behind the first."""
+    V, far = 1000, (1 << 31) + 24
+    x, tokens = make(3, V, dtype, 31)
+    tokens[1] = 7
+    buf = torch.empty(2 * far + V, dtype=dtype, device="cuda")
+    rows = buf.as_strided((3, V), (far, 1))
+    rows.copy_(x)
+    want, got = la.token_logprobs(x, tokens, top=3), la.token_logprobs(rows, tokens, top=3)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    dlp = torch.ones(3, device="cuda")
+    d = la.token_logprobs_backward(x, tokens, want[2], None, dlp)
+    la.token_logprobs_backward(rows, tokens, want[2], None, dlp, dlogits=rows)
+    assert torch.equal(rows, d)
+
+
 def test_gradient_differences(la):
     x, tokens = make(6, 50, torch.float32, 4, sd=1.0)
     g = torch.Generator().manual_seed(2)
