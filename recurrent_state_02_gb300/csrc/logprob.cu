@@ -170,11 +170,12 @@ __device__ __forceinline__ uint4 load_granule(const void *row, int blk, int lane
 // s of 2^a and the sum w of a 2^a, a = (x - m) log2 e, from which lse and the entropy follow.  The alternatives come from
 // maxima that the pass forms anyway: a lane's maximum of four blocks of 32 granules joins its warp's, an entry covers one such
 // group or 2^shift of them, and the entries are gathered to 64 group maxima per CTA, whose top-th largest bounds the top-th
-// best from below.  Only blocks that reach it are read again (about as many as there are alternatives, out of L2), and what
-// reaches it is ranked.
-// Bound by exponentials and issue slots beside HBM: N = 2048, V = 131072, top 8, BF16 98 us (5.5 TB/s; 82 without alternatives,
-// 6.5 TB/s); 5 CTAs per SM hold 48 registers (one instance spills 52 bytes; 6 CTAs spill more and take 100 us).  A row's end costs its CTA
-// about 5 us with alternatives, which short rows feel: N = 8192, V = 32000, top 8 142 us, without 82.
+// best from below.  Only the groups that reach it are read again, by all warps alike (about as many as there are alternatives, out of
+// L2), and what reaches it is ranked by counting what is better.
+// Bound by exponentials and issue slots beside HBM: N = 2048, V = 131072, top 8, BF16 94 us (5.7 TB/s; 82 without alternatives,
+// 6.5 TB/s); 5 CTAs per SM hold 48 registers (one instance spills 12 bytes; 6 CTAs spill more and are slower).  A row's end costs its CTA
+// about 4 us with alternatives, which short rows feel: N = 8192, V = 32000, top 8 133 us, without 83.  (Each warp reading its own
+// groups again and one warp picking the best one by one: 98 and 143.)
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kEntries = 64;       // maxima per warp: an entry covers 2^shift of its groups of 4 blocks
 constexpr int kGroups = 64;        // of a CTA's entries: 8 per warp
@@ -185,10 +186,11 @@ struct ScoreSmem {
     uint32_t group[kGroups];
     unsigned long long cand[kCand];
     unsigned long long best[kMaxTop];              // this CTA's
+    uint16_t again[kWarps * kEntries];             // the entries that reach the bound: warp, entry
     float m[kWarps], s[kWarps], w[kWarps];
     float cm, cs, cw;                              // the CTA's
     uint32_t thr;                                  // what an alternative reaches at least
-    int count;
+    int count, entries;
 };
 
 // Merges (m, s, w) of two parts.
@@ -235,7 +237,8 @@ token_logprobs_kernel(const LogprobArgs args)
     while (((blocks + U * nw - 1) / (U * nw) - 1) >> shift >= kEntries) ++shift;
     if (top) {
         sm.entry[warp][lane] = sm.entry[warp][lane + 32] = 0;
-        if (tid == 0) sm.count = 0;
+        if (tid == 0) sm.count = sm.entries = 0;
+        if (tid < kMaxTop) sm.best[tid] = 0;
         __syncwarp();
     }
     float m = kFloor, s = 0.f, w = 0.f;
@@ -335,40 +338,42 @@ token_logprobs_kernel(const LogprobArgs args)
         // the top-th largest group maximum: four lanes rank a group, a warp its own eight
         const int g = warp * 8 + (lane >> 2);
         const uint32_t mine = sm.group[g];
-        int rank = 0;
+        int above = 0;
 #pragma unroll
         for (int i = 0; i < kGroups / 4; ++i) {
             const int o = i * 4 + (lane & 3);
             const uint32_t v = sm.group[o];
-            rank += v > mine || (v == mine && o < g);
+            above += v > mine || (v == mine && o < g);
         }
-        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-        if (rank == top - 1) sm.thr = max(1u, mine);
+        above += __shfl_xor_sync(0xffffffffu, above, 1);
+        above += __shfl_xor_sync(0xffffffffu, above, 2);
+        if (above == top - 1) sm.thr = max(1u, mine);
         __syncthreads();
         const uint32_t thr = sm.thr;
-        unsigned long long reach = __ballot_sync(0xffffffffu, sm.entry[warp][lane] >= thr) |
-                                   (unsigned long long)__ballot_sync(0xffffffffu, sm.entry[warp][lane + 32] >= thr) << 32;
-        for (; reach; reach &= reach - 1) {
-            const int e = __ffsll(reach) - 1;
-            for (int j = (e << shift) * U, blk = gw + j * nw; j < ((e + 1) << shift) * U && blk < blocks; j += U, blk += U * nw) {
-                uint4 raw[U];
+        // the entries that reach it, as a list: their blocks are read again by all warps alike
+        for (int e = lane; e < kEntries; e += 32)
+            if (sm.entry[warp][e] >= thr) sm.again[atomicAdd(&sm.entries, 1)] = (uint16_t)(warp * kEntries + e);
+        __syncthreads();
+        const int per = U << shift, total = sm.entries * per;        // (blocks behind the row are -infinity)
+        for (int i0 = U * warp; i0 < total; i0 += U * kWarps) {
+            // (U divides what an entry covers)
+            const int from = sm.again[i0 / per], b0 = (int)rank * kWarps + from / kEntries + ((from % kEntries) * per + i0 % per) * nw;
+            uint4 raw[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) raw[u] = load_granule<BF16, ALIGNED>(row, blk + u * nw, lane, V);
+            for (int u = 0; u < U; ++u) raw[u] = load_granule<BF16, ALIGNED>(row, b0 + u * nw, lane, V);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float mx = granule_max<BF16>(raw[u]);
-                    if (!(mx > -INFINITY && order_f32(mx) >= thr)) continue;
-                    float x[GE];
-                    widen<BF16>(raw[u], x);
+            for (int u = 0; u < U; ++u) {
+                const float mx = granule_max<BF16>(raw[u]);
+                if (!(mx > -INFINITY && order_f32(mx) >= thr)) continue;
+                float x[GE];
+                widen<BF16>(raw[u], x);
 #pragma unroll
-                    for (int i = 0; i < GE; ++i)
-                        if (x[i] > -INFINITY && order_f32(x[i]) >= thr) {
-                            const int at = atomicAdd(&sm.count, 1);
-                            if (at < kCand)
-                                sm.cand[at] = make_key(x[i], (ALIGNED ? ((blk + u * nw) * 32 + lane) * GE : (blk + u * nw) * 32 * GE + lane) + i * ES);
-                        }
-                }
+                for (int i = 0; i < GE; ++i)
+                    if (x[i] > -INFINITY && order_f32(x[i]) >= thr) {
+                        const int at = atomicAdd(&sm.count, 1);
+                        if (at < kCand)
+                            sm.cand[at] = make_key(x[i], (ALIGNED ? ((b0 + u * nw) * 32 + lane) * GE : (b0 + u * nw) * 32 * GE + lane) + i * ES);
+                    }
             }
         }
         __syncthreads();
@@ -403,31 +408,13 @@ token_logprobs_kernel(const LogprobArgs args)
             if (lane < top) sm.cand[warp * top + lane] = mine;
             __syncthreads();
         }
-        if (warp == 0) {
-            const int have = count > kCand ? kWarps * top : count;
-            if (have <= 64) {
-                // (the usual case: a key or two per lane)
-                unsigned long long k0 = lane < have ? sm.cand[lane] : 0, k1 = lane + 32 < have ? sm.cand[lane + 32] : 0;
-#pragma unroll 1
-                for (int r = 0; r < top; ++r) {
-                    const unsigned long long best = warp_max(k0 > k1 ? k0 : k1);
-                    if (lane == r) sm.best[r] = best;
-                    if (k0 == best) k0 = 0;
-                    if (k1 == best) k1 = 0;
-                }
-            } else {
-                unsigned long long last = ~0ull;
-#pragma unroll 1
-                for (int r = 0; r < top; ++r) {
-                    unsigned long long best = 0;
-                    for (int i = lane; i < have; i += 32) {
-                        const unsigned long long k = sm.cand[i];
-                        if (k < last && k > best) best = k;
-                    }
-                    last = warp_max(best);
-                    if (lane == 0) sm.best[r] = last;
-                }
-            }
+        // a candidate's place is how many are better
+        const int have = count > kCand ? kWarps * top : count;
+        for (int i = tid; i < have; i += kThreads) {
+            const unsigned long long mine = sm.cand[i];
+            int place = 0;
+            for (int j = 0; j < have && place < top; ++j) place += sm.cand[j] > mine;
+            if (mine && place < top) sm.best[place] = mine;
         }
     }
     if (cs > 1) cluster_sync_all();
