@@ -1153,7 +1153,7 @@ la_status gdelta_forward(const void *q, const void *k, const void *v, la_dtype d
             a.order = a.slot_base + B + 1;
             a.ws += la::gdelta_tc_plan_bytes(B);
         }
-        return from_cuda(la::launch_gdelta_tc(m, a, st));
+        return from_cuda(la::launch_gdelta_tc(m, a, sm_count(), st));
     }
     la::GdeltaForward f;
     f.q = q, f.k = k, f.v = v, f.y = y;

@@ -170,7 +170,7 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (packed) wait_for_last();        // the plan
     // this CTA's head, sequence and chunk
     const int h = blockIdx.x % s.H, hk = h / (s.H / s.Hk);
-    const int slot = blockIdx.x / s.H;
+    int slot = blockIdx.x / s.H;
     int b, c;
     Span sp;
     if (packed) {
@@ -197,8 +197,9 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         c = slot - (int)sp.slot;
         if (!sp.valid || c < 0 || c * kC >= sp.T) return;
     } else {
-        const int nch = (s.T + kC - 1) / kC;
-        b = slot / nch, c = slot % nch;
+        const int nch = (s.T + kC - 1) / kC, part = args.chunks ? args.chunks : nch;
+        b = slot / part, c = args.first + slot % part;
+        slot = b * nch + c;
         sp = span_of(args, b);
     }
     const int t0 = c * kC, nt = min(kC, sp.T - t0);
@@ -503,6 +504,8 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tc_fence_after();
         tmem_dealloc(tmem, 64);
     }
+    // (a later part runs beside the chain before it; it has ended when both have)
+    if (args.first > 0 && blockIdx.x == gridDim.x - 1) wait_for_last();
 }
 
 // ------------------------------------------------------------------ the chain
@@ -577,7 +580,8 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     }
     const Span sp = span_of(args, b);
     if (!sp.valid) return;
-    const int T = sp.T, nch = (T + kC - 1) / kC;
+    const int c0 = args.first, T = sp.T - c0 * kC;      // tokens from this launch's first chunk on
+    const int nch = args.chunks ? min(args.chunks, (T + kC - 1) / kC) : (T + kC - 1) / kC;
     const int ncols = min(128, dv - 128 * tile);        // of this CTA: 128 or 64
     const size_t bh = (size_t)b * H + h;
     const bool tail = packed && nch > 0 && T < nch * kC;
@@ -595,17 +599,18 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    let_next_start();
     wait_for_last();
 
     if (warp >= kIssuer) {
         regs_dec<kRegsRest>();
         if (warp == kLoader && elect_one()) {
             const int hk = h / (H / args.s.Hk);
-            const uint8_t *ws = args.ws + (sp.slot * H + h) * kWsChunk;
+            const uint8_t *ws = args.ws + ((sp.slot + c0) * H + h) * kWsChunk;
             const size_t ws_step = (size_t)H * kWsChunk;      // from one chunk to the next
             auto tok = [&](uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int n, int heads, int head) {
                 if (packed) tma_load(dst, map, bar, x, head, (int)sp.tok0 + n * kC);
-                else tma_load(dst, map, bar, x, n * kC, b * heads + head);
+                else tma_load(dst, map, bar, x, (c0 + n) * kC, b * heads + head);
             };
             int n1 = 0, n2 = 0;                    // chunks whose K, V, X / Q, A loads were started
             bool ok = true;
@@ -738,7 +743,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         const size_t y_step = (packed ? (size_t)H : 1) * dv;
         // this lane's column and token of a block of 8 when rows go out
         const int out_col = 32 * q4 + 8 * (lane & 3), out_tok = lane >> 2;
-        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * H + h) * dv : bh * args.s.T * dv) + 128 * tile + out_col + (size_t)out_tok * y_step;
+        uint16_t *const y0 = args.y + (packed ? (sp.tok0 * H + h) * dv : (bh * args.s.T + (size_t)c0 * kC) * dv) + 128 * tile + out_col + (size_t)out_tok * y_step;
         const float2 scale = make_float2(args.scale, args.scale);
 #pragma unroll 1
         for (int n = 0; n < nch; ++n) {
@@ -834,7 +839,7 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 #pragma unroll
         for (int i = 0; i < KQ / 2; ++i) {
             S[i] = make_float2(0.f, 0.f);
-            if (args.S0 && live) S[i] = make_float2(args.S0[s_at + (size_t)(2 * i) * dv], args.S0[s_at + (size_t)(2 * i + 1) * dv]);
+            if (args.S0 && live) S[i] = make_float2(__ldcg(args.S0 + s_at + (size_t)(2 * i) * dv), __ldcg(args.S0 + s_at + (size_t)(2 * i + 1) * dv));
         }
         // rows 16 x .. of this quarter as left operands
         auto put_s = [&](int x, const float2 *v) {
@@ -967,11 +972,11 @@ static cudaError_t launch_prep(const CUtensorMap &q, const CUtensorMap &k, const
     static OncePerDevice once;
     const cudaError_t e = set_smem_once(gdelta_prep_kernel<KD, BACK>, kPSmemBytes, once);
     if (e != cudaSuccess) return e;
-    const long long n = gdelta_tc_slots(a.s.B, a.s.T, a.s.cu_seqlens != nullptr) * a.s.H;
+    const long long n = (a.chunks ? (long long)a.s.B * a.chunks : gdelta_tc_slots(a.s.B, a.s.T, a.s.cu_seqlens != nullptr)) * a.s.H;
     if (n > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (n == 0) return cudaSuccess;
-    // (packed: after the plan; else nothing to start ahead of)
-    if (a.s.cu_seqlens) return launch_after(gdelta_prep_kernel<KD, BACK>, (unsigned)n, kPThreads, kPSmemBytes, stream, q, k, a);
+    // (packed: after the plan; a later part: beside the chain before it; else nothing to start ahead of)
+    if (a.s.cu_seqlens || a.first) return launch_after(gdelta_prep_kernel<KD, BACK>, (unsigned)n, kPThreads, kPSmemBytes, stream, q, k, a);
     gdelta_prep_kernel<KD, BACK><<<(unsigned)n, kPThreads, kPSmemBytes, stream>>>(q, k, a);
     return cudaGetLastError();
 }
@@ -982,7 +987,7 @@ cudaError_t launch_gdelta_prep_backward(const CUtensorMap &q, const CUtensorMap 
 }
 
 template <int KD>
-static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream)
+static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, int sms, cudaStream_t stream)
 {
     static OncePerDevice once_m;
     cudaError_t e = set_smem_once(gdelta_chain_kernel<KD>, kMSmemBytes<KD>, once_m);
@@ -994,13 +999,26 @@ static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaS
         gdelta_plan_kernel<<<1, kPlanThreads, 0, stream>>>(s.cu_seqlens, s.B, s.T, a.slot_base, a.order, s.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if ((e = launch_prep<KD, false>(m.q, m.k, a, stream)) != cudaSuccess) return e;
-    return launch_after(gdelta_chain_kernel<KD>, (unsigned)nmain, kMThreads, kMSmemBytes<KD>, stream, m.q, m.k, m.v, a);
+    // Few heads leave SMs without a chain: there the sequences go in two parts, and the second one's A and X are formed beside the
+    // chain of the first.  The first part is a little less than what that chain gives time for (3 of 10 chunks: B4 H16 T4096
+    // 200 -> 188 us, T16384 749 -> 703, B1 H16 T16384 611 -> 585; 45 of 100 194, 20 194, three parts 191).  Another launch of the chain costs
+    // about 5 us, which fewer than 8 chunks per SM do not repay.
+    GdeltaTcArgs part = a;
+    const int nch = (s.T + kC - 1) / kC;
+    const bool apart = !s.cu_seqlens && 2 * nmain <= sms && (long long)s.B * s.H * nch >= 8LL * sms && nch >= 16;
+    if (apart) part.chunks = (int)(nch * 3LL / 10);
+    for (;;) {
+        if ((e = launch_prep<KD, false>(m.q, m.k, part, stream)) != cudaSuccess) return e;
+        e = launch_after(gdelta_chain_kernel<KD>, (unsigned)nmain, kMThreads, kMSmemBytes<KD>, stream, m.q, m.k, m.v, part);
+        if (e != cudaSuccess || !apart || part.first) return e;
+        part.first = part.chunks, part.chunks = nch - part.first;
+        part.S0 = a.S_out;
+    }
 }
 
-cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream)
+cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, int sms, cudaStream_t stream)
 {
-    return a.s.r == 64 ? launch_as<64>(m, a, stream) : launch_as<128>(m, a, stream);
+    return a.s.r == 64 ? launch_as<64>(m, a, sms, stream) : launch_as<128>(m, a, sms, stream);
 }
 
 }  // namespace la

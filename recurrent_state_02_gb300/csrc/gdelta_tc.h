@@ -18,6 +18,7 @@ struct GdeltaTcArgs {
     uint16_t *y = nullptr;
     float scale = 1.f;
     uint8_t *ws = nullptr;          // A, X and the gates of every chunk and head (256-byte aligned)
+    int first = 0, chunks = 0;      // dense: this launch's chunks of every sequence (0: all of them)
     int *slot_base = nullptr;       // packed: the plan's tables, B + 1 and B entries
     int *order = nullptr;
 };
@@ -27,7 +28,7 @@ long long gdelta_tc_slots(int B, int T, bool packed);
 size_t gdelta_tc_plan_bytes(int B);
 size_t gdelta_tc_workspace_bytes(int B, int H, int T, bool packed);
 
-cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, cudaStream_t stream);
+cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, int sms, cudaStream_t stream);
 
 // The gradients (gdelta_bwd.cu): [B,H,T,d], r 64 or 128, dv 64 or 128, token arrays 16-byte aligned, the workspace 256-byte.
 struct GdeltaTcBackMaps {

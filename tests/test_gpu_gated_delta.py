@@ -332,6 +332,27 @@ def test_workspace_and_poison(la, dtype):
         la.gated_delta_backward(q, k, v, dy, alpha, beta, S0=S0, dS_T=dS_T, workspace=ws[:-1])
 
 
+def test_long_sequences_of_few_heads(la):
+    """They go in two parts; in place, from a carried state, with a last chunk that is not full, and as a graph."""
+    size = (2, 4, 2, 9800, 64, 64)
+    q, k, v, _, alpha, beta, S0, _ = make(*size, torch.bfloat16, True, 33)
+    S = S0.clone()
+    y, S = la.gated_delta_prefill(q, k, v, alpha, beta, S0=S, S_out=S)
+    apart, S2 = la.gated_delta_prefill(q, k, v, alpha, beta, S0=S0)
+    assert la.last_device_status() == 0 and torch.equal(S, S2) and torch.equal(y, apart)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = la.gated_delta_prefill(q, k, v, alpha, beta, S0=S0)
+    for _ in range(3):
+        for x in held:
+            x.zero_()
+        graph.replay()
+        assert torch.equal(held[0], y) and torch.equal(held[1], S)
+    ref_y, ref_S, _, _ = R.prefill(q, k, v, alpha, beta, S0, 1.0)
+    R.check(S, ref_S, torch.bfloat16, "S", size[3])
+    R.check(y, ref_y, torch.bfloat16, "y", size[3])
+
+
 @DTYPES
 def test_offsets_past_32_bits(la, dtype):
     """A sequence of more than 2^31 elements: its end is that of its last tokens run from the state before them, and the
