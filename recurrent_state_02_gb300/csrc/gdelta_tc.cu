@@ -78,6 +78,49 @@ gdelta_plan_kernel(const int *cu, int B, int total, int *slot_base, int *order, 
     if (tid == 0) slot_base[B] = min(carry, total / kC + B);
 }
 
+// Up to 32 sequences need no plan kernel (16 short ones as a graph: 27 us with it, 23 without): every warp finds its own, sequence b in lane b.
+// Returns the sequence that holds chunk `want` (CHUNK), or the one of rank `want`, longest first; -1 is none.
+constexpr int kSelfPlan = 32;
+template <bool CHUNK>
+__device__ __forceinline__ int self_plan(const GdeltaTcArgs &a, int want, Span &sp)
+{
+    const int lane = threadIdx.x & 31, B = a.s.B;
+    int lo = 0, T = 0, n = -1;
+    if (lane < B) {
+        lo = a.s.cu_seqlens[lane];
+        const int hi = a.s.cu_seqlens[lane + 1];
+        if (lo >= 0 && hi >= lo && hi <= a.s.T) T = hi - lo, n = (T + kC - 1) / kC;
+    }
+    int behind = max(n, 0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, behind, o);
+        if (lane >= o) behind += x;
+    }
+    const int base = behind - max(n, 0);
+    const bool valid = n >= 0 && behind <= a.s.T / kC + B;
+    if (lane < B && !valid && !CHUNK && blockIdx.x == 0) atomicExch(a.s.status, kStatusShape);
+    bool mine;
+    if (CHUNK) {
+        mine = valid && base <= want && want < behind;
+    } else {
+        int rank = 0;
+        for (int i = 0; i < B; ++i) {
+            const int other = __shfl_sync(0xffffffffu, n, i);
+            rank += other > n || (other == n && i < lane);
+        }
+        mine = lane < B && rank == want;
+    }
+    const uint32_t v = __ballot_sync(0xffffffffu, mine);
+    if (!v) return -1;
+    const int b = __ffs(v) - 1;
+    sp.valid = __shfl_sync(0xffffffffu, (int)valid, b);
+    sp.tok0 = __shfl_sync(0xffffffffu, lo, b);
+    sp.T = __shfl_sync(0xffffffffu, T, b);
+    sp.slot = __shfl_sync(0xffffffffu, base, b);
+    return b;
+}
+
 // ------------------------------------------------------- A, X and the gates
 // Four warps per chunk and head.  [G; P] = [K; Q] K^T on the tensor cores; a row of L or A per thread, its decays as running products
 // of the gates from the diagonal to the left (no logarithms, and gates of 0 need no care); then X = (I + L)^{-1} in FP32: the four
@@ -167,13 +210,18 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool packed = s.cu_seqlens != nullptr;
     let_next_start();
-    if (packed) wait_for_last();        // the plan
+    const bool planned = args.slot_base != nullptr;
+    if (planned) wait_for_last();
     // this CTA's head, sequence and chunk
     const int h = blockIdx.x % s.H, hk = h / (s.H / s.Hk);
     int slot = blockIdx.x / s.H;
     int b, c;
     Span sp;
-    if (packed) {
+    if (packed && !planned) {
+        b = self_plan<true>(args, slot, sp);
+        if (b < 0) return;
+        c = slot - (int)sp.slot;
+    } else if (packed) {
         if (slot >= args.slot_base[s.B]) return;
         // the last sequence that starts at or before the slot, 32 probes at a time (-1: skipped ones are passed over)
         int lo = 0, n = s.B;
@@ -574,11 +622,16 @@ gdelta_chain_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     const int tiles = (dv + 127) / 128;
     const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % H;
     int b = blockIdx.x / (tiles * H);
-    if (packed) {
-        wait_for_last();
-        b = args.order[b];
+    Span sp;
+    if (packed && !args.slot_base) {
+        b = self_plan<false>(args, b, sp);
+    } else {
+        if (packed) {
+            wait_for_last();
+            b = args.order[b];
+        }
+        sp = span_of(args, b);
     }
-    const Span sp = span_of(args, b);
     if (!sp.valid) return;
     const int c0 = args.first, T = sp.T - c0 * kC;      // tokens from this launch's first chunk on
     const int nch = args.chunks ? min(args.chunks, (T + kC - 1) / kC) : (T + kC - 1) / kC;
@@ -975,8 +1028,8 @@ static cudaError_t launch_prep(const CUtensorMap &q, const CUtensorMap &k, const
     const long long n = (a.chunks ? (long long)a.s.B * a.chunks : gdelta_tc_slots(a.s.B, a.s.T, a.s.cu_seqlens != nullptr)) * a.s.H;
     if (n > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (n == 0) return cudaSuccess;
-    // (packed: after the plan; a later part: beside the chain before it; else nothing to start ahead of)
-    if (a.s.cu_seqlens || a.first) return launch_after(gdelta_prep_kernel<KD, BACK>, (unsigned)n, kPThreads, kPSmemBytes, stream, q, k, a);
+    // (after the plan; a later part: beside the chain before it; else nothing to start ahead of)
+    if (a.slot_base || a.first) return launch_after(gdelta_prep_kernel<KD, BACK>, (unsigned)n, kPThreads, kPSmemBytes, stream, q, k, a);
     gdelta_prep_kernel<KD, BACK><<<(unsigned)n, kPThreads, kPSmemBytes, stream>>>(q, k, a);
     return cudaGetLastError();
 }
@@ -995,7 +1048,7 @@ static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, int s
     const GdeltaShape &s = a.s;
     const long long nmain = (long long)s.B * s.H * ((s.dv + 127) / 128);
     if (nmain > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (s.cu_seqlens) {
+    if (a.slot_base) {
         gdelta_plan_kernel<<<1, kPlanThreads, 0, stream>>>(s.cu_seqlens, s.B, s.T, a.slot_base, a.order, s.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -1018,7 +1071,9 @@ static cudaError_t launch_as(const GdeltaTcMaps &m, const GdeltaTcArgs &a, int s
 
 cudaError_t launch_gdelta_tc(const GdeltaTcMaps &m, const GdeltaTcArgs &a, int sms, cudaStream_t stream)
 {
-    return a.s.r == 64 ? launch_as<64>(m, a, sms, stream) : launch_as<128>(m, a, sms, stream);
+    GdeltaTcArgs self = a;
+    if (a.s.B <= kSelfPlan) self.slot_base = self.order = nullptr;
+    return a.s.r == 64 ? launch_as<64>(m, self, sms, stream) : launch_as<128>(m, self, sms, stream);
 }
 
 }  // namespace la

@@ -19,7 +19,7 @@ struct GdeltaTcArgs {
     float scale = 1.f;
     uint8_t *ws = nullptr;          // A, X and the gates of every chunk and head (256-byte aligned)
     int first = 0, chunks = 0;      // dense: this launch's chunks of every sequence (0: all of them)
-    int *slot_base = nullptr;       // packed: the plan's tables, B + 1 and B entries
+    int *slot_base = nullptr;       // packed: the plan's tables, B + 1 and B entries, or nullptr (up to 32 sequences: no plan)
     int *order = nullptr;
 };
 
