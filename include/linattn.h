@@ -503,8 +503,10 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  * Kernels:
  *   prompts in chunks of 64 tokens on the tensor cores, the state in FP32, for BF16 with r 64 or 128, dv a multiple of 64
  *   (la_gated_delta_backward: 64 or 128), every token array on a 16-byte boundary and T > 16 (packed sequences: any length);
- *   the token recurrence in FP32 on CUDA cores for everything else (for one token of la_gated_delta_decode_step a kernel
- *   of its own, bound by the state's traffic, when dv is a multiple of 4 and S 16-byte aligned).
+ *   the token recurrence in FP32 on CUDA cores for everything else.  Dense prompts whose heads leave SMs idle go in segments there
+ *   (the workspace is then not 0 bytes for FP32 either, and depends on the current device);
+ *   for one token of la_gated_delta_decode_step a kernel of its own, bound by the state's traffic, when dv is a multiple of 4
+ *   and S 16-byte aligned.
  * In the chunked kernels what is derived from the inputs enters the tensor cores as two BF16 parts (16 bits of it) where
  * it reaches an FP32 result, and as one where it reaches a BF16 one only: relative 2-norms of the errors about 3e-6 and 3e-3.
  * The first call of each kind on a device sets kernel attributes: make it before any stream capture.

@@ -1119,7 +1119,11 @@ bool gdelta_tc_sizes(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv,
 
 size_t gdelta_workspace(la_dtype dtype, int B, int H, int Hk, int T, int r, int dv, bool packed)
 {
-    return gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, packed) ? la::gdelta_tc_workspace_bytes(B, H, T, packed) : 0;
+    if (check_gdelta_sizes(dtype, B, H, Hk, T, r, dv, 1.f, packed) != LA_OK) return 0;
+    // (dense: enough for the recurrence's segments too, which misaligned arrays take)
+    const size_t rec = packed ? 0 : sizeof(float) * la::gdelta_rec_floats(B, H, T, r, dv, sm_count());
+    const size_t tc = gdelta_tc_sizes(dtype, B, H, Hk, T, r, dv, packed) ? la::gdelta_tc_workspace_bytes(B, H, T, packed) : 0;
+    return rec > tc ? rec : tc;
 }
 
 la_status gdelta_forward(const void *q, const void *k, const void *v, la_dtype dtype, const float *alpha, const float *beta,
@@ -1159,6 +1163,8 @@ la_status gdelta_forward(const void *q, const void *k, const void *v, la_dtype d
     f.q = q, f.k = k, f.v = v, f.y = y;
     f.S0 = S0, f.S_out = S_out;
     f.scale = scale;
+    if (!packed)
+        return from_cuda(la::launch_gdelta_rec_segments(s, f, dtype == LA_DTYPE_BF16, sm_count(), static_cast<float *>(workspace), st));
     return from_cuda(la::launch_gdelta_rec(s, f, dtype == LA_DTYPE_BF16, st));
 }
 

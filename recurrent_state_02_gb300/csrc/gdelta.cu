@@ -58,6 +58,12 @@ struct RecArgs {
     const float *S_init;         // [B,H,r,dv] or nullptr
     float *S_fin;                // [B,H,r,dv] or nullptr
     float scale;
+    // kFwd in segments of seg_len tokens (nseg > 1): the first pass leaves what each segment adds to the state, N, and what it makes of
+    // the one before it, M (S -> M S + N); the second one starts from `starts`
+    int nseg = 1, seg_len = 0;
+    bool sums = false;
+    float *N = nullptr, *M = nullptr;        // [B*H][nseg][r][dv], [B*H][nseg][r][r]
+    const float *starts = nullptr;           // [B*H][nseg][r][dv]
 };
 
 constexpr int kRecTok = 16;              // tokens per staged block
@@ -83,7 +89,7 @@ constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2 + 6);
 // warps convert a block of 16 tokens to FP32 while the computing ones work on the one before, and store its
 // results.  4 r dv FMAs per token and head bound it (FP32 B16 H16 T1001, 128 x 128: 1.0 ms, 33 TFLOP/s of about 75, beside the products
 // of the tokens with one another); few heads are bound by a group's latency, 0.4 us at 64 rows (B2 H4 T1001, 64 x 96: 104 us; 240
-// token by token, the sums of one waiting for the ones before, and the next block's loads for one another).
+// token by token, the sums of one waiting for the ones before, and the next block's loads for one another; 90 in segments).
 template <int MODE, bool BF16, int RPL>
 __global__ void __launch_bounds__(kRecThreads)
 gdelta_rec_kernel(const RecArgs a)
@@ -100,12 +106,23 @@ gdelta_rec_kernel(const RecArgs a)
     constexpr int kStage = kRecStageFloats<RPL>;
 
     const int tid = threadIdx.x, lane = tid & 31;
-    const int b = blockIdx.z, h = blockIdx.y, c0 = blockIdx.x * kRecCols;
+    wait_for_last();
+    let_next_start();
     const GdeltaShape &s = a.s;
-    const int rows = kT ? s.dv : s.r, cols = kT ? s.r : s.dv;
+    const bool parts = MODE == kFwd && a.nseg > 1;
+    const int b = parts ? blockIdx.z / a.nseg : blockIdx.z, seg = parts ? blockIdx.z % a.nseg : 0, h = blockIdx.y;
+    // (M's columns behind N's: the recurrence from the unit matrix, with nothing to write but its own decay)
+    const int slices = (s.dv + kRecCols - 1) / kRecCols;
+    const bool unit = parts && a.sums && blockIdx.x >= slices;
+    const int c0 = (blockIdx.x - (unit ? slices : 0)) * kRecCols;
+    const int rows = kT ? s.dv : s.r, cols = kT || unit ? s.r : s.dv;
     const int hk = h / (s.H / s.Hk);
     int T = s.T;
-    size_t tok0 = 0;                         // packed: the sequence's first token
+    size_t tok0 = 0;                         // packed: the sequence's first token; in segments: the segment's
+    if (parts) {
+        tok0 = (size_t)seg * a.seg_len;
+        T = min(a.seg_len, s.T - (int)tok0);
+    }
     const bool packed = s.cu_seqlens != nullptr;
     if (packed) {
         const int lo = s.cu_seqlens[b], hi = s.cu_seqlens[b + 1];
@@ -123,7 +140,7 @@ gdelta_rec_kernel(const RecArgs a)
         ptrdiff_t stride;
     };
     auto rows_of = [&](int heads, int hh, int d) -> Rows {
-        return packed ? Rows{(tok0 * heads + hh) * (size_t)d, (ptrdiff_t)heads * d} : Rows{((size_t)b * heads + hh) * s.T * d, d};
+        return packed ? Rows{(tok0 * heads + hh) * (size_t)d, (ptrdiff_t)heads * d} : Rows{(((size_t)b * heads + hh) * s.T + tok0) * d, d};
     };
     const bool computes = tid < kRecComp;
     const int warp = tid >> 5, g = lane >> 2, jl = (warp & 3) * 8 + 2 * (lane & 3);
@@ -170,7 +187,7 @@ gdelta_rec_kernel(const RecArgs a)
             for (int j = 0; j < kColIters; ++j) {
                 fu[j] = 0.f;
                 if (MODE == kKey) fu2[j] = 0.f;
-                if (i_col + j * (kRecComp / kRecCols) < nt && col < cols) {
+                if (i_col + j * (kRecComp / kRecCols) < nt && col < cols && !unit) {
                     fu[j] = load_elem<BF16>(kT ? a.k : MODE == kFwd ? a.v : a.dy, oc);
                     if (MODE == kKey) fu2[j] = load_elem<BF16>(a.q, oc);
                 }
@@ -292,15 +309,17 @@ gdelta_rec_kernel(const RecArgs a)
         if (nblk > 0) stage_out(nblk - 1);
     } else {
         float X[2][RPL];
+        const float *S_init = a.S_init ? a.S_init + bh * s.r * s.dv : nullptr;
+        if (parts) S_init = a.sums ? nullptr : a.starts + (bh * a.nseg + seg) * s.r * s.dv;
 #pragma unroll
         for (int m = 0; m < RPL; ++m) {
             const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = c0 + jl + c;
-                X[c][m] = 0.f;
-                if (a.S_init && row < rows && col < cols)
-                    X[c][m] = a.S_init[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)];
+                X[c][m] = unit && row == col ? 1.f : 0.f;
+                if (S_init && row < rows && col < cols)
+                    X[c][m] = S_init[(kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)];
             }
         }
         block_sync();
@@ -425,7 +444,11 @@ gdelta_rec_kernel(const RecArgs a)
             }
             block_sync();
         }
-        if (a.S_fin) {
+        float *S_fin = a.S_fin ? a.S_fin + bh * s.r * s.dv : nullptr;
+        if (parts && a.sums) S_fin = unit ? a.M + (bh * a.nseg + seg) * s.r * s.r : a.N + (bh * a.nseg + seg) * s.r * s.dv;
+        else if (parts && seg < a.nseg - 1) S_fin = nullptr;
+        const int width = unit ? s.r : s.dv;
+        if (S_fin) {
 #pragma unroll
             for (int m = 0; m < RPL; ++m) {
                 const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
@@ -433,7 +456,7 @@ gdelta_rec_kernel(const RecArgs a)
                 for (int c = 0; c < 2; ++c) {
                     const int col = c0 + jl + c;
                     if (row < rows && col < cols)
-                        a.S_fin[bh * s.r * s.dv + (kT ? (size_t)col * s.dv + row : (size_t)row * s.dv + col)] = X[c][m];
+                        S_fin[kT ? (size_t)col * s.dv + row : (size_t)row * width + col] = X[c][m];
                 }
             }
         }
@@ -448,7 +471,10 @@ cudaError_t launch_rec_as(const RecArgs &a, cudaStream_t stream)
     const cudaError_t e = set_smem_once(gdelta_rec_kernel<MODE, BF16, RPL>, bytes, once);
     if (e != cudaSuccess) return e;
     const int cols = MODE == kQue || MODE == kKey ? a.s.r : a.s.dv;
-    const dim3 grid((cols + kRecCols - 1) / kRecCols, a.s.H, a.s.B);
+    unsigned slices = (cols + kRecCols - 1) / kRecCols;
+    if (a.sums) slices += (a.s.r + kRecCols - 1) / kRecCols;
+    const dim3 grid(slices, a.s.H, a.s.B * a.nseg);
+    if (a.nseg > 1 && !a.sums) return launch_after(gdelta_rec_kernel<MODE, BF16, RPL>, grid, kRecThreads, bytes, stream, a);
     gdelta_rec_kernel<MODE, BF16, RPL><<<grid, kRecThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
@@ -460,6 +486,75 @@ cudaError_t launch_rec(const RecArgs &a, bool bf16, cudaStream_t stream)
     if (rows <= 64) return bf16 ? launch_rec_as<MODE, true, 8>(a, stream) : launch_rec_as<MODE, false, 8>(a, stream);
     if (rows <= 128) return bf16 ? launch_rec_as<MODE, true, 16>(a, stream) : launch_rec_as<MODE, false, 16>(a, stream);
     return bf16 ? launch_rec_as<MODE, true, 32>(a, stream) : launch_rec_as<MODE, false, 32>(a, stream);
+}
+
+// The states before the segments: S <- M S + N from one segment to the next.  A CTA has 32 columns of a head's state in shared memory
+// and takes M by 32 rows; a warp forms four of them, and what comes next is loaded meanwhile.
+constexpr int kJoinRows = 32;
+__global__ void __launch_bounds__(256)
+gdelta_join_kernel(GdeltaShape s, const float *__restrict__ S0, const float *N, const float *M, float *starts, int nseg)
+{
+    extern __shared__ __align__(16) float sm_join[];
+    const int r = s.r, dv = s.dv, rp = (r + 3) & ~3;        // (columns of M up to rp are 0)
+    float *St = sm_join, *Sn = St + rp * 32, *Mt = Sn + rp * 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = blockIdx.x * 32 + lane;
+    const size_t bh = blockIdx.y;
+    const bool live = col < dv;
+    wait_for_last();
+    let_next_start();
+    for (int row = warp; row < rp; row += 8) St[row * 32 + lane] = S0 && live && row < r ? S0[(bh * r + row) * dv + col] : 0.f;
+    const int tiles = (r + kJoinRows - 1) / kJoinRows, steps = tiles * (nseg - 1);
+    Mt += warp * 4 * rp;                                    // a warp's four rows are its own
+    float next[4][8], n4[4];
+    auto fetch = [&](int i) {
+        const size_t at = bh * nseg + i / tiles;
+        const int row0 = i % tiles * kJoinRows + 4 * warp;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = row0 + j;
+            const float *Mr = M + (at * r + row) * r;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) next[j][k] = row < r && lane + 32 * k < r ? Mr[lane + 32 * k] : 0.f;
+            n4[j] = live && row < r ? N[(at * r + row) * dv + col] : 0.f;
+        }
+    };
+    auto leave = [&](int seg, const float *from) {
+        for (int row = warp; row < r; row += 8)
+            if (live) starts[((bh * nseg + seg) * r + row) * dv + col] = from[row * 32 + lane];
+    };
+    if (steps > 0) fetch(0);
+    __syncthreads();
+    leave(0, St);
+    for (int i = 0; i < steps; ++i) {
+        const int row0 = i % tiles * kJoinRows + 4 * warp;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (lane + 32 * k < rp) Mt[j * rp + lane + 32 * k] = next[j][k];
+        float acc[4] = {n4[0], n4[1], n4[2], n4[3]};
+        __syncwarp();
+        if (i + 1 < steps) fetch(i + 1);
+#pragma unroll 2
+        for (int u = 0; u < rp; u += 4) {
+            const float x[4] = {St[u * 32 + lane], St[(u + 1) * 32 + lane], St[(u + 2) * 32 + lane], St[(u + 3) * 32 + lane]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 m = *reinterpret_cast<const float4 *>(Mt + j * rp + u);
+                acc[j] = fmaf(m.x, x[0], fmaf(m.y, x[1], fmaf(m.z, x[2], fmaf(m.w, x[3], acc[j]))));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (row0 + j < rp) Sn[(row0 + j) * 32 + lane] = acc[j];
+        if (i % tiles == tiles - 1) {
+            __syncthreads();
+            float *x = St;
+            St = Sn, Sn = x;
+            leave(i / tiles + 1, St);
+        }
+    }
 }
 
 // ------------------------------------------------- the gradients' last passes
@@ -684,6 +779,54 @@ cudaError_t launch_last_passes(const GdeltaShape &s, const GdeltaBackward &g, co
 }
 
 }  // namespace
+
+// Segments of a dense forward call (1: none) on `sms` SMs: the least of the estimates, in us, of one pass over the tokens and of two
+// passes over a segment's (5 of set-up each, 8 between the launches) with a join per segment (1.6 + r / 64 for each 32 rows), as long as
+// the first pass's CTAs, N's and M's columns, find an SM each.  Whole and in segments: B2 H4 T1001, 64 x 96 104 and 90 us, T4096 406 and 290;
+// one head of 8192 tokens, 128 x 128, 1285 and 396.  Segments are whole blocks of tokens.
+int gdelta_rec_segments(int B, int H, int T, int r, int dv, int sms)
+{
+    const long long ctas = (long long)B * H * ((dv + kRecCols - 1) / kRecCols + (r + kRecCols - 1) / kRecCols);
+    const double token = r <= 64 ? 0.101 : r <= 128 ? 0.157 : 0.23, join = (1.6 + r / 64.0) * ((r + 31) / 32);
+    int best = 1;
+    double least = T * token;
+    for (int n = 2; n <= 16 && n * ctas <= sms + sms / 8; ++n) {
+        const int len = ((T + n - 1) / n + kRecTok - 1) / kRecTok * kRecTok, used = (T + len - 1) / len;
+        const double t = 2 * (len * token + 5) + 8 + (used - 1) * join;
+        if (used == n && t < least) least = t, best = n;
+    }
+    return best;
+}
+
+size_t gdelta_rec_floats(int B, int H, int T, int r, int dv, int sms)
+{
+    const int n = gdelta_rec_segments(B, H, T, r, dv, sms);
+    return n > 1 ? (size_t)B * H * n * r * (2 * (size_t)dv + r) : 0;
+}
+
+cudaError_t launch_gdelta_rec_segments(const GdeltaShape &s, const GdeltaForward &f, bool bf16, int sms, float *ws, cudaStream_t stream)
+{
+    const int n = gdelta_rec_segments(s.B, s.H, s.T, s.r, s.dv, sms);
+    if (n == 1) return launch_gdelta_rec(s, f, bf16, stream);
+    static OncePerDevice once;
+    const uint32_t rp = (s.r + 3) & ~3;
+    cudaError_t e = set_smem_once(gdelta_join_kernel, 3 * 256 * 32 * 4, once);
+    if (e != cudaSuccess) return e;
+    RecArgs a{};
+    a.s = s;
+    a.q = f.q, a.k = f.k, a.v = f.v;
+    a.scale = f.scale;
+    a.nseg = n, a.seg_len = ((s.T + n - 1) / n + kRecTok - 1) / kRecTok * kRecTok;
+    const size_t state = (size_t)s.B * s.H * n * s.r * s.dv;
+    a.N = ws, a.M = ws + 2 * state, a.starts = ws + state;
+    a.sums = true;
+    if ((e = launch_rec<kFwd>(a, bf16, stream)) != cudaSuccess) return e;
+    e = launch_after(gdelta_join_kernel, dim3((s.dv + 31) / 32, s.B * s.H), 256, 3 * rp * 32 * 4, stream, s, f.S0, a.N, a.M, ws + state, n);
+    if (e != cudaSuccess) return e;
+    a.sums = false;
+    a.y = f.y, a.S_fin = f.S_out;
+    return launch_rec<kFwd>(a, bf16, stream);
+}
 
 cudaError_t launch_gdelta_rec(const GdeltaShape &s, const GdeltaForward &f, bool bf16, cudaStream_t stream)
 {

@@ -25,6 +25,10 @@ struct GdeltaForward {
 // The token recurrence in FP32 on CUDA cores, for any 1 <= r, dv <= 256 and either element type.
 cudaError_t launch_gdelta_rec(const GdeltaShape &s, const GdeltaForward &f, bool bf16, cudaStream_t stream);
 
+// The same for a dense call in segments where few heads leave SMs idle: workspace floats (0: none needed), and the launch.
+size_t gdelta_rec_floats(int B, int H, int T, int r, int dv, int sms);
+cudaError_t launch_gdelta_rec_segments(const GdeltaShape &s, const GdeltaForward &f, bool bf16, int sms, float *ws, cudaStream_t stream);
+
 // One token, S in place; dv a multiple of 4, S 16-byte aligned, r <= 256.
 cudaError_t launch_gdelta_decode(const GdeltaShape &s, const void *q, const void *k, const void *v, bool bf16, float *S,
                                  float scale, void *y, cudaStream_t stream);
