@@ -89,7 +89,7 @@ constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2 + 6);
 // warps convert a block of 16 tokens to FP32 while the computing ones work on the one before, and store its
 // results.  4 r dv FMAs per token and head bound it (FP32 B16 H16 T1001, 128 x 128: 1.0 ms, 33 TFLOP/s of about 75, beside the products
 // of the tokens with one another); few heads are bound by a group's latency, 0.4 us at 64 rows (B2 H4 T1001, 64 x 96: 104 us; 240
-// token by token, the sums of one waiting for the ones before, and the next block's loads for one another; 90 in segments).
+// token by token, the sums of one waiting for the ones before, and the next block's loads for one another; 84 in segments).
 template <int MODE, bool BF16, int RPL>
 __global__ void __launch_bounds__(kRecThreads)
 gdelta_rec_kernel(const RecArgs a)
@@ -489,8 +489,8 @@ cudaError_t launch_rec(const RecArgs &a, bool bf16, cudaStream_t stream)
 }
 
 // The states before the segments: S <- M S + N from one segment to the next.  A CTA has 32 columns of a head's state in shared memory
-// and takes M by 32 rows; a warp forms four of them, and what comes next is loaded meanwhile.
-constexpr int kJoinRows = 32;
+// and takes M by 8 RW rows of up to 32 KW columns; a warp forms RW of them, and what comes next is loaded meanwhile.
+template <int RW, int KW>
 __global__ void __launch_bounds__(256)
 gdelta_join_kernel(GdeltaShape s, const float *__restrict__ S0, const float *N, const float *M, float *starts, int nseg)
 {
@@ -503,19 +503,19 @@ gdelta_join_kernel(GdeltaShape s, const float *__restrict__ S0, const float *N, 
     wait_for_last();
     let_next_start();
     for (int row = warp; row < rp; row += 8) St[row * 32 + lane] = S0 && live && row < r ? S0[(bh * r + row) * dv + col] : 0.f;
-    const int tiles = (r + kJoinRows - 1) / kJoinRows, steps = tiles * (nseg - 1);
-    Mt += warp * 4 * rp;                                    // a warp's four rows are its own
-    float next[4][8], n4[4];
+    const int tiles = (r + 8 * RW - 1) / (8 * RW), steps = tiles * (nseg - 1);
+    Mt += warp * RW * rp;                                   // a warp's rows are its own
+    float next[RW][KW], nn[RW];
     auto fetch = [&](int i) {
         const size_t at = bh * nseg + i / tiles;
-        const int row0 = i % tiles * kJoinRows + 4 * warp;
+        const int row0 = i % tiles * (8 * RW) + RW * warp;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < RW; ++j) {
             const int row = row0 + j;
             const float *Mr = M + (at * r + row) * r;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) next[j][k] = row < r && lane + 32 * k < r ? Mr[lane + 32 * k] : 0.f;
-            n4[j] = live && row < r ? N[(at * r + row) * dv + col] : 0.f;
+            for (int k = 0; k < KW; ++k) next[j][k] = row < r && lane + 32 * k < r ? Mr[lane + 32 * k] : 0.f;
+            nn[j] = live && row < r ? N[(at * r + row) * dv + col] : 0.f;
         }
     };
     auto leave = [&](int seg, const float *from) {
@@ -526,27 +526,29 @@ gdelta_join_kernel(GdeltaShape s, const float *__restrict__ S0, const float *N, 
     __syncthreads();
     leave(0, St);
     for (int i = 0; i < steps; ++i) {
-        const int row0 = i % tiles * kJoinRows + 4 * warp;
+        const int row0 = i % tiles * (8 * RW) + RW * warp;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < RW; ++j)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < KW; ++k)
                 if (lane + 32 * k < rp) Mt[j * rp + lane + 32 * k] = next[j][k];
-        float acc[4] = {n4[0], n4[1], n4[2], n4[3]};
+        float acc[RW];
+#pragma unroll
+        for (int j = 0; j < RW; ++j) acc[j] = nn[j];
         __syncwarp();
         if (i + 1 < steps) fetch(i + 1);
 #pragma unroll 2
         for (int u = 0; u < rp; u += 4) {
             const float x[4] = {St[u * 32 + lane], St[(u + 1) * 32 + lane], St[(u + 2) * 32 + lane], St[(u + 3) * 32 + lane]};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < RW; ++j) {
                 const float4 m = *reinterpret_cast<const float4 *>(Mt + j * rp + u);
                 acc[j] = fmaf(m.x, x[0], fmaf(m.y, x[1], fmaf(m.z, x[2], fmaf(m.w, x[3], acc[j]))));
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < RW; ++j)
             if (row0 + j < rp) Sn[(row0 + j) * 32 + lane] = acc[j];
         if (i % tiles == tiles - 1) {
             __syncthreads();
@@ -781,13 +783,13 @@ cudaError_t launch_last_passes(const GdeltaShape &s, const GdeltaBackward &g, co
 }  // namespace
 
 // Segments of a dense forward call (1: none) on `sms` SMs: the least of the estimates, in us, of one pass over the tokens and of two
-// passes over a segment's (5 of set-up each, 8 between the launches) with a join per segment (1.6 + r / 64 for each 32 rows), as long as
-// the first pass's CTAs, N's and M's columns, find an SM each.  Whole and in segments: B2 H4 T1001, 64 x 96 104 and 90 us, T4096 406 and 290;
-// one head of 8192 tokens, 128 x 128, 1285 and 396.  Segments are whole blocks of tokens.
+// passes over a segment's (5 of set-up each, 8 between the launches) with a join per segment (1.6 + r / 40 up to 64 rows, else 1.6 + r / 64 for each 32), as long as
+// the first pass's CTAs, N's and M's columns, find an SM each.  Whole and in segments: B2 H4 T1001, 64 x 96 104 and 84 us, T4096 406 and 284;
+// one head of 8192 tokens, 128 x 128, 1285 and 391.  Segments are whole blocks of tokens.
 int gdelta_rec_segments(int B, int H, int T, int r, int dv, int sms)
 {
     const long long ctas = (long long)B * H * ((dv + kRecCols - 1) / kRecCols + (r + kRecCols - 1) / kRecCols);
-    const double token = r <= 64 ? 0.101 : r <= 128 ? 0.157 : 0.23, join = (1.6 + r / 64.0) * ((r + 31) / 32);
+    const double token = r <= 64 ? 0.101 : r <= 128 ? 0.157 : 0.23, join = r <= 64 ? 1.6 + r / 40.0 : (1.6 + r / 64.0) * ((r + 31) / 32);
     int best = 1;
     double least = T * token;
     for (int n = 2; n <= 16 && n * ctas <= sms + sms / 8; ++n) {
@@ -810,7 +812,7 @@ cudaError_t launch_gdelta_rec_segments(const GdeltaShape &s, const GdeltaForward
     if (n == 1) return launch_gdelta_rec(s, f, bf16, stream);
     static OncePerDevice once;
     const uint32_t rp = (s.r + 3) & ~3;
-    cudaError_t e = set_smem_once(gdelta_join_kernel, 3 * 256 * 32 * 4, once);
+    cudaError_t e = set_smem_once(gdelta_join_kernel<4, 8>, 3 * 256 * 32 * 4, once);
     if (e != cudaSuccess) return e;
     RecArgs a{};
     a.s = s;
@@ -821,7 +823,10 @@ cudaError_t launch_gdelta_rec_segments(const GdeltaShape &s, const GdeltaForward
     a.N = ws, a.M = ws + 2 * state, a.starts = ws + state;
     a.sums = true;
     if ((e = launch_rec<kFwd>(a, bf16, stream)) != cudaSuccess) return e;
-    e = launch_after(gdelta_join_kernel, dim3((s.dv + 31) / 32, s.B * s.H), 256, 3 * rp * 32 * 4, stream, s, f.S0, a.N, a.M, ws + state, n);
+    // up to 64 rows in one step (B2 H4 T1001, 64 x 96: 90 us by 32 at a time, 84 so)
+    const bool one = s.r <= 64;
+    e = launch_after(one ? gdelta_join_kernel<8, 2> : gdelta_join_kernel<4, 8>, dim3((s.dv + 31) / 32, s.B * s.H), 256,
+                     (one ? 128 : 96) * rp * 4, stream, s, f.S0, a.N, a.M, ws + state, n);
     if (e != cudaSuccess) return e;
     a.sums = false;
     a.y = f.y, a.S_fin = f.S_out;
