@@ -10,10 +10,9 @@
 //     dq_t = scale S_t dy_t,   dk_t = beta_t G_t e_t - S'_t dv_t.
 // Every column of S is a recurrence of its own given k, and so is every column of G: one sweep forwards
 // leaves e, one backwards lam.  With e and dv known every row of S, and of G, is one as well: the products
-// S dy, S' dv and G e are two more sweeps over the transposed states.  The gates: log alpha_t
-// scales what the states from t on hold of the ones before, and taking that scale out of the state moves
-// it to q (e^{+}) and v (e^{-}) of the tokens from t on, so
-//     dL/dlog alpha_t = <S_T, dS_T> + sum_{s >= t} (q_s . dq_s - v_s . dv_s).
+// S dy, S' dv and G e are two more sweeps over the transposed states.  The gates:
+//     dalpha_t = <S_{t-1}, G_t - k_t dv_t^T>,
+// formed chunk by chunk from the states that the first two sweeps leave between chunks (gdelta_gate_kernel).
 
 #include "gdelta.h"
 #include "launch_after.cuh"
@@ -64,6 +63,7 @@ struct RecArgs {
     bool sums = false;
     float *N = nullptr, *M = nullptr;        // [B*H][nseg][r][dv], [B*H][nseg][r][r]
     const float *starts = nullptr;           // [B*H][nseg][r][dv]
+    float *ckpt = nullptr;                   // kFwd: the states before every chunk, kRev: the gradients behind it, [B*H][chunks][r][dv]
 };
 
 constexpr int kRecTok = 16;              // tokens per staged block
@@ -71,6 +71,8 @@ constexpr int kRecComp = 128;            // threads that compute: 4 warps of 8 c
 constexpr int kRecThreads = 2 * kRecComp;   // and as many that stage the next block and write out the last one
 constexpr int kRecCols = 32;
 constexpr int kRecGroup = 4;             // tokens taken together
+constexpr int kGateC = 64;               // tokens per chunk of the gates' gradient
+static_assert(kGateC % kRecTok == 0, "chunks end where staged blocks do");
 
 template <int RPL>
 constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2 + 6);
@@ -145,8 +147,9 @@ gdelta_rec_kernel(const RecArgs a)
     const bool computes = tid < kRecComp;
     const int warp = tid >> 5, g = lane >> 2, jl = (warp & 3) * 8 + 2 * (lane & 3);
     const int nblk = (T + kRecTok - 1) / kRecTok;
-    // token of position i of block n in the sweep's order
-    auto token = [&](int n, int i) { const int t = n * kRecTok + i; return kBack ? T - 1 - t : t; };
+    // token of position i of block n in the sweep's order.  Blocks are whole 16 tokens of the sequence in both directions: a last one
+    // that is not full comes first backwards, behind positions past the sequence's end (zeros, alpha 1).
+    auto token = [&](int n, int i) { const int t = n * kRecTok + i; return kBack ? nblk * kRecTok - 1 - t : t; };
     auto staging_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kRecComp) : "memory"); };
     auto block_sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(kRecThreads) : "memory"); };
     if (!computes) {
@@ -159,9 +162,8 @@ gdelta_rec_kernel(const RecArgs a)
         const Rows key = rows_of(s.Hk, hk, s.r), val = rows_of(s.H, h, s.dv), gate = rows_of(s.H, h, 1), res = rows_of(s.H, h, cols);
         const Rows vec = kT ? val : key, elem = kT ? key : val;
         auto fetch = [&](int n) {
-            const int nt = min(kRecTok, T - n * kRecTok);
             fal = fbe = 1.f;
-            if (sid < nt) {
+            if (sid < kRecTok && token(n, sid) < T) {
                 const size_t o = gate.first + token(n, sid) * gate.stride;
                 if (s.alpha) fal = s.alpha[o];
                 if (s.beta) fbe = s.beta[o];
@@ -174,7 +176,7 @@ gdelta_rec_kernel(const RecArgs a)
                 const size_t oj = o + part * kRecComp;
                 fx[j] = fb[j] = 0.f;
                 if (kT) fd[j] = 0.f;
-                if (i < nt && row0 + part * kRecComp < rows) {
+                if (token(n, i) < T && row0 + part * kRecComp < rows) {
                     fx[j] = load_elem<BF16>(kT ? a.dy : a.q, oj);
                     fb[j] = !kT ? load_elem<BF16>(a.k, oj) : MODE == kQue ? a.lam[oj] : a.e[oj];
                     if (kT) fd[j] = MODE == kQue ? a.e[oj] : a.lam[oj];
@@ -187,7 +189,7 @@ gdelta_rec_kernel(const RecArgs a)
             for (int j = 0; j < kColIters; ++j) {
                 fu[j] = 0.f;
                 if (MODE == kKey) fu2[j] = 0.f;
-                if (i_col + j * (kRecComp / kRecCols) < nt && col < cols && !unit) {
+                if (token(n, i_col + j * (kRecComp / kRecCols)) < T && col < cols && !unit) {
                     fu[j] = load_elem<BF16>(kT ? a.k : MODE == kFwd ? a.v : a.dy, oc);
                     if (MODE == kKey) fu2[j] = load_elem<BF16>(a.q, oc);
                 }
@@ -259,18 +261,17 @@ gdelta_rec_kernel(const RecArgs a)
         };
         auto stage_out = [&](int n) {
             const float *st = st0 + (n & 1) * kStage;
-            const int nt = min(kRecTok, T - n * kRecTok);
             if (col >= cols) return;
             size_t o = res.first + col + (ptrdiff_t)token(n, i_col) * res.stride;
             const ptrdiff_t step = (kBack ? -1 : 1) * (kRecComp / kRecCols) * res.stride;
             float was[kColIters];
 #pragma unroll
             for (int j = 0; j < kColIters; ++j)
-                if (MODE == kKey && i_col + j * (kRecComp / kRecCols) < nt) was[j] = a.w[o + j * step];
+                if (MODE == kKey && token(n, i_col + j * (kRecComp / kRecCols)) < T) was[j] = a.w[o + j * step];
 #pragma unroll
             for (int j = 0; j < kColIters; ++j) {
                 const int i = i_col + j * (kRecComp / kRecCols), x = sid + j * kRecComp;
-                if (i >= nt) break;
+                if (token(n, i) >= T) continue;
                 const float out = st[kOffO + x], out2 = st[kOffO2 + x], bt = st[kOffG + kRecTok + i];
                 const size_t oj = o + j * step;
                 if (MODE == kFwd) {
@@ -325,9 +326,23 @@ gdelta_rec_kernel(const RecArgs a)
         block_sync();
         for (int n = 0; n < nblk; ++n) {
             float *st = st0 + (n & 1) * kStage;
-            const int groups = (min(kRecTok, T - n * kRecTok) + kRecGroup - 1) / kRecGroup;     // tokens after the last are zeros, alpha 1
+            if constexpr (MODE == kFwd || MODE == kRev) {
+                if (a.ckpt && (kBack ? n == 0 || token(n, 0) % kGateC == kGateC - 1 : token(n, 0) % kGateC == 0)) {
+                    float *to = a.ckpt + (bh * ((T + kGateC - 1) / kGateC) + token(n, 0) / kGateC) * s.r * s.dv;
+#pragma unroll
+                    for (int m = 0; m < RPL; ++m) {
+                        const int row = 4 * (8 * (m >> 2) + g) + (m & 3);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (row < rows && c0 + jl + c < cols) to[(size_t)row * s.dv + c0 + jl + c] = X[c][m];
+                    }
+                }
+            }
+            // groups that hold tokens (those past the sequence's end are zeros, alpha 1)
+            const int first = kBack && n == 0 ? (nblk * kRecTok - T) / kRecGroup : 0;
+            const int groups = kBack ? kRecTok / kRecGroup : (min(kRecTok, T - n * kRecTok) + kRecGroup - 1) / kRecGroup;
 #pragma unroll 1
-            for (int gr = 0; gr < groups; ++gr) {
+            for (int gr = first; gr < groups; ++gr) {
                 const int i0 = gr * kRecGroup;
                 const float4 *xr = reinterpret_cast<const float4 *>(st + i0 * W) + g;
                 const float4 *br = reinterpret_cast<const float4 *>(st + kOffB + i0 * W) + g;
@@ -567,30 +582,17 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// dbeta_t = lam . e and the token's part of the gates' gradient, q . dq - v . dv: one warp per (b, h, t).
-template <bool BF16>
+// dbeta_t = lam . e: one warp per (b, h, t).
 __global__ void __launch_bounds__(256)
-gdelta_token_terms_kernel(GdeltaShape s, const void *q, const void *v, const float *dq, const float *lam, const float *e,
-                          float *dbeta, float *dG)
+gdelta_beta_kernel(GdeltaShape s, const float *lam, const float *e, float *dbeta)
 {
     const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (i >= (long long)s.B * s.H * s.T) return;
-    const long long bh = i / s.T, t = i % s.T;
-    const int b = (int)(bh / s.H), hk = (int)(bh % s.H) / (s.H / s.Hk);
-    const size_t qo = (((size_t)b * s.Hk + hk) * s.T + t) * s.r;
-    float db = 0.f, gq = 0.f, gv = 0.f;
-    for (int x = lane; x < s.dv; x += 32) {
-        const float l = lam[i * s.dv + x];
-        db = fmaf(l, e[i * s.dv + x], db);
-        gv = fmaf(l, load_elem<BF16>(v, i * s.dv + x), gv);
-    }
-    for (int x = lane; x < s.r; x += 32) gq = fmaf(load_elem<BF16>(q, qo + x), dq[i * s.r + x], gq);
-    db = warp_sum(db), gq = warp_sum(gq), gv = warp_sum(gv);
-    if (lane == 0) {
-        if (dbeta) dbeta[i] = db;
-        if (dG) dG[i] = gq - (s.beta ? s.beta[i] : 1.f) * gv;
-    }
+    float db = 0.f;
+    for (int x = lane; x < s.dv; x += 32) db = fmaf(lam[i * s.dv + x], e[i * s.dv + x], db);
+    db = warp_sum(db);
+    if (lane == 0) dbeta[i] = db;
 }
 
 // dq and dk of a key head: the sum over the value heads that share it, in their order.
@@ -612,44 +614,177 @@ gdelta_group_sum_kernel(GdeltaShape s, const float *dq, const float *dk, void *d
     store_elem<BF16>(dk_out, i, c);
 }
 
-// dalpha_t = (<S_T, dS_T> + sum_{s >= t} dG_s) / alpha_t: one CTA per (b, h).  The sum runs in 64 bits: over a long
-// sequence it is much smaller than the terms that cancel in it.
+// dalpha_t = <S_{t-1}, G_t - k_t dv_t^T> of a chunk's tokens, one CTA per chunk and head.  With S the state before the chunk, G the
+// gradient behind it and v'_j = beta_j e_j, both factors are sums over the chunk's tokens,
+//     S_{t-1} = (prod_{l < t} alpha_l) S + sum_{j < t} (prod_{j < l < t} alpha_l) k_j v'_j^T,
+//     G_t - k_t dv_t^T = (prod_{l > t} alpha_l) G + sum_{s >= t} (prod_{t < l <= s} alpha_l) (scale q_s dy_s^T - k_s dv_s^T),
+// so alpha_t dalpha_t is the sum over j < t <= s of F_sj = (prod_{j < l <= s} alpha_l) W_sj, where
+//     W_sj = scale (q_s . k_j) (dy_s . v'_j) - (k_s . k_j) (dv_s . v'_j),
+// the state before the chunk stands for a token j = -1 (W_s,-1 = scale q_s . S dy_s - k_s . S dv_s) and the gradient behind it for a token
+// s = 64 (W_64,j = k_j . G v'_j, W_64,-1 = <S, G>).  Every term of the sum has alpha_t as a factor: nothing cancels that is larger than the
+// result by 1 / alpha_t, as the difference of the tokens' q . dq and v . dv would.  Gates below kLeastGate count as that here,
+// zeros too: it is divided out again, and what else they scale is below FP32's rounding.  Three products of 64 tokens with a state and four of the tokens with one another, FP32, in
+// tiles of 64 x 64 with 4 x 4 numbers per thread.
+constexpr float kLeastGate = 5.421010862427522e-20f;     // 2^-64
+template <bool BF16>
 __global__ void __launch_bounds__(256)
-gdelta_gate_sum_kernel(GdeltaShape s, const float *S_T, const float *dS_T, const float *dG, float *dalpha)
+gdelta_gate_kernel(GdeltaShape s, const void *q, const void *k, const void *dy, float scale, const float *e, const float *lam,
+                   const float *S, const float *G, float *dalpha)
 {
-    __shared__ double part[8];
-    const size_t bh = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = s.r * s.dv;
-    double acc = 0.0;
-    if (dS_T)
-        for (int x = tid; x < n; x += 256) acc += (double)S_T[bh * n + x] * dS_T[bh * n + x];
+    constexpr int C = kGateC, LDW = C + 4, KS = 16;
+    __shared__ __align__(16) float ta[KS][LDW], tb[KS][LDW], tc[KS][LDW], td[KS][LDW];
+    __shared__ float F[C][C + 1], al[C], be[C], as[C], bs[C], part[8];
+    const int nch = (s.T + C - 1) / C, c = blockIdx.x % nch, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const size_t bh = blockIdx.x / nch;
+    const size_t key = (bh / s.H * s.Hk + bh % s.H / (s.H / s.Hk)) * s.T + (size_t)c * C, val = bh * s.T + (size_t)c * C;
+    const int nt = min(C, s.T - c * C), r = s.r, dv = s.dv;
+    const float *Sc = S + (bh * nch + c) * r * dv, *Gc = G + (bh * nch + c) * r * dv;
+    if (tid < C) {
+        al[tid] = tid < nt ? fmaxf(s.alpha[val + tid], kLeastGate) : 1.f;
+        be[tid] = tid < nt && s.beta ? s.beta[val + tid] : 1.f;
+    }
+    // 16 columns from u0 on of the chunk's rows of an array of d columns, transposed
+    auto rows_in = [&](float (*to)[LDW], auto elem, size_t first, int d, int u0) {
+        const int u = tid & 15;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) part[warp] = acc;
+        for (int m = 0; m < C / 16; ++m) {
+            const int t = (tid >> 4) + 16 * m;
+            to[u][t] = t < nt && u0 + u < d ? elem((first + t) * d + u0 + u) : 0.f;
+        }
+    };
+    auto q_at = [&](size_t i) { return load_elem<BF16>(q, i); };
+    auto k_at = [&](size_t i) { return load_elem<BF16>(k, i); };
+    auto dy_at = [&](size_t i) { return load_elem<BF16>(dy, i); };
+    auto e_at = [&](size_t i) { return e[i]; };
+    auto lam_at = [&](size_t i) { return lam[i]; };
+    auto mul = [&](float (&acc)[4][4], float4 x, float4 y) {
+        const float a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    };
+    auto f4 = [](const float *p) { return *reinterpret_cast<const float4 *>(p); };
     __syncthreads();
-    double carry = 0.0;
-    for (int w = 0; w < 8; ++w) carry += part[w];
-    for (int t1 = s.T; t1 > 0; t1 -= 256) {       // tokens from the last on, thread i the i-th
-        const int t = t1 - 1 - tid;
-        double x = t >= 0 ? dG[bh * s.T + t] : 0.0;
+
+    // the tokens with the state before the chunk and the gradient behind it
+    float av[4] = {}, bv[4] = {}, anchor = 0.f;
+    for (int d0 = 0; d0 < dv; d0 += C) {
+        float qs[4][4] = {}, ks[4][4] = {}, kg[4][4] = {};
+        for (int u0 = 0; u0 < r; u0 += KS) {
+            rows_in(ta, q_at, key, r, u0);
+            rows_in(tb, k_at, key, r, u0);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            for (int m = 0; m < KS / 4; ++m) {
+                const int u = (tid >> 6) + 4 * m, d = tid & 63;
+                const bool in = u0 + u < r && d0 + d < dv;
+                const size_t at = (size_t)(u0 + u) * dv + d0 + d;
+                const float x = in ? Sc[at] : 0.f, y = in ? Gc[at] : 0.f;
+                tc[u][d] = x, td[u][d] = y;
+                anchor = fmaf(x, y, anchor);
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int u = 0; u < KS; ++u) {
+                const float4 kr = f4(&tb[u][4 * ty]), sc = f4(&tc[u][4 * tx]);
+                mul(qs, f4(&ta[u][4 * ty]), sc);
+                mul(ks, kr, sc);
+                mul(kg, kr, f4(&td[u][4 * tx]));
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * ty + i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int d = d0 + 4 * tx + j;
+                if (t >= nt || d >= dv) continue;
+                const size_t at = (val + t) * dv + d;
+                av[i] = fmaf(scale * qs[i][j], dy_at(at), fmaf(-be[t] * ks[i][j], lam[at], av[i]));
+                bv[i] = fmaf(be[t] * kg[i][j], e[at], bv[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+            av[i] += __shfl_xor_sync(0xffffffffu, av[i], o);
+            bv[i] += __shfl_xor_sync(0xffffffffu, bv[i], o);
+        }
+        if (tx == 0) as[4 * ty + i] = av[i], bs[4 * ty + i] = bv[i];
+    }
+    anchor = warp_sum(anchor);
+    if ((tid & 31) == 0) part[tid >> 5] = anchor;
+
+    // the tokens with one another
+    float qk[4][4] = {}, kk[4][4] = {}, ye[4][4] = {}, le[4][4] = {};
+    for (int u0 = 0; u0 < r; u0 += KS) {
+        rows_in(ta, q_at, key, r, u0);
+        rows_in(tb, k_at, key, r, u0);
+        __syncthreads();
+#pragma unroll 4
+        for (int u = 0; u < KS; ++u) {
+            const float4 kj = f4(&tb[u][4 * tx]);
+            mul(qk, f4(&ta[u][4 * ty]), kj);
+            mul(kk, f4(&tb[u][4 * ty]), kj);
         }
         __syncthreads();
-        if (lane == 31) part[warp] = x;
+    }
+    for (int u0 = 0; u0 < dv; u0 += KS) {
+        rows_in(ta, dy_at, val, dv, u0);
+        rows_in(tb, lam_at, val, dv, u0);
+        rows_in(tc, e_at, val, dv, u0);
         __syncthreads();
-        double before = carry;
-        for (int w = 0; w < 8; ++w) {
-            if (w < warp) before += part[w];
-            carry += part[w];
+#pragma unroll 4
+        for (int u = 0; u < KS; ++u) {
+            const float4 ej = f4(&tc[u][4 * tx]);
+            mul(ye, f4(&ta[u][4 * ty]), ej);
+            mul(le, f4(&tb[u][4 * ty]), ej);
         }
-        if (t >= 0) {
-            const float al = s.alpha[bh * s.T + t];
-            dalpha[bh * s.T + t] = al > 0.f ? (float)((before + x) / (double)al) : 0.f;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = 4 * ty + i, u = 4 * tx + j;
+            F[t][u] = be[u] * fmaf(scale * qk[i][j], ye[i][j], -be[t] * kk[i][j] * le[i][j]);
         }
+    __syncthreads();
+    // F, and in its place its sums over j < t; the row of the gradient behind the chunk in bs
+    if (tid < C) {
+        float m = al[tid];
+        for (int j = tid - 1; j >= 0; --j) {
+            F[tid][j] *= m;
+            m *= al[j];
+        }
+        float sum = as[tid] * m;
+        for (int t = 0; t <= tid; ++t) {
+            const float f = F[tid][t];
+            F[tid][t] = sum;
+            sum += f;
+        }
+    } else if (tid == C) {
+        float m = 1.f, sum = 0.f;
+        for (int j = C - 1; j >= 0; --j) {
+            bs[j] *= m;
+            m *= al[j];
+        }
+        for (int w = 0; w < 8; ++w) sum += part[w];
+        sum *= m;
+        for (int t = 0; t < C; ++t) {
+            const float f = bs[t];
+            bs[t] = sum;
+            sum += f;
+        }
+    }
+    __syncthreads();
+    if (tid < nt) {
+        float sum = bs[tid];
+        for (int t = tid; t < C; ++t) sum += F[t][tid];
+        dalpha[val + tid] = s.alpha[val + tid] > 0.f ? sum / al[tid] : 0.f;
     }
 }
 
@@ -764,22 +899,6 @@ cudaError_t launch_dec(const GdeltaShape &s, const void *q, const void *k, const
     return cudaGetLastError();
 }
 
-template <bool BF16>
-cudaError_t launch_last_passes(const GdeltaShape &s, const GdeltaBackward &g, const float *e, const float *lam, const float *dq,
-                               const float *dk, const float *S_T, float *dG, cudaStream_t stream)
-{
-    const long long tokens = (long long)s.B * s.H * s.T;
-    float *dal = s.alpha ? g.dalpha : nullptr;
-    if (tokens > 0) {
-        gdelta_token_terms_kernel<BF16><<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(s, g.q, g.v, dq, lam, e, g.dbeta,
-                                                                                        dal ? dG : nullptr);
-        const cudaError_t st = launch_gdelta_group_sum(s, dq, dk, BF16, g.dq, g.dk, stream);
-        if (st != cudaSuccess) return st;
-    }
-    if (dal && tokens > 0) gdelta_gate_sum_kernel<<<(unsigned)(s.B * s.H), 256, 0, stream>>>(s, S_T, g.dS_T, dG, dal);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 // Segments of a dense forward call (1: none) on `sms` SMs: the least of the estimates, in us, of one pass over the tokens and of two
@@ -857,18 +976,19 @@ cudaError_t launch_gdelta_group_sum(const GdeltaShape &s, const float *dq, const
                         dk_out);
 }
 
-// e, lam [B,H,T,dv]; w (then dk), dq [B,H,T,r]; S_T; dG [B,H,T]
+// e, lam [B,H,T,dv]; w (then dk), dq [B,H,T,r]; the states before every chunk and the gradients behind it
 size_t gdelta_rec_backward_floats(int B, int H, int T, int r, int dv)
 {
-    const size_t tokens = (size_t)B * H * T;
-    return tokens * (2 * (size_t)dv + 2 * (size_t)r + 1) + (size_t)B * H * r * dv;
+    const size_t heads = (size_t)B * H, chunks = (T + (size_t)kGateC - 1) / kGateC;
+    return heads * T * (2 * (size_t)dv + 2 * (size_t)r) + heads * chunks * 2 * r * dv;
 }
 
 cudaError_t launch_gdelta_rec_backward(const GdeltaShape &s, const GdeltaBackward &g, bool bf16, cudaStream_t stream)
 {
-    const size_t tokens = (size_t)s.B * s.H * s.T;
-    float *e = g.ws, *lam = e + tokens * s.dv, *w = lam + tokens * s.dv, *dq = w + tokens * s.r, *S_T = dq + tokens * s.r,
-          *dG = S_T + (size_t)s.B * s.H * s.r * s.dv;
+    const size_t heads = (size_t)s.B * s.H, tokens = heads * s.T, chunks = heads * ((s.T + kGateC - 1) / kGateC);
+    float *e = g.ws, *lam = e + tokens * s.dv, *w = lam + tokens * s.dv, *dq = w + tokens * s.r, *S = dq + tokens * s.r,
+          *G = S + chunks * s.r * s.dv;
+    const bool gates = s.alpha && g.dalpha;
     RecArgs a{};
     a.s = s;
     a.q = g.q, a.k = g.k, a.v = g.v, a.dy = g.dy;
@@ -876,17 +996,21 @@ cudaError_t launch_gdelta_rec_backward(const GdeltaShape &s, const GdeltaBackwar
     a.e = a.e_out = e, a.lam = a.lam_out = lam;
     a.w = w, a.dq = dq, a.dv_out = g.dv_out;
     cudaError_t st = cudaSuccess;
-    a.S_init = g.S0, a.S_fin = S_T;
+    a.S_init = g.S0, a.ckpt = gates ? S : nullptr;
     if ((st = launch_rec<kFwd>(a, bf16, stream)) != cudaSuccess) return st;
-    a.S_init = g.dS_T, a.S_fin = g.dS0;
+    a.S_init = g.dS_T, a.S_fin = g.dS0, a.ckpt = gates ? G : nullptr;
     if ((st = launch_rec<kRev>(a, bf16, stream)) != cudaSuccess) return st;
-    a.S_fin = nullptr;
+    a.S_fin = a.ckpt = nullptr;
     a.S_init = g.S0;
     if ((st = launch_rec<kQue>(a, bf16, stream)) != cudaSuccess) return st;
     a.S_init = g.dS_T;
     if ((st = launch_rec<kKey>(a, bf16, stream)) != cudaSuccess) return st;
-    return bf16 ? launch_last_passes<true>(s, g, e, lam, dq, w, S_T, dG, stream)
-                : launch_last_passes<false>(s, g, e, lam, dq, w, S_T, dG, stream);
+    if (g.dbeta) gdelta_beta_kernel<<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(s, lam, e, g.dbeta);
+    if ((st = launch_gdelta_group_sum(s, dq, w, bf16, g.dq, g.dk, stream)) != cudaSuccess) return st;
+    if (gates)
+        (bf16 ? gdelta_gate_kernel<true> : gdelta_gate_kernel<false>)<<<(unsigned)chunks, 256, 0, stream>>>(
+            s, g.q, g.k, g.dy, g.scale, e, lam, S, G, g.dalpha);
+    return cudaGetLastError();
 }
 
 }  // namespace la
