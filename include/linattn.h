@@ -567,12 +567,14 @@ la_status la_gated_delta_decode_step(const void *q, const void *k, const void *v
  *     G_t = scale q_t dy_t^T + alpha_{t+1} (G_{t+1} - k_{t+1} dv_{t+1}^T),   G_T = scale q_T dy_T^T + dS_T,
  *     dv_t = beta_t G_t^T k_t,   dk_t = beta_t G_t e_t - S'_t dv_t,   dq_t = scale S_t dy_t,
  *     dbeta_t = (G_t^T k_t) . e_t,   dS0 = alpha_1 (G_1 - k_1 dv_1^T),
- *     dalpha_t = (<S_T, dS_T> + sum_{s >= t} (q_s . dq_s - v_s . dv_s)) / alpha_t.
+ *     dalpha_t = <S_{t-1}, G_t - k_t dv_t^T>.
  *   q, k, v, alpha, beta, S0, scale: as passed to the forward call (its outputs are not needed).
  *   dy       device [B,H,T,dv] dtype         dS_T  device FP32 [B,H,r,dv] or NULL (zero)
  *   dq, dk   device [B,Hk,T,r] dtype         dv_out  device [B,H,T,dv] dtype
- *   dalpha   device FP32 [B,H,T] or NULL (not formed; ignored without alpha).  Defined where alpha > 0 (it is the
- *            log-gate's gradient over alpha); 0 is written where alpha is 0.
+ *   dalpha   device FP32 [B,H,T] or NULL (not formed; ignored without alpha).  It is as accurate at a gate near 0 (denormal numbers
+ *            included) as at 1: off by 1e-7 of |S_{t-1}| |G_t - k_t dv_t^T| / sqrt(r dv) in the recurrence, 2e-6 in chunks (2-norms over all
+ *            tokens).  A gate of exactly 0 is taken for a constant: 0 is written there.  Who wants the derivative at a
+ *            reset passes the smallest normal number for it, 1.2e-38, which keeps nothing of the state either.
  *   dbeta    device FP32 [B,H,T] or NULL (not formed)
  *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL)
  *   workspace  la_gated_delta_backward_workspace_bytes(...) bytes, as above

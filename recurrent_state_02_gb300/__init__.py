@@ -608,7 +608,8 @@ def gated_delta_backward_workspace_bytes(B, H, Hk, T, r, dv, dtype=torch.bfloat1
 def gated_delta_backward(q, k, v, dy, alpha=None, beta=None, S0=None, dS_T=None, scale=1.0, workspace=None):
     """Gradients of gated_delta_prefill: from its inputs, dy [B,H,T,dv] and optionally dS_T [B,H,r,dv] fp32,
     returns (dq, dk, dv, dalpha, dbeta, dS0): dq, dk [B,Hk,T,r] and dv in the input dtype, dalpha and
-    dbeta [B,H,T] fp32 (None for a gate that was not given), dS0 fp32.  dalpha is 0 where alpha is 0."""
+    dbeta [B,H,T] fp32 (None for a gate that was not given), dS0 fp32.  A gate of exactly 0 is taken for a constant (its
+    dalpha is 0); dalpha is as accurate at gates near 0 as at 1."""
     B, Hk, T, r = q.shape
     H, dvd = v.shape[1], v.shape[3]
     dt, dev = _gdelta_inputs(q, k, v, alpha, beta, lambda h: (B, h, T), Hk, H, r, dvd)

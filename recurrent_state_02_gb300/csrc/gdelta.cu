@@ -625,7 +625,6 @@ gdelta_group_sum_kernel(GdeltaShape s, const float *dq, const float *dk, void *d
 // result by 1 / alpha_t, as the difference of the tokens' q . dq and v . dv would.  Gates below kLeastGate count as that here,
 // zeros too: it is divided out again, and what else they scale is below FP32's rounding.  Three products of 64 tokens with a state and four of the tokens with one another, FP32, in
 // tiles of 64 x 64 with 4 x 4 numbers per thread.
-constexpr float kLeastGate = 5.421010862427522e-20f;     // 2^-64
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 gdelta_gate_kernel(GdeltaShape s, const void *q, const void *k, const void *dy, float scale, const float *e, const float *lam,

@@ -5,6 +5,9 @@
 
 namespace la {
 
+// Gates below this count as this in the sums of the gates' gradient, which then divide it out again (2^-64).
+constexpr float kLeastGate = 5.421010862427522e-20f;
+
 // The sizes and gates that every launcher shares.  Value heads H, query and key heads Hk (H a
 // multiple): value head h reads key head h / (H / Hk).
 struct GdeltaShape {

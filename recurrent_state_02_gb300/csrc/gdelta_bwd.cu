@@ -11,15 +11,20 @@
 //     dQ = dP K + scale e^G dY S^T
 //     dK = dP^T Q + dL K + dL^T K - e^G N S^T + beta e^{G_C - G} E dS^T
 //     dbeta_j = Z_jj / beta_j                                                       (N_j is beta_j times its error's gradient)
-//     dlog alpha_t = <S, dS_before> - sum_{s < t, in the chunk} (q_s . (scale e^G dY S^T)_s + sum_j A_sj dA_sj - v_s . N_s)
-// (the gates' gradient is anchored before every chunk, so that nothing is summed over the sequence).
+// The gates: dalpha_t = <S_{t-1}, G_t - k_t dv_t^T>, with G_t the gradient of S_t.  Both factors are sums over the chunk's tokens, so
+//     alpha_t dalpha_t = sum over j < t <= s of F_sj,     F_sj = dec_sj (P_sj dA_sj - (k_s . k_j) beta_j Z_sj),
+// where the state before the chunk stands for a token j = -1 and the gradient behind it for a token s = C:
+//     F_s,-1 = e^{G_s} (scale q_s . (dY S^T)_s - k_s . (N S^T)_s),   F_Cj = e^{G_C - G_j} beta_j k_j . (E dS^T)_j,   F_C,-1 = e^{G_C} <S, dS>.
+// Every term has alpha_t as a factor, so the division cancels nothing: relative to the two factors' sizes the result is as good at a gate of
+// 1e-42 as at 1 (as a difference of the tokens' q . dq and v . dv it was off by 1 % at 1e-3).  Gates below 2^-64 count as that in the
+// exponents of F, where it is divided out again, and as 0 in dec elsewhere.
 // Kernels: gdelta_prep (A, X, gates, scale e^G Q); the forward chain again, keeping the states between the chunks and E, and beside
 // it the backward chain, keeping their gradients and N; and a kernel over all chunks.
 // At B4 H16 T4096, 128 wide: 78 us, 240 us (both chains, 128 CTAs; 1.44 GB moved, 6 TB/s) and 236 us (1.21 GB, 5.1 TB/s), so that what the
 // kernels hand one another, the states between the chunks and E and N above all, is what bounds them.  Forming each chunk's
 // gradients inside the chains would spare half of it, but needs both chains at the same chunk.
-// Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand; what reaches dq and
-// dk only, the high one.
+// Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand (the product of two low
+// ones left out); what reaches dq and dk only, the high one.
 
 #include "gdelta_tc.cuh"
 
@@ -355,13 +360,13 @@ __device__ __forceinline__ void back_chain(const CUtensorMap &map_k, const CUten
         const uint32_t c16 = (d & 63) >> 3, col = (d >> 6) * kTile + (d & 7) * 2;
         const bool live = d < dv;
         const bool first = tid == 32 * kBringer;
-        // (one iteration more for the last state; a warp that gave up waiting still meets the others at their barriers)
+        // (a warp that gave up waiting still meets the others at their barriers)
         bool ok = true;
 #pragma unroll 1
-        for (int n = 0; n <= nch; ++n) {
+        for (int n = 0; n < nch; ++n) {
             const int c = chunk(n);
             const uint32_t st = s0 + (n & 1) * Cfg::kStage;
-            if (!REV && n < nch) {
+            if (!REV) {
                 // V's column (0 past the sequence's end, where TMA fills up), once the last chunk's is used
                 if (ok) ok = waitw(BBAR(full, n & 1), (n >> 1) & 1);
                 if (ok && n > 0) ok = waitw(BBAR(got_r, 0), (n - 1) & 1) && waitw(BBAR(got_r, 1), (n - 1) & 1);
@@ -416,7 +421,7 @@ __device__ __forceinline__ void back_chain(const CUtensorMap &map_k, const CUten
             }
             named_barrier_sync(2, 32 * kHelpers);
             if (first && ok) {
-                bulk_store((REV ? args.dS : args.S) + (bh * (nch + 1) + (REV ? c + 1 : c)) * (2 * kStateImg<KD>), s0 + Cfg::kOutS,
+                bulk_store((REV ? args.dS : args.S) + (bh * nch + c) * (2 * kStateImg<KD>), s0 + Cfg::kOutS,
                            2 * kStateImg<KD>);
                 tma_store_commit();
             }
@@ -570,21 +575,28 @@ constexpr int kGComp = 8, kGIssuer = 8, kGLoader = 9, kGThreads = 320;
 template <int KD>
 struct GradCfg {
     static constexpr uint32_t kTK = KD / 64 * kTile;
-    // Q, K, dY, V, E and N (two parts each), S (two parts; then dS's high one in place of the low one), dP, dL, the gates (two)
-    static constexpr uint32_t kQ = 0, kK = kTK, kY = 2 * kTK, kV = kY + 2 * kTile, kE = kV + 2 * kTile, kN = kE + kTokImg,
-                              kS = kN + kTokImg, kP = kS + 2 * kStateImg<KD>, kL = kP + kTile, kGates = kL + kTile,
+    // Q, K, dY, E's high part and (two buffers, in turn) its low one, N (two parts), S (two parts; then dS's low and high one in
+    // their place), dP, dL, the gates (two)
+    static constexpr uint32_t kQ = 0, kK = kTK, kY = 2 * kTK, kE = kY + 2 * kTile, kEl = kE + kImg, kN = kEl + 2 * kImg, kS = kN + kTokImg,
+                              kP = kS + 2 * kStateImg<KD>, kL = kP + kTile, kGates = kL + kTile,
                               kSmall = kGates + 2 * kGateStep;
 };
-// TMEM columns: Q K^T, dY E^T, N E^T, V N^T (then dP K and dP^T Q + dL K + dL^T K), dY S^T (then E dS^T), N S^T
-constexpr uint32_t kgP = 0, kgYE = 64, kgNE = 128, kgVN = 192, kgQ = 0, kgK = 128, kgYS = 256, kgNS = 384;
+// TMEM columns: Q K^T, dY E^T, N E^T, K K^T (then dP K and dP^T Q + dL K + dL^T K), dY S^T (then E dS^T), N S^T
+constexpr uint32_t kgP = 0, kgYE = 64, kgNE = 128, kgKK = 192, kgQ = 0, kgK = 128, kgYS = 256, kgNS = 384;
 struct alignas(16) GSmall {
-    uint64_t full[3];              // Q, K, dY, V, E, N; S; dS
+    uint64_t full[3];              // Q, K, dY, E, N; S; dS
     uint64_t got_p, got_x, got_e;  // dP and dL are in shared memory; dY S^T and S have been read; all accumulators have
     uint64_t doneG, doneS, doneQ, doneF;
     uint64_t fin;
     uint32_t tmem_base;
     int abort_flag;
-    float dG[2][kC], diag[kC], anchor[kGComp];
+    // of even and odd chunks (the first warp sums one chunk's up while the others are at the next)
+    struct {
+        // F over the chunk's own tokens, by blocks of 16 columns: every row's sum; per 16 rows s, for every column t, the sum of
+        // F_sj over s >= t and the block's j < t.  F_s,-1 and F_Cj by halves of the state's rows.
+        float row[4][kC], part[4][kC], head[2][kC], tail[2][kC];
+        float diag[kC], anchor[kGComp];
+    } sums[2];
 };
 #define GBAR(name, i) (sS + (uint32_t)offsetof(GSmall, name) + 8 * (uint32_t)(i))
 template <int KD>
@@ -594,8 +606,7 @@ static_assert(kGSmemBytes<128> <= 232448, "shared memory budget");
 template <int KD, bool OUT32>
 __global__ void __launch_bounds__(kGThreads, 1)
 gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dy,
-                   const __grid_constant__ GdeltaTcBackArgs args, int total)
+                   const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ GdeltaTcBackArgs args, int total)
 {
     using Cfg = GradCfg<KD>;
     extern __shared__ uint8_t smem_raw[];
@@ -639,33 +650,29 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int h = (int)(bh % H), b = (int)(bh / H), kh = b * args.s.Hk + h / (H / args.s.Hk);
                 const uint8_t *w = args.ws + (((size_t)b * nch + c) * H + h) * kWsChunkB;
                 const uint8_t *E = args.E + (bh * nch + c) * kTokImg, *N = args.N + (bh * nch + c) * kTokImg,
-                              *S = args.S + (bh * (nch + 1) + c) * (2 * kStateImg<KD>);
+                              *S = args.S + (bh * nch + c) * (2 * kStateImg<KD>);
                 const uint32_t f0 = GBAR(full, 0), f1 = GBAR(full, 1);
                 if (i > 0 && !wait1(GBAR(got_x, 0), ph)) break;
                 if (load) {
-                    bar_expect(f0, 2 * Cfg::kTK + 2 * (dv / 64) * kTile + 2 * kTokImg + kGateBytesB);
+                    bar_expect(f0, 2 * Cfg::kTK + dv / 64 * kTile + 2 * kTokImg + kGateBytesB);
                     bar_expect(f1, 2 * kStateImg<KD>);
                     started = true;
                 }
                 if (i > 0) {
-                    const int p = item(i - 1);
-                    bar_expect(GBAR(full, 2), kStateImg<KD>);
-                    bulk_copy(s0 + Cfg::kS + kStateImg<KD>, args.dS + ((size_t)(p / nch) * (nch + 1) + p % nch + 1) * (2 * kStateImg<KD>),
-                              kStateImg<KD>, GBAR(full, 2));
+                    const uint8_t *dS = args.dS + (size_t)item(i - 1) * (2 * kStateImg<KD>);
+                    bar_expect(GBAR(full, 2), 2 * kStateImg<KD>);
+                    bulk_copy(s0 + Cfg::kS + kStateImg<KD>, dS, kStateImg<KD>, GBAR(full, 2));
+                    bulk_copy(s0 + Cfg::kS, dS + kStateImg<KD>, kStateImg<KD>, GBAR(full, 2));
                 }
                 if (load) {
                     bulk_copy(s0 + Cfg::kGates + (i & 1) * kGateStep, w + kWsGates, kGateBytesB, f0);
 #pragma unroll 1
-                    for (int x = 0; x < dv / 64; ++x) {
-                        tma_load(s0 + Cfg::kY + x * kTile, &map_dy, f0, 64 * x, c * kC, (int)bh);
-                        tma_load(s0 + Cfg::kV + x * kTile, &map_v, f0, 64 * x, c * kC, (int)bh);
-                    }
-                    bulk_copy(s0 + Cfg::kE + kImg, E + kImg, kImg, f0);
+                    for (int x = 0; x < dv / 64; ++x) tma_load(s0 + Cfg::kY + x * kTile, &map_dy, f0, 64 * x, c * kC, (int)bh);
+                    bulk_copy(s0 + Cfg::kEl + (i & 1) * kImg, E + kImg, kImg, f0);
                     bulk_copy(s0 + Cfg::kN, N, kTokImg, f0);
-                    bulk_copy(s0 + Cfg::kS, S, kStateImg<KD>, f1);
                     // what has to wait for its buffer comes into L2 meanwhile
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(E), "r"(kImg) : "memory");
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S + kStateImg<KD>), "r"(kStateImg<KD>) : "memory");
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "r"(2 * kStateImg<KD>) : "memory");
                 }
                 if (i > 0 && !wait1(GBAR(doneQ, 0), ph)) break;
                 if (load) {
@@ -678,7 +685,7 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (i > 0 && !wait1(GBAR(doneF, 0), ph)) break;
                 if (load) {
                     bulk_copy(s0 + Cfg::kE, E, kImg, f0);
-                    bulk_copy(s0 + Cfg::kS + kStateImg<KD>, S + kStateImg<KD>, kStateImg<KD>, f1);
+                    bulk_copy(s0 + Cfg::kS, S, 2 * kStateImg<KD>, f1);
                     // (a last chunk's loads have landed when its products are done)
                     started = false;
                 }
@@ -693,28 +700,27 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             constexpr uint32_t M = 64;
             const int nk = dv / 16;
             const uint32_t qk = desc_lo(s0 + Cfg::kQ, 16), kk_ = desc_lo(s0 + Cfg::kK, 16), y = desc_lo(s0 + Cfg::kY, 16),
-                           v = desc_lo(s0 + Cfg::kV, 16), e = desc_lo(s0 + Cfg::kE, kImg), nn = desc_lo(s0 + Cfg::kN, kImg),
-                           S = desc_lo(s0 + Cfg::kS, kImg);
-            constexpr uint32_t kLo = kImg >> 4, kMn = 2048 >> 4;
+                           e = desc_lo(s0 + Cfg::kE, kImg), nn = desc_lo(s0 + Cfg::kN, kImg), S = desc_lo(s0 + Cfg::kS, kImg);
+            constexpr uint32_t kLo = kImg >> 4, kLoS = kStateImg<KD> >> 4, kMn = 2048 >> 4;
             auto kmaj = [&](int k) { return (uint32_t)((k >> 2) * (kTile >> 4) + (k & 3) * 2); };
 #pragma unroll 1
             for (int i = 0; i < nit; ++i) {
-                const uint32_t ph = i & 1;
+                const uint32_t ph = i & 1, el = desc_lo(s0 + Cfg::kEl + ph * kImg, kImg);
                 if (!wait1(GBAR(full, 0), ph) || (i > 0 && !wait1(GBAR(got_e, 0), ph ^ 1))) break;
                 tc_fence_after();
 #pragma unroll 2
-                for (int k = 0; k < KD / 16; ++k)
+                for (int k = 0; k < KD / 16; ++k) {
                     mma_ss(kgP, qk + kmaj(k), kHi128, kk_ + kmaj(k), kHi128, idesc_bf16_f32(M, 64, false, false), k > 0);
+                    mma_ss(kgKK, kk_ + kmaj(k), kHi128, kk_ + kmaj(k), kHi128, idesc_bf16_f32(M, 64, false, false), k > 0);
+                }
 #pragma unroll 1
                 for (int k = 0; k < nk; ++k) {
                     constexpr uint32_t idK = idesc_bf16_f32(M, 64, false, true), idM = idesc_bf16_f32(M, 64, true, true);
                     const uint32_t o = k * kMn, ok = kmaj(k);
                     mma_ss(kgYE, y + ok, kHi128, e + o, kHi128, idK, k > 0);
                     mma_ss(kgNE, nn + o, kHi128, e + o, kHi128, idM, k > 0);
-                    mma_ss(kgVN, v + ok, kHi128, nn + o, kHi128, idK, k > 0);
-                    mma_ss(kgYE, y + ok, kHi128, e + kLo + o, kHi128, idK, true);
-                    mma_ss(kgNE, nn + o, kHi128, e + kLo + o, kHi128, idM, true);
-                    mma_ss(kgVN, v + ok, kHi128, nn + kLo + o, kHi128, idK, true);
+                    mma_ss(kgYE, y + ok, kHi128, el + o, kHi128, idK, true);
+                    mma_ss(kgNE, nn + o, kHi128, el + o, kHi128, idM, true);
                     mma_ss(kgNE, nn + kLo + o, kHi128, e + o, kHi128, idM, true);
                 }
                 bar_commit(GBAR(doneG, 0));
@@ -726,7 +732,9 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     const uint32_t o = k * kMn, ok = kmaj(k);
                     mma_ss(kgYS, y + ok, kHi128, S + o, kHi128, idK, k > 0);
                     mma_ss(kgNS, nn + o, kHi128, S + o, kHi128, idM, k > 0);
-                    mma_ss(kgYS, y + ok, kHi128, S + (kStateImg<KD> >> 4) + o, kHi128, idK, true);
+                    mma_ss(kgYS, y + ok, kHi128, S + kLoS + o, kHi128, idK, true);
+                    mma_ss(kgNS, nn + o, kHi128, S + kLoS + o, kHi128, idM, true);
+                    mma_ss(kgNS, nn + kLo + o, kHi128, S + o, kHi128, idM, true);
                 }
                 bar_commit(GBAR(doneS, 0));
                 if (!wait1(GBAR(got_p, 0), ph)) break;
@@ -744,13 +752,17 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                 }
                 bar_commit(GBAR(doneQ, 0));
-                if (!wait1(GBAR(full, 2), ph)) break;          // (dS was loaded once dY S^T had been read)
+                if (!wait1(GBAR(full, 2), ph)) break;          // (dS was loaded once S had been read)
                 tc_fence_after();
                 {
                     constexpr uint32_t idM = idesc_bf16_f32(M, KD, true, true);
-                    const uint32_t dS = desc_lo(s0 + Cfg::kS + kStateImg<KD>, kImg);
 #pragma unroll 2
-                    for (int k = 0; k < nk; ++k) mma_ss(kgYS, e + k * kMn, kHi128, dS + k * kMn, kHi128, idM, k > 0);
+                    for (int k = 0; k < nk; ++k) {                 // dS's high part is in the low one's place
+                        const uint32_t o = k * kMn;
+                        mma_ss(kgYS, e + o, kHi128, S + kLoS + o, kHi128, idM, k > 0);
+                        mma_ss(kgYS, e + o, kHi128, S + o, kHi128, idM, true);
+                        mma_ss(kgYS, el + o, kHi128, S + kLoS + o, kHi128, idM, true);
+                    }
                 }
                 bar_commit(GBAR(doneF, 0));
             }
@@ -764,42 +776,47 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t tq = (uint32_t)(32 * q4) << 16;
         const float scale = args.scale;
         bool ok = true;
+        // log2 e^G of a token (no gate below kLeastGate), less another's
+        auto log_from = [&](uint32_t gates, int i, float Gh, float Gl) {
+            return (ldsf(gates + kGateLog + 8 * i) - Gh) + (ldsf(gates + kGateLog + 8 * i + 4) - Gl);
+        };
         // (a warp that gave up waiting still meets the others at their barrier)
 #pragma unroll 1
         for (int it = 0; it < nit; ++it) {
             const uint32_t ph = it & 1, gates = s0 + Cfg::kGates + (it & 1) * kGateStep;
             const int c = item(it) % nch;
             const size_t bh = item(it) / nch;
+            auto &sums = sm->sums[it & 1];
             float x[KD / 4];                 // scale e^G dY S^T: columns KD / 2 gq + 32 p + 16 hl + u
+            uint32_t kw[KD / 8];             // K's there
             ok = ok && waitw(GBAR(full, 0), ph) && waitw(GBAR(doneG, 0), ph);
-            float eG = 0.f, eR = 0.f, be = 0.f, acc = 0.f;
+            float eG = 0.f, eR = 0.f, be = 0.f, Gh = 0.f, Gl = 0.f;
             if (ok) {
                 tc_fence_after();
                 eG = ldsf(gates + 4 * i), eR = ldsf(gates + 4 * kC + 4 * i), be = ldsf(gates + 8 * kC + 4 * i);
-                const float Gh = ldsf(gates + kGateLog + 8 * i), Gl = ldsf(gates + kGateLog + 8 * i + 4);
-                float P[16], YE[16], NE[16], VN[16];
+                Gh = ldsf(gates + kGateLog + 8 * i), Gl = ldsf(gates + kGateLog + 8 * i + 4);
+                const float closed = ldsf(gates + kGateClosed + 4 * i);
+                float P[16], YE[16], NE[16], F[16];
                 tc_ld_16x32bx2_x16<16>(tq + kgP + 32 * gq, P);
                 tc_ld_16x32bx2_x16<16>(tq + kgYE + 32 * gq, YE);
                 tc_ld_16x32bx2_x16<16>(tq + kgNE + 32 * gq, NE);
-                tc_ld_16x32bx2_x16<16>(tq + kgVN + 32 * gq, VN);
+                tc_ld_16x32bx2_x16<16>(tq + kgKK + 32 * gq, F);
                 wait_loaded(P);
                 wait_loaded(YE);
                 wait_loaded(NE);
-                wait_loaded(VN);
+                wait_loaded(F);
                 const int j0 = 32 * gq + 16 * hl;
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
                     const int j = j0 + u;
                     const float bj = ldsf(gates + 8 * kC + 4 * j);
-                    const float dec = ex2((Gh - ldsf(gates + kGateLog + 8 * j)) + (Gl - ldsf(gates + kGateLog + 8 * j + 4)));
-                    const float dA = scale * bj * YE[u];
-                    if (j == i) {
-                        acc -= VN[u];
-                        sm->diag[i] = NE[u];
-                    }
-                    if (j <= i) acc = fmaf(dec * P[u], dA, acc);
-                    P[u] = j <= i ? dec * dA : 0.f;
-                    NE[u] = j < i ? -bj * dec * NE[u] : 0.f;
+                    const float dec = ex2(-log_from(gates, j, Gh, Gl));
+                    const bool open = closed == ldsf(gates + kGateClosed + 4 * j);      // (no gate of about 0 in between)
+                    const float dA = scale * bj * YE[u], L = -bj * NE[u];
+                    if (j == i) sums.diag[i] = NE[u];
+                    F[u] = j < i ? dec * fmaf(P[u], dA, F[u] * L) : 0.f;
+                    P[u] = j <= i && open ? dec * dA : 0.f;
+                    NE[u] = j < i && open ? dec * L : 0.f;
                 }
                 const uint32_t o = s0 + sw128_offset(i, j0 >> 3), o2 = s0 + sw128_offset(i, (j0 >> 3) + 1);
                 const uint4 p0 = pack8(P), p1 = pack8(P + 8), l0 = pack8(NE), l1 = pack8(NE + 8);
@@ -810,11 +827,31 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 fence_proxy_async_smem();
                 tc_fence_before();
                 bar_arrive_warp(GBAR(got_p, 0));
+                // F over the columns before each one of its block, over the rows from that one on: summed over the 16 lanes of the
+                // rows, lane l ends with column l
+                float run = 0.f;
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const float f = F[u];
+                    F[u] = j0 + u <= i ? run : 0.f;
+                    run += f;
+                }
+                sums.row[2 * gq + hl][i] = run;
+#pragma unroll
+                for (int w = 8; w; w >>= 1) {
+                    const bool up = lane & w;
+#pragma unroll
+                    for (int z = 0; z < w; ++z) {
+                        const float keep = up ? F[z + w] : F[z], give = up ? F[z] : F[z + w];
+                        F[z] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+                    }
+                }
+                sums.part[q4][j0 + (lane & 15)] = F[0];
             }
             ok = ok && waitw(GBAR(full, 1), ph);
             if (ok) {
-                // <S, dS> before the chunk: both are images of the same layout, so any order does
-                const uint4 *ds = reinterpret_cast<const uint4 *>(args.dS + (bh * (nch + 1) + c) * (2 * kStateImg<KD>));
+                // <S, dS>: both are images of the same layout, so any order does
+                const uint4 *ds = reinterpret_cast<const uint4 *>(args.dS + (bh * nch + c) * (2 * kStateImg<KD>));
                 constexpr int kWords = kStateImg<KD> / 16, kRow = KD / 64 * 8;    // (rows behind dv hold nothing)
                 float2 dot = make_float2(0.f, 0.f);
 #pragma unroll 4
@@ -829,67 +866,48 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 float p = dot.x + dot.y;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-                if (lane == 0) sm->anchor[warp] = p;
+                if (lane == 0) sums.anchor[warp] = p;
             }
             ok = ok && waitw(GBAR(doneS, 0), ph);
             if (ok) {
                 tc_fence_after();
                 const float f = scale * eG;
+                float qs = 0.f, ks = 0.f;
 #pragma unroll
                 for (int p = 0; p < KD / 64; ++p) {
                     const int c0 = KD / 2 * gq + 32 * p;
-                    float t[16];
+                    float t[16], ns[16];
                     tc_ld_16x32bx2_x16<16>(tq + kgYS + c0, t);
+                    tc_ld_16x32bx2_x16<16>(tq + kgNS + c0, ns);
                     wait_loaded(t);
+                    wait_loaded(ns);
                     const int cc = c0 + 16 * hl;
-                    const uint32_t qa = s0 + Cfg::kQ + (cc >> 6) * kTile;
-                    const uint4 q0 = lds4(qa + sw128_offset(i, (cc & 63) >> 3)), q1 = lds4(qa + sw128_offset(i, ((cc & 63) >> 3) + 1));
-                    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    const uint32_t qa = s0 + Cfg::kQ + (cc >> 6) * kTile, o0 = sw128_offset(i, (cc & 63) >> 3), o1 = sw128_offset(i, ((cc & 63) >> 3) + 1);
+                    const uint4 q0 = lds4(qa + o0), q1 = lds4(qa + o1), k0 = lds4(qa + Cfg::kK + o0), k1 = lds4(qa + Cfg::kK + o1);
+                    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w}, kv[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         x[16 * p + 2 * u] = f * t[2 * u];
                         x[16 * p + 2 * u + 1] = f * t[2 * u + 1];
-                        acc = fmaf(bf16_lo(qw[u]), x[16 * p + 2 * u], acc);
-                        acc = fmaf(bf16_hi(qw[u]), x[16 * p + 2 * u + 1], acc);
+                        qs = fmaf(bf16_lo(qw[u]), t[2 * u], fmaf(bf16_hi(qw[u]), t[2 * u + 1], qs));
+                        ks = fmaf(bf16_lo(kv[u]), ns[2 * u], fmaf(bf16_hi(kv[u]), ns[2 * u + 1], ks));
+                        kw[8 * p + u] = kv[u];
                     }
                 }
                 tc_fence_before();
                 bar_arrive_warp(GBAR(got_x, 0));
-                acc += __shfl_xor_sync(0xffffffffu, acc, 16);
-                if (hl == 0) sm->dG[gq][i] = acc;
+                float head = fmaf(scale, qs, -ks);
+                head += __shfl_xor_sync(0xffffffffu, head, 16);
+                if (hl == 0) sums.head[gq][i] = ex2(Gh + Gl) * head;
             }
-            named_barrier_sync(1, 32 * kGComp);
             const int t0 = c * kC;
-            if (ok && warp == 0) {
-                // dlog alpha: <S, dS> before the chunk, less the terms of the tokens before each one
-                const int a0 = 2 * lane;
-                const float d0 = sm->dG[0][a0] + sm->dG[1][a0], d1 = sm->dG[0][a0 + 1] + sm->dG[1][a0 + 1];
-                float inc = d0 + d1;         // up to this lane
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                float anchor = 0.f;
-                for (int w = 0; w < kGComp; ++w) anchor += sm->anchor[w];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = t0 + a0 + u;
-                    if (t >= T) continue;
-                    const size_t at = bh * T + t;
-                    if (args.dalpha && args.s.alpha) {
-                        const float al = args.s.alpha[at];
-                        args.dalpha[at] = al > 0.f ? (anchor - (u ? inc - d1 : inc - d0 - d1)) / al : 0.f;
-                    }
-                    if (args.dbeta) args.dbeta[at] = sm->diag[a0 + u] / ldsf(gates + 8 * kC + 4 * (a0 + u));
-                }
-            }
             ok = ok && waitw(GBAR(doneQ, 0), ph) && waitw(GBAR(doneF, 0), ph);
             if (ok) {
                 tc_fence_after();
                 const size_t row = (bh * T + t0 + i) * KD;
                 const bool in = t0 + i < T;
                 const float fe = be * eR;
+                float tail = 0.f;
 #pragma unroll
                 for (int p = 0; p < KD / 64; ++p) {
                     const int c0 = KD / 2 * gq + 32 * p;
@@ -908,6 +926,8 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
 #pragma unroll
                     for (int u = 0; u < 16; ++u) {
+                        const uint32_t k2 = kw[8 * p + u / 2];
+                        tail = fmaf(u & 1 ? bf16_hi(k2) : bf16_lo(k2), ed[u], tail);
                         a[u] += x[16 * p + u];
                         k3[u] = fmaf(fe, ed[u], fmaf(-eG, ns[u], k3[u]));
                     }
@@ -927,6 +947,62 @@ gdelta_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             }
                         }
                     }
+                }
+                tail += __shfl_xor_sync(0xffffffffu, tail, 16);
+                if (hl == 0) sums.tail[gq][i] = be * ex2(log_from(gates, kC - 1, Gh, Gl)) * tail;
+            }
+            named_barrier_sync(1, 32 * kGComp);
+            if (ok && warp == 0) {
+                // alpha_t dalpha_t, two tokens per lane: F over the rows from each one on, of the state before the chunk and of the blocks of
+                // columns before the token's own (suffix sums, one per block), of its own block, and of the gradient behind the chunk
+                const int a0 = 2 * lane, bt = lane >> 3;
+                float h[2], sfx[4], own0 = 0.f, own1 = 0.f, behind = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) h[u] = sums.head[0][a0 + u] + sums.head[1][a0 + u];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (b == bt) own0 = h[0], own1 = h[1];
+                    sfx[b] = h[0] + h[1];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) h[u] += sums.row[b][a0 + u];
+                }
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const float y = __shfl_down_sync(0xffffffffu, sfx[b], o);
+                        if (lane + o < 32) sfx[b] += y;
+                    }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const float y = __shfl_down_sync(0xffffffffu, sfx[b], 1);
+                    if (b == bt && lane < 31) behind = y;
+                }
+                const float c0 = sums.tail[0][a0] + sums.tail[1][a0], c1 = sums.tail[0][a0 + 1] + sums.tail[1][a0 + 1];
+                float last = c0 + c1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, last, o);
+                    if (lane >= o) last += y;
+                }
+                last = __shfl_up_sync(0xffffffffu, last, 1);
+                if (lane == 0) last = 0.f;
+                float anchor = 0.f;
+                for (int w = 0; w < kGComp; ++w) anchor += sums.anchor[w];
+                last = fmaf(ex2(log_from(gates, kC - 1, 0.f, 0.f)), anchor, last);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = t0 + a0 + u;
+                    if (t >= T) continue;
+                    const size_t at = bh * T + t;
+                    if (args.dalpha && args.s.alpha) {
+                        float d = (u ? behind + own1 : behind + own1 + own0) + (u ? last + c0 : last);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) d += sums.part[w][a0 + u];
+                        const float al = args.s.alpha[at];
+                        args.dalpha[at] = al > 0.f ? d / fmaxf(al, kLeastGate) : 0.f;
+                    }
+                    if (args.dbeta) args.dbeta[at] = sums.diag[a0 + u] / ldsf(gates + 8 * kC + 4 * (a0 + u));
                 }
             }
         }
@@ -954,8 +1030,8 @@ BackSpace back_space(const GdeltaShape &s)
     p.E = p.ws + heads * nch * kWsChunkB;
     p.N = p.E + heads * nch * kTokImg;
     p.S = p.N + heads * nch * kTokImg;
-    p.dS = p.S + heads * (nch + 1) * 2 * state;
-    p.dq = p.dS + heads * (nch + 1) * 2 * state;
+    p.dS = p.S + heads * nch * 2 * state;
+    p.dq = p.dS + heads * nch * 2 * state;
     const size_t part = s.Hk < s.H ? round_up(heads * s.T * s.r * sizeof(float)) : 0;
     p.dk = p.dq + part;
     p.bytes = p.dk + part;
@@ -976,7 +1052,7 @@ cudaError_t launch_as(const GdeltaTcBackMaps &m, GdeltaTcBackArgs a, const Gdelt
         return e;
     const unsigned grid = sms > 0 && (unsigned)sms < chunks ? sms : chunks;
     return launch_after(a.s.Hk < a.s.H ? gdelta_grad_kernel<KD, true> : gdelta_grad_kernel<KD, false>, grid, kGThreads, kGSmemBytes<KD>, stream,
-                        m.q, m.k, m.v, m.dy, a, (int)chunks);
+                        m.q, m.k, m.dy, a, (int)chunks);
 }
 
 }  // namespace

@@ -315,9 +315,13 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         if (BACK) {
             reinterpret_cast<float2 *>(expG)[lane] = make_float2(before * al[0], before * al[0] * al[1]);
             // G itself in 64 bits, kept as two FP32 parts: differences over a few tokens stay exact to FP32 behind gates near 0.
-            // A gate of 0 counts as 2^-400, which every exponential takes to 0.
-            const double l0 = al[0] > 0.f ? (double)log2f(al[0]) : -400.0, l1 = al[1] > 0.f ? (double)log2f(al[1]) : -400.0;
+            // Gates below kLeastGate count as that there, and how many there are is kept beside: what they scale is 0.
+            const double l0 = log2f(fmaxf(al[0], kLeastGate)), l1 = log2f(fmaxf(al[1], kLeastGate));
             double inc = l0 + l1;
+            const uint32_t c0 = __ballot_sync(0xffffffffu, al[0] < kLeastGate), c1 = __ballot_sync(0xffffffffu, al[1] < kLeastGate);
+            const uint32_t up = 0xffffffffu >> (31 - lane);
+            reinterpret_cast<float2 *>(wsc + kWsGates + kGateClosed)[lane] = make_float2(__popc(c0 & up) + __popc(c1 & (up >> 1)),
+                                                                                        __popc(c0 & up) + __popc(c1 & up));
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const double y = __shfl_up_sync(0xffffffffu, inc, o);

@@ -16,11 +16,12 @@ constexpr uint32_t kHi128 = desc_hi(1024, 2);   // SBO and swizzle of 128-byte r
 constexpr uint32_t kTile = kC * 128;            // 8 KB: 64 rows of 64 BF16
 // workspace per chunk and head: A, X's high and low parts (BF16 shared-memory images), then 64 floats each of e^G, e^{G_C - G}
 // and beta.  For the gradients also A's low part and scale e^G Q (two parts of up to two blocks of 64 features), and behind the gates
-// log2 e^G as pairs of a high and a low FP32 part and the true beta over the one used.
+// log2 e^G as pairs of a high and a low FP32 part (no gate below kLeastGate), the true beta over the one used, and how many gates up to
+// the token are below kLeastGate.
 constexpr uint32_t kWsA = 0, kWsX = kTile, kWsGates = 3 * kTile, kWsChunk = kWsGates + 1024;
 constexpr uint32_t kWsAl = kWsGates + 2048, kWsQ = kWsAl + kTile, kWsChunkB = kWsQ + 4 * kTile;
-constexpr uint32_t kGateBytes = 3 * kC * 4, kGateBytesB = 6 * kC * 4;
-constexpr uint32_t kGateLog = 3 * kC * 4, kGateRatio = 5 * kC * 4;
+constexpr uint32_t kGateBytes = 3 * kC * 4, kGateBytesB = 7 * kC * 4;
+constexpr uint32_t kGateLog = 3 * kC * 4, kGateRatio = 5 * kC * 4, kGateClosed = 6 * kC * 4;
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
 {

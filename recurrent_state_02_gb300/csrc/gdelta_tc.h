@@ -41,8 +41,7 @@ struct GdeltaTcBackArgs {
     uint16_t *dv_out = nullptr;
     void *dq = nullptr, *dk = nullptr;      // BF16 [B,H,T,r], or FP32 where key heads are shared
     float scale = 1.f;
-    // per chunk and head: prep's images and gates; E and N (two parts); the states between the chunks and their gradients
-    // (two parts), one more per head
+    // per chunk and head: prep's images and gates; E and N (two parts); the state before it and the gradient behind it (two parts)
     uint8_t *ws = nullptr, *E = nullptr, *N = nullptr, *S = nullptr, *dS = nullptr;
 };
 size_t gdelta_tc_backward_bytes(const GdeltaShape &s);

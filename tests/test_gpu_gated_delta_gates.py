@@ -12,10 +12,9 @@ import pytest
 import torch
 
 import gdelta_reference as R
-from test_gpu_gated_delta import ids, la, make  # noqa: F401  (la: the fixture)
+from test_gpu_gated_delta import DTYPES, ids, la, make  # noqa: F401  (la: the fixture)
 
 pytestmark = pytest.mark.gpu
-DTYPES = pytest.mark.parametrize("dtype", [torch.float32], ids=["fp32"])
 
 
 def sizes_and_gradient(q, k, v, dy, alpha, beta, S0, dS_T, scale):
