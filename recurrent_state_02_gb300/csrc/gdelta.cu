@@ -908,6 +908,7 @@ int gdelta_rec_segments(int B, int H, int T, int r, int dv, int sms)
 {
     const long long ctas = (long long)B * H * ((dv + kRecCols - 1) / kRecCols + (r + kRecCols - 1) / kRecCols);
     const double token = r <= 64 ? 0.101 : r <= 128 ? 0.157 : 0.23, join = r <= 64 ? 1.6 + r / 40.0 : (1.6 + r / 64.0) * ((r + 31) / 32);
+    if (T == 0) return 1;
     int best = 1;
     double least = T * token;
     for (int n = 2; n <= 16 && n * ctas <= sms + sms / 8; ++n) {
