@@ -10,8 +10,9 @@ namespace {
 // In the earlier kernel: the next one may be placed once every CTA has been here (or has ended).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// In the later one, before it reads or writes any global memory: the earlier kernel has ended and what it wrote is visible.  An
-// earlier kernel that has waited here itself has seen the one before it end.  Nothing after an ordinary launch.
+// In the later one, before it reads what the earlier kernel writes or writes what that one reads or writes: it has ended here, and what it
+// wrote is visible.  (What neither touches may come before: inputs that were ready when the earlier one was launched in the ordinary way,
+// and memory of one's own.)  An earlier kernel that has waited here itself has seen the one before it end.  Nothing after an ordinary launch.
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... P, class... A>
