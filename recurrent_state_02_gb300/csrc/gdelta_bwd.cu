@@ -24,7 +24,7 @@
 // kernels hand one another, the states between the chunks and E and N above all, is what bounds them.  Forming each chunk's
 // gradients inside the chains would spare half of it, but needs both chains at the same chunk.
 // Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand (the product of two low
-// ones left out); what reaches dq and dk only, the high one.
+// ones left out); dP and dL, which reach dq and dk only, are rounded to one.
 
 #include "gdelta_tc.cuh"
 

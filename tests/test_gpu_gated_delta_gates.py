@@ -135,6 +135,25 @@ def test_small_gate_against_differences(la, dtype):  # noqa: F811
     assert slope.abs().max() > 4 * 2.0 ** -18 * scale          # (there is a slope to find)
 
 
+@DTYPES
+def test_gradients_that_nobody_wants(la, dtype):  # noqa: F811
+    """Without room for dalpha or dbeta the C entry forms the others all the same, to the bit."""
+    B, H, Hk, T, r, dv = size = (1, 4, 2, 150, 128, 128)
+    q, k, v, dy, alpha, beta, S0, dS_T = make(*size, dtype, True, 77)
+    want = la.gated_delta_backward(q, k, v, dy, alpha, beta, S0=S0, dS_T=dS_T, scale=0.2)
+    need = la.gated_delta_backward_workspace_bytes(*size, dtype=dtype)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    for left_out in ((3,), (4,), (3, 4)):
+        out = [None if i in left_out else torch.full_like(x, float("nan")) for i, x in enumerate(want)]
+        at = [0 if x is None else x.data_ptr() for x in out]
+        la._call("la_gated_delta_backward", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), 0 if dtype == torch.bfloat16 else 1,
+                 alpha.data_ptr(), beta.data_ptr(), S0.data_ptr(), B, H, Hk, T, r, dv, 0.2, dy.data_ptr(), dS_T.data_ptr(), *at[:3],
+                 at[3] or None, at[4] or None, at[5], ws.data_ptr(), need)
+        assert la.last_device_status() == 0
+        for x, z in zip(out, want):
+            assert x is None or torch.equal(x, z), left_out
+
+
 def test_repeated_calls_and_workspaces(la):  # noqa: F811
     """A workspace full of NaN and a captured call give the same bits."""
     for dtype in (torch.bfloat16, torch.float32):

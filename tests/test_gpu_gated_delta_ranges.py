@@ -203,3 +203,22 @@ def test_long_sequences_in_two_parts(la, size):  # noqa: F811
     ref_y, ref_S, _, _ = R.prefill(*part(cut, T), before, 0.2)
     R.check(S, ref_S, BF, "S", 150)
     R.check(y[:, :, cut:], ref_y, BF, "y", 150)
+
+
+@pytest.mark.parametrize("size", [(1, 4, 2, 500, 128, 128), (2, 2, 2, 333, 64, 64), (1, 2, 2, 300, 128, 64), (1, 2, 1, 260, 64, 128)], ids=ids)
+def test_roundings_of_bf16_results(la, size):  # noqa: F811
+    """The 2-norms of the errors of y, dq, dk and dv in chunks, by counting their roundings.  Rounding to BF16 is off by at most 2^-8 of a value and, spread
+    evenly over a step, by 2^-8 / sqrt(3) in the 2-norm.  y: its own, and S's, or A's and V's, whichever product a term comes from: at most three,
+    together 2^-8.  dq: its own, and dP's: two.  dk: its own, and dP's or dL's: two.  dv: its own.  What goes in two parts adds 2^-16, the sums in FP32
+    less."""
+    T = size[3]
+    q, k, v, dy, alpha, beta, S0, dS_T = make(*size, BF, True, 61)
+    y, S = la.gated_delta_prefill(q, k, v, alpha, beta, S0=S0, scale=0.2)
+    got = la.gated_delta_backward(q, k, v, dy, alpha, beta, S0=S0, dS_T=dS_T, scale=0.2)
+    ref_y, _, _, _ = R.prefill(q, k, v, alpha, beta, S0, 0.2)
+    ref, _ = R.backward(q, k, v, dy, alpha, beta, S0, dS_T, 0.2)
+    rounding = 2.0 ** -8 / 3 ** 0.5
+    for x, z, n, name in ((y, ref_y, 3, "y"), (got[0], ref[0], 2, "dq"), (got[1], ref[1], 2, "dk"), (got[2], ref[2], 1, "dv")):
+        rel = float((R.f64(x) - z).norm() / z.norm())
+        print(f"[roundings] {name} {size}: {rel:.2e} of {n ** 0.5 * rounding + 2.0 ** -15:.2e}")
+        assert rel <= n ** 0.5 * rounding + 2.0 ** -15, (name, rel)
