@@ -16,6 +16,7 @@
 
 #include "gdelta.h"
 #include "launch_after.cuh"
+#include "mma_tf32.cuh"
 #include "sm103_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -92,7 +93,8 @@ constexpr int kRecStageFloats = kRecTok * (3 * 8 * RPL + 4 * kRecCols + 2 + 6);
 // results.  4 r dv FMAs per token and head bound it (FP32 B16 H16 T1001, 128 x 128: 1.0 ms, 33 TFLOP/s of about 75, beside the products
 // of the tokens with one another); few heads are bound by a group's latency, 0.4 us at 64 rows (B2 H4 T1001, 64 x 96: 104 us; 240
 // token by token, the sums of one waiting for the ones before, and the next block's loads for one another; 84 in segments).
-template <int MODE, bool BF16, int RPL>
+// CKPT: the gradients' first two sweeps with a gate, which leave the state (its gradient) at every chunk's border.
+template <int MODE, bool BF16, int RPL, bool CKPT>
 __global__ void __launch_bounds__(kRecThreads)
 gdelta_rec_kernel(const RecArgs a)
 {
@@ -326,8 +328,8 @@ gdelta_rec_kernel(const RecArgs a)
         block_sync();
         for (int n = 0; n < nblk; ++n) {
             float *st = st0 + (n & 1) * kStage;
-            if constexpr (MODE == kFwd || MODE == kRev) {
-                if (a.ckpt && (kBack ? n == 0 || token(n, 0) % kGateC == kGateC - 1 : token(n, 0) % kGateC == 0)) {
+            if constexpr (CKPT) {
+                if (kBack ? n == 0 || token(n, 0) % kGateC == kGateC - 1 : token(n, 0) % kGateC == 0) {
                     float *to = a.ckpt + (bh * ((T + kGateC - 1) / kGateC) + token(n, 0) / kGateC) * s.r * s.dv;
 #pragma unroll
                     for (int m = 0; m < RPL; ++m) {
@@ -478,19 +480,21 @@ gdelta_rec_kernel(const RecArgs a)
         }
 }
 
-template <int MODE, bool BF16, int RPL>
+template <int MODE, bool BF16, int RPL, bool CKPT = false>
 cudaError_t launch_rec_as(const RecArgs &a, cudaStream_t stream)
 {
+    if constexpr (!CKPT && (MODE == kFwd || MODE == kRev))
+        if (a.ckpt) return launch_rec_as<MODE, BF16, RPL, true>(a, stream);
     static OncePerDevice once;
     constexpr uint32_t bytes = 2 * kRecStageFloats<RPL> * 4;
-    const cudaError_t e = set_smem_once(gdelta_rec_kernel<MODE, BF16, RPL>, bytes, once);
+    const cudaError_t e = set_smem_once(gdelta_rec_kernel<MODE, BF16, RPL, CKPT>, bytes, once);
     if (e != cudaSuccess) return e;
     const int cols = MODE == kQue || MODE == kKey ? a.s.r : a.s.dv;
     unsigned slices = (cols + kRecCols - 1) / kRecCols;
     if (a.sums) slices += (a.s.r + kRecCols - 1) / kRecCols;
     const dim3 grid(slices, a.s.H, a.s.B * a.nseg);
-    if (a.nseg > 1 && !a.sums) return launch_after(gdelta_rec_kernel<MODE, BF16, RPL>, grid, kRecThreads, bytes, stream, a);
-    gdelta_rec_kernel<MODE, BF16, RPL><<<grid, kRecThreads, bytes, stream>>>(a);
+    if (a.nseg > 1 && !a.sums) return launch_after(gdelta_rec_kernel<MODE, BF16, RPL, CKPT>, grid, kRecThreads, bytes, stream, a);
+    gdelta_rec_kernel<MODE, BF16, RPL, CKPT><<<grid, kRecThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -623,17 +627,38 @@ gdelta_group_sum_kernel(GdeltaShape s, const float *dq, const float *dk, void *d
 // the state before the chunk stands for a token j = -1 (W_s,-1 = scale q_s . S dy_s - k_s . S dv_s) and the gradient behind it for a token
 // s = 64 (W_64,j = k_j . G v'_j, W_64,-1 = <S, G>).  Every term of the sum has alpha_t as a factor: nothing cancels that is larger than the
 // result by 1 / alpha_t, as the difference of the tokens' q . dq and v . dv would.  Gates below kLeastGate count as that here,
-// zeros too: it is divided out again, and what else they scale is below FP32's rounding.  Three products of 64 tokens with a state and four of the tokens with one another, FP32, in
-// tiles of 64 x 64 with 4 x 4 numbers per thread.
+// zeros too: it is divided out again, and what else they scale is below FP32's rounding.
+//
+// Three products of 64 tokens with a state and four of the tokens with one another, as warp-wide TF32 products of numbers in two parts (one, for
+// BF16 inputs): a warp has 16 rows and 32 columns of a tile of 64 x 64, and the next 16 rows of each operand are in flight meanwhile.
+// Bound by shared memory and the splits' instructions: FP32 B4 H16 T1024, 128 x 128, 279 us of the gradients' 1597 (with FP32 multiply-adds, 4 x 4
+// numbers per thread, 370).  The sweeps that leave the states write 2 r dv FP32 words per chunk and head, 15 us each there.
+constexpr int kGateThreads = 256;
+
+// c += A B for 8 columns and a step of 8.  A1, B1: BF16 numbers, which have no low part.  The tensor cores cut their sums off instead of rounding
+// them, so that a long sum would shrink: every step starts at 0 and is added in FP32.
+template <bool A1, bool B1>
+__device__ __forceinline__ void gate_product(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2], const uint32_t (&bl)[2])
+{
+    float d[4] = {};
+    if (!A1) mma_tf32(d, al, bh[0], bh[1]);
+    if (!B1) mma_tf32(d, ah, bl[0], bl[1]);
+    mma_tf32(d, ah, bh[0], bh[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] += d[i];
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kGateThreads, 2)
 gdelta_gate_kernel(GdeltaShape s, const void *q, const void *k, const void *dy, float scale, const float *e, const float *lam,
                    const float *S, const float *G, float *dalpha)
 {
-    constexpr int C = kGateC, LDW = C + 4, KS = 16;
-    __shared__ __align__(16) float ta[KS][LDW], tb[KS][LDW], tc[KS][LDW], td[KS][LDW];
-    __shared__ float F[C][C + 1], al[C], be[C], as[C], bs[C], part[8];
-    const int nch = (s.T + C - 1) / C, c = blockIdx.x % nch, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    constexpr int C = kGateC, KS = 16, LDR = KS + 4, LDC = C + 8, NL = C * KS / kGateThreads;   // (strides without bank conflicts)
+    __shared__ float ra[C][LDR], rb[C][LDR], rc[C][LDR];      // [token][column]
+    __shared__ float ca[KS][LDC], cb[KS][LDC];                // [state row][value column]
+    __shared__ float F[C][C + 1], al[C], be[C], as[2][C], bs[2][C], part[kGateThreads / 32];
+    const int nch = (s.T + C - 1) / C, c = blockIdx.x % nch, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t4 = lane & 3, row0 = 16 * (warp & 3), half = warp >> 2, col0 = 32 * half;
     const size_t bh = blockIdx.x / nch;
     const size_t key = (bh / s.H * s.Hk + bh % s.H / (s.H / s.Hk)) * s.T + (size_t)c * C, val = bh * s.T + (size_t)c * C;
     const int nt = min(C, s.T - c * C), r = s.r, dv = s.dv;
@@ -642,124 +667,187 @@ gdelta_gate_kernel(GdeltaShape s, const void *q, const void *k, const void *dy, 
         al[tid] = tid < nt ? fmaxf(s.alpha[val + tid], kLeastGate) : 1.f;
         be[tid] = tid < nt && s.beta ? s.beta[val + tid] : 1.f;
     }
-    // 16 columns from u0 on of the chunk's rows of an array of d columns, transposed
-    auto rows_in = [&](float (*to)[LDW], auto elem, size_t first, int d, int u0) {
-        const int u = tid & 15;
+    // a thread's share of 16 columns, from u0 on, of the chunk's rows of an array of d columns
+    const int ru = tid & 15, rt = tid >> 4, cu = tid >> 6, cd = tid & 63;
+    auto rows_at = [&](float (&x)[NL], auto elem, size_t first, int d, int u0) {
 #pragma unroll
-        for (int m = 0; m < C / 16; ++m) {
-            const int t = (tid >> 4) + 16 * m;
-            to[u][t] = t < nt && u0 + u < d ? elem((first + t) * d + u0 + u) : 0.f;
+        for (int m = 0; m < NL; ++m) {
+            const int t = rt + 16 * m;
+            x[m] = t < nt && u0 + ru < d ? elem((first + t) * d + u0 + ru) : 0.f;
         }
+    };
+    auto put_rows = [&](float (*to)[LDR], const float (&x)[NL]) {
+#pragma unroll
+        for (int m = 0; m < NL; ++m) to[rt + 16 * m][ru] = x[m];
     };
     auto q_at = [&](size_t i) { return load_elem<BF16>(q, i); };
     auto k_at = [&](size_t i) { return load_elem<BF16>(k, i); };
     auto dy_at = [&](size_t i) { return load_elem<BF16>(dy, i); };
     auto e_at = [&](size_t i) { return e[i]; };
     auto lam_at = [&](size_t i) { return lam[i]; };
-    auto mul = [&](float (&acc)[4][4], float4 x, float4 y) {
-        const float a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+    // operands of a step of 8: this warp's rows, 8 columns from tokens' rows, 8 columns of a state
+    auto left = [&](const float (*from)[LDR], int k0, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        for (int i = 0; i < 4; ++i) split_tf32_near(from[row0 + g + 8 * (i & 1)][k0 + t4 + 4 * (i >> 1)], hi[i], lo[i]);
     };
-    auto f4 = [](const float *p) { return *reinterpret_cast<const float4 *>(p); };
+    auto right_rows = [&](const float (*from)[LDR], int k0, int n, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_tf32_near(from[col0 + 8 * n + g][k0 + t4 + 4 * i], hi[i], lo[i]);
+    };
+    auto right_state = [&](const float (*from)[LDC], int k0, int n, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_tf32_near(from[k0 + t4 + 4 * i][col0 + 8 * n + g], hi[i], lo[i]);
+    };
     __syncthreads();
 
     // the tokens with the state before the chunk and the gradient behind it
-    float av[4] = {}, bv[4] = {}, anchor = 0.f;
-    for (int d0 = 0; d0 < dv; d0 += C) {
-        float qs[4][4] = {}, ks[4][4] = {}, kg[4][4] = {};
-        for (int u0 = 0; u0 < r; u0 += KS) {
-            rows_in(ta, q_at, key, r, u0);
-            rows_in(tb, k_at, key, r, u0);
+    float av[2] = {}, bv[2] = {}, anchor = 0.f;
+    float n0[NL], n1[NL], n2[NL], n3[NL];
+    const int usteps = (r + KS - 1) / KS, steps = usteps * ((dv + C - 1) / C);
+    auto fetch_states = [&](int i) {
+        const int u0 = i % usteps * KS, d = i / usteps * C + cd;
+        rows_at(n0, q_at, key, r, u0);
+        rows_at(n1, k_at, key, r, u0);
 #pragma unroll
-            for (int m = 0; m < KS / 4; ++m) {
-                const int u = (tid >> 6) + 4 * m, d = tid & 63;
-                const bool in = u0 + u < r && d0 + d < dv;
-                const size_t at = (size_t)(u0 + u) * dv + d0 + d;
-                const float x = in ? Sc[at] : 0.f, y = in ? Gc[at] : 0.f;
-                tc[u][d] = x, td[u][d] = y;
-                anchor = fmaf(x, y, anchor);
+        for (int m = 0; m < NL; ++m) {
+            const int u = u0 + cu + 4 * m;
+            const bool in = u < r && d < dv;
+            const size_t at = (size_t)u * dv + d;
+            n2[m] = in ? Sc[at] : 0.f, n3[m] = in ? Gc[at] : 0.f;
+        }
+    };
+    fetch_states(0);
+    for (int i0 = 0; i0 < steps; i0 += usteps) {
+        float qs[4][4] = {}, ks[4][4] = {}, kg[4][4] = {};
+        for (int i = i0; i < i0 + usteps; ++i) {
+            put_rows(ra, n0);
+            put_rows(rb, n1);
+#pragma unroll
+            for (int m = 0; m < NL; ++m) {
+                ca[cu + 4 * m][cd] = n2[m], cb[cu + 4 * m][cd] = n3[m];
+                anchor = fmaf(n2[m], n3[m], anchor);
             }
             __syncthreads();
-#pragma unroll 4
-            for (int u = 0; u < KS; ++u) {
-                const float4 kr = f4(&tb[u][4 * ty]), sc = f4(&tc[u][4 * tx]);
-                mul(qs, f4(&ta[u][4 * ty]), sc);
-                mul(ks, kr, sc);
-                mul(kg, kr, f4(&td[u][4 * tx]));
+            if (i + 1 < steps) fetch_states(i + 1);
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += 8) {
+                uint32_t qh[4], ql[4], kh[4], kl[4];
+                left(ra, k0, qh, ql);
+                left(rb, k0, kh, kl);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    uint32_t sh[2], sl[2], gh[2], gl[2];
+                    right_state(ca, k0, n, sh, sl);
+                    right_state(cb, k0, n, gh, gl);
+                    gate_product<BF16, false>(qs[n], qh, ql, sh, sl);
+                    gate_product<BF16, false>(ks[n], kh, kl, sh, sl);
+                    gate_product<BF16, false>(kg[n], kh, kl, gh, gl);
+                }
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * ty + i;
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int d = d0 + 4 * tx + j;
-                if (t >= nt || d >= dv) continue;
+                const int t = row0 + g + 8 * (j >> 1), d = i0 / usteps * C + col0 + 8 * n + 2 * t4 + (j & 1);
+                const bool in = t < nt && d < dv;
                 const size_t at = (val + t) * dv + d;
-                av[i] = fmaf(scale * qs[i][j], dy_at(at), fmaf(-be[t] * ks[i][j], lam[at], av[i]));
-                bv[i] = fmaf(be[t] * kg[i][j], e[at], bv[i]);
+                const float y = in ? dy_at(at) : 0.f, l = in ? lam[at] : 0.f, er = in ? e[at] : 0.f;
+                av[j >> 1] = fmaf(scale * qs[n][j], y, fmaf(-be[t] * ks[n][j], l, av[j >> 1]));
+                bv[j >> 1] = fmaf(be[t] * kg[n][j], er, bv[j >> 1]);
             }
-        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int o = 8; o; o >>= 1) {
+        for (int o = 2; o; o >>= 1) {
             av[i] += __shfl_xor_sync(0xffffffffu, av[i], o);
             bv[i] += __shfl_xor_sync(0xffffffffu, bv[i], o);
         }
-        if (tx == 0) as[4 * ty + i] = av[i], bs[4 * ty + i] = bv[i];
+        if (t4 == 0) as[half][row0 + g + 8 * i] = av[i], bs[half][row0 + g + 8 * i] = bv[i];
     }
     anchor = warp_sum(anchor);
-    if ((tid & 31) == 0) part[tid >> 5] = anchor;
+    if (lane == 0) part[warp] = anchor;
 
-    // the tokens with one another
+    // the tokens with one another, where a column of the warp's is not behind all its rows
+    const int blocks = min(4, max(0, (row0 + 16 - col0) / 8));
     float qk[4][4] = {}, kk[4][4] = {}, ye[4][4] = {}, le[4][4] = {};
+    rows_at(n0, q_at, key, r, 0);
+    rows_at(n1, k_at, key, r, 0);
     for (int u0 = 0; u0 < r; u0 += KS) {
-        rows_in(ta, q_at, key, r, u0);
-        rows_in(tb, k_at, key, r, u0);
+        put_rows(ra, n0);
+        put_rows(rb, n1);
         __syncthreads();
-#pragma unroll 4
-        for (int u = 0; u < KS; ++u) {
-            const float4 kj = f4(&tb[u][4 * tx]);
-            mul(qk, f4(&ta[u][4 * ty]), kj);
-            mul(kk, f4(&tb[u][4 * ty]), kj);
+        if (u0 + KS < r) {
+            rows_at(n0, q_at, key, r, u0 + KS);
+            rows_at(n1, k_at, key, r, u0 + KS);
         }
+        if (blocks)
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += 8) {
+                uint32_t qh[4], ql[4], kh[4], kl[4];
+                left(ra, k0, qh, ql);
+                left(rb, k0, kh, kl);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if (n >= blocks) break;
+                    uint32_t jh[2], jl[2];
+                    right_rows(rb, k0, n, jh, jl);
+                    gate_product<BF16, BF16>(qk[n], qh, ql, jh, jl);
+                    gate_product<BF16, BF16>(kk[n], kh, kl, jh, jl);
+                }
+            }
         __syncthreads();
     }
+    rows_at(n0, dy_at, val, dv, 0);
+    rows_at(n1, lam_at, val, dv, 0);
+    rows_at(n2, e_at, val, dv, 0);
     for (int u0 = 0; u0 < dv; u0 += KS) {
-        rows_in(ta, dy_at, val, dv, u0);
-        rows_in(tb, lam_at, val, dv, u0);
-        rows_in(tc, e_at, val, dv, u0);
+        put_rows(ra, n0);
+        put_rows(rb, n1);
+        put_rows(rc, n2);
         __syncthreads();
-#pragma unroll 4
-        for (int u = 0; u < KS; ++u) {
-            const float4 ej = f4(&tc[u][4 * tx]);
-            mul(ye, f4(&ta[u][4 * ty]), ej);
-            mul(le, f4(&tb[u][4 * ty]), ej);
+        if (u0 + KS < dv) {
+            rows_at(n0, dy_at, val, dv, u0 + KS);
+            rows_at(n1, lam_at, val, dv, u0 + KS);
+            rows_at(n2, e_at, val, dv, u0 + KS);
         }
+        if (blocks)
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += 8) {
+                uint32_t yh[4], yl[4], lh[4], ll[4];
+                left(ra, k0, yh, yl);
+                left(rb, k0, lh, ll);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if (n >= blocks) break;
+                    uint32_t eh[2], el[2];
+                    right_rows(rc, k0, n, eh, el);
+                    gate_product<BF16, false>(ye[n], yh, yl, eh, el);
+                    gate_product<false, false>(le[n], lh, ll, eh, el);
+                }
+            }
         __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int t = 4 * ty + i, u = 4 * tx + j;
-            F[t][u] = be[u] * fmaf(scale * qk[i][j], ye[i][j], -be[t] * kk[i][j] * le[i][j]);
+            const int t = row0 + g + 8 * (j >> 1), u = col0 + 8 * n + 2 * t4 + (j & 1);
+            F[t][u] = be[u] * fmaf(scale * qk[n][j], ye[n][j], -be[t] * kk[n][j] * le[n][j]);
         }
     __syncthreads();
     // F, and in its place its sums over j < t; the row of the gradient behind the chunk in bs
     if (tid < C) {
         float m = al[tid];
+#pragma unroll 4
         for (int j = tid - 1; j >= 0; --j) {
             F[tid][j] *= m;
             m *= al[j];
         }
-        float sum = as[tid] * m;
+        float sum = (as[0][tid] + as[1][tid]) * m;
+#pragma unroll 4
         for (int t = 0; t <= tid; ++t) {
             const float f = F[tid][t];
             F[tid][t] = sum;
@@ -767,21 +855,24 @@ gdelta_gate_kernel(GdeltaShape s, const void *q, const void *k, const void *dy, 
         }
     } else if (tid == C) {
         float m = 1.f, sum = 0.f;
+#pragma unroll 4
         for (int j = C - 1; j >= 0; --j) {
-            bs[j] *= m;
+            bs[0][j] = (bs[0][j] + bs[1][j]) * m;
             m *= al[j];
         }
-        for (int w = 0; w < 8; ++w) sum += part[w];
+        for (int w = 0; w < kGateThreads / 32; ++w) sum += part[w];
         sum *= m;
+#pragma unroll 4
         for (int t = 0; t < C; ++t) {
-            const float f = bs[t];
-            bs[t] = sum;
+            const float f = bs[0][t];
+            bs[0][t] = sum;
             sum += f;
         }
     }
     __syncthreads();
     if (tid < nt) {
-        float sum = bs[tid];
+        float sum = bs[0][tid];
+#pragma unroll 4
         for (int t = tid; t < C; ++t) sum += F[t][tid];
         dalpha[val + tid] = s.alpha[val + tid] > 0.f ? sum / al[tid] : 0.f;
     }
@@ -1008,7 +1099,7 @@ cudaError_t launch_gdelta_rec_backward(const GdeltaShape &s, const GdeltaBackwar
     if (g.dbeta) gdelta_beta_kernel<<<(unsigned)((tokens + 7) / 8), 256, 0, stream>>>(s, lam, e, g.dbeta);
     if ((st = launch_gdelta_group_sum(s, dq, w, bf16, g.dq, g.dk, stream)) != cudaSuccess) return st;
     if (gates)
-        (bf16 ? gdelta_gate_kernel<true> : gdelta_gate_kernel<false>)<<<(unsigned)chunks, 256, 0, stream>>>(
+        (bf16 ? gdelta_gate_kernel<true> : gdelta_gate_kernel<false>)<<<(unsigned)chunks, kGateThreads, 0, stream>>>(
             s, g.q, g.k, g.dy, g.scale, e, lam, S, G, g.dalpha);
     return cudaGetLastError();
 }

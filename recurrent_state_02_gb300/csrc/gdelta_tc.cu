@@ -23,6 +23,7 @@
 // state is off by 3e-6 and y by 2.7e-3 (relative 2-norms; the rounding of y alone is 1.7e-3).
 
 #include "gdelta_tc.cuh"
+#include "mma_tf32.cuh"
 
 namespace la {
 namespace {
@@ -152,22 +153,8 @@ struct alignas(16) PSmall {
 };
 constexpr uint32_t kPSmemBytes = kPSmall + sizeof(PSmall) + 1024;
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// x as two TF32 numbers, 11 bits of it and the next 11, cut off: less than 2^-20 of it is lost (X goes on as two BF16 parts, 2^-17)
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo)
-{
-    hi = __float_as_uint(x) & 0xffffe000u;
-    lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
-}
-
 // A warp: c += A B, A 16 x 8 K8 (element (row, k) = a(row, k)), B 8 K8 x 8 N, in FP32 but for the product of the low parts (2^-20
-// of the terms).  c[n][0..3]: rows lane / 4 (+ 8), columns 8 n + 2 (lane % 4) (+ 1) as (row, col), (row, col + 1), (row + 8, ..)
+// of the terms; X goes on as two BF16 parts, 2^-17).  c[n][0..3]: rows lane / 4 (+ 8), columns 8 n + 2 (lane % 4) (+ 1) as (row, col), (row, col + 1), (row + 8, ..)
 template <int K8, int N, class A, class B>
 __device__ __forceinline__ void small_product(float (&c)[N][4], int lane, A a, B b)
 {
