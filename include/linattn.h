@@ -508,7 +508,7 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  *   for one token of la_gated_delta_decode_step a kernel of its own, bound by the state's traffic, when dv is a multiple of 4
  *   and S 16-byte aligned.
  * In the chunked kernels what is derived from the inputs enters the tensor cores as two BF16 parts (16 bits of it) where
- * it reaches an FP32 result, and as one where it reaches a BF16 one only: relative 2-norms of the errors about 3e-6 and 3e-3.
+ * it reaches an FP32 result, and as one where it reaches a BF16 one only: relative 2-norms of the errors about 4e-6 (dalpha and dbeta 7e-6) and 2e-3 to 3e-3.
  * The first call of each kind on a device sets kernel attributes: make it before any stream capture.
  * Requires 1 <= r, dv <= 256, B, H <= 65535, T <= 2^30 and, but for packed sequences, B H (T + 1) <= 2^30; BF16 arrays
  * 2-byte, FP32 and int32 arrays 4-byte aligned, workspaces 256-byte.

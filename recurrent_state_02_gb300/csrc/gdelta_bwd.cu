@@ -20,7 +20,8 @@
 // exponents of F, where it is divided out again, and as 0 in dec elsewhere.
 // Kernels: gdelta_prep (A, X, gates, scale e^G Q); the forward chain again, keeping the states between the chunks and E, and beside
 // it the backward chain, keeping their gradients and N; and a kernel over all chunks.
-// At B4 H16 T4096, 128 wide: 78 us, 240 us (both chains, 128 CTAs; 1.44 GB moved, 6 TB/s) and 236 us (1.21 GB, 5.1 TB/s), so that what the
+// At B4 H16 T4096, 128 wide: 75 us, 241 us (both chains, 128 CTAs; 1.44 GB moved, 6 TB/s) and 254 us (1.14 GB, 4.5 TB/s; 237 before dalpha's
+// products with the states went in all parts), so that what the
 // kernels hand one another, the states between the chunks and E and N above all, is what bounds them.  Forming each chunk's
 // gradients inside the chains would spare half of it, but needs both chains at the same chunk.
 // Precision: what reaches an FP32 result (dalpha, dbeta, dS0) takes both BF16 parts of a derived operand (the product of two low
