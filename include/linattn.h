@@ -573,8 +573,9 @@ la_status la_gated_delta_decode_step(const void *q, const void *k, const void *v
  *   dq, dk   device [B,Hk,T,r] dtype         dv_out  device [B,H,T,dv] dtype
  *   dalpha   device FP32 [B,H,T] or NULL (not formed; ignored without alpha).  It is as accurate at a gate near 0 (denormal numbers
  *            included) as at 1: off by 1e-7 of |S_{t-1}| |G_t - k_t dv_t^T| / sqrt(r dv) in the recurrence, 2e-6 in chunks (2-norms over all
- *            tokens).  A gate of exactly 0 is taken for a constant: 0 is written there.  Who wants the derivative at a
- *            reset passes the smallest normal number for it, 1.2e-38, which keeps nothing of the state either.
+ *            tokens), beside at most 2^-62 of what several nearly closed gates shut out together.  A gate of exactly 0 is taken for a
+ *            constant: 0 is written there.  Who wants the derivative at a reset passes the smallest normal number for it,
+ *            1.2e-38, which keeps nothing of the state either.
  *   dbeta    device FP32 [B,H,T] or NULL (not formed)
  *   dS0      device FP32 [B,H,r,dv] (written also when S0 is NULL)
  *   workspace  la_gated_delta_backward_workspace_bytes(...) bytes, as above

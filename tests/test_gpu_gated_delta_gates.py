@@ -136,6 +136,26 @@ def test_small_gate_against_differences(la, dtype):  # noqa: F811
 
 
 @DTYPES
+def test_reset_by_the_smallest_gate(la, dtype):  # noqa: F811
+    """The smallest normal number for a gate of 0: the same outputs and other gradients, and there the derivative (at 0 itself, 0 is written)."""
+    q, k, v, dy, alpha, beta, S0, dS_T = make(1, 2, 2, 150, 128, 128, dtype, True, 78)
+    where = torch.zeros_like(alpha, dtype=torch.bool)
+    where[:, 0, [0, 30, 64]], where[:, 1, [63, 149]] = True, True
+    least = torch.where(where, torch.finfo(torch.float32).tiny, alpha)
+    reset = torch.where(where, 0.0, alpha)
+    for x, z in zip(la.gated_delta_prefill(q, k, v, least, beta, S0=S0), la.gated_delta_prefill(q, k, v, reset, beta, S0=S0)):
+        assert torch.equal(x, z)
+    got, at_0 = (la.gated_delta_backward(q, k, v, dy, a, beta, S0=S0, dS_T=dS_T) for a in (least, reset))
+    for i in (0, 1, 2, 4):
+        assert torch.equal(got[i], at_0[i]), R.NAMES[i]
+    assert torch.equal(got[3][~where], at_0[3][~where]) and not at_0[3][where].any()
+    ref, size = sizes_and_gradient(q, k, v, dy, reset, beta, S0, dS_T, 1.0)      # (the derivative at 0)
+    err = (got[3].cpu().double() - ref).abs()[where.cpu()]
+    assert (err <= 8 * R.tolerance(dtype, torch.float32, 150) * (math.sqrt(2) * size + ref.abs())[where.cpu()]).all(), err
+    assert ref[where.cpu()].abs().min() > 1e-3
+
+
+@DTYPES
 def test_gradients_that_nobody_wants(la, dtype):  # noqa: F811
     """Without room for dalpha or dbeta the C entry forms the others all the same, to the bit."""
     B, H, Hk, T, r, dv = size = (1, 4, 2, 150, 128, 128)
