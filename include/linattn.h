@@ -508,7 +508,8 @@ la_status la_decay_backward(const void *q, const void *k, const void *v, la_dtyp
  *   for one token of la_gated_delta_decode_step a kernel of its own, bound by the state's traffic, when dv is a multiple of 4
  *   and S 16-byte aligned.
  * In the chunked kernels what is derived from the inputs enters the tensor cores as two BF16 parts (16 bits of it) where
- * it reaches an FP32 result, and as one where it reaches a BF16 one only: relative 2-norms of the errors about 4e-6 (dalpha and dbeta 7e-6) and 2e-3 to 3e-3.
+ * it reaches an FP32 result, and as one where it reaches a BF16 one only: relative 2-norms of the errors about 4e-6 (dalpha and dbeta
+ * 7e-6) and 2e-3 to 3e-3.
  * The first call of each kind on a device sets kernel attributes: make it before any stream capture.
  * Requires 1 <= r, dv <= 256, B, H <= 65535, T <= 2^30 and, but for packed sequences, B H (T + 1) <= 2^30; BF16 arrays
  * 2-byte, FP32 and int32 arrays 4-byte aligned, workspaces 256-byte.
@@ -610,6 +611,32 @@ la_status la_gated_delta_backward(const void *q, const void *k, const void *v, l
  * beam as parent, token 0 and its own done.
  * next_scores may equal scores, done_out may equal done.
  * One launch, one cluster of 2 to 8 CTAs per request, the logits read once; rows that start on
+ * 16-byte boundaries are read fastest.
+ * Requires 1 <= K <= 32, 1 <= V <= 2^30, row_stride >= V, B <= 65535; logits aligned to their
+ * element size, FP32 and int32 arrays 4-byte aligned.
+ * Errors: LA_ERR_NULL, LA_ERR_SHAPE (sizes < 1, row_stride < V, eos out of range or missing),
+ *         LA_ERR_DTYPE, LA_ERR_ALIGN, LA_ERR_UNSUPPORTED (K > 32, other sizes), LA_ERR_CUDA.
+ */
+la_status la_beam_select(const void *logits, la_dtype dtype, long long row_stride, const float *scores,
+                         const unsigned char *done, int B, int K, int V, int eos, float *next_scores, int *parents,
+                         int *tokens, unsigned char *done_out, la_stream_t stream);
+
+/*
+ * la_token_logprobs -- scores of given tokens under rows of logits (what a model answered with, or is trained
+ * on):  lse = log sum_v exp x_v,  logprob = x_token - lse,  entropy = lse - sum_v p_v x_v  with p_v = exp(x_v - lse),
+ * and the best alternatives of the row.
+ *   logits    device [N,V] dtype, row n at element n row_stride
+ *   tokens    device int32 [N].  A negative token skips its row (padding), which is not read: its logprob,
+ *             entropy and lse are 0 and it has no alternatives.  A token >= V does the same and is
+ *             recorded as LA_ERR_SHAPE in the device status word.
+ *   top       alternatives per row, 0 .. 32
+ *   logprobs  device FP32 [N];  entropy, lse  device FP32 [N] or NULL
+ *   top_logprobs, top_tokens  device FP32, int32 [N,top] (may be NULL when top is 0): the top most probable
+ *             tokens, best first, equal logits in the order of their indices
+ * A logit of -infinity (a masked token) has probability 0 and is no alternative; slots left over get -infinity and token -1.
+ * A row of nothing else has lse and logprob -infinity and entropy 0.  A row with a NaN or +infinity gives NaN
+ * and no alternatives.
+ * One launch, the logits read once (blocks that hold an alternative once more, out of the L2 cache); rows that start on
  * 16-byte boundaries are read fastest.  A row's results do not depend on the other rows' values.  How many rows there are decides
  * how many CTAs share one, and with that the order of its sums: among more or fewer rows its results differ in the last bits
  * (2^-20 of their size, the entropy 2^-19; its best tokens and their order do not differ).  The same N, V, layout and device give
