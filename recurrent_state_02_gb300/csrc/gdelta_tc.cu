@@ -196,7 +196,6 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const GdeltaShape &s = args.s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool packed = s.cu_seqlens != nullptr;
-    let_next_start();
     const bool planned = args.slot_base != nullptr;
     if (planned) wait_for_last();
     // this CTA's head, sequence and chunk
@@ -322,6 +321,8 @@ gdelta_prep_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (the chain's CTAs take all TMEM of an SM and then wait for this kernel: none is placed before every CTA here has its columns)
+    let_next_start();
     const uint32_t tmem = sm->tmem_base;
 
     // [G; P] = [K; Q] K^T (M = 128: G in TMEM lanes 0..63, P in lanes 64..127)

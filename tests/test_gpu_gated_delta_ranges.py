@@ -222,3 +222,34 @@ def test_roundings_of_bf16_results(la, size):  # noqa: F811
         rel = float((R.f64(x) - z).norm() / z.norm())
         print(f"[roundings] {name} {size}: {rel:.2e} of {n ** 0.5 * rounding + 2.0 ** -15:.2e}")
         assert rel <= n ** 0.5 * rounding + 2.0 ** -15, (name, rel)
+
+
+def test_calls_at_once(la):  # noqa: F811
+    """Calls of every kind on four streams at the same time, each waiting for parts of its own while the others hold SMs: the bits of the
+    calls alone."""
+    jobs = []
+    for seed, size in ((1, (2, 8, 4, 1500, 128, 128)), (2, (4, 8, 8, 700, 64, 64)), (3, (1, 8, 8, 10000, 128, 128)), (4, (2, 4, 4, 900, 64, 128))):
+        q, k, v, dy, alpha, beta, S0, dS_T = make(*size, BF, True, seed)
+        tok = [x[0].transpose(0, 1).contiguous() for x in (q, k, v, alpha, beta)]
+        n = size[3] // 40
+        cu = torch.tensor([min(i * n, size[3]) for i in range(41)], dtype=torch.int32, device="cuda")
+
+        def job(q=q, k=k, v=v, dy=dy, alpha=alpha, beta=beta, S0=S0, dS_T=dS_T, tok=tok, cu=cu):
+            out = [*la.gated_delta_prefill(q, k, v, alpha, beta, S0=S0)]
+            out += la.gated_delta_backward(q, k, v, dy, alpha, beta, S0=S0, dS_T=dS_T)
+            out += la.gated_delta_prefill_varlen(*tok[:3], cu, *tok[3:], y=torch.zeros_like(tok[2]))
+            return out
+        jobs.append(job)
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(4):
+        held = []
+        for job, stream in zip(jobs, streams):
+            with torch.cuda.stream(stream):
+                held.append(job())
+        torch.cuda.synchronize()
+        for a, b in zip(alone, held):
+            for x, z in zip(a, b):
+                assert torch.equal(x, z)
+    assert la.last_device_status() == 0
