@@ -253,3 +253,24 @@ def test_calls_at_once(la):  # noqa: F811
             for x, z in zip(a, b):
                 assert torch.equal(x, z)
     assert la.last_device_status() == 0
+
+
+@DTYPES
+def test_gradients_past_32_bits(la, dtype):  # noqa: F811
+    """Arrays of more than 2^31 elements: the last heads' gradients have the bits of those heads alone."""
+    H, T, r, dv = (17, 1 << 20, 128, 128) if dtype == BF else (8704, 2048, 128, 128)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    normal = lambda sd: torch.randn((1, H, T, r), generator=g, device="cuda", dtype=dtype).mul_(sd)  # noqa: E731
+    q, k, v, dy = normal(r ** -0.5), normal(r ** -0.5), normal(1.0), normal(1.0)
+    assert v.numel() > 1 << 31
+    alpha, beta = (torch.rand((1, H, T), generator=g, device="cuda").mul_(0.3).add_(c) for c in (0.7, 0.1))
+    alpha[:, :, ::1000] = 1e-9
+    got = la.gated_delta_backward(q, k, v, dy, alpha, beta, scale=0.1)
+    assert la.last_device_status() == 0
+    for h in (H - 1, 0):
+        one = lambda x: x[:, h:h + 1].contiguous()  # noqa: E731
+        for x, z, name in zip(got, la.gated_delta_backward(*(one(x) for x in (q, k, v, dy, alpha, beta)), scale=0.1), R.NAMES):
+            assert torch.isfinite(z).all() and z.any(), name
+            assert torch.equal(one(x), z), (h, name)
+    del q, k, v, dy, got
+    torch.cuda.empty_cache()
